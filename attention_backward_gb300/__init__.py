@@ -34,3 +34,11 @@ from ._binding import (  # noqa: F401
     tile_schedule_split,
     workspace_size,
 )
+from ._kv_cache import (  # noqa: F401
+    KvPlan,
+    forward_kv_cache,
+    kv_block_tables,
+    kv_cache_workspace_size,
+    kv_cache_write,
+    new_kv_cache,
+)

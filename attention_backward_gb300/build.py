@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libattn_bwd.so")
-SOURCES = ["api.cu", "preprocess.cu", "dense_bwd.cu", "dense128_bwd.cu", "dense_fwd.cu", "sparse_bwd.cu", "noalloc.cu", "host_pipeline.cu"]
+SOURCES = ["api.cu", "preprocess.cu", "dense_bwd.cu", "dense128_bwd.cu", "dense_fwd.cu", "sparse_bwd.cu", "noalloc.cu", "host_pipeline.cu",
+           "kv_api.cu", "kv_cache.cu", "kv_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -35,7 +36,8 @@ def _stale(obj: str, src: str) -> bool:
         return True
     t = os.path.getmtime(obj)
     deps = [src] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    deps.append(os.path.join(ROOT, "include", "attn_bwd.h"))
+    inc = os.path.join(ROOT, "include")
+    deps += [os.path.join(inc, f) for f in os.listdir(inc)]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -1,0 +1,81 @@
+// Parameter blocks and launchers of the paged 8-bit cache operators (internal
+// to the library).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_kv_cache.h"
+#include "common.cuh"
+
+namespace ab {
+
+struct KvTablesParams {
+  const int* ctx;
+  const int* add;
+  int N;
+  int* table;
+  int64_t table_stride;
+  int max_blocks;
+  const int* free_blocks;
+  int num_free;
+  const int* free_start;  // device scalar, or null: 0
+  int page_log2, num_blocks, T;
+  int* cu;
+  int* kv_lens;
+  int* slot_map;
+  int* positions;
+  int* counts;
+};
+
+struct KvWriteParams {
+  const uint8_t* x[2];  // k, v: 16-bit [T,HKV,D]
+  int64_t sx_s[2], sx_h[2];  // element strides
+  uint8_t* cache[2];
+  int64_t sc_b[2], sc_s[2], sc_h[2];
+  float* scale[2];  // [num_blocks, HKV]
+  const int* slot_map;
+  int T, HKV, D, page_log2, num_blocks;
+};
+
+// Attention over the cache.
+struct KvAttnParams {
+  const uint8_t* q;
+  int64_t sq_s, sq_h;  // element strides
+  uint8_t* o;
+  int64_t so_s, so_h;
+  float* lse;
+  int64_t sl_s, sl_h;
+  const uint8_t* k;
+  int64_t sk_b, sk_s, sk_h;
+  const uint8_t* v;
+  int64_t sv_b, sv_s, sv_h;
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;
+  int64_t table_stride;
+  int max_blocks, num_blocks, page_log2;
+  const int* cu;
+  const int* kv_lens;
+  int N, T, HQ, HKV, G, D;
+  int causal, window;
+  float scale_log2;  // sm_scale * log2(e), > 0
+  // workspace
+  int* err;
+  int4* desc;      // per CTA: the unit whose split it finishes (see kv_decode.cu)
+  float2* part_ml;  // [2 * ctas][rows] running max (log2 units) and sum
+  float* part_o;    // [2 * ctas][rows][D] unnormalised O
+  uint64_t timeout_ns;
+};
+
+// Rows (query, head of the group) of a decode unit, and keys per step of its CTA.
+constexpr int kKvDecRows = 16;
+constexpr int kKvDecKeys = 64;
+// Most CTAs of a launch: sizes the workspace's partials.
+constexpr int kKvDecMaxCtas = 512;
+
+cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);
+cudaError_t launch_kv_write(const KvWriteParams& p, bool bf16, cudaStream_t st);
+cudaError_t launch_kv_decode(const KvAttnParams& p, bool bf16, int sms, cudaStream_t st);
+
+}  // namespace ab
