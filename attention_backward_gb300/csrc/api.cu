@@ -21,9 +21,7 @@
 #include "kernels.h"
 #include "sink.h"
 
-namespace {
-
-using namespace ab;
+namespace ab {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -38,6 +36,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+}  // namespace ab
+
+namespace {
+
+using namespace ab;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

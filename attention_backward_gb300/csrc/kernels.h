@@ -1,6 +1,7 @@
 // Parameter blocks and launchers of the kernels (internal to the library).
 #pragma once
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -9,6 +10,9 @@
 #include "common.cuh"
 
 namespace ab {
+
+// The driver's cuTensorMapEncodeTiled, looked up once (null without a driver).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 struct PreprocessParams {
   const uint8_t* o;

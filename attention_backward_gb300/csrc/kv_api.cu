@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "attn_kv_cache.h"
+#include "kernels.h"
 #include "kv_cache.h"
 
 namespace {
@@ -47,16 +48,31 @@ attn_status_t check_cache(const attn_kv_cache_t* c) {
 
 bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_DT_F16 || dt == ATTN_DT_BF16; }
 
-// Workspace of attention over the cache: the header, a descriptor per CTA,
+bool make_cache_map(CUtensorMap* m, const void* base, const attn_strides_t& st, const attn_kv_cache_t& c) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.HKV),
+                        static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.num_blocks)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.h), static_cast<cuuint64_t>(st.s),
+                           static_cast<cuuint64_t>(st.b)};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(c.D), 1, kKvBoxTokens, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of attention over the cache: the header, an error word and a descriptor per CTA,
 // then two partial slots a CTA.
 struct KvWs {
-  int64_t desc_off, ml_off, o_off, total;
+  int64_t err_off, desc_off, ml_off, o_off, total;
 };
 
 KvWs kv_ws(int64_t D) {
   KvWs w;
   const int64_t slots = 2 * kKvDecMaxCtas;
-  w.desc_off = kHeaderBytes;
+  w.err_off = kHeaderBytes;
+  w.desc_off = w.err_off + kKvDecMaxCtas * 4;
   w.ml_off = w.desc_off + kKvDecMaxCtas * 16;
   w.o_off = w.ml_off + slots * kKvDecRows * 8;
   w.total = w.o_off + slots * kKvDecRows * D * 4;
@@ -167,11 +183,15 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   p.causal = causal ? 1 : 0, p.window = window_left;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.err = &reinterpret_cast<WsHeader*>(ws)->err;
+  p.cta_err = reinterpret_cast<int*>(ws + L.err_off);
   p.desc = reinterpret_cast<int4*>(ws + L.desc_off);
   p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.timeout_ns = kWaitTimeoutNs;
-  return launch_status(launch_kv_decode(p, dtype == ATTN_DT_BF16, sm_count(), static_cast<cudaStream_t>(stream)));
+  KvMaps maps;
+  if (!make_cache_map(&maps.k, cache->k, cache->sk, *cache) || !make_cache_map(&maps.v, cache->v, cache->sv, *cache))
+    return ATTN_ERR_INVALID_ARG;
+  return launch_status(launch_kv_decode(p, maps, dtype == ATTN_DT_BF16, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // Parameter blocks and launchers of the paged 8-bit cache operators (internal
 // to the library).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -62,20 +63,28 @@ struct KvAttnParams {
   float scale_log2;  // sm_scale * log2(e), > 0
   // workspace
   int* err;
-  int4* desc;      // per CTA: the unit whose split it finishes (see kv_decode.cu)
+  int* cta_err;     // per CTA: its error code
+  int4* desc;       // per CTA: the unit whose split it finishes (see kv_decode.cu)
   float2* part_ml;  // [2 * ctas][rows] running max (log2 units) and sum
   float* part_o;    // [2 * ctas][rows][D] unnormalised O
   uint64_t timeout_ns;
 };
 
-// Rows (query, head of the group) of a decode unit, and keys per step of its CTA.
+// Tensor maps of the cache's bytes, dims (D, HKV, page_size, num_blocks): box D
+// bytes x 16 tokens of one head, swizzled over rows of D bytes.
+struct KvMaps {
+  CUtensorMap k, v;
+};
+constexpr int kKvBoxTokens = 16;
+
+// Most rows (query, head of the group) of a decode unit, and keys per tile.
 constexpr int kKvDecRows = 16;
 constexpr int kKvDecKeys = 64;
 // Most CTAs of a launch: sizes the workspace's partials.
-constexpr int kKvDecMaxCtas = 512;
+constexpr int kKvDecMaxCtas = 1024;
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);
 cudaError_t launch_kv_write(const KvWriteParams& p, bool bf16, cudaStream_t st);
-cudaError_t launch_kv_decode(const KvAttnParams& p, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, cudaStream_t st);
 
 }  // namespace ab

@@ -9,29 +9,32 @@
 // only when it grows by more than 2^8).  Bound by the bytes of K and V: 2 D
 // bytes and 4 D G flops a key.
 //
-// Split: the line of kv_sched.cuh, units of 16 rows and tiles of 64 keys, over
-// persistent CTAs of 4 warps.  A warp takes 16 keys of every tile and keeps
-// its own m, l and O; the four are joined in shared memory when the unit (or
-// the CTA's part of it) ends.  A unit that one CTA holds whole is written at
-// once; parts go to the workspace, at most two a CTA, and kv_join_kernel adds
-// them in CTA order (the same result from run to run).
+// Split: the line of kv_sched.cuh, units of 8 or 16 rows and tiles of 64 keys,
+// over persistent CTAs of 4 warps.  A warp takes 16 keys of every tile and
+// keeps its own m, l and O; the four are joined in shared memory when the unit
+// (or the CTA's part of it) ends.  A unit that one CTA holds whole is written
+// at once; parts go to the workspace, at most two a CTA, and kv_join_kernel
+// adds them in CTA order (the same result from run to run).
 //
-// Products: mma.m16n8k16 on fp16.  tcgen05 needs 64 or 128 rows, and here the
-// group's 1 to 16 rows ride on 16, so the tensor work stays far under the time
-// of the loads.  e4m3 is exact in fp16; a row of Q is brought to fp16's upper
-// range by a power of two (bf16 rows keep every bit of their leading values,
-// what falls under 2^-24 of fp16 is 2^-38 of the row's largest value); the
-// K scale and the row's power go to the f32 score, the V scale to p before it
-// is rounded to fp16, relative to the largest V scale met so far, so that
-// neither scale can overflow.
+// Products: mma.m16n8k16 on fp16, transposed: S^T = K Q^T with 16 keys by 8
+// rows, O^T += V^T P^T with 16 columns by 8 rows.  tcgen05 needs 64 or 128 rows
+// of A and its operands in shared memory at 16 bits; here the few rows are the
+// N of the product, so none of its work is padding beyond 8 rows, and K and V
+// go from their ring to registers as bytes.  e4m3 is exact in fp16; a row of Q
+// is brought to fp16's upper range by a power of two (bf16 rows keep every bit
+// of their leading values, what falls under fp16's 2^-24 is 2^-38 of the row's
+// largest value); the K scale and the row's power go to the f32 score, the V
+// scale to p before it is rounded to fp16, relative to the largest V scale met
+// so far, so that neither scale can overflow.
 //
-// Layout: no operand needs a transpose through shared memory.  The sum over d
-// may run in any order, so the thread that holds K column pairs c of key n in
-// an mma takes 16 consecutive bytes of the key (its own cp.async of 16 bytes
-// and one 16-byte read back); Q is permuted to match.  Likewise the O columns:
-// the thread of column n takes bytes [n D/8, (n + 1) D/8) of its four keys, and
-// two keys' bytes are paired by one byte permute before the conversion.  Each
-// thread reads back only what it copied itself, so the ring needs no barrier.
+// Layout: no operand goes through a transpose in shared memory.  The sum over d
+// may run in any order, so the thread that holds k columns 2c, 2c + 1 of key n
+// takes 16 consecutive bytes of the key (its own cp.async of 16 bytes and one
+// 16-byte read back), and Q is permuted to match.  Likewise the rows of O^T:
+// thread n takes bytes [n D/8, (n + 1) D/8) of its four keys, and two keys'
+// bytes are paired by one byte permute before the conversion.  P^T turns with
+// one movmatrix for 8 keys.  Each thread reads back only what it copied itself,
+// so the ring needs no barrier.
 #include <cuda_fp16.h>
 
 #include "cvt.cuh"
@@ -44,32 +47,24 @@ namespace ab {
 
 namespace {
 
-constexpr int RT = kKvDecRows, KT = kKvDecKeys;
+constexpr int KT = kKvDecKeys;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kStages = 4;       // ring of 16-key steps per warp
-constexpr int kCtasPerSm = 3;
+constexpr int kStages = 3;       // ring of 16-key slots per warp
 constexpr float kRescale = 8.f;  // log2 growth of a row max that triggers a rescale
 
-template <int D>
+template <int D, int NB>
 struct DecCfg {
-  static constexpr int STEP = 16 * D * 2;                       // bytes of K and V of 16 keys
-  static constexpr int WARP = kStages * STEP;                   // a warp's ring
-  static constexpr int JOIN = 16 * (D + 4) * 4;                 // a warp's O rows when the warps are joined
-  static constexpr int REGION = WARP > JOIN ? WARP : JOIN;
-  static constexpr int SMEM = kWarps * REGION + kWarps * 16 * 8;  // and its (m, l) pairs
+  static constexpr int RT = 8 * NB;                             // rows of a unit
+  static constexpr int CTAS = NB == 1 ? 4 : 3;                  // resident per SM
+  static constexpr int TILE = 16 * D;                           // bytes of K, or of V, of 16 keys
+  static constexpr int WARP = kStages * 2 * TILE;               // a warp's ring
+  static constexpr int JOIN = RT * (D + 4) * 4;                 // a warp's O rows when the warps are joined
+  static constexpr int REGION = ((WARP > JOIN ? WARP : JOIN) + 1023) / 1024 * 1024;
+  static constexpr int OFF_ML = kWarps * REGION;                // the warps' (m, l) pairs
+  static constexpr int OFF_BAR = OFF_ML + kWarps * RT * 8;
+  static constexpr int OFF_ABORT = OFF_BAR + kWarps * kStages * 8;
+  static constexpr int SMEM = OFF_ABORT + 8;
 };
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // Four e4m3 bytes -> two fp16 pairs (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* lo, uint32_t* hi) {
@@ -84,6 +79,13 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held as one pair a lane.
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Power of two that brings a largest absolute value into [2^14, 2^15), and its
@@ -108,6 +110,7 @@ struct Cursor {
 // Every thread of the CTA: the launch's tiles in all, and the cursor of the
 // CTA's first one.  A thread sums ceil(N / 128) consecutive requests; the one
 // whose requests hold the position walks them.
+template <int RT>
 __device__ __forceinline__ void locate(const KvAttnParams& p, int64_t* total, int* ctas, int64_t* begin,
                                        int64_t* end, Cursor* cur) {
   __shared__ int64_t s_warp[kWarps];
@@ -193,27 +196,52 @@ __device__ __forceinline__ void store_lse(const KvAttnParams& p, int64_t t, int 
   p.lse[hq * p.sl_h + t * p.sl_s] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_decode_kernel(const KvAttnParams p) {
-  using C = DecCfg<D>;
+// Byte offset of 16-byte chunk ``c`` of row ``r`` in a tile of D-byte rows, as
+// the copies' 128-byte (D = 128) or 64-byte (D = 64) swizzle places it.
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+template <int D, int NB, bool BF16>
+__global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
+    kv_decode_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ KvAttnParams p) {
+  using C = DecCfg<D, NB>;
+  constexpr int RT = C::RT;
   constexpr int KC = D / 64;   // 16-byte chunks of a key's row per thread
   constexpr int VB = D / 8;    // bytes of a value row per thread
-  constexpr int NT = D / 8;    // column tiles of O
-  extern __shared__ __align__(16) uint8_t sm[];
+  constexpr int MT = D / 16;   // row tiles of O^T
+  extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r8 = lane >> 2, c4 = lane & 3;
   uint8_t* const ring = sm + warp * C::REGION;
-  const uint32_t ring_s = smem_u32(ring);
-  float2* const ml = reinterpret_cast<float2*>(sm + kWarps * C::REGION);  // [warp][16]
+  float2* const ml = reinterpret_cast<float2*>(sm + C::OFF_ML);  // [warp][RT]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR) + warp * kStages;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
 
+  if (tid == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(reinterpret_cast<uint64_t*>(sm + C::OFF_BAR) + i, 1);
+    fence_mbar_init();
+  }
   grid_dependency_wait();
-  if (blockIdx.x == 0 && tid == 0) *p.err = 0;
+  // The CTA's own error word: kv_join_kernel gathers them, so that no word has
+  // to be cleared by a launch of its own.
+  const WaitCtx wc{abort_flag, p.cta_err + blockIdx.x, p.timeout_ns};
+  const bool aligned = (smem_u32(sm) & 1023u) == 0;  // the swizzled tiles need it
+  if (tid == 0) {
+    *wc.err = aligned ? kErrNone : kErrAlign;
+    p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
   int64_t total, begin, end;
   int ctas;
   Cursor cur;
-  locate(p, &total, &ctas, &begin, &end, &cur);
-  if (tid == 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (begin >= end) return;
+  locate<RT>(p, &total, &ctas, &begin, &end, &cur);  // (its barriers publish what thread 0 wrote)
+  if (!aligned || begin >= end) return;
+  // slots filled and read so far, as (slot, parity) of the next one
+  int in_slot = 0, out_slot = 0, pending = 0;
+  uint32_t out_par = 0;
+  bool ok = true;
 
   KvReq rq = kv_request(cur.n, p);
   for (int64_t x = begin; x < end;) {
@@ -224,17 +252,58 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_decode_kernel(const K
     const int part1 = kt.n - part0 <= left ? kt.n : part0 + static_cast<int>(left);
     const int row0 = cur.rt * RT;
     const int rows = imin(RT, rq.R - row0);
-    // my two rows: their queries and key ranges, and Q in fp16
-    int lo[2], hi[2];
-    float rs[2];
-    uint32_t qa[KC * 4][4];  // [k step][a0..a3]
+
+    // Page ids of my slots, 32 tiles at a time: lane i holds that of tile
+    // ``batch + i`` (-1: no page, or no key that the unit sees).
+    auto key0_of = [&](int t) { return (kt.t0 + t) * KT + warp * 16; };
+    auto load_ids = [&](int batch) {
+      const int t = batch + lane;
+      int b = -1;
+      if (t < part1) {
+        const int k0 = key0_of(t);
+        if (k0 < kt.hi && k0 + 16 > kt.lo) {
+          b = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
+          if (b < 0 || b >= p.num_blocks) b = -1;
+        }
+      }
+      return b;
+    };
+    int ld_batch = part0, ld_blk = load_ids(part0);
+    auto issue = [&](int t) {  // copies of tile t's 16 keys into the next slot
+      if (t >= part1) return;
+      if (t - ld_batch == 32) {
+        ld_batch = t;
+        ld_blk = load_ids(t);
+      }
+      const int b = __shfl_sync(0xffffffffu, ld_blk, t - ld_batch);
+      if (lane == 0) {
+        uint64_t* const bar = &full[in_slot];
+        if (b >= 0) {
+          uint8_t* const dst = ring + in_slot * (2 * C::TILE);
+          const int s0 = key0_of(t) & ((1 << p.page_log2) - 1);
+          mbar_arrive_expect_tx(bar, 2 * C::TILE);
+          tma_load_4d(dst, &maps.k, bar, 0, cur.h, s0, b);
+          tma_load_4d(dst + C::TILE, &maps.v, bar, 0, cur.h, s0, b);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
+      ++pending;
+    };
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int i = 0; i < kStages; ++i) issue(part0 + i);
+
+    // Q in fp16: the thread holds row r8 of each 8 rows; the scores of a thread
+    // belong to rows 2 c4 and 2 c4 + 1
+    int lo[NB][2], hi[NB][2];
+    float rs[NB][2];
+    uint32_t qb[NB][KC * 4][2];  // [8 rows][k step][b0, b1]
+#pragma unroll
+    for (int e = 0; e < NB; ++e) {
       const int r = r8 + 8 * e;
       const bool live = r < rows;
       const int i = (row0 + r) / p.G, g = (row0 + r) % p.G;
-      lo[e] = hi[e] = 0;
-      if (live) kv_row_keys(rq, i, p.causal, p.window, &lo[e], &hi[e]);
       const uint8_t* src = p.q + 2 * ((static_cast<int64_t>(rq.a) + i) * p.sq_s +
                                       static_cast<int64_t>(cur.h * p.G + g) * p.sq_h);
       uint32_t w[KC][8];
@@ -244,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_decode_kernel(const K
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint4 x4 = make_uint4(0u, 0u, 0u, 0u);
-          if (live) x4 = *reinterpret_cast<const uint4*>(src + 2 * (c * 64 + c4 * 16 + u * 8));
+          if (live) x4 = *reinterpret_cast<const uint4*>(src + 2 * ((c4 * KC + c) * 16 + u * 8));
           w[c][4 * u] = x4.x, w[c][4 * u + 1] = x4.y, w[c][4 * u + 2] = x4.z, w[c][4 * u + 3] = x4.w;
         }
 #pragma unroll
@@ -257,256 +326,236 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_decode_kernel(const K
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       float back;
       const float up = to_top(amax, &back);
-      rs[e] = back * p.scale_log2;
+      back *= p.scale_log2;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const float2 f = unpack2<BF16>(w[c][u]);
           // bytes 4j .. 4j + 3 of the chunk are k step 4c + j: pairs (0,1) and (2,3)
-          qa[c * 4 + u / 2][e + 2 * (u & 1)] = pack2<false>(f.x * up, f.y * up);
+          qb[e][c * 4 + u / 2][u & 1] = pack2<false>(f.x * up, f.y * up);
         }
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int rr = 8 * e + 2 * c4 + y;
+        rs[e][y] = __shfl_sync(0xffffffffu, back, (2 * c4 + y) * 4);
+        lo[e][y] = hi[e][y] = 0;
+        if (rr < rows) kv_row_keys(rq, (row0 + rr) / p.G, p.causal, p.window, &lo[e][y], &hi[e][y]);
+      }
     }
     // keys that every live row sees lie in [lo_all, hi_all)
     int lo_all, hi_all, xx;
     kv_row_keys(rq, (row0 + rows - 1) / p.G, p.causal, p.window, &lo_all, &xx);
     kv_row_keys(rq, row0 / p.G, p.causal, p.window, &xx, &hi_all);
 
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f, vinv = 0.f;
-    float o[NT][4];
+    // A row's scores are kept relative to nm (its m, 0 before its first key)
+    // and compared with th (kRescale, -inf before its first key).
+    float nm[NB][2], th[NB][2], l[NB][2], vref = 0.f, vinv = 0.f;
+    float o[NB][MT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    for (int e = 0; e < NB; ++e) {
+      nm[e][0] = nm[e][1] = l[e][0] = l[e][1] = 0.f;
+      th[e][0] = th[e][1] = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) o[e][t][0] = o[e][t][1] = o[e][t][2] = o[e][t][3] = 0.f;
+    }
 
-    // Page ids of my steps, 32 tiles at a time: lane i holds those of tile
-    // ``batch + i``; scales likewise.
-    const uint8_t* const kh = p.k + static_cast<int64_t>(cur.h) * p.sk_h;
-    const uint8_t* const vh = p.v + static_cast<int64_t>(cur.h) * p.sv_h;
-    int ld_batch = part0, blk_l = -1;
-    auto key0_of = [&](int t) { return (kt.t0 + t) * KT + warp * 16; };
-    auto load_ids = [&](int batch) {
-      const int t = batch + lane;
-      int b = -1;
-      if (t < part1) {
-        const int k0 = key0_of(t);
-        if (k0 < kt.hi && k0 + 16 > kt.lo) {
-          b = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
-          if (b < 0 || b >= p.num_blocks) b = -1;
-        }
-      }
-      blk_l = b;
-    };
-    load_ids(part0);
-    float ks_l = 0.f, vs_l = 0.f;  // scales of the batch being computed
-    int cp_blk = -1;               // its ids (the load side may be a batch ahead)
-    auto issue = [&](int t) {  // copies of tile t's 16 keys into stage t % kStages
-      if (t - ld_batch == 32) {
-        ld_batch += 32;
-        load_ids(ld_batch);
-      }
-      if (t < part1) {
-        const int b = __shfl_sync(0xffffffffu, blk_l, t - ld_batch);
-        const uint32_t dst = ring_s + ((t - part0) % kStages) * C::STEP;
-        const bool in = b >= 0;
-        const int s0 = key0_of(t) & ((1 << p.page_log2) - 1);
-        const int64_t bb = in ? b : 0;
-        const uint8_t* ks = kh + bb * p.sk_b + (in ? s0 : 0) * p.sk_s;
-        const uint8_t* vs = vh + bb * p.sv_b + (in ? s0 : 0) * p.sv_s;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int c = 0; c < KC; ++c)
-            cp16(dst + ((j * KC + c) * 32 + lane) * 16, ks + (j * 8 + r8) * p.sk_s + c * 64 + c4 * 16, in);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = 2 * c4 + (e & 1) + 8 * (e >> 1);
-          const uint32_t d = dst + 16 * D + (e * 32 + lane) * VB;
-          if constexpr (VB == 16)
-            cp16(d, vs + key * p.sv_s + r8 * VB, in);
-          else
-            cp8(d, vs + key * p.sv_s + r8 * VB, in);
-        }
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(part0 + i);
-
+    float ks_l = 0.f, vs_l = 0.f;  // scales of the 32 tiles being computed,
+    int cp_blk = -1;               // and their ids (the load side may be ahead)
     int cp_batch = part0 - 32;
     for (int t = part0; t < part1; ++t) {
       if (t - cp_batch == 32) {
-        // scales of the next 32 tiles (their ids once more: the load side may
-        // have moved on)
         cp_batch = t;
-        const int u = t + lane;
-        cp_blk = -1, ks_l = vs_l = 0.f;
-        if (u < part1) {
-          const int k0 = key0_of(u);
-          if (k0 < kt.hi && k0 + 16 > kt.lo) {
-            const int b = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
-            if (b >= 0 && b < p.num_blocks) {
-              cp_blk = b;
-              const int64_t at = static_cast<int64_t>(b) * p.HKV + cur.h;
-              ks_l = p.k_scale[at];
-              vs_l = p.v_scale[at] < 0x1p-126f ? 0.f : p.v_scale[at];  // (its inverse is taken)
+        cp_blk = load_ids(t);
+        ks_l = vs_l = 0.f;
+        if (cp_blk >= 0) {
+          const int64_t at = static_cast<int64_t>(cp_blk) * p.HKV + cur.h;
+          ks_l = p.k_scale[at];
+          vs_l = p.v_scale[at] < 0x1p-126f ? 0.f : p.v_scale[at];  // (its inverse is taken)
+        }
+      }
+      const int bi = t - cp_batch;
+      const float ks = __shfl_sync(0xffffffffu, ks_l, bi), vs = __shfl_sync(0xffffffffu, vs_l, bi);
+      const bool have = __shfl_sync(0xffffffffu, cp_blk, bi) >= 0;
+      if (!(ok = mbar_wait_warp(&full[out_slot], out_par, wc, kErrWaitKV))) break;
+      const uint8_t* const st = ring + out_slot * (2 * C::TILE);
+      if (++out_slot == kStages) out_slot = 0, out_par ^= 1;
+      --pending;
+      if (have) {
+        const int k0 = key0_of(t);
+        const bool edge = k0 < lo_all || k0 + 16 > hi_all;
+        // ---- S^T of 16 keys by 8 NB rows, in two chains
+        float s2[NB][2][4], s[NB][4];
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) s2[e][y][0] = s2[e][y][1] = s2[e][y][2] = s2[e][y][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint4 x0 = *reinterpret_cast<const uint4*>(st + chunk_at<D>(r8, c4 * KC + c));
+          const uint4 x8 = *reinterpret_cast<const uint4*>(st + 8 * D + chunk_at<D>(r8, c4 * KC + c));
+          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w8[4] = {x8.x, x8.y, x8.z, x8.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t a[4];
+            e4m3x4_to_f16(w0[u], &a[0], &a[2]);
+            e4m3x4_to_f16(w8[u], &a[1], &a[3]);
+#pragma unroll
+            for (int e = 0; e < NB; ++e) mma16816(s2[e][u & 1], a, qb[e][c * 4 + u][0], qb[e][c * 4 + u][1]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            s[e][y] = (s2[e][0][y] + s2[e][1][y]) * (ks * rs[e][y & 1]) - nm[e][y & 1];
+        if (edge) {
+#pragma unroll
+          for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int k = k0 + r8 + 8 * (y >> 1);
+              if (k < lo[e][y & 1] || k >= hi[e][y & 1]) s[e][y] = -INFINITY;
+            }
+        }
+        // ---- a max that grew past the threshold, or a larger V scale: rescale
+        bool grew = vs > vref;
+#pragma unroll
+        for (int e = 0; e < NB; ++e)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) grew |= s[e][y] > th[e][y & 1];
+        if (__any_sync(0xffffffffu, grew)) {
+          float g = 1.f;
+          if (vs > vref) {
+            g = vref / vs;
+            vref = vs;
+            vinv = 1.f / vs;
+          }
+#pragma unroll
+          for (int e = 0; e < NB; ++e) {
+            float f[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float mx = fmaxf(s[e][y], s[e][2 + y]);  // the row's largest score, relative to nm
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              f[y] = 1.f;
+              if (mx > th[e][y]) {
+                f[y] = th[e][y] == -INFINITY ? 0.f : ex2(-mx);
+                nm[e][y] += mx;
+                th[e][y] = kRescale;
+                s[e][y] -= mx, s[e][2 + y] -= mx;
+              }
+              l[e][y] *= f[y];
+              f[y] *= g;
+            }
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+              o[e][u][0] *= f[0], o[e][u][1] *= f[1], o[e][u][2] *= f[0], o[e][u][3] *= f[1];
+          }
+        }
+        uint32_t pb[NB][2];
+        const float ratio = vs * vinv;  // at most 1
+#pragma unroll
+        for (int e = 0; e < NB; ++e) {
+          const float p0 = ex2(s[e][0]), p1 = ex2(s[e][1]), p2 = ex2(s[e][2]), p3 = ex2(s[e][3]);
+          l[e][0] += p0 + p2;
+          l[e][1] += p1 + p3;
+          pb[e][0] = turn8x8(pack2<false>(p0 * ratio, p1 * ratio));
+          pb[e][1] = turn8x8(pack2<false>(p2 * ratio, p3 * ratio));
+        }
+        // ---- O^T += V^T P^T
+        constexpr int VW = VB / 4;
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 2 * c4 + (e & 1) + 8 * (e >> 1);
+          const uint8_t* const at = st + C::TILE + chunk_at<D>(key, r8 * VB / 16) + (r8 * VB) % 16;
+          if constexpr (VB == 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(at);
+            vw[e][0] = w.x, vw[e][1] = w.y, vw[e][2] = w.z, vw[e][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(at);
+            vw[e][0] = w.x, vw[e][1] = w.y;
+          }
+        }
+        if (edge) {  // a zero P times a NaN byte would be NaN: keys that no row sees are zeroed
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = k0 + 2 * c4 + (e & 1) + 8 * (e >> 1);
+            if (k < kt.lo || k >= kt.hi) {
+#pragma unroll
+              for (int u = 0; u < VW; ++u) vw[e][u] = 0u;
             }
           }
         }
-      }
-      cp_wait<kStages - 2>();
-      issue(t + kStages - 1);
-      const int bi = t - cp_batch;
-      const float ks = __shfl_sync(0xffffffffu, ks_l, bi), vs = __shfl_sync(0xffffffffu, vs_l, bi);
-      if (__shfl_sync(0xffffffffu, cp_blk, bi) < 0) continue;
-      const uint8_t* const st = ring + ((t - part0) % kStages) * C::STEP;
-      const int k0 = key0_of(t);
-
-      // ---- scores of 16 keys
-      float s[2][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        for (int u = 0; u < VW; ++u) {
+          // bytes 4u .. 4u + 3 of keys (0, 1) and (2, 3) paired; byte 2i is row r8 of tile i, 2i + 1 its row r8 + 8
+          uint32_t a[2][4];
+          e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x5140), &a[0][0], &a[0][1]);
+          e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x7362), &a[1][0], &a[1][1]);
+          e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x5140), &a[0][2], &a[0][3]);
+          e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x7362), &a[1][2], &a[1][3]);
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(st + ((j * KC + c) * 32 + lane) * 16);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int e = 0; e < NB; ++e)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16(ww[u], &b0, &b1);
-            mma16816(s[j], qa[c * 4 + u], b0, b1);
-          }
+            for (int y = 0; y < 2; ++y) mma16816(o[e][2 * u + y], a[y], pb[e][0], pb[e][1]);
         }
       }
-      const bool edge = k0 < lo_all || k0 + 16 > hi_all;
-      const float f0 = ks * rs[0], f1 = ks * rs[1];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        s[j][0] *= f0, s[j][1] *= f0, s[j][2] *= f1, s[j][3] *= f1;
-        if (edge) {
-          const int k = k0 + j * 8 + 2 * c4;
-          if (k < lo[0] || k >= hi[0]) s[j][0] = -INFINITY;
-          if (k + 1 < lo[0] || k + 1 >= hi[0]) s[j][1] = -INFINITY;
-          if (k < lo[1] || k >= hi[1]) s[j][2] = -INFINITY;
-          if (k + 1 < lo[1] || k + 1 >= hi[1]) s[j][3] = -INFINITY;
-        }
-      }
-      // ---- running max, lazily adopted; the V scale's reference likewise
-      float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-      // (a row without a key yet has m = -inf and adopts any finite max)
-      const bool up0 = mx0 > m[0] + kRescale, up1 = mx1 > m[1] + kRescale;
-      if (__any_sync(0xffffffffu, up0 || up1 || vs > vref)) {
-        const float a0 = up0 ? ex2(m[0] - mx0) : 1.f, a1 = up1 ? ex2(m[1] - mx1) : 1.f;  // ex2(-inf) = 0
-        if (up0) m[0] = mx0;
-        if (up1) m[1] = mx1;
-        float g = 1.f;
-        if (vs > vref) {
-          g = vref / vs;
-          vref = vs;
-          vinv = 1.f / vs;
-        }
-        l[0] *= a0, l[1] *= a1;
-        const float g0 = a0 * g, g1 = a1 * g;
-#pragma unroll
-        for (int u = 0; u < NT; ++u) o[u][0] *= g0, o[u][1] *= g0, o[u][2] *= g1, o[u][3] *= g1;
-      }
-      const float ratio = vs * vinv;  // at most 1
-      const float n0 = m[0] == -INFINITY ? 0.f : m[0], n1 = m[1] == -INFINITY ? 0.f : m[1];
-      uint32_t pa[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float p0 = ex2(s[j][0] - n0), p1 = ex2(s[j][1] - n0), p2 = ex2(s[j][2] - n1), p3 = ex2(s[j][3] - n1);
-        l[0] += p0 + p1;
-        l[1] += p2 + p3;
-        pa[2 * j] = pack2<false>(p0 * ratio, p1 * ratio);
-        pa[2 * j + 1] = pack2<false>(p2 * ratio, p3 * ratio);
-      }
-      // ---- O += P V
-      constexpr int VW = VB / 4;
-      uint32_t vw[4][VW];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint8_t* at = st + 16 * D + (e * 32 + lane) * VB;
-        if constexpr (VB == 16) {
-          const uint4 w = *reinterpret_cast<const uint4*>(at);
-          vw[e][0] = w.x, vw[e][1] = w.y, vw[e][2] = w.z, vw[e][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(at);
-          vw[e][0] = w.x, vw[e][1] = w.y;
-        }
-        if (edge) {  // a zero P times a NaN byte would be NaN: keys that no row sees are zeroed
-          const int k = k0 + 2 * c4 + (e & 1) + 8 * (e >> 1);
-          if (k < kt.lo || k >= kt.hi) {
-#pragma unroll
-            for (int u = 0; u < VW; ++u) vw[e][u] = 0u;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < VW; ++u) {
-        // bytes 4u .. 4u + 3 of keys (0, 1) and (2, 3) paired: columns 4u .. 4u + 3
-        uint32_t b[4][2];
-        e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x5140), &b[0][0], &b[1][0]);
-        e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x7362), &b[2][0], &b[3][0]);
-        e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x5140), &b[0][1], &b[1][1]);
-        e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x7362), &b[2][1], &b[3][1]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) mma16816(o[u * 4 + y], pa, b[y][0], b[y][1]);
-      }
+      __syncwarp();            // every lane has read the slot,
+      issue(t + kStages);      // which is filled again
     }
-    cp_wait<0>();  // (the last groups are empty) the ring is free
 
     // ---------------------------------------------------------- the warps joined
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    // a wait that ran out: all warps leave, copies in flight land first
+    if (__syncthreads_or(!ok)) {
+      if (lane == 0) {
+        for (int i = 0; i < pending; ++i) mbar_drain(&full[(out_slot + i) % kStages], out_par ^ (out_slot + i >= kStages));
+      }
+      return;
     }
-    // every lane has read its last stage before the warp's region is reused
-    __syncwarp();
     float* const jo = reinterpret_cast<float*>(ring);
-    // O rows of D + 4 floats; column 2 c4 e' of tile u is d = (2 c4 + e') D/8 + u
+    // O rows of D + 4 floats; my values of rows 2 c4 and 2 c4 + 1 are columns [r8 VB, (r8 + 1) VB)
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < NB; ++e)
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
+      for (int y = 0; y < 2; ++y) {
+        float sum = l[e][y];
 #pragma unroll
-        for (int u = 0; u < NT; u += 4) {
-          float4 w = make_float4(o[u][2 * e + y], o[u + 1][2 * e + y], o[u + 2][2 * e + y], o[u + 3][2 * e + y]);
-          w.x *= vref, w.y *= vref, w.z *= vref, w.w *= vref;
-          *reinterpret_cast<float4*>(jo + (r8 + 8 * e) * (D + 4) + (2 * c4 + y) * NT + u) = w;
-        }
-    if (c4 == 0) {
-      ml[warp * 16 + r8] = make_float2(m[0], l[0]);
-      ml[warp * 16 + r8 + 8] = make_float2(m[1], l[1]);
-    }
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const int row = 8 * e + 2 * c4 + y;
+        if (r8 == 0) ml[warp * RT + row] = make_float2(nm[e][y], sum);
+#pragma unroll
+        for (int u = 0; u < MT; u += 2)
+          *reinterpret_cast<float4*>(jo + row * (D + 4) + r8 * VB + 2 * u) =
+              make_float4(o[e][u][y] * vref, o[e][u][2 + y] * vref, o[e][u + 1][y] * vref, o[e][u + 1][2 + y] * vref);
+      }
     __syncthreads();
     const bool whole = part0 == 0 && part1 == kt.n;
     const int slot = 2 * blockIdx.x + (part0 > 0 ? 0 : 1);
-    constexpr int ND = D / 8;  // columns a thread joins: 8 threads a row
-    const int row = tid >> 3, d0 = (tid & 7) * ND;
+    constexpr int TPR = kThreads / RT, ND = D / TPR;  // threads a row, columns a thread
+    const int row = tid / TPR, d0 = (tid % TPR) * ND;
     if (row < rows) {
-      float mm = -INFINITY, w[kWarps], ll = 0.f, acc[ND];
+      float mm = -INFINITY, ll = 0.f, acc[ND];
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, ml[i * 16 + row].x);
+      for (int i = 0; i < kWarps; ++i) {
+        const float2 v = ml[i * RT + row];
+        mm = fmaxf(mm, v.y == 0.f ? -INFINITY : v.x);
+      }
 #pragma unroll
       for (int u = 0; u < ND; ++u) acc[u] = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        const float2 v = ml[i * 16 + row];
-        w[i] = v.y == 0.f ? 0.f : ex2(v.x - mm);
-        ll += w[i] * v.y;
+        const float2 v = ml[i * RT + row];
+        if (v.y == 0.f) continue;
+        const float w = ex2(v.x - mm);
+        ll += w * v.y;
         const float* from = reinterpret_cast<const float*>(sm + i * C::REGION) + row * (D + 4) + d0;
-        if (v.y != 0.f) {
 #pragma unroll
-          for (int u = 0; u < ND; u += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(from + u);
-            acc[u] += w[i] * f.x, acc[u + 1] += w[i] * f.y, acc[u + 2] += w[i] * f.z, acc[u + 3] += w[i] * f.w;
-          }
+        for (int u = 0; u < ND; u += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(from + u);
+          acc[u] += w * f.x, acc[u + 1] += w * f.y, acc[u + 2] += w * f.z, acc[u + 3] += w * f.w;
         }
       }
       if (whole) {
@@ -529,7 +578,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_decode_kernel(const K
       const int c0 = kv_cta_of(total, begin - part0, ctas);
       p.desc[blockIdx.x] = make_int4(cur.n, cur.rt, cur.h, c0);
     }
-    __syncthreads();  // the joined rows are read before the ring fills again
+    fence_proxy_async_smem();  // (the ring's next copies come after these writes and reads)
+    __syncthreads();           // the joined rows are read before the ring fills again
 
     // ---------------------------------------------------------- next unit
     x += part1 - part0;
@@ -550,10 +600,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_decode_kernel(const K
 // CTA c finished (a CTA finishes at most one that it did not begin), its parts
 // from c0 (which began it) to c in order.  A warp a row: lanes first take the
 // parts' (m, l) together, then D/32 columns each.
-template <int D, bool BF16>
+template <int D, int RT, bool BF16>
 __global__ void __launch_bounds__(RT * 32) kv_join_kernel(const KvAttnParams p) {
   grid_dependency_wait();
   const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (c == 0 && row == 0) {  // the launch's error word
+    int e = kErrNone;
+    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) e = imax(e, p.cta_err[i]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) e = imax(e, __shfl_xor_sync(0xffffffffu, e, s));
+    if (lane == 0) *p.err = e;
+  }
   const int4 d = p.desc[c];
   if (d.x < 0) return;
   const KvReq rq = kv_request(d.x, p);
@@ -562,7 +619,10 @@ __global__ void __launch_bounds__(RT * 32) kv_join_kernel(const KvAttnParams p) 
   const int c0 = d.w, parts = c - c0 + 1;
   auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
   float m = -INFINITY;
-  for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot_of(i) * RT + row].x);
+  for (int i = lane; i < parts; i += 32) {
+    const float2 v = p.part_ml[slot_of(i) * RT + row];
+    m = fmaxf(m, v.y == 0.f ? -INFINITY : v.x);
+  }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
   constexpr int ND = D / 32;
@@ -603,22 +663,31 @@ __global__ void __launch_bounds__(RT * 32) kv_join_kernel(const KvAttnParams p) 
   if (lane == 0) store_lse(p, static_cast<int64_t>(rq.a) + i, hq, m, l);
 }
 
+template <int D, int NB, bool BF16>
+cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
+  using C = DecCfg<D, NB>;
+  auto kern = kv_decode_kernel<D, NB, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int grid = imin(sms * C::CTAS, kKvDecMaxCtas);
+  e = launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);
+  if (e != cudaSuccess) return e;
+  return launch_after_previous(kv_join_kernel<D, C::RT, BF16>, grid, C::RT * 32, 0, st, p);
+}
+
+// Units of 8 rows where a request's rows (by the mean number of its queries)
+// fit them, of 16 otherwise; either serves any number.
 template <int D, bool BF16>
-cudaError_t launch_t(const KvAttnParams& p, int sms, cudaStream_t st) {
-  auto kern = kv_decode_kernel<D, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DecCfg<D>::SMEM);
-  if (e != cudaSuccess) return e;
-  const int grid = imin(sms * kCtasPerSm, kKvDecMaxCtas);
-  e = launch_after_previous(kern, grid, kThreads, DecCfg<D>::SMEM, st, p);
-  if (e != cudaSuccess) return e;
-  return launch_after_previous(kv_join_kernel<D, BF16>, grid, RT * 32, 0, st, p);
+cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
+  const int64_t mean = (p.T + p.N - 1) / p.N;
+  return mean * p.G <= 8 ? launch_nb<D, 1, BF16>(p, maps, sms, st) : launch_nb<D, 2, BF16>(p, maps, sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_decode(const KvAttnParams& p, bool bf16, int sms, cudaStream_t st) {
-  if (p.D == 64) return bf16 ? launch_t<64, true>(p, sms, st) : launch_t<64, false>(p, sms, st);
-  return bf16 ? launch_t<128, true>(p, sms, st) : launch_t<128, false>(p, sms, st);
+cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, cudaStream_t st) {
+  if (p.D == 64) return bf16 ? launch_t<64, true>(p, maps, sms, st) : launch_t<64, false>(p, maps, sms, st);
+  return bf16 ? launch_t<128, true>(p, maps, sms, st) : launch_t<128, false>(p, maps, sms, st);
 }
 
 }  // namespace ab
