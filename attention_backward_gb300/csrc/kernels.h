@@ -142,10 +142,10 @@ attn_status_t check_gqa_call(const void* q, attn_strides_t sq, const void* k, at
 // while the previous kernel on ``st`` finishes, and waits for it with
 // grid_dependency_wait before reading its results.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_after_previous(void (*kern)(KArgs...), int grid, int threads, int smem, cudaStream_t st,
+cudaError_t launch_after_previous(void (*kern)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t st,
                                   Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;

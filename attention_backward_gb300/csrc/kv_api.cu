@@ -62,20 +62,20 @@ bool make_cache_map(CUtensorMap* m, const void* base, const attn_strides_t& st, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of attention over the cache: the header, an error word and a descriptor per CTA,
-// then two partial slots a CTA.
+// Workspace of attention over the cache: the header, an error word a CTA, a
+// flag and a descriptor a worker, then the partial rows.
 struct KvWs {
-  int64_t err_off, desc_off, ml_off, o_off, total;
+  int64_t err_off, fin_off, desc_off, ml_off, o_off, total;
 };
 
 KvWs kv_ws(int64_t D) {
   KvWs w;
-  const int64_t slots = 2 * kKvDecMaxCtas;
   w.err_off = kHeaderBytes;
-  w.desc_off = w.err_off + kKvDecMaxCtas * 4;
-  w.ml_off = w.desc_off + kKvDecMaxCtas * 16;
-  w.o_off = w.ml_off + slots * kKvDecRows * 8;
-  w.total = w.o_off + slots * kKvDecRows * D * 4;
+  w.fin_off = w.err_off + kKvDecMaxWorkers * 4;
+  w.desc_off = w.fin_off + kKvDecMaxWorkers * 4;
+  w.ml_off = w.desc_off + kKvDecMaxWorkers * 16;
+  w.o_off = w.ml_off + kKvDecMaxRows * 8;
+  w.total = w.o_off + kKvDecMaxRows * D * 4;
   return w;
 }
 
@@ -184,6 +184,7 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.err = &reinterpret_cast<WsHeader*>(ws)->err;
   p.cta_err = reinterpret_cast<int*>(ws + L.err_off);
+  p.fin = reinterpret_cast<int*>(ws + L.fin_off);
   p.desc = reinterpret_cast<int4*>(ws + L.desc_off);
   p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
   p.part_o = reinterpret_cast<float*>(ws + L.o_off);

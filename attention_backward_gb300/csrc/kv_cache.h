@@ -64,9 +64,10 @@ struct KvAttnParams {
   // workspace
   int* err;
   int* cta_err;     // per CTA: its error code
-  int4* desc;       // per CTA: the unit whose split it finishes (see kv_decode.cu)
-  float2* part_ml;  // [2 * ctas][rows] running max (log2 units) and sum
-  float* part_o;    // [2 * ctas][rows][D] unnormalised O
+  int* fin;         // per worker: the first part of that unit, or -1
+  int4* desc;       // per worker: the unit whose split it finishes (see kv_decode.cu)
+  float2* part_ml;  // [2 * workers][rows] running max (log2 units) and sum
+  float* part_o;    // [2 * workers][rows][D] unnormalised O
   uint64_t timeout_ns;
 };
 
@@ -77,11 +78,13 @@ struct KvMaps {
 };
 constexpr int kKvBoxTokens = 16;
 
-// Most rows (query, head of the group) of a decode unit, and keys per tile.
-constexpr int kKvDecRows = 16;
-constexpr int kKvDecKeys = 64;
-// Most CTAs of a launch: sizes the workspace's partials.
-constexpr int kKvDecMaxCtas = 1024;
+// Keys per tile of the decode kernel, and what starting a unit costs in tiles.
+constexpr int kKvDecKeys = 16;
+constexpr int kKvUnitCost = 2;
+// Most partial rows of a launch (2 slots a worker, 8 or 16 rows a slot) and most
+// workers: these size the workspace and bound the grid.
+constexpr int kKvDecMaxRows = 65536;
+constexpr int kKvDecMaxWorkers = kKvDecMaxRows / 16;
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);
 cudaError_t launch_kv_write(const KvWriteParams& p, bool bf16, cudaStream_t st);

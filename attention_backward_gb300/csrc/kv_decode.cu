@@ -9,12 +9,16 @@
 // only when it grows by more than 2^8).  Bound by the bytes of K and V: 2 D
 // bytes and 4 D G flops a key.
 //
-// Split: the line of kv_sched.cuh, units of 8 or 16 rows and tiles of 64 keys,
-// over persistent CTAs of 4 warps.  A warp takes 16 keys of every tile and
-// keeps its own m, l and O; the four are joined in shared memory when the unit
-// (or the CTA's part of it) ends.  A unit that one CTA holds whole is written
-// at once; parts go to the workspace, at most two a CTA, and kv_join_kernel
-// adds them in CTA order (the same result from run to run).
+// Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 16
+// keys, over persistent warps.  Every KV head has the same line, so worker
+// (warp) w takes head w % HKV and part w / HKV of its line: the warps of a CTA
+// walk the same pages of neighbouring heads together, which reads pages stored
+// token by token in rows of several heads (one head at a time, 128 B out of
+// every 1 KB, ran at two thirds of that on 64 requests of up to 8192 keys).  A
+// warp keeps m, l and O of its unit in registers and needs no other warp; a
+// unit that one warp holds whole is written at once, parts go to the workspace,
+// at most two a warp, and kv_join_kernel adds them in order (the same result
+// from run to run).
 //
 // Products: mma.m16n8k16 on fp16, transposed: S^T = K Q^T with 16 keys by 8
 // rows, O^T += V^T P^T with 16 columns by 8 rows.  tcgen05 needs 64 or 128 rows
@@ -51,17 +55,17 @@ constexpr int KT = kKvDecKeys;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kStages = 3;       // ring of 16-key slots per warp
 constexpr float kRescale = 8.f;  // log2 growth of a row max that triggers a rescale
+// Fewest line positions of a worker: below it, more parts cost more to join
+// than they save.
+constexpr int kMinWork = 8;
 
 template <int D, int NB>
 struct DecCfg {
-  static constexpr int RT = 8 * NB;                             // rows of a unit
-  static constexpr int CTAS = NB == 1 ? 4 : 3;                  // resident per SM
-  static constexpr int TILE = 16 * D;                           // bytes of K, or of V, of 16 keys
-  static constexpr int WARP = kStages * 2 * TILE;               // a warp's ring
-  static constexpr int JOIN = RT * (D + 4) * 4;                 // a warp's O rows when the warps are joined
-  static constexpr int REGION = ((WARP > JOIN ? WARP : JOIN) + 1023) / 1024 * 1024;
-  static constexpr int OFF_ML = kWarps * REGION;                // the warps' (m, l) pairs
-  static constexpr int OFF_BAR = OFF_ML + kWarps * RT * 8;
+  static constexpr int RT = 8 * NB;                  // rows of a unit
+  static constexpr int CTAS = NB == 1 ? 4 : 3;       // resident per SM
+  static constexpr int TILE = KT * D;                // bytes of K, or of V, of 16 keys
+  static constexpr int WARP = kStages * 2 * TILE;    // a warp's ring
+  static constexpr int OFF_BAR = kWarps * WARP;
   static constexpr int OFF_ABORT = OFF_BAR + kWarps * kStages * 8;
   static constexpr int SMEM = OFF_ABORT + 8;
 };
@@ -102,28 +106,25 @@ __device__ __forceinline__ float to_top(float amax, float* back) {
   return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 }
 
-// Where the tile at line position ``x`` lies.
+// Where line position ``x`` lies: request, row tile, position in the unit.
 struct Cursor {
-  int n, rt, h, t;
+  int n, rt, pos;
 };
 
-// Every thread of the CTA: the launch's tiles in all, and the cursor of the
-// CTA's first one.  A thread sums ceil(N / 128) consecutive requests; the one
-// whose requests hold the position walks them.
+// All threads of a CTA: the length of the line.  A thread sums ceil(N / 128)
+// consecutive requests; ``before`` (shared, kThreads entries) gets the sums
+// before each thread's.
 template <int RT>
-__device__ __forceinline__ void locate(const KvAttnParams& p, int64_t* total, int* ctas, int64_t* begin,
-                                       int64_t* end, Cursor* cur) {
+__device__ __forceinline__ int64_t line_length(const KvAttnParams& p, int64_t* before) {
   __shared__ int64_t s_warp[kWarps];
-  __shared__ Cursor s_cur;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = (p.N + kThreads - 1) / kThreads;
   int64_t w = 0;
   for (int i = 0; i < K; ++i) {
     const int64_t n = static_cast<int64_t>(tid) * K + i;
     if (n >= p.N) break;
-    w += kv_request_tiles<RT, KT>(kv_request(static_cast<int>(n), p), p);
+    w += kv_request_work<RT, KT>(kv_request(static_cast<int>(n), p), p);
   }
-  w *= p.HKV;
   int64_t inc = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -138,39 +139,39 @@ __device__ __forceinline__ void locate(const KvAttnParams& p, int64_t* total, in
     if (i < warp) base += s_warp[i];
     all += s_warp[i];
   }
-  *total = all;
-  // no more CTAs than tiles: every CTA of a split unit then holds some of it
-  const int C = all < static_cast<int64_t>(gridDim.x) ? static_cast<int>(all) : static_cast<int>(gridDim.x);
-  *ctas = C;
-  *begin = *end = 0;
-  if (static_cast<int>(blockIdx.x) < C) {
-    *begin = kv_cta_begin(all, blockIdx.x, C);
-    *end = kv_cta_begin(all, blockIdx.x + 1, C);
-  }
-  int64_t x = *begin - (base + inc - w);  // relative to my requests
-  if (*begin < *end && x >= 0 && x < w) {
-    for (int n = tid * K;; ++n) {
-      const KvReq r = kv_request(n, p);
-      const int64_t wn = kv_request_tiles<RT, KT>(r, p) * p.HKV;
-      if (x >= wn) {
-        x -= wn;
-        continue;
-      }
-      for (int rt = 0;; ++rt) {
-        const KvTiles k = kv_row_tile<RT, KT>(r, rt, p);
-        const int64_t wr = static_cast<int64_t>(k.n) * p.HKV;
-        if (x >= wr) {
-          x -= wr;
-          continue;
-        }
-        s_cur = Cursor{n, rt, static_cast<int>(x / k.n), static_cast<int>(x % k.n)};
-        break;
-      }
-      break;
-    }
-  }
+  before[tid] = base + inc - w;
   __syncthreads();
-  *cur = s_cur;
+  return all;
+}
+
+// A warp's cursor at position x (below the line's length).
+template <int RT>
+__device__ __forceinline__ Cursor locate(const KvAttnParams& p, const int64_t* before, int64_t x) {
+  const int K = (p.N + kThreads - 1) / kThreads;
+  int lo = 0, hi = kThreads;  // before[lo] <= x < before[lo + 1]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  x -= before[lo];
+  Cursor c{lo * K, 0, 0};
+  KvReq r;
+  while (true) {
+    r = kv_request(c.n, p);
+    const int64_t w = kv_request_work<RT, KT>(r, p);
+    if (x < w) break;
+    x -= w;
+    ++c.n;
+  }
+  while (true) {
+    const int w = kv_row_tile<RT, KT>(r, c.rt, p).n + kKvUnitCost;
+    if (x < w) break;
+    x -= w;
+    ++c.rt;
+  }
+  c.pos = static_cast<int>(x);
+  return c;
 }
 
 // Writes of one row's final O (16-bit, ND values from column d0) and LSE.
@@ -212,10 +213,10 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
   constexpr int VB = D / 8;    // bytes of a value row per thread
   constexpr int MT = D / 16;   // row tiles of O^T
   extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ int64_t before[kThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r8 = lane >> 2, c4 = lane & 3;
-  uint8_t* const ring = sm + warp * C::REGION;
-  float2* const ml = reinterpret_cast<float2*>(sm + C::OFF_ML);  // [warp][RT]
+  uint8_t* const ring = sm + warp * C::WARP;
   uint64_t* const full = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR) + warp * kStages;
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
 
@@ -229,51 +230,64 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
   // to be cleared by a launch of its own.
   const WaitCtx wc{abort_flag, p.cta_err + blockIdx.x, p.timeout_ns};
   const bool aligned = (smem_u32(sm) & 1023u) == 0;  // the swizzled tiles need it
-  if (tid == 0) {
-    *wc.err = aligned ? kErrNone : kErrAlign;
-    p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  }
-  int64_t total, begin, end;
-  int ctas;
-  Cursor cur;
-  locate<RT>(p, &total, &ctas, &begin, &end, &cur);  // (its barriers publish what thread 0 wrote)
-  if (!aligned || begin >= end) return;
+  const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
+  if (tid == 0) *wc.err = aligned ? kErrNone : kErrAlign;
+  if (lane == 0) p.fin[worker] = -1;
+  const int64_t total = line_length<RT>(p, before);  // (its barriers publish what thread 0 wrote)
+  if (!aligned || total == 0) return;
+  // Parts of a head's line, at least kMinWork positions each; with more heads
+  // than workers, one part and several heads a worker.
+  const int64_t most = imax(1, workers / p.HKV), want = (total + kMinWork - 1) / kMinWork;
+  const int parts = static_cast<int>(most < want ? most : want);
+  const int g = worker / p.HKV;
+  if (g >= parts) return;
+  const int64_t begin = kv_part_begin(total, g, parts), end = kv_part_begin(total, g + 1, parts);
   // slots filled and read so far, as (slot, parity) of the next one
   int in_slot = 0, out_slot = 0, pending = 0;
   uint32_t out_par = 0;
-  bool ok = true;
 
+  const Cursor first = locate<RT>(p, before, begin);
+  for (int head = worker % p.HKV; head < p.HKV; head += workers) {
+  Cursor cur = first;
   KvReq rq = kv_request(cur.n, p);
   for (int64_t x = begin; x < end;) {
-    // ---------------------------------------------------------- the unit and the CTA's part of it
+    // ---------------------------------------------------------- the unit and the worker's part of it
     const KvTiles kt = kv_row_tile<RT, KT>(rq, cur.rt, p);
-    const int part0 = cur.t;
-    const int64_t left = end - x;
-    const int part1 = kt.n - part0 <= left ? kt.n : part0 + static_cast<int>(left);
+    const int64_t unit0 = x - cur.pos;  // where the unit starts on the line
+    const int64_t stop = unit0 + kKvUnitCost + kt.n < end ? unit0 + kKvUnitCost + kt.n : end;
+    const int part0 = imax(0, cur.pos - kKvUnitCost);
+    const int part1 = imax(0, static_cast<int>(stop - unit0) - kKvUnitCost);
     const int row0 = cur.rt * RT;
     const int rows = imin(RT, rq.R - row0);
 
-    // Page ids of my slots, 32 tiles at a time: lane i holds that of tile
-    // ``batch + i`` (-1: no page, or no key that the unit sees).
-    auto key0_of = [&](int t) { return (kt.t0 + t) * KT + warp * 16; };
-    auto load_ids = [&](int batch) {
-      const int t = batch + lane;
-      int b = -1;
+    // Page ids of my slots and their scales, 32 tiles at a time: lane i holds
+    // those of tile ``ld_batch + i`` (-1: no page, or no key that the unit sees).
+    auto key0_of = [&](int t) { return (kt.t0 + t) * KT; };
+    int ld_batch = part0, ld_blk = -1;
+    float ld_ks = 0.f, ld_vs = 0.f;
+    auto load_ids = [&]() {
+      const int t = ld_batch + lane;
+      ld_blk = -1, ld_ks = ld_vs = 0.f;
       if (t < part1) {
         const int k0 = key0_of(t);
-        if (k0 < kt.hi && k0 + 16 > kt.lo) {
-          b = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
-          if (b < 0 || b >= p.num_blocks) b = -1;
+        if (k0 < kt.hi && k0 + KT > kt.lo) {
+          ld_blk = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
+          if (ld_blk < 0 || ld_blk >= p.num_blocks) ld_blk = -1;
         }
       }
-      return b;
     };
-    int ld_batch = part0, ld_blk = load_ids(part0);
+    auto load_scales = [&]() {
+      if (ld_blk >= 0) {
+        const int64_t at = static_cast<int64_t>(ld_blk) * p.HKV + head;
+        ld_ks = p.k_scale[at], ld_vs = p.v_scale[at];
+      }
+    };
     auto issue = [&](int t) {  // copies of tile t's 16 keys into the next slot
       if (t >= part1) return;
       if (t - ld_batch == 32) {
         ld_batch = t;
-        ld_blk = load_ids(t);
+        load_ids();
+        load_scales();
       }
       const int b = __shfl_sync(0xffffffffu, ld_blk, t - ld_batch);
       if (lane == 0) {
@@ -282,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
           uint8_t* const dst = ring + in_slot * (2 * C::TILE);
           const int s0 = key0_of(t) & ((1 << p.page_log2) - 1);
           mbar_arrive_expect_tx(bar, 2 * C::TILE);
-          tma_load_4d(dst, &maps.k, bar, 0, cur.h, s0, b);
-          tma_load_4d(dst + C::TILE, &maps.v, bar, 0, cur.h, s0, b);
+          tma_load_4d(dst, &maps.k, bar, 0, head, s0, b);
+          tma_load_4d(dst + C::TILE, &maps.v, bar, 0, head, s0, b);
         } else {
           mbar_arrive(bar);
         }
@@ -291,8 +305,10 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
       in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
       ++pending;
     };
+    load_ids();
 #pragma unroll
     for (int i = 0; i < kStages; ++i) issue(part0 + i);
+    load_scales();
 
     // Q in fp16: the thread holds row r8 of each 8 rows; the scores of a thread
     // belong to rows 2 c4 and 2 c4 + 1
@@ -303,9 +319,9 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
     for (int e = 0; e < NB; ++e) {
       const int r = r8 + 8 * e;
       const bool live = r < rows;
-      const int i = (row0 + r) / p.G, g = (row0 + r) % p.G;
+      const int i = (row0 + r) / p.G, gq = (row0 + r) % p.G;
       const uint8_t* src = p.q + 2 * ((static_cast<int64_t>(rq.a) + i) * p.sq_s +
-                                      static_cast<int64_t>(cur.h * p.G + g) * p.sq_h);
+                                      static_cast<int64_t>(head * p.G + gq) * p.sq_h);
       uint32_t w[KC][8];
       float amax = 0.f;
 #pragma unroll
@@ -360,19 +376,15 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
       for (int t = 0; t < MT; ++t) o[e][t][0] = o[e][t][1] = o[e][t][2] = o[e][t][3] = 0.f;
     }
 
-    float ks_l = 0.f, vs_l = 0.f;  // scales of the 32 tiles being computed,
-    int cp_blk = -1;               // and their ids (the load side may be ahead)
+    float ks_l = 0.f, vs_l = 0.f;  // scales of the 32 tiles being computed, and
+    int cp_blk = -1;               // their ids
     int cp_batch = part0 - 32;
+    bool ok = true;
     for (int t = part0; t < part1; ++t) {
-      if (t - cp_batch == 32) {
+      if (t - cp_batch == 32) {  // (the copies are kStages tiles ahead: in this batch already)
         cp_batch = t;
-        cp_blk = load_ids(t);
-        ks_l = vs_l = 0.f;
-        if (cp_blk >= 0) {
-          const int64_t at = static_cast<int64_t>(cp_blk) * p.HKV + cur.h;
-          ks_l = p.k_scale[at];
-          vs_l = p.v_scale[at] < 0x1p-126f ? 0.f : p.v_scale[at];  // (its inverse is taken)
-        }
+        cp_blk = ld_blk, ks_l = ld_ks;
+        vs_l = ld_vs < 0x1p-126f ? 0.f : ld_vs;  // (its inverse is taken)
       }
       const int bi = t - cp_batch;
       const float ks = __shfl_sync(0xffffffffu, ks_l, bi), vs = __shfl_sync(0xffffffffu, vs_l, bi);
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
       --pending;
       if (have) {
         const int k0 = key0_of(t);
-        const bool edge = k0 < lo_all || k0 + 16 > hi_all;
+        const bool edge = k0 < lo_all || k0 + KT > hi_all;
         // ---- S^T of 16 keys by 8 NB rows, in two chains
         float s2[NB][2][4], s[NB][4];
 #pragma unroll
@@ -507,160 +519,210 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
       issue(t + kStages);      // which is filled again
     }
 
-    // ---------------------------------------------------------- the warps joined
-    // a wait that ran out: all warps leave, copies in flight land first
-    if (__syncthreads_or(!ok)) {
-      if (lane == 0) {
-        for (int i = 0; i < pending; ++i) mbar_drain(&full[(out_slot + i) % kStages], out_par ^ (out_slot + i >= kStages));
-      }
+    if (!ok) {  // a wait that ran out: the copies in flight land before the warp leaves
+      if (lane == 0)
+        for (int i = 0; i < pending; ++i)
+          mbar_drain(&full[(out_slot + i) % kStages], out_par ^ (out_slot + i >= kStages ? 1u : 0u));
       return;
     }
-    float* const jo = reinterpret_cast<float*>(ring);
-    // O rows of D + 4 floats; my values of rows 2 c4 and 2 c4 + 1 are columns [r8 VB, (r8 + 1) VB)
+
+    // ---------------------------------------------------------- the unit's rows, or my part of them
+    if (part1 > part0) {
+      const bool whole = part0 == 0 && part1 == kt.n;
+      const int slot = 2 * worker + (part0 > 0 ? 0 : 1);
 #pragma unroll
-    for (int e = 0; e < NB; ++e)
+      for (int e = 0; e < NB; ++e)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float sum = l[e][y];
+        for (int y = 0; y < 2; ++y) {
+          float sum = l[e][y];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const int row = 8 * e + 2 * c4 + y;
-        if (r8 == 0) ml[warp * RT + row] = make_float2(nm[e][y], sum);
+          for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const int row = 8 * e + 2 * c4 + y;
+          if (row >= rows) continue;
+          // columns [r8 VB, (r8 + 1) VB)
+          const float f = whole ? (sum == 0.f ? 0.f : vref / sum) : vref;
+          float v[VB];
 #pragma unroll
-        for (int u = 0; u < MT; u += 2)
-          *reinterpret_cast<float4*>(jo + row * (D + 4) + r8 * VB + 2 * u) =
-              make_float4(o[e][u][y] * vref, o[e][u][2 + y] * vref, o[e][u + 1][y] * vref, o[e][u + 1][2 + y] * vref);
-      }
-    __syncthreads();
-    const bool whole = part0 == 0 && part1 == kt.n;
-    const int slot = 2 * blockIdx.x + (part0 > 0 ? 0 : 1);
-    constexpr int TPR = kThreads / RT, ND = D / TPR;  // threads a row, columns a thread
-    const int row = tid / TPR, d0 = (tid % TPR) * ND;
-    if (row < rows) {
-      float mm = -INFINITY, ll = 0.f, acc[ND];
+          for (int u = 0; u < MT; ++u) v[2 * u] = o[e][u][y] * f, v[2 * u + 1] = o[e][u][2 + y] * f;
+          if (whole) {
+            const int64_t at = static_cast<int64_t>(rq.a) + (row0 + row) / p.G;
+            const int hq = head * p.G + (row0 + row) % p.G;
+            store_o<BF16, VB>(p, at, hq, r8 * VB, v);
+            if (r8 == 0) store_lse(p, at, hq, nm[e][y], sum);
+          } else {
+            float* const to = p.part_o + (static_cast<int64_t>(slot) * RT + row) * D + r8 * VB;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float2 v = ml[i * RT + row];
-        mm = fmaxf(mm, v.y == 0.f ? -INFINITY : v.x);
-      }
-#pragma unroll
-      for (int u = 0; u < ND; ++u) acc[u] = 0.f;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float2 v = ml[i * RT + row];
-        if (v.y == 0.f) continue;
-        const float w = ex2(v.x - mm);
-        ll += w * v.y;
-        const float* from = reinterpret_cast<const float*>(sm + i * C::REGION) + row * (D + 4) + d0;
-#pragma unroll
-        for (int u = 0; u < ND; u += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(from + u);
-          acc[u] += w * f.x, acc[u + 1] += w * f.y, acc[u + 2] += w * f.z, acc[u + 3] += w * f.w;
+            for (int u = 0; u < VB; u += 4)
+              *reinterpret_cast<float4*>(to + u) = make_float4(v[u], v[u + 1], v[u + 2], v[u + 3]);
+            if (r8 == 0) p.part_ml[slot * RT + row] = make_float2(nm[e][y], sum);
+          }
         }
-      }
-      if (whole) {
-        const int i = (row0 + row) / p.G, hq = cur.h * p.G + (row0 + row) % p.G;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-#pragma unroll
-        for (int u = 0; u < ND; ++u) acc[u] *= inv;
-        store_o<BF16, ND>(p, static_cast<int64_t>(rq.a) + i, hq, d0, acc);
-        if (d0 == 0) store_lse(p, static_cast<int64_t>(rq.a) + i, hq, mm, ll);
-      } else {
-        float* to = p.part_o + (static_cast<int64_t>(slot) * RT + row) * D + d0;
-#pragma unroll
-        for (int u = 0; u < ND; u += 4)
-          *reinterpret_cast<float4*>(to + u) = make_float4(acc[u], acc[u + 1], acc[u + 2], acc[u + 3]);
-        if (d0 == 0) p.part_ml[slot * RT + row] = make_float2(mm, ll);
+      if (lane == 0 && part0 > 0 && part1 == kt.n) {  // ends a unit that part g0 began
+        const int g0 = kv_part_of(total, unit0 + kKvUnitCost, parts);
+        p.desc[worker] = make_int4(cur.n, cur.rt, head, g0);
+        p.fin[worker] = g0;
       }
     }
-    if (tid == 0 && part0 > 0 && part1 == kt.n) {
-      // this part ends a unit that CTA c0 began
-      const int c0 = kv_cta_of(total, begin - part0, ctas);
-      p.desc[blockIdx.x] = make_int4(cur.n, cur.rt, cur.h, c0);
-    }
-    fence_proxy_async_smem();  // (the ring's next copies come after these writes and reads)
-    __syncthreads();           // the joined rows are read before the ring fills again
 
     // ---------------------------------------------------------- next unit
-    x += part1 - part0;
-    cur.t = 0;
-    if (x < end && ++cur.h == p.HKV) {
-      cur.h = 0;
-      if (++cur.rt == kv_row_tiles<RT>(rq)) {
-        cur.rt = 0;
-        do {
-          rq = kv_request(++cur.n, p);
-        } while (rq.R == 0);
-      }
+    x = stop;
+    cur.pos = 0;
+    if (x < end && ++cur.rt == kv_row_tiles<RT>(rq)) {
+      cur.rt = 0;
+      do {
+        rq = kv_request(++cur.n, p);
+      } while (rq.R == 0);
     }
+  }
   }
 }
 
-// Joins the parts of each unit that was split over CTAs: block c the unit that
-// CTA c finished (a CTA finishes at most one that it did not begin), its parts
-// from c0 (which began it) to c in order.  A warp a row: lanes first take the
-// parts' (m, l) together, then D/32 columns each.
+// Joins the parts of each unit that was split over workers: entry w of ``desc``
+// names the unit that worker w finished (a worker finishes at most one that it
+// did not begin), its parts d.w to w / HKV in order; ``fin`` holds d.w, or -1
+// where there is none.  Every block lists the finished units (a scan of one
+// flag a worker); their rows are then spread over all warps of the launch,
+// with as many warps a row as there are to spare.  These add fixed shares of
+// the parts in order: lanes first take the parts' (m, l) together, then D/32
+// columns each.  Latency-bound: a few parts a unit as a rule, hundreds where few
+// requests have all the workers.
+constexpr int kJoinWarps = 16;
+
 template <int D, int RT, bool BF16>
-__global__ void __launch_bounds__(RT * 32) kv_join_kernel(const KvAttnParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnParams p, int ctas) {
+  constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
+  __shared__ uint16_t list[kKvDecMaxWorkers];
+  __shared__ int s_cnt[kJoinWarps];
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
   grid_dependency_wait();
-  const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (c == 0 && row == 0) {  // the launch's error word
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int workers = ctas * kWarps;
+  if (blockIdx.x == 0 && warp == 0) {  // the launch's error word
     int e = kErrNone;
-    for (int i = lane; i < static_cast<int>(gridDim.x); i += 32) e = imax(e, p.cta_err[i]);
+    for (int i = lane; i < ctas; i += 32) e = imax(e, p.cta_err[i]);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) e = imax(e, __shfl_xor_sync(0xffffffffu, e, s));
     if (lane == 0) *p.err = e;
   }
-  const int4 d = p.desc[c];
-  if (d.x < 0) return;
-  const KvReq rq = kv_request(d.x, p);
-  const int row0 = d.y * RT;
-  if (row0 + row >= rq.R) return;
-  const int c0 = d.w, parts = c - c0 + 1;
-  auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-  float m = -INFINITY;
-  for (int i = lane; i < parts; i += 32) {
-    const float2 v = p.part_ml[slot_of(i) * RT + row];
-    m = fmaxf(m, v.y == 0.f ? -INFINITY : v.x);
-  }
+  uint32_t mine = 0;  // my PER workers that finished a unit
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  constexpr int ND = D / 32;
-  float acc[ND], l = 0.f;
-#pragma unroll
-  for (int u = 0; u < ND; ++u) acc[u] = 0.f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < parts) {
-      const float2 v = p.part_ml[slot_of(i0 + lane) * RT + row];
-      w = v.y == 0.f ? 0.f : ex2(v.x - m);
-      l += w * v.y;
+  for (int i = 0; i < PER; i += 4) {
+    if (tid * PER + i < workers) {  // (workers and PER are multiples of 4)
+      const int4 f = *reinterpret_cast<const int4*>(p.fin + tid * PER + i);
+      mine |= ((f.x >= 0 ? 1u : 0u) | (f.y >= 0 ? 2u : 0u) | (f.z >= 0 ? 4u : 0u) | (f.w >= 0 ? 8u : 0u)) << i;
     }
-    const int n = imin(32, parts - i0);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float f = __shfl_sync(0xffffffffu, w, i);
-      const float* from = p.part_o + (static_cast<int64_t>(slot_of(i0 + i)) * RT + row) * D + lane * ND;
-      float v[ND];
-      if constexpr (ND == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(from);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(from);
-        v[0] = x.x, v[1] = x.y;
+  }
+  int at0 = __popc(mine);
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at0, s);
+    if (lane >= s) at0 += v;
+  }
+  if (lane == 31) s_cnt[warp] = at0;
+  __syncthreads();
+  at0 -= __popc(mine);
+  int units = 0;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) {
+    if (i < warp) at0 += s_cnt[i];
+    units += s_cnt[i];
+  }
+  for (uint32_t m = mine; m != 0; m &= m - 1) list[at0++] = static_cast<uint16_t>(tid * PER + __ffs(m) - 1);
+  __syncthreads();
+  const int rows = units * RT;  // those past a unit's last row are skipped
+  int shares = 1;               // warps a row
+  while (shares < kJoinWarps && rows * shares * 2 <= static_cast<int>(gridDim.x) * kJoinWarps) shares *= 2;
+  const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
+  for (int r0 = blockIdx.x * groups; r0 < rows; r0 += gridDim.x * groups) {
+    const int item = r0 + group;
+    KvReq rq{};
+    int4 d = make_int4(-1, 0, 0, 0);
+    int row0 = 0, live = 0, i0 = 0, i1 = 0;
+    const int row = item % RT;
+    if (item < rows) {
+      const int w = list[item / RT];
+      d = p.desc[w];
+      rq = kv_request(d.x, p);
+      row0 = d.y * RT, live = imin(RT, rq.R - row0);
+      const int parts = w / p.HKV - d.w + 1;
+      i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
+    }
+    auto slot_of = [&](int i) { return 2 * ((d.w + i) * p.HKV + d.z) + (i == 0 ? 1 : 0); };
+    float m = -INFINITY, l = 0.f, acc[ND];
+#pragma unroll
+    for (int u = 0; u < ND; ++u) acc[u] = 0.f;
+    if (row < live) {
+      for (int j = i0; j < i1; j += 32) {
+        // (m, l) of up to 32 parts, then their rows, rescaled where m grows
+        const float2 v = j + lane < i1 ? p.part_ml[slot_of(j + lane) * RT + row] : make_float2(0.f, 0.f);
+        float mx = v.y == 0.f ? -INFINITY : v.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        mx = fmaxf(mx, m);
+        if (mx > m) {
+          const float g = m == -INFINITY ? 0.f : ex2(m - mx);
+          l *= g;
+#pragma unroll
+          for (int u = 0; u < ND; ++u) acc[u] *= g;
+          m = mx;
+        }
+        const float f = v.y == 0.f ? 0.f : ex2(v.x - m);
+        l += f * v.y;
+        const int n = imin(32, i1 - j);
+        for (int i = 0; i < n; i += 8) {  // eight rows in flight
+          float x[8][ND];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int at = slot_of(j + imin(i + k, n - 1));
+            const float* from = p.part_o + (static_cast<int64_t>(at) * RT + row) * D + lane * ND;
+            if constexpr (ND == 4) {
+              const float4 y = *reinterpret_cast<const float4*>(from);
+              x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+            } else {
+              const float2 y = *reinterpret_cast<const float2*>(from);
+              x[k][0] = y.x, x[k][1] = y.y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, (i + k) & 31);
+            if (i + k < n && fk != 0.f) {  // (a part that saw no key of the row says nothing)
+#pragma unroll
+              for (int u = 0; u < ND; ++u) acc[u] += fk * x[k][u];
+            }
+          }
+        }
       }
 #pragma unroll
-      for (int u = 0; u < ND; ++u) acc[u] += f != 0.f ? f * v[u] : 0.f;
+      for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+      if (share > 0) {
+#pragma unroll
+        for (int u = 0; u < ND; ++u) s_o[warp][lane * ND + u] = acc[u];
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
+      }
     }
+    if (shares > 1) __syncthreads();
+    if (share == 0 && row < live) {
+      for (int k = 1; k < shares; ++k) {
+        const float2 v = s_ml[warp + k];
+        if (v.y == 0.f) continue;
+        const float mx = fmaxf(m, v.x), g = l == 0.f ? 0.f : ex2(m - mx), f = ex2(v.x - mx);
+        l = l * g + v.y * f;
+        m = mx;
+#pragma unroll
+        for (int u = 0; u < ND; ++u) acc[u] = acc[u] * g + s_o[warp + k][lane * ND + u] * f;
+      }
+      const int64_t at = static_cast<int64_t>(rq.a) + (row0 + row) / p.G;
+      const int hq = d.z * p.G + (row0 + row) % p.G;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int u = 0; u < ND; ++u) acc[u] *= inv;
+      store_o<BF16, ND>(p, at, hq, lane * ND, acc);
+      if (lane == 0) store_lse(p, at, hq, m, l);
+    }
+    if (shares > 1) __syncthreads();
   }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-  const int i = (row0 + row) / p.G, hq = d.z * p.G + (row0 + row) % p.G;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int u = 0; u < ND; ++u) acc[u] *= inv;
-  store_o<BF16, ND>(p, static_cast<int64_t>(rq.a) + i, hq, lane * ND, acc);
-  if (lane == 0) store_lse(p, static_cast<int64_t>(rq.a) + i, hq, m, l);
 }
 
 template <int D, int NB, bool BF16>
@@ -669,10 +731,10 @@ cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaSt
   auto kern = kv_decode_kernel<D, NB, BF16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const int grid = imin(sms * C::CTAS, kKvDecMaxCtas);
+  const int grid = imin(sms * C::CTAS, kKvDecMaxRows / (2 * kWarps * C::RT));
   e = launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);
   if (e != cudaSuccess) return e;
-  return launch_after_previous(kv_join_kernel<D, C::RT, BF16>, grid, C::RT * 32, 0, st, p);
+  return launch_after_previous(kv_join_kernel<D, C::RT, BF16>, 2 * sms, kJoinWarps * 32, 0, st, p, grid);
 }
 
 // Units of 8 rows where a request's rows (by the mean number of its queries)

@@ -4,11 +4,13 @@
 // A unit is a row tile (RT consecutive rows of a request, row = query * G +
 // head of the group) of one KV head, with the key tiles of KT keys that some
 // row of it sees; a unit that sees nothing has one empty tile, so that its
-// rows are written.  Units are ordered by request, row tile, head (heads
-// innermost), which lays all tiles of the launch on one line; CTA c of C takes
-// the tiles [W c / C, W (c + 1) / C) of its W tiles.  So every CTA gets the
-// same work whatever the lengths, a long row spreads over many CTAs and many
-// short ones share a CTA, and no length is needed on the host.
+// rows are written.  A head's units, ordered by request and row tile, are laid
+// on one line, each as kKvUnitCost positions for its start and end (its table
+// row, its queries, its first copies: about as long as that many tiles) and one
+// position a tile.  Part g of C takes the positions [W g / C, W (g + 1) / C) of
+// the W: every part gets the same work whatever the lengths, a long row spreads
+// over many parts, many short ones share a part, and no length is needed on
+// the host.
 #pragma once
 #include "kv_cache.h"
 
@@ -70,21 +72,21 @@ __host__ __device__ __forceinline__ int kv_row_tiles(const KvReq& r) {
   return (r.R + RT - 1) / RT;
 }
 
-// Tiles of one KV head of a request.
+// Positions of a request on a head's line.
 template <int RT, int KT>
-__host__ __device__ __forceinline__ int64_t kv_request_tiles(const KvReq& r, const KvAttnParams& p) {
+__host__ __device__ __forceinline__ int64_t kv_request_work(const KvReq& r, const KvAttnParams& p) {
   int64_t w = 0;
   const int nt = kv_row_tiles<RT>(r);
-  for (int rt = 0; rt < nt; ++rt) w += kv_row_tile<RT, KT>(r, rt, p).n;
+  for (int rt = 0; rt < nt; ++rt) w += kv_row_tile<RT, KT>(r, rt, p).n + kKvUnitCost;
   return w;
 }
 
-// First and last-but-one tile of CTA c of C, and the CTA that holds tile x.
-__host__ __device__ __forceinline__ int64_t kv_cta_begin(int64_t total, int c, int C) { return total * c / C; }
-__host__ __device__ __forceinline__ int kv_cta_of(int64_t total, int64_t x, int C) {
+// First position of part c of C, and the part that holds position x.
+__host__ __device__ __forceinline__ int64_t kv_part_begin(int64_t total, int c, int C) { return total * c / C; }
+__host__ __device__ __forceinline__ int kv_part_of(int64_t total, int64_t x, int C) {
   int c = static_cast<int>((x * C) / total);
-  while (c > 0 && kv_cta_begin(total, c, C) > x) --c;
-  while (c + 1 < C && kv_cta_begin(total, c + 1, C) <= x) ++c;
+  while (c > 0 && kv_part_begin(total, c, C) > x) --c;
+  while (c + 1 < C && kv_part_begin(total, c + 1, C) <= x) ++c;
   return c;
 }
 
