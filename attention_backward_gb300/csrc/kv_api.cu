@@ -62,21 +62,35 @@ bool make_cache_map(CUtensorMap* m, const void* base, const attn_strides_t& st, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Workspace of attention over the cache: the header, an error word a CTA, a
-// flag and a descriptor a worker, then the partial rows.
+// Workspace of attention over the cache: the header, then for each of its two
+// kernels an error word a CTA, a flag and a descriptor a worker, and the
+// partial rows.
 struct KvWs {
   int64_t err_off, fin_off, desc_off, ml_off, o_off, total;
 };
 
-KvWs kv_ws(int64_t D) {
+KvWs kv_ws(int64_t start, int64_t workers, int64_t rows, int64_t D) {
   KvWs w;
-  w.err_off = kHeaderBytes;
-  w.fin_off = w.err_off + kKvDecMaxWorkers * 4;
-  w.desc_off = w.fin_off + kKvDecMaxWorkers * 4;
-  w.ml_off = w.desc_off + kKvDecMaxWorkers * 16;
-  w.o_off = w.ml_off + kKvDecMaxRows * 8;
-  w.total = w.o_off + kKvDecMaxRows * D * 4;
+  w.err_off = start;
+  w.fin_off = w.err_off + round_up(workers * 4, 256);
+  w.desc_off = w.fin_off + round_up(workers * 4, 256);
+  w.ml_off = w.desc_off + workers * 16;
+  w.o_off = w.ml_off + rows * 8;
+  w.total = w.o_off + rows * D * 4;
   return w;
+}
+KvWs kv_ws_decode(int64_t D) { return kv_ws(kHeaderBytes, kKvDecMaxWorkers, kKvDecMaxRows, D); }
+KvWs kv_ws_prompt(int64_t D) { return kv_ws(kv_ws_decode(D).total, kKvPrMaxCtas, 2 * kKvPrMaxCtas * kKvPrRows, D); }
+
+// Whether a call of T queries may hold a request of kKvPrMinRows rows or more.
+bool kv_may_prompt(int64_t T, int64_t G) { return T * G >= kKvPrMinRows; }
+
+void kv_place(KvAttnParams* p, const KvWs& w, uint8_t* ws) {
+  p->cta_err = reinterpret_cast<int*>(ws + w.err_off);
+  p->fin = reinterpret_cast<int*>(ws + w.fin_off);
+  p->desc = reinterpret_cast<int4*>(ws + w.desc_off);
+  p->part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
+  p->part_o = reinterpret_cast<float*>(ws + w.o_off);
 }
 
 }  // namespace
@@ -141,7 +155,7 @@ attn_status_t attn_kv_cache_write(const void* k, attn_strides_t sk, const void* 
 
 size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int64_t HKV, int64_t D) {
   if (T < 0 || HQ < 1 || HKV < 1 || HQ % HKV || (D != 64 && D != 128) || T >= kMax32 / HQ) return 0;
-  return static_cast<size_t>(kv_ws(D).total);
+  return static_cast<size_t>(kv_may_prompt(T, HQ / HKV) ? kv_ws_prompt(D).total : kv_ws_decode(D).total);
 }
 
 attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int64_t HQ, attn_dtype_t dtype,
@@ -165,8 +179,7 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   for (const attn_strides_t* s : {&sq, &so})
     if (!stride_ok(s->s, 2) || !stride_ok(s->h, 2)) return ATTN_ERR_INVALID_ARG;
   if (slse.s < 1 || slse.h < 1) return ATTN_ERR_INVALID_ARG;
-  const KvWs L = kv_ws(cache->D);
-  if (workspace_bytes < static_cast<size_t>(L.total)) return ATTN_ERR_WORKSPACE;
+  if (workspace_bytes < attn_fwd_kv_cache_workspace_size(T, HQ, cache->HKV, cache->D)) return ATTN_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   KvAttnParams p{};
   p.q = static_cast<const uint8_t*>(q), p.sq_s = sq.s, p.sq_h = sq.h;
@@ -183,16 +196,28 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   p.causal = causal ? 1 : 0, p.window = window_left;
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.err = &reinterpret_cast<WsHeader*>(ws)->err;
-  p.cta_err = reinterpret_cast<int*>(ws + L.err_off);
-  p.fin = reinterpret_cast<int*>(ws + L.fin_off);
-  p.desc = reinterpret_cast<int4*>(ws + L.desc_off);
-  p.part_ml = reinterpret_cast<float2*>(ws + L.ml_off);
-  p.part_o = reinterpret_cast<float*>(ws + L.o_off);
   p.timeout_ns = kWaitTimeoutNs;
   KvMaps maps;
   if (!make_cache_map(&maps.k, cache->k, cache->sk, *cache) || !make_cache_map(&maps.v, cache->v, cache->sv, *cache))
     return ATTN_ERR_INVALID_ARG;
-  return launch_status(launch_kv_decode(p, maps, dtype == ATTN_DT_BF16, sm_count(), static_cast<cudaStream_t>(stream)));
+  const bool bf16 = dtype == ATTN_DT_BF16;
+  const int sms = sm_count();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Which kernels: requests of kKvPrMinRows rows or more go to the prompt kernel.
+  // Its launches are left out where there can be none, or where the mean request
+  // is so small that one would be the odd one out of a decode step (the decode
+  // kernel serves any number of rows).
+  const bool prompts = kv_may_prompt(T, p.G) && T * p.G >= num_seqs * (kKvPrMinRows / 4);
+  const bool decodes = !prompts || num_seqs > 1 || T * p.G < kKvPrMinRows;
+  p.rows_min = 0, p.rows_max = prompts ? kKvPrMinRows - 1 : 0x7fffffff;
+  if (decodes) {
+    kv_place(&p, kv_ws_decode(cache->D), ws);
+    if (const cudaError_t e = launch_kv_decode(p, maps, bf16, sms, st); e != cudaSuccess) return launch_status(e);
+  }
+  if (!prompts) return ATTN_OK;
+  p.rows_min = decodes ? kKvPrMinRows : 0, p.rows_max = 0x7fffffff;
+  kv_place(&p, kv_ws_prompt(cache->D), ws);
+  return launch_status(launch_kv_prompt(p, maps, bf16, sms, !decodes, st));
 }
 
 }  // extern "C"

@@ -60,7 +60,8 @@ struct KvAttnParams {
   const int* kv_lens;
   int N, T, HQ, HKV, G, D;
   int causal, window;
-  float scale_log2;  // sm_scale * log2(e), > 0
+  int rows_min, rows_max;  // requests of other sizes are left to another kernel
+  float scale_log2;        // sm_scale * log2(e), > 0
   // workspace
   int* err;
   int* cta_err;     // per CTA: its error code
@@ -78,16 +79,33 @@ struct KvMaps {
 };
 constexpr int kKvBoxTokens = 16;
 
-// Keys per tile of the decode kernel, and what starting a unit costs in tiles.
+// Requests of at least this many rows (queries * heads of a group) go to the
+// prompt kernel, the others to the decode kernel.
+constexpr int kKvPrMinRows = 65;
+
+// Decode kernel: keys per tile, and what starting a unit costs in tiles.
 constexpr int kKvDecKeys = 16;
-constexpr int kKvUnitCost = 2;
+constexpr int kKvDecCost = 2;
 // Most partial rows of a launch (2 slots a worker, 8 or 16 rows a slot) and most
 // workers: these size the workspace and bound the grid.
 constexpr int kKvDecMaxRows = 65536;
 constexpr int kKvDecMaxWorkers = kKvDecMaxRows / 16;
 
+// Prompt kernel: rows of a unit, keys per block, what starting a unit costs in
+// blocks, fewest line positions of a CTA's part, most CTAs.
+constexpr int kKvPrRows = 256;
+constexpr int kKvPrKeys = 128;
+constexpr int kKvPrCost = 3;
+constexpr int kKvPrMinWork = 5;
+constexpr int kKvPrMaxCtas = 160;
+
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);
 cudaError_t launch_kv_write(const KvWriteParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_kv_prompt(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, bool first, cudaStream_t st);
+// Joins split rows: units of rt rows, ``workers`` workers in ``ctas`` CTAs, ``stride`` of them to a part; ``first``:
+// the error word is written, not added to.
+cudaError_t launch_kv_join(const KvAttnParams& p, bool bf16, int rt, int workers, int ctas, int stride, bool first,
+                           int grid, cudaStream_t st);
 
 }  // namespace ab

@@ -44,6 +44,7 @@
 #include "cvt.cuh"
 #include "kernels.h"
 #include "kv_cache.h"
+#include "kv_common.cuh"
 #include "kv_sched.cuh"
 #include "sm103.cuh"
 
@@ -70,13 +71,6 @@ struct DecCfg {
   static constexpr int SMEM = OFF_ABORT + 8;
 };
 
-// Four e4m3 bytes -> two fp16 pairs (exact).
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* lo, uint32_t* hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(*lo), "=r"(*hi)
-      : "r"(w));
-}
-
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
@@ -90,20 +84,6 @@ __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Power of two that brings a largest absolute value into [2^14, 2^15), and its
-// inverse; 1 for 0, infinities and NaN.
-__device__ __forceinline__ float to_top(float amax, float* back) {
-  const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased
-  if (!(amax > 0.f) || e == 255) {
-    *back = 1.f;
-    return 1.f;
-  }
-  int up = 14 - (e - 127);
-  up = up > 126 ? 126 : up;  // subnormal rows
-  *back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-  return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 }
 
 // Where line position ``x`` lies: request, row tile, position in the unit.
@@ -123,7 +103,7 @@ __device__ __forceinline__ int64_t line_length(const KvAttnParams& p, int64_t* b
   for (int i = 0; i < K; ++i) {
     const int64_t n = static_cast<int64_t>(tid) * K + i;
     if (n >= p.N) break;
-    w += kv_request_work<RT, KT>(kv_request(static_cast<int>(n), p), p);
+    w += kv_request_work<RT, KT, kKvDecCost>(kv_request(static_cast<int>(n), p), p);
   }
   int64_t inc = w;
 #pragma unroll
@@ -159,49 +139,19 @@ __device__ __forceinline__ Cursor locate(const KvAttnParams& p, const int64_t* b
   KvReq r;
   while (true) {
     r = kv_request(c.n, p);
-    const int64_t w = kv_request_work<RT, KT>(r, p);
+    const int64_t w = kv_request_work<RT, KT, kKvDecCost>(r, p);
     if (x < w) break;
     x -= w;
     ++c.n;
   }
   while (true) {
-    const int w = kv_row_tile<RT, KT>(r, c.rt, p).n + kKvUnitCost;
+    const int w = kv_row_tile<RT, KT>(r, c.rt, p).n + kKvDecCost;
     if (x < w) break;
     x -= w;
     ++c.rt;
   }
   c.pos = static_cast<int>(x);
   return c;
-}
-
-// Writes of one row's final O (16-bit, ND values from column d0) and LSE.
-template <bool BF16, int ND>
-__device__ __forceinline__ void store_o(const KvAttnParams& p, int64_t t, int hq, int d0, const float* o) {
-  uint8_t* out = p.o + 2 * (t * p.so_s + static_cast<int64_t>(hq) * p.so_h + d0);
-  if constexpr (ND >= 8) {
-#pragma unroll
-    for (int i = 0; i < ND; i += 8) {
-      uint4 w;
-      w.x = pack2<BF16>(o[i], o[i + 1]), w.y = pack2<BF16>(o[i + 2], o[i + 3]);
-      w.z = pack2<BF16>(o[i + 4], o[i + 5]), w.w = pack2<BF16>(o[i + 6], o[i + 7]);
-      *reinterpret_cast<uint4*>(out + 2 * i) = w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < ND; i += 2) *reinterpret_cast<uint32_t*>(out + 2 * i) = pack2<BF16>(o[i], o[i + 1]);
-  }
-}
-
-// m in log2 units; a row that saw no key has l = 0.
-__device__ __forceinline__ void store_lse(const KvAttnParams& p, int64_t t, int hq, float m, float l) {
-  p.lse[hq * p.sl_h + t * p.sl_s] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-}
-
-// Byte offset of 16-byte chunk ``c`` of row ``r`` in a tile of D-byte rows, as
-// the copies' 128-byte (D = 128) or 64-byte (D = 64) swizzle places it.
-template <int D>
-__device__ __forceinline__ int chunk_at(int r, int c) {
-  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
 template <int D, int NB, bool BF16>
@@ -254,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
     // ---------------------------------------------------------- the unit and the worker's part of it
     const KvTiles kt = kv_row_tile<RT, KT>(rq, cur.rt, p);
     const int64_t unit0 = x - cur.pos;  // where the unit starts on the line
-    const int64_t stop = unit0 + kKvUnitCost + kt.n < end ? unit0 + kKvUnitCost + kt.n : end;
-    const int part0 = imax(0, cur.pos - kKvUnitCost);
-    const int part1 = imax(0, static_cast<int>(stop - unit0) - kKvUnitCost);
+    const int64_t stop = unit0 + kKvDecCost + kt.n < end ? unit0 + kKvDecCost + kt.n : end;
+    const int part0 = imax(0, cur.pos - kKvDecCost);
+    const int part1 = imax(0, static_cast<int>(stop - unit0) - kKvDecCost);
     const int row0 = cur.rt * RT;
     const int rows = imin(RT, rq.R - row0);
 
@@ -404,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
           for (int y = 0; y < 2; ++y) s2[e][y][0] = s2[e][y][1] = s2[e][y][2] = s2[e][y][3] = 0.f;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(st + chunk_at<D>(r8, c4 * KC + c));
-          const uint4 x8 = *reinterpret_cast<const uint4*>(st + 8 * D + chunk_at<D>(r8, c4 * KC + c));
+          const uint4 x0 = *reinterpret_cast<const uint4*>(st + kv_chunk_at<D>(r8, c4 * KC + c));
+          const uint4 x8 = *reinterpret_cast<const uint4*>(st + 8 * D + kv_chunk_at<D>(r8, c4 * KC + c));
           const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w8[4] = {x8.x, x8.y, x8.z, x8.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -482,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = 2 * c4 + (e & 1) + 8 * (e >> 1);
-          const uint8_t* const at = st + C::TILE + chunk_at<D>(key, r8 * VB / 16) + (r8 * VB) % 16;
+          const uint8_t* const at = st + C::TILE + kv_chunk_at<D>(key, r8 * VB / 16) + (r8 * VB) % 16;
           if constexpr (VB == 16) {
             const uint4 w = *reinterpret_cast<const uint4*>(at);
             vw[e][0] = w.x, vw[e][1] = w.y, vw[e][2] = w.z, vw[e][3] = w.w;
@@ -558,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
           }
         }
       if (lane == 0 && part0 > 0 && part1 == kt.n) {  // ends a unit that part g0 began
-        const int g0 = kv_part_of(total, unit0 + kKvUnitCost, parts);
+        const int g0 = kv_part_of(total, unit0 + kKvDecCost, parts);
         p.desc[worker] = make_int4(cur.n, cur.rt, head, g0);
         p.fin[worker] = g0;
       }
@@ -577,154 +527,6 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
   }
 }
 
-// Joins the parts of each unit that was split over workers: entry w of ``desc``
-// names the unit that worker w finished (a worker finishes at most one that it
-// did not begin), its parts d.w to w / HKV in order; ``fin`` holds d.w, or -1
-// where there is none.  Every block lists the finished units (a scan of one
-// flag a worker); their rows are then spread over all warps of the launch,
-// with as many warps a row as there are to spare.  These add fixed shares of
-// the parts in order: lanes first take the parts' (m, l) together, then D/32
-// columns each.  Latency-bound: a few parts a unit as a rule, hundreds where few
-// requests have all the workers.
-constexpr int kJoinWarps = 16;
-
-template <int D, int RT, bool BF16>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const KvAttnParams p, int ctas) {
-  constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
-  __shared__ uint16_t list[kKvDecMaxWorkers];
-  __shared__ int s_cnt[kJoinWarps];
-  __shared__ float s_o[kJoinWarps][D];
-  __shared__ float2 s_ml[kJoinWarps];
-  grid_dependency_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int workers = ctas * kWarps;
-  if (blockIdx.x == 0 && warp == 0) {  // the launch's error word
-    int e = kErrNone;
-    for (int i = lane; i < ctas; i += 32) e = imax(e, p.cta_err[i]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) e = imax(e, __shfl_xor_sync(0xffffffffu, e, s));
-    if (lane == 0) *p.err = e;
-  }
-  uint32_t mine = 0;  // my PER workers that finished a unit
-#pragma unroll
-  for (int i = 0; i < PER; i += 4) {
-    if (tid * PER + i < workers) {  // (workers and PER are multiples of 4)
-      const int4 f = *reinterpret_cast<const int4*>(p.fin + tid * PER + i);
-      mine |= ((f.x >= 0 ? 1u : 0u) | (f.y >= 0 ? 2u : 0u) | (f.z >= 0 ? 4u : 0u) | (f.w >= 0 ? 8u : 0u)) << i;
-    }
-  }
-  int at0 = __popc(mine);
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, at0, s);
-    if (lane >= s) at0 += v;
-  }
-  if (lane == 31) s_cnt[warp] = at0;
-  __syncthreads();
-  at0 -= __popc(mine);
-  int units = 0;
-#pragma unroll
-  for (int i = 0; i < kJoinWarps; ++i) {
-    if (i < warp) at0 += s_cnt[i];
-    units += s_cnt[i];
-  }
-  for (uint32_t m = mine; m != 0; m &= m - 1) list[at0++] = static_cast<uint16_t>(tid * PER + __ffs(m) - 1);
-  __syncthreads();
-  const int rows = units * RT;  // those past a unit's last row are skipped
-  int shares = 1;               // warps a row
-  while (shares < kJoinWarps && rows * shares * 2 <= static_cast<int>(gridDim.x) * kJoinWarps) shares *= 2;
-  const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
-  for (int r0 = blockIdx.x * groups; r0 < rows; r0 += gridDim.x * groups) {
-    const int item = r0 + group;
-    KvReq rq{};
-    int4 d = make_int4(-1, 0, 0, 0);
-    int row0 = 0, live = 0, i0 = 0, i1 = 0;
-    const int row = item % RT;
-    if (item < rows) {
-      const int w = list[item / RT];
-      d = p.desc[w];
-      rq = kv_request(d.x, p);
-      row0 = d.y * RT, live = imin(RT, rq.R - row0);
-      const int parts = w / p.HKV - d.w + 1;
-      i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
-    }
-    auto slot_of = [&](int i) { return 2 * ((d.w + i) * p.HKV + d.z) + (i == 0 ? 1 : 0); };
-    float m = -INFINITY, l = 0.f, acc[ND];
-#pragma unroll
-    for (int u = 0; u < ND; ++u) acc[u] = 0.f;
-    if (row < live) {
-      for (int j = i0; j < i1; j += 32) {
-        // (m, l) of up to 32 parts, then their rows, rescaled where m grows
-        const float2 v = j + lane < i1 ? p.part_ml[slot_of(j + lane) * RT + row] : make_float2(0.f, 0.f);
-        float mx = v.y == 0.f ? -INFINITY : v.x;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        mx = fmaxf(mx, m);
-        if (mx > m) {
-          const float g = m == -INFINITY ? 0.f : ex2(m - mx);
-          l *= g;
-#pragma unroll
-          for (int u = 0; u < ND; ++u) acc[u] *= g;
-          m = mx;
-        }
-        const float f = v.y == 0.f ? 0.f : ex2(v.x - m);
-        l += f * v.y;
-        const int n = imin(32, i1 - j);
-        for (int i = 0; i < n; i += 8) {  // eight rows in flight
-          float x[8][ND];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int at = slot_of(j + imin(i + k, n - 1));
-            const float* from = p.part_o + (static_cast<int64_t>(at) * RT + row) * D + lane * ND;
-            if constexpr (ND == 4) {
-              const float4 y = *reinterpret_cast<const float4*>(from);
-              x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-            } else {
-              const float2 y = *reinterpret_cast<const float2*>(from);
-              x[k][0] = y.x, x[k][1] = y.y;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, (i + k) & 31);
-            if (i + k < n && fk != 0.f) {  // (a part that saw no key of the row says nothing)
-#pragma unroll
-              for (int u = 0; u < ND; ++u) acc[u] += fk * x[k][u];
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-      if (share > 0) {
-#pragma unroll
-        for (int u = 0; u < ND; ++u) s_o[warp][lane * ND + u] = acc[u];
-        if (lane == 0) s_ml[warp] = make_float2(m, l);
-      }
-    }
-    if (shares > 1) __syncthreads();
-    if (share == 0 && row < live) {
-      for (int k = 1; k < shares; ++k) {
-        const float2 v = s_ml[warp + k];
-        if (v.y == 0.f) continue;
-        const float mx = fmaxf(m, v.x), g = l == 0.f ? 0.f : ex2(m - mx), f = ex2(v.x - mx);
-        l = l * g + v.y * f;
-        m = mx;
-#pragma unroll
-        for (int u = 0; u < ND; ++u) acc[u] = acc[u] * g + s_o[warp + k][lane * ND + u] * f;
-      }
-      const int64_t at = static_cast<int64_t>(rq.a) + (row0 + row) / p.G;
-      const int hq = d.z * p.G + (row0 + row) % p.G;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int u = 0; u < ND; ++u) acc[u] *= inv;
-      store_o<BF16, ND>(p, at, hq, lane * ND, acc);
-      if (lane == 0) store_lse(p, at, hq, m, l);
-    }
-    if (shares > 1) __syncthreads();
-  }
-}
-
 template <int D, int NB, bool BF16>
 cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
   using C = DecCfg<D, NB>;
@@ -734,7 +536,7 @@ cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaSt
   const int grid = imin(sms * C::CTAS, kKvDecMaxRows / (2 * kWarps * C::RT));
   e = launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);
   if (e != cudaSuccess) return e;
-  return launch_after_previous(kv_join_kernel<D, C::RT, BF16>, 2 * sms, kJoinWarps * 32, 0, st, p, grid);
+  return launch_kv_join(p, BF16, C::RT, grid * kWarps, grid, p.HKV, true, 2 * sms, st);
 }
 
 // Units of 8 rows where a request's rows (by the mean number of its queries)

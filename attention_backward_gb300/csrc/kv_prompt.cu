@@ -1,0 +1,773 @@
+// Attention over the paged 8-bit cache for many rows (query, head of the group)
+// per KV head: prompts and chunks of prompts against what is cached of them.
+//
+// The mathematics of kv_decode.cu, on tcgen05 as in the dense forward: units of
+// two 128-row tiles of one KV head, key blocks of 128,
+//   S_w = Q_w K_j^T in tensor memory, P_w = 2^(S_w f - m) back into it as the
+//   fp16 A operand of O_w += P_w V_j,
+// two softmax warpgroups in turn, one row a thread, O rescaled only when a row
+// max grows by more than 2^8.  Rows are packed (query, head), so a group's heads
+// share each key block and short chunks fill the tiles.
+//
+// Bound by the tensor cores and the exponentials, with the bytes of K and V a
+// small part; what is new against the dense forward is that the operands have
+// to be made.  TMA brings pages as bytes into a raw ring; two warps convert them
+// to fp16 (exact) in the 128-byte-swizzled tiles that the products read.  A K
+// block's page scales (at most one per 16 keys) multiply the f32 scores, 16
+// columns at a time.  V is converted at v * vs / vref, vref the largest V scale
+// of the unit's pages: exact for powers of two (what falls under fp16's range
+// is 2^-34 of the largest value), rounded to fp16 once more for others.  Each
+// softmax thread loads its own row of Q, brings it to fp16's upper range by a
+// power of two and writes it into the swizzled Q tile.
+//
+// Work: the line of kv_sched.cuh over all heads, cut evenly over one CTA per
+// SM; at most two parts of units per CTA go through the workspace.
+//
+// Warp roles (12 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 copies (and the
+// walk along the line: it publishes each unit through a two-slot ring), 9 MMA
+// issue, 10-11 conversion.  Every wait is bounded.
+#include <cuda_fp16.h>
+
+#define AB_INLINE_WAITS 1
+#include "cvt.cuh"
+#include "kernels.h"
+#include "kv_cache.h"
+#include "kv_common.cuh"
+#include "kv_sched.cuh"
+#include "sm103.cuh"
+
+namespace ab {
+
+namespace {
+
+constexpr int BQ = 128, RT = kKvPrRows, KT = kKvPrKeys, COST = kKvPrCost;
+constexpr int kWarps = 12, THREADS = kWarps * 32;
+constexpr uint32_t REG_SOFT = 208, REG_CTL = 88;
+static_assert(2 * REG_SOFT + REG_CTL == 3 * 168, "register split must equal the launch's registers");
+constexpr float kRescaleLog2 = 8.f;
+constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
+constexpr int kScaleRing = 8;     // blocks of scales; deeper than the conversion can run ahead of the softmax
+
+template <int D>
+struct PrCfg {
+  static constexpr int NSLAB = D / 64;
+  static constexpr int SLAB = 128 * 128;         // [128 rows x 64 columns] fp16, 128-byte swizzled
+  static constexpr int TILE = NSLAB * SLAB;      // a 128-row tile of Q, K or V
+  static constexpr int RAW = KT * D;             // 128 keys as bytes
+  static constexpr int NT = D == 64 ? 6 : 3;     // ring of converted tiles, K and V in turn
+  static constexpr int NR = D == 64 ? 8 : 4;     // ring of raw tiles, K and V in turn
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_T = OFF_Q + 2 * TILE;
+  static constexpr int OFF_RAW = OFF_T + NT * TILE;
+  static constexpr int OFF_UNIT = OFF_RAW + NR * RAW;   // 2 unit descriptors of 64 bytes
+  static constexpr int OFF_SC = OFF_UNIT + 2 * 64;      // K scales [kScaleRing][8], V ratios [kScaleRing][8]
+  static constexpr int OFF_BAR = OFF_SC + kScaleRing * 64;
+  static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
+  static constexpr int SMEM = OFF_MISC + 32;
+  static_assert(SMEM + 256 <= 227 * 1024, "shared memory budget");
+  static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + D;
+};
+
+enum PrBar : int {
+  Q_FULL0 = 0,                 // per tile: 4 softmax warps wrote Q
+  RAW_FULL0 = Q_FULL0 + 2,     // NR
+  RAW_EMPTY0 = RAW_FULL0 + 8,  // NR: 2 conversion warps read it
+  T_FULL0 = RAW_EMPTY0 + 8,    // NT: 2 conversion warps wrote it
+  T_EMPTY0 = T_FULL0 + 6,      // NT: its products have completed
+  S_FULL0 = T_EMPTY0 + 6,      // per tile
+  P_READY0 = S_FULL0 + 2,      // per tile: 4 softmax warps stored P
+  O_DONE0 = P_READY0 + 2,      // per tile: the P V products issued so far completed
+  O_FREE0 = O_DONE0 + 2,       // per tile: 4 softmax warps read the unit's O rows
+  UNIT_FULL0 = O_FREE0 + 2,    // 2 slots
+  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the other 11 warps read it
+  DRAIN = UNIT_EMPTY0 + 2,
+  NUM_BARS
+};
+static_assert(NUM_BARS <= 48, "barrier storage");
+
+// A unit, or the CTA's part of one: key blocks [j0, j1).
+struct PrUnit {
+  int a, nq, L, off, R;  // the request (kv_sched.cuh)
+  int row0, head;
+  int j0, j1;            // j0 == j1: no block, its rows are zero
+  int lo, hi;            // keys that some row of the unit sees
+  int slot;              // -1: the whole unit, else the slot of its partial rows
+  float vref;
+  int valid;
+};
+static_assert(sizeof(PrUnit) <= 64, "descriptor slot");
+
+// Key blocks [lo, hi) of tile w of the unit, within its part, and the keys that
+// all its live rows see.
+struct PrTile {
+  int lo, hi, all_lo, all_hi;
+};
+
+__device__ __forceinline__ PrTile tile_of(const PrUnit& u, int w, const KvAttnParams& p) {
+  PrTile t{0, 0, 0, 0};
+  const int r0 = u.row0 + w * BQ, r1 = imin(u.R, r0 + BQ);
+  if (r0 >= r1) return t;
+  KvReq r{u.a, u.nq, u.L, u.off, u.R};
+  int lo, hi;
+  kv_row_keys(r, r0 / p.G, p.causal, p.window, &lo, &t.all_hi);
+  kv_row_keys(r, (r1 - 1) / p.G, p.causal, p.window, &t.all_lo, &hi);
+  if (hi <= lo) return t;
+  t.lo = imax(lo / KT, u.j0), t.hi = imin((hi + KT - 1) / KT, u.j1);
+  if (t.hi < t.lo) t.lo = t.hi = 0;
+  return t;
+}
+
+// ---------------------------------------------------------------- the walk
+// (one warp; every lane holds the same cursor)
+
+struct PrCursor {
+  int n, rt, head, pos;
+};
+
+// Positions of a request on the line of one head, all lanes together.
+__device__ __forceinline__ int64_t lanes_work(const KvAttnParams& p, const KvReq& r) {
+  int64_t w = 0;
+  const int nt = kv_row_tiles<RT>(r);
+  for (int rt = threadIdx.x & 31; rt < nt; rt += 32) w += kv_row_tile<RT, KT>(r, rt, p).n + COST;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return w;
+}
+
+// Calls f(n, request) for the requests of [n0, n1) that have rows here, in
+// order, until it returns true; 32 requests are looked up at once.
+template <typename F>
+__device__ __forceinline__ void each_request(const KvAttnParams& p, int n0, int n1, F f) {
+  const int lane = threadIdx.x & 31;
+  for (int b = n0; b < n1; b += 32) {
+    KvReq mine{};
+    if (b + lane < n1) mine = kv_request(b + lane, p);
+    for (uint32_t m = __ballot_sync(0xffffffffu, mine.R > 0); m != 0; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      KvReq r;
+      r.a = __shfl_sync(0xffffffffu, mine.a, src), r.nq = __shfl_sync(0xffffffffu, mine.nq, src);
+      r.L = __shfl_sync(0xffffffffu, mine.L, src), r.off = __shfl_sync(0xffffffffu, mine.off, src);
+      r.R = __shfl_sync(0xffffffffu, mine.R, src);
+      if (f(b + src, r)) return;
+    }
+  }
+}
+
+// Cursor of position x counted from request n0 (all heads).
+__device__ __forceinline__ PrCursor walk_to(const KvAttnParams& p, int n0, int64_t x) {
+  const int lane = threadIdx.x & 31;
+  PrCursor c{n0, 0, 0, 0};
+  each_request(p, n0, p.N, [&](int n, const KvReq& r) {
+    c.n = n;
+    const int64_t w = lanes_work(p, r) * p.HKV;
+    if (x < w) return true;
+    x -= w;
+    return false;
+  });
+  const KvReq r = kv_request(c.n, p);
+  const int nt = kv_row_tiles<RT>(r);
+  for (int b = 0;; b += 32) {
+    const int n = b + lane < nt ? kv_row_tile<RT, KT>(r, b + lane, p).n + COST : 0;
+    const int64_t w = static_cast<int64_t>(n) * p.HKV;
+    int64_t inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, x < inc);
+    if (past == 0) {
+      x -= __shfl_sync(0xffffffffu, inc, 31);
+      continue;
+    }
+    const int src = __ffs(past) - 1;
+    x -= __shfl_sync(0xffffffffu, inc - w, src);
+    const int size = __shfl_sync(0xffffffffu, n, src);
+    c.rt = b + src;
+    c.head = static_cast<int>(x / size);
+    c.pos = static_cast<int>(x % size);
+    return c;
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_constant__ KvMaps maps,
+                                                               const __grid_constant__ KvAttnParams p) {
+  using C = PrCfg<D>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  __shared__ int64_t s_work[kWarps];
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);
+  PrUnit* const units = reinterpret_cast<PrUnit*>(sm + C::OFF_UNIT);
+  float* const k_scales = reinterpret_cast<float*>(sm + C::OFF_SC);               // [kScaleRing][8]; -1: no page
+  float* const v_ratios = k_scales + kScaleRing * kGroups;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  grid_dependency_wait();
+  const WaitCtx wc{abort_flag, p.cta_err + blockIdx.x, p.timeout_ns};
+  const bool aligned = (smem_u32(sm) & 1023u) == 0;
+  if (threadIdx.x == 0) {
+    *wc.err = aligned ? kErrNone : kErrAlign;
+    p.fin[blockIdx.x] = -1;
+    *abort_flag = 0;
+  }
+  // ---------------------------------------------------------------- the line, and the CTA's part of it
+  const int per = (p.N + kWarps - 1) / kWarps;
+  {
+    int64_t w = 0;
+    each_request(p, imin(p.N, warp * per), imin(p.N, (warp + 1) * per), [&](int, const KvReq& r) {
+      w += lanes_work(p, r) * p.HKV;
+      return false;
+    });
+    if (lane == 0) s_work[warp] = w;
+  }
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) total += s_work[i];
+  if (!aligned || total == 0) return;
+  const int64_t want = (total + kKvPrMinWork - 1) / kKvPrMinWork;
+  const int parts = want < static_cast<int64_t>(gridDim.x) ? static_cast<int>(want) : static_cast<int>(gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= parts) return;
+  const int64_t begin = kv_part_begin(total, blockIdx.x, parts), end = kv_part_begin(total, blockIdx.x + 1, parts);
+
+  // ---------------------------------------------------------------- set-up
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bars[Q_FULL0 + w], 4);
+      mbar_init(&bars[S_FULL0 + w], 1);
+      mbar_init(&bars[P_READY0 + w], 4);
+      mbar_init(&bars[O_DONE0 + w], 1);
+      mbar_init(&bars[O_FREE0 + w], 4);
+      mbar_init(&bars[UNIT_FULL0 + w], 1);
+      mbar_init(&bars[UNIT_EMPTY0 + w], kWarps - 1);
+    }
+    for (int i = 0; i < C::NR; ++i) {
+      mbar_init(&bars[RAW_FULL0 + i], 1);
+      mbar_init(&bars[RAW_EMPTY0 + i], 2);
+    }
+    for (int i = 0; i < C::NT; ++i) {
+      mbar_init(&bars[T_FULL0 + i], 2);
+      mbar_init(&bars[T_EMPTY0 + i], 1);
+    }
+    mbar_init(&bars[DRAIN], 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto finish = [&]() {
+    tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+    if (warp == 9) {
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  };
+  // the uc-th unit of this CTA
+  auto next_unit = [&](uint32_t uc, bool* okp) -> PrUnit {
+    const uint32_t slot = uc & 1;
+    PrUnit u{};
+    if (!(*okp = mbar_wait_warp(&bars[UNIT_FULL0 + slot], (uc >> 1) & 1, wc, kErrWaitTile))) return u;
+    u = units[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[UNIT_EMPTY0 + slot]);
+    return u;
+  };
+
+  if (warp >= 8) {
+    setmaxnreg_dec<REG_CTL>();
+    if (warp == 8) {
+      // ============================================================ copies
+      int w0 = 0;
+      int64_t x = begin;
+      while (x >= s_work[w0]) x -= s_work[w0++];
+      PrCursor cur = walk_to(p, w0 * per, x);
+      KvReq rq = kv_request(cur.n, p);
+      uint32_t ic = 0;  // raw tiles so far
+      bool ok = true;
+      uint32_t uc = 0;
+      for (x = begin; ok; ++uc) {
+        const uint32_t slot = uc & 1;
+        if (uc >= 2 && !(ok = mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wc, kErrWaitTile)))
+          break;
+        PrUnit u{};
+        u.valid = x < end;
+        KvTiles kt{};
+        int64_t stop = x;
+        bool ends = false;
+        if (u.valid) {
+          kt = kv_row_tile<RT, KT>(rq, cur.rt, p);
+          const int64_t unit0 = x - cur.pos;
+          stop = unit0 + COST + kt.n < end ? unit0 + COST + kt.n : end;
+          const int part0 = imax(0, cur.pos - COST), part1 = imax(0, static_cast<int>(stop - unit0) - COST);
+          u.a = rq.a, u.nq = rq.nq, u.L = rq.L, u.off = rq.off, u.R = rq.R;
+          u.row0 = cur.rt * RT, u.head = cur.head;
+          u.lo = kt.lo, u.hi = kt.hi;
+          u.j0 = kt.t0 + part0, u.j1 = kt.t0 + part1;
+          const bool whole = part0 == 0 && part1 == kt.n;
+          u.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (part0 > 0 ? 0 : 1);
+          const bool none = part1 <= part0;  // only the start-up positions: nothing to do
+          ends = part0 > 0 && part1 == kt.n;
+          if (ends && lane == 0) {
+            const int g0 = kv_part_of(total, unit0 + COST, parts);
+            p.desc[blockIdx.x] = make_int4(cur.n, cur.rt, cur.head, g0);
+            p.fin[blockIdx.x] = g0;
+          }
+          if (kt.hi <= kt.lo) u.j1 = u.j0;  // the one tile of a unit that sees nothing
+          if (none) u.valid = 2;            // (consumers skip it)
+        }
+        auto page_of = [&](int k0) {  // page of keys [k0, k0 + 16), -1 where there is none or nothing is seen
+          if (k0 >= kt.hi || k0 + 16 <= kt.lo) return -1;
+          const int b = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
+          return b >= 0 && b < p.num_blocks ? b : -1;
+        };
+        if (u.valid == 1) {
+          // the largest V scale of the part's pages
+          float vref = 0.f;
+          for (int k0 = u.j0 * KT + lane * 16; k0 < u.j1 * KT; k0 += 32 * 16) {
+            const int b = page_of(k0);
+            if (b >= 0) vref = fmaxf(vref, p.v_scale[static_cast<int64_t>(b) * p.HKV + cur.head]);
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, o));
+          u.vref = vref < 0x1p-126f ? 0.f : vref;
+        }
+        if (lane == 0) {
+          units[slot] = u;
+          mbar_arrive(&bars[UNIT_FULL0 + slot]);
+        }
+        if (!u.valid) break;
+        if (u.valid == 1) {
+          const float vinv = u.vref > 0.f ? 1.f / u.vref : 0.f;
+          // page ids and scales of four blocks at a time: lane i those of 16-key group i
+          int blk = -1;
+          float ksc = -1.f, vra = 0.f;
+          const int s_mask = (1 << p.page_log2) - 1;
+          for (int j = u.j0; j < u.j1 && ok; ++j) {
+            const int q4 = (j - u.j0) & 3;
+            if (q4 == 0) {
+              const int k0 = j * KT + lane * 16;
+              blk = k0 < u.j1 * KT ? page_of(k0) : -1;
+              ksc = -1.f, vra = 0.f;
+              if (blk >= 0) {
+                const int64_t at = static_cast<int64_t>(blk) * p.HKV + cur.head;
+                ksc = p.k_scale[at], vra = p.v_scale[at] * vinv;
+              }
+            }
+            for (int kv = 0; kv < 2; ++kv, ++ic) {
+              const int rs = ic % C::NR;
+              const uint32_t n = ic / C::NR;
+              if (n >= 1 && !(ok = mbar_wait_warp(&bars[RAW_EMPTY0 + rs], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
+              const uint32_t have = (__ballot_sync(0xffffffffu, blk >= 0) >> (8 * q4)) & 0xffu;
+              if (kv == 0) {
+                // the block's scales (the ring is deep enough that its last readers are done)
+                const uint32_t sr = (ic >> 1) % kScaleRing;
+                if ((lane >> 3) == q4) {
+                  k_scales[sr * kGroups + (lane & 7)] = ksc;
+                  v_ratios[sr * kGroups + (lane & 7)] = vra;
+                }
+                __syncwarp();
+              }
+              if (lane == 0) {
+                if (have) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], __popc(have) * 16 * D);
+                else mbar_arrive(&bars[RAW_FULL0 + rs]);
+              }
+              for (int g = 0; g < kGroups; ++g) {
+                const int b = __shfl_sync(0xffffffffu, blk, 8 * q4 + g);
+                if (lane == 0 && b >= 0)
+                  tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + g * 16 * D, kv ? &maps.v : &maps.k, &bars[RAW_FULL0 + rs],
+                              0, u.head, (j * KT + g * 16) & s_mask, b);
+              }
+            }
+          }
+          if (!ok) break;
+        }
+        // next unit
+        x = stop;
+        cur.pos = 0;
+        if (x < end && ++cur.head == p.HKV) {
+          cur.head = 0;
+          if (++cur.rt == kv_row_tiles<RT>(rq)) {
+            cur.rt = 0;
+            do {
+              rq = kv_request(++cur.n, p);
+            } while (rq.R == 0);
+          }
+        }
+      }
+      // copies still in flight land before the CTA exits
+      if (lane == 0)
+        for (uint32_t i = ic > static_cast<uint32_t>(C::NR) ? ic - C::NR : 0u; i < ic; ++i)
+          mbar_drain(&bars[RAW_FULL0 + i % C::NR], (i / C::NR) & 1);
+      __syncwarp();
+    } else if (warp == 9) {
+      // ============================================================ MMA issue
+      constexpr uint32_t IDESC_S = idesc_f16(false, 128, KT, false, false);
+      constexpr uint32_t IDESC_PV = idesc_f16(false, 128, D, false, true);
+      const uint32_t sbase = smem_u32(sm);
+      const uint64_t q_kmaj = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
+      const uint64_t t_kmaj = sdesc_sw128(sbase + C::OFF_T, 16, 1024);
+      const uint64_t t_mn = sdesc_sw128(sbase + C::OFF_T, C::SLAB, 1024);
+      uint32_t bc = 0, qc0 = 0, qc1 = 0, npv0 = 0, npv1 = 0, oc0 = 0, oc1 = 0;  // bc: blocks so far
+      bool ok = true;
+      for (uint32_t uc = 0; ok; ++uc) {
+        const PrUnit u = next_unit(uc, &ok);
+        if (!ok || !u.valid) break;
+        if (u.valid == 2 || u.j1 <= u.j0) continue;
+        const PrTile t0 = tile_of(u, 0, p), t1 = tile_of(u, 1, p);
+        const uint32_t bc0 = bc;
+        auto in = [&](int w, int j) { return w ? t1.lo <= j && j < t1.hi : t0.lo <= j && j < t0.hi; };
+        auto wait_tile = [&](int j, int kv) {  // converted tile of K (0) or V (1) of block j
+          const uint32_t i = 2 * (bc0 + j - u.j0) + kv;
+          return mbar_wait_warp(&bars[T_FULL0 + i % C::NT], (i / C::NT) & 1, wc, kErrWaitKV);
+        };
+        auto tile_at = [&](int j, int kv) { return (2 * (bc0 + j - u.j0) + kv) % C::NT; };
+        auto issue_s = [&](int w, int j) {
+          const uint64_t ko0 = sdesc_step(tile_at(j, 0) * C::TILE), qo = sdesc_step(w * C::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t ko = sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32);
+            mma_ss_w(tmem + (w ? C::T_S1 : C::T_S0), q_kmaj + qo + ko, t_kmaj + ko0 + ko, IDESC_S, kk > 0);
+          }
+          mma_commit_w(&bars[S_FULL0 + w]);
+        };
+        auto issue_pv = [&](int w, int j) -> bool {
+          uint32_t& npv = w ? npv1 : npv0;
+          if (!mbar_wait_warp(&bars[P_READY0 + w], npv & 1, wc, kErrWaitP)) return false;
+          const int lo = w ? t1.lo : t0.lo;
+          if (j == lo) {
+            const uint32_t oc = w ? oc1 : oc0;
+            if (oc >= 1 && !mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wc, kErrWaitDQEmpty)) return false;
+          }
+          tc_fence_after();
+          const uint64_t vo = sdesc_step(tile_at(j, 1) * C::TILE);
+          const uint32_t ts = tmem + (w ? C::T_S1 : C::T_S0), to = tmem + (w ? C::T_O1 : C::T_O0);
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            mma_ts_w(to, ts + kk * 8, t_mn + vo + sdesc_step(kk * 2048), IDESC_PV, j > lo || kk > 0);
+          mma_commit_w(&bars[O_DONE0 + w]);
+          ++npv;
+          return true;
+        };
+        // the unit's Q tiles
+        if (t0.lo < t0.hi) ok = mbar_wait_warp(&bars[Q_FULL0], qc0++ & 1, wc, kErrWaitStageFull);
+        if (ok && t1.lo < t1.hi) ok = mbar_wait_warp(&bars[Q_FULL0 + 1], qc1++ & 1, wc, kErrWaitStageFull);
+        ok = ok && wait_tile(u.j0, 0);
+        if (!ok) break;
+        tc_fence_after();
+        if (in(0, u.j0)) issue_s(0, u.j0);
+        if (in(1, u.j0)) issue_s(1, u.j0);
+        mma_commit_w(&bars[T_EMPTY0 + tile_at(u.j0, 0)]);
+        for (int j = u.j0; j < u.j1; ++j) {
+          if (!(ok = wait_tile(j, 1))) break;
+          tc_fence_after();
+          if (in(0, j) && !(ok = issue_pv(0, j))) break;
+          const bool next = j + 1 < u.j1;
+          if (next) {
+            if (!(ok = wait_tile(j + 1, 0))) break;
+            tc_fence_after();
+            if (in(0, j + 1)) issue_s(0, j + 1);
+          }
+          if (in(1, j) && !(ok = issue_pv(1, j))) break;
+          mma_commit_w(&bars[T_EMPTY0 + tile_at(j, 1)]);
+          if (next) {
+            if (in(1, j + 1)) issue_s(1, j + 1);
+            mma_commit_w(&bars[T_EMPTY0 + tile_at(j + 1, 0)]);
+          }
+        }
+        if (!ok) break;
+        bc += u.j1 - u.j0;
+        oc0 += t0.lo < t0.hi ? 1u : 0u;
+        oc1 += t1.lo < t1.hi ? 1u : 0u;
+      }
+      // every MMA issued by this warp completes before TMEM is released
+      mma_commit_w(&bars[DRAIN]);
+      if (lane == 0) mbar_drain(&bars[DRAIN], 0);
+      __syncwarp();
+    } else {
+      // ============================================================ conversion (2 warps)
+      // A lane takes 16 bytes of a row (16 values) and writes two 16-byte chunks
+      // of fp16.  Eight lanes (one shared-memory phase) hold rows r and r ^ 5 of
+      // an 8-row group: reads then fall in different halves of the 128-byte
+      // lines and writes on chunks of different parity, without bank conflicts.
+      const int cw = warp - 10;
+      const int row8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), c4 = lane & 3;
+      uint32_t ic = 0;
+      bool ok = true;
+      for (uint32_t uc = 0; ok; ++uc) {
+        const PrUnit u = next_unit(uc, &ok);
+        if (!ok || !u.valid) break;
+        if (u.valid == 2) continue;
+        for (int j = u.j0; j < u.j1 && ok; ++j)
+          for (int kv = 0; kv < 2; ++kv, ++ic) {
+            const int rs = ic % C::NR, ts = ic % C::NT;
+            const uint32_t n = ic / C::NT;
+            if (!(ok = mbar_wait_warp(&bars[RAW_FULL0 + rs], (ic / C::NR) & 1, wc, kErrWaitStage))) break;
+            if (n >= 1 && !(ok = mbar_wait_warp(&bars[T_EMPTY0 + ts], (n - 1) & 1, wc, kErrWaitKVFree))) break;
+            const uint8_t* const raw = sm + C::OFF_RAW + rs * C::RAW;
+            uint8_t* const out = sm + C::OFF_T + ts * C::TILE;
+            const float* const ratio = v_ratios + ((ic >> 1) % kScaleRing) * kGroups;
+            const float* const ksc = k_scales + ((ic >> 1) % kScaleRing) * kGroups;
+#pragma unroll 2
+            for (int g = cw; g < kGroups; g += 2) {
+              const __half2 f = kv ? __float2half2_rn(ratio[g]) : __float2half2_rn(1.f);
+              const bool page = ksc[g] >= 0.f;
+              uint4 w[2 * C::NSLAB];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int s = 0; s < C::NSLAB; ++s) {
+                  const int row = g * 16 + h * 8 + row8;
+                  w[h * C::NSLAB + s] = *reinterpret_cast<const uint4*>(raw + kv_chunk_at<D>(row, s * 4 + c4));
+                }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int row = g * 16 + h * 8 + row8, key = j * KT + row;
+                // keys that no row sees: a zero P times a NaN would be NaN
+                const bool zero = kv && (!page || key < u.lo || key >= u.hi);
+#pragma unroll
+                for (int s = 0; s < C::NSLAB; ++s) {
+                  const uint4 x = w[h * C::NSLAB + s];
+                  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                  uint32_t y[8];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
+                    if (kv) {
+                      y[2 * e] = mul_f16x2(y[2 * e], f);
+                      y[2 * e + 1] = mul_f16x2(y[2 * e + 1], f);
+                    }
+                    if (zero) y[2 * e] = y[2 * e + 1] = 0u;
+                  }
+                  uint8_t* const slab = out + s * C::SLAB;
+                  *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                  *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bars[RAW_EMPTY0 + rs]);
+              mbar_arrive(&bars[T_FULL0 + ts]);
+            }
+          }
+      }
+    }
+    finish();
+    return;
+  }
+
+  setmaxnreg_inc<REG_SOFT>();
+  // ============================================================ softmax of tile w (one row a thread)
+  const int w = warp >> 2, quad = warp & 3;
+  const int trow = quad * 32 + lane;
+  const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t tS = tmem + lane_off + (w ? C::T_S1 : C::T_S0);
+  const uint32_t tO = tmem + lane_off + (w ? C::T_O1 : C::T_O0);
+  uint32_t c = 0, bc = 0;  // blocks of this tile, and of the CTA, over all units so far
+  bool ok = true;
+  for (uint32_t uc = 0; ok; ++uc) {
+    const PrUnit u = next_unit(uc, &ok);
+    if (!ok || !u.valid) break;
+    if (u.valid == 2) continue;
+    const uint32_t bc0 = bc;
+    bc += u.j1 - u.j0;
+    const PrTile tl = tile_of(u, w, p);
+    const int row = u.row0 + w * BQ + trow;  // of the request
+    if (u.row0 + w * BQ >= u.R) continue;    // the tile is past the request's rows
+    const bool live = row < u.R;
+    const int qi = row / p.G, hq = u.head * p.G + row % p.G;
+    const int64_t pos = static_cast<int64_t>(u.a) + qi;
+    const bool any = tl.lo < tl.hi;
+    float rs = 0.f;  // what a raw score is multiplied with, beside its page's scale
+    int my_lo = 0, my_hi = 0;
+    if (any) {
+      // ---- my row of Q in fp16 (the tile's last S products completed before its last softmax block)
+      const KvReq r{u.a, u.nq, u.L, u.off, u.R};
+      if (live) kv_row_keys(r, qi, p.causal, p.window, &my_lo, &my_hi);
+      const uint8_t* const src = p.q + 2 * (pos * p.sq_s + static_cast<int64_t>(hq) * p.sq_h);
+      float amax = 0.f;
+      uint4 x[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (live) x[i] = *reinterpret_cast<const uint4*>(src + 16 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack2<BF16>(xs[e]);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      float back;
+      const float up = to_top(amax, &back);
+      rs = back * p.scale_log2;
+      uint8_t* const qt = sm + C::OFF_Q + w * C::TILE;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack2<BF16>(xs[e]);
+          y[e] = pack2<false>(f.x * up, f.y * up);
+        }
+        *reinterpret_cast<uint4*>(qt + (i / 8) * C::SLAB + sw128_offset(trow, i % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Q_FULL0 + w]);
+    }
+    float m_used = -INFINITY, l = 0.f;
+    for (int j = tl.lo; j < tl.hi; ++j, ++c) {
+      if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
+      tc_fence_after();
+      uint32_t sr[KT];
+#pragma unroll
+      for (int ch = 0; ch < KT / 32; ++ch) tmem_ld32(tS + ch * 32, sr + ch * 32);
+      const float* const sc = k_scales + ((bc0 + j - u.j0) % kScaleRing) * kGroups;
+      const float4 sa = *reinterpret_cast<const float4*>(sc), sb = *reinterpret_cast<const float4*>(sc + 4);
+      float f[kGroups] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+      const int k0 = j * KT;
+      bool masked = k0 < tl.all_lo || k0 + KT > tl.all_hi;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) masked |= f[g] < 0.f;
+      tmem_ld_wait();
+      if (masked) {
+        const int a = my_lo - k0, b = my_hi - k0;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+          if (k < a || k >= b || f[k / 16] < 0.f) sr[k] = __float_as_uint(-INFINITY);
+      }
+      // largest raw score of each 16 columns, then of the row in log2 units
+      float m_new = m_used;
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(sr[g * 16 + k]));
+        const float top = fmaxf(mx[0], mx[1]);
+        f[g] = fabsf(f[g]) * rs;  // (a group without a page has no finite score)
+        m_new = fmaxf(m_new, top == -INFINITY ? -INFINITY : top * f[g]);
+      }
+      const bool resc = m_used != -INFINITY && m_new > m_used + kRescaleLog2;
+      const float shrink = resc ? ex2(m_used - m_new) : 1.f;
+      if (__any_sync(0xffffffffu, resc)) {
+        if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t r[32];
+          tmem_ld32(tO + ch * 32, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * shrink);
+          tmem_st16(tO + ch * 32, r);
+          tmem_st16(tO + ch * 32 + 16, r + 16);
+        }
+      }
+      l *= shrink;
+      if (resc || m_used == -INFINITY) m_used = m_new;
+      const float msub = m_used == -INFINITY ? 0.f : m_used;
+      const float2 nm2 = make_float2(-msub, -msub);
+      float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int ch = 0; ch < KT / 32; ++ch) {
+        uint32_t pw[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float fg = f[ch * 2 + e / 8];
+          float2 y = make_float2(__uint_as_float(sr[ch * 32 + 2 * e]), __uint_as_float(sr[ch * 32 + 2 * e + 1]));
+          if (masked) {  // (a zero scale times -inf would be NaN)
+            y.x = y.x == -INFINITY ? -INFINITY : y.x * fg - msub;
+            y.y = y.y == -INFINITY ? -INFINITY : y.y * fg - msub;
+          } else {
+            y = __ffma2_rn(y, make_float2(fg, fg), nm2);
+          }
+          const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+          sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
+          pw[e] = pack2<false>(pp.x, pp.y);
+        }
+        tmem_st16(tS + ch * 16, pw);
+      }
+      l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[P_READY0 + w]);
+    }
+    if (!ok) break;
+    // ---- the row's O and LSE, or its part
+    if (any) {
+      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
+      tc_fence_after();
+    }
+    const bool whole = u.slot < 0;
+    const int64_t prow = whole ? 0 : static_cast<int64_t>(u.slot) * RT + w * BQ + trow;
+    const float fo = whole ? (l == 0.f ? 0.f : u.vref / l) : u.vref;
+    if (live) {
+      if (whole) store_lse(p, pos, hq, m_used, l);
+      else p.part_ml[prow] = make_float2(m_used, l);
+    }
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t r[32];
+      float v[32];
+      if (any) {
+        tmem_ld32(tO + ch * 32, r);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = any ? __uint_as_float(r[e]) * fo : 0.f;
+      if (live) {
+        if (whole) {
+          store_o<BF16, 32>(p, pos, hq, ch * 32, v);
+        } else {
+          float* const to = p.part_o + prow * D + ch * 32;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      }
+    }
+    if (any) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[O_FREE0 + w]);
+    }
+  }
+  finish();
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int grid, cudaStream_t st) {
+  using C = PrCfg<D>;
+  auto kern = kv_prompt_kernel<D, BF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_after_previous(kern, grid, THREADS, C::SMEM, st, maps, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prompt(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, bool first, cudaStream_t st) {
+  const int grid = imin(sms, kKvPrMaxCtas);
+  cudaError_t e;
+  if (p.D == 64) e = bf16 ? launch_t<64, true>(p, maps, grid, st) : launch_t<64, false>(p, maps, grid, st);
+  else e = bf16 ? launch_t<128, true>(p, maps, grid, st) : launch_t<128, false>(p, maps, grid, st);
+  if (e != cudaSuccess) return e;
+  return launch_kv_join(p, bf16, RT, grid, grid, 1, first, 2 * sms, st);
+}
+
+}  // namespace ab

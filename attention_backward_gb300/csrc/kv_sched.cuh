@@ -5,9 +5,10 @@
 // head of the group) of one KV head, with the key tiles of KT keys that some
 // row of it sees; a unit that sees nothing has one empty tile, so that its
 // rows are written.  A head's units, ordered by request and row tile, are laid
-// on one line, each as kKvUnitCost positions for its start and end (its table
+// on one line, each as COST positions for its start and end (its table
 // row, its queries, its first copies: about as long as that many tiles) and one
-// position a tile.  Part g of C takes the positions [W g / C, W (g + 1) / C) of
+// position a tile.  (The prompt kernel has one line for all heads, a row tile's
+// heads one after another.)  Part g of C takes the positions [W g / C, W (g + 1) / C) of
 // the W: every part gets the same work whatever the lengths, a long row spreads
 // over many parts, many short ones share a part, and no length is needed on
 // the host.
@@ -30,6 +31,7 @@ __host__ __device__ __forceinline__ KvReq kv_request(int n, const KvAttnParams& 
   r.L = len < width ? len : static_cast<int>(width);
   r.off = len - r.nq;
   r.R = r.nq * p.G;
+  if (r.R < p.rows_min || r.R > p.rows_max) r.R = 0;  // another kernel's
   return r;
 }
 
@@ -73,11 +75,11 @@ __host__ __device__ __forceinline__ int kv_row_tiles(const KvReq& r) {
 }
 
 // Positions of a request on a head's line.
-template <int RT, int KT>
+template <int RT, int KT, int COST>
 __host__ __device__ __forceinline__ int64_t kv_request_work(const KvReq& r, const KvAttnParams& p) {
   int64_t w = 0;
   const int nt = kv_row_tiles<RT>(r);
-  for (int rt = 0; rt < nt; ++rt) w += kv_row_tile<RT, KT>(r, rt, p).n + kKvUnitCost;
+  for (int rt = 0; rt < nt; ++rt) w += kv_row_tile<RT, KT>(r, rt, p).n + COST;
   return w;
 }
 

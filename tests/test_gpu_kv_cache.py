@@ -318,7 +318,9 @@ def run_attend(prob, name, causal=True, window=-1, scale=None, heads_first=False
     return o[0].double().cpu().numpy(), lse[0].double().cpu().numpy()
 
 
-def check_attend(prob, name, causal=True, window=-1, scale=None, **kw):
+def check_attend(prob, name, causal=True, window=-1, scale=None, v_rounded=False, **kw):
+    """v_rounded: many rows and V scales that are no powers of two; their values
+    are rounded to fp16 at the largest scale, 2^-11 relative."""
     q, kc, vc, ks, vs, table, cu, kv = prob
     D = q.shape[2]
     got, glse = run_attend(prob, name, causal, window, scale, **kw)
@@ -334,7 +336,7 @@ def check_attend(prob, name, causal=True, window=-1, scale=None, **kw):
     assert (np.abs(glse - lse)[some] <= tl[some]).all(), (np.abs(glse - lse)[some] / tl[some]).max()
     half = 2.0 ** -11 if name == "f16" else 2.0 ** -8
     tiny = 2.0 ** -25 if name == "f16" else 0.0  # half of fp16's smallest step
-    tol = half * np.abs(o) + (2.0 ** -11 + e.T[..., None]) * mag * (1 + half) + (2.0 ** -24 * seen * vmax).T[..., None] + tiny
+    tol = half * np.abs(o) + (2.0 ** -11 * (1 + v_rounded) + e.T[..., None]) * mag * (1 + half) + (2.0 ** -24 * seen * vmax).T[..., None] + tiny
     err = np.abs(got - o)[live.T]
     assert (err <= tol[live.T]).all(), (err / tol[live.T]).max()
 
@@ -368,6 +370,74 @@ def test_attend(case, name):
 def test_attend_masks(causal, window, D):
     lens = [(1, 1000), (4, 4), (9, 300), (1, 1), (2, 71), (40, 130), (1, 513)]
     check_attend(attend_problem("bf16", lens, 6, 2, D, 16, 7, spare_rows=3), "bf16", causal, window)
+
+
+PROMPTS = [
+    ([(300, 300)], 8, 2, 128, 16),
+    ([(257, 900)], 4, 4, 64, 64),
+    ([(65, 65)], 1, 1, 128, 128),
+    ([(128, 128), (1, 700), (65, 66), (500, 2000), (3, 3), (0, 9)], 6, 2, 128, 32),
+    ([(1000, 1001)], 7, 1, 64, 128),
+    ([(90, 5000)], 32, 4, 128, 64),
+    ([(9, 4000), (2, 300), (33, 40)], 40, 2, 64, 16),  # groups of 20 heads
+    ([(140, 150 + 70 * i) for i in range(20)], 4, 2, 64, 64),
+    ([(1, 60 + i) for i in range(40)] + [(400, 400)], 16, 2, 128, 16),
+]
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_attend_prompts(case, name):
+    lens, HQ, HKV, D, page = PROMPTS[case]
+    check_attend(attend_problem(name, lens, HQ, HKV, D, page, 60 + case), name)
+
+
+@pytest.mark.parametrize("causal,window", [(False, -1), (True, 1), (True, 70), (True, 128), (True, 300), (False, 33)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_prompts_masks(causal, window, D):
+    lens = [(300, 1000), (129, 129), (1, 400), (200, 170), (80, 1), (66, 0), (400, 700)]
+    check_attend(attend_problem("bf16", lens, 6, 2, D, 16, 16, spare_rows=3), "bf16", causal, window)
+
+
+def test_attend_prompts_with_lacking_pages_and_far_scales():
+    prob = attend_problem("f16", [(200, 900), (120, 500)], 8, 2, 128, 16, 17)
+    q, kc, vc, ks, vs, table, cu, kv = prob
+    table[0, 3], table[0, 8:25], table[1, :5], table[1, 30] = -1, 1 << 29, -9, -1
+    check_attend(prob, "f16")
+    rng = np.random.default_rng(5)
+    far = (q, kc, vc, ks * np.exp2(rng.integers(-3, 4, ks.shape)), vs * np.exp2(rng.integers(-12, 13, vs.shape)), table,
+           cu, kv)
+    check_attend(far, "f16", heads_first=True)
+    odd = (q, kc, vc, (ks * rng.uniform(0.7, 1.4, ks.shape)).astype(np.float32).astype(np.float64),
+           (vs * rng.uniform(0.1, 9.0, vs.shape)).astype(np.float32).astype(np.float64), table, cu, kv)
+    check_attend(odd, "f16", v_rounded=True)
+    check_attend((q, kc, vc, ks, vs * 0.0, table, cu, kv), "f16")
+
+
+def test_attend_prompts_of_far_ranges():
+    q, kc, vc, ks, vs, table, cu, kv = attend_problem("bf16", [(150, 300), (70, 70)], 4, 1, 64, 16, 18)
+    for qs, kz in ((2.0 ** 14, 2.0 ** -14), (2.0 ** -13, 2.0 ** 12)):
+        check_attend((q * qs, kc, vc, ks * kz, vs * 2.0 ** 60, table, cu, kv), "bf16")
+
+
+def test_attend_prompts_not_finite_queries_stay_in_their_rows():
+    prob = attend_problem("f16", [(200, 300), (150, 170)], 4, 1, 64, 16, 19)
+    ref, rl = run_attend(prob, "f16")
+    q = prob[0].copy()
+    q[7, 1, 5], q[222, 2, 0] = np.nan, np.inf
+    got, gl = run_attend((q,) + prob[1:], "f16")
+    bad = np.zeros(gl.shape, bool)
+    bad[1, 7] = bad[2, 222] = True
+    assert np.isnan(gl[bad]).all() and np.isnan(got[bad.T]).all()
+    assert np.array_equal(gl[~bad], rl[~bad]) and np.array_equal(got[~bad.T], ref[~bad.T])
+
+
+def test_attend_prompts_are_the_same_from_run_to_run():
+    prob = attend_problem("bf16", [(700, 3500), (1, 900)], 8, 2, 128, 64, 20)
+    a, al = run_attend(prob, "bf16")
+    for _ in range(3):
+        b, bl = run_attend(prob, "bf16")
+        assert np.array_equal(a, b) and np.array_equal(al, bl)
 
 
 def test_attend_rows_without_keys():
