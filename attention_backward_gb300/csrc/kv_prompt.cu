@@ -23,9 +23,9 @@
 // Work: the line of kv_sched.cuh over all heads, cut evenly over one CTA per
 // SM; at most two parts of units per CTA go through the workspace.
 //
-// Warp roles (12 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 copies (and the
+// Warp roles (16 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 copies (and the
 // walk along the line: it publishes each unit through a two-slot ring), 9 MMA
-// issue, 10-11 conversion.  Every wait is bounded.
+// issue, 10-11 idle, 12-13 conversion of K, 14-15 of V.  Every wait is bounded.
 #include <cuda_fp16.h>
 
 #define AB_INLINE_WAITS 1
@@ -41,9 +41,12 @@ namespace ab {
 namespace {
 
 constexpr int BQ = 128, RT = kKvPrRows, KT = kKvPrKeys, COST = kKvPrCost;
-constexpr int kWarps = 12, THREADS = kWarps * 32;
-constexpr uint32_t REG_SOFT = 208, REG_CTL = 88;
-static_assert(2 * REG_SOFT + REG_CTL == 3 * 168, "register split must equal the launch's registers");
+constexpr int kWarps = 16, THREADS = kWarps * 32;
+// launched at 128 registers a thread, re-split per warpgroup: the softmax
+// warpgroups hold half a row of scores a thread (64; the row's max takes a pass
+// of its own over tensor memory, cheaper than the spills of a whole row)
+constexpr uint32_t REG_SOFT = 160, REG_CTL = 104, REG_CONV = 88;
+static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
 constexpr int kScaleRing = 8;     // blocks of scales; deeper than the conversion can run ahead of the softmax
@@ -79,7 +82,7 @@ enum PrBar : int {
   O_DONE0 = P_READY0 + 2,      // per tile: the P V products issued so far completed
   O_FREE0 = O_DONE0 + 2,       // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,    // 2 slots
-  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the other 11 warps read it
+  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the 13 other working warps read it
   DRAIN = UNIT_EMPTY0 + 2,
   NUM_BARS
 };
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       mbar_init(&bars[O_DONE0 + w], 1);
       mbar_init(&bars[O_FREE0 + w], 4);
       mbar_init(&bars[UNIT_FULL0 + w], 1);
-      mbar_init(&bars[UNIT_EMPTY0 + w], kWarps - 1);
+      mbar_init(&bars[UNIT_EMPTY0 + w], 13);
     }
     for (int i = 0; i < C::NR; ++i) {
       mbar_init(&bars[RAW_FULL0 + i], 1);
@@ -282,6 +285,92 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
     return u;
   };
 
+  if (warp >= 12) {
+    // ============================================================ conversion: two warps for K, two for V
+    // A lane takes 16 bytes of a row (16 values) and writes two 16-byte chunks of
+    // fp16.  Eight lanes (one shared-memory phase) hold rows r and r ^ 5 of an
+    // 8-row group: reads then fall in different halves of the 128-byte lines and
+    // writes on chunks of different parity, without bank conflicts.
+    setmaxnreg_dec<REG_CONV>();
+    const int kv = (warp - 12) >> 1, cw = (warp - 12) & 1;
+    const int row8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), c4 = lane & 3;
+    uint32_t bc = 0;
+    bool ok = true;
+    for (uint32_t uc = 0; ok; ++uc) {
+      const PrUnit u = next_unit(uc, &ok);
+      if (!ok || !u.valid) break;
+      if (u.valid == 2) continue;
+      for (int j = u.j0; j < u.j1; ++j, ++bc) {
+        const uint32_t ic = 2 * bc + kv;
+        const int rs = ic % C::NR, ts = ic % C::NT;
+        const uint32_t n = ic / C::NT;
+        if (!(ok = mbar_wait_warp(&bars[RAW_FULL0 + rs], (ic / C::NR) & 1, wc, kErrWaitStage))) break;
+        if (n >= 1 && !(ok = mbar_wait_warp(&bars[T_EMPTY0 + ts], (n - 1) & 1, wc, kErrWaitKVFree))) break;
+        const uint8_t* const raw = sm + C::OFF_RAW + rs * C::RAW;
+        uint8_t* const out = sm + C::OFF_T + ts * C::TILE;
+        const float* const ratio = v_ratios + (bc % kScaleRing) * kGroups;
+        // V rows that no query sees are zeroed: a zero P times a NaN would be NaN
+        bool edge = false;
+        if (kv) {
+          edge = j * KT < u.lo || (j + 1) * KT > u.hi;
+          const float* const ksc = k_scales + (bc % kScaleRing) * kGroups;
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) edge |= ksc[g] < 0.f;
+        }
+#pragma unroll 2
+        for (int it = 0; it < 8; ++it) {  // 8 rows
+          const int row = cw * 64 + it * 8 + row8;
+          uint4 x[C::NSLAB];
+#pragma unroll
+          for (int s = 0; s < C::NSLAB; ++s)
+            x[s] = *reinterpret_cast<const uint4*>(raw + kv_chunk_at<D>(row, s * 4 + c4));
+          if (kv) {
+            const __half2 f = __float2half2_rn(ratio[row >> 4]);
+            if (edge) {
+              const int key = j * KT + row;
+              const bool page = k_scales[(bc % kScaleRing) * kGroups + (row >> 4)] >= 0.f;
+              if (!page || key < u.lo || key >= u.hi) {
+#pragma unroll
+                for (int s = 0; s < C::NSLAB; ++s) x[s] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+#pragma unroll
+            for (int s = 0; s < C::NSLAB; ++s) {
+              const uint32_t xs[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
+                y[2 * e] = mul_f16x2(y[2 * e], f), y[2 * e + 1] = mul_f16x2(y[2 * e + 1], f);
+              }
+              uint8_t* const slab = out + s * C::SLAB;
+              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+          } else {
+#pragma unroll
+            for (int s = 0; s < C::NSLAB; ++s) {
+              const uint32_t xs[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
+              uint8_t* const slab = out + s * C::SLAB;
+              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars[RAW_EMPTY0 + rs]);
+          mbar_arrive(&bars[T_FULL0 + ts]);
+        }
+      }
+    }
+    finish();
+    return;
+  }
   if (warp >= 8) {
     setmaxnreg_dec<REG_CTL>();
     if (warp == 8) {
@@ -492,76 +581,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       mma_commit_w(&bars[DRAIN]);
       if (lane == 0) mbar_drain(&bars[DRAIN], 0);
       __syncwarp();
-    } else {
-      // ============================================================ conversion (2 warps)
-      // A lane takes 16 bytes of a row (16 values) and writes two 16-byte chunks
-      // of fp16.  Eight lanes (one shared-memory phase) hold rows r and r ^ 5 of
-      // an 8-row group: reads then fall in different halves of the 128-byte
-      // lines and writes on chunks of different parity, without bank conflicts.
-      const int cw = warp - 10;
-      const int row8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), c4 = lane & 3;
-      uint32_t ic = 0;
-      bool ok = true;
-      for (uint32_t uc = 0; ok; ++uc) {
-        const PrUnit u = next_unit(uc, &ok);
-        if (!ok || !u.valid) break;
-        if (u.valid == 2) continue;
-        for (int j = u.j0; j < u.j1 && ok; ++j)
-          for (int kv = 0; kv < 2; ++kv, ++ic) {
-            const int rs = ic % C::NR, ts = ic % C::NT;
-            const uint32_t n = ic / C::NT;
-            if (!(ok = mbar_wait_warp(&bars[RAW_FULL0 + rs], (ic / C::NR) & 1, wc, kErrWaitStage))) break;
-            if (n >= 1 && !(ok = mbar_wait_warp(&bars[T_EMPTY0 + ts], (n - 1) & 1, wc, kErrWaitKVFree))) break;
-            const uint8_t* const raw = sm + C::OFF_RAW + rs * C::RAW;
-            uint8_t* const out = sm + C::OFF_T + ts * C::TILE;
-            const float* const ratio = v_ratios + ((ic >> 1) % kScaleRing) * kGroups;
-            const float* const ksc = k_scales + ((ic >> 1) % kScaleRing) * kGroups;
-#pragma unroll 2
-            for (int g = cw; g < kGroups; g += 2) {
-              const __half2 f = kv ? __float2half2_rn(ratio[g]) : __float2half2_rn(1.f);
-              const bool page = ksc[g] >= 0.f;
-              uint4 w[2 * C::NSLAB];
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int s = 0; s < C::NSLAB; ++s) {
-                  const int row = g * 16 + h * 8 + row8;
-                  w[h * C::NSLAB + s] = *reinterpret_cast<const uint4*>(raw + kv_chunk_at<D>(row, s * 4 + c4));
-                }
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int row = g * 16 + h * 8 + row8, key = j * KT + row;
-                // keys that no row sees: a zero P times a NaN would be NaN
-                const bool zero = kv && (!page || key < u.lo || key >= u.hi);
-#pragma unroll
-                for (int s = 0; s < C::NSLAB; ++s) {
-                  const uint4 x = w[h * C::NSLAB + s];
-                  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                  uint32_t y[8];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
-                    if (kv) {
-                      y[2 * e] = mul_f16x2(y[2 * e], f);
-                      y[2 * e + 1] = mul_f16x2(y[2 * e + 1], f);
-                    }
-                    if (zero) y[2 * e] = y[2 * e + 1] = 0u;
-                  }
-                  uint8_t* const slab = out + s * C::SLAB;
-                  *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                  *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-                }
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&bars[RAW_EMPTY0 + rs]);
-              mbar_arrive(&bars[T_FULL0 + ts]);
-            }
-          }
-      }
     }
+    // warps 10-11: nothing to do
     finish();
     return;
   }
@@ -634,9 +655,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
     for (int j = tl.lo; j < tl.hi; ++j, ++c) {
       if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
       tc_fence_after();
-      uint32_t sr[KT];
-#pragma unroll
-      for (int ch = 0; ch < KT / 32; ++ch) tmem_ld32(tS + ch * 32, sr + ch * 32);
       const float* const sc = k_scales + ((bc0 + j - u.j0) % kScaleRing) * kGroups;
       const float4 sa = *reinterpret_cast<const float4*>(sc), sb = *reinterpret_cast<const float4*>(sc + 4);
       float f[kGroups] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
@@ -644,23 +662,40 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       bool masked = k0 < tl.all_lo || k0 + KT > tl.all_hi;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) masked |= f[g] < 0.f;
-      tmem_ld_wait();
+      uint32_t no_page = 0;  // groups without a page
       if (masked) {
-        const int a = my_lo - k0, b = my_hi - k0;
 #pragma unroll
-        for (int k = 0; k < KT; ++k)
-          if (k < a || k >= b || f[k / 16] < 0.f) sr[k] = __float_as_uint(-INFINITY);
+        for (int g = 0; g < kGroups; ++g) no_page |= f[g] < 0.f ? 1u << g : 0u;
       }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) f[g] = fabsf(f[g]) * rs;
+      const int v_lo = my_lo - k0, v_hi = my_hi - k0;
+      uint32_t sr[64];
+      // 64 scores of the row from column 64 h on, -inf where the key is not seen
+      auto load_half = [&](int h) {
+        tmem_ld32(tS + h * 64, sr);
+        tmem_ld32(tS + h * 64 + 32, sr + 32);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (h * 64 + k < v_lo || h * 64 + k >= v_hi || (no_page >> (h * 4 + k / 16) & 1u))
+              sr[k] = __float_as_uint(-INFINITY);
+        }
+      };
       // largest raw score of each 16 columns, then of the row in log2 units
       float m_new = m_used;
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        float mx[2] = {-INFINITY, -INFINITY};
+      for (int h = 0; h < 2; ++h) {
+        load_half(h);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(sr[g * 16 + k]));
-        const float top = fmaxf(mx[0], mx[1]);
-        f[g] = fabsf(f[g]) * rs;  // (a group without a page has no finite score)
-        m_new = fmaxf(m_new, top == -INFINITY ? -INFINITY : top * f[g]);
+        for (int g = 0; g < 4; ++g) {
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 16; ++k) mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(sr[g * 16 + k]));
+          const float top = fmaxf(mx[0], mx[1]);
+          m_new = fmaxf(m_new, top == -INFINITY ? -INFINITY : top * f[h * 4 + g]);
+        }
       }
       const bool resc = m_used != -INFINITY && m_new > m_used + kRescaleLog2;
       const float shrink = resc ? ex2(m_used - m_new) : 1.f;
@@ -684,23 +719,28 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       const float2 nm2 = make_float2(-msub, -msub);
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int ch = 0; ch < KT / 32; ++ch) {
-        uint32_t pw[16];
+      for (int h = 0; h < 2; ++h) {
+        load_half(h);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float fg = f[ch * 2 + e / 8];
-          float2 y = make_float2(__uint_as_float(sr[ch * 32 + 2 * e]), __uint_as_float(sr[ch * 32 + 2 * e + 1]));
-          if (masked) {  // (a zero scale times -inf would be NaN)
-            y.x = y.x == -INFINITY ? -INFINITY : y.x * fg - msub;
-            y.y = y.y == -INFINITY ? -INFINITY : y.y * fg - msub;
-          } else {
-            y = __ffma2_rn(y, make_float2(fg, fg), nm2);
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float fg = f[h * 4 + ch * 2 + e / 8];
+            float2 y = make_float2(__uint_as_float(sr[ch * 32 + 2 * e]), __uint_as_float(sr[ch * 32 + 2 * e + 1]));
+            if (masked) {  // (a zero scale times -inf would be NaN)
+              y.x = y.x == -INFINITY ? -INFINITY : y.x * fg - msub;
+              y.y = y.y == -INFINITY ? -INFINITY : y.y * fg - msub;
+            } else {
+              y = __ffma2_rn(y, make_float2(fg, fg), nm2);
+            }
+            const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+            sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
+            pw[e] = pack2<false>(pp.x, pp.y);
           }
-          const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-          sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
-          pw[e] = pack2<false>(pp.x, pp.y);
+          // P pairs into the columns of scores that have been read for good
+          tmem_st16(tS + h * 32 + ch * 16, pw);
         }
-        tmem_st16(tS + ch * 16, pw);
       }
       l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
       tmem_st_wait();
