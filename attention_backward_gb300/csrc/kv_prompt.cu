@@ -23,9 +23,10 @@
 // Work: the line of kv_sched.cuh over all heads, cut evenly over one CTA per
 // SM; at most two parts of units per CTA go through the workspace.
 //
-// Warp roles (16 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 copies (and the
-// walk along the line: it publishes each unit through a two-slot ring), 9 MMA
-// issue, 10-11 idle, 12-13 conversion of K, 14-15 of V.  Every wait is bounded.
+// Warp roles (16 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 copies, 9 MMA
+// issue, 10 the walk along the line, a unit ahead of the others (it publishes
+// units, with their largest V scale, through a two-slot ring), 11 idle, 12-13
+// conversion of K, 14-15 of V.  Every wait is bounded.
 #include <cuda_fp16.h>
 
 #define AB_INLINE_WAITS 1
@@ -82,7 +83,7 @@ enum PrBar : int {
   O_DONE0 = P_READY0 + 2,      // per tile: the P V products issued so far completed
   O_FREE0 = O_DONE0 + 2,       // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,    // 2 slots
-  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the 13 other working warps read it
+  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the 14 other working warps read it
   DRAIN = UNIT_EMPTY0 + 2,
   NUM_BARS
 };
@@ -90,7 +91,7 @@ static_assert(NUM_BARS <= 48, "barrier storage");
 
 // A unit, or the CTA's part of one: key blocks [j0, j1).
 struct PrUnit {
-  int a, nq, L, off, R;  // the request (kv_sched.cuh)
+  int n, a, nq, L, off, R;  // the request (kv_sched.cuh)
   int row0, head;
   int j0, j1;            // j0 == j1: no block, its rows are zero
   int lo, hi;            // keys that some row of the unit sees
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       mbar_init(&bars[O_DONE0 + w], 1);
       mbar_init(&bars[O_FREE0 + w], 4);
       mbar_init(&bars[UNIT_FULL0 + w], 1);
-      mbar_init(&bars[UNIT_EMPTY0 + w], 13);
+      mbar_init(&bars[UNIT_EMPTY0 + w], 14);
     }
     for (int i = 0; i < C::NR; ++i) {
       mbar_init(&bars[RAW_FULL0 + i], 1);
@@ -373,113 +374,64 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   }
   if (warp >= 8) {
     setmaxnreg_dec<REG_CTL>();
-    if (warp == 8) {
-      // ============================================================ copies
+    if (warp == 10) {
+      // ============================================================ the walk
       int w0 = 0;
       int64_t x = begin;
       while (x >= s_work[w0]) x -= s_work[w0++];
       PrCursor cur = walk_to(p, w0 * per, x);
       KvReq rq = kv_request(cur.n, p);
-      uint32_t ic = 0;  // raw tiles so far
-      bool ok = true;
-      uint32_t uc = 0;
-      for (x = begin; ok; ++uc) {
-        const uint32_t slot = uc & 1;
-        if (uc >= 2 && !(ok = mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wc, kErrWaitTile)))
-          break;
+      x = begin;
+      for (uint32_t uc = 0;; ++uc) {
         PrUnit u{};
-        u.valid = x < end;
-        KvTiles kt{};
         int64_t stop = x;
-        bool ends = false;
+        u.valid = x < end;
         if (u.valid) {
-          kt = kv_row_tile<RT, KT>(rq, cur.rt, p);
+          const KvTiles kt = kv_row_tile<RT, KT>(rq, cur.rt, p);
           const int64_t unit0 = x - cur.pos;
           stop = unit0 + COST + kt.n < end ? unit0 + COST + kt.n : end;
           const int part0 = imax(0, cur.pos - COST), part1 = imax(0, static_cast<int>(stop - unit0) - COST);
-          u.a = rq.a, u.nq = rq.nq, u.L = rq.L, u.off = rq.off, u.R = rq.R;
+          const bool whole = part0 == 0 && part1 == kt.n;
+          u.n = cur.n, u.a = rq.a, u.nq = rq.nq, u.L = rq.L, u.off = rq.off, u.R = rq.R;
           u.row0 = cur.rt * RT, u.head = cur.head;
           u.lo = kt.lo, u.hi = kt.hi;
-          u.j0 = kt.t0 + part0, u.j1 = kt.t0 + part1;
-          const bool whole = part0 == 0 && part1 == kt.n;
+          u.j0 = kt.t0 + part0;
+          u.j1 = kt.hi > kt.lo ? kt.t0 + part1 : u.j0;  // (a unit that sees nothing has no block)
           u.slot = whole ? -1 : 2 * static_cast<int>(blockIdx.x) + (part0 > 0 ? 0 : 1);
-          const bool none = part1 <= part0;  // only the start-up positions: nothing to do
-          ends = part0 > 0 && part1 == kt.n;
-          if (ends && lane == 0) {
+          if (part1 <= part0) u.valid = 2;  // only start-up positions: nothing to do
+          if (lane == 0 && part0 > 0 && part1 == kt.n) {
             const int g0 = kv_part_of(total, unit0 + COST, parts);
             p.desc[blockIdx.x] = make_int4(cur.n, cur.rt, cur.head, g0);
             p.fin[blockIdx.x] = g0;
           }
-          if (kt.hi <= kt.lo) u.j1 = u.j0;  // the one tile of a unit that sees nothing
-          if (none) u.valid = 2;            // (consumers skip it)
         }
-        auto page_of = [&](int k0) {  // page of keys [k0, k0 + 16), -1 where there is none or nothing is seen
-          if (k0 >= kt.hi || k0 + 16 <= kt.lo) return -1;
-          const int b = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
-          return b >= 0 && b < p.num_blocks ? b : -1;
-        };
         if (u.valid == 1) {
-          // the largest V scale of the part's pages
-          float vref = 0.f;
-          for (int k0 = u.j0 * KT + lane * 16; k0 < u.j1 * KT; k0 += 32 * 16) {
-            const int b = page_of(k0);
-            if (b >= 0) vref = fmaxf(vref, p.v_scale[static_cast<int64_t>(b) * p.HKV + cur.head]);
+          // the largest V scale of the pages that the part sees, four pages a lane in flight
+          float top = 0.f;
+          const int k0 = imax(u.lo, u.j0 * KT), k1 = imin(u.hi, u.j1 * KT);
+          const int pg1 = k1 > k0 ? ((k1 - 1) >> p.page_log2) + 1 : 0;
+          for (int pg = (k0 >> p.page_log2) + lane; pg < pg1; pg += 128) {
+            int b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              b[i] = pg + 32 * i < pg1 ? p.table[u.n * p.table_stride + pg + 32 * i] : -1;
+              if (b[i] >= p.num_blocks) b[i] = -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (b[i] >= 0) top = fmaxf(top, p.v_scale[static_cast<int64_t>(b[i]) * p.HKV + u.head]);
           }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, o));
-          u.vref = vref < 0x1p-126f ? 0.f : vref;
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          u.vref = top < 0x1p-126f ? 0.f : top;
         }
+        const uint32_t slot = uc & 1;
+        if (uc >= 2 && !mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wc, kErrWaitTile)) break;
         if (lane == 0) {
           units[slot] = u;
           mbar_arrive(&bars[UNIT_FULL0 + slot]);
         }
         if (!u.valid) break;
-        if (u.valid == 1) {
-          const float vinv = u.vref > 0.f ? 1.f / u.vref : 0.f;
-          // page ids and scales of four blocks at a time: lane i those of 16-key group i
-          int blk = -1;
-          float ksc = -1.f, vra = 0.f;
-          const int s_mask = (1 << p.page_log2) - 1;
-          for (int j = u.j0; j < u.j1 && ok; ++j) {
-            const int q4 = (j - u.j0) & 3;
-            if (q4 == 0) {
-              const int k0 = j * KT + lane * 16;
-              blk = k0 < u.j1 * KT ? page_of(k0) : -1;
-              ksc = -1.f, vra = 0.f;
-              if (blk >= 0) {
-                const int64_t at = static_cast<int64_t>(blk) * p.HKV + cur.head;
-                ksc = p.k_scale[at], vra = p.v_scale[at] * vinv;
-              }
-            }
-            for (int kv = 0; kv < 2; ++kv, ++ic) {
-              const int rs = ic % C::NR;
-              const uint32_t n = ic / C::NR;
-              if (n >= 1 && !(ok = mbar_wait_warp(&bars[RAW_EMPTY0 + rs], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
-              const uint32_t have = (__ballot_sync(0xffffffffu, blk >= 0) >> (8 * q4)) & 0xffu;
-              if (kv == 0) {
-                // the block's scales (the ring is deep enough that its last readers are done)
-                const uint32_t sr = (ic >> 1) % kScaleRing;
-                if ((lane >> 3) == q4) {
-                  k_scales[sr * kGroups + (lane & 7)] = ksc;
-                  v_ratios[sr * kGroups + (lane & 7)] = vra;
-                }
-                __syncwarp();
-              }
-              if (lane == 0) {
-                if (have) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], __popc(have) * 16 * D);
-                else mbar_arrive(&bars[RAW_FULL0 + rs]);
-              }
-              for (int g = 0; g < kGroups; ++g) {
-                const int b = __shfl_sync(0xffffffffu, blk, 8 * q4 + g);
-                if (lane == 0 && b >= 0)
-                  tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + g * 16 * D, kv ? &maps.v : &maps.k, &bars[RAW_FULL0 + rs],
-                              0, u.head, (j * KT + g * 16) & s_mask, b);
-              }
-            }
-          }
-          if (!ok) break;
-        }
-        // next unit
         x = stop;
         cur.pos = 0;
         if (x < end && ++cur.head == p.HKV) {
@@ -489,6 +441,64 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             do {
               rq = kv_request(++cur.n, p);
             } while (rq.R == 0);
+          }
+        }
+      }
+    } else if (warp == 8) {
+      // ============================================================ copies
+      // Lane i looks up 16-key group i of four blocks, and copies it: page ids
+      // and scales are fetched four blocks ahead.
+      const int s_mask = (1 << p.page_log2) - 1;
+      uint32_t ic = 0;  // raw tiles so far
+      bool ok = true;
+      for (uint32_t uc = 0; ok; ++uc) {
+        const PrUnit u = next_unit(uc, &ok);
+        if (!ok || !u.valid) break;
+        if (u.valid == 2) continue;
+        const float vinv = u.vref > 0.f ? 1.f / u.vref : 0.f;
+        const int k_end = imin(u.hi, u.j1 * KT);
+        auto page_of = [&](int k0) {  // page of keys [k0, k0 + 16), -1 where there is none or nothing is seen
+          if (k0 >= k_end || k0 + 16 <= u.lo) return -1;
+          const int b = p.table[u.n * p.table_stride + (k0 >> p.page_log2)];
+          return b >= 0 && b < p.num_blocks ? b : -1;
+        };
+        int blk = -1, nblk = page_of(u.j0 * KT + lane * 16);
+        float ksc = -1.f, vra = 0.f, nks = 0.f, nvs = 0.f;
+        auto scales_of = [&]() {
+          if (nblk < 0) return;
+          const int64_t at = static_cast<int64_t>(nblk) * p.HKV + u.head;
+          nks = p.k_scale[at], nvs = p.v_scale[at];
+        };
+        scales_of();
+        for (int j = u.j0; j < u.j1 && ok; ++j) {
+          const int q4 = (j - u.j0) & 3;
+          if (q4 == 0) {
+            blk = nblk, ksc = blk >= 0 ? nks : -1.f, vra = blk >= 0 ? nvs * vinv : 0.f;
+            nblk = page_of((j + 4) * KT + lane * 16);
+          } else if (q4 == 2) {
+            scales_of();
+          }
+          const uint32_t have = (__ballot_sync(0xffffffffu, blk >= 0) >> (8 * q4)) & 0xffu;
+          const bool mine = (lane >> 3) == q4;
+          for (int kv = 0; kv < 2; ++kv, ++ic) {
+            const int rs = ic % C::NR;
+            const uint32_t n = ic / C::NR;
+            if (n >= 1 && !(ok = mbar_wait_warp(&bars[RAW_EMPTY0 + rs], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
+            if (kv == 0 && mine) {
+              // the block's scales (the ring is deep enough that its last readers are done)
+              const uint32_t sr = (ic >> 1) % kScaleRing;
+              k_scales[sr * kGroups + (lane & 7)] = ksc;
+              v_ratios[sr * kGroups + (lane & 7)] = vra;
+            }
+            __syncwarp();
+            if (lane == 0) {
+              if (have) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], __popc(have) * 16 * D);
+              else mbar_arrive(&bars[RAW_FULL0 + rs]);
+            }
+            __syncwarp();
+            if (mine && blk >= 0)
+              tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + (lane & 7) * 16 * D, kv ? &maps.v : &maps.k,
+                          &bars[RAW_FULL0 + rs], 0, u.head, (j * KT + (lane & 7) * 16) & s_mask, blk);
           }
         }
       }
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       if (lane == 0) mbar_drain(&bars[DRAIN], 0);
       __syncwarp();
     }
-    // warps 10-11: nothing to do
+    // warp 11: nothing to do
     finish();
     return;
   }
@@ -668,7 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         for (int g = 0; g < kGroups; ++g) no_page |= f[g] < 0.f ? 1u << g : 0u;
       }
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) f[g] = fabsf(f[g]) * rs;
+      for (int g = 0; g < kGroups; ++g) f[g] = fmaxf(fabsf(f[g]) * rs, 0x1p-126f);  // (0 times -inf would be NaN)
       const int v_lo = my_lo - k0, v_hi = my_hi - k0;
       uint32_t sr[64];
       // 64 scores of the row from column 64 h on, -inf where the key is not seen
@@ -694,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
 #pragma unroll
           for (int k = 0; k < 16; ++k) mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(sr[g * 16 + k]));
           const float top = fmaxf(mx[0], mx[1]);
-          m_new = fmaxf(m_new, top == -INFINITY ? -INFINITY : top * f[h * 4 + g]);
+          m_new = fmaxf(m_new, top * f[h * 4 + g]);
         }
       }
       const bool resc = m_used != -INFINITY && m_new > m_used + kRescaleLog2;
@@ -728,12 +738,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           for (int e = 0; e < 16; ++e) {
             const float fg = f[h * 4 + ch * 2 + e / 8];
             float2 y = make_float2(__uint_as_float(sr[ch * 32 + 2 * e]), __uint_as_float(sr[ch * 32 + 2 * e + 1]));
-            if (masked) {  // (a zero scale times -inf would be NaN)
-              y.x = y.x == -INFINITY ? -INFINITY : y.x * fg - msub;
-              y.y = y.y == -INFINITY ? -INFINITY : y.y * fg - msub;
-            } else {
-              y = __ffma2_rn(y, make_float2(fg, fg), nm2);
-            }
+            y = __ffma2_rn(y, make_float2(fg, fg), nm2);
             const float2 pp = make_float2(ex2(y.x), ex2(y.y));
             sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
             pw[e] = pack2<false>(pp.x, pp.y);
