@@ -48,18 +48,23 @@ attn_status_t check_cache(const attn_kv_cache_t* c) {
 
 bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_DT_F16 || dt == ATTN_DT_BF16; }
 
-bool make_cache_map(CUtensorMap* m, const void* base, const attn_strides_t& st, const attn_kv_cache_t& c) {
+bool make_cache_map(CUtensorMap* m, const void* base, const attn_strides_t& st, const attn_kv_cache_t& c,
+                    int64_t box_tokens) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.HKV),
                         static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.num_blocks)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.h), static_cast<cuuint64_t>(st.s),
                            static_cast<cuuint64_t>(st.b)};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(c.D), 1, kKvBoxTokens, 1};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(c.D), 1, static_cast<cuuint32_t>(box_tokens), 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_maps(KvMaps* m, const attn_kv_cache_t& c, int64_t box_tokens) {
+  return make_cache_map(&m->k, c.k, c.sk, c, box_tokens) && make_cache_map(&m->v, c.v, c.sv, c, box_tokens);
 }
 
 // Workspace of attention over the cache: the header, then for each of its two
@@ -197,27 +202,28 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.err = &reinterpret_cast<WsHeader*>(ws)->err;
   p.timeout_ns = kWaitTimeoutNs;
-  KvMaps maps;
-  if (!make_cache_map(&maps.k, cache->k, cache->sk, *cache) || !make_cache_map(&maps.v, cache->v, cache->sv, *cache))
-    return ATTN_ERR_INVALID_ARG;
   const bool bf16 = dtype == ATTN_DT_BF16;
   const int sms = sm_count();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Which kernels: requests of kKvPrMinRows rows or more go to the prompt kernel.
-  // Its launches are left out where there can be none, or where the mean request
-  // is so small that one would be the odd one out of a decode step (the decode
-  // kernel serves any number of rows).
-  const bool prompts = kv_may_prompt(T, p.G) && T * p.G >= num_seqs * (kKvPrMinRows / 4);
-  const bool decodes = !prompts || num_seqs > 1 || T * p.G < kKvPrMinRows;
+  // Which kernels: requests of kKvPrMinRows rows or more go to the prompt kernel,
+  // the others to the decode kernel; either serves any number of rows.  One of
+  // them is left out where the other can take the odd requests along: by the mean
+  // of rows a request, below a quarter of that limit or above four times it.
+  const int64_t mean = T * p.G / num_seqs;
+  const bool prompts = kv_may_prompt(T, p.G) && mean >= kKvPrMinRows / 4;
+  const bool decodes = !prompts || (num_seqs > 1 && mean < 4 * kKvPrMinRows);
+  KvMaps small, large;
+  if ((decodes && !make_maps(&small, *cache, kKvDecKeys)) || (prompts && !make_maps(&large, *cache, cache->page_size)))
+    return ATTN_ERR_INVALID_ARG;
   p.rows_min = 0, p.rows_max = prompts ? kKvPrMinRows - 1 : 0x7fffffff;
   if (decodes) {
     kv_place(&p, kv_ws_decode(cache->D), ws);
-    if (const cudaError_t e = launch_kv_decode(p, maps, bf16, sms, st); e != cudaSuccess) return launch_status(e);
+    if (const cudaError_t e = launch_kv_decode(p, small, bf16, sms, st); e != cudaSuccess) return launch_status(e);
   }
   if (!prompts) return ATTN_OK;
   p.rows_min = decodes ? kKvPrMinRows : 0, p.rows_max = 0x7fffffff;
   kv_place(&p, kv_ws_prompt(cache->D), ws);
-  return launch_status(launch_kv_prompt(p, maps, bf16, sms, !decodes, st));
+  return launch_status(launch_kv_prompt(p, large, bf16, sms, !decodes, st));
 }
 
 }  // extern "C"

@@ -73,11 +73,11 @@ struct KvAttnParams {
 };
 
 // Tensor maps of the cache's bytes, dims (D, HKV, page_size, num_blocks): box D
-// bytes x 16 tokens of one head, swizzled over rows of D bytes.
+// bytes x tokens of one head (16 in the decode kernel, a page in the prompt
+// kernel), swizzled over rows of D bytes.
 struct KvMaps {
   CUtensorMap k, v;
 };
-constexpr int kKvBoxTokens = 16;
 
 // Requests of at least this many rows (queries * heads of a group) go to the
 // prompt kernel, the others to the decode kernel.

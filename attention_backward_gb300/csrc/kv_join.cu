@@ -27,9 +27,11 @@ template <int D, int RT, bool BF16>
 __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAttnParams p, int workers, int ctas, int stride,
                                                                   bool first) {
   constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
+  // rows of a warp at once: one where parts are many and rows few, eight where a unit has 256
+  constexpr int NR = RT > 16 ? 8 : 1, PF = 8 / NR;  // and parts in flight
   __shared__ uint16_t list[kKvDecMaxWorkers];
   __shared__ int s_cnt[kJoinWarps];
-  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float s_o[NR == 1 ? kJoinWarps : 1][D];
   __shared__ float2 s_ml[kJoinWarps];
   grid_dependency_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -68,18 +70,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
   }
   for (uint32_t m = mine; m != 0; m &= m - 1) list[at0++] = static_cast<uint16_t>(tid * PER + __ffs(m) - 1);
   __syncthreads();
-  const int rows = units * RT;  // those past a unit's last row are skipped
-  int shares = 1;               // warps a row
-  while (shares < kJoinWarps && rows * shares * 2 <= static_cast<int>(gridDim.x) * kJoinWarps) shares *= 2;
+  const int items = units * (RT / NR);  // those past a unit's last row are skipped
+  int shares = 1;                       // warps an item
+  if (NR == 1)
+    while (shares < kJoinWarps && items * shares * 2 <= static_cast<int>(gridDim.x) * kJoinWarps) shares *= 2;
   const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
-  for (int r0 = blockIdx.x * groups; r0 < rows; r0 += static_cast<int>(gridDim.x) * groups) {
-    const int item = r0 + group;
+  for (int t0 = blockIdx.x * groups; t0 < items; t0 += static_cast<int>(gridDim.x) * groups) {
+    const int item = t0 + group;
     KvReq rq{};
     int4 d = make_int4(-1, 0, 0, 0);
     int row0 = 0, live = 0, i0 = 0, i1 = 0;
-    const int row = item % RT;
-    if (item < rows) {
-      const int w = list[item / RT];
+    const int row = item % (RT / NR) * NR;  // my first row of the unit
+    if (item < items) {
+      const int w = list[item / (RT / NR)];
       d = p.desc[w];
       rq = kv_request(d.x, p);
       row0 = d.y * RT, live = imin(RT, rq.R - row0);
@@ -87,77 +90,101 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
       i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
     }
     auto slot_of = [&](int i) { return 2 * ((d.w + i) * stride + (stride > 1 ? d.z : 0)) + (i == 0 ? 1 : 0); };
-    float m = -INFINITY, l = 0.f, acc[ND];
+    float m[NR], l[NR], acc[NR][ND];
 #pragma unroll
-    for (int u = 0; u < ND; ++u) acc[u] = 0.f;
+    for (int r = 0; r < NR; ++r) {
+      m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+      for (int u = 0; u < ND; ++u) acc[r][u] = 0.f;
+    }
     if (row < live) {
-      for (int j = i0; j < i1; j += 32) {
-        // (m, l) of up to 32 parts, then their rows, rescaled where m grows
-        const float2 v = j + lane < i1 ? p.part_ml[slot_of(j + lane) * RT + row] : make_float2(0.f, 0.f);
+      // PF parts of NR rows in flight; (m, l) of up to 32 / NR parts looked up together, a lane each
+      constexpr int LOOK = 32 / NR;
+      for (int j = i0; j < i1; j += LOOK) {
+        const int n = imin(LOOK, i1 - j);
+        float2 v = make_float2(0.f, 0.f);
+        if (lane / NR < n && row + lane % NR < live) v = p.part_ml[static_cast<int64_t>(slot_of(j + lane / NR)) * RT + row + lane % NR];
+        // the rows' max over these parts (lanes of one row are NR apart), then their weights
         float mx = v.y == 0.f ? -INFINITY : v.x;
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        mx = fmaxf(mx, m);
-        if (mx > m) {
-          const float g = m == -INFINITY ? 0.f : ex2(m - mx);
-          l *= g;
+        for (int s = NR; s < 32; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        float mine_m = m[0];
 #pragma unroll
-          for (int u = 0; u < ND; ++u) acc[u] *= g;
-          m = mx;
+        for (int r = 1; r < NR; ++r) mine_m = lane % NR == r ? m[r] : mine_m;
+        mx = fmaxf(mx, mine_m);  // of row lane % NR
+        const float w = v.y == 0.f ? 0.f : ex2(v.x - mx);
+        const float wl = w * v.y;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float mr = __shfl_sync(0xffffffffu, mx, r);
+          const float g = m[r] == mr ? 1.f : (m[r] == -INFINITY ? 0.f : ex2(m[r] - mr));
+          m[r] = mr;
+          l[r] *= g;
+#pragma unroll
+          for (int u = 0; u < ND; ++u) acc[r][u] *= g;
+          if (lane % NR == r) l[r] += wl;
         }
-        const float f = v.y == 0.f ? 0.f : ex2(v.x - m);
-        l += f * v.y;
-        const int n = imin(32, i1 - j);
-        for (int i = 0; i < n; i += 8) {  // eight rows in flight
-          float x[8][ND];
+        for (int i = 0; i < n; i += PF) {
+          float x[PF][NR][ND];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int at = slot_of(j + imin(i + k, n - 1));
-            const float* from = p.part_o + (static_cast<int64_t>(at) * RT + row) * D + lane * ND;
-            if constexpr (ND == 4) {
-              const float4 y = *reinterpret_cast<const float4*>(from);
-              x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-            } else {
-              const float2 y = *reinterpret_cast<const float2*>(from);
-              x[k][0] = y.x, x[k][1] = y.y;
+          for (int k = 0; k < PF; ++k) {
+            const int64_t at = static_cast<int64_t>(slot_of(j + imin(i + k, n - 1))) * RT + row;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const float* from = p.part_o + (at + imin(r, live - 1 - row)) * D + lane * ND;
+              if constexpr (ND == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(from);
+                x[k][r][0] = y.x, x[k][r][1] = y.y, x[k][r][2] = y.z, x[k][r][3] = y.w;
+              } else {
+                const float2 y = *reinterpret_cast<const float2*>(from);
+                x[k][r][0] = y.x, x[k][r][1] = y.y;
+              }
             }
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, (i + k) & 31);
-            if (i + k < n && fk != 0.f) {  // (a part that saw no key of the row says nothing)
+          for (int k = 0; k < PF; ++k)
 #pragma unroll
-              for (int u = 0; u < ND; ++u) acc[u] += fk * x[k][u];
+            for (int r = 0; r < NR; ++r) {
+              const float f = __shfl_sync(0xffffffffu, w, ((i + k) * NR + r) & 31);
+              if (i + k < n && f != 0.f) {  // (a part that saw no key of the row says nothing)
+#pragma unroll
+                for (int u = 0; u < ND; ++u) acc[r][u] += f * x[k][r][u];
+              }
             }
-          }
         }
       }
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
       if (share > 0) {
 #pragma unroll
-        for (int u = 0; u < ND; ++u) s_o[warp][lane * ND + u] = acc[u];
-        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        for (int u = 0; u < ND; ++u) s_o[NR == 1 ? warp : 0][lane * ND + u] = acc[0][u];
+        if (lane == 0) s_ml[warp] = make_float2(m[0], l[0]);
       }
     }
     if (shares > 1) __syncthreads();
-    if (share == 0 && row < live) {
-      for (int k = 1; k < shares; ++k) {
-        const float2 v = s_ml[warp + k];
-        if (v.y == 0.f) continue;
-        const float mx = fmaxf(m, v.x), g = l == 0.f ? 0.f : ex2(m - mx), f = ex2(v.x - mx);
-        l = l * g + v.y * f;
-        m = mx;
+    if (share == 0) {
 #pragma unroll
-        for (int u = 0; u < ND; ++u) acc[u] = acc[u] * g + s_o[warp + k][lane * ND + u] * f;
+      for (int r = 0; r < NR; ++r) {
+        if (row + r >= live) continue;
+        for (int k = 1; k < shares; ++k) {
+          const float2 v = s_ml[warp + k];
+          if (v.y == 0.f) continue;
+          const float mx = fmaxf(m[r], v.x), g = l[r] == 0.f ? 0.f : ex2(m[r] - mx), f = ex2(v.x - mx);
+          l[r] = l[r] * g + v.y * f;
+          m[r] = mx;
+#pragma unroll
+          for (int u = 0; u < ND; ++u) acc[r][u] = acc[r][u] * g + s_o[NR == 1 ? warp + k : 0][lane * ND + u] * f;
+        }
+        const int64_t at = static_cast<int64_t>(rq.a) + (row0 + row + r) / p.G;
+        const int hq = d.z * p.G + (row0 + row + r) % p.G;
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+        for (int u = 0; u < ND; ++u) acc[r][u] *= inv;
+        store_o<BF16, ND>(p, at, hq, lane * ND, acc[r]);
+        if (lane == 0) store_lse(p, at, hq, m[r], l[r]);
       }
-      const int64_t at = static_cast<int64_t>(rq.a) + (row0 + row) / p.G;
-      const int hq = d.z * p.G + (row0 + row) % p.G;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-      for (int u = 0; u < ND; ++u) acc[u] *= inv;
-      store_o<BF16, ND>(p, at, hq, lane * ND, acc);
-      if (lane == 0) store_lse(p, at, hq, m, l);
     }
     if (shares > 1) __syncthreads();
   }

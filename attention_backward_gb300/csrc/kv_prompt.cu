@@ -44,9 +44,8 @@ namespace {
 constexpr int BQ = 128, RT = kKvPrRows, KT = kKvPrKeys, COST = kKvPrCost;
 constexpr int kWarps = 16, THREADS = kWarps * 32;
 // launched at 128 registers a thread, re-split per warpgroup: the softmax
-// warpgroups hold half a row of scores a thread (64; the row's max takes a pass
-// of its own over tensor memory, cheaper than the spills of a whole row)
-constexpr uint32_t REG_SOFT = 160, REG_CTL = 104, REG_CONV = 88;
+// warpgroups hold a row of 64 P pairs and 32 scores a thread
+constexpr uint32_t REG_SOFT = 168, REG_CTL = 88, REG_CONV = 88;
 static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
@@ -446,9 +445,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       }
     } else if (warp == 8) {
       // ============================================================ copies
-      // Lane i looks up 16-key group i of four blocks, and copies it: page ids
-      // and scales are fetched four blocks ahead.
-      const int s_mask = (1 << p.page_log2) - 1;
+      // Lane i looks up 16-key group i of four blocks (page ids and scales four
+      // blocks ahead); the first lane of a page that has seen keys copies it.
+      const int gp = 1 << (p.page_log2 - 4);  // groups a page
+      const uint32_t page_lanes = ((1u << gp) - 1u) << (lane & ~(gp - 1));
       uint32_t ic = 0;  // raw tiles so far
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
@@ -457,15 +457,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         if (u.valid == 2) continue;
         const float vinv = u.vref > 0.f ? 1.f / u.vref : 0.f;
         const int k_end = imin(u.hi, u.j1 * KT);
-        auto page_of = [&](int k0) {  // page of keys [k0, k0 + 16), -1 where there is none or nothing is seen
-          if (k0 >= k_end || k0 + 16 <= u.lo) return -1;
-          const int b = p.table[u.n * p.table_stride + (k0 >> p.page_log2)];
-          return b >= 0 && b < p.num_blocks ? b : -1;
+        auto look_up = [&](int k0) {  // table entry of keys [k0, k0 + 16), -1 where nothing is seen
+          return k0 >= k_end || k0 + 16 <= u.lo ? -1 : p.table[u.n * p.table_stride + (k0 >> p.page_log2)];
         };
-        int blk = -1, nblk = page_of(u.j0 * KT + lane * 16);
+        auto held = [&](int b) { return b >= 0 && b < p.num_blocks; };
+        int blk = -1, nblk = look_up(u.j0 * KT + lane * 16);
         float ksc = -1.f, vra = 0.f, nks = 0.f, nvs = 0.f;
         auto scales_of = [&]() {
-          if (nblk < 0) return;
+          if (!held(nblk)) return;
           const int64_t at = static_cast<int64_t>(nblk) * p.HKV + u.head;
           nks = p.k_scale[at], nvs = p.v_scale[at];
         };
@@ -473,13 +472,17 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         for (int j = u.j0; j < u.j1 && ok; ++j) {
           const int q4 = (j - u.j0) & 3;
           if (q4 == 0) {
-            blk = nblk, ksc = blk >= 0 ? nks : -1.f, vra = blk >= 0 ? nvs * vinv : 0.f;
-            nblk = page_of((j + 4) * KT + lane * 16);
+            blk = held(nblk) ? nblk : -1;
+            ksc = blk >= 0 ? nks : -1.f, vra = blk >= 0 ? nvs * vinv : 0.f;
+            nblk = look_up((j + 4) * KT + lane * 16);
           } else if (q4 == 2) {
             scales_of();
           }
-          const uint32_t have = (__ballot_sync(0xffffffffu, blk >= 0) >> (8 * q4)) & 0xffu;
           const bool mine = (lane >> 3) == q4;
+          const uint32_t seen = __ballot_sync(0xffffffffu, mine && blk >= 0);
+          const bool leads = mine && blk >= 0 && (seen & page_lanes & ((1u << lane) - 1u)) == 0;
+          const int pages = __popc(__ballot_sync(0xffffffffu, leads));
+          const int row0 = ((lane & 7) & ~(gp - 1)) * 16;  // of my page in the block
           for (int kv = 0; kv < 2; ++kv, ++ic) {
             const int rs = ic % C::NR;
             const uint32_t n = ic / C::NR;
@@ -492,13 +495,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             }
             __syncwarp();
             if (lane == 0) {
-              if (have) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], __popc(have) * 16 * D);
+              if (pages) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], (pages * D) << p.page_log2);
               else mbar_arrive(&bars[RAW_FULL0 + rs]);
             }
             __syncwarp();
-            if (mine && blk >= 0)
-              tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + (lane & 7) * 16 * D, kv ? &maps.v : &maps.k,
-                          &bars[RAW_FULL0 + rs], 0, u.head, (j * KT + (lane & 7) * 16) & s_mask, blk);
+            if (leads)
+              tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + row0 * D, kv ? &maps.v : &maps.k, &bars[RAW_FULL0 + rs], 0,
+                          u.head, 0, blk);
           }
         }
       }
@@ -661,7 +664,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[Q_FULL0 + w]);
     }
-    float m_used = -INFINITY, l = 0.f;
+    // (rows past the request's last one go along with a max of their own)
+    float m_used = live ? -INFINITY : 0.f, l = 0.f;
     for (int j = tl.lo; j < tl.hi; ++j, ++c) {
       if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
       tc_fence_after();
@@ -680,71 +684,98 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) f[g] = fmaxf(fabsf(f[g]) * rs, 0x1p-126f);  // (0 times -inf would be NaN)
       const int v_lo = my_lo - k0, v_hi = my_hi - k0;
-      uint32_t sr[64];
-      // 64 scores of the row from column 64 h on, -inf where the key is not seen
-      auto load_half = [&](int h) {
-        tmem_ld32(tS + h * 64, sr);
-        tmem_ld32(tS + h * 64 + 32, sr + 32);
+      // One pass with the max at hand.  Where a row outgrows it by more than 2^8,
+      // or meets its first key, the max is found first and the block computed
+      // again (its scores are still there: P is stored last).
+      auto load_scores = [&](int h, uint32_t* sr) {  // 32 scores of the row, -inf where the key is not seen
+        tmem_ld32(tS + h * 32, sr);
         tmem_ld_wait();
         if (masked) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (h * 64 + k < v_lo || h * 64 + k >= v_hi || (no_page >> (h * 4 + k / 16) & 1u))
+          for (int k = 0; k < 32; ++k)
+            if (h * 32 + k < v_lo || h * 32 + k >= v_hi || (no_page >> (h * 2 + k / 16) & 1u))
               sr[k] = __float_as_uint(-INFINITY);
         }
       };
-      // largest raw score of each 16 columns, then of the row in log2 units
-      float m_new = m_used;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        load_half(h);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int k = 0; k < 16; ++k) mx[k & 1] = fmaxf(mx[k & 1], __uint_as_float(sr[g * 16 + k]));
-          const float top = fmaxf(mx[0], mx[1]);
-          m_new = fmaxf(m_new, top * f[h * 4 + g]);
-        }
-      }
-      const bool resc = m_used != -INFINITY && m_new > m_used + kRescaleLog2;
-      const float shrink = resc ? ex2(m_used - m_new) : 1.f;
-      if (__any_sync(0xffffffffu, resc)) {
-        if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t r[32];
-          tmem_ld32(tO + ch * 32, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * shrink);
-          tmem_st16(tO + ch * 32, r);
-          tmem_st16(tO + ch * 32 + 16, r + 16);
-        }
-      }
-      l *= shrink;
-      if (resc || m_used == -INFINITY) m_used = m_new;
-      const float msub = m_used == -INFINITY ? 0.f : m_used;
-      const float2 nm2 = make_float2(-msub, -msub);
+      const bool first = m_used == -INFINITY;
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      bool again = __any_sync(0xffffffffu, first);
+      if (!again) {
+        uint32_t pw[KT / 2];
+        const float2 nm2 = make_float2(-m_used, -m_used);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        load_half(h);
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          uint32_t pw[16];
+        for (int h = 0; h < KT / 32; ++h) {
+          uint32_t sr[32];
+          load_scores(h, sr);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float fg = f[h * 4 + ch * 2 + e / 8];
-            float2 y = make_float2(__uint_as_float(sr[ch * 32 + 2 * e]), __uint_as_float(sr[ch * 32 + 2 * e + 1]));
-            y = __ffma2_rn(y, make_float2(fg, fg), nm2);
+            const float fg = f[h * 2 + e / 8];
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+                                        make_float2(fg, fg), nm2);
+            mx[e & 3] = fmaxf(mx[e & 3], fmaxf(y.x, y.y));
             const float2 pp = make_float2(ex2(y.x), ex2(y.y));
             sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
+            pw[h * 16 + e] = pack2<false>(pp.x, pp.y);
+          }
+        }
+        again = __any_sync(0xffffffffu, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRescaleLog2);
+        if (!again) {
+#pragma unroll
+          for (int h = 0; h < KT / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
+        }
+      }
+      if (again) {
+        float m_new = m_used;
+#pragma unroll 1
+        for (int h = 0; h < KT / 32; ++h) {
+          uint32_t sr[32];
+          load_scores(h, sr);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(sr[g * 16 + k]));
+            const float fg = h == 0 ? f[g] : h == 1 ? f[2 + g] : h == 2 ? f[4 + g] : f[6 + g];
+            m_new = fmaxf(m_new, top * fg);
+          }
+        }
+        const bool grew = first || m_new > m_used + kRescaleLog2;
+        if (__any_sync(0xffffffffu, grew && !first)) {
+          // the tile's previous P V (of this unit: some max is finite) has completed before its O rows are scaled
+          if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
+          tc_fence_after();
+          const float shrink = grew && !first ? ex2(m_used - m_new) : 1.f;
+          l *= shrink;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t r[32];
+            tmem_ld32(tO + ch * 32, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * shrink);
+            tmem_st16(tO + ch * 32, r);
+            tmem_st16(tO + ch * 32 + 16, r + 16);
+          }
+        }
+        if (grew) m_used = m_new;
+        const float msub = m_used == -INFINITY ? 0.f : m_used;
+        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int h = 0; h < KT / 32; ++h) {
+          uint32_t sr[32], pw[16];
+          load_scores(h, sr);
+          const float fa = h == 0 ? f[0] : h == 1 ? f[2] : h == 2 ? f[4] : f[6];
+          const float fb = h == 0 ? f[1] : h == 1 ? f[3] : h == 2 ? f[5] : f[7];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float fg = e < 8 ? fa : fb;
+            const float2 pp = make_float2(ex2(__uint_as_float(sr[2 * e]) * fg - msub),
+                                          ex2(__uint_as_float(sr[2 * e + 1]) * fg - msub));
+            sum2[0] = __fadd2_rn(sum2[0], pp);
             pw[e] = pack2<false>(pp.x, pp.y);
           }
-          // P pairs into the columns of scores that have been read for good
-          tmem_st16(tS + h * 32 + ch * 16, pw);
+          tmem_st16(tS + h * 16, pw);  // over scores that have been read for good
         }
       }
       l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
