@@ -5,8 +5,8 @@
 // two 128-row tiles of one KV head, key blocks of 128,
 //   S_w = Q_w K_j^T in tensor memory, P_w = 2^(S_w f - m) back into it as the
 //   fp16 A operand of O_w += P_w V_j,
-// two softmax warpgroups in turn, one row a thread, O rescaled only when a row
-// max grows by more than 2^8.  Rows are packed (query, head), so a group's heads
+// two softmax warpgroups in turn, one row a thread, O rescaled only when P
+// outgrows fp16.  Rows are packed (query, head), so a group's heads
 // share each key block and short chunks fill the tiles.
 //
 // Bound by the tensor cores and the exponentials, with the bytes of K and V a
@@ -47,7 +47,7 @@ constexpr int kWarps = 16, THREADS = kWarps * 32;
 // warpgroups hold a row of 64 P pairs and 32 scores a thread
 constexpr uint32_t REG_SOFT = 168, REG_CTL = 88, REG_CONV = 88;
 static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kMostSum = 32768.f;  // of a block's P before a row's max is taken anew
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
 constexpr int kScaleRing = 8;     // blocks of scales; deeper than the conversion can run ahead of the softmax
 
@@ -684,9 +684,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) f[g] = fmaxf(fabsf(f[g]) * rs, 0x1p-126f);  // (0 times -inf would be NaN)
       const int v_lo = my_lo - k0, v_hi = my_hi - k0;
-      // One pass with the max at hand.  Where a row outgrows it by more than 2^8,
-      // or meets its first key, the max is found first and the block computed
-      // again (its scores are still there: P is stored last).
+      // One pass with the max at hand, no max taken: while the block's sum of P
+      // stays at or below 2^15, no P is above it, which fp16 and the f32 sums
+      // hold as well as P up to 1.  Past that (or at a row's first key), the max
+      // is found and the block computed again (its scores are still there: P is
+      // stored last).
       auto load_scores = [&](int h, uint32_t* sr) {  // 32 scores of the row, -inf where the key is not seen
         tmem_ld32(tS + h * 32, sr);
         tmem_ld_wait();
@@ -703,7 +705,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       if (!again) {
         uint32_t pw[KT / 2];
         const float2 nm2 = make_float2(-m_used, -m_used);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int h = 0; h < KT / 32; ++h) {
           uint32_t sr[32];
@@ -713,13 +714,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             const float fg = f[h * 2 + e / 8];
             const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
                                         make_float2(fg, fg), nm2);
-            mx[e & 3] = fmaxf(mx[e & 3], fmaxf(y.x, y.y));
             const float2 pp = make_float2(ex2(y.x), ex2(y.y));
             sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
             pw[h * 16 + e] = pack2<false>(pp.x, pp.y);
           }
         }
-        again = __any_sync(0xffffffffu, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) > kRescaleLog2);
+        const float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+        again = __any_sync(0xffffffffu, !(sum <= kMostSum));
         if (!again) {
 #pragma unroll
           for (int h = 0; h < KT / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             m_new = fmaxf(m_new, top * fg);
           }
         }
-        const bool grew = first || m_new > m_used + kRescaleLog2;
+        const bool grew = first || m_new > m_used;
         if (__any_sync(0xffffffffu, grew && !first)) {
           // the tile's previous P V (of this unit: some max is finite) has completed before its O rows are scaled
           if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
