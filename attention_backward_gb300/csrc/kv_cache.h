@@ -73,8 +73,8 @@ struct KvAttnParams {
 };
 
 // Tensor maps of the cache's bytes, dims (D, HKV, page_size, num_blocks): box D
-// bytes x tokens of one head (16 in the decode kernel, a page in the prompt
-// kernel), swizzled over rows of D bytes.
+// bytes x tokens of one head (16 in the decode kernel, a page but at most a
+// block in the prompt kernel), swizzled over rows of D bytes.
 struct KvMaps {
   CUtensorMap k, v;
 };
@@ -94,9 +94,9 @@ constexpr int kKvDecMaxWorkers = kKvDecMaxRows / 16;
 // Prompt kernel: rows of a unit, keys per block, what starting a unit costs in
 // blocks, fewest line positions of a CTA's part, most CTAs.
 constexpr int kKvPrRows = 256;
-constexpr int kKvPrKeys = 128;
-constexpr int kKvPrCost = 3;
-constexpr int kKvPrMinWork = 5;
+constexpr int kKvPrKeys = 64;
+constexpr int kKvPrCost = 6;
+constexpr int kKvPrMinWork = 10;
 constexpr int kKvPrMaxCtas = 160;
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);

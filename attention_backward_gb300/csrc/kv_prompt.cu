@@ -2,11 +2,13 @@
 // per KV head: prompts and chunks of prompts against what is cached of them.
 //
 // The mathematics of kv_decode.cu, on tcgen05 as in the dense forward: units of
-// two 128-row tiles of one KV head, key blocks of 128,
+// two 128-row tiles of one KV head, key blocks of 64,
 //   S_w = Q_w K_j^T in tensor memory, P_w = 2^(S_w f - m) back into it as the
 //   fp16 A operand of O_w += P_w V_j,
-// two softmax warpgroups in turn, one row a thread, O rescaled only when P
-// outgrows fp16.  Rows are packed (query, head), so a group's heads
+// two softmax warpgroups, one row a thread, O rescaled only when P outgrows
+// fp16.  Each tile has two score buffers of 64 columns: S of block j + 2 follows
+// P V of block j in the one, while the softmax works on block j + 1 in the other,
+// so that it does not wait for the products' latency.  Rows are packed (query, head), so a group's heads
 // share each key block and short chunks fill the tiles.
 //
 // Bound by the tensor cores and the exponentials, with the bytes of K and V a
@@ -44,31 +46,34 @@ namespace {
 constexpr int BQ = 128, RT = kKvPrRows, KT = kKvPrKeys, COST = kKvPrCost;
 constexpr int kWarps = 16, THREADS = kWarps * 32;
 // launched at 128 registers a thread, re-split per warpgroup: the softmax
-// warpgroups hold a row of 64 P pairs and 32 scores a thread
+// warpgroups hold 64 scores and 32 P pairs a thread
 constexpr uint32_t REG_SOFT = 168, REG_CTL = 88, REG_CONV = 88;
 static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
 constexpr float kMostSum = 32768.f;  // of a block's P before a row's max is taken anew
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
-constexpr int kScaleRing = 8;     // blocks of scales; deeper than the conversion can run ahead of the softmax
+static_assert(kGroups == 4, "a block's scales are one 16-byte load");
+constexpr int kScaleRing = 16;    // blocks of scales; the copies run at most 8 ahead of the softmax
 
 template <int D>
 struct PrCfg {
   static constexpr int NSLAB = D / 64;
-  static constexpr int SLAB = 128 * 128;         // [128 rows x 64 columns] fp16, 128-byte swizzled
-  static constexpr int TILE = NSLAB * SLAB;      // a 128-row tile of Q, K or V
-  static constexpr int RAW = KT * D;             // 128 keys as bytes
-  static constexpr int NT = D == 64 ? 6 : 3;     // ring of converted tiles, K and V in turn
-  static constexpr int NR = D == 64 ? 8 : 4;     // ring of raw tiles, K and V in turn
+  static constexpr int QSLAB = 128 * 128;        // [128 rows x 64 columns] fp16, 128-byte swizzled
+  static constexpr int QTILE = NSLAB * QSLAB;    // a tile of Q
+  static constexpr int SLAB = KT * 128;          // [64 keys x 64 columns]
+  static constexpr int TILE = NSLAB * SLAB;      // a block's K or V
+  static constexpr int RAW = KT * D;             // the same as bytes
+  static constexpr int NT = 6;                   // ring of converted tiles, K and V in turn
+  static constexpr int NR = 8;                   // ring of raw tiles, K and V in turn
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_T = OFF_Q + 2 * TILE;
+  static constexpr int OFF_T = OFF_Q + 2 * QTILE;
   static constexpr int OFF_RAW = OFF_T + NT * TILE;
   static constexpr int OFF_UNIT = OFF_RAW + NR * RAW;   // 2 unit descriptors of 64 bytes
-  static constexpr int OFF_SC = OFF_UNIT + 2 * 64;      // K scales [kScaleRing][8], V ratios [kScaleRing][8]
-  static constexpr int OFF_BAR = OFF_SC + kScaleRing * 64;
-  static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
+  static constexpr int OFF_SC = OFF_UNIT + 2 * 64;      // K scales, then V ratios, [kScaleRing][kGroups] each
+  static constexpr int OFF_BAR = OFF_SC + 2 * kScaleRing * kGroups * 4;
+  static constexpr int OFF_MISC = OFF_BAR + 56 * 8;
   static constexpr int SMEM = OFF_MISC + 32;
   static_assert(SMEM + 256 <= 227 * 1024, "shared memory budget");
-  static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + D;
+  static constexpr uint32_t T_S = 0, T_O = 256;  // tile w: scores at 128 w + 64 buffer, O at 256 + D w
 };
 
 enum PrBar : int {
@@ -77,16 +82,16 @@ enum PrBar : int {
   RAW_EMPTY0 = RAW_FULL0 + 8,  // NR: 2 conversion warps read it
   T_FULL0 = RAW_EMPTY0 + 8,    // NT: 2 conversion warps wrote it
   T_EMPTY0 = T_FULL0 + 6,      // NT: its products have completed
-  S_FULL0 = T_EMPTY0 + 6,      // per tile
-  P_READY0 = S_FULL0 + 2,      // per tile: 4 softmax warps stored P
-  O_DONE0 = P_READY0 + 2,      // per tile: the P V products issued so far completed
-  O_FREE0 = O_DONE0 + 2,       // per tile: 4 softmax warps read the unit's O rows
+  S_FULL0 = T_EMPTY0 + 6,      // per tile and buffer
+  P_READY0 = S_FULL0 + 4,      // per tile and buffer: 4 softmax warps stored P
+  O_DONE0 = P_READY0 + 4,      // per tile and buffer: its P V, and all before it, completed
+  O_FREE0 = O_DONE0 + 4,       // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,    // 2 slots
   UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the 14 other working warps read it
   DRAIN = UNIT_EMPTY0 + 2,
   NUM_BARS
 };
-static_assert(NUM_BARS <= 48, "barrier storage");
+static_assert(NUM_BARS <= 56, "barrier storage");
 
 // A unit, or the CTA's part of one: key blocks [j0, j1).
 struct PrUnit {
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);
   PrUnit* const units = reinterpret_cast<PrUnit*>(sm + C::OFF_UNIT);
-  float* const k_scales = reinterpret_cast<float*>(sm + C::OFF_SC);               // [kScaleRing][8]; -1: no page
+  float* const k_scales = reinterpret_cast<float*>(sm + C::OFF_SC);               // [kScaleRing][kGroups]; -1: no page
   float* const v_ratios = k_scales + kScaleRing * kGroups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -239,9 +244,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars[Q_FULL0 + w], 4);
-      mbar_init(&bars[S_FULL0 + w], 1);
-      mbar_init(&bars[P_READY0 + w], 4);
-      mbar_init(&bars[O_DONE0 + w], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars[S_FULL0 + 2 * w + b], 1);
+        mbar_init(&bars[P_READY0 + 2 * w + b], 4);
+        mbar_init(&bars[O_DONE0 + 2 * w + b], 1);
+      }
       mbar_init(&bars[O_FREE0 + w], 4);
       mbar_init(&bars[UNIT_FULL0 + w], 1);
       mbar_init(&bars[UNIT_EMPTY0 + w], 14);
@@ -318,8 +325,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           for (int g = 0; g < kGroups; ++g) edge |= ksc[g] < 0.f;
         }
 #pragma unroll 2
-        for (int it = 0; it < 8; ++it) {  // 8 rows
-          const int row = cw * 64 + it * 8 + row8;
+        for (int it = 0; it < KT / 16; ++it) {  // 8 rows
+          const int row = cw * (KT / 2) + it * 8 + row8;
           uint4 x[C::NSLAB];
 #pragma unroll
           for (int s = 0; s < C::NSLAB; ++s)
@@ -445,10 +452,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       }
     } else if (warp == 8) {
       // ============================================================ copies
-      // Lane i looks up 16-key group i of four blocks (page ids and scales four
-      // blocks ahead); the first lane of a page that has seen keys copies it.
-      const int gp = 1 << (p.page_log2 - 4);  // groups a page
-      const uint32_t page_lanes = ((1u << gp) - 1u) << (lane & ~(gp - 1));
+      // Lane i looks up 16-key group i of eight blocks (page ids and scales eight
+      // blocks ahead); the first lane of a box (a page, at most a block) that has
+      // seen keys copies it.
+      const int box_log2 = imin(p.page_log2, 6), gp = 1 << (box_log2 - 4);  // groups a box
+      const uint32_t box_lanes = ((1u << gp) - 1u) << (lane & ~(gp - 1));
+      const int s_mask = (1 << p.page_log2) - 1;
       uint32_t ic = 0;  // raw tiles so far
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
@@ -470,19 +479,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         };
         scales_of();
         for (int j = u.j0; j < u.j1 && ok; ++j) {
-          const int q4 = (j - u.j0) & 3;
-          if (q4 == 0) {
+          const int q8 = (j - u.j0) & 7;
+          if (q8 == 0) {
             blk = held(nblk) ? nblk : -1;
             ksc = blk >= 0 ? nks : -1.f, vra = blk >= 0 ? nvs * vinv : 0.f;
-            nblk = look_up((j + 4) * KT + lane * 16);
-          } else if (q4 == 2) {
+            nblk = look_up((j + 8) * KT + lane * 16);
+          } else if (q8 == 4) {
             scales_of();
           }
-          const bool mine = (lane >> 3) == q4;
+          const bool mine = lane / kGroups == q8;
           const uint32_t seen = __ballot_sync(0xffffffffu, mine && blk >= 0);
-          const bool leads = mine && blk >= 0 && (seen & page_lanes & ((1u << lane) - 1u)) == 0;
-          const int pages = __popc(__ballot_sync(0xffffffffu, leads));
-          const int row0 = ((lane & 7) & ~(gp - 1)) * 16;  // of my page in the block
+          const bool leads = mine && blk >= 0 && (seen & box_lanes & ((1u << lane) - 1u)) == 0;
+          const int boxes = __popc(__ballot_sync(0xffffffffu, leads));
+          const int row0 = ((lane % kGroups) & ~(gp - 1)) * 16;  // of my box in the block
           for (int kv = 0; kv < 2; ++kv, ++ic) {
             const int rs = ic % C::NR;
             const uint32_t n = ic / C::NR;
@@ -490,18 +499,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             if (kv == 0 && mine) {
               // the block's scales (the ring is deep enough that its last readers are done)
               const uint32_t sr = (ic >> 1) % kScaleRing;
-              k_scales[sr * kGroups + (lane & 7)] = ksc;
-              v_ratios[sr * kGroups + (lane & 7)] = vra;
+              k_scales[sr * kGroups + lane % kGroups] = ksc;
+              v_ratios[sr * kGroups + lane % kGroups] = vra;
             }
             __syncwarp();
             if (lane == 0) {
-              if (pages) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], (pages * D) << p.page_log2);
+              if (boxes) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], (boxes * D) << box_log2);
               else mbar_arrive(&bars[RAW_FULL0 + rs]);
             }
             __syncwarp();
             if (leads)
               tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + row0 * D, kv ? &maps.v : &maps.k, &bars[RAW_FULL0 + rs], 0,
-                          u.head, 0, blk);
+                          u.head, (j * KT + row0) & s_mask, blk);
           }
         }
       }
@@ -518,77 +527,74 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       const uint64_t q_kmaj = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       const uint64_t t_kmaj = sdesc_sw128(sbase + C::OFF_T, 16, 1024);
       const uint64_t t_mn = sdesc_sw128(sbase + C::OFF_T, C::SLAB, 1024);
-      uint32_t bc = 0, qc0 = 0, qc1 = 0, npv0 = 0, npv1 = 0, oc0 = 0, oc1 = 0;  // bc: blocks so far
+      // blocks of the CTA so far; per tile units, S and P V products so far
+      uint32_t bc = 0, qc0 = 0, qc1 = 0, ns0 = 0, ns1 = 0, npv0 = 0, npv1 = 0;
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
         const PrUnit u = next_unit(uc, &ok);
         if (!ok || !u.valid) break;
         if (u.valid == 2 || u.j1 <= u.j0) continue;
         const PrTile t0 = tile_of(u, 0, p), t1 = tile_of(u, 1, p);
-        const uint32_t bc0 = bc;
+        const uint32_t ib = 2 * bc;  // ring index of the unit's first K tile
         auto in = [&](int w, int j) { return w ? t1.lo <= j && j < t1.hi : t0.lo <= j && j < t0.hi; };
-        auto wait_tile = [&](int j, int kv) {  // converted tile of K (0) or V (1) of block j
-          const uint32_t i = 2 * (bc0 + j - u.j0) + kv;
+        auto wait_tile = [&](uint32_t i) {
           return mbar_wait_warp(&bars[T_FULL0 + i % C::NT], (i / C::NT) & 1, wc, kErrWaitKV);
         };
-        auto tile_at = [&](int j, int kv) { return (2 * (bc0 + j - u.j0) + kv) % C::NT; };
-        auto issue_s = [&](int w, int j) {
-          const uint64_t ko0 = sdesc_step(tile_at(j, 0) * C::TILE), qo = sdesc_step(w * C::TILE);
+        auto issue_s = [&](int w, uint32_t i) {
+          uint32_t& ns = w ? ns1 : ns0;
+          const uint32_t b = ns++ & 1;
+          const uint64_t ko0 = sdesc_step((i % C::NT) * C::TILE), qo0 = sdesc_step(w * C::QTILE);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t ko = sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32);
-            mma_ss_w(tmem + (w ? C::T_S1 : C::T_S0), q_kmaj + qo + ko, t_kmaj + ko0 + ko, IDESC_S, kk > 0);
-          }
-          mma_commit_w(&bars[S_FULL0 + w]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss_w(tmem + C::T_S + w * 128 + b * 64, q_kmaj + qo0 + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
+                     t_kmaj + ko0 + sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32), IDESC_S, kk > 0);
+          mma_commit_w(&bars[S_FULL0 + 2 * w + b]);
         };
-        auto issue_pv = [&](int w, int j) -> bool {
+        auto issue_pv = [&](int w, int j, uint32_t i) -> bool {
           uint32_t& npv = w ? npv1 : npv0;
-          if (!mbar_wait_warp(&bars[P_READY0 + w], npv & 1, wc, kErrWaitP)) return false;
+          const uint32_t b = npv & 1;
+          if (!mbar_wait_warp(&bars[P_READY0 + 2 * w + b], (npv >> 1) & 1, wc, kErrWaitP)) return false;
+          ++npv;
           const int lo = w ? t1.lo : t0.lo;
-          if (j == lo) {
-            const uint32_t oc = w ? oc1 : oc0;
+          if (j == lo) {  // the tile's O: its softmax warps have read the previous unit's
+            const uint32_t oc = (w ? qc1 : qc0) - 1;
             if (oc >= 1 && !mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wc, kErrWaitDQEmpty)) return false;
           }
           tc_fence_after();
-          const uint64_t vo = sdesc_step(tile_at(j, 1) * C::TILE);
-          const uint32_t ts = tmem + (w ? C::T_S1 : C::T_S0), to = tmem + (w ? C::T_O1 : C::T_O0);
+          const uint64_t vo = sdesc_step((i % C::NT) * C::TILE);
+          const uint32_t ts = tmem + C::T_S + w * 128 + b * 64, to = tmem + C::T_O + w * D;
 #pragma unroll
           for (int kk = 0; kk < KT / 16; ++kk)
             mma_ts_w(to, ts + kk * 8, t_mn + vo + sdesc_step(kk * 2048), IDESC_PV, j > lo || kk > 0);
-          mma_commit_w(&bars[O_DONE0 + w]);
-          ++npv;
+          mma_commit_w(&bars[O_DONE0 + 2 * w + b]);
           return true;
         };
         // the unit's Q tiles
         if (t0.lo < t0.hi) ok = mbar_wait_warp(&bars[Q_FULL0], qc0++ & 1, wc, kErrWaitStageFull);
         if (ok && t1.lo < t1.hi) ok = mbar_wait_warp(&bars[Q_FULL0 + 1], qc1++ & 1, wc, kErrWaitStageFull);
-        ok = ok && wait_tile(u.j0, 0);
-        if (!ok) break;
-        tc_fence_after();
-        if (in(0, u.j0)) issue_s(0, u.j0);
-        if (in(1, u.j0)) issue_s(1, u.j0);
-        mma_commit_w(&bars[T_EMPTY0 + tile_at(u.j0, 0)]);
-        for (int j = u.j0; j < u.j1; ++j) {
-          if (!(ok = wait_tile(j, 1))) break;
-          tc_fence_after();
-          if (in(0, j) && !(ok = issue_pv(0, j))) break;
-          const bool next = j + 1 < u.j1;
-          if (next) {
-            if (!(ok = wait_tile(j + 1, 0))) break;
+        // S of block j + 2 goes behind P V of block j, in the same buffer
+        for (int j = u.j0 - 2; j < u.j1 && ok; ++j) {
+          const uint32_t iv = ib + 2 * (j - u.j0) + 1, ik = ib + 2 * (j + 2 - u.j0);
+          const bool pv = j >= u.j0, s = j + 2 < u.j1;
+          if (pv && !(ok = wait_tile(iv))) break;
+          if (pv) tc_fence_after();
+          if (pv && in(0, j) && !(ok = issue_pv(0, j, iv))) break;
+          if (s) {
+            if (!(ok = wait_tile(ik))) break;
             tc_fence_after();
-            if (in(0, j + 1)) issue_s(0, j + 1);
+            if (in(0, j + 2)) issue_s(0, ik);
           }
-          if (in(1, j) && !(ok = issue_pv(1, j))) break;
-          mma_commit_w(&bars[T_EMPTY0 + tile_at(j, 1)]);
-          if (next) {
-            if (in(1, j + 1)) issue_s(1, j + 1);
-            mma_commit_w(&bars[T_EMPTY0 + tile_at(j + 1, 0)]);
+          if (pv) {
+            if (in(1, j) && !(ok = issue_pv(1, j, iv))) break;
+            mma_commit_w(&bars[T_EMPTY0 + iv % C::NT]);
+          }
+          if (s) {
+            if (in(1, j + 2)) issue_s(1, ik);
+            mma_commit_w(&bars[T_EMPTY0 + ik % C::NT]);
           }
         }
         if (!ok) break;
         bc += u.j1 - u.j0;
-        oc0 += t0.lo < t0.hi ? 1u : 0u;
-        oc1 += t1.lo < t1.hi ? 1u : 0u;
       }
       // every MMA issued by this warp completes before TMEM is released
       mma_commit_w(&bars[DRAIN]);
@@ -605,8 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   const int w = warp >> 2, quad = warp & 3;
   const int trow = quad * 32 + lane;
   const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-  const uint32_t tS = tmem + lane_off + (w ? C::T_S1 : C::T_S0);
-  const uint32_t tO = tmem + lane_off + (w ? C::T_O1 : C::T_O0);
+  const uint32_t tO = tmem + lane_off + C::T_O + w * D;
   uint32_t c = 0, bc = 0;  // blocks of this tile, and of the CTA, over all units so far
   bool ok = true;
   for (uint32_t uc = 0; ok; ++uc) {
@@ -648,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       float back;
       const float up = to_top(amax, &back);
       rs = back * p.scale_log2;
-      uint8_t* const qt = sm + C::OFF_Q + w * C::TILE;
+      uint8_t* const qt = sm + C::OFF_Q + w * C::QTILE;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           const float2 f = unpack2<BF16>(xs[e]);
           y[e] = pack2<false>(f.x * up, f.y * up);
         }
-        *reinterpret_cast<uint4*>(qt + (i / 8) * C::SLAB + sw128_offset(trow, i % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(qt + (i / 8) * C::QSLAB + sw128_offset(trow, i % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -667,11 +672,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
     // (rows past the request's last one go along with a max of their own)
     float m_used = live ? -INFINITY : 0.f, l = 0.f;
     for (int j = tl.lo; j < tl.hi; ++j, ++c) {
-      if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
+      const uint32_t tS = tmem + lane_off + C::T_S + w * 128 + (c & 1) * 64;
+      if (!(ok = mbar_wait_warp(&bars[S_FULL0 + 2 * w + (c & 1)], (c >> 1) & 1, wc, kErrWaitS))) break;
       tc_fence_after();
       const float* const sc = k_scales + ((bc0 + j - u.j0) % kScaleRing) * kGroups;
-      const float4 sa = *reinterpret_cast<const float4*>(sc), sb = *reinterpret_cast<const float4*>(sc + 4);
-      float f[kGroups] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+      const float4 sa = *reinterpret_cast<const float4*>(sc);
+      float f[kGroups] = {sa.x, sa.y, sa.z, sa.w};
       const int k0 = j * KT;
       bool masked = k0 < tl.all_lo || k0 + KT > tl.all_hi;
 #pragma unroll
@@ -701,10 +707,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       };
       const bool first = m_used == -INFINITY;
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      bool again = __any_sync(0xffffffffu, first);
-      if (!again) {
+      bool need = first;  // (row by row, so that no row's result depends on another's)
+      {
         uint32_t pw[KT / 2];
-        const float2 nm2 = make_float2(-m_used, -m_used);
+        const float msub = first ? 0.f : m_used;
+        const float2 nm2 = make_float2(-msub, -msub);
 #pragma unroll
         for (int h = 0; h < KT / 32; ++h) {
           uint32_t sr[32];
@@ -719,14 +726,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             pw[h * 16 + e] = pack2<false>(pp.x, pp.y);
           }
         }
-        const float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-        again = __any_sync(0xffffffffu, !(sum <= kMostSum));
-        if (!again) {
+        need |= !((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y) <= kMostSum);
+        if (!__any_sync(0xffffffffu, need)) {
 #pragma unroll
           for (int h = 0; h < KT / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
         }
       }
-      if (again) {
+      if (__any_sync(0xffffffffu, need)) {
         float m_new = m_used;
 #pragma unroll 1
         for (int h = 0; h < KT / 32; ++h) {
@@ -737,14 +743,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(sr[g * 16 + k]));
-            const float fg = h == 0 ? f[g] : h == 1 ? f[2 + g] : h == 2 ? f[4 + g] : f[6 + g];
+            const float fg = h == 0 ? f[g] : f[2 + g];
             m_new = fmaxf(m_new, top * fg);
           }
         }
-        const bool grew = first || m_new > m_used;
+        const bool grew = need && m_new > m_used;
         if (__any_sync(0xffffffffu, grew && !first)) {
           // the tile's previous P V (of this unit: some max is finite) has completed before its O rows are scaled
-          if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
+          if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + ((c - 1) & 1)], ((c - 1) >> 1) & 1, wc, kErrWaitDQFull))) break;
           tc_fence_after();
           const float shrink = grew && !first ? ex2(m_used - m_new) : 1.f;
           l *= shrink;
@@ -766,14 +772,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         for (int h = 0; h < KT / 32; ++h) {
           uint32_t sr[32], pw[16];
           load_scores(h, sr);
-          const float fa = h == 0 ? f[0] : h == 1 ? f[2] : h == 2 ? f[4] : f[6];
-          const float fb = h == 0 ? f[1] : h == 1 ? f[3] : h == 2 ? f[5] : f[7];
+          const float fa = h == 0 ? f[0] : f[2], fb = h == 0 ? f[1] : f[3];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float fg = e < 8 ? fa : fb;
-            const float2 pp = make_float2(ex2(__uint_as_float(sr[2 * e]) * fg - msub),
-                                          ex2(__uint_as_float(sr[2 * e + 1]) * fg - msub));
-            sum2[0] = __fadd2_rn(sum2[0], pp);
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+                                        make_float2(fg, fg), make_float2(-msub, -msub));
+            const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+            sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
             pw[e] = pack2<false>(pp.x, pp.y);
           }
           tmem_st16(tS + h * 16, pw);  // over scores that have been read for good
@@ -783,12 +789,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[P_READY0 + w]);
+      if (lane == 0) mbar_arrive(&bars[P_READY0 + 2 * w + (c & 1)]);
     }
     if (!ok) break;
     // ---- the row's O and LSE, or its part
     if (any) {
-      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
+      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + ((c - 1) & 1)], ((c - 1) >> 1) & 1, wc, kErrWaitDQFull))) break;
       tc_fence_after();
     }
     const bool whole = u.slot < 0;
