@@ -94,9 +94,9 @@ constexpr int kKvDecMaxWorkers = kKvDecMaxRows / 16;
 // Prompt kernel: rows of a unit, keys per block, what starting a unit costs in
 // blocks, fewest line positions of a CTA's part, most CTAs.
 constexpr int kKvPrRows = 256;
-constexpr int kKvPrKeys = 64;
-constexpr int kKvPrCost = 6;
-constexpr int kKvPrMinWork = 10;
+constexpr int kKvPrKeys = 128;
+constexpr int kKvPrCost = 3;
+constexpr int kKvPrMinWork = 5;
 constexpr int kKvPrMaxCtas = 160;
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);

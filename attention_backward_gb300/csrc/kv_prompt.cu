@@ -2,13 +2,12 @@
 // per KV head: prompts and chunks of prompts against what is cached of them.
 //
 // The mathematics of kv_decode.cu, on tcgen05 as in the dense forward: units of
-// two 128-row tiles of one KV head, key blocks of 64,
+// two 128-row tiles of one KV head, key blocks of 128,
 //   S_w = Q_w K_j^T in tensor memory, P_w = 2^(S_w f - m) back into it as the
 //   fp16 A operand of O_w += P_w V_j,
 // two softmax warpgroups, one row a thread, O rescaled only when P outgrows
-// fp16.  Each tile has two score buffers of 64 columns: S of block j + 2 follows
-// P V of block j in the one, while the softmax works on block j + 1 in the other,
-// so that it does not wait for the products' latency.  Rows are packed (query, head), so a group's heads
+// fp16.  P goes to the products in halves of 64 keys, so that P V of the first
+// runs while the softmax works on the second.  Rows are packed (query, head), so a group's heads
 // share each key block and short chunks fill the tiles.
 //
 // Bound by the tensor cores and the exponentials, with the bytes of K and V a
@@ -51,7 +50,8 @@ constexpr uint32_t REG_SOFT = 168, REG_CTL = 88, REG_CONV = 88;
 static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
 constexpr float kMostSum = 32768.f;  // of a block's P before a row's max is taken anew
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
-static_assert(kGroups == 4, "a block's scales are one 16-byte load");
+constexpr int HK = 64;            // keys of a half block
+static_assert(KT == 2 * HK && kGroups == 8, "a half block's scales are one 16-byte load");
 constexpr int kScaleRing = 16;    // blocks of scales; the copies run at most 8 ahead of the softmax
 
 template <int D>
@@ -59,11 +59,11 @@ struct PrCfg {
   static constexpr int NSLAB = D / 64;
   static constexpr int QSLAB = 128 * 128;        // [128 rows x 64 columns] fp16, 128-byte swizzled
   static constexpr int QTILE = NSLAB * QSLAB;    // a tile of Q
-  static constexpr int SLAB = KT * 128;          // [64 keys x 64 columns]
+  static constexpr int SLAB = KT * 128;          // [128 keys x 64 columns]
   static constexpr int TILE = NSLAB * SLAB;      // a block's K or V
   static constexpr int RAW = KT * D;             // the same as bytes
-  static constexpr int NT = 6;                   // ring of converted tiles, K and V in turn
-  static constexpr int NR = 8;                   // ring of raw tiles, K and V in turn
+  static constexpr int NT = D == 64 ? 6 : 3;     // ring of converted tiles, K and V in turn
+  static constexpr int NR = D == 64 ? 8 : 4;     // ring of raw tiles, K and V in turn
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_T = OFF_Q + 2 * QTILE;
   static constexpr int OFF_RAW = OFF_T + NT * TILE;
@@ -73,7 +73,7 @@ struct PrCfg {
   static constexpr int OFF_MISC = OFF_BAR + 56 * 8;
   static constexpr int SMEM = OFF_MISC + 32;
   static_assert(SMEM + 256 <= 227 * 1024, "shared memory budget");
-  static constexpr uint32_t T_S = 0, T_O = 256;  // tile w: scores at 128 w + 64 buffer, O at 256 + D w
+  static constexpr uint32_t T_S = 0, T_O = 256;  // tile w: scores at 128 w, O at 256 + D w
 };
 
 enum PrBar : int {
@@ -82,9 +82,9 @@ enum PrBar : int {
   RAW_EMPTY0 = RAW_FULL0 + 8,  // NR: 2 conversion warps read it
   T_FULL0 = RAW_EMPTY0 + 8,    // NT: 2 conversion warps wrote it
   T_EMPTY0 = T_FULL0 + 6,      // NT: its products have completed
-  S_FULL0 = T_EMPTY0 + 6,      // per tile and buffer
-  P_READY0 = S_FULL0 + 4,      // per tile and buffer: 4 softmax warps stored P
-  O_DONE0 = P_READY0 + 4,      // per tile and buffer: its P V, and all before it, completed
+  S_FULL0 = T_EMPTY0 + 6,      // per tile
+  P_READY0 = S_FULL0 + 2,      // per tile and half: 4 softmax warps stored P
+  O_DONE0 = P_READY0 + 4,      // per tile and half: its P V, and all before it, completed
   O_FREE0 = O_DONE0 + 4,       // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,    // 2 slots
   UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 slots: the 14 other working warps read it
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars[Q_FULL0 + w], 4);
+      mbar_init(&bars[S_FULL0 + w], 1);
       for (int b = 0; b < 2; ++b) {
-        mbar_init(&bars[S_FULL0 + 2 * w + b], 1);
         mbar_init(&bars[P_READY0 + 2 * w + b], 4);
         mbar_init(&bars[O_DONE0 + 2 * w + b], 1);
       }
@@ -452,12 +452,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       }
     } else if (warp == 8) {
       // ============================================================ copies
-      // Lane i looks up 16-key group i of eight blocks (page ids and scales eight
-      // blocks ahead); the first lane of a box (a page, at most a block) that has
-      // seen keys copies it.
-      const int box_log2 = imin(p.page_log2, 6), gp = 1 << (box_log2 - 4);  // groups a box
-      const uint32_t box_lanes = ((1u << gp) - 1u) << (lane & ~(gp - 1));
-      const int s_mask = (1 << p.page_log2) - 1;
+      // Lane i looks up 16-key group i of four blocks (page ids and scales four
+      // blocks ahead); the first lane of a page that has seen keys copies it.
+      const int gp = 1 << (p.page_log2 - 4);  // groups a page
+      const uint32_t page_lanes = ((1u << gp) - 1u) << (lane & ~(gp - 1));
       uint32_t ic = 0;  // raw tiles so far
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
@@ -479,19 +477,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         };
         scales_of();
         for (int j = u.j0; j < u.j1 && ok; ++j) {
-          const int q8 = (j - u.j0) & 7;
-          if (q8 == 0) {
+          const int q4 = (j - u.j0) & 3;
+          if (q4 == 0) {
             blk = held(nblk) ? nblk : -1;
             ksc = blk >= 0 ? nks : -1.f, vra = blk >= 0 ? nvs * vinv : 0.f;
-            nblk = look_up((j + 8) * KT + lane * 16);
-          } else if (q8 == 4) {
+            nblk = look_up((j + 4) * KT + lane * 16);
+          } else if (q4 == 2) {
             scales_of();
           }
-          const bool mine = lane / kGroups == q8;
+          const bool mine = lane / kGroups == q4;
           const uint32_t seen = __ballot_sync(0xffffffffu, mine && blk >= 0);
-          const bool leads = mine && blk >= 0 && (seen & box_lanes & ((1u << lane) - 1u)) == 0;
-          const int boxes = __popc(__ballot_sync(0xffffffffu, leads));
-          const int row0 = ((lane % kGroups) & ~(gp - 1)) * 16;  // of my box in the block
+          const bool leads = mine && blk >= 0 && (seen & page_lanes & ((1u << lane) - 1u)) == 0;
+          const int pages = __popc(__ballot_sync(0xffffffffu, leads));
+          const int row0 = ((lane % kGroups) & ~(gp - 1)) * 16;  // of my page in the block
           for (int kv = 0; kv < 2; ++kv, ++ic) {
             const int rs = ic % C::NR;
             const uint32_t n = ic / C::NR;
@@ -504,13 +502,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             }
             __syncwarp();
             if (lane == 0) {
-              if (boxes) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], (boxes * D) << box_log2);
+              if (pages) mbar_arrive_expect_tx(&bars[RAW_FULL0 + rs], (pages * D) << p.page_log2);
               else mbar_arrive(&bars[RAW_FULL0 + rs]);
             }
             __syncwarp();
             if (leads)
               tma_load_4d(sm + C::OFF_RAW + rs * C::RAW + row0 * D, kv ? &maps.v : &maps.k, &bars[RAW_FULL0 + rs], 0,
-                          u.head, (j * KT + row0) & s_mask, blk);
+                          u.head, 0, blk);
           }
         }
       }
@@ -527,8 +525,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       const uint64_t q_kmaj = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       const uint64_t t_kmaj = sdesc_sw128(sbase + C::OFF_T, 16, 1024);
       const uint64_t t_mn = sdesc_sw128(sbase + C::OFF_T, C::SLAB, 1024);
-      // blocks of the CTA so far; per tile units, S and P V products so far
-      uint32_t bc = 0, qc0 = 0, qc1 = 0, ns0 = 0, ns1 = 0, npv0 = 0, npv1 = 0;
+      // blocks of the CTA so far; per tile units and blocks so far
+      uint32_t bc = 0, qc0 = 0, qc1 = 0, nb0 = 0, nb1 = 0;
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
         const PrUnit u = next_unit(uc, &ok);
@@ -541,55 +539,56 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           return mbar_wait_warp(&bars[T_FULL0 + i % C::NT], (i / C::NT) & 1, wc, kErrWaitKV);
         };
         auto issue_s = [&](int w, uint32_t i) {
-          uint32_t& ns = w ? ns1 : ns0;
-          const uint32_t b = ns++ & 1;
           const uint64_t ko0 = sdesc_step((i % C::NT) * C::TILE), qo0 = sdesc_step(w * C::QTILE);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_w(tmem + C::T_S + w * 128 + b * 64, q_kmaj + qo0 + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
+            mma_ss_w(tmem + C::T_S + w * 128, q_kmaj + qo0 + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
                      t_kmaj + ko0 + sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32), IDESC_S, kk > 0);
-          mma_commit_w(&bars[S_FULL0 + 2 * w + b]);
+          mma_commit_w(&bars[S_FULL0 + w]);
         };
         auto issue_pv = [&](int w, int j, uint32_t i) -> bool {
-          uint32_t& npv = w ? npv1 : npv0;
-          const uint32_t b = npv & 1;
-          if (!mbar_wait_warp(&bars[P_READY0 + 2 * w + b], (npv >> 1) & 1, wc, kErrWaitP)) return false;
-          ++npv;
+          uint32_t& nb = w ? nb1 : nb0;
           const int lo = w ? t1.lo : t0.lo;
-          if (j == lo) {  // the tile's O: its softmax warps have read the previous unit's
-            const uint32_t oc = (w ? qc1 : qc0) - 1;
-            if (oc >= 1 && !mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wc, kErrWaitDQEmpty)) return false;
-          }
-          tc_fence_after();
           const uint64_t vo = sdesc_step((i % C::NT) * C::TILE);
-          const uint32_t ts = tmem + C::T_S + w * 128 + b * 64, to = tmem + C::T_O + w * D;
+          const uint32_t ts = tmem + C::T_S + w * 128, to = tmem + C::T_O + w * D;
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            mma_ts_w(to, ts + kk * 8, t_mn + vo + sdesc_step(kk * 2048), IDESC_PV, j > lo || kk > 0);
-          mma_commit_w(&bars[O_DONE0 + 2 * w + b]);
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_wait_warp(&bars[P_READY0 + 2 * w + h], nb & 1, wc, kErrWaitP)) return false;
+            if (h == 0 && j == lo) {  // the tile's O: its softmax warps have read the previous unit's
+              const uint32_t oc = (w ? qc1 : qc0) - 1;
+              if (oc >= 1 && !mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wc, kErrWaitDQEmpty)) return false;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < HK / 16; ++kk)
+              mma_ts_w(to, ts + h * 64 + kk * 8, t_mn + vo + sdesc_step((h * HK / 16 + kk) * 2048), IDESC_PV,
+                       j > lo || h > 0 || kk > 0);
+            mma_commit_w(&bars[O_DONE0 + 2 * w + h]);
+          }
+          ++nb;
           return true;
         };
         // the unit's Q tiles
         if (t0.lo < t0.hi) ok = mbar_wait_warp(&bars[Q_FULL0], qc0++ & 1, wc, kErrWaitStageFull);
         if (ok && t1.lo < t1.hi) ok = mbar_wait_warp(&bars[Q_FULL0 + 1], qc1++ & 1, wc, kErrWaitStageFull);
-        // S of block j + 2 goes behind P V of block j, in the same buffer
-        for (int j = u.j0 - 2; j < u.j1 && ok; ++j) {
-          const uint32_t iv = ib + 2 * (j - u.j0) + 1, ik = ib + 2 * (j + 2 - u.j0);
-          const bool pv = j >= u.j0, s = j + 2 < u.j1;
+        // S of block j + 1 goes behind P V of block j, over its P
+        for (int j = u.j0 - 1; j < u.j1 && ok; ++j) {
+          const uint32_t iv = ib + 2 * (j - u.j0) + 1, ik = iv + 1;
+          const bool pv = j >= u.j0, s = j + 1 < u.j1;
           if (pv && !(ok = wait_tile(iv))) break;
           if (pv) tc_fence_after();
           if (pv && in(0, j) && !(ok = issue_pv(0, j, iv))) break;
           if (s) {
             if (!(ok = wait_tile(ik))) break;
             tc_fence_after();
-            if (in(0, j + 2)) issue_s(0, ik);
+            if (in(0, j + 1)) issue_s(0, ik);
           }
           if (pv) {
             if (in(1, j) && !(ok = issue_pv(1, j, iv))) break;
             mma_commit_w(&bars[T_EMPTY0 + iv % C::NT]);
           }
           if (s) {
-            if (in(1, j + 2)) issue_s(1, ik);
+            if (in(1, j + 1)) issue_s(1, ik);
             mma_commit_w(&bars[T_EMPTY0 + ik % C::NT]);
           }
         }
@@ -671,24 +670,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
     }
     // (rows past the request's last one go along with a max of their own)
     float m_used = live ? -INFINITY : 0.f, l = 0.f;
-    for (int j = tl.lo; j < tl.hi; ++j, ++c) {
-      const uint32_t tS = tmem + lane_off + C::T_S + w * 128 + (c & 1) * 64;
-      if (!(ok = mbar_wait_warp(&bars[S_FULL0 + 2 * w + (c & 1)], (c >> 1) & 1, wc, kErrWaitS))) break;
-      tc_fence_after();
-      const float* const sc = k_scales + ((bc0 + j - u.j0) % kScaleRing) * kGroups;
+    for (int jh = 2 * tl.lo; jh < 2 * tl.hi; ++jh) {
+      const int h2 = jh & 1, k0 = jh * HK;
+      const uint32_t tS = tmem + lane_off + C::T_S + w * 128 + h2 * 64;
+      if (h2 == 0) {
+        if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
+        tc_fence_after();
+      }
+      const float* const sc = k_scales + ((bc0 + (jh >> 1) - u.j0) % kScaleRing) * kGroups + h2 * 4;
       const float4 sa = *reinterpret_cast<const float4*>(sc);
-      float f[kGroups] = {sa.x, sa.y, sa.z, sa.w};
-      const int k0 = j * KT;
-      bool masked = k0 < tl.all_lo || k0 + KT > tl.all_hi;
+      float f[4] = {sa.x, sa.y, sa.z, sa.w};
+      bool masked = k0 < tl.all_lo || k0 + HK > tl.all_hi;
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) masked |= f[g] < 0.f;
+      for (int g = 0; g < 4; ++g) masked |= f[g] < 0.f;
       uint32_t no_page = 0;  // groups without a page
       if (masked) {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) no_page |= f[g] < 0.f ? 1u << g : 0u;
+        for (int g = 0; g < 4; ++g) no_page |= f[g] < 0.f ? 1u << g : 0u;
       }
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) f[g] = fmaxf(fabsf(f[g]) * rs, 0x1p-126f);  // (0 times -inf would be NaN)
+      for (int g = 0; g < 4; ++g) f[g] = fmaxf(fabsf(f[g]) * rs, 0x1p-126f);  // (0 times -inf would be NaN)
       const int v_lo = my_lo - k0, v_hi = my_hi - k0;
       // One pass with the max at hand, no max taken: while the block's sum of P
       // stays at or below 2^15, no P is above it, which fp16 and the f32 sums
@@ -709,11 +710,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool need = first;  // (row by row, so that no row's result depends on another's)
       {
-        uint32_t pw[KT / 2];
+        uint32_t pw[HK / 2];
         const float msub = first ? 0.f : m_used;
         const float2 nm2 = make_float2(-msub, -msub);
 #pragma unroll
-        for (int h = 0; h < KT / 32; ++h) {
+        for (int h = 0; h < HK / 32; ++h) {
           uint32_t sr[32];
           load_scores(h, sr);
 #pragma unroll
@@ -729,13 +730,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         need |= !((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y) <= kMostSum);
         if (!__any_sync(0xffffffffu, need)) {
 #pragma unroll
-          for (int h = 0; h < KT / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
+          for (int h = 0; h < HK / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
         }
       }
       if (__any_sync(0xffffffffu, need)) {
         float m_new = m_used;
 #pragma unroll 1
-        for (int h = 0; h < KT / 32; ++h) {
+        for (int h = 0; h < HK / 32; ++h) {
           uint32_t sr[32];
           load_scores(h, sr);
 #pragma unroll
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         const bool grew = need && m_new > m_used;
         if (__any_sync(0xffffffffu, grew && !first)) {
           // the tile's previous P V (of this unit: some max is finite) has completed before its O rows are scaled
-          if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + ((c - 1) & 1)], ((c - 1) >> 1) & 1, wc, kErrWaitDQFull))) break;
+          if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + (h2 ^ 1)], (c - 1 + h2) & 1, wc, kErrWaitDQFull))) break;
           tc_fence_after();
           const float shrink = grew && !first ? ex2(m_used - m_new) : 1.f;
           l *= shrink;
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         const float msub = m_used == -INFINITY ? 0.f : m_used;
         sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int h = 0; h < KT / 32; ++h) {
+        for (int h = 0; h < HK / 32; ++h) {
           uint32_t sr[32], pw[16];
           load_scores(h, sr);
           const float fa = h == 0 ? f[0] : f[2], fb = h == 0 ? f[1] : f[3];
@@ -789,12 +790,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[P_READY0 + 2 * w + (c & 1)]);
+      if (lane == 0) mbar_arrive(&bars[P_READY0 + 2 * w + h2]);
+      c += h2;
     }
     if (!ok) break;
     // ---- the row's O and LSE, or its part
     if (any) {
-      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + ((c - 1) & 1)], ((c - 1) >> 1) & 1, wc, kErrWaitDQFull))) break;
+      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + 1], (c - 1) & 1, wc, kErrWaitDQFull))) break;
       tc_fence_after();
     }
     const bool whole = u.slot < 0;
