@@ -30,9 +30,13 @@ from ._binding import AttnBwdError, Strides, c_f32, c_i32, c_i64, c_sz, c_vp
 DT = {torch.float16: _binding.DT_F16, torch.bfloat16: _binding.DT_BF16}
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", c_vp), ("sk", Strides), ("v", c_vp), ("sv", Strides), ("k_scale", c_vp), ("v_scale", c_vp),
-                ("num_blocks", c_i64), ("page_size", c_i64), ("HKV", c_i64), ("D", c_i64)]
+_F8, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+
+
+class _Cache(ctypes.Structure):  # attn_kv_cache_t, its strides spelled out
+    _fields_ = [("k", c_vp), ("k_b", c_i64), ("k_s", c_i64), ("k_h", c_i64), ("v", c_vp), ("v_b", c_i64),
+                ("v_s", c_i64), ("v_h", c_i64), ("k_scale", c_vp), ("v_scale", c_vp), ("num_blocks", c_i64),
+                ("page_size", c_i64), ("HKV", c_i64), ("D", c_i64)]
 
 
 _binding._SIGS.update({
@@ -56,8 +60,9 @@ class KvPlan(NamedTuple):
 
 
 class _Launch:
-    """Context of one call: the tensors' device current, work on ``stream``
-    (None: that device's current stream), new tensors made on it."""
+    """Context of a call with a stream or device of its own: the tensors' device
+    current, work on ``stream`` (None: that device's current stream), new tensors
+    made on it."""
 
     __slots__ = ("device", "stream", "_ctx")
 
@@ -66,8 +71,6 @@ class _Launch:
 
     def __enter__(self):
         device, stream = self.device, self.stream
-        if stream is None and device.index == torch.cuda.current_device():
-            return torch.cuda.current_stream(device).cuda_stream
         with contextlib.ExitStack() as ctx:
             ctx.enter_context(torch.cuda.device(device))
             if stream is None:
@@ -81,12 +84,30 @@ class _Launch:
         return stream.cuda_stream
 
     def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc) if self._ctx is not None else None
+        return self._ctx.__exit__(*exc)
+
+
+def _run(device, stream, body):
+    """body(stream pointer) with ``device`` current.  (The common case, the
+    current stream of the current device, takes no context manager: a decode
+    step's calls are bound by the host.)"""
+    if stream is None and device.index == torch.cuda.current_device():
+        return body(_raw_stream(device.index))
+    with _Launch(device, stream) as ptr:
+        return body(ptr)
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # noqa: F811  (the same without a Stream object)
 
 
 def _on(device, **tensors):
     for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        if not isinstance(t, torch.Tensor) or t.device != device:
             raise AttnBwdError(f"{name} must be a CUDA tensor on the device of the other tensors")
 
 
@@ -97,13 +118,13 @@ def _device(name, t):
 
 
 def _vec(name, t, n=None):
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+    if t.dtype != _I32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
         raise AttnBwdError(f"{name} must be a contiguous int32 vector" + ("" if n is None else f" of {n}"))
     return t.data_ptr()
 
 
 def _table(t, n):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != n or t.stride(1) != 1:
+    if t.dtype != _I32 or t.dim() != 2 or t.shape[0] != n or t.stride(1) != 1:
         raise AttnBwdError(f"block_table must be int32 [{n}, max_blocks] with contiguous rows")
     # (the stride of a single row says nothing)
     return t.data_ptr(), t.stride(0) if n > 1 else max(t.stride(0), t.shape[1]), t.shape[1]
@@ -112,24 +133,28 @@ def _table(t, n):
 def _strides(name, t, shape=None):
     """Strides of a 4-D tensor; those of dimensions of size one, which no
     address uses, are replaced by a value that passes the checks."""
-    if t.dim() != 4 or t.stride(3) != 1 or (shape is not None and tuple(t.shape) != shape):
-        raise AttnBwdError(f"{name} must be a 4-D tensor with a contiguous head dimension"
-                           + ("" if shape is None else f" and shape {list(shape)}"))
-    s, n = t.stride(), t.shape
-    return Strides(*(s[i] if n[i] > 1 else 128 for i in range(3)))
+    if t.dim() != 4 or (shape is not None and t.shape != shape):
+        raise AttnBwdError(f"{name} must be a 4-D tensor" + ("" if shape is None else f" of shape {list(shape)}"))
+    b, s, h, d = t.stride()
+    if d != 1:
+        raise AttnBwdError(f"{name} must have a contiguous head dimension")
+    nb, ns, nh, _ = t.shape
+    return b if nb > 1 else 128, s if ns > 1 else 128, h if nh > 1 else 128
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, device):
     _on(device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
+    if k_cache.dtype != _F8 or v_cache.dtype != _F8:
         raise AttnBwdError("k_cache and v_cache must be float8_e4m3fn")
     sk = _strides("k_cache", k_cache)
-    shape = tuple(k_cache.shape)
+    shape = k_cache.shape
     sv = _strides("v_cache", v_cache, shape)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (shape[0], shape[2]) or not t.is_contiguous():
-            raise AttnBwdError(f"{name} must be contiguous float32 [num_blocks, HKV]")
-    return _Cache(k_cache.data_ptr(), sk, v_cache.data_ptr(), sv, k_scale.data_ptr(), v_scale.data_ptr(), *shape)
+    nb, page, hkv, d = shape
+    for t in (k_scale, v_scale):
+        if t.dtype != _F32 or t.shape != (nb, hkv) or not t.is_contiguous():
+            raise AttnBwdError("k_scale and v_scale must be contiguous float32 [num_blocks, HKV]")
+    return _Cache(k_cache.data_ptr(), *sk, v_cache.data_ptr(), *sv, k_scale.data_ptr(), v_scale.data_ptr(), nb, page,
+                  hkv, d)
 
 
 def new_kv_cache(num_blocks: int, page_size: int, HKV: int, D: int, device=None):
@@ -160,21 +185,28 @@ def kv_block_tables(ctx_lens, new_lens, block_table, free_blocks, page_size: int
     if free_start is not None:
         _on(device, free_start=free_start)
         start = _vec("free_start", free_start, 1)
-    with _Launch(device, stream) as ptr:
-        if out is None:
-            # one buffer for the five outputs
-            m = int(max_tokens)
-            buf = torch.empty(2 * n + 4 + 2 * m, dtype=torch.int32, device=device)
-            out = KvPlan(buf[:n + 1], buf[n + 1:2 * n + 1], buf[2 * n + 4:2 * n + 4 + m], buf[2 * n + 4 + m:],
-                         buf[2 * n + 1:2 * n + 4])
+    sizes = (n + 1, n, max_tokens, max_tokens, 3)
+
+    def body(ptr):
+        plan, ptrs = out, None
+        if plan is None:
+            if max_tokens < 0:
+                raise AttnBwdError("max_tokens must not be negative")
+            buf = torch.empty(sum(sizes), dtype=_I32, device=device)  # one buffer for the five outputs
+            plan = KvPlan(*buf.split(sizes))
+            at, ptrs = buf.data_ptr(), []
+            for k in sizes:
+                ptrs.append(at)
+                at += 4 * k
         else:
-            _on(device, **out._asdict())
-        sizes = (n + 1, n, max_tokens, max_tokens, 3)
-        ptrs = [_vec(name, t, k) for (name, t), k in zip(out._asdict().items(), sizes)]
+            _on(device, **plan._asdict())
+            ptrs = [_vec(name, t, k) for name, t, k in zip(plan._fields, plan, sizes)]
         _binding._status(_binding.library().attn_kv_block_tables(
             ctx, add, n, table, stride, width, free, free_blocks.shape[0], start, page_size, num_blocks, max_tokens,
             *ptrs, ptr), "attn_kv_block_tables")
-    return out
+        return plan
+
+    return _run(device, stream, body)
 
 
 def kv_cache_write(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
@@ -184,19 +216,18 @@ def kv_cache_write(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, stream=No
     device = _device("k", k)
     _on(device, v=v, slot_map=slot_map)
     c = _cache(k_cache, v_cache, k_scale, v_scale, device)
-    sk = _strides("k", k)
+    sk = Strides(*_strides("k", k))
     T = k.shape[1]
     shape = (1, T, c.HKV, c.D)
-    if tuple(k.shape) != shape:
+    if k.shape != shape:
         raise AttnBwdError(f"k must be [1, T, {c.HKV}, {c.D}]")
-    sv = _strides("v", v, shape)
+    sv = Strides(*_strides("v", v, shape))
     dt = DT.get(k.dtype)
     if dt is None or v.dtype != k.dtype:
         raise AttnBwdError(f"unsupported dtypes {k.dtype}, {v.dtype}: both fp16 or both bf16")
     slots = _vec("slot_map", slot_map, T)
-    with _Launch(device, stream) as ptr:
-        _binding._status(_binding.library().attn_kv_cache_write(k.data_ptr(), sk, v.data_ptr(), sv, slots, T, dt,
-                                                                ctypes.byref(c), ptr), "attn_kv_cache_write")
+    _run(device, stream, lambda ptr: _binding._status(_binding.library().attn_kv_cache_write(
+        k.data_ptr(), sk, v.data_ptr(), sv, slots, T, dt, ctypes.byref(c), ptr), "attn_kv_cache_write"))
 
 
 def kv_cache_workspace_size(T: int, HQ: int, HKV: int, D: int) -> int:
@@ -216,7 +247,7 @@ def forward_kv_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seql
     device = _device("q", q)
     _on(device, block_table=block_table, cu_seqlens=cu_seqlens, kv_lens=kv_lens)
     c = _cache(k_cache, v_cache, k_scale, v_scale, device)
-    sq = _strides("q", q)
+    sq = Strides(*_strides("q", q))
     b, T, HQ, D = q.shape
     dt = DT.get(q.dtype)
     if dt is None:
@@ -229,24 +260,32 @@ def forward_kv_cache(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seql
     if sm_scale is None:
         sm_scale = D ** -0.5
     lib = _binding.library()
-    with _Launch(device, stream) as ptr:
+
+    def body(ptr):
         if out is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=device)
-            lse = torch.empty(1, HQ, T, dtype=torch.float32, device=device)
+            o = torch.empty_like(q, memory_format=torch.contiguous_format)
+            lse = torch.empty((1, HQ, T), dtype=_F32, device=device)
+            so, sl = Strides(T * HQ * D, HQ * D, D), Strides(1, 1, max(T, 1))
         else:
             o, lse = out
             _on(device, o=o, lse=lse)
-            if o.dtype != q.dtype or lse.dtype != torch.float32 or tuple(lse.shape) != (1, HQ, T):
+            if o.dtype != q.dtype or lse.dtype != _F32 or lse.shape != (1, HQ, T):
                 raise AttnBwdError("out must be o (of q's dtype and shape) and lse (float32 [1, HQ, T])")
-        so = _strides("o", o, (1, T, HQ, D))
+            so = Strides(*_strides("o", o, q.shape))
+            sl = Strides(1, lse.stride(2) if T > 1 else 1, lse.stride(1) if HQ > 1 else 1)
         if workspace is None:
-            workspace = torch.empty(lib.attn_fwd_kv_cache_workspace_size(T, HQ, c.HKV, D), dtype=torch.uint8,
-                                    device=device)
+            ws = torch.empty(lib.attn_fwd_kv_cache_workspace_size(T, HQ, c.HKV, D), dtype=torch.uint8, device=device)
+            nbytes = ws.numel()
         else:
-            _on(device, workspace=workspace)
-        sl = Strides(1, lse.stride(2) if T > 1 else 1, lse.stride(1) if HQ > 1 else 1)
+            ws = workspace
+            _on(device, workspace=ws)
+            if not ws.is_contiguous():
+                raise AttnBwdError("workspace must be contiguous")
+            nbytes = ws.numel() * ws.element_size()
         _binding._status(lib.attn_fwd_kv_cache(
             q.data_ptr(), sq, T, HQ, dt, sm_scale, ctypes.byref(c), table, stride, width, cu, lens, n,
-            1 if causal else 0, window, o.data_ptr(), so, lse.data_ptr(), sl, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), ptr), "attn_fwd_kv_cache")
-    return o, lse
+            1 if causal else 0, window, o.data_ptr(), so, lse.data_ptr(), sl, ws.data_ptr(), nbytes, ptr),
+            "attn_fwd_kv_cache")
+        return o, lse
+
+    return _run(device, stream, body)

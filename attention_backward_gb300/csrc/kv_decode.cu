@@ -531,7 +531,8 @@ template <int D, int NB, bool BF16>
 cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
   using C = DecCfg<D, NB>;
   auto kern = kv_decode_kernel<D, NB, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem_once(kern, C::SMEM, &done);
   if (e != cudaSuccess) return e;
   const int grid = imin(sms * C::CTAS, kKvDecMaxRows / (2 * kWarps * C::RT));
   e = launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);

@@ -839,7 +839,8 @@ template <int D, bool BF16>
 cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int grid, cudaStream_t st) {
   using C = PrCfg<D>;
   auto kern = kv_prompt_kernel<D, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem_once(kern, C::SMEM, &done);
   if (e != cudaSuccess) return e;
   return launch_after_previous(kern, grid, THREADS, C::SMEM, st, maps, p);
 }

@@ -58,12 +58,12 @@ def test_block_tables_refusals(ab, kw, want):
 
 
 def cache(ab, **kw):
-    S = ab._binding.Strides
-    c = dict(k=A, sk=S(4096, 256, 128), v=A * 8, sv=S(4096, 256, 128), k_scale=A * 16, v_scale=A * 17, num_blocks=32,
+    c = dict(k=A, sk=(4096, 256, 128), v=A * 8, sv=(4096, 256, 128), k_scale=A * 16, v_scale=A * 17, num_blocks=32,
              page_size=16, HKV=2, D=128)
     assert set(kw) <= set(c)
-    c.update({k: S(*v) if isinstance(v, tuple) else v for k, v in kw.items()})
-    return ctypes.byref(ab._kv_cache._Cache(*c.values()))
+    c.update(kw)
+    flat = [x for v in c.values() for x in (v if isinstance(v, tuple) else (v,))]
+    return ctypes.byref(ab._kv_cache._Cache(*flat))
 
 
 BAD_CACHES = [
