@@ -73,8 +73,7 @@ struct KvAttnParams {
 };
 
 // Tensor maps of the cache's bytes, dims (D, HKV, page_size, num_blocks): box D
-// bytes x tokens of one head (16 in the decode kernel, a page but at most a
-// block in the prompt kernel), swizzled over rows of D bytes.
+// bytes x tokens of one head (a page, but at most a kernel's tile), swizzled over rows of D bytes.
 struct KvMaps {
   CUtensorMap k, v;
 };
@@ -83,8 +82,9 @@ struct KvMaps {
 // prompt kernel, the others to the decode kernel.
 constexpr int kKvPrMinRows = 65;
 
-// Decode kernel: keys per tile, and what starting a unit costs in tiles.
-constexpr int kKvDecKeys = 16;
+// Decode kernel: keys per tile (2 KB of K and of V), and what starting a unit
+// costs in tiles.
+constexpr int kv_dec_keys(int64_t D) { return D == 64 ? 32 : 16; }
 constexpr int kKvDecCost = 2;
 // Most partial rows of a launch (2 slots a worker, 8 or 16 rows a slot) and most
 // workers: these size the workspace and bound the grid.

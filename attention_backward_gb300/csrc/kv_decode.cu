@@ -9,8 +9,8 @@
 // only when it grows by more than 2^8).  Bound by the bytes of K and V: 2 D
 // bytes and 4 D G flops a key.
 //
-// Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 16
-// keys, over persistent warps.  Every KV head has the same line, so worker
+// Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 2 KB
+// of K and of V (16 or 32 keys), over persistent warps.  Every KV head has the same line, so worker
 // (warp) w takes head w % HKV and part w / HKV of its line: the warps of a CTA
 // walk the same pages of neighbouring heads together, which reads pages stored
 // token by token in rows of several heads (one head at a time, 128 B out of
@@ -52,9 +52,8 @@ namespace ab {
 
 namespace {
 
-constexpr int KT = kKvDecKeys;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kStages = 3;       // ring of 16-key slots per warp
+constexpr int kStages = 3;       // ring of slots (one tile each) per warp
 constexpr float kRescale = 8.f;  // log2 growth of a row max that triggers a rescale
 // Fewest line positions of a worker: below it, more parts cost more to join
 // than they save.
@@ -63,8 +62,9 @@ constexpr int kMinWork = 8;
 template <int D, int NB>
 struct DecCfg {
   static constexpr int RT = 8 * NB;                  // rows of a unit
+  static constexpr int KT = kv_dec_keys(D);          // keys of a tile
   static constexpr int CTAS = NB == 1 ? 4 : 3;       // resident per SM
-  static constexpr int TILE = KT * D;                // bytes of K, or of V, of 16 keys
+  static constexpr int TILE = KT * D;                // bytes of K, or of V, of a tile
   static constexpr int WARP = kStages * 2 * TILE;    // a warp's ring
   static constexpr int OFF_BAR = kWarps * WARP;
   static constexpr int OFF_ABORT = OFF_BAR + kWarps * kStages * 8;
@@ -94,7 +94,7 @@ struct Cursor {
 // All threads of a CTA: the length of the line.  A thread sums ceil(N / 128)
 // consecutive requests; ``before`` (shared, kThreads entries) gets the sums
 // before each thread's.
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ int64_t line_length(const KvAttnParams& p, int64_t* before) {
   __shared__ int64_t s_warp[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -125,7 +125,7 @@ __device__ __forceinline__ int64_t line_length(const KvAttnParams& p, int64_t* b
 }
 
 // A warp's cursor at position x (below the line's length).
-template <int RT>
+template <int RT, int KT>
 __device__ __forceinline__ Cursor locate(const KvAttnParams& p, const int64_t* before, int64_t x) {
   const int K = (p.N + kThreads - 1) / kThreads;
   int lo = 0, hi = kThreads;  // before[lo] <= x < before[lo + 1]
@@ -158,7 +158,8 @@ template <int D, int NB, bool BF16>
 __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
     kv_decode_kernel(const __grid_constant__ KvMaps maps, const __grid_constant__ KvAttnParams p) {
   using C = DecCfg<D, NB>;
-  constexpr int RT = C::RT;
+  constexpr int RT = C::RT, KT = C::KT;
+  constexpr int NZ = KT / 16;  // 16-key groups of a tile, a page each
   constexpr int KC = D / 64;   // 16-byte chunks of a key's row per thread
   constexpr int VB = D / 8;    // bytes of a value row per thread
   constexpr int MT = D / 16;   // row tiles of O^T
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
   const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
   if (tid == 0) *wc.err = aligned ? kErrNone : kErrAlign;
   if (lane == 0) p.fin[worker] = -1;
-  const int64_t total = line_length<RT>(p, before);  // (its barriers publish what thread 0 wrote)
+  const int64_t total = line_length<RT, KT>(p, before);  // (its barriers publish what thread 0 wrote)
   if (!aligned || total == 0) return;
   // Parts of a head's line, at least kMinWork positions each; with more heads
   // than workers, one part and several heads a worker.
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
   int in_slot = 0, out_slot = 0, pending = 0;
   uint32_t out_par = 0;
 
-  const Cursor first = locate<RT>(p, before, begin);
+  const Cursor first = locate<RT, KT>(p, before, begin);
   for (int head = worker % p.HKV; head < p.HKV; head += workers) {
   Cursor cur = first;
   KvReq rq = kv_request(cur.n, p);
@@ -210,17 +211,17 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
     const int row0 = cur.rt * RT;
     const int rows = imin(RT, rq.R - row0);
 
-    // Page ids of my slots and their scales, 32 tiles at a time: lane i holds
-    // those of tile ``ld_batch + i`` (-1: no page, or no key that the unit sees).
+    // Page ids of 32 16-key groups and their scales at a time: lane i holds those
+    // of group i behind tile ``ld_batch`` (-1: no page, or no key that the unit sees).
+    constexpr int BATCH = 32 / NZ;
     auto key0_of = [&](int t) { return (kt.t0 + t) * KT; };
     int ld_batch = part0, ld_blk = -1;
     float ld_ks = 0.f, ld_vs = 0.f;
     auto load_ids = [&]() {
-      const int t = ld_batch + lane;
       ld_blk = -1, ld_ks = ld_vs = 0.f;
-      if (t < part1) {
-        const int k0 = key0_of(t);
-        if (k0 < kt.hi && k0 + KT > kt.lo) {
+      if (ld_batch + lane / NZ < part1) {
+        const int k0 = key0_of(ld_batch) + lane * 16;
+        if (k0 < kt.hi && k0 + 16 > kt.lo) {
           ld_blk = p.table[cur.n * p.table_stride + (k0 >> p.page_log2)];
           if (ld_blk < 0 || ld_blk >= p.num_blocks) ld_blk = -1;
         }
@@ -232,24 +233,37 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
         ld_ks = p.k_scale[at], ld_vs = p.v_scale[at];
       }
     };
-    auto issue = [&](int t) {  // copies of tile t's 16 keys into the next slot
+    auto issue = [&](int t) {  // copies of tile t's keys into the next slot
       if (t >= part1) return;
-      if (t - ld_batch == 32) {
+      if (t - ld_batch == BATCH) {
         ld_batch = t;
         load_ids();
         load_scales();
       }
-      const int b = __shfl_sync(0xffffffffu, ld_blk, t - ld_batch);
+      int b[NZ], most = -1, held = 0;
+#pragma unroll
+      for (int z = 0; z < NZ; ++z) {
+        b[z] = __shfl_sync(0xffffffffu, ld_blk, (t - ld_batch) * NZ + z);
+        most = imax(most, b[z]), held += b[z] >= 0 ? 1 : 0;
+      }
       if (lane == 0) {
         uint64_t* const bar = &full[in_slot];
-        if (b >= 0) {
-          uint8_t* const dst = ring + in_slot * (2 * C::TILE);
-          const int s0 = key0_of(t) & ((1 << p.page_log2) - 1);
-          mbar_arrive_expect_tx(bar, 2 * C::TILE);
-          tma_load_4d(dst, &maps.k, bar, 0, head, s0, b);
-          tma_load_4d(dst + C::TILE, &maps.v, bar, 0, head, s0, b);
-        } else {
+        uint8_t* const dst = ring + in_slot * (2 * C::TILE);
+        const int s0 = key0_of(t) & ((1 << p.page_log2) - 1);
+        if (most < 0) {
           mbar_arrive(bar);
+        } else if ((16 << (p.page_log2 - 4)) >= KT) {  // the tile lies in one page
+          mbar_arrive_expect_tx(bar, 2 * C::TILE);
+          tma_load_4d(dst, &maps.k, bar, 0, head, s0, most);
+          tma_load_4d(dst + C::TILE, &maps.v, bar, 0, head, s0, most);
+        } else {
+          mbar_arrive_expect_tx(bar, held * 2 * 16 * D);
+#pragma unroll
+          for (int z = 0; z < NZ; ++z)
+            if (b[z] >= 0) {
+              tma_load_4d(dst + z * 16 * D, &maps.k, bar, 0, head, 0, b[z]);
+              tma_load_4d(dst + C::TILE + z * 16 * D, &maps.v, bar, 0, head, 0, b[z]);
+            }
         }
       }
       in_slot = in_slot + 1 == kStages ? 0 : in_slot + 1;
@@ -326,79 +340,98 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
       for (int t = 0; t < MT; ++t) o[e][t][0] = o[e][t][1] = o[e][t][2] = o[e][t][3] = 0.f;
     }
 
-    float ks_l = 0.f, vs_l = 0.f;  // scales of the 32 tiles being computed, and
+    float ks_l = 0.f, vs_l = 0.f;  // scales of the 32 groups being computed, and
     int cp_blk = -1;               // their ids
-    int cp_batch = part0 - 32;
+    int cp_batch = part0 - BATCH;
     bool ok = true;
     for (int t = part0; t < part1; ++t) {
-      if (t - cp_batch == 32) {  // (the copies are kStages tiles ahead: in this batch already)
+      if (t - cp_batch == BATCH) {  // (the copies are kStages tiles ahead: in this batch already)
         cp_batch = t;
         cp_blk = ld_blk, ks_l = ld_ks;
         vs_l = ld_vs < 0x1p-126f ? 0.f : ld_vs;  // (its inverse is taken)
       }
-      const int bi = t - cp_batch;
-      const float ks = __shfl_sync(0xffffffffu, ks_l, bi), vs = __shfl_sync(0xffffffffu, vs_l, bi);
-      const bool have = __shfl_sync(0xffffffffu, cp_blk, bi) >= 0;
+      float ks[NZ], vs[NZ];
+      bool have[NZ], any = false, edge = false;
+#pragma unroll
+      for (int z = 0; z < NZ; ++z) {
+        const int from = (t - cp_batch) * NZ + z;
+        ks[z] = __shfl_sync(0xffffffffu, ks_l, from), vs[z] = __shfl_sync(0xffffffffu, vs_l, from);
+        have[z] = __shfl_sync(0xffffffffu, cp_blk, from) >= 0;
+        any |= have[z], edge |= !have[z];
+      }
       if (!(ok = mbar_wait_warp(&full[out_slot], out_par, wc, kErrWaitKV))) break;
       const uint8_t* const st = ring + out_slot * (2 * C::TILE);
       if (++out_slot == kStages) out_slot = 0, out_par ^= 1;
       --pending;
-      if (have) {
+      if (any) {
         const int k0 = key0_of(t);
-        const bool edge = k0 < lo_all || k0 + KT > hi_all;
+        edge |= k0 < lo_all || k0 + KT > hi_all;
         // ---- S^T of 16 keys by 8 NB rows, in two chains
-        float s2[NB][2][4], s[NB][4];
+        float s[NZ][NB][4];
 #pragma unroll
-        for (int e = 0; e < NB; ++e)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) s2[e][y][0] = s2[e][y][1] = s2[e][y][2] = s2[e][y][3] = 0.f;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const uint4 x0 = *reinterpret_cast<const uint4*>(st + kv_chunk_at<D>(r8, c4 * KC + c));
-          const uint4 x8 = *reinterpret_cast<const uint4*>(st + 8 * D + kv_chunk_at<D>(r8, c4 * KC + c));
-          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w8[4] = {x8.x, x8.y, x8.z, x8.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t a[4];
-            e4m3x4_to_f16(w0[u], &a[0], &a[2]);
-            e4m3x4_to_f16(w8[u], &a[1], &a[3]);
-#pragma unroll
-            for (int e = 0; e < NB; ++e) mma16816(s2[e][u & 1], a, qb[e][c * 4 + u][0], qb[e][c * 4 + u][1]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < NB; ++e)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            s[e][y] = (s2[e][0][y] + s2[e][1][y]) * (ks * rs[e][y & 1]) - nm[e][y & 1];
-        if (edge) {
+        for (int z = 0; z < NZ; ++z) {
+          float s2[NB][2][4];
 #pragma unroll
           for (int e = 0; e < NB; ++e)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int k = k0 + r8 + 8 * (y >> 1);
-              if (k < lo[e][y & 1] || k >= hi[e][y & 1]) s[e][y] = -INFINITY;
+            for (int y = 0; y < 2; ++y) s2[e][y][0] = s2[e][y][1] = s2[e][y][2] = s2[e][y][3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const uint4 x0 = *reinterpret_cast<const uint4*>(st + kv_chunk_at<D>(16 * z + r8, c4 * KC + c));
+            const uint4 x8 = *reinterpret_cast<const uint4*>(st + kv_chunk_at<D>(16 * z + r8 + 8, c4 * KC + c));
+            const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w8[4] = {x8.x, x8.y, x8.z, x8.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t a[4];
+              e4m3x4_to_f16(w0[u], &a[0], &a[2]);
+              e4m3x4_to_f16(w8[u], &a[1], &a[3]);
+#pragma unroll
+              for (int e = 0; e < NB; ++e) mma16816(s2[e][u & 1], a, qb[e][c * 4 + u][0], qb[e][c * 4 + u][1]);
             }
+          }
+#pragma unroll
+          for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              s[z][e][y] = (s2[e][0][y] + s2[e][1][y]) * (ks[z] * rs[e][y & 1]) - nm[e][y & 1];
+        }
+        if (edge) {
+#pragma unroll
+          for (int z = 0; z < NZ; ++z)
+#pragma unroll
+            for (int e = 0; e < NB; ++e)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int k = k0 + 16 * z + r8 + 8 * (y >> 1);
+                if (!have[z] || k < lo[e][y & 1] || k >= hi[e][y & 1]) s[z][e][y] = -INFINITY;
+              }
         }
         // ---- a max that grew past the threshold, or a larger V scale: rescale
-        bool grew = vs > vref;
+        float vmx = vs[0];
 #pragma unroll
-        for (int e = 0; e < NB; ++e)
+        for (int z = 1; z < NZ; ++z) vmx = fmaxf(vmx, vs[z]);
+        bool grew = vmx > vref;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) grew |= s[e][y] > th[e][y & 1];
+        for (int z = 0; z < NZ; ++z)
+#pragma unroll
+          for (int e = 0; e < NB; ++e)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) grew |= s[z][e][y] > th[e][y & 1];
         if (__any_sync(0xffffffffu, grew)) {
           float g = 1.f;
-          if (vs > vref) {
-            g = vref / vs;
-            vref = vs;
-            vinv = 1.f / vs;
+          if (vmx > vref) {
+            g = vref / vmx;
+            vref = vmx;
+            vinv = 1.f / vmx;
           }
 #pragma unroll
           for (int e = 0; e < NB; ++e) {
             float f[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              float mx = fmaxf(s[e][y], s[e][2 + y]);  // the row's largest score, relative to nm
+              float mx = -INFINITY;  // the row's largest score, relative to nm
+#pragma unroll
+              for (int z = 0; z < NZ; ++z) mx = fmaxf(mx, fmaxf(s[z][e][y], s[z][e][2 + y]));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
               f[y] = 1.f;
@@ -406,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
                 f[y] = th[e][y] == -INFINITY ? 0.f : ex2(-mx);
                 nm[e][y] += mx;
                 th[e][y] = kRescale;
-                s[e][y] -= mx, s[e][2 + y] -= mx;
+#pragma unroll
+                for (int z = 0; z < NZ; ++z) s[z][e][y] -= mx, s[z][e][2 + y] -= mx;
               }
               l[e][y] *= f[y];
               f[y] *= g;
@@ -416,53 +450,59 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
               o[e][u][0] *= f[0], o[e][u][1] *= f[1], o[e][u][2] *= f[0], o[e][u][3] *= f[1];
           }
         }
-        uint32_t pb[NB][2];
-        const float ratio = vs * vinv;  // at most 1
+        uint32_t pb[NZ][NB][2];
 #pragma unroll
-        for (int e = 0; e < NB; ++e) {
-          const float p0 = ex2(s[e][0]), p1 = ex2(s[e][1]), p2 = ex2(s[e][2]), p3 = ex2(s[e][3]);
-          l[e][0] += p0 + p2;
-          l[e][1] += p1 + p3;
-          pb[e][0] = turn8x8(pack2<false>(p0 * ratio, p1 * ratio));
-          pb[e][1] = turn8x8(pack2<false>(p2 * ratio, p3 * ratio));
+        for (int z = 0; z < NZ; ++z) {
+          const float ratio = vs[z] * vinv;  // at most 1
+#pragma unroll
+          for (int e = 0; e < NB; ++e) {
+            const float p0 = ex2(s[z][e][0]), p1 = ex2(s[z][e][1]), p2 = ex2(s[z][e][2]), p3 = ex2(s[z][e][3]);
+            l[e][0] += p0 + p2;
+            l[e][1] += p1 + p3;
+            pb[z][e][0] = turn8x8(pack2<false>(p0 * ratio, p1 * ratio));
+            pb[z][e][1] = turn8x8(pack2<false>(p2 * ratio, p3 * ratio));
+          }
         }
         // ---- O^T += V^T P^T
         constexpr int VW = VB / 4;
-        uint32_t vw[4][VW];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = 2 * c4 + (e & 1) + 8 * (e >> 1);
-          const uint8_t* const at = st + C::TILE + kv_chunk_at<D>(key, r8 * VB / 16) + (r8 * VB) % 16;
-          if constexpr (VB == 16) {
-            const uint4 w = *reinterpret_cast<const uint4*>(at);
-            vw[e][0] = w.x, vw[e][1] = w.y, vw[e][2] = w.z, vw[e][3] = w.w;
-          } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(at);
-            vw[e][0] = w.x, vw[e][1] = w.y;
-          }
-        }
-        if (edge) {  // a zero P times a NaN byte would be NaN: keys that no row sees are zeroed
+        for (int z = 0; z < NZ; ++z) {
+          uint32_t vw[4][VW];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int k = k0 + 2 * c4 + (e & 1) + 8 * (e >> 1);
-            if (k < kt.lo || k >= kt.hi) {
-#pragma unroll
-              for (int u = 0; u < VW; ++u) vw[e][u] = 0u;
+            const int key = 16 * z + 2 * c4 + (e & 1) + 8 * (e >> 1);
+            const uint8_t* const at = st + C::TILE + kv_chunk_at<D>(key, r8 * VB / 16) + (r8 * VB) % 16;
+            if constexpr (VB == 16) {
+              const uint4 w = *reinterpret_cast<const uint4*>(at);
+              vw[e][0] = w.x, vw[e][1] = w.y, vw[e][2] = w.z, vw[e][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(at);
+              vw[e][0] = w.x, vw[e][1] = w.y;
             }
           }
-        }
+          if (edge) {  // a zero P times a NaN byte would be NaN: keys that no row sees are zeroed
 #pragma unroll
-        for (int u = 0; u < VW; ++u) {
-          // bytes 4u .. 4u + 3 of keys (0, 1) and (2, 3) paired; byte 2i is row r8 of tile i, 2i + 1 its row r8 + 8
-          uint32_t a[2][4];
-          e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x5140), &a[0][0], &a[0][1]);
-          e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x7362), &a[1][0], &a[1][1]);
-          e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x5140), &a[0][2], &a[0][3]);
-          e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x7362), &a[1][2], &a[1][3]);
+            for (int e = 0; e < 4; ++e) {
+              const int k = k0 + 16 * z + 2 * c4 + (e & 1) + 8 * (e >> 1);
+              if (!have[z] || k < kt.lo || k >= kt.hi) {
 #pragma unroll
-          for (int e = 0; e < NB; ++e)
+                for (int u = 0; u < VW; ++u) vw[e][u] = 0u;
+              }
+            }
+          }
 #pragma unroll
-            for (int y = 0; y < 2; ++y) mma16816(o[e][2 * u + y], a[y], pb[e][0], pb[e][1]);
+          for (int u = 0; u < VW; ++u) {
+            // bytes 4u .. 4u + 3 of keys (0, 1) and (2, 3) paired; byte 2i is row r8 of tile i, 2i + 1 its row r8 + 8
+            uint32_t a[2][4];
+            e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x5140), &a[0][0], &a[0][1]);
+            e4m3x4_to_f16(__byte_perm(vw[0][u], vw[1][u], 0x7362), &a[1][0], &a[1][1]);
+            e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x5140), &a[0][2], &a[0][3]);
+            e4m3x4_to_f16(__byte_perm(vw[2][u], vw[3][u], 0x7362), &a[1][2], &a[1][3]);
+#pragma unroll
+            for (int e = 0; e < NB; ++e)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) mma16816(o[e][2 * u + y], a[y], pb[z][e][0], pb[z][e][1]);
+          }
         }
       }
       __syncwarp();            // every lane has read the slot,
