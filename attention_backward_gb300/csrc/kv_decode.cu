@@ -57,13 +57,13 @@ constexpr int kStages = 3;       // ring of slots (one tile each) per warp
 constexpr float kRescale = 8.f;  // log2 growth of a row max that triggers a rescale
 // Fewest line positions of a worker: below it, more parts cost more to join
 // than they save.
-constexpr int kMinWork = 8;
+constexpr int kMinWork = 4;
 
 template <int D, int NB>
 struct DecCfg {
   static constexpr int RT = 8 * NB;                  // rows of a unit
   static constexpr int KT = kv_dec_keys(D);          // keys of a tile
-  static constexpr int CTAS = NB == 1 ? 4 : 3;       // resident per SM
+  static constexpr int CTAS = 2;                     // resident per SM
   static constexpr int TILE = KT * D;                // bytes of K, or of V, of a tile
   static constexpr int WARP = kStages * 2 * TILE;    // a warp's ring
   static constexpr int OFF_BAR = kWarps * WARP;
@@ -100,6 +100,7 @@ __device__ __forceinline__ int64_t line_length(const KvAttnParams& p, int64_t* b
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = (p.N + kThreads - 1) / kThreads;
   int64_t w = 0;
+#pragma unroll 1  // (small code: a launch starts with a cold instruction cache)
   for (int i = 0; i < K; ++i) {
     const int64_t n = static_cast<int64_t>(tid) * K + i;
     if (n >= p.N) break;
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
         }
       if (lane == 0 && part0 > 0 && part1 == kt.n) {  // ends a unit that part g0 began
         const int g0 = kv_part_of(total, unit0 + kKvDecCost, parts);
-        p.desc[worker] = make_int4(cur.n, cur.rt, head, g0);
+        p.desc[worker] = make_int4(rq.a, row0, head << 16 | rows, g0);
         p.fin[worker] = g0;
       }
     }

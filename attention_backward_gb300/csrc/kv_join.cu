@@ -4,7 +4,6 @@
 #include "kernels.h"
 #include "kv_cache.h"
 #include "kv_common.cuh"
-#include "kv_sched.cuh"
 #include "sm103.cuh"
 
 namespace ab {
@@ -12,7 +11,8 @@ namespace ab {
 namespace {
 
 // Joins the parts of each unit that was split over workers: entry w of ``desc``
-// names the unit that worker w finished (a worker finishes at most one that it
+// (first row of q of the request, first row of the unit in the request, head and
+// rows, first part) names the unit that worker w finished (a worker finishes at most one that it
 // did not begin), its parts d.w to w / stride in order; ``fin`` holds d.w, or -1
 // where there is none.  stride: workers per part (one a head in kv_decode.cu, 1
 // in kv_prompt.cu).  Every block lists the finished units (a scan of one
@@ -77,19 +77,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
   const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
   for (int t0 = blockIdx.x * groups; t0 < items; t0 += static_cast<int>(gridDim.x) * groups) {
     const int item = t0 + group;
-    KvReq rq{};
-    int4 d = make_int4(-1, 0, 0, 0);
-    int row0 = 0, live = 0, i0 = 0, i1 = 0;
+    int4 d = make_int4(0, 0, 0, 0);
+    int head = 0, live = 0, i0 = 0, i1 = 0;
     const int row = item % (RT / NR) * NR;  // my first row of the unit
     if (item < items) {
       const int w = list[item / (RT / NR)];
       d = p.desc[w];
-      rq = kv_request(d.x, p);
-      row0 = d.y * RT, live = imin(RT, rq.R - row0);
+      head = d.z >> 16, live = d.z & 0xffff;
       const int parts = w / stride - d.w + 1;
       i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
     }
-    auto slot_of = [&](int i) { return 2 * ((d.w + i) * stride + (stride > 1 ? d.z : 0)) + (i == 0 ? 1 : 0); };
+    auto slot_of = [&](int i) { return 2 * ((d.w + i) * stride + (stride > 1 ? head : 0)) + (i == 0 ? 1 : 0); };
     float m[NR], l[NR], acc[NR][ND];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -177,8 +175,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
 #pragma unroll
           for (int u = 0; u < ND; ++u) acc[r][u] = acc[r][u] * g + s_o[NR == 1 ? warp + k : 0][lane * ND + u] * f;
         }
-        const int64_t at = static_cast<int64_t>(rq.a) + (row0 + row + r) / p.G;
-        const int hq = d.z * p.G + (row0 + row + r) % p.G;
+        const int64_t at = static_cast<int64_t>(d.x) + (d.y + row + r) / p.G;
+        const int hq = head * p.G + (d.y + row + r) % p.G;
         const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
 #pragma unroll
         for (int u = 0; u < ND; ++u) acc[r][u] *= inv;

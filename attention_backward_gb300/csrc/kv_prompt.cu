@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           if (part1 <= part0) u.valid = 2;  // only start-up positions: nothing to do
           if (lane == 0 && part0 > 0 && part1 == kt.n) {
             const int g0 = kv_part_of(total, unit0 + COST, parts);
-            p.desc[blockIdx.x] = make_int4(cur.n, cur.rt, cur.head, g0);
+            p.desc[blockIdx.x] = make_int4(rq.a, u.row0, cur.head << 16 | imin(RT, rq.R - u.row0), g0);
             p.fin[blockIdx.x] = g0;
           }
         }

@@ -54,9 +54,8 @@ struct KvTiles {
 template <int RT, int KT>
 __host__ __device__ __forceinline__ KvTiles kv_row_tile(const KvReq& r, int rt, const KvAttnParams& p) {
   KvTiles t;
-  const int i0 = rt * RT / p.G, r1 = imin(r.R, (rt + 1) * RT);
-  const int i1 = (r1 - 1) / p.G;
-  int x;
+  int i0 = 0, i1 = r.nq - 1, x;
+  if (r.R > RT) i0 = rt * RT / p.G, i1 = (imin(r.R, (rt + 1) * RT) - 1) / p.G;
   kv_row_keys(r, i0, p.causal, p.window, &t.lo, &x);
   kv_row_keys(r, i1, p.causal, p.window, &x, &t.hi);
   if (t.hi <= t.lo) {
@@ -79,12 +78,16 @@ template <int RT, int KT, int COST>
 __host__ __device__ __forceinline__ int64_t kv_request_work(const KvReq& r, const KvAttnParams& p) {
   int64_t w = 0;
   const int nt = kv_row_tiles<RT>(r);
+#pragma unroll 1
   for (int rt = 0; rt < nt; ++rt) w += kv_row_tile<RT, KT>(r, rt, p).n + COST;
   return w;
 }
 
 // First position of part c of C, and the part that holds position x.
-__host__ __device__ __forceinline__ int64_t kv_part_begin(int64_t total, int c, int C) { return total * c / C; }
+__host__ __device__ __forceinline__ int64_t kv_part_begin(int64_t total, int c, int C) {
+  if (total <= 0xffffffffll / C) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(C);
+  return total * c / C;
+}
 __host__ __device__ __forceinline__ int kv_part_of(int64_t total, int64_t x, int C) {
   int c = static_cast<int>((x * C) / total);
   while (c > 0 && kv_part_begin(total, c, C) > x) --c;
