@@ -69,17 +69,16 @@ bool make_maps(KvMaps* m, const attn_kv_cache_t& c, int64_t box_tokens) {
 }
 
 // Workspace of attention over the cache: the header, then for each of its two
-// kernels an error word a CTA, a flag and a descriptor a worker, and the
-// partial rows.
+// kernels an error word a CTA, a descriptor a worker, and the partial
+// rows.
 struct KvWs {
-  int64_t err_off, fin_off, desc_off, ml_off, o_off, total;
+  int64_t err_off, desc_off, ml_off, o_off, total;
 };
 
 KvWs kv_ws(int64_t start, int64_t workers, int64_t rows, int64_t D) {
   KvWs w;
   w.err_off = start;
-  w.fin_off = w.err_off + round_up(workers * 4, 256);
-  w.desc_off = w.fin_off + round_up(workers * 4, 256);
+  w.desc_off = w.err_off + round_up(workers * 4, 256);
   w.ml_off = w.desc_off + workers * 16;
   w.o_off = w.ml_off + rows * 8;
   w.total = w.o_off + rows * D * 4;
@@ -93,7 +92,6 @@ bool kv_may_prompt(int64_t T, int64_t G) { return T * G >= kKvPrMinRows; }
 
 void kv_place(KvAttnParams* p, const KvWs& w, uint8_t* ws) {
   p->cta_err = reinterpret_cast<int*>(ws + w.err_off);
-  p->fin = reinterpret_cast<int*>(ws + w.fin_off);
   p->desc = reinterpret_cast<int4*>(ws + w.desc_off);
   p->part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   p->part_o = reinterpret_cast<float*>(ws + w.o_off);

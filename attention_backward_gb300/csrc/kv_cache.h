@@ -65,7 +65,6 @@ struct KvAttnParams {
   // workspace
   int* err;
   int* cta_err;     // per CTA: its error code
-  int* fin;         // per worker: the first part of that unit, or -1
   int4* desc;       // per worker: the unit whose split it finishes (see kv_decode.cu)
   float2* part_ml;  // [2 * workers][rows] running max (log2 units) and sum
   float* part_o;    // [2 * workers][rows][D] unnormalised O
@@ -88,7 +87,7 @@ constexpr int kv_dec_keys(int64_t D) { return D == 64 ? 64 : 32; }
 constexpr int kKvDecCost = 2;
 // Most partial rows of a launch (2 slots a worker, 8 or 16 rows a slot) and most
 // workers: these size the workspace and bound the grid.
-constexpr int kKvDecMaxRows = 65536;
+constexpr int kKvDecMaxRows = 32768;
 constexpr int kKvDecMaxWorkers = kKvDecMaxRows / 16;
 
 // Prompt kernel: rows of a unit, keys per block, what starting a unit costs in

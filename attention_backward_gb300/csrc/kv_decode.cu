@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
   const bool aligned = (smem_u32(sm) & 1023u) == 0;  // the swizzled tiles need it
   const int worker = blockIdx.x * kWarps + warp, workers = gridDim.x * kWarps;
   if (tid == 0) *wc.err = aligned ? kErrNone : kErrAlign;
-  if (lane == 0) p.fin[worker] = -1;
+  if (lane == 0) p.desc[worker] = make_int4(0, 0, 0, -1);
   const int64_t total = line_length<RT, KT>(p, before);  // (its barriers publish what thread 0 wrote)
   if (!aligned || total == 0) return;
   // Parts of a head's line, at least kMinWork positions each; with more heads
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
     // Page ids of 32 16-key groups and their scales at a time: lane i holds those
     // of group i behind tile ``ld_batch`` (-1: no page, or no key that the unit sees).
     constexpr int BATCH = 32 / NZ;
+    const int gb = imin(NZ, 1 << (p.page_log2 - 4));  // groups of a box of the maps
     auto key0_of = [&](int t) { return (kt.t0 + t) * KT; };
     int ld_batch = part0, ld_blk = -1;
     float ld_ks = 0.f, ld_vs = 0.f;
@@ -241,29 +242,32 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
         load_ids();
         load_scales();
       }
-      int b[NZ], most = -1, held = 0;
+      // a box is a page, at most a tile: ``gb`` groups, copied where one of them has an id
+      int b[NZ];
 #pragma unroll
-      for (int z = 0; z < NZ; ++z) {
-        b[z] = __shfl_sync(0xffffffffu, ld_blk, (t - ld_batch) * NZ + z);
-        most = imax(most, b[z]), held += b[z] >= 0 ? 1 : 0;
-      }
+      for (int z = 0; z < NZ; ++z) b[z] = __shfl_sync(0xffffffffu, ld_blk, (t - ld_batch) * NZ + z);
       if (lane == 0) {
+        int boxes = 0;
+#pragma unroll
+        for (int z = 0; z < NZ; ++z) {
+#pragma unroll
+          for (int y = 1; y < NZ - z; ++y)
+            if (y < gb) b[z] = imax(b[z], b[z + y]);
+          if ((z & (gb - 1)) != 0) b[z] = -1;
+          boxes += b[z] >= 0 ? 1 : 0;
+        }
         uint64_t* const bar = &full[in_slot];
         uint8_t* const dst = ring + in_slot * (2 * C::TILE);
-        const int s0 = key0_of(t) & ((1 << p.page_log2) - 1);
-        if (most < 0) {
+        if (boxes == 0) {
           mbar_arrive(bar);
-        } else if ((16 << (p.page_log2 - 4)) >= KT) {  // the tile lies in one page
-          mbar_arrive_expect_tx(bar, 2 * C::TILE);
-          tma_load_4d(dst, &maps.k, bar, 0, head, s0, most);
-          tma_load_4d(dst + C::TILE, &maps.v, bar, 0, head, s0, most);
         } else {
-          mbar_arrive_expect_tx(bar, held * 2 * 16 * D);
+          mbar_arrive_expect_tx(bar, boxes * gb * (2 * 16 * D));
 #pragma unroll
           for (int z = 0; z < NZ; ++z)
             if (b[z] >= 0) {
-              tma_load_4d(dst + z * 16 * D, &maps.k, bar, 0, head, 0, b[z]);
-              tma_load_4d(dst + C::TILE + z * 16 * D, &maps.v, bar, 0, head, 0, b[z]);
+              const int s0 = (key0_of(t) + 16 * z) & ((1 << p.page_log2) - 1);
+              tma_load_4d(dst + z * 16 * D, &maps.k, bar, 0, head, s0, b[z]);
+              tma_load_4d(dst + C::TILE + z * 16 * D, &maps.v, bar, 0, head, s0, b[z]);
             }
         }
       }
@@ -551,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
       if (lane == 0 && part0 > 0 && part1 == kt.n) {  // ends a unit that part g0 began
         const int g0 = kv_part_of(total, unit0 + kKvDecCost, parts);
         p.desc[worker] = make_int4(rq.a, row0, head << 16 | rows, g0);
-        p.fin[worker] = g0;
       }
     }
 

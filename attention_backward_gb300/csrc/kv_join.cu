@@ -13,10 +13,10 @@ namespace {
 // Joins the parts of each unit that was split over workers: entry w of ``desc``
 // (first row of q of the request, first row of the unit in the request, head and
 // rows, first part) names the unit that worker w finished (a worker finishes at most one that it
-// did not begin), its parts d.w to w / stride in order; ``fin`` holds d.w, or -1
-// where there is none.  stride: workers per part (one a head in kv_decode.cu, 1
-// in kv_prompt.cu).  Every block lists the finished units (a scan of one
-// flag a worker); their rows are then spread over all warps of the launch,
+// did not begin), its parts d.w to w / stride in order; d.w is -1 where there is
+// none.  stride: workers per part (one a head in kv_decode.cu, 1
+// in kv_prompt.cu).  Every block lists the finished units (a scan of all
+// entries); their rows are then spread over all warps of the launch,
 // with as many warps a row as there are to spare.  These add fixed shares of
 // the parts in order: lanes first take the parts' (m, l) together, then D/32
 // columns each.  Latency-bound: a few parts a unit as a rule, hundreds where few
@@ -24,52 +24,53 @@ namespace {
 constexpr int kJoinWarps = 16;
 
 template <int D, int RT, bool BF16>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAttnParams p, int workers, int ctas, int stride,
+__global__ void __launch_bounds__(kJoinWarps * 32, RT > 16 ? 1 : 2) kv_join_kernel(const KvAttnParams p, int workers, int ctas, int stride,
                                                                   bool first) {
   constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
   // rows of a warp at once: one where parts are many and rows few, eight where a unit has 256
   constexpr int NR = RT > 16 ? 8 : 1, PF = 8 / NR;  // and parts in flight
-  __shared__ uint16_t list[kKvDecMaxWorkers];
+  __shared__ int4 list[kKvDecMaxWorkers];  // entries, their parts in place of the first part's number
   __shared__ int s_cnt[kJoinWarps];
   __shared__ float s_o[NR == 1 ? kJoinWarps : 1][D];
   __shared__ float2 s_ml[kJoinWarps];
   grid_dependency_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x == 0 && warp == 0) {  // the launch's error word
-    int e = kErrNone;
-    for (int i = lane; i < ctas; i += 32) e = imax(e, p.cta_err[i]);
+  int4 d[PER];  // of workers tid * PER + i
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) e = imax(e, __shfl_xor_sync(0xffffffffu, e, s));
-    if (lane == 0) *p.err = first ? e : imax(e, *p.err);
+  for (int i = 0; i < PER; ++i) {
+    d[i] = make_int4(0, 0, 0, -1);
+    if (tid * PER + i < workers) d[i] = p.desc[tid * PER + i];
   }
-  uint32_t mine = 0;  // my PER workers that finished a unit
+  const int err = tid < ctas ? p.cta_err[tid] : kErrNone;  // (no more CTAs than threads)
+  int mine = 0;
 #pragma unroll
-  for (int i = 0; i < PER; i += 4) {
-    const int w = tid * PER + i;
-    if (w < workers) {  // (the flags' space is a multiple of 16 bytes)
-      const int4 f = *reinterpret_cast<const int4*>(p.fin + w);
-      mine |= ((f.x >= 0 ? 1u : 0u) | (f.y >= 0 && w + 1 < workers ? 2u : 0u) | (f.z >= 0 && w + 2 < workers ? 4u : 0u) |
-               (f.w >= 0 && w + 3 < workers ? 8u : 0u))
-              << i;
-    }
-  }
-  int at0 = __popc(mine);
+  for (int i = 0; i < PER; ++i) mine += d[i].w >= 0 ? 1 : 0;
+  int at0 = mine;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, at0, s);
     if (lane >= s) at0 += v;
   }
   if (lane == 31) s_cnt[warp] = at0;
-  __syncthreads();
-  at0 -= __popc(mine);
+  const bool failed = __syncthreads_or(err != kErrNone);
+  at0 -= mine;
   int units = 0;
 #pragma unroll
   for (int i = 0; i < kJoinWarps; ++i) {
     if (i < warp) at0 += s_cnt[i];
     units += s_cnt[i];
   }
-  for (uint32_t m = mine; m != 0; m &= m - 1) list[at0++] = static_cast<uint16_t>(tid * PER + __ffs(m) - 1);
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (d[i].w >= 0) list[at0++] = make_int4(d[i].x, d[i].y, d[i].z, d[i].w << 16 | ((tid * PER + i) / stride - d[i].w + 1));
   __syncthreads();
+  if (blockIdx.x == 0) {  // the launch's error word: some CTA's error, if there is any
+    if (tid == 0 && first) *p.err = kErrNone;
+    if (failed) {
+      __syncthreads();
+      if (err != kErrNone) *p.err = err;
+    }
+  }
   const int items = units * (RT / NR);  // those past a unit's last row are skipped
   int shares = 1;                       // warps an item
   if (NR == 1)
@@ -77,17 +78,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
   const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
   for (int t0 = blockIdx.x * groups; t0 < items; t0 += static_cast<int>(gridDim.x) * groups) {
     const int item = t0 + group;
-    int4 d = make_int4(0, 0, 0, 0);
+    int4 u = make_int4(0, 0, 0, 0);
     int head = 0, live = 0, i0 = 0, i1 = 0;
     const int row = item % (RT / NR) * NR;  // my first row of the unit
     if (item < items) {
-      const int w = list[item / (RT / NR)];
-      d = p.desc[w];
-      head = d.z >> 16, live = d.z & 0xffff;
-      const int parts = w / stride - d.w + 1;
+      u = list[item / (RT / NR)];
+      head = u.z >> 16, live = u.z & 0xffff;
+      const int parts = u.w & 0xffff;
       i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
     }
-    auto slot_of = [&](int i) { return 2 * ((d.w + i) * stride + (stride > 1 ? head : 0)) + (i == 0 ? 1 : 0); };
+    const int g0 = u.w >> 16;  // its first part
+    auto slot_of = [&](int i) { return 2 * ((g0 + i) * stride + (stride > 1 ? head : 0)) + (i == 0 ? 1 : 0); };
     float m[NR], l[NR], acc[NR][ND];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -102,6 +103,25 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
         const int n = imin(LOOK, i1 - j);
         float2 v = make_float2(0.f, 0.f);
         if (lane / NR < n && row + lane % NR < live) v = p.part_ml[static_cast<int64_t>(slot_of(j + lane / NR)) * RT + row + lane % NR];
+        float x[PF][NR][ND];
+        auto load = [&](int i) {  // PF parts' rows from part i on
+#pragma unroll
+          for (int k = 0; k < PF; ++k) {
+            const int64_t at = static_cast<int64_t>(slot_of(j + imin(i + k, n - 1))) * RT + row;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const float* from = p.part_o + (at + imin(r, live - 1 - row)) * D + lane * ND;
+              if constexpr (ND == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(from);
+                x[k][r][0] = y.x, x[k][r][1] = y.y, x[k][r][2] = y.z, x[k][r][3] = y.w;
+              } else {
+                const float2 y = *reinterpret_cast<const float2*>(from);
+                x[k][r][0] = y.x, x[k][r][1] = y.y;
+              }
+            }
+          }
+        };
+        load(0);  // (in flight while the weights are made)
         // the rows' max over these parts (lanes of one row are NR apart), then their weights
         float mx = v.y == 0.f ? -INFINITY : v.x;
 #pragma unroll
@@ -123,22 +143,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
           if (lane % NR == r) l[r] += wl;
         }
         for (int i = 0; i < n; i += PF) {
-          float x[PF][NR][ND];
-#pragma unroll
-          for (int k = 0; k < PF; ++k) {
-            const int64_t at = static_cast<int64_t>(slot_of(j + imin(i + k, n - 1))) * RT + row;
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const float* from = p.part_o + (at + imin(r, live - 1 - row)) * D + lane * ND;
-              if constexpr (ND == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(from);
-                x[k][r][0] = y.x, x[k][r][1] = y.y, x[k][r][2] = y.z, x[k][r][3] = y.w;
-              } else {
-                const float2 y = *reinterpret_cast<const float2*>(from);
-                x[k][r][0] = y.x, x[k][r][1] = y.y;
-              }
-            }
-          }
+          if (i > 0) load(i);
 #pragma unroll
           for (int k = 0; k < PF; ++k)
 #pragma unroll
@@ -175,8 +180,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
 #pragma unroll
           for (int u = 0; u < ND; ++u) acc[r][u] = acc[r][u] * g + s_o[NR == 1 ? warp + k : 0][lane * ND + u] * f;
         }
-        const int64_t at = static_cast<int64_t>(d.x) + (d.y + row + r) / p.G;
-        const int hq = head * p.G + (d.y + row + r) % p.G;
+        const int64_t at = static_cast<int64_t>(u.x) + (u.y + row + r) / p.G;
+        const int hq = head * p.G + (u.y + row + r) % p.G;
         const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
 #pragma unroll
         for (int u = 0; u < ND; ++u) acc[r][u] *= inv;

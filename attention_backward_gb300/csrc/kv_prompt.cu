@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   const bool aligned = (smem_u32(sm) & 1023u) == 0;
   if (threadIdx.x == 0) {
     *wc.err = aligned ? kErrNone : kErrAlign;
-    p.fin[blockIdx.x] = -1;
+    p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
     *abort_flag = 0;
   }
   // ---------------------------------------------------------------- the line, and the CTA's part of it
@@ -408,7 +408,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           if (lane == 0 && part0 > 0 && part1 == kt.n) {
             const int g0 = kv_part_of(total, unit0 + COST, parts);
             p.desc[blockIdx.x] = make_int4(rq.a, u.row0, cur.head << 16 | imin(RT, rq.R - u.row0), g0);
-            p.fin[blockIdx.x] = g0;
           }
         }
         if (u.valid == 1) {
