@@ -212,7 +212,7 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   const bool prompts = kv_may_prompt(T, p.G) && mean >= kKvPrMinRows / 4;
   const bool decodes = !prompts || (num_seqs > 1 && mean < 4 * kKvPrMinRows);
   KvMaps small, large;
-  if ((decodes && !make_maps(&small, *cache, std::min<int64_t>(cache->page_size, kv_dec_keys(cache->D)))) || (prompts && !make_maps(&large, *cache, std::min<int64_t>(cache->page_size, kKvPrKeys))))
+  if ((decodes && !make_maps(&small, *cache, std::min<int64_t>(cache->page_size, kKvDecKeys))) || (prompts && !make_maps(&large, *cache, std::min<int64_t>(cache->page_size, kKvPrKeys))))
     return ATTN_ERR_INVALID_ARG;
   p.rows_min = 0, p.rows_max = prompts ? kKvPrMinRows - 1 : 0x7fffffff;
   if (decodes) {

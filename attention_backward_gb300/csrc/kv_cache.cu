@@ -169,30 +169,40 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
 
-// A warp per (run, head, tensor).  A block takes a window of TW tokens and HC
-// of the 2 HKV (tensor, head) rows; one ballot over the window's slots finds
-// the runs that start in it, and its warps share them.  A run is read twice,
-// for its largest value and for its bytes: 2 * 16 B loads a lane in flight
-// cover the latency, and the second read hits L1/L2 (a run is at most 32 KB).
-// Windows of 32 tokens for long inputs (few blocks without a run's start),
-// of 4 for short ones, where each token is usually a run of its own.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kWrThreads) kv_write_kernel(const KvWriteParams p, int TW, int HC) {
+// A team of W = page / 16 warps per (run, head, tensor): a warp holds 16 tokens
+// of the run in registers (two 16-byte loads in flight a lane and token pair, all
+// at once), the team joins their largest value in shared memory, and the bytes
+// are written from the registers, so that x is read once.  (One warp a run, with
+// a second read from L2, took 38.6 us on 33771 tokens of 4 heads of 128 in pages
+// of 64, latency-bound.)  A block takes a window of TW tokens and as many of the
+// 2 HKV (tensor, head) rows as it has teams; one ballot over the window's slots
+// finds the runs that start in it, and its teams share them.  TW grows with the
+// tokens: a window without a run's start is a block for nothing, one with many
+// keeps them waiting.  A run with skipped tokens inside, or a page's scale that is
+// no power of two, takes a second read (and true divisions) instead.
+template <int D, bool BF16, int W>
+__global__ void __launch_bounds__(kWrThreads, 4) kv_write_kernel(const KvWriteParams p, int TW) {
+  constexpr int TEAMS = kWrThreads / 32 / W;
   constexpr int LPT = D / 8;      // lanes per token: 8 values (16 bytes) a lane
-  constexpr int TPW = 32 / LPT;   // tokens per warp pass
+  constexpr int TPW = 32 / LPT;   // tokens per warp load
+  constexpr int LOADS = 16 / TPW;
+  __shared__ float s_max[2][kWrThreads / 32];
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int team = warp / W, tw = warp % W;
   const int P = 1 << p.page_log2;
   const int64_t slots = static_cast<int64_t>(p.num_blocks) << p.page_log2;
   const int t0 = blockIdx.x * TW;
   const int t = t0 + lane;
   auto valid = [&](int s) { return s >= 0 && s < slots; };
   bool begins = false;
+  const int my_slot = lane < TW && t < p.T ? p.slot_map[t] : -1;
   if (lane < TW && t < p.T) {
-    const int s = p.slot_map[t];
+    const int s = my_slot;
     if (valid(s)) {
       // the valid token before mine, at most kWrGap tokens back
       int before = -1;
+#pragma unroll 1
       for (int k = 1; k <= kWrGap && k <= t; ++k) {
         before = p.slot_map[t - k];
         if (valid(before)) break;
@@ -203,17 +213,39 @@ __global__ void __launch_bounds__(kWrThreads) kv_write_kernel(const KvWriteParam
   }
   const uint32_t runs = __ballot_sync(0xffffffffu, begins);
   const int nruns = __popc(runs);
-  const int rows = imin(HC, 2 * p.HKV - static_cast<int>(blockIdx.y) * HC);
-  for (int item = warp; item < nruns * rows; item += kWrThreads / 32) {
+  const int row0 = blockIdx.y * TEAMS, rows = imin(TEAMS, 2 * p.HKV - row0);
+  int buf = 0;
+  for (int item = team; item < nruns * rows; item += TEAMS, buf ^= 1) {
     uint32_t rest = runs;
     for (int i = item / rows; i > 0; --i) rest &= rest - 1;
-    const int row = blockIdx.y * HC + item % rows;
+    const int row = row0 + item % rows;
     const int which = row >= p.HKV ? 1 : 0, h = row - which * p.HKV;
     const int ts = t0 + __ffs(rest) - 1;
-    const int slot = p.slot_map[ts];
+    const int slot = __shfl_sync(0xffffffffu, my_slot, __ffs(rest) - 1);
     const int blk = slot >> p.page_log2, off = slot & (P - 1);
-    // tokens [ts, ts + len): up to the first valid one that begins a run itself
-    int len = 1, last = slot;  // last: slot of the valid token at ts + len - 1
+    // Tokens [ts, ts + len): up to the first valid one that begins a run itself.
+    // First the tokens in consecutive slots, all looked up at once; the loop then
+    // looks whether others of the page follow.
+    int len = 1;
+    {
+      const int most = imin(P - off, p.T - ts);
+      int ahead[W == 1 ? 1 : W / 2];
+#pragma unroll
+      for (int k = 0; k < (W == 1 ? 1 : W / 2); ++k) {
+        const int i = 1 + 32 * k + lane;
+        ahead[k] = i < most ? p.slot_map[ts + i] - i : -1;
+      }
+      bool on = true;
+#pragma unroll
+      for (int k = 0; k < (W == 1 ? 1 : W / 2); ++k) {
+        const uint32_t other = __ballot_sync(0xffffffffu, ahead[k] != slot);
+        if (on) len += other ? __ffs(other) - 1 : 32;
+        on = on && other == 0;
+      }
+      len = imin(len, most);
+    }
+    int last = slot + len - 1, count = len;  // last: slot of the valid token at ts + len - 1; count: valid ones
+#pragma unroll 1
     while ((last & (P - 1)) != P - 1) {
       const int base = ts + len;  // 32 tokens from here on
       const int s = base + lane < p.T ? p.slot_map[base + lane] : -1;
@@ -230,17 +262,17 @@ __global__ void __launch_bounds__(kWrThreads) kv_write_kernel(const KvWriteParam
         const int at = 31 - __clz(mine);
         last = __shfl_sync(0xffffffffu, s, at);
         len += at + 1;
+        count += __popc(mine);
       }
       if (e) break;
     }
+    // no token and no slot skipped: token i goes to off + i, and len <= P
+    const bool dense = count == len && last - slot == len - 1;
     const int sub = lane / LPT, d0 = (lane % LPT) * 8;
     const uint8_t* x = p.x[which] + 2 * (static_cast<int64_t>(ts) * p.sx_s[which] + h * p.sx_h[which] + d0);
     const int64_t xs = 2 * p.sx_s[which];
     float amax = 0.f;
-#pragma unroll 4
-    for (int i = sub; i < len; i += TPW) {
-      if (!valid(p.slot_map[ts + i])) continue;
-      const uint4 w = *reinterpret_cast<const uint4*>(x + i * xs);
+    auto largest = [&](const uint4& w) {
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -249,18 +281,42 @@ __global__ void __launch_bounds__(kWrThreads) kv_write_kernel(const KvWriteParam
         if (a < INFINITY) amax = fmaxf(amax, a);  // NaN compares false
         if (b < INFINITY) amax = fmaxf(amax, b);
       }
+    };
+    uint4 held[LOADS];
+    if (dense) {
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) {
+        const int i = tw * 16 + k * TPW + sub;
+        held[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < len) held[k] = *reinterpret_cast<const uint4*>(x + i * xs);
+      }
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) largest(held[k]);
+    } else {
+#pragma unroll 1
+      for (int i = tw * TPW + sub; i < len; i += W * TPW)
+        if (valid(p.slot_map[ts + i])) largest(*reinterpret_cast<const uint4*>(x + i * xs));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     float* const sp = p.scale[which] + static_cast<int64_t>(blk) * p.HKV + h;
+    const float old = off > 0 ? *sp : 0.f;
+    if constexpr (W > 1) {
+      if (lane == 0) s_max[buf][warp] = amax;
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
+#pragma unroll
+      for (int i = 0; i < W; ++i) amax = fmaxf(amax, s_max[buf][team * W + i]);
+    } else {
+      __syncwarp();  // every lane has read the old scale
+    }
     float now = scale_for(amax);
-    uint8_t* y = p.cache[which] + static_cast<int64_t>(blk) * p.sc_b[which] + h * p.sc_h[which] + d0;
+    uint8_t* const y = p.cache[which] + static_cast<int64_t>(blk) * p.sc_b[which] + h * p.sc_h[which] + d0;
     const int64_t ys = p.sc_s[which];
     if (off > 0) {
-      const float old = *sp;
       if (now > old) {  // the page's older values at the larger scale
         const float f = old / now;
-        for (int i = sub; i < off; i += TPW) {
+#pragma unroll 2
+        for (int i = tw * TPW + sub; i < off; i += W * TPW) {
           uint2* at = reinterpret_cast<uint2*>(y + i * ys);
           const uint2 w = *at;
           const uint32_t ws[2] = {w.x, w.y};
@@ -276,35 +332,52 @@ __global__ void __launch_bounds__(kWrThreads) kv_write_kernel(const KvWriteParam
         now = old;
       }
     }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *sp = now;
+    if (tw == 0 && lane == 0) *sp = now;
     const float inv = 1.f / now;
     const bool pow2 = (__float_as_uint(now) & 0x7fffffu) == 0;  // x * inv is then exact
-#pragma unroll 4
-    for (int i = sub; i < len; i += TPW) {
-      const int s = p.slot_map[ts + i];
-      if (!valid(s)) continue;
-      const uint4 w = *reinterpret_cast<const uint4*>(x + i * xs);
+    auto store = [&](int s, const uint4& w, bool exact) {
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
       uint32_t r[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 f = unpack2<BF16>(ws[e]);
-        r[e] = pow2 ? to_e4m3x2(f.x * inv, f.y * inv) : to_e4m3x2(f.x / now, f.y / now);
+        r[e] = exact ? to_e4m3x2(f.x * inv, f.y * inv) : to_e4m3x2(f.x / now, f.y / now);
       }
-      *reinterpret_cast<uint2*>(y + (s & (P - 1)) * ys) = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+      *reinterpret_cast<uint2*>(y + s * ys) = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+    };
+    if (dense && pow2) {
+#pragma unroll
+      for (int k = 0; k < LOADS; ++k) {
+        const int i = tw * 16 + k * TPW + sub;
+        if (i < len) store(off + i, held[k], true);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = tw * TPW + sub; i < len; i += W * TPW) {
+        const int s = p.slot_map[ts + i];
+        if (valid(s)) store(s & (P - 1), *reinterpret_cast<const uint4*>(x + i * xs), false);
+      }
     }
   }
 }
 
+template <int D, bool BF16, int W>
+cudaError_t launch_write_w(const KvWriteParams& p, cudaStream_t st) {
+  constexpr int TEAMS = kWrThreads / 32 / W;
+  const int TW = imax(1, imin(32, p.T / 512));
+  const dim3 grid((p.T + TW - 1) / TW, (2 * p.HKV + TEAMS - 1) / TEAMS);
+  kv_write_kernel<D, BF16, W><<<grid, kWrThreads, 0, st>>>(p, TW);
+  return cudaGetLastError();
+}
+
 template <int D, bool BF16>
 cudaError_t launch_write_t(const KvWriteParams& p, cudaStream_t st) {
-  const bool small = p.T <= 4096;
-  const int TW = small ? 4 : 32;
-  const int HC = imin(2 * p.HKV, small ? 2 : 8);
-  const dim3 grid((p.T + TW - 1) / TW, (2 * p.HKV + HC - 1) / HC);
-  kv_write_kernel<D, BF16><<<grid, kWrThreads, 0, st>>>(p, TW, HC);
-  return cudaGetLastError();
+  switch (p.page_log2) {
+    case 4: return launch_write_w<D, BF16, 1>(p, st);
+    case 5: return launch_write_w<D, BF16, 2>(p, st);
+    case 6: return launch_write_w<D, BF16, 4>(p, st);
+    default: return launch_write_w<D, BF16, 8>(p, st);
+  }
 }
 
 }  // namespace

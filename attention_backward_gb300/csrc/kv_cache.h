@@ -81,9 +81,8 @@ struct KvMaps {
 // prompt kernel, the others to the decode kernel.
 constexpr int kKvPrMinRows = 65;
 
-// Decode kernel: keys per tile (4 KB of K and of V), and what starting a unit
-// costs in tiles.
-constexpr int kv_dec_keys(int64_t D) { return D == 64 ? 64 : 32; }
+// Decode kernel: keys per tile, and what starting a unit costs in tiles.
+constexpr int kKvDecKeys = 32;
 constexpr int kKvDecCost = 2;
 // Most partial rows of a launch (2 slots a worker, 8 or 16 rows a slot) and most
 // workers: these size the workspace and bound the grid.

@@ -9,8 +9,8 @@
 // only when it grows by more than 2^8).  Bound by the bytes of K and V: 2 D
 // bytes and 4 D G flops a key.
 //
-// Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 2 KB
-// of K and of V (16 or 32 keys), over persistent warps.  Every KV head has the same line, so worker
+// Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 32
+// keys, over persistent warps.  Every KV head has the same line, so worker
 // (warp) w takes head w % HKV and part w / HKV of its line: the warps of a CTA
 // walk the same pages of neighbouring heads together, which reads pages stored
 // token by token in rows of several heads (one head at a time, 128 B out of
@@ -62,8 +62,8 @@ constexpr int kMinWork = 4;
 template <int D, int NB>
 struct DecCfg {
   static constexpr int RT = 8 * NB;                  // rows of a unit
-  static constexpr int KT = kv_dec_keys(D);          // keys of a tile
-  static constexpr int CTAS = 2;                     // resident per SM
+  static constexpr int KT = kKvDecKeys;             // keys of a tile
+  static constexpr int CTAS = D == 64 ? 3 : 2;       // resident per SM
   static constexpr int TILE = KT * D;                // bytes of K, or of V, of a tile
   static constexpr int WARP = kStages * 2 * TILE;    // a warp's ring
   static constexpr int OFF_BAR = kWarps * WARP;
