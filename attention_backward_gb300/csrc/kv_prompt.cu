@@ -214,6 +214,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
 
   grid_dependency_wait();
   const WaitCtx wc{abort_flag, p.cta_err + blockIdx.x, p.timeout_ns};
+  // a unit lasts as long as its keys do: waits for one to begin or to be taken
+  // have a limit of their own (any wait that runs out ends the others too)
+  const WaitCtx wu{abort_flag, p.cta_err + blockIdx.x, 64 * p.timeout_ns};
   const bool aligned = (smem_u32(sm) & 1023u) == 0;
   if (threadIdx.x == 0) {
     *wc.err = aligned ? kErrNone : kErrAlign;
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
   auto next_unit = [&](uint32_t uc, bool* okp) -> PrUnit {
     const uint32_t slot = uc & 1;
     PrUnit u{};
-    if (!(*okp = mbar_wait_warp(&bars[UNIT_FULL0 + slot], (uc >> 1) & 1, wc, kErrWaitTile))) return u;
+    if (!(*okp = mbar_wait_warp(&bars[UNIT_FULL0 + slot], (uc >> 1) & 1, wu, kErrWaitTile))) return u;
     u = units[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[UNIT_EMPTY0 + slot]);
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           u.vref = top < 0x1p-126f ? 0.f : top;
         }
         const uint32_t slot = uc & 1;
-        if (uc >= 2 && !mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wc, kErrWaitTile)) break;
+        if (uc >= 2 && !mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wu, kErrWaitTile)) break;
         if (lane == 0) {
           units[slot] = u;
           mbar_arrive(&bars[UNIT_FULL0 + slot]);

@@ -131,9 +131,16 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * table_stride;  cu_seqlens [num_seqs + 1], kv_lens [num_seqs] : int32, device
  * memory;  HQ a multiple of HKV, query head h reads KV head h / (HQ / HKV);
  * sm_scale finite and > 0.
- * The products run on 16-bit operands with f32 sums: e4m3 values are exact in
- * fp16, each q row is brought into fp16's range by a power of two of its own,
- * scales are applied to the f32 scores and to P before its rounding to fp16.
+ * The products run on fp16 operands with f32 sums, for either dtype of q: e4m3
+ * values are exact in fp16, each q row is brought into fp16's range by a power
+ * of two of its own, K scales multiply the f32 scores, and P is rounded to fp16.
+ * V scales enter relative to the largest one met: for requests of few rows
+ * (queries * heads of a group) they multiply P before its rounding, for many
+ * rows they multiply V, which is exact for powers of two (as
+ * attn_kv_cache_write makes them) and rounds V to fp16 once for others.
+ * Requests of few rows are served by one kernel and those of many by another,
+ * both queued where the batch may hold both; rows whose keys were split over
+ * CTAs are joined by a last launch.  No length is needed on the host.
  *   workspace : attn_fwd_kv_cache_workspace_size(T, HQ, HKV, D) bytes, 16-byte
  *   aligned, owned by the caller until the work is done; its contents on entry
  *   do not matter; attn_bwd_check_error reports a kernel whose bounded wait ran

@@ -332,8 +332,9 @@ def check_attend(prob, name, causal=True, window=-1, scale=None, v_rounded=False
     assert np.array_equal(np.isneginf(glse), none) and (got[none.T] == 0).all()
     e = 2 * (D * 2.0 ** -23 * dots + 2.0 ** -21)
     some = live & ~none
-    tl = e + 2.0 ** -23 * np.abs(lse) + 2.0 ** -20
-    assert (np.abs(glse - lse)[some] <= tl[some]).all(), (np.abs(glse - lse)[some] / tl[some]).max()
+    tl = (e + 2.0 ** -23 * np.abs(lse) + 2.0 ** -20)[some]
+    el = np.abs(glse[some] - lse[some])
+    assert (el <= tl).all(), (el / tl).max()
     half = 2.0 ** -11 if name == "f16" else 2.0 ** -8
     tiny = 2.0 ** -25 if name == "f16" else 0.0  # half of fp16's smallest step
     tol = half * np.abs(o) + (2.0 ** -11 * (1 + v_rounded) + e.T[..., None]) * mag * (1 + half) + (2.0 ** -24 * seen * vmax).T[..., None] + tiny
@@ -355,6 +356,24 @@ DECODE = [
     ([(2, 300), (1, 2), (5, 5), (3, 1000), (7, 90)], 8, 8, 128, 32),
     ([(3, 700), (6, 129), (1, 64)], 28, 4, 64, 64),
 ]
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 32), (128, 16), (128, 64)])
+def test_attend_with_more_heads_than_workers(D, page):
+    """2100 KV heads: more than the warps of a launch, so each serves several."""
+    check_attend(attend_problem("f16", [(1, 70), (0, 3), (2, 33)], 2100, 2100, D, page, 30), "f16")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_attend_every_page_size(D, page):
+    """Lengths around tiles, blocks and pages, for few rows and for many."""
+    few = [(1, L) for L in (15, 16, 17, 31, 33, 63, 65, 127, 128, 129, 255, 257)]
+    check_attend(attend_problem("bf16", few, 3, 1, D, page, 31), "bf16")
+    check_attend(attend_problem("bf16", few, 3, 1, D, page, 31), "bf16", window=40)
+    many = [(70, L) for L in (70, 127, 128, 129, 200, 257)]
+    check_attend(attend_problem("bf16", many, 3, 1, D, page, 32), "bf16")
+    check_attend(attend_problem("bf16", many, 3, 1, D, page, 32), "bf16", window=40)
 
 
 @pytest.mark.parametrize("name", ["f16", "bf16"])
