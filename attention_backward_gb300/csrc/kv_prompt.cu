@@ -679,6 +679,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
         tc_fence_after();
       }
+      uint32_t sr[HK];  // my row's scores (in flight while the scales are looked at)
+      tmem_ld32(tS, sr);
+      tmem_ld32(tS + 32, sr + 32);
       const float* const sc = k_scales + ((bc0 + (jh >> 1) - u.j0) % kScaleRing) * kGroups + h2 * 4;
       const float4 sa = *reinterpret_cast<const float4*>(sc);
       float f[4] = {sa.x, sa.y, sa.z, sa.w};
@@ -698,16 +701,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       // hold as well as P up to 1.  Past that (or at a row's first key), the max
       // is found and the block computed again (its scores are still there: P is
       // stored last).
-      auto load_scores = [&](int h, uint32_t* sr) {  // 32 scores of the row, -inf where the key is not seen
-        tmem_ld32(tS + h * 32, sr);
-        tmem_ld_wait();
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (h * 32 + k < v_lo || h * 32 + k >= v_hi || (no_page >> (h * 2 + k / 16) & 1u))
-              sr[k] = __float_as_uint(-INFINITY);
-        }
-      };
       const bool first = m_used == -INFINITY;
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool need = first;  // (row by row, so that no row's result depends on another's)
@@ -715,19 +708,20 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         uint32_t pw[HK / 2];
         const float msub = first ? 0.f : m_used;
         const float2 nm2 = make_float2(-msub, -msub);
+        tmem_ld_wait();
+        if (masked) {
 #pragma unroll
-        for (int h = 0; h < HK / 32; ++h) {
-          uint32_t sr[32];
-          load_scores(h, sr);
+          for (int k = 0; k < HK; ++k)
+            if (k < v_lo || k >= v_hi || (no_page >> (k / 16) & 1u)) sr[k] = __float_as_uint(-INFINITY);
+        }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float fg = f[h * 2 + e / 8];
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
-                                        make_float2(fg, fg), nm2);
-            const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-            sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
-            pw[h * 16 + e] = pack2<false>(pp.x, pp.y);
-          }
+        for (int e = 0; e < HK / 2; ++e) {
+          const float fg = f[e / 8];
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+                                      make_float2(fg, fg), nm2);
+          const float2 pp = make_float2(ex2(y.x), ex2(y.y));
+          sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
+          pw[e] = pack2<false>(pp.x, pp.y);
         }
         need |= !((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y) <= kMostSum);
         if (!__any_sync(0xffffffffu, need)) {
@@ -736,16 +730,26 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         }
       }
       if (__any_sync(0xffffffffu, need)) {
+        auto load_scores = [&](int h, uint32_t* x) {  // 32 scores of the row, -inf where the key is not seen
+          tmem_ld32(tS + h * 32, x);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (h * 32 + k < v_lo || h * 32 + k >= v_hi || (no_page >> (h * 2 + k / 16) & 1u))
+                x[k] = __float_as_uint(-INFINITY);
+          }
+        };
         float m_new = m_used;
 #pragma unroll 1
         for (int h = 0; h < HK / 32; ++h) {
-          uint32_t sr[32];
-          load_scores(h, sr);
+          uint32_t x[32];
+          load_scores(h, x);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             float top = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(sr[g * 16 + k]));
+            for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(x[g * 16 + k]));
             const float fg = h == 0 ? f[g] : f[2 + g];
             m_new = fmaxf(m_new, top * fg);
           }
@@ -773,13 +777,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int h = 0; h < HK / 32; ++h) {
-          uint32_t sr[32], pw[16];
-          load_scores(h, sr);
+          uint32_t x[32], pw[16];
+          load_scores(h, x);
           const float fa = h == 0 ? f[0] : f[2], fb = h == 0 ? f[1] : f[3];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float fg = e < 8 ? fa : fb;
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
                                         make_float2(fg, fg), make_float2(-msub, -msub));
             const float2 pp = make_float2(ex2(y.x), ex2(y.y));
             sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
