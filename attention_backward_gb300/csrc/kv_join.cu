@@ -24,11 +24,13 @@ namespace {
 constexpr int kJoinWarps = 16;
 
 template <int D, int RT, bool BF16>
-__global__ void __launch_bounds__(kJoinWarps * 32, RT > 16 ? 1 : 2) kv_join_kernel(const KvAttnParams p, int workers, int ctas, int stride,
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAttnParams p, int workers, int ctas, int stride,
                                                                   bool first) {
   constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
-  // rows of a warp at once: one where parts are many and rows few, eight where a unit has 256
-  constexpr int NR = RT > 16 ? 8 : 1, PF = 8 / NR;  // and parts in flight
+  // rows of a warp at once, and parts in flight: parts may be many where units are
+  // of few rows, and are two or three as a rule where they are of 256 (there, eight
+  // rows at once took 18 us where two take 15)
+  constexpr int NR = RT > 16 ? 2 : 1, PF = RT > 16 ? 2 : 8;
   __shared__ int4 list[kKvDecMaxWorkers];  // entries, their parts in place of the first part's number
   __shared__ int s_cnt[kJoinWarps];
   __shared__ float s_o[NR == 1 ? kJoinWarps : 1][D];
