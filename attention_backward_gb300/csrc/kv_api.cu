@@ -15,6 +15,9 @@ namespace {
 using namespace ab;
 
 constexpr int64_t kMax32 = int64_t(1) << 31;
+// Rows, keys and tokens stay this far below it: the kernels count them in 32 bits,
+// up to a few tiles past the last one.
+constexpr int64_t kMaxCount = kMax32 - 4096;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -138,7 +141,7 @@ attn_status_t attn_kv_cache_write(const void* k, attn_strides_t sk, const void* 
                                   const attn_kv_cache_t* cache, void* stream) {
   if (const attn_status_t st = check_cache(cache); st != ATTN_OK) return st;
   if (T < 0) return ATTN_ERR_INVALID_ARG;
-  if (!dtype_ok(dtype) || T >= kMax32) return ATTN_ERR_UNSUPPORTED;
+  if (!dtype_ok(dtype) || T > kMaxCount) return ATTN_ERR_UNSUPPORTED;
   if (T == 0) return ATTN_OK;
   if (!k || !v || !slot_map) return ATTN_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4)) return ATTN_ERR_INVALID_ARG;
@@ -158,7 +161,7 @@ attn_status_t attn_kv_cache_write(const void* k, attn_strides_t sk, const void* 
 }
 
 size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int64_t HKV, int64_t D) {
-  if (T < 0 || HQ < 1 || HKV < 1 || HQ % HKV || (D != 64 && D != 128) || T >= kMax32 / HQ) return 0;
+  if (T < 0 || HQ < 1 || HKV < 1 || HQ % HKV || (D != 64 && D != 128) || T > kMaxCount / HQ) return 0;
   return static_cast<size_t>(kv_may_prompt(T, HQ / HKV) ? kv_ws_prompt(D).total : kv_ws_decode(D).total);
 }
 
@@ -173,7 +176,7 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
     return ATTN_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return ATTN_ERR_INVALID_ARG;
   if (window_left == 0 || window_left < -1) return ATTN_ERR_INVALID_ARG;
-  if (!dtype_ok(dtype) || T >= kMax32 / HQ || num_seqs > (1 << 20) || max_blocks >= kMax32 / cache->page_size)
+  if (!dtype_ok(dtype) || T > kMaxCount / HQ || num_seqs > (1 << 20) || max_blocks > kMaxCount / cache->page_size)
     return ATTN_ERR_UNSUPPORTED;
   if (T == 0) return ATTN_OK;
   if (!q || !o || !lse || !block_table || !cu_seqlens || !kv_lens || !workspace) return ATTN_ERR_INVALID_ARG;
@@ -212,7 +215,8 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
   const bool prompts = kv_may_prompt(T, p.G) && mean >= kKvPrMinRows / 4;
   const bool decodes = !prompts || (num_seqs > 1 && mean < 4 * kKvPrMinRows);
   KvMaps small, large;
-  if ((decodes && !make_maps(&small, *cache, std::min<int64_t>(cache->page_size, kKvDecKeys))) || (prompts && !make_maps(&large, *cache, std::min<int64_t>(cache->page_size, kKvPrKeys))))
+  if ((decodes && !make_maps(&small, *cache, std::min<int64_t>(cache->page_size, kKvDecKeys))) ||
+      (prompts && !make_maps(&large, *cache, std::min<int64_t>(cache->page_size, kKvPrKeys))))
     return ATTN_ERR_INVALID_ARG;
   p.rows_min = 0, p.rows_max = prompts ? kKvPrMinRows - 1 : 0x7fffffff;
   if (decodes) {

@@ -33,12 +33,12 @@
 //
 // Layout: no operand goes through a transpose in shared memory.  The sum over d
 // may run in any order, so the thread that holds k columns 2c, 2c + 1 of key n
-// takes 16 consecutive bytes of the key (its own cp.async of 16 bytes and one
-// 16-byte read back), and Q is permuted to match.  Likewise the rows of O^T:
-// thread n takes bytes [n D/8, (n + 1) D/8) of its four keys, and two keys'
-// bytes are paired by one byte permute before the conversion.  P^T turns with
-// one movmatrix for 8 keys.  Each thread reads back only what it copied itself,
-// so the ring needs no barrier.
+// takes 16 consecutive bytes of the key (one read of the swizzled tile), and Q
+// is permuted to match.  Likewise the rows of O^T: thread n takes bytes
+// [n D/8, (n + 1) D/8) of its four keys, and two keys' bytes are paired by one
+// byte permute before the conversion.  P^T turns with one movmatrix for 8 keys.
+// The ring is the warp's own: its first lane queues a tile's copies (a box a
+// page) on the slot's barrier once the warp has read the slot.
 #include <cuda_fp16.h>
 
 #include "cvt.cuh"
@@ -588,7 +588,7 @@ cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaSt
 // fit them, of 16 otherwise; either serves any number.
 template <int D, bool BF16>
 cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
-  const int64_t mean = (p.T + p.N - 1) / p.N;
+  const int64_t mean = (static_cast<int64_t>(p.T) + p.N - 1) / p.N;
   return mean * p.G <= 8 ? launch_nb<D, 1, BF16>(p, maps, sms, st) : launch_nb<D, 2, BF16>(p, maps, sms, st);
 }
 

@@ -97,12 +97,13 @@ ATTN_BWD_API attn_status_t attn_kv_block_tables(const int32_t* ctx_lens, const i
  * e4m3() rounds to nearest, ties to even; infinities become +-448, NaN stays.
  * With powers of two, a page's older values keep every bit through a raise
  * unless they drop below the e4m3 normal range of the new scale.  Bytes of the
- * page that the run skips or that lie behind it are left as they were.  One call's runs go to different
- * pages (as slots of attn_kv_block_tables do): where two runs of a call share
- * a page, that page's contents are unspecified, and nothing else is touched.
+ * page that the run skips or that lie behind it are left as they were.  One
+ * call's runs go to different pages (as slots of attn_kv_block_tables do):
+ * where two runs of a call share a page, that page's contents are unspecified,
+ * and nothing else is touched.
  *   k, v : [1,T,HKV,D] 16-bit (strides b unused);  slot_map : int32 [T].
  * T = 0 queues nothing.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED
- * (dtype, head dim, page size, sizes past 2^31), ATTN_ERR_LAUNCH. */
+ * (dtype, head dim, page size, T above 2^31 - 4096), ATTN_ERR_LAUNCH. */
 ATTN_BWD_API attn_status_t attn_kv_cache_write(const void* k, attn_strides_t sk, const void* v, attn_strides_t sv,
                                                const int32_t* slot_map, int64_t T, attn_dtype_t dtype,
                                                const attn_kv_cache_t* cache, void* stream);
@@ -125,7 +126,8 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * table entry lies outside [0, num_blocks) are not visible.  A query that sees
  * no key gets O = 0 and LSE = -inf.  Cached bytes and scales that no query of
  * the request sees are never used as operands: they may hold anything, NaN
- * included.  Rows of q past cu_seqlens[num_seqs] are not written.
+ * included.  (A NaN that one query of a request sees may make others of it NaN,
+ * as 0 * NaN does.)  Rows of q past cu_seqlens[num_seqs] are not written.
  * q, o : [1,T,HQ,D] 16-bit (strides b unused);  lse : f32, lse[h*slse.h +
  * t*slse.s];  block_table : int32 [num_seqs, max_blocks], row stride
  * table_stride;  cu_seqlens [num_seqs + 1], kv_lens [num_seqs] : int32, device
@@ -140,13 +142,17 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * attn_kv_cache_write makes them) and rounds V to fp16 once for others.
  * Requests of few rows are served by one kernel and those of many by another,
  * both queued where the batch may hold both; rows whose keys were split over
- * CTAs are joined by a last launch.  No length is needed on the host.
+ * CTAs are joined by a last launch.  No length is needed on the host.  Pages may
+ * be listed by several requests, and twice by one.  o, lse and the workspace
+ * overlap no input and not each other.
  *   workspace : attn_fwd_kv_cache_workspace_size(T, HQ, HKV, D) bytes, 16-byte
  *   aligned, owned by the caller until the work is done; its contents on entry
  *   do not matter; attn_bwd_check_error reports a kernel whose bounded wait ran
  *   out.
- * T = 0 queues nothing.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED,
- * ATTN_ERR_WORKSPACE before anything is queued; ATTN_ERR_LAUNCH. */
+ * T = 0 queues nothing.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED
+ * (dtype, head dim, page size, T * HQ or max_blocks * page_size above
+ * 2^31 - 4096, more than 2^20 requests), ATTN_ERR_WORKSPACE before anything is
+ * queued; ATTN_ERR_LAUNCH. */
 ATTN_BWD_API attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int64_t HQ,
                                              attn_dtype_t dtype, float sm_scale, const attn_kv_cache_t* cache,
                                              const int32_t* block_table, int64_t table_stride, int64_t max_blocks,

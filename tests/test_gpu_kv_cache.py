@@ -485,6 +485,16 @@ def test_attend_past_the_table():
     check_attend((q, kc, vc, ks, vs, table[:, :4].copy(), cu, kv + [2 ** 31 - 65, 0]), "f16", causal=False)
 
 
+@pytest.mark.parametrize("m", [1, 40])
+def test_attend_pages_held_twice(m):
+    """A prefix that two requests share, and a page twice in one row."""
+    q, kc, vc, ks, vs, table, cu, kv = attend_problem("bf16", [(m, 200), (m + 1, 180), (m, 300)], 8, 2, 64, 32, 30)
+    table[1, :4] = table[0, :4]
+    table[2, 5] = table[2, 2]
+    table[2, 7] = table[1, 1]
+    check_attend((q, kc, vc, ks, vs, table, cu, kv), "bf16")
+
+
 def test_attend_of_other_layouts_and_scales():
     prob = attend_problem("bf16", [(1, 700), (3, 90)], 8, 2, 128, 64, 11, size=0.1)
     check_attend(prob, "bf16", scale=0.3, heads_first=True)
@@ -698,6 +708,54 @@ def test_two_streams_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for o, lse in got:
         assert np.array_equal(o[0].double().cpu().numpy(), ref) and np.array_equal(lse[0].double().cpu().numpy(), rl)
+
+
+def test_prompt_graphs_side_by_side():
+    """Mixed batches captured with a workspace each, replayed at the same time
+    on two streams and again with other lengths in the same buffers."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    probs = [attend_problem("bf16", lens, 16, 2, 128, 64, 31 + i)
+             for i, lens in enumerate([[(300, 900), (1, 700), (3, 64)], [(2, 500), (1, 900), (301, 400)]])]
+    refs = [run_attend(p, "bf16") for p in probs]
+    assert probs[0][0].shape == probs[1][0].shape
+    sides, graphs, held = [torch.cuda.Stream() for _ in range(2)], [], []
+    for (q, kc, vc, ks, vs, table, cu, kv), st in zip(probs, sides):
+        args = [cuda(q, torch.bfloat16)[None], fp8(kc), fp8(vc), cuda(ks.astype(np.float32)),
+                cuda(vs.astype(np.float32)), i32(table), i32(cu), i32(kv)]
+        ws = torch.empty(ab.kv_cache_workspace_size(q.shape[0], 16, 2, 128), dtype=torch.uint8, device="cuda")
+        out = (torch.empty_like(args[0]), torch.empty(1, 16, q.shape[0], device="cuda"))
+        ab.forward_kv_cache(*args, workspace=ws, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            ab.forward_kv_cache(*args, workspace=ws, out=out)
+        graphs.append(g)
+        held.append((args, ws, out))
+    for _ in range(5):
+        for _, _, out in held:
+            out[0].fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, sides):
+            with torch.cuda.stream(st):
+                g.replay()
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, _, (o, lse)), (ref, rl) in zip(held, refs):
+            assert np.array_equal(o[0].double().cpu().numpy(), ref)
+            assert np.array_equal(lse[0].double().cpu().numpy(), rl)
+    # the second batch's row ranges and lengths in the first graph's buffers
+    (args, ws, out), (_, kc, vc, ks, vs, table, cu, kv) = held[0], probs[0]
+    cu, kv = probs[1][6], np.array([400, 650, 64])
+    args[6].copy_(i32(cu)), args[7].copy_(i32(kv))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    ref, rl = run_attend((probs[0][0], kc, vc, ks, vs, table, cu, kv), "bf16")
+    assert np.array_equal(out[0][0].double().cpu().numpy(), ref)
+    assert np.array_equal(out[1][0].double().cpu().numpy(), rl)
+    check_attend((probs[0][0], kc, vc, ks, vs, table, cu, kv), "bf16")
 
 
 def test_no_tokens():

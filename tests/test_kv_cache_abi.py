@@ -127,6 +127,17 @@ def test_one_byte_less_workspace_is_refused(ab):
         assert ab.kv_cache_workspace_size(*bad) == 0
 
 
+def test_counts_just_below_two_to_the_31_are_refused(ab):
+    """Counts that 32 bits hold, but not with a tile more: refused before anything is read."""
+    big = (1 << 31) - 4095
+    assert call(ab, "attn_kv_cache_write", write_args(ab), T=big) == UNSUPPORTED
+    assert call(ab, "attn_kv_cache_write", write_args(ab), T=(1 << 31) - 1) == UNSUPPORTED
+    assert call(ab, "attn_fwd_kv_cache", attend_args(ab), T=big // 8 + 1) == UNSUPPORTED
+    assert call(ab, "attn_fwd_kv_cache", attend_args(ab), width=(1 << 27) - 1, stride=1 << 27) == UNSUPPORTED
+    assert ab.kv_cache_workspace_size(big, 1, 1, 128) == 0
+    assert ab.kv_cache_workspace_size(big - 1, 1, 1, 128) > 0
+
+
 def test_binding_refuses_host_tensors(ab):
     import torch
 
