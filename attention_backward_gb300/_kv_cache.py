@@ -193,7 +193,7 @@ def kv_block_tables(ctx_lens, new_lens, block_table, free_blocks, page_size: int
             if max_tokens < 0:
                 raise AttnBwdError("max_tokens must not be negative")
             buf = torch.empty(sum(sizes), dtype=_I32, device=device)  # one buffer for the five outputs
-            plan = KvPlan(*buf.split(sizes))
+            plan = KvPlan(*torch.unsafe_split_with_sizes(buf, sizes))  # (split()'s views would cost twice that)
             at, ptrs = buf.data_ptr(), []
             for k in sizes:
                 ptrs.append(at)

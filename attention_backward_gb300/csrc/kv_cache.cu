@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include "cvt.cuh"
+#include "kernels.h"
 #include "kv_cache.h"
 #include "sm103.cuh"
 
@@ -47,6 +48,7 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesPa
   __shared__ int64_t s_tok[kTabThreads + 1], s_pg[kTabThreads + 1];
   __shared__ int64_t w_tok[kTabThreads / 32], w_pg[kTabThreads / 32], w_wide[kTabThreads / 32];
   grid_dependency_wait();
+  grid_dependents_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = (p.N + kTabThreads - 1) / kTabThreads;
   const int64_t start = p.free_start ? imax(*p.free_start, 0) : 0;
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kWrThreads, 4) kv_write_kernel(const KvWritePa
   constexpr int LOADS = 16 / TPW;
   __shared__ float s_max[2][kWrThreads / 32];
   grid_dependency_wait();
+  grid_dependents_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int team = warp / W, tw = warp % W;
   const int P = 1 << p.page_log2;
@@ -366,8 +369,7 @@ cudaError_t launch_write_w(const KvWriteParams& p, cudaStream_t st) {
   constexpr int TEAMS = kWrThreads / 32 / W;
   const int TW = imax(1, imin(32, p.T / 512));
   const dim3 grid((p.T + TW - 1) / TW, (2 * p.HKV + TEAMS - 1) / TEAMS);
-  kv_write_kernel<D, BF16, W><<<grid, kWrThreads, 0, st>>>(p, TW);
-  return cudaGetLastError();
+  return launch_after_previous(kv_write_kernel<D, BF16, W>, grid, kWrThreads, 0, st, p, TW);
 }
 
 template <int D, bool BF16>
@@ -383,8 +385,7 @@ cudaError_t launch_write_t(const KvWriteParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st) {
-  kv_tables_kernel<<<grid, kTabThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_after_previous(kv_tables_kernel, grid, kTabThreads, 0, st, p);
 }
 
 cudaError_t launch_kv_write(const KvWriteParams& p, bool bf16, cudaStream_t st) {
