@@ -219,14 +219,18 @@ attn_status_t attn_fwd_kv_cache(const void* q, attn_strides_t sq, int64_t T, int
       (prompts && !make_maps(&large, *cache, std::min<int64_t>(cache->page_size, kKvPrKeys))))
     return ATTN_ERR_INVALID_ARG;
   p.rows_min = 0, p.rows_max = prompts ? kKvPrMinRows - 1 : 0x7fffffff;
+  KvJoinPart few{}, many{};
   if (decodes) {
     kv_place(&p, kv_ws_decode(cache->D), ws);
-    if (const cudaError_t e = launch_kv_decode(p, small, bf16, sms, st); e != cudaSuccess) return launch_status(e);
+    if (const cudaError_t e = launch_kv_decode(p, small, bf16, sms, &few, st); e != cudaSuccess) return launch_status(e);
   }
-  if (!prompts) return ATTN_OK;
-  p.rows_min = decodes ? kKvPrMinRows : 0, p.rows_max = 0x7fffffff;
-  kv_place(&p, kv_ws_prompt(cache->D), ws);
-  return launch_status(launch_kv_prompt(p, large, bf16, sms, !decodes, st));
+  if (prompts) {
+    p.rows_min = decodes ? kKvPrMinRows : 0, p.rows_max = 0x7fffffff;
+    kv_place(&p, kv_ws_prompt(cache->D), ws);
+    if (const cudaError_t e = launch_kv_prompt(p, large, bf16, sms, &many, st); e != cudaSuccess)
+      return launch_status(e);
+  }
+  return launch_status(launch_kv_join(p, bf16, few, many, sms, st));
 }
 
 }  // extern "C"

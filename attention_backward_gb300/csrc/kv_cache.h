@@ -100,11 +100,28 @@ constexpr int kKvPrMaxCtas = 160;
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, int grid, cudaStream_t st);
 cudaError_t launch_kv_write(const KvWriteParams& p, bool bf16, cudaStream_t st);
-cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, cudaStream_t st);
-cudaError_t launch_kv_prompt(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, bool first, cudaStream_t st);
-// Joins split rows: units of rt rows, ``workers`` workers in ``ctas`` CTAs, ``stride`` of them to a part; ``first``:
-// the error word is written, not added to.
-cudaError_t launch_kv_join(const KvAttnParams& p, bool bf16, int rt, int workers, int ctas, int stride, bool first,
-                           int grid, cudaStream_t st);
+// What a kernel leaves to be joined: an error word per CTA, a descriptor per
+// worker (``stride`` workers to a part of the line), partial rows of units of
+// ``rows`` rows.  workers = 0: nothing.
+struct KvJoinPart {
+  const int* cta_err;
+  const int4* desc;
+  const float2* part_ml;
+  const float* part_o;
+  int workers, ctas, stride, rows;
+};
+inline KvJoinPart kv_join_part(const KvAttnParams& p, int workers, int ctas, int stride, int rows) {
+  return {p.cta_err, p.desc, p.part_ml, p.part_o, workers, ctas, stride, rows};
+}
+
+// Both fill ``left`` with what launch_kv_join has to finish.
+cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, KvJoinPart* left,
+                             cudaStream_t st);
+cudaError_t launch_kv_prompt(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, KvJoinPart* left,
+                             cudaStream_t st);
+// Joins the rows that the kernels of few and of many rows split, and writes the
+// call's error word.
+cudaError_t launch_kv_join(const KvAttnParams& p, bool bf16, const KvJoinPart& few, const KvJoinPart& many, int sms,
+                           cudaStream_t st);
 
 }  // namespace ab

@@ -574,31 +574,31 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
 }
 
 template <int D, int NB, bool BF16>
-cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
+cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, KvJoinPart* left, cudaStream_t st) {
   using C = DecCfg<D, NB>;
   auto kern = kv_decode_kernel<D, NB, BF16>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem_once(kern, C::SMEM, &done);
   if (e != cudaSuccess) return e;
   const int grid = imin(sms * C::CTAS, kKvDecMaxRows / (2 * kWarps * C::RT));
-  e = launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);
-  if (e != cudaSuccess) return e;
-  return launch_kv_join(p, BF16, C::RT, grid * kWarps, grid, p.HKV, true, 2 * sms, st);
+  *left = kv_join_part(p, grid * kWarps, grid, p.HKV, C::RT);
+  return launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);
 }
 
 // Units of 8 rows where a request's rows (by the mean number of its queries)
 // fit them, of 16 otherwise; either serves any number.
 template <int D, bool BF16>
-cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int sms, cudaStream_t st) {
+cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int sms, KvJoinPart* left, cudaStream_t st) {
   const int64_t mean = (static_cast<int64_t>(p.T) + p.N - 1) / p.N;
-  return mean * p.G <= 8 ? launch_nb<D, 1, BF16>(p, maps, sms, st) : launch_nb<D, 2, BF16>(p, maps, sms, st);
+  return mean * p.G <= 8 ? launch_nb<D, 1, BF16>(p, maps, sms, left, st) : launch_nb<D, 2, BF16>(p, maps, sms, left, st);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, cudaStream_t st) {
-  if (p.D == 64) return bf16 ? launch_t<64, true>(p, maps, sms, st) : launch_t<64, false>(p, maps, sms, st);
-  return bf16 ? launch_t<128, true>(p, maps, sms, st) : launch_t<128, false>(p, maps, sms, st);
+cudaError_t launch_kv_decode(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, KvJoinPart* left,
+                             cudaStream_t st) {
+  if (p.D == 64) return bf16 ? launch_t<64, true>(p, maps, sms, left, st) : launch_t<64, false>(p, maps, sms, left, st);
+  return bf16 ? launch_t<128, true>(p, maps, sms, left, st) : launch_t<128, false>(p, maps, sms, left, st);
 }
 
 }  // namespace ab

@@ -24,26 +24,21 @@ namespace {
 constexpr int kJoinWarps = 16;
 
 template <int D, int RT, bool BF16>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAttnParams p, int workers, int ctas, int stride,
-                                                                  bool first) {
+__device__ __forceinline__ void join_units(const KvAttnParams& p, const KvJoinPart& from, int block, int blocks,
+                                           int4* list, float (*s_o)[D], float2* s_ml, int* s_cnt) {
   constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
   // rows of a warp at once, and parts in flight: parts may be many where units are
   // of few rows, and are two or three as a rule where they are of 256 (there, eight
   // rows at once took 18 us where two take 15)
   constexpr int NR = RT > 16 ? 2 : 1, PF = RT > 16 ? 2 : 8;
-  __shared__ int4 list[kKvDecMaxWorkers];  // entries, their parts in place of the first part's number
-  __shared__ int s_cnt[kJoinWarps];
-  __shared__ float s_o[NR == 1 ? kJoinWarps : 1][D];
-  __shared__ float2 s_ml[kJoinWarps];
-  grid_dependency_wait();
+  const int workers = from.workers, stride = from.stride;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int4 d[PER];  // of workers tid * PER + i
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     d[i] = make_int4(0, 0, 0, -1);
-    if (tid * PER + i < workers) d[i] = p.desc[tid * PER + i];
+    if (tid * PER + i < workers) d[i] = from.desc[tid * PER + i];
   }
-  const int err = tid < ctas ? p.cta_err[tid] : kErrNone;  // (no more CTAs than threads)
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) mine += d[i].w >= 0 ? 1 : 0;
@@ -54,7 +49,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
     if (lane >= s) at0 += v;
   }
   if (lane == 31) s_cnt[warp] = at0;
-  const bool failed = __syncthreads_or(err != kErrNone);
+  __syncthreads();
   at0 -= mine;
   int units = 0;
 #pragma unroll
@@ -66,19 +61,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
   for (int i = 0; i < PER; ++i)
     if (d[i].w >= 0) list[at0++] = make_int4(d[i].x, d[i].y, d[i].z, d[i].w << 16 | ((tid * PER + i) / stride - d[i].w + 1));
   __syncthreads();
-  if (blockIdx.x == 0) {  // the launch's error word: some CTA's error, if there is any
-    if (tid == 0 && first) *p.err = kErrNone;
-    if (failed) {
-      __syncthreads();
-      if (err != kErrNone) *p.err = err;
-    }
-  }
   const int items = units * (RT / NR);  // those past a unit's last row are skipped
   int shares = 1;                       // warps an item
   if (NR == 1)
-    while (shares < kJoinWarps && items * shares * 2 <= static_cast<int>(gridDim.x) * kJoinWarps) shares *= 2;
+    while (shares < kJoinWarps && items * shares * 2 <= blocks * kJoinWarps) shares *= 2;
   const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
-  for (int t0 = blockIdx.x * groups; t0 < items; t0 += static_cast<int>(gridDim.x) * groups) {
+  for (int t0 = block * groups; t0 < items; t0 += blocks * groups) {
     const int item = t0 + group;
     int4 u = make_int4(0, 0, 0, 0);
     int head = 0, live = 0, i0 = 0, i1 = 0;
@@ -104,7 +92,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
       for (int j = i0; j < i1; j += LOOK) {
         const int n = imin(LOOK, i1 - j);
         float2 v = make_float2(0.f, 0.f);
-        if (lane / NR < n && row + lane % NR < live) v = p.part_ml[static_cast<int64_t>(slot_of(j + lane / NR)) * RT + row + lane % NR];
+        if (lane / NR < n && row + lane % NR < live) v = from.part_ml[static_cast<int64_t>(slot_of(j + lane / NR)) * RT + row + lane % NR];
         float x[PF][NR][ND];
         auto load = [&](int i) {  // PF parts' rows from part i on
 #pragma unroll
@@ -112,12 +100,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
             const int64_t at = static_cast<int64_t>(slot_of(j + imin(i + k, n - 1))) * RT + row;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              const float* from = p.part_o + (at + imin(r, live - 1 - row)) * D + lane * ND;
+              const float* src = from.part_o + (at + imin(r, live - 1 - row)) * D + lane * ND;
               if constexpr (ND == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(from);
+                const float4 y = *reinterpret_cast<const float4*>(src);
                 x[k][r][0] = y.x, x[k][r][1] = y.y, x[k][r][2] = y.z, x[k][r][3] = y.w;
               } else {
-                const float2 y = *reinterpret_cast<const float2*>(from);
+                const float2 y = *reinterpret_cast<const float2*>(src);
                 x[k][r][0] = y.x, x[k][r][1] = y.y;
               }
             }
@@ -195,22 +183,49 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) kv_join_kernel(const KvAtt
   }
 }
 
+// The first ``blocks_a`` blocks join the units of a, of RT rows, the others those
+// of b, of kKvPrRows (a batch of few and many rows: both kernels' in one launch).
+template <int D, int RT, bool BF16>
+__global__ void __launch_bounds__(kJoinWarps * 32, 2)
+    kv_join_kernel(const KvAttnParams p, const KvJoinPart a, const KvJoinPart b, int blocks_a) {
+  __shared__ int4 list[kKvDecMaxWorkers];  // entries, their parts in place of the first part's number
+  __shared__ int s_cnt[kJoinWarps];
+  __shared__ float s_o[RT > 16 ? 1 : kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
+  grid_dependency_wait();
+  const int tid = threadIdx.x, block = blockIdx.x;
+  int err = kErrNone;  // (no kernel has more CTAs than a block has threads)
+  if (block == 0) {
+    if (tid < b.ctas) err = b.cta_err[tid];
+    if (tid < a.ctas && a.cta_err[tid] != kErrNone) err = a.cta_err[tid];
+  }
+  if (RT > 16 || block < blocks_a)
+    join_units<D, RT, BF16>(p, a, block, blocks_a, list, s_o, s_ml, s_cnt);
+  else
+    join_units<D, kKvPrRows, BF16>(p, b, block - blocks_a, gridDim.x - blocks_a, list, s_o, s_ml, s_cnt);
+  if (block == 0) {  // the call's error word: some CTA's error, if there is any
+    if (tid == 0) *p.err = kErrNone;
+    if (__syncthreads_or(err != kErrNone) && err != kErrNone) *p.err = err;
+  }
+}
+
 template <int D, bool BF16>
-cudaError_t launch_rt(const KvAttnParams& p, int rt, int workers, int ctas, int stride, bool first, int grid,
+cudaError_t launch_rt(const KvAttnParams& p, int rt, const KvJoinPart& a, const KvJoinPart& b, int sms,
                       cudaStream_t st) {
   auto kern = rt == 8 ? kv_join_kernel<D, 8, BF16> : rt == 16 ? kv_join_kernel<D, 16, BF16> : kv_join_kernel<D, kKvPrRows, BF16>;
-  return launch_after_previous(kern, grid, kJoinWarps * 32, 0, st, p, workers, ctas, stride, first);
+  return launch_after_previous(kern, 2 * sms, kJoinWarps * 32, 0, st, p, a, b, b.workers > 0 ? sms : 2 * sms);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_join(const KvAttnParams& p, bool bf16, int rt, int workers, int ctas, int stride, bool first,
-                           int grid, cudaStream_t st) {
+cudaError_t launch_kv_join(const KvAttnParams& p, bool bf16, const KvJoinPart& few, const KvJoinPart& many, int sms,
+                           cudaStream_t st) {
+  const bool both = few.workers > 0 && many.workers > 0;
+  const KvJoinPart &a = few.workers > 0 ? few : many, b = both ? many : KvJoinPart{};
+  const int rt = few.workers > 0 ? few.rows : kKvPrRows;
   if (p.D == 64)
-    return bf16 ? launch_rt<64, true>(p, rt, workers, ctas, stride, first, grid, st)
-                : launch_rt<64, false>(p, rt, workers, ctas, stride, first, grid, st);
-  return bf16 ? launch_rt<128, true>(p, rt, workers, ctas, stride, first, grid, st)
-              : launch_rt<128, false>(p, rt, workers, ctas, stride, first, grid, st);
+    return bf16 ? launch_rt<64, true>(p, rt, a, b, sms, st) : launch_rt<64, false>(p, rt, a, b, sms, st);
+  return bf16 ? launch_rt<128, true>(p, rt, a, b, sms, st) : launch_rt<128, false>(p, rt, a, b, sms, st);
 }
 
 }  // namespace ab

@@ -853,13 +853,12 @@ cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int grid, cudaSt
 
 }  // namespace
 
-cudaError_t launch_kv_prompt(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, bool first, cudaStream_t st) {
+cudaError_t launch_kv_prompt(const KvAttnParams& p, const KvMaps& maps, bool bf16, int sms, KvJoinPart* left,
+                             cudaStream_t st) {
   const int grid = imin(sms, kKvPrMaxCtas);
-  cudaError_t e;
-  if (p.D == 64) e = bf16 ? launch_t<64, true>(p, maps, grid, st) : launch_t<64, false>(p, maps, grid, st);
-  else e = bf16 ? launch_t<128, true>(p, maps, grid, st) : launch_t<128, false>(p, maps, grid, st);
-  if (e != cudaSuccess) return e;
-  return launch_kv_join(p, bf16, RT, grid, grid, 1, first, 2 * sms, st);
+  *left = kv_join_part(p, grid, grid, 1, RT);
+  if (p.D == 64) return bf16 ? launch_t<64, true>(p, maps, grid, st) : launch_t<64, false>(p, maps, grid, st);
+  return bf16 ? launch_t<128, true>(p, maps, grid, st) : launch_t<128, false>(p, maps, grid, st);
 }
 
 }  // namespace ab
