@@ -62,10 +62,11 @@ __device__ __forceinline__ void join_units(const KvAttnParams& p, const KvJoinPa
     if (d[i].w >= 0) list[at0++] = make_int4(d[i].x, d[i].y, d[i].z, d[i].w << 16 | ((tid * PER + i) / stride - d[i].w + 1));
   __syncthreads();
   const int items = units * (RT / NR);  // those past a unit's last row are skipped
-  int shares = 1;                       // warps an item
+  int ls = 0;                           // log2 of the warps an item
   if (NR == 1)
-    while (shares < kJoinWarps && items * shares * 2 <= blocks * kJoinWarps) shares *= 2;
-  const int group = warp / shares, share = warp % shares, groups = kJoinWarps / shares;
+    while ((1 << ls) < kJoinWarps && items << (ls + 1) <= blocks * kJoinWarps) ++ls;
+  const int shares = NR == 1 ? 1 << ls : 1;
+  const int group = warp >> ls, share = warp & (shares - 1), groups = kJoinWarps >> ls;
   for (int t0 = block * groups; t0 < items; t0 += blocks * groups) {
     const int item = t0 + group;
     int4 u = make_int4(0, 0, 0, 0);
@@ -75,14 +76,14 @@ __device__ __forceinline__ void join_units(const KvAttnParams& p, const KvJoinPa
       u = list[item / (RT / NR)];
       head = u.z >> 16, live = u.z & 0xffff;
       const int parts = u.w & 0xffff;
-      i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
+      i0 = parts * share >> ls, i1 = parts * (share + 1) >> ls;
     }
     const int g0 = u.w >> 16;  // its first part
     auto slot_of = [&](int i) { return 2 * ((g0 + i) * stride + (stride > 1 ? head : 0)) + (i == 0 ? 1 : 0); };
-    float m[NR], l[NR], acc[NR][ND];
+    float m[NR], acc[NR][ND], l = 0.f;  // l: my lane's share of row lane % NR's
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      m[r] = -INFINITY, l[r] = 0.f;
+      m[r] = -INFINITY;
 #pragma unroll
       for (int u = 0; u < ND; ++u) acc[r][u] = 0.f;
     }
@@ -121,16 +122,14 @@ __device__ __forceinline__ void join_units(const KvAttnParams& p, const KvJoinPa
         for (int r = 1; r < NR; ++r) mine_m = lane % NR == r ? m[r] : mine_m;
         mx = fmaxf(mx, mine_m);  // of row lane % NR
         const float w = v.y == 0.f ? 0.f : ex2(v.x - mx);
-        const float wl = w * v.y;
+        l = (mine_m == mx ? l : (mine_m == -INFINITY ? 0.f : l * ex2(mine_m - mx))) + w * v.y;
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float mr = __shfl_sync(0xffffffffu, mx, r);
           const float g = m[r] == mr ? 1.f : (m[r] == -INFINITY ? 0.f : ex2(m[r] - mr));
           m[r] = mr;
-          l[r] *= g;
 #pragma unroll
           for (int u = 0; u < ND; ++u) acc[r][u] *= g;
-          if (lane % NR == r) l[r] += wl;
         }
         for (int i = 0; i < n; i += PF) {
           if (i > 0) load(i);
@@ -147,36 +146,39 @@ __device__ __forceinline__ void join_units(const KvAttnParams& p, const KvJoinPa
         }
       }
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
+      for (int s = 16; s >= NR; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
       if (share > 0) {
 #pragma unroll
         for (int u = 0; u < ND; ++u) s_o[NR == 1 ? warp : 0][lane * ND + u] = acc[0][u];
-        if (lane == 0) s_ml[warp] = make_float2(m[0], l[0]);
+        if (lane == 0) s_ml[warp] = make_float2(m[0], l);
       }
     }
     if (shares > 1) __syncthreads();
-    if (share == 0) {
+    if (share == 0 && row < live) {
+      int i = (u.y + row) / p.G, h = (u.y + row) % p.G;  // query and head of the group of my first row
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        if (row + r >= live) continue;
-        for (int k = 1; k < shares; ++k) {
-          const float2 v = s_ml[warp + k];
-          if (v.y == 0.f) continue;
-          const float mx = fmaxf(m[r], v.x), g = l[r] == 0.f ? 0.f : ex2(m[r] - mx), f = ex2(v.x - mx);
-          l[r] = l[r] * g + v.y * f;
-          m[r] = mx;
+        if (row + r >= live) break;
+        float lr = NR == 1 ? l : __shfl_sync(0xffffffffu, l, r);
+        if constexpr (NR == 1) {
+          for (int k = 1; k < shares; ++k) {
+            const float2 v = s_ml[warp + k];
+            if (v.y == 0.f) continue;
+            const float mx = fmaxf(m[r], v.x), g = lr == 0.f ? 0.f : ex2(m[r] - mx), f = ex2(v.x - mx);
+            lr = lr * g + v.y * f;
+            m[r] = mx;
 #pragma unroll
-          for (int u = 0; u < ND; ++u) acc[r][u] = acc[r][u] * g + s_o[NR == 1 ? warp + k : 0][lane * ND + u] * f;
+            for (int u = 0; u < ND; ++u) acc[r][u] = acc[r][u] * g + s_o[warp + k][lane * ND + u] * f;
+          }
         }
-        const int64_t at = static_cast<int64_t>(u.x) + (u.y + row + r) / p.G;
-        const int hq = head * p.G + (u.y + row + r) % p.G;
-        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        const int64_t at = static_cast<int64_t>(u.x) + i;
+        const int hq = head * p.G + h;
+        const float inv = lr == 0.f ? 0.f : 1.f / lr;
 #pragma unroll
         for (int u = 0; u < ND; ++u) acc[r][u] *= inv;
         store_o<BF16, ND>(p, at, hq, lane * ND, acc[r]);
-        if (lane == 0) store_lse(p, at, hq, m[r], l[r]);
+        if (lane == 0) store_lse(p, at, hq, m[r], lr);
+        if (++h == p.G) h = 0, ++i;
       }
     }
     if (shares > 1) __syncthreads();
