@@ -27,10 +27,11 @@ template <int D, int RT, bool BF16>
 __device__ __forceinline__ void join_units(const KvAttnParams& p, const KvJoinPart& from, int block, int blocks,
                                            int4* list, float (*s_o)[D], float2* s_ml, int* s_cnt) {
   constexpr int ND = D / 32, PER = kKvDecMaxWorkers / (kJoinWarps * 32);
-  // rows of a warp at once, and parts in flight: parts may be many where units are
-  // of few rows, and are two or three as a rule where they are of 256 (there, eight
-  // rows at once took 18 us where two take 15)
-  constexpr int NR = RT > 16 ? 2 : 1, PF = RT > 16 ? 2 : 8;
+  // Rows of a warp at once, and parts in flight: parts may be many where units are
+  // of few rows, and are two or three as a rule where they are of 256 (two or four
+  // rows at once take 15 us on 3761 prompt tokens, eight 18; eight parts in flight
+  // instead of four take 1 us more on 32 requests of drafted tokens).
+  constexpr int NR = RT > 16 ? 4 : 1, PF = RT > 16 ? 1 : 4;
   const int workers = from.workers, stride = from.stride;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int4 d[PER];  // of workers tid * PER + i
