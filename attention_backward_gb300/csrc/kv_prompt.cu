@@ -527,75 +527,70 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       const uint64_t q_kmaj = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       const uint64_t t_kmaj = sdesc_sw128(sbase + C::OFF_T, 16, 1024);
       const uint64_t t_mn = sdesc_sw128(sbase + C::OFF_T, C::SLAB, 1024);
-      // blocks of the CTA so far; per tile units and blocks so far
-      uint32_t bc = 0, qc0 = 0, qc1 = 0, nb0 = 0, nb1 = 0;
+      // Turns taken so far, a bit each: of Q, P and O of tile w (bit w), of the slots.
+      // One body serves both tiles: the warp's code is fetched anew for every block
+      // beside the softmax's and the conversions', and what it takes to fetch and run
+      // is in the way of every tile (two copies of it cost 5 %).
+      uint32_t q_turn = 0, p_turn = 0, o_turn = 3, k_slot = 0, k_turn = 0, v_slot = 1, v_turn = 0;
+      auto next_slot = [](uint32_t* slot, uint32_t* turn) {
+        *slot += 2;
+        if (*slot >= C::NT) *slot -= C::NT, *turn ^= 1;
+      };
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
         const PrUnit u = next_unit(uc, &ok);
         if (!ok || !u.valid) break;
         if (u.valid == 2 || u.j1 <= u.j0) continue;
         const PrTile t0 = tile_of(u, 0, p), t1 = tile_of(u, 1, p);
-        const uint32_t ib = 2 * bc;  // ring index of the unit's first K tile
-        auto in = [&](int w, int j) { return w ? t1.lo <= j && j < t1.hi : t0.lo <= j && j < t0.hi; };
-        auto wait_tile = [&](uint32_t i) {
-          return mbar_wait_warp(&bars[T_FULL0 + i % C::NT], (i / C::NT) & 1, wc, kErrWaitKV);
-        };
-        auto issue_s = [&](int w, uint32_t i) {
-          const uint64_t ko0 = sdesc_step((i % C::NT) * C::TILE), qo0 = sdesc_step(w * C::QTILE);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss_w(tmem + C::T_S + w * 128, q_kmaj + qo0 + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
-                     t_kmaj + ko0 + sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32), IDESC_S, kk > 0);
-          mma_commit_w(&bars[S_FULL0 + w]);
-        };
-        auto issue_pv = [&](int w, int j, uint32_t i) -> bool {
-          uint32_t& nb = w ? nb1 : nb0;
-          const int lo = w ? t1.lo : t0.lo;
-          const uint64_t vo = sdesc_step((i % C::NT) * C::TILE);
-          const uint32_t ts = tmem + C::T_S + w * 128, to = tmem + C::T_O + w * D;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!mbar_wait_warp(&bars[P_READY0 + 2 * w + h], nb & 1, wc, kErrWaitP)) return false;
-            if (h == 0 && j == lo) {  // the tile's O: its softmax warps have read the previous unit's
-              const uint32_t oc = (w ? qc1 : qc0) - 1;
-              if (oc >= 1 && !mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wc, kErrWaitDQEmpty)) return false;
-            }
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < HK / 16; ++kk)
-              mma_ts_w(to, ts + h * 64 + kk * 8, t_mn + vo + sdesc_step((h * HK / 16 + kk) * 2048), IDESC_PV,
-                       j > lo || h > 0 || kk > 0);
-            mma_commit_w(&bars[O_DONE0 + 2 * w + h]);
-          }
-          ++nb;
-          return true;
-        };
-        // the unit's Q tiles
-        if (t0.lo < t0.hi) ok = mbar_wait_warp(&bars[Q_FULL0], qc0++ & 1, wc, kErrWaitStageFull);
-        if (ok && t1.lo < t1.hi) ok = mbar_wait_warp(&bars[Q_FULL0 + 1], qc1++ & 1, wc, kErrWaitStageFull);
         // S of block j + 1 goes behind P V of block j, over its P
         for (int j = u.j0 - 1; j < u.j1 && ok; ++j) {
-          const uint32_t iv = ib + 2 * (j - u.j0) + 1, ik = iv + 1;
           const bool pv = j >= u.j0, s = j + 1 < u.j1;
-          if (pv && !(ok = wait_tile(iv))) break;
-          if (pv) tc_fence_after();
-          if (pv && in(0, j) && !(ok = issue_pv(0, j, iv))) break;
-          if (s) {
-            if (!(ok = wait_tile(ik))) break;
-            tc_fence_after();
-            if (in(0, j + 1)) issue_s(0, ik);
+          if (pv && !(ok = mbar_wait_warp(&bars[T_FULL0 + v_slot], v_turn, wc, kErrWaitKV))) break;
+#pragma unroll 1
+          for (int w = 0; w < 2 && ok; ++w) {
+            const int lo = w ? t1.lo : t0.lo, hi = w ? t1.hi : t0.hi;
+            const uint32_t ts = tmem + C::T_S + w * 128, to = tmem + C::T_O + w * D;
+            if (pv && lo <= j && j < hi) {
+              const uint64_t v = t_mn + sdesc_step(v_slot * C::TILE);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!(ok = mbar_wait_warp(&bars[P_READY0 + 2 * w + h], p_turn >> w & 1, wc, kErrWaitP))) break;
+                if (h == 0 && j == lo) {  // the tile's O: its softmax warps have read the previous unit's
+                  if (!(ok = mbar_wait_warp(&bars[O_FREE0 + w], o_turn >> w & 1, wc, kErrWaitDQEmpty))) break;
+                  o_turn ^= 1u << w;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < HK / 16; ++kk)
+                  mma_ts_w(to, ts + h * 64 + kk * 8, v + sdesc_step((h * HK / 16 + kk) * 2048), IDESC_PV,
+                           j > lo || h > 0 || kk > 0);
+                mma_commit_w(&bars[O_DONE0 + 2 * w + h]);
+              }
+              if (!ok) break;
+              p_turn ^= 1u << w;
+            }
+            if (pv && w == 1) mma_commit_w(&bars[T_EMPTY0 + v_slot]);
+            if (s) {
+              if (w == 0 && !(ok = mbar_wait_warp(&bars[T_FULL0 + k_slot], k_turn, wc, kErrWaitKV))) break;
+              if (lo <= j + 1 && j + 1 < hi) {
+                if (j + 1 == lo) {  // the unit's Q
+                  if (!(ok = mbar_wait_warp(&bars[Q_FULL0 + w], q_turn >> w & 1, wc, kErrWaitStageFull))) break;
+                  q_turn ^= 1u << w;
+                }
+                tc_fence_after();
+                const uint64_t q = q_kmaj + sdesc_step(w * C::QTILE), k = t_kmaj + sdesc_step(k_slot * C::TILE);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                  mma_ss_w(ts, q + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
+                           k + sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32), IDESC_S, kk > 0);
+                mma_commit_w(&bars[S_FULL0 + w]);
+              }
+              if (w == 1) mma_commit_w(&bars[T_EMPTY0 + k_slot]);
+            }
           }
-          if (pv) {
-            if (in(1, j) && !(ok = issue_pv(1, j, iv))) break;
-            mma_commit_w(&bars[T_EMPTY0 + iv % C::NT]);
-          }
-          if (s) {
-            if (in(1, j + 1)) issue_s(1, ik);
-            mma_commit_w(&bars[T_EMPTY0 + ik % C::NT]);
-          }
+          if (pv) next_slot(&v_slot, &v_turn);
+          if (s) next_slot(&k_slot, &k_turn);
         }
-        if (!ok) break;
-        bc += u.j1 - u.j0;
       }
       // every MMA issued by this warp completes before TMEM is released
       mma_commit_w(&bars[DRAIN]);
@@ -709,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         const float msub = first ? 0.f : m_used;
         const float2 nm2 = make_float2(-msub, -msub);
         tmem_ld_wait();
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
 #pragma unroll
           for (int k = 0; k < HK; ++k)
             if (k < v_lo || k >= v_hi || (no_page >> (k / 16) & 1u)) sr[k] = __float_as_uint(-INFINITY);
@@ -724,12 +719,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           pw[e] = pack2<false>(pp.x, pp.y);
         }
         need |= !((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y) <= kMostSum);
-        if (!__any_sync(0xffffffffu, need)) {
+        if (__builtin_expect(!__any_sync(0xffffffffu, need), 1)) {
 #pragma unroll
           for (int h = 0; h < HK / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
         }
       }
-      if (__any_sync(0xffffffffu, need)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
         auto load_scores = [&](int h, uint32_t* x) {  // 32 scores of the row, -inf where the key is not seen
           tmem_ld32(tS + h * 32, x);
           tmem_ld_wait();
