@@ -142,6 +142,11 @@ __device__ __forceinline__ int64_t lanes_work(const KvAttnParams& p, const KvReq
   return w;
 }
 
+template <typename T>
+__device__ __forceinline__ T warp_uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // Calls f(n, request) for the requests of [n0, n1) that have rows here, in
 // order, until it returns true; 32 requests are looked up at once.
 template <typename F>
@@ -523,14 +528,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       // ============================================================ MMA issue
       constexpr uint32_t IDESC_S = idesc_f16(false, 128, KT, false, false);
       constexpr uint32_t IDESC_PV = idesc_f16(false, 128, D, false, true);
-      const uint32_t sbase = smem_u32(sm);
+      const uint32_t sbase = smem_u32(sm), tm = warp_uniform(tmem), elected = elect_lane();
       const uint64_t q_kmaj = sdesc_sw128(sbase + C::OFF_Q, 16, 1024);
       const uint64_t t_kmaj = sdesc_sw128(sbase + C::OFF_T, 16, 1024);
       const uint64_t t_mn = sdesc_sw128(sbase + C::OFF_T, C::SLAB, 1024);
       // Turns taken so far, a bit each: of Q, P and O of tile w (bit w), of the slots.
-      // One body serves both tiles: the warp's code is fetched anew for every block
-      // beside the softmax's and the conversions', and what it takes to fetch and run
-      // is in the way of every tile (two copies of it cost 5 %).
+      // This warp is what the kernel waits for: of 4180 cycles a block it waits 900,
+      // the products take 2048, the rest is their issue beside a scheduler's softmax
+      // and conversion warps.  Hence one body for both tiles (two copies, fetched
+      // anew for every block, cost 5 %), the lane elected once (3 %).
       uint32_t q_turn = 0, p_turn = 0, o_turn = 3, k_slot = 0, k_turn = 0, v_slot = 1, v_turn = 0;
       auto next_slot = [](uint32_t* slot, uint32_t* turn) {
         *slot += 2;
@@ -541,15 +547,18 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         const PrUnit u = next_unit(uc, &ok);
         if (!ok || !u.valid) break;
         if (u.valid == 2 || u.j1 <= u.j0) continue;
+        // (lane 0's, so that the compiler takes them, the loop and what is computed in it for uniform)
         const PrTile t0 = tile_of(u, 0, p), t1 = tile_of(u, 1, p);
+        const int lo0 = warp_uniform(t0.lo), hi0 = warp_uniform(t0.hi), lo1 = warp_uniform(t1.lo),
+                  hi1 = warp_uniform(t1.hi), j0 = warp_uniform(u.j0), j1 = warp_uniform(u.j1);
         // S of block j + 1 goes behind P V of block j, over its P
-        for (int j = u.j0 - 1; j < u.j1 && ok; ++j) {
-          const bool pv = j >= u.j0, s = j + 1 < u.j1;
+        for (int j = j0 - 1; j < j1 && ok; ++j) {
+          const bool pv = j >= j0, s = j + 1 < j1;
           if (pv && !(ok = mbar_wait_warp(&bars[T_FULL0 + v_slot], v_turn, wc, kErrWaitKV))) break;
 #pragma unroll 1
           for (int w = 0; w < 2 && ok; ++w) {
-            const int lo = w ? t1.lo : t0.lo, hi = w ? t1.hi : t0.hi;
-            const uint32_t ts = tmem + C::T_S + w * 128, to = tmem + C::T_O + w * D;
+            const int lo = w ? lo1 : lo0, hi = w ? hi1 : hi0;
+            const uint32_t ts = tm + C::T_S + w * 128, to = tm + C::T_O + w * D;
             if (pv && lo <= j && j < hi) {
               const uint64_t v = t_mn + sdesc_step(v_slot * C::TILE);
 #pragma unroll
@@ -562,8 +571,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < HK / 16; ++kk)
-                  mma_ts_w(to, ts + h * 64 + kk * 8, v + sdesc_step((h * HK / 16 + kk) * 2048), IDESC_PV,
-                           j > lo || h > 0 || kk > 0);
+                  mma_ts_e(to, ts + h * 64 + kk * 8, v + sdesc_step((h * HK / 16 + kk) * 2048), IDESC_PV,
+                           j > lo || h > 0 || kk > 0, elected);
                 mma_commit_w(&bars[O_DONE0 + 2 * w + h]);
               }
               if (!ok) break;
@@ -581,8 +590,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
                 const uint64_t q = q_kmaj + sdesc_step(w * C::QTILE), k = t_kmaj + sdesc_step(k_slot * C::TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                  mma_ss_w(ts, q + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
-                           k + sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32), IDESC_S, kk > 0);
+                  mma_ss_e(ts, q + sdesc_step((kk / 4) * C::QSLAB + (kk % 4) * 32),
+                           k + sdesc_step((kk / 4) * C::SLAB + (kk % 4) * 32), IDESC_S, kk > 0, elected);
                 mma_commit_w(&bars[S_FULL0 + w]);
               }
               if (w == 1) mma_commit_w(&bars[T_EMPTY0 + k_slot]);

@@ -418,6 +418,38 @@ def test_attend_prompts_masks(causal, window, D):
     check_attend(attend_problem("bf16", lens, 6, 2, D, 16, 16, spare_rows=3), "bf16", causal, window)
 
 
+@pytest.mark.parametrize("causal,window", [(True, -1), (False, -1), (True, 100), (False, 200)])
+@pytest.mark.parametrize("lens,HQ,HKV,D,page", [
+    ([(65, 65), (128, 128), (70, 129), (100, 256)], 2, 2, 64, 16),           # one block and two
+    ([(65, 257), (128, 385), (127, 2000), (66, 66)], 2, 2, 128, 64),
+    ([(16, 3000), (9, 128), (13, 513), (16, 16)], 32, 4, 128, 32),           # groups of 8 heads
+    ([(70 + i, 200 + 37 * i) for i in range(40)], 12, 12, 64, 64),           # many units a CTA
+    ([(80, 300), (300, 400), (90, 1000), (257, 300), (500, 640)], 8, 8, 64, 128),  # beside large ones
+    ([(100, 20000)], 1, 1, 128, 128),                                        # many parts of one unit
+])
+def test_attend_prompts_of_at_most_128_rows(lens, HQ, HKV, D, page, causal, window):
+    check_attend(attend_problem("bf16", lens, HQ, HKV, D, page, 80), "bf16", causal, window)
+
+
+def test_attend_prompts_of_at_most_128_rows_special():
+    """Lacking pages, rows without keys, scales far apart, a batch of which one row is not finite."""
+    prob = attend_problem("f16", [(100, 700), (90, 20), (70, 0), (128, 900)], 2, 1, 64, 16, 81)
+    prob[5][0, 3:30], prob[5][3, :9] = -1, -1
+    check_attend(prob, "f16")
+    q, kc, vc, ks, vs, table, cu, kv = attend_problem("bf16", [(100, 700), (70, 300)], 2, 1, 128, 32, 82)
+    vs = vs * np.exp2(np.random.default_rng(4).integers(-12, 13, vs.shape))
+    check_attend((q, kc, vc, ks, vs, table, cu, kv), "bf16")
+    ref, rl = run_attend((q, kc, vc, ks, vs, table, cu, kv), "bf16")
+    for _ in range(3):
+        o, lse = run_attend((q, kc, vc, ks, vs, table, cu, kv), "bf16")
+        assert np.array_equal(o, ref) and np.array_equal(lse, rl)
+    q[7, 0, 3] = np.nan
+    o, lse = run_attend((q, kc, vc, ks, vs, table, cu, kv), "bf16")
+    keep = np.ones(o.shape[:2], bool)
+    keep[7, 0] = False
+    assert np.isnan(o[7, 0]).all() and np.array_equal(o[keep], ref[keep])
+
+
 def test_attend_prompts_with_lacking_pages_and_far_scales():
     prob = attend_problem("f16", [(200, 900), (120, 500)], 8, 2, 128, 16, 17)
     q, kc, vc, ks, vs, table, cu, kv = prob
