@@ -790,6 +790,49 @@ def test_prompt_graphs_side_by_side():
     check_attend((probs[0][0], kc, vc, ks, vs, table, cu, kv), "bf16")
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 33, 70]])
+def test_offsets_past_32_bits(new):
+    """Pages beyond 4 GB of the caches, rows of q and o beyond 4 GB: the same
+    results, bit for bit, as from small buffers."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    HQ, HKV, D, page = 8, 4, 128, 16
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    ctx, T = [50, 0, 33], sum(new)
+    rng = np.random.default_rng(90)
+    lens = np.array(ctx) + new
+    width = int(-(-lens.max() // page)) + 1
+    small = np.arange(3 * width).reshape(3, width)
+    nb = (1 << 32) // (page * HKV * D) + 4000
+    x = [cuda(rounded(rng, (1, int(lens.sum()), HKV, D), "bf16"), torch.bfloat16) for _ in range(2)]
+    q = cuda(rounded(rng, (1, T, HQ, D), "bf16"), torch.bfloat16)
+    wide = (2 ** 31 // (T - 1) // 8 + 1) * 8  # elements between rows: the last one lies past 2^32 bytes
+    results = []
+    for big in (False, True):
+        table = nb - 1 - 7 * small if big else small
+        caches = [torch.empty(nb if big else 3 * width, page, HKV, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        caches = [c.view(torch.float8_e4m3fn) for c in caches]
+        scales = [torch.zeros(c.shape[0], HKV, device="cuda") for c in caches]
+        slots = np.concatenate([table[r, np.arange(n) // page] * page + np.arange(n) % page for r, n in enumerate(lens)])
+        assert not big or slots.min() * HKV * D > 2 ** 32
+        ab.kv_cache_write(x[0], x[1], i32(slots), *caches, *scales)
+        tq, o = q, torch.zeros_like(q)
+        if big:
+            room = torch.empty(2, T * wide, dtype=torch.bfloat16, device="cuda")
+            tq, o = (r.as_strided((1, T, HQ, D), (T * wide, wide, D, 1), r.storage_offset()) for r in room)
+            tq.copy_(q)
+        lse = torch.zeros(1, HQ, T, device="cuda")
+        cu = np.concatenate([[0], np.cumsum(new)])
+        ab.forward_kv_cache(tq, *caches, *scales, i32(table), i32(cu), i32(lens), out=(o, lse))
+        torch.cuda.synchronize()
+        results.append((o.clone(), lse.clone()))
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+    assert results[0][0].abs().max() > 0.1
+
+
 def test_no_tokens():
     import torch
 
