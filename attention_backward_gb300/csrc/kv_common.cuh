@@ -37,6 +37,20 @@ __device__ __forceinline__ float to_top(float amax, float* back) {
   return __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
 }
 
+// The weight of key j in O_i is p_ij vs_j, p = 2^(x - m_i) and vs its page's V scale.
+// It is rounded to fp16 as p vs 2^ref_i, ref_i a whole number of the row's own: where
+// it is set, the row's largest weight so far lands in (2^(kKvTop - 1), 2^kKvTop].  (Set
+// for a whole unit by its pages' largest V scale, it let the weights of rows that
+// do not see that page, or give it none, fall below fp16's range.)
+constexpr float kKvTop = 0.f;
+constexpr float kKvRefNone = 100.f;  // of a row that has met no weight above 2^-100
+__device__ __forceinline__ float weight_ref(float log2_top) {
+  return fminf(fmaxf(kKvTop - ceilf(log2_top), -126.f), kKvRefNone);
+}
+// 2^(log2 vs + ref), finite also where a row without weights meets a large scale
+// (its p are then tiny or 0).
+__device__ __forceinline__ float weight_factor(float log2_vs, float ref) { return ex2(fminf(log2_vs + ref, 126.f)); }
+
 // Writes of one row's final O (16-bit, ND values from column d0) and LSE.
 template <bool BF16, int ND>
 __device__ __forceinline__ void store_o(const KvAttnParams& p, int64_t t, int hq, int d0, const float* o) {

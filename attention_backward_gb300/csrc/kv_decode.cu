@@ -31,8 +31,8 @@
 // is brought to fp16's upper range by a power of two (bf16 rows keep every bit
 // of their leading values, what falls under fp16's 2^-24 is 2^-38 of the row's
 // largest value); the K scale and the row's power go to the f32 score, the V
-// scale to p before it is rounded to fp16, relative to the largest V scale met
-// so far, so that neither scale can overflow.
+// scale to p before it is rounded to fp16, with a power of two that follows the
+// row's largest product of the two (kv_common.cuh).
 //
 // Layout: no operand goes through a transpose in shared memory.  The sum over d
 // may run in any order, so the thread that holds k columns 2c, 2c + 1 of key n
@@ -59,7 +59,7 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 // Ring of slots (one tile each) per warp: with the 8 or 12 warps of an SM, 96 to
 // 128 KB in flight; a third slot made every case 1 to 4 % slower.
 constexpr int kStages = 2;
-constexpr float kRescale = 8.f;  // log2 growth of a row max that triggers a rescale
+constexpr float kRescale = 8.f;  // log2 growth of a row's max, or largest weight, that triggers a rescale
 // Fewest line positions of a worker: below it, more parts cost more to join
 // than they save.
 constexpr int kMinWork = 4;
@@ -339,33 +339,34 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
     kv_row_keys(rq, row0 / p.G, p.causal, p.window, &xx, &hi_all);
 
     // A row's scores are kept relative to nm (its m, 0 before its first key)
-    // and compared with th (kRescale, -inf before its first key).
-    float nm[NB][2], th[NB][2], l[NB][2], vref = 0.f, vinv = 0.f;
+    // and compared with th (kRescale, -inf before its first key); its weights and
+    // O are at 2^ref.
+    float nm[NB][2], th[NB][2], l[NB][2], ref[NB][2];
     float o[NB][MT][4];
 #pragma unroll
     for (int e = 0; e < NB; ++e) {
       nm[e][0] = nm[e][1] = l[e][0] = l[e][1] = 0.f;
       th[e][0] = th[e][1] = -INFINITY;
+      ref[e][0] = ref[e][1] = kKvRefNone;
 #pragma unroll
       for (int t = 0; t < MT; ++t) o[e][t][0] = o[e][t][1] = o[e][t][2] = o[e][t][3] = 0.f;
     }
 
-    float ks_l = 0.f, vs_l = 0.f;  // scales of the 32 groups being computed, and
-    int cp_blk = -1;               // their ids
+    float ks_l = 0.f, lv_l = 0.f;  // K scales, log2 of the V scales of the 32 groups
+    int cp_blk = -1;               // being computed, and their ids
     int cp_batch = part0 - BATCH;
     bool ok = true;
     for (int t = part0; t < part1; ++t) {
       if (t - cp_batch == BATCH) {  // (the copies are kStages tiles ahead: in this batch already)
         cp_batch = t;
-        cp_blk = ld_blk, ks_l = ld_ks;
-        vs_l = ld_vs < 0x1p-126f ? 0.f : ld_vs;  // (its inverse is taken)
+        cp_blk = ld_blk, ks_l = ld_ks, lv_l = log2f(ld_vs);
       }
-      float ks[NZ], vs[NZ];
+      float ks[NZ], lv[NZ];
       bool have[NZ], any = false, edge = false;
 #pragma unroll
       for (int z = 0; z < NZ; ++z) {
         const int from = (t - cp_batch) * NZ + z;
-        ks[z] = __shfl_sync(0xffffffffu, ks_l, from), vs[z] = __shfl_sync(0xffffffffu, vs_l, from);
+        ks[z] = __shfl_sync(0xffffffffu, ks_l, from), lv[z] = __shfl_sync(0xffffffffu, lv_l, from);
         have[z] = __shfl_sync(0xffffffffu, cp_blk, from) >= 0;
         any |= have[z], edge |= !have[z];
       }
@@ -416,44 +417,51 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
                 if (!have[z] || k < lo[e][y & 1] || k >= hi[e][y & 1]) s[z][e][y] = -INFINITY;
               }
         }
-        // ---- a max that grew past the threshold, or a larger V scale: rescale
-        float vmx = vs[0];
-#pragma unroll
-        for (int z = 1; z < NZ; ++z) vmx = fmaxf(vmx, vs[z]);
-        bool grew = vmx > vref;
+        // ---- a max or a weight that grew past its threshold: rescale the row
+        auto most = [&](int z, int e, int y) {  // score, relative to nm, up to which neither did
+          return fminf(th[e][y], kKvTop + kRescale - (lv[z] + ref[e][y]));
+        };
+        bool grew = false;
 #pragma unroll
         for (int z = 0; z < NZ; ++z)
 #pragma unroll
-          for (int e = 0; e < NB; ++e)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) grew |= s[z][e][y] > th[e][y & 1];
-        if (__any_sync(0xffffffffu, grew)) {
-          float g = 1.f;
-          if (vmx > vref) {
-            g = vref / vmx;
-            vref = vmx;
-            vinv = 1.f / vmx;
+          for (int e = 0; e < NB; ++e) {
+            const float m0 = most(z, e, 0), m1 = most(z, e, 1);
+            grew |= s[z][e][0] > m0 || s[z][e][1] > m1 || s[z][e][2] > m0 || s[z][e][3] > m1;
           }
+        if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
           for (int e = 0; e < NB; ++e) {
             float f[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              float mx = -INFINITY;  // the row's largest score, relative to nm
+              // the row's largest score, weight (log2) and excess over a threshold
+              float mx = -INFINITY, top = -INFINITY, over = -INFINITY;
 #pragma unroll
-              for (int z = 0; z < NZ; ++z) mx = fmaxf(mx, fmaxf(s[z][e][y], s[z][e][2 + y]));
+              for (int z = 0; z < NZ; ++z) {
+                const float x = fmaxf(s[z][e][y], s[z][e][2 + y]);
+                mx = fmaxf(mx, x), top = fmaxf(top, x + lv[z]), over = fmaxf(over, x - most(z, e, y));
+              }
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+              for (int d = 4; d < 32; d <<= 1) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                over = fmaxf(over, __shfl_xor_sync(0xffffffffu, over, d));
+              }
               f[y] = 1.f;
-              if (mx > th[e][y]) {
-                f[y] = th[e][y] == -INFINITY ? 0.f : ex2(-mx);
-                nm[e][y] += mx;
+              if (over > 0.f) {  // (row by row, so that no row's result depends on another's)
+                const bool first = th[e][y] == -INFINITY;
+                const float up = mx > th[e][y] ? mx : 0.f;
+                // the largest weight: this tile's or, as it was where ref was set, an earlier one's
+                const float now = weight_ref(first ? top - up : fmaxf(top, kKvTop - ref[e][y]) - up);
+                f[y] = first ? 0.f : ex2(now - ref[e][y] - up);
+                l[e][y] *= first ? 0.f : ex2(-up);
+                ref[e][y] = now;
+                nm[e][y] += up;
                 th[e][y] = kRescale;
 #pragma unroll
-                for (int z = 0; z < NZ; ++z) s[z][e][y] -= mx, s[z][e][2 + y] -= mx;
+                for (int z = 0; z < NZ; ++z) s[z][e][y] -= up, s[z][e][2 + y] -= up;
               }
-              l[e][y] *= f[y];
-              f[y] *= g;
             }
 #pragma unroll
             for (int u = 0; u < MT; ++u)
@@ -463,14 +471,14 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
         uint32_t pb[NZ][NB][2];
 #pragma unroll
         for (int z = 0; z < NZ; ++z) {
-          const float ratio = vs[z] * vinv;  // at most 1
 #pragma unroll
           for (int e = 0; e < NB; ++e) {
+            const float w0 = weight_factor(lv[z], ref[e][0]), w1 = weight_factor(lv[z], ref[e][1]);
             const float p0 = ex2(s[z][e][0]), p1 = ex2(s[z][e][1]), p2 = ex2(s[z][e][2]), p3 = ex2(s[z][e][3]);
             l[e][0] += p0 + p2;
             l[e][1] += p1 + p3;
-            pb[z][e][0] = turn8x8(pack2<false>(p0 * ratio, p1 * ratio));
-            pb[z][e][1] = turn8x8(pack2<false>(p2 * ratio, p3 * ratio));
+            pb[z][e][0] = turn8x8(pack2<false>(p0 * w0, p1 * w1));
+            pb[z][e][1] = turn8x8(pack2<false>(p2 * w0, p3 * w1));
           }
         }
         // ---- O^T += V^T P^T
@@ -540,7 +548,8 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
           const int row = 8 * e + 2 * c4 + y;
           if (row >= rows) continue;
           // columns [r8 VB, (r8 + 1) VB)
-          const float f = whole ? (sum == 0.f ? 0.f : vref / sum) : vref;
+          const float back = ex2(-ref[e][y]);
+          const float f = whole ? (sum == 0.f ? 0.f : back / sum) : back;
           float v[VB];
 #pragma unroll
           for (int u = 0; u < MT; ++u) v[2 * u] = o[e][u][y] * f, v[2 * u + 1] = o[e][u][2 + y] * f;
