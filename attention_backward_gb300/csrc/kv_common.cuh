@@ -1,7 +1,5 @@
 // Device helpers of attention over the 8-bit cache.
 #pragma once
-#include <cuda_fp16.h>
-
 #include "cvt.cuh"
 #include "kv_cache.h"
 
@@ -12,15 +10,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t* lo, uint32_t
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(*lo), "=r"(*hi)
       : "r"(w));
-}
-
-// Product of two fp16 pairs.
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, __half2 f) {
-  __half2 x;
-  memcpy(&x, &a, 4);
-  x = __hmul2(x, f);
-  memcpy(&a, &x, 4);
-  return a;
 }
 
 // Power of two that brings a largest absolute value into [2^14, 2^15), and its
@@ -43,7 +32,7 @@ __device__ __forceinline__ float to_top(float amax, float* back) {
 // for a whole unit by its pages' largest V scale, it let the weights of rows that
 // do not see that page, or give it none, fall below fp16's range.)
 constexpr float kKvTop = 0.f;
-constexpr float kKvRefNone = 100.f;  // of a row that has met no weight above 2^-100
+constexpr float kKvRefNone = 88.f;  // of a row that has met no weight above 2^-88
 __device__ __forceinline__ float weight_ref(float log2_top) {
   return fminf(fmaxf(kKvTop - ceilf(log2_top), -126.f), kKvRefNone);
 }

@@ -15,11 +15,12 @@
 // to be made.  2048 + 1713 tokens on 14336 cached ones, 32 query and 8 KV heads of
 // 128: 499 us, 1.24 PFLOP/s, 64 % of the measured peak, held back by the issue of
 // the products (below).  TMA brings pages as bytes into a raw ring; four warps convert them
-// to fp16 (exact) in the 128-byte-swizzled tiles that the products read.  A K
-// block's page scales (at most one per 16 keys) multiply the f32 scores, 16
-// columns at a time.  V is converted at v * vs / vref, vref the largest V scale
-// of the unit's pages: exact for powers of two (what falls under fp16's range
-// is 2^-34 of the largest value), rounded to fp16 once more for others.  Each
+// to fp16 (exact) in the 128-byte-swizzled tiles that the products read.  A
+// block's page scales (at most one per 16 keys) are applied by the softmax, 16
+// columns at a time: K's as factors of the f32 scores, V's in the exponent, so that
+// the power is the weight P vs 2^ref (kv_common.cuh) that is rounded to fp16; its
+// sum over 16 columns, divided by vs, goes into l, which is kept at 2^ref as well.
+// (A product of P with the scale for each weight took 3 % longer.)  Each
 // softmax thread loads its own row of Q, brings it to fp16's upper range by a
 // power of two and writes it into the swizzled Q tile.
 //
@@ -28,7 +29,7 @@
 //
 // Warp roles (16 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 copies, 9 MMA
 // issue, 10 the walk along the line, a unit ahead of the others (it publishes
-// units, with their largest V scale, through a two-slot ring), 11 idle, 12-13
+// units through a two-slot ring), 11 idle, 12-13
 // conversion of K, 14-15 of V.  Every wait is bounded.
 #include <cuda_fp16.h>
 
@@ -50,7 +51,15 @@ constexpr int kWarps = 16, THREADS = kWarps * 32;
 // warpgroups hold 64 scores and 32 P pairs a thread
 constexpr uint32_t REG_SOFT = 168, REG_CTL = 88, REG_CONV = 88;
 static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
-constexpr float kMostSum = 32768.f;  // of a block's P before a row's max is taken anew
+constexpr float kMostSum = 32768.f;  // of half a block's P, or weights, before a row's max is taken anew
+// Largest |log2| of a V scale whose weights' sum gives l: the weights of P down to
+// 2^-36 then stay above f32's 2^-126 while ref is -45 or more.  A group with another
+// (0, or 2^-100 of a page of zeros), or a row with a smaller ref, sends its half
+// block through the slow path.
+constexpr float kFarScale = 45.f;
+__device__ __forceinline__ float most_sum(float ref) {  // of a half block's P at 2^ref; -1: always the slow path
+  return ref < -kFarScale ? -1.f : kMostSum * ex2(ref);
+}
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
 constexpr int HK = 64;            // keys of a half block
 static_assert(KT == 2 * HK && kGroups == 8, "a half block's scales are one 16-byte load");
@@ -93,11 +102,12 @@ struct PrCfg {
   static constexpr int OFF_T = OFF_Q + 2 * QTILE;
   static constexpr int OFF_RAW = OFF_T + NT * TILE;
   static constexpr int OFF_UNIT = OFF_RAW + NR * RAW;   // 2 unit descriptors of 64 bytes
-  static constexpr int OFF_SC = OFF_UNIT + 2 * 64;      // K scales, then V ratios, [kScaleRing][kGroups] each
-  static constexpr int OFF_BAR = OFF_SC + 2 * kScaleRing * kGroups * 4;
+  static constexpr int OFF_SC = OFF_UNIT + 2 * 64;      // K scales, log2 of V scales and their inverses, [kScaleRing][kGroups] each
+  static constexpr int OFF_BAR = OFF_SC + 3 * kScaleRing * kGroups * 4;
   static constexpr int OFF_MISC = OFF_BAR + 56 * 8;
-  static constexpr int SMEM = OFF_MISC + 32;
-  static_assert(SMEM + 256 <= 227 * 1024, "shared memory budget");
+  static constexpr int OFF_WORK = OFF_MISC + 32;        // the line's length, a share of the requests per warp
+  static constexpr int SMEM = OFF_WORK + kWarps * 8;    // (all of it: nothing static beside the 1024-byte aligned tiles)
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t T_S = 0, T_O = 256;  // tile w: scores at 128 w, O at 256 + D w
 };
 
@@ -125,7 +135,6 @@ struct PrUnit {
   int j0, j1;            // j0 == j1: no block, its rows are zero
   int lo, hi;            // keys that some row of the unit sees
   int slot;              // -1: the whole unit, else the slot of its partial rows
-  float vref;
   int valid;
 };
 static_assert(sizeof(PrUnit) <= 64, "descriptor slot");
@@ -233,13 +242,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
                                                                const __grid_constant__ KvAttnParams p) {
   using C = PrCfg<D>;
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ int64_t s_work[kWarps];
+  int64_t* const s_work = reinterpret_cast<int64_t*>(sm + C::OFF_WORK);
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(sm + C::OFF_MISC + 8);
   PrUnit* const units = reinterpret_cast<PrUnit*>(sm + C::OFF_UNIT);
   float* const k_scales = reinterpret_cast<float*>(sm + C::OFF_SC);               // [kScaleRing][kGroups]; -1: no page
-  float* const v_ratios = k_scales + kScaleRing * kGroups;
+  float* const v_logs = k_scales + kScaleRing * kGroups;
+  float* const v_invs = v_logs + kScaleRing * kGroups;  // NaN: far (kFarScale)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   grid_dependency_wait();
@@ -348,7 +358,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         if (n >= 1 && !(ok = mbar_wait_warp(&bars[T_EMPTY0 + ts], (n - 1) & 1, wc, kErrWaitKVFree))) break;
         const uint8_t* const raw = sm + C::OFF_RAW + rs * C::RAW;
         uint8_t* const out = sm + C::OFF_T + ts * C::TILE;
-        const float* const ratio = v_ratios + (bc % kScaleRing) * kGroups;
         // V rows that no query sees are zeroed: a zero P times a NaN would be NaN
         bool edge = false;
         if (kv) {
@@ -364,40 +373,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
 #pragma unroll
           for (int s = 0; s < C::NSLAB; ++s)
             x[s] = *reinterpret_cast<const uint4*>(raw + kv_chunk_at<D>(row, s * 4 + c4));
-          if (kv) {
-            const __half2 f = __float2half2_rn(ratio[row >> 4]);
-            if (edge) {
-              const int key = j * KT + row;
-              const bool page = k_scales[(bc % kScaleRing) * kGroups + (row >> 4)] >= 0.f;
-              if (!page || key < u.lo || key >= u.hi) {
+          if (edge) {
+            const int key = j * KT + row;
+            const bool page = k_scales[(bc % kScaleRing) * kGroups + (row >> 4)] >= 0.f;
+            if (!page || key < u.lo || key >= u.hi) {
 #pragma unroll
-                for (int s = 0; s < C::NSLAB; ++s) x[s] = make_uint4(0u, 0u, 0u, 0u);
-              }
+              for (int s = 0; s < C::NSLAB; ++s) x[s] = make_uint4(0u, 0u, 0u, 0u);
             }
+          }
 #pragma unroll
-            for (int s = 0; s < C::NSLAB; ++s) {
-              const uint32_t xs[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-              uint32_t y[8];
+          for (int s = 0; s < C::NSLAB; ++s) {
+            const uint32_t xs[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+            uint32_t y[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
-                y[2 * e] = mul_f16x2(y[2 * e], f), y[2 * e + 1] = mul_f16x2(y[2 * e + 1], f);
-              }
-              uint8_t* const slab = out + s * C::SLAB;
-              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-            }
-          } else {
-#pragma unroll
-            for (int s = 0; s < C::NSLAB; ++s) {
-              const uint32_t xs[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
-              uint8_t* const slab = out + s * C::SLAB;
-              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-            }
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16(xs[e], &y[2 * e], &y[2 * e + 1]);
+            uint8_t* const slab = out + s * C::SLAB;
+            *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(slab + sw128_offset(row, 2 * c4 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
         }
         fence_proxy_async_smem();
@@ -443,26 +435,6 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             p.desc[blockIdx.x] = make_int4(rq.a, u.row0, cur.head << 16 | imin(RT, rq.R - u.row0), g0);
           }
         }
-        if (u.valid == 1) {
-          // the largest V scale of the pages that the part sees, four pages a lane in flight
-          float top = 0.f;
-          const int k0 = imax(u.lo, u.j0 * KT), k1 = imin(u.hi, u.j1 * KT);
-          const int pg1 = k1 > k0 ? ((k1 - 1) >> p.page_log2) + 1 : 0;
-          for (int pg = (k0 >> p.page_log2) + lane; pg < pg1; pg += 128) {
-            int b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              b[i] = pg + 32 * i < pg1 ? p.table[u.n * p.table_stride + pg + 32 * i] : -1;
-              if (b[i] >= p.num_blocks) b[i] = -1;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (b[i] >= 0) top = fmaxf(top, p.v_scale[static_cast<int64_t>(b[i]) * p.HKV + u.head]);
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          u.vref = top < 0x1p-126f ? 0.f : top;
-        }
         const uint32_t slot = uc & 1;
         if (uc >= 2 && !mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wu, kErrWaitTile)) break;
         if (lane == 0) {
@@ -494,14 +466,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         const PrUnit u = next_unit(uc, &ok);
         if (!ok || !u.valid) break;
         if (u.valid == 2) continue;
-        const float vinv = u.vref > 0.f ? 1.f / u.vref : 0.f;
         const int k_end = imin(u.hi, u.j1 * KT);
         auto look_up = [&](int k0) {  // table entry of keys [k0, k0 + 16), -1 where nothing is seen
           return k0 >= k_end || k0 + 16 <= u.lo ? -1 : p.table[u.n * p.table_stride + (k0 >> p.page_log2)];
         };
         auto held = [&](int b) { return b >= 0 && b < p.num_blocks; };
         int blk = -1, nblk = look_up(u.j0 * KT + lane * 16);
-        float ksc = -1.f, vra = 0.f, nks = 0.f, nvs = 0.f;
+        float ksc = -1.f, vlg = 0.f, vin = 1.f, nks = 0.f, nvs = 0.f;
         auto scales_of = [&]() {
           if (!held(nblk)) return;
           const int64_t at = static_cast<int64_t>(nblk) * p.HKV + u.head;
@@ -512,7 +483,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
           const int q4 = (j - u.j0) & 3;
           if (q4 == 0) {
             blk = held(nblk) ? nblk : -1;
-            ksc = blk >= 0 ? nks : -1.f, vra = blk >= 0 ? nvs * vinv : 0.f;
+            ksc = blk >= 0 ? nks : -1.f, vlg = blk >= 0 ? log2f(nvs) : 0.f;
+            vin = fabsf(vlg) <= kFarScale ? 1.f / (blk >= 0 ? nvs : 1.f) : NAN;
             nblk = look_up((j + 4) * KT + lane * 16);
           } else if (q4 == 2) {
             scales_of();
@@ -530,7 +502,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
               // the block's scales (the ring is deep enough that its last readers are done)
               const uint32_t sr = (ic >> 1) % kScaleRing;
               k_scales[sr * kGroups + lane % kGroups] = ksc;
-              v_ratios[sr * kGroups + lane % kGroups] = vra;
+              v_logs[sr * kGroups + lane % kGroups] = vlg;
+              v_invs[sr * kGroups + lane % kGroups] = vin;
             }
             __syncwarp();
             if (lane == 0) {
@@ -699,8 +672,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[Q_FULL0 + w]);
     }
-    // (rows past the request's last one go along with a max of their own)
-    float m_used = live ? -INFINITY : 0.f, l = 0.f;
+    // The row's weights, their sum l and O are at 2^ref.  (Rows past the request's last one go
+    // along with a max of their own.)
+    float m_used = live ? -INFINITY : 0.f, l = 0.f, ref = kKvRefNone, most = most_sum(ref);
     for (int jh = 2 * tl.lo; jh < 2 * tl.hi; ++jh) {
       const int h2 = jh & 1, k0 = jh * HK;
       const uint32_t tS = tmem + lane_off + C::T_S + w * 128 + h2 * 64;
@@ -713,6 +687,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       tmem_ld32(tS + 32, sr + 32);
       const float* const sc = k_scales + ((bc0 + (jh >> 1) - u.j0) % kScaleRing) * kGroups + h2 * 4;
       const float4 sa = *reinterpret_cast<const float4*>(sc);
+      const float4 sb = *reinterpret_cast<const float4*>(sc + kScaleRing * kGroups);
+      const float4 si = *reinterpret_cast<const float4*>(sc + 2 * kScaleRing * kGroups);
       float f[4] = {sa.x, sa.y, sa.z, sa.w};
       bool masked = k0 < tl.all_lo || k0 + HK > tl.all_hi;
 #pragma unroll
@@ -725,34 +701,41 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
 #pragma unroll
       for (int g = 0; g < 4; ++g) f[g] = fmaxf(fabsf(f[g]) * rs, 0x1p-126f);  // (0 times -inf would be NaN)
       const int v_lo = my_lo - k0, v_hi = my_hi - k0;
-      // One pass with the max at hand, no max taken: while the block's sum of P
-      // stays at or below 2^15, no P is above it, which fp16 and the f32 sums
-      // hold as well as P up to 1.  Past that (or at a row's first key), the max
-      // is found and the block computed again (its scores are still there: P is
-      // stored last).
+      // One pass with the max at hand, no max taken: while the half block's sums of P
+      // and of the weights stay at or below 2^15, none is above it, which fp16 and
+      // the f32 sums hold as well as smaller ones.  Past that (or at a row's first
+      // key), the max is found and the half computed again (its scores are still
+      // there: the weights are stored last).
       const bool first = m_used == -INFINITY;
-      float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      float2 sum;  // of P at 2^ref
       bool need = first;  // (row by row, so that no row's result depends on another's)
       {
         uint32_t pw[HK / 2];
-        const float msub = first ? 0.f : m_used;
-        const float2 nm2 = make_float2(-msub, -msub);
+        const float base = ref - (first ? 0.f : m_used);
+        const float b[4] = {sb.x + base, sb.y + base, sb.z + base, sb.w + base};
         tmem_ld_wait();
         if (__builtin_expect(masked, 0)) {
 #pragma unroll
           for (int k = 0; k < HK; ++k)
             if (k < v_lo || k >= v_hi || (no_page >> (k / 16) & 1u)) sr[k] = __float_as_uint(-INFINITY);
         }
+        float2 part[4];  // sums of the weights of each group
 #pragma unroll
         for (int e = 0; e < HK / 2; ++e) {
-          const float fg = f[e / 8];
+          const float fg = f[e / 8], bg = b[e / 8];
           const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
-                                      make_float2(fg, fg), nm2);
-          const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-          sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
-          pw[e] = pack2<false>(pp.x, pp.y);
+                                      make_float2(fg, fg), make_float2(bg, bg));
+          const float2 w = make_float2(ex2(y.x), ex2(y.y));
+          part[e / 8] = e % 8 == 0 ? w : __fadd2_rn(part[e / 8], w);
+          pw[e] = pack2<false>(w.x, w.y);
         }
-        need |= !((sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y) <= kMostSum);
+        const float2 all = __fadd2_rn(__fadd2_rn(part[0], part[1]), __fadd2_rn(part[2], part[3]));
+        sum = __fmul2_rn(part[0], make_float2(si.x, si.x));
+        sum = __ffma2_rn(part[1], make_float2(si.y, si.y), sum);
+        sum = __ffma2_rn(part[2], make_float2(si.z, si.z), sum);
+        sum = __ffma2_rn(part[3], make_float2(si.w, si.w), sum);
+        need |= !(sum.x + sum.y <= most && all.x + all.y <= kMostSum);
+        need &= live;
         if (__builtin_expect(!__any_sync(0xffffffffu, need), 1)) {
 #pragma unroll
           for (int h = 0; h < HK / 32; ++h) tmem_st16(tS + h * 16, pw + h * 16);
@@ -769,26 +752,33 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
                 x[k] = __float_as_uint(-INFINITY);
           }
         };
-        float m_new = m_used;
+        float m_new = m_used, top = -INFINITY;  // top: log2 of the largest weight here, beside the max
 #pragma unroll 1
         for (int h = 0; h < HK / 32; ++h) {
           uint32_t x[32];
           load_scores(h, x);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            float top = -INFINITY;
+            float mx = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) top = fmaxf(top, __uint_as_float(x[g * 16 + k]));
-            const float fg = h == 0 ? f[g] : f[2 + g];
-            m_new = fmaxf(m_new, top * fg);
+            for (int k = 0; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(x[g * 16 + k]));
+            mx *= h == 0 ? f[g] : f[2 + g];
+            m_new = fmaxf(m_new, mx);
+            top = fmaxf(top, mx + (g == 0 ? (h == 0 ? sb.x : sb.z) : (h == 0 ? sb.y : sb.w)));
           }
         }
-        const bool grew = need && m_new > m_used;
-        if (__any_sync(0xffffffffu, grew && !first)) {
+        float up = 0.f, now = ref;  // what the max grows by, the row's new ref
+        if (need && m_new != -INFINITY) {
+          up = first ? 0.f : m_new - m_used;
+          // the largest weight: one of these or, as it was where ref was set, an earlier one
+          now = weight_ref(first ? top - m_new : fmaxf(top - m_new, kKvTop - ref - up));
+          m_used = m_new;
+        }
+        if (__any_sync(0xffffffffu, !first && (up != 0.f || now != ref))) {
           // the tile's previous P V (of this unit: some max is finite) has completed before its O rows are scaled
           if (!(ok = mbar_wait_warp(&bars[O_DONE0 + 2 * w + (h2 ^ 1)], (c - 1 + h2) & 1, wc, kErrWaitDQFull))) break;
           tc_fence_after();
-          const float shrink = grew && !first ? ex2(m_used - m_new) : 1.f;
+          const float shrink = first ? 1.f : ex2(now - ref - up);
           l *= shrink;
 #pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -801,27 +791,34 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
             tmem_st16(tO + ch * 32 + 16, r + 16);
           }
         }
-        if (grew) m_used = m_new;
-        const float msub = m_used == -INFINITY ? 0.f : m_used;
-        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+        ref = now, most = most_sum(ref);
+        const float msub = m_used == -INFINITY ? 0.f : m_used, base = ref - msub;
+        sum = make_float2(0.f, 0.f);
 #pragma unroll 1
         for (int h = 0; h < HK / 32; ++h) {
           uint32_t x[32], pw[16];
           load_scores(h, x);
-          const float fa = h == 0 ? f[0] : f[2], fb = h == 0 ? f[1] : f[3];
+          float2 part[2];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float fg = e < 8 ? fa : fb;
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                        make_float2(fg, fg), make_float2(-msub, -msub));
-            const float2 pp = make_float2(ex2(y.x), ex2(y.y));
-            sum2[e & 1] = __fadd2_rn(sum2[e & 1], pp);
-            pw[e] = pack2<false>(pp.x, pp.y);
+          for (int g = 0; g < 2; ++g) {
+            const float fg = h == 0 ? f[g] : f[2 + g];
+            const float lv = g == 0 ? (h == 0 ? sb.x : sb.z) : (h == 0 ? sb.y : sb.w);
+            float iv = g == 0 ? (h == 0 ? si.x : si.z) : (h == 0 ? si.y : si.w), bg = lv + base, wg = 1.f;
+            if (!(iv == iv) || most < 0.f) bg = -msub, wg = weight_factor(lv, ref), iv = ex2(ref);  // P, and the weight as a product
+#pragma unroll
+            for (int e = 8 * g; e < 8 * g + 8; ++e) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                          make_float2(fg, fg), make_float2(bg, bg));
+              const float2 w = make_float2(ex2(y.x), ex2(y.y));
+              part[g] = e % 8 == 0 ? w : __fadd2_rn(part[g], w);
+              pw[e] = pack2<false>(w.x * wg, w.y * wg);
+            }
+            sum = __ffma2_rn(part[g], make_float2(iv, iv), sum);
           }
           tmem_st16(tS + h * 16, pw);  // over scores that have been read for good
         }
       }
-      l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      l += sum.x + sum.y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -836,10 +833,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
     }
     const bool whole = u.slot < 0;
     const int64_t prow = whole ? 0 : static_cast<int64_t>(u.slot) * RT + w * BQ + trow;
-    const float fo = whole ? (l == 0.f ? 0.f : u.vref / l) : u.vref;
+    const float back = ex2(-ref), fo = whole ? (l == 0.f ? 0.f : 1.f / l) : back;
     if (live) {
-      if (whole) store_lse(p, pos, hq, m_used, l);
-      else p.part_ml[prow] = make_float2(m_used, l);
+      if (whole) store_lse(p, pos, hq, m_used, l * back);
+      else p.part_ml[prow] = make_float2(m_used, l * back);
     }
 #pragma unroll 1
     for (int ch = 0; ch < D / 32; ++ch) {

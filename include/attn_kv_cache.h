@@ -135,11 +135,11 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * sm_scale finite and > 0.
  * The products run on fp16 operands with f32 sums, for either dtype of q: e4m3
  * values are exact in fp16, each q row is brought into fp16's range by a power
- * of two of its own, K scales multiply the f32 scores, and P is rounded to fp16.
- * V scales enter relative to the largest one met: for requests of few rows
- * (queries * heads of a group) they multiply P before its rounding, for many
- * rows they multiply V, which is exact for powers of two (as
- * attn_kv_cache_write makes them) and rounds V to fp16 once for others.
+ * of two of its own, K scales multiply the f32 scores, and V scales multiply P in
+ * f32.  These weights, P vs, are rounded to fp16 once, after a power of two of the
+ * row's own that follows its largest one: V scales of any size and spread serve
+ * (down to 2^-88; smaller weights than that lose bits), and what a row does not
+ * see, or gives no weight, costs it nothing.
  * Requests of few rows are served by one kernel and those of many by another,
  * both queued where the batch may hold both; rows whose keys were split over
  * CTAs are joined by a last launch.  No length is needed on the host.  Pages may

@@ -77,6 +77,7 @@ def pages_of(prob, n, first, last):
 
 
 FEW = [([(6, 66)], 2, 2, 64, 16), ([(4, 1026)], 8, 2, 128, 64), ([(3, 2050), (1, 40), (2, 130)], 6, 1, 128, 128)]
+MANY = [([(150, 200)], 2, 1, 64, 16), ([(300, 700)], 4, 4, 128, 64), ([(90, 5000), (70, 90)], 2, 1, 64, 32)]
 
 
 @pytest.mark.parametrize("up", [2.0 ** 26, 1.3 * 2.0 ** 24, 2.0 ** 40])
@@ -94,6 +95,16 @@ def test_few_rows_beside_a_page_that_some_do_not_see(case, up):
     begin = (L - m) // page * page
     prob[4][pages_of(prob, 0, begin - page, begin)] *= np.float32(up)
     check(prob, "bf16", window=L - begin - m // 2)
+
+
+@pytest.mark.parametrize("up", [2.0 ** 26, 1.3 * 2.0 ** 24, 2.0 ** 40])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_rows_beside_pages_that_some_do_not_see(case, up):
+    lens, HQ, HKV, D, page = MANY[case]
+    prob = attend_problem("bf16", lens, HQ, HKV, D, page, 210 + case)
+    m, L = lens[0]
+    prob[4][pages_of(prob, 0, L - m // 2, L)] *= np.float32(up)
+    check(prob, "bf16")
 
 
 def against(prob, n, first, last, size):
@@ -114,7 +125,7 @@ def against(prob, n, first, last, size):
 
 
 @pytest.mark.parametrize("page,up", [(16, 2.0 ** 16), (64, 2.0 ** 20), (32, 1.7 * 2.0 ** 25)])
-@pytest.mark.parametrize("lens,HQ,D", [([(1, 900)], 2, 64), ([(1, 5000), (1, 700)], 1, 128)])
+@pytest.mark.parametrize("lens,HQ,D", [([(1, 900)], 2, 64), ([(1, 5000), (1, 700)], 1, 128), ([(100, 1000)], 1, 128)])
 def test_a_far_larger_page_of_no_weight(lens, HQ, D, page, up):
     """Scores of 100 below the others': its V scale says nothing about the row."""
     prob = attend_problem("f16", lens, HQ, HQ, D, page, 220 + page)
@@ -128,7 +139,7 @@ def test_a_far_larger_page_of_no_weight(lens, HQ, D, page, up):
 
 @pytest.mark.parametrize("vs", [0.0, 2.0 ** -100])
 @pytest.mark.parametrize("at", [0, 3])
-@pytest.mark.parametrize("lens,HQ,D", [([(1, 900)], 2, 64), ([(1, 5000)], 1, 128)])
+@pytest.mark.parametrize("lens,HQ,D", [([(1, 900)], 2, 64), ([(1, 5000)], 1, 128), ([(100, 1000)], 1, 64)])
 def test_a_page_of_zeros_with_the_weight(lens, HQ, D, at, vs):
     """A page of zero values far above the others in score (a sink), met first or
     later: what little the others weigh is all there is of O."""
@@ -140,7 +151,7 @@ def test_a_page_of_zeros_with_the_weight(lens, HQ, D, at, vs):
     check(prob, "bf16")
 
 
-@pytest.mark.parametrize("lens", [[(1, 3000), (5, 77)]])
+@pytest.mark.parametrize("lens", [[(1, 3000), (5, 77)], [(120, 600)]])
 @pytest.mark.parametrize("name", ["f16", "bf16"])
 def test_scales_of_any_size(name, lens):
     """V scales of the pages spread over 2^60, no powers of two; some are zero."""
