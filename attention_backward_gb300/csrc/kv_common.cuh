@@ -28,13 +28,16 @@ __device__ __forceinline__ float to_top(float amax, float* back) {
 
 // The weight of key j in O_i is p_ij vs_j, p = 2^(x - m_i) and vs its page's V scale.
 // It is rounded to fp16 as p vs 2^ref_i, ref_i a whole number of the row's own: where
-// it is set, the row's largest weight so far lands in (2^(kKvTop - 1), 2^kKvTop].  (Set
-// for a whole unit by its pages' largest V scale, it let the weights of rows that
-// do not see that page, or give it none, fall below fp16's range.)
-constexpr float kKvTop = 0.f;
+// it is set, the row's largest weight so far lands in (2^(top - 1), 2^top], top being the
+// kernel's.  Below fp16's normal range, from 2^(-14 - top) of that largest on, a weight
+// keeps the steps of 2^(-24 - top) of it; above, there is room to grow before ref is
+// set anew.  (Set for a whole unit by its pages' largest V scale, ref let the weights of
+// rows that do not see that page, or give it none, fall below fp16's range.  At a top
+// of 0, the many small weights beside one large one, a sink, were lost from 2^-25 on,
+// while l counted them whole.)
 constexpr float kKvRefNone = 88.f;  // of a row that has met no weight above 2^-88
-__device__ __forceinline__ float weight_ref(float log2_top) {
-  return fminf(fmaxf(kKvTop - ceilf(log2_top), -126.f), kKvRefNone);
+__device__ __forceinline__ float weight_ref(float top, float log2_top) {
+  return fminf(fmaxf(top - ceilf(log2_top), -126.f), kKvRefNone);
 }
 // 2^(log2 vs + ref), finite also where a row without weights meets a large scale
 // (its p are then tiny or 0).

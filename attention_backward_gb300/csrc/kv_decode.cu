@@ -59,6 +59,7 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 // Ring of slots (one tile each) per warp: with the 8 or 12 warps of an SM, 96 to
 // 128 KB in flight; a third slot made every case 1 to 4 % slower.
 constexpr int kStages = 2;
+constexpr float kTop = 7.f;      // of weight_ref; with the growth below, weights stay at 2^15, in fp16
 constexpr float kRescale = 8.f;  // log2 growth of a row's max, or largest weight, that triggers a rescale
 // Fewest line positions of a worker: below it, more parts cost more to join
 // than they save.
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
         }
         // ---- a max or a weight that grew past its threshold: rescale the row
         auto most = [&](int z, int e, int y) {  // score, relative to nm, up to which neither did
-          return fminf(th[e][y], kKvTop + kRescale - (lv[z] + ref[e][y]));
+          return fminf(th[e][y], kTop + kRescale - (lv[z] + ref[e][y]));
         };
         bool grew = false;
 #pragma unroll
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, (DecCfg<D, NB>::CTAS))
                 const bool first = th[e][y] == -INFINITY;
                 const float up = mx > th[e][y] ? mx : 0.f;
                 // the largest weight: this tile's or, as it was where ref was set, an earlier one's
-                const float now = weight_ref(first ? top - up : fmaxf(top, kKvTop - ref[e][y]) - up);
+                const float now = weight_ref(kTop, first ? top - up : fmaxf(top, kTop - ref[e][y]) - up);
                 f[y] = first ? 0.f : ex2(now - ref[e][y] - up);
                 l[e][y] *= first ? 0.f : ex2(-up);
                 ref[e][y] = now;

@@ -52,6 +52,10 @@ constexpr int kWarps = 16, THREADS = kWarps * 32;
 constexpr uint32_t REG_SOFT = 168, REG_CTL = 88, REG_CONV = 88;
 static_assert(2 * REG_SOFT + REG_CTL + REG_CONV == 4 * 128, "register split must equal the launch's registers");
 constexpr float kMostSum = 32768.f;  // of half a block's P, or weights, before a row's max is taken anew
+// Of weight_ref.  The room from here to kMostSum decides how often a row's max is taken
+// anew: the chunk case takes 528 us at 0 to 3, 531 to 536 at 4, 548 at 6, 556 at 7, cross
+// attention 57.7, 58.5, 59.2, 62.8, 63.7.
+constexpr float kTop = 3.f;
 // Largest |log2| of a V scale whose weights' sum gives l: the weights of P down to
 // 2^-36 then stay above f32's 2^-126 while ref is -45 or more.  A group with another
 // (0, or 2^-100 of a page of zeros), or a row with a smaller ref, sends its half
@@ -771,7 +775,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
         if (need && m_new != -INFINITY) {
           up = first ? 0.f : m_new - m_used;
           // the largest weight: one of these or, as it was where ref was set, an earlier one
-          now = weight_ref(first ? top - m_new : fmaxf(top - m_new, kKvTop - ref - up));
+          now = weight_ref(kTop, first ? top - m_new : fmaxf(top - m_new, kTop - ref - up));
           m_used = m_new;
         }
         if (__any_sync(0xffffffffu, !first && (up != 0.f || now != ref))) {

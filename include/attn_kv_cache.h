@@ -139,7 +139,9 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * f32.  These weights, P vs, are rounded to fp16 once, after a power of two of the
  * row's own that follows its largest one: V scales of any size and spread serve
  * (down to 2^-88; smaller weights than that lose bits), and what a row does not
- * see, or gives no weight, costs it nothing.
+ * see, or gives no weight, costs it nothing.  Weights below 2^-21 (few rows: queries
+ * * heads of a group) or 2^-17 (many) of the row's largest are held in steps of 2^-31
+ * or 2^-27 of it.
  * Requests of few rows are served by one kernel and those of many by another,
  * both queued where the batch may hold both; rows whose keys were split over
  * CTAs are joined by a last launch.  No length is needed on the host.  Pages may

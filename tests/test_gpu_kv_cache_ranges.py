@@ -10,11 +10,12 @@ bound of O, element by element, is
   2^-11 sum p |v|                           fp16 rounding of the weights
   sum p e |v| + |o| sum p e                 errors e_j of their exponents, in the
                                             numerator and the denominator
-  2^-25 / 2^(top - 1) n 448 max_j p_j vs_j  weights below fp16's normal range,
-                                            times bytes of at most 448
+  2^-25 / 2^(top - 1) max_j p_j vs_j sum b  weights below fp16's normal range, b the
+                                            absolute values that the bytes of the seen keys stand for
 with e_j = D 2^-23 sum |q||k_j| scale + 2^-21: f32 sums of D products, the rounding
 of the scaled score and of its power.  The LSE has sum p e + 2^-23 |lse| + 2^-20.
-Nothing of a key that the row does not see enters.  ``top`` = 0.
+Nothing of a key that the row does not see enters.  ``top``: FEW_TOP for the kernel of few rows, MANY_TOP
+for that of many (kv_decode.cu, kv_prompt.cu).
 """
 import numpy as np
 import pytest
@@ -24,15 +25,17 @@ from test_gpu_kv_cache import attend_problem, rounded, run_attend
 
 pytestmark = pytest.mark.gpu
 
+FEW_TOP, MANY_TOP = 7, 3
+
 
 def plain(prob, causal, window, scale):
     """Row by row: O, sum p |v|, the error of O by the exponents, LSE and its
-    error, the largest p vs and the keys seen.  Rows of no key have O = 0."""
+    error, the largest p vs times the sums of the bytes' values.  Rows of no key have O = 0."""
     q, kc, vc, ks, vs, table, cu, kv = prob
     T, HQ, D = q.shape
     page, HKV = kc.shape[1], kc.shape[2]
-    o, mag, oe = (np.zeros((T, HQ, D)) for _ in range(3))
-    lse, le, most, seen = np.full((T, HQ), -np.inf), *(np.zeros((T, HQ)) for _ in range(3))
+    o, mag, oe, low = (np.zeros((T, HQ, D)) for _ in range(4))
+    lse, le = np.full((T, HQ), -np.inf), np.zeros((T, HQ))
     for n, L in enumerate(kv):
         m = cu[n + 1] - cu[n]
         for i in range(m):
@@ -44,7 +47,8 @@ def plain(prob, causal, window, scale):
             for f in range(HQ):
                 h = f * HKV // HQ
                 K = oracle.E4M3[kc[blk, j % page, h]] * ks[blk, h][:, None]
-                V = oracle.E4M3[vc[blk, j % page, h]] * vs[blk, h][:, None]
+                b = oracle.E4M3[vc[blk, j % page, h]]
+                V = b * vs[blk, h][:, None]
                 x = K @ q[t, f] * scale
                 p = np.exp(x - x.max())
                 lse[t, f] = x.max() + np.log(p.sum())
@@ -52,20 +56,20 @@ def plain(prob, causal, window, scale):
                 e = D * 2.0 ** -23 * (np.abs(K) @ np.abs(q[t, f])) * scale + 2.0 ** -21
                 o[t, f], mag[t, f], le[t, f] = p @ V, p @ np.abs(V), p @ e
                 oe[t, f] = (p * e) @ np.abs(V) + np.abs(o[t, f]) * le[t, f]
-                most[t, f], seen[t, f] = (p * vs[blk, h]).max(), len(j)
-    return o, mag, oe, lse, le, most, seen
+                low[t, f] = (p * vs[blk, h]).max() * np.abs(b).sum(0)
+    return o, mag, oe, lse, le, low
 
 
 def check(prob, name, causal=True, window=-1, top=0):
     scale = prob[0].shape[2] ** -0.5
     got, glse = run_attend(prob, name, causal, window)
-    o, mag, oe, lse, le, most, seen = plain(prob, causal, window, scale)
+    o, mag, oe, lse, le, low = plain(prob, causal, window, scale)
     none = np.isneginf(lse)
     assert (got[none] == 0).all() and np.isneginf(glse.T[none]).all()
     el, tl = np.abs(glse.T - lse)[~none], (le + 2.0 ** -23 * np.abs(lse) + 2.0 ** -20)[~none]
     assert (el <= tl).all(), (el / tl).max()
     half, tiny = (2.0 ** -11, 2.0 ** -25) if name == "f16" else (2.0 ** -8, 0.0)
-    tol = half * np.abs(o) + (2.0 ** -11 * mag + oe + (2.0 ** (-24 - top) * 448 * seen * most)[..., None]) * (1 + half) + tiny
+    tol = half * np.abs(o) + (2.0 ** -11 * mag + oe + 2.0 ** (-24 - top) * low) * (1 + half) + tiny
     err = np.abs(got - o)
     assert np.isfinite(got).all() and (err <= tol).all(), (err / np.where(tol > 0, tol, 1)).max()
 
@@ -108,9 +112,9 @@ def test_many_rows_beside_pages_that_some_do_not_see(case, up):
 
 
 def against(prob, n, first, last, size):
-    """Keys [first, last) of request n, whole pages, point against its queries'
-    mean (size < 0) or along it (size > 0): scores of about ``size`` where the
-    queries are one."""
+    """Keys [first, last) of request n point against its queries' mean (size < 0) or
+    along it (size > 0): scores of about ``size`` where the queries are one.
+    (Their pages' K scales change: whole pages, but for the test of one key.)"""
     q, kc, _, ks, _, table, cu, _ = prob
     page, HKV = kc.shape[1], kc.shape[2]
     rows = q[cu[n]:cu[n + 1]]
@@ -163,3 +167,23 @@ def test_scales_of_any_size(name, lens):
     check(prob, name)
     check(prob, name, window=20)
     check(prob, name, causal=False)
+
+
+@pytest.mark.parametrize("lens,HQ,D", [([(1, 900)], 2, 64), ([(1, 40000)], 1, 128), ([(1, 5000), (1, 700)], 2, 128),
+                                       ([(100, 1000)], 1, 64), ([(80, 5000)], 1, 128)])
+@pytest.mark.parametrize("size", [14, 17, 18])
+def test_one_key_with_the_weight(lens, HQ, D, size):
+    """A key without value far above the others in score: weights of 2^-20, 2^-24.5
+    and 2^-26 of its own are all there is of O.  The others' scores are equal and
+    their values of one sign, so that what is lost of them adds up."""
+    prob = attend_problem("bf16", lens, HQ, HQ, D, 16, 250)
+    q, kc, vc, ks, vs, table, cu, kv = prob
+    q[:] = rounded(np.random.default_rng(8), (1, HQ, D), "bf16")
+    for n, L in enumerate(kv):
+        j = np.arange(L)
+        kc[table[n, j // 16], j % 16] = 0
+        vc[table[n, j // 16], j % 16] &= 0x7F
+        vs[table[n, j // 16]] = 2.0 ** -6
+        against(prob, n, 0, 1, size)
+        vc[table[n, 0], 0] = 0
+    check(prob, "bf16", top=FEW_TOP if lens[0][0] == 1 else MANY_TOP)
