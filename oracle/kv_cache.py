@@ -152,5 +152,5 @@ def forward(q, k_cache, v_cache, k_scale, v_scale, table, cu, kv_lens, scale, ca
                 if L:
                     dots[f, a:e] = np.where(see, (np.abs(Q) @ np.abs(K).T) * scale, 0).max(1)
                     seen[f, a:e] = see.sum(1)
-                    vmax[f, a:e] = np.abs(V).max()
+                    vmax[f, a:e] = np.where(see, np.abs(V).max(1), 0).max(1)
     return o, lse, mag, dots, seen, vmax
