@@ -169,6 +169,8 @@ def _cache(shape, seed, salt):
 def _tables(c, seed):
     """Block table of every request's pages (-1 behind them), in shuffled blocks."""
     ctx, new, kv = _lens(c)
+    if c["op"] == "tables":  # the new tokens get pages, whatever attends to them
+        kv = [x + y for x, y in zip(ctx, new)]
     p = c["page"]
     need = [(max(a, b) + p - 1) // p for a, b in zip(ctx, kv)]
     total = sum(need)
