@@ -162,7 +162,7 @@ def new_kv_cache(num_blocks: int, page_size: int, HKV: int, D: int, device=None)
     by head ([num_blocks, HKV, page_size, D] in memory, seen as [num_blocks,
     page_size, HKV, D]), so that what attention reads of a page for one head is
     contiguous."""
-    device = torch.device(device or "cuda")
+    device = torch.device("cuda" if device is None else device)
     kv = [torch.zeros(num_blocks, HKV, page_size, D, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
           .transpose(1, 2) for _ in range(2)]
     return (*kv, *(torch.zeros(num_blocks, HKV, dtype=torch.float32, device=device) for _ in range(2)))
