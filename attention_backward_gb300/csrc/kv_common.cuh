@@ -35,7 +35,7 @@ __device__ __forceinline__ float to_top(float amax, float* back) {
 // rows that do not see that page, or give it none, fall below fp16's range.  At a top
 // of 0, the many small weights beside one large one, a sink, were lost from 2^-25 on,
 // while l counted them whole.)
-constexpr float kKvRefNone = 88.f;  // of a row that has met no weight above 2^-88
+constexpr float kKvRefNone = 100.f;  // of a row that has met no weight above 2^-100, the smallest scale of a write
 __device__ __forceinline__ float weight_ref(float top, float log2_top) {
   return fminf(fmaxf(top - ceilf(log2_top), -126.f), kKvRefNone);
 }

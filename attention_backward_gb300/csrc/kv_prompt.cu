@@ -61,8 +61,10 @@ constexpr float kTop = 3.f;
 // (0, or 2^-100 of a page of zeros), or a row with a smaller ref, sends its half
 // block through the slow path.
 constexpr float kFarScale = 45.f;
-__device__ __forceinline__ float most_sum(float ref) {  // of a half block's P at 2^ref; -1: always the slow path
-  return ref < -kFarScale ? -1.f : kMostSum * ex2(ref);
+// Largest sum of a half block's P at 2^ref that goes into l as it is (l, a sum of one
+// for each 64 keys, stays finite at any ref); -1: none does.
+__device__ __forceinline__ float most_sum(float ref) {
+  return ref < -kFarScale ? -1.f : fminf(kMostSum * ex2(ref), 0x1p109f);
 }
 constexpr int kGroups = KT / 16;  // 16-key groups of a block: a page scale each
 constexpr int HK = 64;            // keys of a half block

@@ -138,7 +138,7 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * of two of its own, K scales multiply the f32 scores, and V scales multiply P in
  * f32.  These weights, P vs, are rounded to fp16 once, after a power of two of the
  * row's own that follows its largest one: V scales of any size and spread serve
- * (down to 2^-88; smaller weights than that lose bits), and what a row does not
+ * (rows whose weights are all below 2^-100 lose bits), and what a row does not
  * see, or gives no weight, costs it nothing.  Weights below 2^-21 (few rows: queries
  * * heads of a group) or 2^-17 (many) of the row's largest are held in steps of 2^-31
  * or 2^-27 of it.

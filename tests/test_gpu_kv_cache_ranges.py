@@ -187,3 +187,15 @@ def test_one_key_with_the_weight(lens, HQ, D, size):
         against(prob, n, 0, 1, size)
         vc[table[n, 0], 0] = 0
     check(prob, "bf16", top=FEW_TOP if lens[0][0] == 1 else MANY_TOP)
+
+
+@pytest.mark.parametrize("lens", [[(1, 3000), (5, 77)], [(120, 600), (70, 90)]])
+def test_rows_of_the_smallest_scales_alone(lens):
+    """Pages at a write's smallest scale, 2^-100, that some rows see alone and others
+    beside ordinary ones; their largest weights sit at 1."""
+    prob = attend_problem("bf16", lens, 4, 2, 64, 16, 260)
+    kv, vs = prob[7], prob[4]
+    for n, L in enumerate(kv):
+        vs[pages_of(prob, n, 0, L - (lens[n][0] + 1) // 2)] = 2.0 ** -100
+    check(prob, "bf16", top=0)
+    check(prob, "bf16", window=20, top=0)
