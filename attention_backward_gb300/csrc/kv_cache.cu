@@ -44,7 +44,11 @@ __device__ __forceinline__ Need request_need(int n, const KvTablesParams& p, int
 // over the 512 sums in shared memory, then a walk inside one thread's
 // requests).  Slots of fresh pages are computed from the free list, not read
 // back from the table, so blocks do not depend on one another.  3.7 us for 256
-// requests of one token, 4.5 us for 97 requests of 100753 tokens together.
+// requests of one token, 4.5 us for 97 requests of 100753 tokens together.  A token's
+// request is found by a walk inside a thread's share of them, ceil(N / 512), for each
+// token: made for thousands of requests, its work grows with N^2 (one token each,
+// whole calls: 27 us, the host's, up to 4096 requests, 72 us for 16384, 0.38 ms for
+// 65536, 45 ms for 2^20).
 __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const KvTablesParams p) {
   __shared__ int64_t s_tok[kTabThreads + 1], s_pg[kTabThreads + 1];
   __shared__ int64_t w_tok[kTabThreads / 32], w_pg[kTabThreads / 32], w_wide[kTabThreads / 32];
