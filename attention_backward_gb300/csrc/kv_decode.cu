@@ -8,8 +8,8 @@
 // with k_j, v_j the stored e4m3 values, in one pass with a running m (rescaled
 // only when it grows by more than 2^8).  Bound by the bytes of K and V: 2 D
 // bytes and 4 D G flops a key.  64 requests of up to 8192 keys, 32 query and 8 KV
-// heads of 128: 85 us, 6.2 TB/s (the plain copy reaches 6.8); 3 requests of up to
-// 131072, 4 KV heads: 42 us, 5.2 TB/s, of which 12 are start-up and the spread of
+// heads of 128: 87 us, 6.05 TB/s (the plain copy reaches 6.8); 3 requests of up to
+// 131072, 4 KV heads: 42 us, 5.1 TB/s, of which 12 are start-up and the spread of
 // the warps' ends; 128 windows of 1024 keys, 8 KV heads of 64: 35 us, 3.8 TB/s.
 //
 // Split: the line of kv_sched.cuh with units of 8 or 16 rows and tiles of 32

@@ -13,7 +13,7 @@
 // Bound by the tensor cores and the exponentials, with the bytes of K and V a
 // small part; what is new against the dense forward is that the operands have
 // to be made.  2048 + 1713 tokens on 14336 cached ones, 32 query and 8 KV heads of
-// 128: 499 us, 1.24 PFLOP/s, 64 % of the measured peak, held back by the issue of
+// 128: 514 us, 1.20 PFLOP/s, 62 % of the measured peak, held back by the issue of
 // the products (below).  TMA brings pages as bytes into a raw ring; four warps convert them
 // to fp16 (exact) in the 128-byte-swizzled tiles that the products read.  A
 // block's page scales (at most one per 16 keys) are applied by the softmax, 16
@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prompt_kernel(const __grid_cons
       const uint64_t t_kmaj = sdesc_sw128(sbase + C::OFF_T, 16, 1024);
       const uint64_t t_mn = sdesc_sw128(sbase + C::OFF_T, C::SLAB, 1024);
       // Turns taken so far, a bit each: of Q, P and O of tile w (bit w), of the slots.
-      // This warp is what the kernel waits for: of 4180 cycles a block it waits 900,
+      // This warp is what the kernel waits for: of 4180 cycles a block (before V scales
+      // went into the softmax's exponent, which made it 3 % longer) it waits 900,
       // the products take 2048, the rest is their issue beside a scheduler's softmax
       // and conversion warps.  Hence one body for both tiles (two copies, fetched
       // anew for every block, cost 5 %), the lane elected once (3 %).

@@ -142,9 +142,12 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * see, or gives no weight, costs it nothing.  Weights below 2^-21 (few rows: queries
  * * heads of a group) or 2^-17 (many) of the row's largest are held in steps of 2^-31
  * or 2^-27 of it.
- * Requests of few rows are served by one kernel and those of many by another,
- * both queued where the batch may hold both; rows whose keys were split over
- * CTAs are joined by a last launch.  No length is needed on the host.  Pages may
+ * One kernel is made for requests of few rows and another for many; either serves
+ * any.  No length is needed on the host: it queues one of them or both by the mean
+ * of rows a request, T (padding rows included) * HQ / HKV / num_seqs, so that a request
+ * far from its batch's mean may run in the slower one (both from 16 to 259; below, a
+ * long chunk beside many single tokens takes up to five times its time).  Rows whose keys
+ * were split over CTAs are joined by a last launch.  Pages may
  * be listed by several requests, and twice by one.  o, lse and the workspace
  * overlap no input and not each other.
  *   workspace : attn_fwd_kv_cache_workspace_size(T, HQ, HKV, D) bytes, 16-byte
