@@ -137,9 +137,10 @@ ATTN_BWD_API size_t attn_fwd_kv_cache_workspace_size(int64_t T, int64_t HQ, int6
  * values are exact in fp16, each q row is brought into fp16's range by a power
  * of two of its own, K scales multiply the f32 scores, and V scales multiply P in
  * f32.  These weights, P vs, are rounded to fp16 once, after a power of two of the
- * row's own that follows its largest one: V scales of any size and spread serve
- * (rows whose weights are all below 2^-100 lose bits), and what a row does not
- * see, or gives no weight, costs it nothing.  Weights below 2^-21 (few rows: queries
+ * row's own that follows its largest one: V scales of any spread serve, up to 2^70
+ * (rows of split keys are summed before they are divided by l), and what a row
+ * does not see, or gives no weight, costs it nothing.  (Rows whose weights are all
+ * below 2^-100 lose bits.)  Weights below 2^-21 (few rows: queries
  * * heads of a group) or 2^-17 (many) of the row's largest are held in steps of 2^-31
  * or 2^-27 of it.
  * One kernel is made for requests of few rows and another for many; either serves

@@ -199,3 +199,14 @@ def test_rows_of_the_smallest_scales_alone(lens):
         vs[pages_of(prob, n, 0, L - (lens[n][0] + 1) // 2)] = 2.0 ** -100
     check(prob, "bf16", top=0)
     check(prob, "bf16", window=20, top=0)
+
+
+@pytest.mark.parametrize("lens", [[(1, 9000), (5, 77)], [(120, 4000), (70, 90)]])
+def test_scales_up_to_the_largest(lens):
+    """2^70, on rows whose keys are split over workers too, alone and beside ordinary pages."""
+    prob = attend_problem("bf16", lens, 4, 2, 64, 16, 270)
+    q, kc, vc, ks, vs, table, cu, kv = prob
+    check((q, kc, vc, ks, vs * 2.0 ** 75, table, cu, kv), "bf16", top=0)
+    rng = np.random.default_rng(9)
+    some = vs * np.where(rng.random(vs.shape) < 0.3, 2.0 ** 75, 1.0)
+    check((q, kc, vc, ks, some, table, cu, kv), "bf16", window=100, top=0)
