@@ -42,3 +42,15 @@ from ._kv_cache import (  # noqa: F401
     kv_cache_write,
     new_kv_cache,
 )
+from ._latent import (  # noqa: F401
+    RopeTable,
+    forward_latent,
+    forward_latent_cache,
+    latent_cache_workspace_size,
+    latent_cache_write,
+    new_latent_cache,
+    rope,
+    rope_frequencies,
+    rope_table,
+    sparse_forward,
+)

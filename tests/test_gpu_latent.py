@@ -1,0 +1,361 @@
+"""GPU parity of latent attention (cache, lists, expanded form) with its float64
+definition.
+
+The bound of O, element by element, with p the normalised weights over n keys (parts
+from oracle/latent.py):
+  eps/2 |o|                        the rounding of the output
+  eps/2 sum p |v|                  rounding of the weights to the 16-bit type
+  sum p e |v| + |o| sum p e        errors of the weights' exponents
+  2 n 2^-24 sum p |v|              f32 sums of O and l
+  2^-32 sum |v|                    fp16: weights below the normal range, steps of 2^-24
+                                   where the row's largest is 2^7 or more
+The LSE has sum p e + n 2^-24 + 2^-23 |lse| + 2^-20.
+"""
+import numpy as np
+import pytest
+
+from oracle import latent as oracle
+from test_gpu_rope import EPS, dt_of, f64, i32, rounded
+
+pytestmark = pytest.mark.gpu
+
+
+def near(o, lse, r, name):
+    """o [..., H, dv] and lse [..., H] against r; rows that r leaves NaN are not looked at."""
+    o, lse = f64(o), f64(lse)
+    known = ~np.isnan(r.lse)
+    none = np.isneginf(r.lse)
+    assert (o[none] == 0).all() and np.isneginf(lse[none]).all()
+    live = known & ~none
+    n = r.seen[live]
+    tol = EPS[name] * (np.abs(r.o) + r.mag)[live] + r.oe[live] + (2 * n * 2.0 ** -24)[:, None] * r.mag[live]
+    tol += (2.0 ** -32 if name == "f16" else 0) * r.low[live] + 2.0 ** -25
+    err = np.abs(o[live] - r.o[live])
+    assert (err <= tol).all(), (err / tol).max()
+    tol = r.le[live] + n * 2.0 ** -24 + 2.0 ** -23 * np.abs(r.lse[live]) + 2.0 ** -20
+    err = np.abs(lse[live] - r.lse[live])
+    assert (err <= tol).all(), (err / tol).max()
+
+
+def cache_problem(kv, new, H, page, name, seed, spare=3, size=1.0):
+    rng = np.random.default_rng(seed)
+    need = [-(-max(0, x) // page) for x in kv]
+    nb = sum(need) + spare
+    order = rng.permutation(nb)
+    table = np.full((len(kv), max(1, max(need))), -1)
+    at = 0
+    for r, m in enumerate(need):
+        table[r, :m] = order[at:at + m]
+        at += m
+    q = rounded(rng, (1, sum(new), H, 576), name, size)
+    cache = rounded(rng, (nb, page, 576), name)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    return q, cache, table, cu, np.asarray(kv)
+
+
+def run_cache(prob, scale, causal=True, **kw):
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    q, cache, table, cu, kv = prob
+    T, H = q.shape[1:3]
+    out = (torch.full((1, T, H, 512), float("nan"), dtype=q.dtype, device="cuda"), torch.full((1, H, T), float("nan"), device="cuda"))
+    ws = torch.full((ab.latent_cache_workspace_size(),), 255, dtype=torch.uint8, device="cuda")
+    kw = {"out": out, "workspace": ws, **kw}
+    o, lse = ab.forward_latent_cache(q, cache, i32(table), i32(cu), i32(kv), scale, causal=causal, **kw)
+    ab.check_error(ws)
+    return o[0], lse[0].t()
+
+
+def check_cache(prob, name, scale=192 ** -0.5, causal=True):
+    q, cache, table, cu, kv = prob
+    r = oracle.cache_forward(f64(q)[0], f64(cache), table, cu, kv, scale, causal)
+    near(*run_cache(prob, scale, causal), r, name)
+
+
+@pytest.mark.parametrize("kv,new,H,page,name,causal", [
+    ([1], [1], 1, 16, "bf16", True), ([5], [1], 16, 16, "f16", True), ([64], [1], 64, 64, "bf16", True),
+    ([65], [1], 128, 32, "f16", True), ([384], [1], 16, 16, "bf16", True), ([1000, 3, 0, 77], [1, 1, 1, 1], 64, 128, "bf16", True),
+    ([700, 129, 64], [3, 2, 5], 20, 16, "f16", True), ([40, 200], [40, 7], 32, 64, "bf16", True),
+    ([3000], [2], 128, 64, "bf16", True), ([250, 90, 333], [1, 0, 1], 96, 32, "f16", True),
+    ([100, 31], [6, 4], 48, 16, "bf16", False), ([10, 5], [12, 9], 8, 16, "f16", True), ([0, 0], [2, 1], 64, 64, "bf16", True),
+    ([5000, 2, 900, 64, 1, 4000], [1, 1, 1, 1, 1, 1], 64, 64, "f16", True), ([300], [300], 3, 32, "bf16", True)])
+def test_cache(kv, new, H, page, name, causal):
+    check_cache(cache_problem(kv, new, H, page, name, 10 + sum(kv)), name, causal=causal)
+
+
+def test_cache_many_short_requests():
+    rng = np.random.default_rng(3)
+    kv, new = rng.integers(0, 200, 700).tolist(), rng.integers(0, 3, 700).tolist()
+    check_cache(cache_problem(kv, new, 4, 16, "bf16", 5), "bf16")
+    check_cache(cache_problem(kv[:100], [2] * 100, 40, 32, "f16", 6), "f16")
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_cache_scores_of_any_size(name):
+    """Large scores, rising along the keys (a new reference again and again), a
+    sink far above many small weights, and all scores far below zero."""
+    q, cache, table, cu, kv = cache_problem([900, 700], [2, 3], 40, 64, name, 7)
+    import torch
+
+    flat = torch.from_numpy(table[0]).cuda()
+    ramp = torch.linspace(-3, 3, 64 * len(flat[flat >= 0]), device="cuda").view(-1, 64, 1)
+    cache[flat[flat >= 0], :, 512:] = ramp.to(cache.dtype)
+    q[0, :2, :, 512:] = 1.5
+    check_cache((q, cache, table, cu, kv), name, scale=0.25)
+    cache[flat[0], 0, 512:] = 6.0  # the sink
+    check_cache((q, cache, table, cu, kv), name, scale=0.04)
+    q[0, :2, :, 512:] = -20.0
+    cache[flat[flat >= 0], :, 512:] = 10.0
+    check_cache((q, cache, table, cu, kv), name, scale=0.3)
+
+
+def test_cache_ignores_what_no_query_sees():
+    """NaN behind the last key, in free pages and in pages that the table names past
+    the lengths; entries outside the cache are not visible; rows past the last request
+    are not written."""
+    import torch
+
+    q, cache, table, cu, kv = cache_problem([130, 17, 64], [2, 1, 3], 24, 32, "f16", 9)
+    want = run_cache((q, cache, table, cu, kv), 0.1)
+    used = np.zeros(cache.shape[:2], bool)
+    for r, n in enumerate(kv):
+        for p in range(n):
+            used[table[r, p // 32], p % 32] = True
+    cache[torch.from_numpy(~used).cuda()] = float("nan")
+    wide = np.concatenate([table, np.full((3, 2), cache.shape[0] - 1)], 1)
+    got = run_cache((q, cache, wide, cu, kv), 0.1)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    holes = table.copy()
+    holes[0, 1], holes[0, 3], holes[2, 1] = -1, cache.shape[0], 2 ** 31 - 1
+    q2 = torch.cat([q, q[:, :2]], 1)  # two rows of no request
+    prob = (q2, cache, holes, cu, kv)
+    o, lse = run_cache(prob, 0.1)
+    near(o, lse, oracle.cache_forward(f64(q2)[0], np.nan_to_num(f64(cache)), holes, cu, kv, 0.1), "f16")
+    assert o[-2:].isnan().all() and lse[-2:].isnan().all()
+    # a table narrower than the lengths: keys past its width are not visible
+    narrow = (q, cache, table[:, :2], cu, kv)
+    near(*run_cache(narrow, 0.1), oracle.cache_forward(f64(q)[0], np.nan_to_num(f64(cache)), table[:, :2], cu, kv, 0.1), "f16")
+
+
+def test_cache_strides_shared_pages_and_repeats():
+    """Rows of q and o inside wider tensors, a cache of wider rows, one prefix listed by
+    several requests and twice by one; the same call again gives the same bits."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    q, cache, table, cu, kv = cache_problem([200, 200, 96], [1, 2, 1], 72, 32, "bf16", 11)
+    table[1, :4] = table[0, :4]
+    table[2, 1] = table[2, 0]
+    prob = (q, cache, table, cu, kv)
+    check_cache(prob, "bf16")
+    want = run_cache(prob, 0.07)
+    wide_q = torch.zeros(1, 4, 80, 600, dtype=q.dtype, device="cuda")
+    wide_q[:, :, 4:76, 8:584] = q
+    wide_c = torch.zeros(*cache.shape[:2], 584, dtype=q.dtype, device="cuda")
+    wide_c[:, :, 8:] = cache
+    wide_o = torch.zeros(1, 72, 4, 520, dtype=q.dtype, device="cuda").transpose(1, 2)  # head by head
+    lse = torch.zeros(1, 4, 72, device="cuda").transpose(1, 2)
+    got = run_cache((wide_q[:, :, 4:76, 8:584], wide_c[:, :, 8:], table, cu, kv), 0.07, out=(wide_o[..., 8:], lse))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and (wide_o[..., :8] == 0).all()
+    again = run_cache(prob, 0.07)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    o, l = ab.forward_latent_cache(q[:, :0], cache, i32(table), i32(cu * 0), i32(kv), 0.1)
+    assert o.shape == (1, 0, 72, 512) and l.shape == (1, 72, 0)
+
+
+def test_cache_graphs_and_streams():
+    """A captured step replays over longer lengths; calls on two streams with
+    workspaces of their own do not disturb each other."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    q, cache, table, cu, kv = cache_problem([700, 300], [1, 1], 32, 64, "bf16", 13)
+    t, c, n = i32(table), i32(cu), i32(kv - 100)
+    ws = [torch.empty(ab.latent_cache_workspace_size(), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = (torch.empty(1, 2, 32, 512, dtype=q.dtype, device="cuda"), torch.empty(1, 32, 2, device="cuda"))
+    call = lambda out, w, **k: ab.forward_latent_cache(q, cache, t, c, n, 0.1, workspace=w, out=out, **k)  # noqa: E731
+    first = [x.clone() for x in call(out, ws[0])]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, ws[0])
+    n += 100
+    graph.replay()
+    near(out[0][0], out[1][0].t(), oracle.cache_forward(f64(q)[0], f64(cache), table, cu, kv, 0.1), "bf16")
+    assert not torch.equal(out[0], first[0])
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(x) for x in out] for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            call(tuple(outs[i]), ws[i], stream=st[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, out))
+
+
+@pytest.mark.parametrize("B,S,SKV,H,HKV,topk,name", [
+    (1, 1, 1, 1, 1, 1, "bf16"), (1, 40, 300, 64, 1, 130, "bf16"), (2, 21, 90, 96, 3, 64, "f16"), (1, 9, 70, 48, 2, 65, "f16"),
+    (1, 170, 170, 16, 1, 7, "bf16"), (1, 5, 2000, 64, 1, 1111, "f16")])
+def test_lists(B, S, SKV, H, HKV, topk, name):
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(S + topk)
+    q, kv = rounded(rng, (B, S, H, 576), name), rounded(rng, (B, SKV, HKV, 576), name)
+    idx = rng.integers(0, SKV, (B, S, HKV, topk))  # (repeated rows count once a slot)
+    idx[rng.random(idx.shape) < 0.2] = -1
+    idx[rng.random(idx.shape) < 0.05] = SKV + 3
+    idx[rng.random(idx.shape) < 0.02] = -2 ** 31
+    if S > 4:
+        idx[:, 2] = -1
+        idx[:, 3, :, 1:] = -1
+        idx[:, 4, :, : topk - 1] = -1
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    out = (torch.full((B, S, H, 512), float("nan"), dtype=q.dtype, device="cuda"), torch.full((B, H, S), float("nan"), device="cuda"))
+    o, lse = ab.sparse_forward(q, kv, i32(idx), workspace=ws, out=out)
+    ab.check_error(ws)
+    near(o, lse.transpose(1, 2), oracle.list_forward(f64(q), f64(kv), idx, 576 ** -0.5), name)
+
+
+def test_lists_skip_rows_that_are_not_listed():
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(2)
+    q, kv = rounded(rng, (1, 6, 32, 576), "bf16"), rounded(rng, (1, 200, 1, 576), "bf16")
+    idx = i32(rng.integers(0, 100, (1, 6, 1, 90)) * 2)
+    want = ab.sparse_forward(q, kv, idx)
+    kv[:, 1::2] = float("nan")
+    got = ab.sparse_forward(q, kv, idx)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_sparse_training_step():
+    """Rotary positions, the forward over lists, the backward that takes its O and
+    LSE, and the gradients turned back, against the float64 definitions end to end.
+    The backward's own tolerance for these shapes is (1e-2, 2e-2)."""
+    import torch
+
+    import attention_backward_gb300 as ab
+    from oracle import attention
+
+    rng = np.random.default_rng(12)
+    S, H, topk = 140, 32, 100
+    table = ab.rope_table(64)
+    freqs, _ = ab.rope_frequencies(64)
+    q, kv, do = (rounded(rng, s, "bf16") for s in ((1, S, H, 576), (1, S, 1, 576), (1, S, H, 512)))
+    pos = i32(np.arange(S))
+    qr, kr = ab.rope(q, pos, table, k=kv, start=512, k_start=512)
+    idx = np.full((1, S, 1, topk), -1)
+    for t in range(S):
+        pick = np.sort(rng.permutation(t + 1)[:topk])
+        idx[0, t, 0, :len(pick)] = pick
+    o, lse = ab.sparse_forward(qr, kr, i32(idx))
+    near(o, lse.transpose(1, 2), oracle.list_forward(f64(qr), f64(kr), idx, 576 ** -0.5), "bf16")
+    dq, dkv = ab.sparse_backward(qr, kr, o, do, lse, i32(idx))
+    rq, rkv = attention.sparse_backward(f64(qr), f64(kr), f64(o), f64(do), f64(lse), idx, 576 ** -0.5, 512)
+    for got, ref in ((dq, rq), (dkv, rkv)):
+        assert (np.abs(f64(got) - ref) <= 1e-2 + 2e-2 * np.abs(ref)).all()
+    gq, gkv = ab.rope(dq, pos, table, k=dkv, start=512, k_start=512, inverse=True)
+    for got, x in ((gq, dq), (gkv, dkv)):
+        ref, size = oracle.turn(f64(x), 512, freqs, np.arange(S)[None, :, None], inverse=True)
+        assert (np.abs(f64(got) - ref) <= EPS["bf16"] * np.abs(ref) + 2.0 ** -20 * size).all()
+
+
+@pytest.mark.parametrize("B,S,Sk,H,causal,cu,name", [
+    (1, 1, 1, 1, True, None, "bf16"), (1, 128, 128, 2, True, None, "f16"), (2, 300, 300, 3, True, None, "bf16"),
+    (1, 257, 700, 2, True, None, "f16"), (1, 400, 130, 2, True, None, "bf16"), (2, 200, 450, 2, False, None, "f16"),
+    (1, 1, 900, 4, True, None, "bf16"), (1, 700, 700, 2, True, (0, 1, 1, 130, 390, 640), "bf16"),
+    (1, 520, 520, 2, False, (0, 257, 513), "f16"), (3, 1000, 1000, 1, True, None, "f16")])
+def test_expanded(B, S, Sk, H, causal, cu, name):
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(S + Sk)
+    q, up, kr = rounded(rng, (B, S, H, 192), name), rounded(rng, (B, Sk, H, 256), name), rounded(rng, (B, Sk, 64), name)
+    kn, v = up[..., :128], up[..., 128:]
+    ref = oracle.expanded_forward(f64(q), f64(kn), f64(kr), f64(v), 192 ** -0.5, causal, cu)
+    if cu is not None:  # rows of no sequence may hold anything
+        for x in (q, up, kr):
+            x[:, cu[-1]:] = float("nan")
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    out = (torch.full((B, S, H, 128), float("nan"), dtype=q.dtype, device="cuda"), torch.full((B, H, S), float("nan"), device="cuda"))
+    o, lse = ab.forward_latent(q, kn, kr, v, 192 ** -0.5, causal=causal, cu_seqlens=None if cu is None else i32(cu),
+                               workspace=ws, out=out)
+    ab.check_error(ws)
+    near(o, lse.transpose(1, 2), ref, name)
+    if cu is not None:
+        assert o[:, cu[-1]:].isnan().all() and lse[:, :, cu[-1]:].isnan().all()
+
+
+def test_expanded_sequences_do_not_touch_each_other():
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(21)
+    q, kn, kr, v = (rounded(rng, s, "bf16") for s in ((1, 400, 2, 192), (1, 400, 2, 128), (1, 400, 64), (1, 400, 2, 128)))
+    cu = i32([0, 150, 300, 400])
+    want = ab.forward_latent(q, kn, kr, v, 0.1, cu_seqlens=cu)
+    for x in (kn, kr, v):
+        x[:, 150:300] = float("nan")
+    got = ab.forward_latent(q, kn, kr, v, 0.1, cu_seqlens=cu)
+    for a, b in zip(got, want):
+        a, b = (x if x.dim() == 4 else x.transpose(1, 2) for x in (a, b))
+        assert torch.equal(a[:, :150], b[:, :150]) and torch.equal(a[:, 300:], b[:, 300:])
+
+
+@pytest.mark.parametrize("name", ["f16", "bf16"])
+def test_serving_step(name):
+    """A prompt and three tokens of two requests: plan, rows written with norm and
+    rotation, rotated queries, absorbed attention; the prompt in the expanded form too,
+    whose results the absorbed form reproduces through the projections."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(31)
+    H, page, nb, scale = 8, 16, 40, 192 ** -0.5
+    dt = dt_of(name)
+    table64 = ab.rope_table(64)
+    freqs, _ = ab.rope_frequencies(64)
+    wuk, wuv = (rng.standard_normal((H, 512, 128)) * 512 ** -0.5 for _ in range(2))
+    weight = rounded(rng, (512,), name)
+    cache = ab.new_latent_cache(nb, page, dt)
+    table = torch.full((2, 16), -1, dtype=torch.int32, device="cuda")
+    lens, free, start = i32([0, 0]), i32(rng.permutation(nb)), i32([0])
+    for new in ([70, 33], [1, 2]):
+        T = sum(new)
+        plan = ab.kv_block_tables(lens, i32(new), table, free, page, nb, T, start)
+        kv = rounded(rng, (1, T, 576), name)
+        rows = torch.empty_like(kv)
+        ab.latent_cache_write(kv, plan.slot_map, cache, norm_weight=weight, positions=plan.positions, table=table64,
+                              interleaved=True, out=rows)
+        ref, size = oracle.cache_rows(f64(kv)[0], f64(weight), 1e-6, freqs, plan.positions.cpu().numpy(), 1.0, True)
+        assert (np.abs(f64(rows)[0] - ref) <= EPS[name] * np.abs(ref) + 2.0 ** -20 * size + 2.0 ** -25).all()
+        q = rounded(rng, (1, T, H, 192), name)
+        ab.rope(q, plan.positions, table64, interleaved=True, start=128, out=(q, None))
+        x = f64(q)[0]
+        qa = np.concatenate([np.einsum("thd,hcd->thc", x[..., :128], wuk), x[..., 128:]], -1)
+        qa = torch.from_numpy(qa)[None].to(dt).cuda()
+        o, lse = ab.forward_latent_cache(qa, cache, table, plan.cu_seqlens, plan.kv_lens, scale)
+        r = oracle.cache_forward(f64(qa)[0], f64(cache), table.cpu().numpy(), plan.cu_seqlens.cpu().numpy(),
+                                 plan.kv_lens.cpu().numpy(), scale)
+        near(o[0], lse[0].t(), r, name)
+        if new[0] == 70:
+            c = f64(rows)[0, :, :512]
+            kn, v = (torch.from_numpy(np.einsum("tc,hcd->thd", c, w))[None].to(dt).cuda() for w in (wuk, wuv))
+            oe, le = ab.forward_latent(q, kn, rows[:, :, 512:], v, scale, cu_seqlens=plan.cu_seqlens)
+            near(oe, le.transpose(1, 2), oracle.expanded_forward(f64(q), f64(kn), f64(rows)[:, :, 512:], f64(v), scale, True,
+                                                                  plan.cu_seqlens.cpu().numpy()), name)
+            # both forms of one attention: rounded keys, values and queries differ by steps of the type
+            got = np.einsum("thc,hcd->thd", f64(o)[0], wuv)
+            assert np.linalg.norm(got - f64(oe)[0]) <= 4 * EPS[name] * np.linalg.norm(got)
+        start += plan.counts[1:2]
+        lens.copy_(plan.kv_lens)
