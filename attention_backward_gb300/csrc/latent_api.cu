@@ -40,37 +40,27 @@ attn_status_t launch_status(cudaError_t e) { return e == cudaSuccess ? ATTN_OK :
 
 bool dtype_ok(attn_dtype_t dt) { return dt == ATTN_DT_F16 || dt == ATTN_DT_BF16; }
 
-CUtensorMapDataType map_type(attn_dtype_t dt) {
-  return dt == ATTN_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-}
-
-// Latent rows as a 2-D tensor, box 64 columns x 1 row (for gather4), 128-byte swizzle.
-bool make_rows_map(CUtensorMap* m, const void* base, attn_dtype_t dt, int64_t rows, int64_t row_stride) {
+// A 4-D tensor of 16-bit values, 128-byte swizzle; ``strides`` (elements) and
+// ``box`` of the dimensions after the first, whose box is 64 columns.
+bool make_map(CUtensorMap* m, const void* base, attn_dtype_t dt, int64_t D, const int64_t (&size)[3],
+              const int64_t (&stride)[3], const int (&rows)[3]) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(kLatRow), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride * 2)};
-  cuuint32_t box[2] = {64, 1};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, map_type(dt), 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D)}, strides[3];
+  cuuint32_t box[4] = {64}, es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = static_cast<cuuint64_t>(size[i]), strides[i] = static_cast<cuuint64_t>(stride[i] * 2);
+    box[i + 1] = static_cast<cuuint32_t>(rows[i]);
+  }
+  return fn(m, dt == ATTN_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [B,S,H,D] 16-bit, box 64 columns x 128 rows of one head, 128-byte swizzle.
-bool make_tile_map(CUtensorMap* m, const void* base, attn_dtype_t dt, int64_t B, int64_t S, int64_t H, int64_t D,
-                   const attn_strides_t& st) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(S),
-                        static_cast<cuuint64_t>(B)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.h * 2), static_cast<cuuint64_t>(st.s * 2),
-                           static_cast<cuuint64_t>(st.b * 2)};
-  cuuint32_t box[4] = {64, 1, 128, 1};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  return fn(m, map_type(dt), 4, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// [B,S,H,D], box 64 columns x ``heads`` x ``rows`` of the sequence.
+bool make_bshd_map(CUtensorMap* m, const void* base, attn_dtype_t dt, int64_t B, int64_t S, int64_t H, int64_t D,
+                   const attn_strides_t& st, int heads, int rows) {
+  return make_map(m, base, dt, D, {H, S, B}, {st.h, st.s, st.b}, {heads, rows, 1});
 }
 
 attn_status_t check_rope(const attn_rope_tensor_t* t, int64_t R) {
@@ -187,8 +177,11 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   if (slse.s < 1 || slse.h < 1) return ATTN_ERR_INVALID_ARG;
   const LatWs w = lat_ws();
   if (workspace_bytes < static_cast<size_t>(w.total)) return ATTN_ERR_WORKSPACE;
-  CUtensorMap rows;
-  if (!make_rows_map(&rows, cache->rows, dtype, cache->num_blocks * cache->page_size, cache->row_stride))
+  CUtensorMap pages;
+  const int64_t page_stride = cache->page_size * cache->row_stride;
+  if (page_stride >= (int64_t(1) << 39)) return ATTN_ERR_UNSUPPORTED;
+  if (!make_map(&pages, cache->rows, dtype, kLatRow, {cache->page_size, cache->num_blocks, 1},
+                {cache->row_stride, page_stride, page_stride}, {imin(static_cast<int>(cache->page_size), kLatKeys), 1, 1}))
     return ATTN_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   LatParams lp{};
@@ -215,7 +208,7 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   // more) does not fit one.
   const int group = T * H > num_seqs * kLatRows ? 2 : 1;
   const int ctas = imin(sms, kLatMaxCtas) / group * group;
-  if (const cudaError_t e = launch_latent_cache(lp, rows, bf16, group, sms, st); e != cudaSuccess) return launch_status(e);
+  if (const cudaError_t e = launch_latent_cache(lp, pages, bf16, group, sms, st); e != cudaSuccess) return launch_status(e);
   return launch_status(launch_latent_join(lp, bf16, group, ctas, sms, st));
 }
 
@@ -240,11 +233,11 @@ attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, 
   if (skv.h < kLatRow || skv.h % 8 || skv.s != HKV * skv.h || skv.b != SKV * skv.s) return ATTN_ERR_UNSUPPORTED;
   if (sidx.b < 0 || sidx.s < 0 || sidx.h < 0 || slse.b < 0 || slse.s < 0 || slse.h < 0) return ATTN_ERR_INVALID_ARG;
   if (workspace_bytes < static_cast<size_t>(kHeaderBytes)) return ATTN_ERR_WORKSPACE;
-  CUtensorMap rows;
-  if (!make_rows_map(&rows, kv, dtype, B * SKV * HKV, skv.h)) return ATTN_ERR_INVALID_ARG;
+  CUtensorMap heads;
+  if (!make_bshd_map(&heads, q, dtype, B, S, H, kLatRow, sq, kLatRows, 1)) return ATTN_ERR_INVALID_ARG;
   LatParams lp{};
   KvAttnParams& p = lp.a;
-  p.q = static_cast<const uint8_t*>(q), p.sq_s = sq.s, p.sq_h = sq.h, lp.sq_b = sq.b;
+  lp.rows = static_cast<const uint8_t*>(kv), lp.row_stride = skv.h;
   p.o = static_cast<uint8_t*>(o), p.so_s = so.s, p.so_h = so.h, lp.so_b = so.b;
   p.lse = lse, p.sl_s = slse.s, p.sl_h = slse.h, lp.sl_b = slse.b;
   lp.idx = idx, lp.si_b = sidx.b, lp.si_s = sidx.s, lp.si_h = sidx.h;
@@ -256,7 +249,7 @@ attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // the error word starts clear; the kernel records the first wait that ran out
   if (cudaMemsetAsync(p.err, 0, sizeof(int), st) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  return launch_status(launch_latent_lists(lp, rows, dtype == ATTN_DT_BF16, sm_count(), st));
+  return launch_status(launch_latent_lists(lp, heads, dtype == ATTN_DT_BF16, sm_count(), st));
 }
 
 attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, attn_strides_t skn, const void* kr,
@@ -293,8 +286,10 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
   const int64_t units = ((S + 255) / 256 + p.num_seqs) * B * H;
   if (units > kMaxCount) return ATTN_ERR_UNSUPPORTED;
   LatFwdMaps m;
-  if (!make_tile_map(&m.q, q, dtype, B, S, H, 192, sq) || !make_tile_map(&m.kn, kn, dtype, B, Sk, H, 128, skn) ||
-      !make_tile_map(&m.kr, kr, dtype, B, Sk, 1, 64, {skr.b, skr.s, 64}) || !make_tile_map(&m.v, v, dtype, B, Sk, H, 128, sv))
+  if (!make_bshd_map(&m.q, q, dtype, B, S, H, 192, sq, 1, 128) ||
+      !make_bshd_map(&m.kn, kn, dtype, B, Sk, H, 128, skn, 1, 128) ||
+      !make_bshd_map(&m.kr, kr, dtype, B, Sk, 1, 64, {skr.b, skr.s, 64}, 1, 128) ||
+      !make_bshd_map(&m.v, v, dtype, B, Sk, H, 128, sv, 1, 128))
     return ATTN_ERR_INVALID_ARG;
   p.B = static_cast<int>(B), p.S = static_cast<int>(S), p.Sk = static_cast<int>(Sk), p.H = static_cast<int>(H);
   p.scale_log2 = sm_scale * 1.4426950408889634f;

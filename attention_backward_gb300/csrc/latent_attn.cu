@@ -7,8 +7,7 @@
 // list, with the tiles of 64 keys that they see.  Per tile, with the rows of Q as
 // the products' N:
 //
-//   gather  64 latent rows (TMA tile::gather4, nine slabs of 64 columns; keys that
-//           are not visible read zeros)
+//   load    64 latent rows into nine 128-byte-swizzled slabs of 64 columns
 //   S^T  = K Q^T          M = 64 keys, N = 64 rows, K = 576
 //   P^T  = 2^(S^T scale log2 e - m)     16 bits, in shared memory
 //   O^T += C^T P^T        four M-tiles of 128 latent columns, N = 64, K = 64 keys
@@ -29,8 +28,18 @@
 // than 64 rows two CTAs share a part, 64 rows each of units of 128, so that the second
 // reads its keys from L2.  Lists: a unit a token and KV group, longest lists first.
 //
-// Warp roles (12 warps): 0-3 softmax and output, 4-7 loads of Q, 8 gathers, 9 MMA
-// issue, 10 the walk, a unit ahead of the others, 11 idle.  Every wait is bounded.
+// Rows of a page come as TMA boxes; listed rows by 16-byte asynchronous copies of four
+// warps, a slab's swizzle written by address.  (TMA gathers of four rows took 37 ns each,
+// 5.4 us a tile, four times what the products and the softmax of one take.)
+//
+// Keys that nobody sees: scores of rows that were not loaded are masked; their 16-key
+// groups are left out of the O products, and rows behind the last key inside a group are
+// zeroed by the softmax warps (0 * NaN is NaN).  Listed rows that are not visible are
+// filled with zeros.
+//
+// Warp roles (12 warps): 0-3 softmax and output, 4-7 loads of Q (lists: of listed rows),
+// 8 pages (lists: Q), 9 MMA issue, 10 the walk, a unit ahead of the others, 11 idle.
+// Every wait is bounded.
 #include <cmath>
 
 #include "cvt.cuh"
@@ -53,9 +62,9 @@ constexpr float kTop = 7.f, kMost = 15.f;  // log2 of a row's largest weight whe
 constexpr float kNone = -1e30f;            // reference of a row that has seen no key
 
 enum LatBar : int {
-  Q_FULL = 0,                // 4 loading warps
+  Q_FULL = 0,                // 4 loading warps (lists: a copy)
   Q_EMPTY,                   // every S of the unit has completed
-  KV_FULL0,                  // per stage
+  KV_FULL0,                  // per stage (lists: 4 loading warps)
   KV_EMPTY0 = KV_FULL0 + STAGES,
   S_FULL0 = KV_EMPTY0 + STAGES,  // per score buffer
   P_READY = S_FULL0 + 2,     // 4 softmax warps
@@ -83,7 +92,7 @@ struct LatShared {
   float ref[NR];
   int hi[NR];         // keys that a row sees
   LatUnit units[2];
-  uint32_t bits[STAGES][4];  // key 4 i + e of a stage's tile is visible: bit i of word e
+  uint32_t bits[STAGES][4];  // of a stage's tile and 16-key group: its keys that are loaded and visible, if its mask leaves them
   uint64_t bars[NUM_BARS];
   int64_t work[kWarps];
   uint32_t tmem;
@@ -286,10 +295,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
-    mbar_init(&bars[Q_FULL], 4);
+    mbar_init(&bars[Q_FULL], LISTS ? 1 : 4);
     mbar_init(&bars[Q_EMPTY], 1);
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&bars[KV_FULL0 + i], 1);
+      mbar_init(&bars[KV_FULL0 + i], LISTS ? 4 : 1);
       mbar_init(&bars[KV_EMPTY0 + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -398,65 +407,64 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp == 8) {
-    // ============================================================ gathers
-    // Lanes i and i + 16 hold rows 4 i .. 4 i + 3 of a tile and copy the even and
-    // the odd slabs of them.
-    const int q4 = 4 * (lane & 15), odd = lane >> 4;
-    uint32_t kc = 0;
+    uint32_t kc = 0, qc = 0;
     bool ok = true;
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
-      if (u.valid == 2) continue;
-      const int* list = nullptr;
+      if (u.valid == 2 || u.j1 <= u.j0) continue;
       if constexpr (LISTS) {
-        list = lp.idx + u.n * lp.si_b + static_cast<int64_t>(u.a) * lp.si_s + (u.row0 / lp.gh) * lp.si_h;
-      } else {
-        list = p.table + static_cast<int64_t>(u.n) * p.table_stride;
-      }
-      int rows[4];
-      auto look_up = [&](int j) {
-        const int k0 = j * KT + q4;
-        if constexpr (LISTS) {
-          const int g = u.row0 / lp.gh;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = j < u.j1 && k0 + e < lp.topk ? list[k0 + e] : -1;
-            rows[e] = i >= 0 && i < lp.SKV ? (u.n * lp.SKV + i) * lp.HKV + g : -1;
-          }
-        } else {
-          const int page = j < u.j1 && k0 < u.L ? list[k0 >> p.page_log2] : -1;
-          const bool held = page >= 0 && page < p.num_blocks;
-          const int row = (page << p.page_log2) + (k0 & ((1 << p.page_log2) - 1));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) rows[e] = held && k0 + e < u.L ? row + e : -1;
-        }
-      };
-      look_up(u.j0);
-      for (int j = u.j0; j < u.j1; ++j, ++kc) {
-        const int st = kc % STAGES;
-        const uint32_t n = kc / STAGES;
-        uint32_t bit[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) bit[e] = __ballot_sync(0xffffffffu, rows[e] >= 0) & 0xffffu;
-        if (n >= 1 && !(ok = mbar_wait_warp(&bars[KV_EMPTY0 + st], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
-        if (lane == 0) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sh.bits[st][e] = bit[e];
-          mbar_arrive_expect_tx(&bars[KV_FULL0 + st], TILE);
-        }
+        // ========================================================== Q: 64 heads of the token (those past its group are not used)
+        if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bars[Q_FULL], TILE);
         __syncwarp();
-        uint8_t* const dst = sm + OFF_K + st * TILE + q4 * 128;
-#pragma unroll 1
-        for (int s = odd; s < NSLAB; s += 2)
-          tma_gather4(dst + s * SLAB, &map, &bars[KV_FULL0 + st], s * 64, rows[0], rows[1], rows[2], rows[3]);
-        look_up(j + 1);
+        if (lane < NSLAB)
+          tma_load_4d(sm + OFF_Q + lane * SLAB, &map, &bars[Q_FULL], lane * 64, u.row0, u.a, u.n);
+        ++qc;
+      } else {
+        // ========================================================== pages
+        // Lanes 0-3 look up the pages of a tile's 16-key groups, a tile ahead; a copy
+        // takes 64 columns of a page's tokens in the tile.
+        const int* const table = p.table + static_cast<int64_t>(u.n) * p.table_stride;
+        const int span = p.page_log2 >= 6 ? 4 : 1 << (p.page_log2 - 4);  // groups a copy
+        auto look_up = [&](int j) {
+          const int k = j * KT + 16 * lane;
+          const int page = lane < 4 && j < u.j1 && k < u.L ? table[k >> p.page_log2] : -1;
+          return page < p.num_blocks ? page : -1;
+        };
+        int next = look_up(u.j0);
+        for (int j = u.j0; j < u.j1; ++j, ++kc) {
+          const int st = kc % STAGES;
+          const uint32_t n = kc / STAGES;
+          const int page = next;
+          const uint32_t held = __ballot_sync(0xffffffffu, page >= 0);
+          if (n >= 1 && !(ok = mbar_wait_warp(&bars[KV_EMPTY0 + st], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
+          if (lane < 4) sh.bits[st][lane] = page >= 0 ? 0xffffu : 0u;
+          __syncwarp();
+          if (lane == 0) {
+            int copies = 0;
+            for (int g = 0; g < 4; g += span) copies += held >> g & 1;
+            if (copies) mbar_arrive_expect_tx(&bars[KV_FULL0 + st], copies * span * 16 * 128 * NSLAB);
+            else mbar_arrive(&bars[KV_FULL0 + st]);
+          }
+          __syncwarp();
+          for (int i = lane; i - lane < 4 / span * NSLAB; i += 32) {
+            const int g = i / NSLAB * span, s = i % NSLAB;
+            const int pg = __shfl_sync(0xffffffffu, page, g & 3);
+            if (g < 4 && pg >= 0)
+              tma_load_4d(sm + OFF_K + st * TILE + s * SLAB + g * 2048, &map, &bars[KV_FULL0 + st], s * 64,
+                          (j * KT + 16 * g) & ((1 << p.page_log2) - 1), pg, 0);
+          }
+          next = look_up(j + 1);
+        }
       }
     }
-    // gathers in flight land before the CTA exits
-    if (lane == 0)
+    // copies in flight land before the CTA exits
+    if (lane == 0) {
+      if (qc >= 1) mbar_drain(&bars[Q_FULL], (qc - 1) & 1);
       for (uint32_t i = kc > static_cast<uint32_t>(STAGES) ? kc - STAGES : 0u; i < kc; ++i)
         mbar_drain(&bars[KV_FULL0 + i % STAGES], (i / STAGES) & 1);
+    }
     __syncwarp();
   } else if (warp == 9) {
     // ============================================================ MMA issue
@@ -487,6 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!(ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
       ++qc;
       bool early = false;  // this tile's scores have been issued already
+      bool begun = false;  // O holds something of this unit
       for (int j = u.j0; j < u.j1; ++j, ++kc) {
         const bool next = j + 1 < u.j1;
         if (!early) {
@@ -511,12 +520,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (j == u.j0 && oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE], (oc - 1) & 1, wc, kErrWaitDQEmpty))) break;
         tc_fence_after();
         const uint64_t a = c_mn + sdesc_step((kc % STAGES) * TILE);
+        bool loaded[4] = {true, true, true, true};  // 16-key groups
+        if constexpr (!LISTS) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+          for (int kk = 0; kk < 4; ++kk) loaded[kk] = sh.bits[kc % STAGES][kk] != 0u && j * KT + 16 * kk < u.L;
+        }
+        if (loaded[0] && loaded[1] && loaded[2] && loaded[3]) {
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            mma_ss_w(tmem + T_O + 64 * m, a + sdesc_step(2 * m * SLAB + kk * 2048), p_mn + sdesc_step(kk * 2048), IDESC_O,
-                     j > u.j0 || kk > 0);
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss_w(tmem + T_O + 64 * m, a + sdesc_step(2 * m * SLAB + kk * 2048), p_mn + sdesc_step(kk * 2048), IDESC_O,
+                       begun || kk > 0);
+          begun = true;
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk < 4; ++kk) {
+            if (!loaded[kk]) continue;
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              mma_ss_w(tmem + T_O + 64 * m, a + sdesc_step(2 * m * SLAB + kk * 2048), p_mn + sdesc_step(kk * 2048), IDESC_O,
+                       begun);
+            begun = true;
+          }
+        }
         mma_commit_w(&bars[KV_EMPTY0 + kc % STAGES]);
         mma_commit_w(&bars[O_DONE]);
       }
@@ -527,45 +554,92 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) mbar_drain(&bars[DRAIN], 0);
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
-    // ============================================================ loads of Q
     const int tid = threadIdx.x - 128;
-    uint32_t qc = 0;
-    bool ok = true;
+    uint32_t qc = 0, kc = 0;
+    bool ok = true, flushed = false;  // the tile before has been published already
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
       if (u.valid == 2 || u.j1 <= u.j0) continue;
-      if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
-      ++qc;
-      constexpr int PIECES = kLatRow / 8;  // of a row
-#pragma unroll 4
-      for (int i = tid; i < NR * PIECES; i += 128) {
-        const int r = i / PIECES, c = i % PIECES;
-        const bool on = r < u.live;
-        const uint8_t* src = p.q;
-        if (on) {
-          int64_t at;
-          if constexpr (LISTS) {
-            at = u.n * lp.sq_b + u.a * p.sq_s + (u.row0 + r) * p.sq_h;
-          } else {
-            const int row = u.row0 + r;
-            at = static_cast<int64_t>(u.a + row / p.G) * p.sq_s + (row % p.G) * p.sq_h;
+      constexpr int PIECES = kLatRow / 8;  // 16-byte pieces of a row
+      if constexpr (LISTS) {
+        // ========================================================== listed rows: 16 of a tile a warp
+        // A tile's copies are in flight while the next one's are issued.
+        const int w = warp - 4, g = u.row0 / lp.gh;
+        const int* const list = lp.idx + u.n * lp.si_b + static_cast<int64_t>(u.a) * lp.si_s + g * lp.si_h;
+        const int64_t base = static_cast<int64_t>(u.n) * lp.SKV;
+        auto look_up = [&](int j) {
+          const int k = j * KT + 16 * w + (lane & 15);
+          const int i = j < u.j1 && k < lp.topk ? list[k] : -1;
+          return i >= 0 && i < lp.SKV ? i : -1;
+        };
+        auto publish = [&](uint32_t i) {  // tile i's copies of this warp have landed
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[KV_FULL0 + i % STAGES]);
+        };
+        int next = look_up(u.j0);
+        for (int j = u.j0; j < u.j1; ++j, ++kc) {
+          const int st = kc % STAGES;
+          const uint32_t n = kc / STAGES;
+          const int row = next;
+          next = look_up(j + 1);
+          const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+          if (n >= 1 && j > u.j0 && !__all_sync(0xffffffffu, mbar_test(&bars[KV_EMPTY0 + st], (n - 1) & 1))) {
+            // nothing to issue yet: the tile in flight is published meanwhile
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            publish(kc - 1);
+            flushed = true;
           }
-          src += 2 * (at + 8 * c);
+          ok = n < 1 || mbar_wait_warp(&bars[KV_EMPTY0 + st], (n - 1) & 1, wc, kErrWaitStageEmpty);
+          if (!ok) break;
+          if (lane == 0) sh.bits[st][w] = seen;
+          uint8_t* const tile = sm + OFF_K + st * TILE;
+#pragma unroll
+          for (int r4 = 0; r4 < 16; r4 += 4) {
+#pragma unroll
+            for (int k = 0; k < 4 * PIECES / 32; ++k) {
+              const int i = k * 32 + lane, r = r4 + i / PIECES, c = i % PIECES;
+              const int at = __shfl_sync(0xffffffffu, row, r);
+              const uint8_t* const src = lp.rows + (at < 0 ? 0 : 2 * (((base + at) * lp.HKV + g) * lp.row_stride + 8 * c));
+              copy16_async(smem_u32(tile + (c >> 3) * SLAB + sw128_offset(16 * w + r, c & 7)), src, at < 0 ? 0 : 16);
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (j > u.j0 && !flushed) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            publish(kc - 1);
+          }
+          flushed = false;
         }
-        copy16_async(smem_u32(sm + OFF_Q + (c >> 3) * SLAB + sw128_offset(r, c & 7)), src, on ? 16 : 0);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (ok && !flushed) publish(kc - 1);
+        flushed = false;
+      } else {
+        // ========================================================== Q
+        if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
+        ++qc;
+#pragma unroll 4
+        for (int i = tid; i < NR * PIECES; i += 128) {
+          const int r = i / PIECES, c = i % PIECES;
+          const bool on = r < u.live;
+          const int row = u.row0 + r;
+          const uint8_t* src = p.q;
+          if (on) src += 2 * (static_cast<int64_t>(u.a + row / p.G) * p.sq_s + (row % p.G) * p.sq_h + 8 * c);
+          copy16_async(smem_u32(sm + OFF_Q + (c >> 3) * SLAB + sw128_offset(r, c & 7)), src, on ? 16 : 0);
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Q_FULL]);
       }
-      asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Q_FULL]);
     }
   } else if (warp < 4) {
     // ============================================================ softmax and output
     const int tid = threadIdx.x;
     const int ka = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);  // my keys: ka, ka + 8; my rows: 8 j + c0 + (0, 1)
     const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t bit_a = 1u << (ka >> 2), bit_b = 1u << ((ka + 8) >> 2);
+    const uint32_t bit_a = 1u << (ka & 15), bit_b = bit_a << 8;  // of group ``warp``
     uint32_t kc = 0;
     // The four warps meet at named barriers, which have no limit: a warp whose wait ran
     // out goes on (its results are void) to the next vote, where all four leave.
@@ -599,8 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld_wait();
         float* const s = reinterpret_cast<float*>(sr);
         if ((b0 & b1 & b2 & b3) != 0xffffu || (j + 1) * KT > hi_all) {
-          const int e = ka & 3;
-          const uint32_t w = e == 0 ? b0 : e == 1 ? b1 : e == 2 ? b2 : b3;
+          const uint32_t w = sh.bits[st][warp];
           const bool va = w & bit_a, vb = w & bit_b;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -656,6 +729,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             tmem_st_wait();
           }
+        }
+        if (!LISTS && (u.L & 15) && j == (u.L - 1) / KT) {
+          // rows behind the last key of its group: the scores have been made, the O products follow
+          const int r0 = u.L & (KT - 1), n = (16 - (u.L & 15)) * 64;
+          for (int i = tid; i < n; i += 128)
+            *reinterpret_cast<uint4*>(sm + OFF_K + st * TILE + (i & 7) * SLAB + (r0 + (i >> 6)) * 128 + (i >> 3 & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
         }
         uint32_t pa[8], pb[8];
 #pragma unroll
@@ -740,7 +820,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           // neighbouring lanes swap, so that each stores two columns of one row of a pair
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float x = __uint_as_float(r[e]) * sh.f[r0 + e], y = __uint_as_float(r[e + 1]) * sh.f[r0 + e + 1];
+            // (a row that has seen no key may find anything in O)
+            const float f0 = sh.f[r0 + e], f1 = sh.f[r0 + e + 1];
+            const float x = f0 == 0.f ? 0.f : __uint_as_float(r[e]) * f0, y = f1 == 0.f ? 0.f : __uint_as_float(r[e + 1]) * f1;
             const float z = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
             const uint32_t w = lane & 1 ? pack2<BF16>(z, y) : pack2<BF16>(x, z);
             const int row = r0 + e + (lane & 1);
@@ -768,26 +850,26 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int GROUP, bool BF16>
-cudaError_t launch_t(const LatParams& p, const CUtensorMap& rows, int grid, cudaStream_t st) {
+cudaError_t launch_t(const LatParams& p, const CUtensorMap& map, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = latent_kernel<GROUP, BF16>;
   if (const cudaError_t e = allow_smem_once(kern, SMEM, &done); e != cudaSuccess) return e;
-  return launch_chained(kern, dim3(grid), THREADS, SMEM, st, rows, p);
+  return launch_chained(kern, dim3(grid), THREADS, SMEM, st, map, p);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& rows, bool bf16, int group, int sms,
+cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& pages, bool bf16, int group, int sms,
                                 cudaStream_t st) {
   const int grid = imin(sms, kLatMaxCtas) / group * group;
-  if (group == 1) return bf16 ? launch_t<1, true>(p, rows, grid, st) : launch_t<1, false>(p, rows, grid, st);
-  return bf16 ? launch_t<2, true>(p, rows, grid, st) : launch_t<2, false>(p, rows, grid, st);
+  if (group == 1) return bf16 ? launch_t<1, true>(p, pages, grid, st) : launch_t<1, false>(p, pages, grid, st);
+  return bf16 ? launch_t<2, true>(p, pages, grid, st) : launch_t<2, false>(p, pages, grid, st);
 }
 
-cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& rows, bool bf16, int sms, cudaStream_t st) {
+cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st) {
   const int64_t units = static_cast<int64_t>(p.B) * p.S * p.HKV;
   const int grid = static_cast<int>(units < sms ? units : sms);
-  return bf16 ? launch_t<0, true>(p, rows, grid, st) : launch_t<0, false>(p, rows, grid, st);
+  return bf16 ? launch_t<0, true>(p, q, grid, st) : launch_t<0, false>(p, q, grid, st);
 }
 
 }  // namespace ab
