@@ -16,12 +16,12 @@
 // (M-major), and 512 columns of O fit tensor memory beside the scores: rows as M
 // would need all of it.  Few rows cost no more products than 64.
 //
-// Softmax: the scores arrive as fragments of 16 keys x 64 rows a warp (a thread: 2
-// keys, 16 rows).  A row's reference m is kept until a weight would pass 2^15:
-// one vote of the four warps a tile, and only then is the max taken, l scaled and O^T
-// scaled in tensor memory.  m is set so that the largest weight is 2^7: fp16 weights
-// keep their normal range down to 2^-21 of it and steps of 2^-31.  l is summed from the f32
-// weights, a thread's share of the keys in registers until the unit ends.
+// Softmax: eight warps, a quarter of the keys and half of the rows each; the scores
+// arrive as fragments (a thread: 2 keys, 8 rows).  A row's reference m is kept until a
+// weight would pass 2^15: one vote of the warps a tile, and only then is the max taken,
+// l scaled and O^T scaled in tensor memory.  m is set so that the largest weight is 2^7: fp16
+// weights keep their normal range down to 2^-21 of it and steps of 2^-31.  l is summed from
+// the f32 weights, a thread's share of the keys in registers until the unit ends.
 //
 // Cache: the line of kv_sched.cuh, cut evenly over the CTAs; a unit split over
 // several leaves f32 partials that latent_join.cu joins.  Where requests have more
@@ -37,10 +37,11 @@
 // zeroed by the softmax warps (0 * NaN is NaN).  Listed rows that are not visible are
 // filled with zeros.
 //
-// Warp roles (12 warps): 0-3 softmax and output, 4-7 loads of Q (lists: of listed rows),
-// 8 pages (lists: Q), 9 MMA issue, 10 the walk, a unit ahead of the others, 11 idle.
-// Every wait is bounded.
+// Warp roles (16 warps): 0-7 softmax and output, 8-11 loads of Q (lists: of listed
+// rows), 12 pages (lists: Q), 13 issue of the scores, 14 the walk, a unit ahead of the
+// others, 15 issue of O.  Every wait is bounded.
 #include <cmath>
+#include <type_traits>
 
 #include "cvt.cuh"
 #include "kv_launch.h"
@@ -57,23 +58,28 @@ constexpr int NSLAB = kLatRow / 64;
 constexpr int SLAB = KT * 128;  // [64 rows x 64 columns] 16-bit, 128-byte swizzled
 constexpr int TILE = NSLAB * SLAB;
 constexpr int STAGES = 2;
-constexpr int kWarps = 12, THREADS = kWarps * 32;
+// A stage is loaded and freed in five groups: the two slabs of each M-tile of O, and the
+// key part, whose slab takes P once the scores are made.
+constexpr int GROUPS = 5;
+__device__ __forceinline__ int group_slabs(int g) { return g < 4 ? 2 : 1; }
+constexpr int kWarps = 16, THREADS = kWarps * 32;
+constexpr int SOFT = 256;  // threads of the softmax warps
 constexpr float kTop = 7.f, kMost = 15.f;  // log2 of a row's largest weight when its max is taken, and of the most it may grow to
 constexpr float kNone = -1e30f;            // reference of a row that has seen no key
 
 enum LatBar : int {
   Q_FULL = 0,                // 4 loading warps (lists: a copy)
   Q_EMPTY,                   // every S of the unit has completed
-  KV_FULL0,                  // per stage (lists: 4 loading warps)
-  KV_EMPTY0 = KV_FULL0 + STAGES,
-  S_FULL0 = KV_EMPTY0 + STAGES,  // per score buffer
-  P_READY = S_FULL0 + 2,     // 4 softmax warps
-  O_DONE,                    // the tile's O products, and all before them
-  O_FREE,                    // 4 softmax warps read the unit's O
+  FULL0,                     // per stage and group of slabs
+  EMPTY0 = FULL0 + STAGES * GROUPS,  // the same: its last products have completed
+  S_FULL0 = EMPTY0 + STAGES * GROUPS,  // per score buffer
+  P_READY0 = S_FULL0 + 2,    // tiles in turn: the softmax warps
+  O_DONE0 = P_READY0 + 2,    // tiles in turn: its O products, and all before them
+  O_FREE = O_DONE0 + 2,      // the softmax warps read the unit's O
   UNIT_FULL0,                // 2 slots
-  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 10 warps
-  DRAIN = UNIT_EMPTY0 + 2,
-  NUM_BARS
+  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 15 warps
+  DRAIN0 = UNIT_EMPTY0 + 2,  // of the issuing warps
+  NUM_BARS = DRAIN0 + 2
 };
 
 // A unit, or the CTA's part of one: key tiles [j0, j1).
@@ -87,7 +93,8 @@ struct LatUnit {
 };
 
 struct LatShared {
-  float mx[4][NR];    // per softmax warp and row: a max, or a sum
+  int64_t row[NR];    // a row's place in o
+  float mx[4][NR];    // per quarter of the keys and row: a max, or a sum
   float f[NR];        // per row: a factor
   float ref[NR];
   int hi[NR];         // keys that a row sees
@@ -101,54 +108,74 @@ struct LatShared {
 
 constexpr int OFF_Q = 0;
 constexpr int OFF_K = OFF_Q + TILE;
-constexpr int OFF_P = OFF_K + STAGES * TILE;
-constexpr int OFF_SH = OFF_P + KT * 128;
+constexpr int OFF_SH = OFF_K + STAGES * TILE;
+__device__ __forceinline__ int p_at(uint32_t stage) { return OFF_K + stage * TILE + (NSLAB - 1) * SLAB; }
 constexpr int SMEM = OFF_SH + static_cast<int>(sizeof(LatShared));
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 
 constexpr uint32_t T_S = 0, T_O = 128;  // score buffers at 0 and 64; O^T tile m at 128 + 64 m
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
+// A value that all lanes have, as one the compiler knows to be the warp's.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_max_sync(0xffffffffu, x); }
+
+// 16 lanes x 32 columns of a warp's quarter as fragments: registers 4 j + (0, 1) are
+// row lane / 4, columns 8 j + 2 (lane % 4) + (0, 1); 4 j + (2, 3) row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
-// 16 lanes x 64 columns of a warp's quarter as fragments: registers 4 j + (0, 1) are
-// row lane / 4, columns 8 j + 2 (lane % 4) + (0, 1); 4 j + (2, 3) row lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, uint32_t* r) {
+// mma_ss_w with the lane elected beforehand (``elected`` not 0 in one lane).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(x));
+  return x;
+}
+__device__ __forceinline__ void mma_ss_e(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected));
 }
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {  // the rest reads zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// The four softmax warps; true in all of them if it is in one.
+// The softmax warps; true in all of them if it is in one.
 __device__ __forceinline__ bool softmax_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 2, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(static_cast<uint32_t>(x))
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); }
+
+// Of 8 values in each of the lanes l, l ^ 4, l ^ 8, .. (8 of them), the one of column
+// column_of(lane) over all 8.
+__device__ __forceinline__ int column_of(int lane) { return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1); }
+template <typename F>
+__device__ __forceinline__ float reduce8(float (&v)[8], int lane, F f) {
+#pragma unroll
+  for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = f(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  return v[0];
+}
 
 // ---------------------------------------------------------------- the walk along the line (one warp)
 
@@ -293,26 +320,34 @@ __global__ void __launch_bounds__(THREADS, 1)
     begin = kv_part_begin(total, part, parts), end = kv_part_begin(total, part + 1, parts);
   }
 
+  LatCursor cur{};
+  if (!LISTS && warp == 14) {  // (while the others set up)
+    int w0 = 0;
+    int64_t x = begin;
+    while (x >= sh.work[w0]) x -= sh.work[w0++];
+    cur = walk_to<RT>(p, w0 * per, x);
+  }
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
     mbar_init(&bars[Q_FULL], LISTS ? 1 : 4);
     mbar_init(&bars[Q_EMPTY], 1);
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&bars[KV_FULL0 + i], LISTS ? 4 : 1);
-      mbar_init(&bars[KV_EMPTY0 + i], 1);
+    for (int i = 0; i < STAGES * GROUPS; ++i) {
+      // (lists: every copying thread; of the last group also a lane a warp, for the bits)
+      mbar_init(&bars[FULL0 + i], LISTS ? (i % GROUPS == GROUPS - 1 ? 132 : 128) : 1);
+      mbar_init(&bars[EMPTY0 + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[S_FULL0 + i], 1);
+      mbar_init(&bars[P_READY0 + i], SOFT / 32);
+      mbar_init(&bars[O_DONE0 + i], 1);
       mbar_init(&bars[UNIT_FULL0 + i], 1);
-      mbar_init(&bars[UNIT_EMPTY0 + i], 10);
+      mbar_init(&bars[UNIT_EMPTY0 + i], 15);
+      mbar_init(&bars[DRAIN0 + i], 1);
     }
-    mbar_init(&bars[P_READY], 4);
-    mbar_init(&bars[O_DONE], 1);
-    mbar_init(&bars[O_FREE], 4);
-    mbar_init(&bars[DRAIN], 1);
+    mbar_init(&bars[O_FREE], SOFT / 32);
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 13) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
@@ -332,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     return u;
   };
 
-  if (warp == 10) {
+  if (warp == 14) {
     // ============================================================ the walk
     auto publish = [&](uint32_t uc, const LatUnit& u) -> bool {
       const uint32_t slot = uc & 1;
@@ -370,12 +405,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!publish(uc, u) || !u.valid) break;
       }
     } else {
-      int w0 = 0;
-      int64_t x = begin;
-      while (x >= sh.work[w0]) x -= sh.work[w0++];
-      LatCursor cur = walk_to<RT>(p, w0 * per, x);
       KvReq rq = kv_request(cur.n, p);
-      x = begin;
+      int64_t x = begin;
       for (uint32_t uc = 0;; ++uc) {
         LatUnit u{};
         int64_t stop = x;
@@ -406,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     uint32_t kc = 0, qc = 0;
     bool ok = true;
     for (uint32_t uc = 0; ok; ++uc) {
@@ -438,23 +469,27 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t n = kc / STAGES;
           const int page = next;
           const uint32_t held = __ballot_sync(0xffffffffu, page >= 0);
-          if (n >= 1 && !(ok = mbar_wait_warp(&bars[KV_EMPTY0 + st], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
-          if (lane < 4) sh.bits[st][lane] = page >= 0 ? 0xffffu : 0u;
-          __syncwarp();
-          if (lane == 0) {
-            int copies = 0;
-            for (int g = 0; g < 4; g += span) copies += held >> g & 1;
-            if (copies) mbar_arrive_expect_tx(&bars[KV_FULL0 + st], copies * span * 16 * 128 * NSLAB);
-            else mbar_arrive(&bars[KV_FULL0 + st]);
+          int copies = 0;  // of a slab
+          for (int g = 0; g < 4; g += span) copies += held >> g & 1;
+          // lane i copies the i / 2-th piece of a group's first or second slab
+          const int piece = (lane >> 1) * span, pg = __shfl_sync(0xffffffffu, page, piece & 3);
+          const bool mine = piece < 4 && pg >= 0;
+          const int token = (j * KT + 16 * piece) & ((1 << p.page_log2) - 1);
+          uint8_t* const dst = sm + OFF_K + st * TILE + piece * 2048;
+          for (int g = 0; g < GROUPS; ++g) {
+            uint64_t* const full = &bars[FULL0 + st * GROUPS + g];
+            if (n >= 1 && !(ok = mbar_wait_warp(&bars[EMPTY0 + st * GROUPS + g], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
+            if (g == GROUPS - 1 && lane < 4) sh.bits[st][lane] = page >= 0 ? 0xffffu : 0u;
+            __syncwarp();
+            if (lane == 0) {
+              if (copies) mbar_arrive_expect_tx(full, copies * span * 16 * 128 * group_slabs(g));
+              else mbar_arrive(full);
+            }
+            __syncwarp();
+            const int slab = 2 * g + (lane & 1);
+            if (mine && slab < NSLAB) tma_load_4d(dst + slab * SLAB, &map, full, slab * 64, token, pg, 0);
           }
-          __syncwarp();
-          for (int i = lane; i - lane < 4 / span * NSLAB; i += 32) {
-            const int g = i / NSLAB * span, s = i % NSLAB;
-            const int pg = __shfl_sync(0xffffffffu, page, g & 3);
-            if (g < 4 && pg >= 0)
-              tma_load_4d(sm + OFF_K + st * TILE + s * SLAB + g * 2048, &map, &bars[KV_FULL0 + st], s * 64,
-                          (j * KT + 16 * g) & ((1 << p.page_log2) - 1), pg, 0);
-          }
+          if (!ok) break;
           next = look_up(j + 1);
         }
       }
@@ -463,120 +498,122 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) {
       if (qc >= 1) mbar_drain(&bars[Q_FULL], (qc - 1) & 1);
       for (uint32_t i = kc > static_cast<uint32_t>(STAGES) ? kc - STAGES : 0u; i < kc; ++i)
-        mbar_drain(&bars[KV_FULL0 + i % STAGES], (i / STAGES) & 1);
+        for (int g = 0; g < GROUPS; ++g) mbar_drain(&bars[FULL0 + i % STAGES * GROUPS + g], (i / STAGES) & 1);
     }
     __syncwarp();
-  } else if (warp == 9) {
-    // ============================================================ MMA issue
-    constexpr uint32_t IDESC_S = idesc_f16(BF16, KT, NR, false, false);
-    constexpr uint32_t IDESC_O = idesc_f16(BF16, 128, NR, true, true);
-    const uint32_t sbase = smem_u32(sm);
-    const uint64_t k_kmaj = sdesc_sw128(sbase + OFF_K, 16, 1024);
-    const uint64_t q_kmaj = sdesc_sw128(sbase + OFF_Q, 16, 1024);
-    const uint64_t c_mn = sdesc_sw128(sbase + OFF_K, SLAB, 1024);
-    const uint64_t p_mn = sdesc_sw128(sbase + OFF_P, 0, 1024);
-    uint32_t kc = 0, qc = 0, oc = 0;
+  } else if (warp == 13) {
+    // ============================================================ scores
+    // (O has a warp of its own: the products are so short that their issue counts, and
+    // neither warp waits on what the other is waiting for)
+    constexpr uint32_t IDESC = idesc_f16(BF16, KT, NR, false, false);
+    const uint64_t k_kmaj = sdesc_sw128(smem_u32(sm) + OFF_K, 16, 1024);
+    const uint64_t q_kmaj = sdesc_sw128(smem_u32(sm) + OFF_Q, 16, 1024);
+    const uint32_t one = elect_lane();
+    uint32_t kc = 0, qc = 0;
     bool ok = true;
-    auto issue_s = [&](uint32_t i) {
-      tc_fence_after();
-      const uint32_t d = tmem + T_S + 64 * (i & 1);
-      const uint64_t a = k_kmaj + sdesc_step((i % STAGES) * TILE);
-#pragma unroll
-      for (int s = 0; s < NSLAB; ++s)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss_w(d, a + sdesc_step(s * SLAB + kk * 32), q_kmaj + sdesc_step(s * SLAB + kk * 32), IDESC_S, s > 0 || kk > 0);
-      mma_commit_w(&bars[S_FULL0 + (i & 1)]);
-    };
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
       if (u.valid == 2 || u.j1 <= u.j0) continue;
       if (!(ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
       ++qc;
-      bool early = false;  // this tile's scores have been issued already
-      bool begun = false;  // O holds something of this unit
-      for (int j = u.j0; j < u.j1; ++j, ++kc) {
-        const bool next = j + 1 < u.j1;
-        if (!early) {
-          if (!(ok = mbar_wait_warp(&bars[KV_FULL0 + kc % STAGES], (kc / STAGES) & 1, wc, kErrWaitKV))) break;
-          issue_s(kc);
-          if (!next) mma_commit_w(&bars[Q_EMPTY]);
-        }
-        early = false;
-        // while the softmax works: the next tile's scores, if its rows are there
-        if (next) {
-          for (int spin = 0; spin < 4096; ++spin) {
-            if (__any_sync(0xffffffffu, mbar_test(&bars[P_READY], kc & 1))) break;
-            if (__all_sync(0xffffffffu, mbar_test(&bars[KV_FULL0 + (kc + 1) % STAGES], ((kc + 1) / STAGES) & 1))) {
-              issue_s(kc + 1);
-              if (j + 2 >= u.j1) mma_commit_w(&bars[Q_EMPTY]);
-              early = true;
-              break;
-            }
+      for (const uint32_t end = kc + uniform(u.j1 - u.j0); kc < end; ++kc) {
+        const uint32_t st = kc % STAGES, phase = (kc / STAGES) & 1, d = tmem + T_S + 64 * (kc & 1);
+        // the softmax has read the scores of two tiles ago
+        if (kc >= 2 && !(ok = mbar_wait_warp(&bars[P_READY0 + (kc & 1)], ((kc >> 1) - 1) & 1, wc, kErrWaitSFree))) break;
+        const uint64_t a = k_kmaj + sdesc_step(st * TILE);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          if (!(ok = mbar_wait_warp(&bars[FULL0 + st * GROUPS + g], phase, wc, kErrWaitKV))) break;
+          if constexpr (LISTS) fence_proxy_async_smem();  // (the copies are the generic proxy's)
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < (g < 4 ? 8 : 4); ++kk) {
+            const uint64_t o = sdesc_step((2 * g + kk / 4) * SLAB + kk % 4 * 32);
+            mma_ss_e(d, a + o, q_kmaj + o, IDESC, g + kk > 0, one);
           }
         }
-        if (!(ok = mbar_wait_warp(&bars[P_READY], kc & 1, wc, kErrWaitP))) break;
-        if (j == u.j0 && oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE], (oc - 1) & 1, wc, kErrWaitDQEmpty))) break;
-        tc_fence_after();
-        const uint64_t a = c_mn + sdesc_step((kc % STAGES) * TILE);
-        bool loaded[4] = {true, true, true, true};  // 16-key groups
-        if constexpr (!LISTS) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) loaded[kk] = sh.bits[kc % STAGES][kk] != 0u && j * KT + 16 * kk < u.L;
-        }
-        if (loaded[0] && loaded[1] && loaded[2] && loaded[3]) {
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss_w(tmem + T_O + 64 * m, a + sdesc_step(2 * m * SLAB + kk * 2048), p_mn + sdesc_step(kk * 2048), IDESC_O,
-                       begun || kk > 0);
-          begun = true;
-        } else {
-#pragma unroll 1
-          for (int kk = 0; kk < 4; ++kk) {
-            if (!loaded[kk]) continue;
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              mma_ss_w(tmem + T_O + 64 * m, a + sdesc_step(2 * m * SLAB + kk * 2048), p_mn + sdesc_step(kk * 2048), IDESC_O,
-                       begun);
-            begun = true;
-          }
-        }
-        mma_commit_w(&bars[KV_EMPTY0 + kc % STAGES]);
-        mma_commit_w(&bars[O_DONE]);
+        if (!ok) break;
+        mma_commit_w(&bars[S_FULL0 + (kc & 1)]);
       }
-      ++oc;
+      mma_commit_w(&bars[Q_EMPTY]);
     }
     // every product issued by this warp completes before tensor memory is released
-    mma_commit_w(&bars[DRAIN]);
-    if (lane == 0) mbar_drain(&bars[DRAIN], 0);
+    mma_commit_w(&bars[DRAIN0]);
+    if (lane == 0) mbar_drain(&bars[DRAIN0], 0);
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
-    const int tid = threadIdx.x - 128;
-    uint32_t qc = 0, kc = 0;
-    bool ok = true, flushed = false;  // the tile before has been published already
+  } else if (warp == 15) {
+    // ============================================================ O
+    constexpr uint32_t IDESC = idesc_f16(BF16, 128, NR, true, true);
+    const uint64_t c_mn = sdesc_sw128(smem_u32(sm) + OFF_K, SLAB, 1024);
+    const uint64_t p_mn = sdesc_sw128(smem_u32(sm) + p_at(0), 0, 1024);
+    const uint32_t one = elect_lane();
+    uint32_t kc = 0, oc = 0;
+    bool ok = true;
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
       if (u.valid == 2 || u.j1 <= u.j0) continue;
-      constexpr int PIECES = kLatRow / 8;  // 16-byte pieces of a row
+      // the softmax warps have read the O of the unit before
+      if (oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
+      ++oc;
+      uint32_t begun = 0;  // O holds something of this unit
+      for (const uint32_t end = kc + uniform(u.j1 - u.j0); kc < end; ++kc) {
+        const uint32_t st = kc % STAGES;
+        if (!(ok = mbar_wait_warp(&bars[P_READY0 + (kc & 1)], (kc >> 1) & 1, wu, kErrWaitP))) break;
+        tc_fence_after();
+        const uint64_t c = c_mn + sdesc_step(st * TILE), pp = p_mn + sdesc_step(st * TILE);
+        uint32_t mask = 15;  // 16-key groups that are loaded
+        if constexpr (!LISTS) mask = __ballot_sync(0xffffffffu, lane < 4 && sh.bits[st][lane & 3] != 0u);
+        if (mask == 15) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss_e(tmem + T_O + 64 * m, c + sdesc_step(2 * m * SLAB + kk * 2048), pp + sdesc_step(kk * 2048), IDESC,
+                       kk > 0 ? 1u : begun, one);
+            mma_commit_w(&bars[EMPTY0 + st * GROUPS + m]);
+          }
+        } else {
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            uint32_t some = begun;
+#pragma unroll 1
+            for (int kk = 0; kk < 4; ++kk)
+              if (mask >> kk & 1) {
+                mma_ss_e(tmem + T_O + 64 * m, c + sdesc_step(2 * m * SLAB + kk * 2048), pp + sdesc_step(kk * 2048), IDESC,
+                         some, one);
+                some = 1;
+              }
+            mma_commit_w(&bars[EMPTY0 + st * GROUPS + m]);
+          }
+        }
+        begun |= mask;
+        mma_commit_w(&bars[EMPTY0 + st * GROUPS + GROUPS - 1]);
+        mma_commit_w(&bars[O_DONE0 + (kc & 1)]);
+      }
+    }
+    mma_commit_w(&bars[DRAIN0 + 1]);
+    if (lane == 0) mbar_drain(&bars[DRAIN0 + 1], 0);
+    __syncwarp();
+  } else if (warp >= 8 && warp < 12) {
+    const int w = warp - 8, r = lane >> 3, c = lane & 7;  // 16 rows a warp, 4 at once, 128 bytes each
+    uint32_t qc = 0, kc = 0;
+    bool ok = true;
+    for (uint32_t uc = 0; ok; ++uc) {
+      const LatUnit u = next_unit(uc, &ok);
+      if (!ok || !u.valid) break;
+      if (u.valid == 2 || u.j1 <= u.j0) continue;
       if constexpr (LISTS) {
         // ========================================================== listed rows: 16 of a tile a warp
-        // A tile's copies are in flight while the next one's are issued.
-        const int w = warp - 4, g = u.row0 / lp.gh;
+        // (a barrier counts the copies' completion itself)
+        const int g = u.row0 / lp.gh;
         const int* const list = lp.idx + u.n * lp.si_b + static_cast<int64_t>(u.a) * lp.si_s + g * lp.si_h;
         const int64_t base = static_cast<int64_t>(u.n) * lp.SKV;
         auto look_up = [&](int j) {
           const int k = j * KT + 16 * w + (lane & 15);
           const int i = j < u.j1 && k < lp.topk ? list[k] : -1;
           return i >= 0 && i < lp.SKV ? i : -1;
-        };
-        auto publish = [&](uint32_t i) {  // tile i's copies of this warp have landed
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[KV_FULL0 + i % STAGES]);
         };
         int next = look_up(u.j0);
         for (int j = u.j0; j < u.j1; ++j, ++kc) {
@@ -585,48 +622,44 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int row = next;
           next = look_up(j + 1);
           const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-          if (n >= 1 && j > u.j0 && !__all_sync(0xffffffffu, mbar_test(&bars[KV_EMPTY0 + st], (n - 1) & 1))) {
-            // nothing to issue yet: the tile in flight is published meanwhile
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            publish(kc - 1);
-            flushed = true;
+          const uint8_t* src[4];
+          uint32_t dst[4], bytes[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // my rows 4 i + r
+            const int at = __shfl_sync(0xffffffffu, row, 4 * i + r);
+            src[i] = lp.rows + (at < 0 ? 0 : 2 * (((base + at) * lp.HKV + g) * lp.row_stride + 8 * c));
+            dst[i] = smem_u32(sm + OFF_K + st * TILE) + sw128_offset(16 * w + 4 * i + r, c);
+            bytes[i] = at < 0 ? 0u : 16u;
           }
-          ok = n < 1 || mbar_wait_warp(&bars[KV_EMPTY0 + st], (n - 1) & 1, wc, kErrWaitStageEmpty);
-          if (!ok) break;
-          if (lane == 0) sh.bits[st][w] = seen;
-          uint8_t* const tile = sm + OFF_K + st * TILE;
 #pragma unroll
-          for (int r4 = 0; r4 < 16; r4 += 4) {
-#pragma unroll
-            for (int k = 0; k < 4 * PIECES / 32; ++k) {
-              const int i = k * 32 + lane, r = r4 + i / PIECES, c = i % PIECES;
-              const int at = __shfl_sync(0xffffffffu, row, r);
-              const uint8_t* const src = lp.rows + (at < 0 ? 0 : 2 * (((base + at) * lp.HKV + g) * lp.row_stride + 8 * c));
-              copy16_async(smem_u32(tile + (c >> 3) * SLAB + sw128_offset(16 * w + r, c & 7)), src, at < 0 ? 0 : 16);
+          for (int k = 0; k < GROUPS; ++k) {
+            uint64_t* const full = &bars[FULL0 + st * GROUPS + k];
+            if (n >= 1 && !(ok = mbar_wait_warp(&bars[EMPTY0 + st * GROUPS + k], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
+            if (k == GROUPS - 1 && lane == 0) {
+              sh.bits[st][w] = seen;
+              mbar_arrive(full);
             }
+#pragma unroll
+            for (int s = 2 * k; s < (k < 4 ? 2 * k + 2 : NSLAB); ++s)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) copy16_async(dst[i] + s * SLAB, bytes[i] ? src[i] + s * 128 : lp.rows, bytes[i]);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (j > u.j0 && !flushed) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            publish(kc - 1);
-          }
-          flushed = false;
+          if (!ok) break;
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        if (ok && !flushed) publish(kc - 1);
-        flushed = false;
       } else {
         // ========================================================== Q
         if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
         ++qc;
-#pragma unroll 4
-        for (int i = tid; i < NR * PIECES; i += 128) {
-          const int r = i / PIECES, c = i % PIECES;
-          const bool on = r < u.live;
-          const int row = u.row0 + r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = 16 * w + 4 * i + r, row = u.row0 + at;
+          const bool on = at < u.live;
           const uint8_t* src = p.q;
           if (on) src += 2 * (static_cast<int64_t>(u.a + row / p.G) * p.sq_s + (row % p.G) * p.sq_h + 8 * c);
-          copy16_async(smem_u32(sm + OFF_Q + (c >> 3) * SLAB + sw128_offset(r, c & 7)), src, on ? 16 : 0);
+          const uint32_t dst = smem_u32(sm + OFF_Q) + sw128_offset(at, c);
+#pragma unroll
+          for (int s = 0; s < NSLAB; ++s) copy16_async(dst + s * SLAB, on ? src + s * 128 : src, on ? 16 : 0);
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         fence_proxy_async_smem();
@@ -634,15 +667,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&bars[Q_FULL]);
       }
     }
-  } else if (warp < 4) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // copies in flight land before the CTA exits
+  } else if (warp < 8) {
     // ============================================================ softmax and output
-    const int tid = threadIdx.x;
-    const int ka = 16 * warp + (lane >> 2), c0 = 2 * (lane & 3);  // my keys: ka, ka + 8; my rows: 8 j + c0 + (0, 1)
-    const uint32_t quarter = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t bit_a = 1u << (ka & 15), bit_b = bit_a << 8;  // of group ``warp``
+    const int tid = threadIdx.x, w4 = warp & 3, half = warp >> 2;
+    const int ka = 16 * w4 + (lane >> 2);             // my keys: ka, ka + 8
+    const int c0 = 32 * half + 2 * (lane & 3);        // my rows: c0 + 8 j + (0, 1), j < 4
+    const int mine = column_of(lane), cm = c0 + 8 * (mine >> 1) + (mine & 1);  // the row that reduce8 leaves me
+    const uint32_t quarter = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t bit_a = 1u << (ka & 15), bit_b = bit_a << 8;  // of group w4
+    const auto larger = [](float x, float y) { return fmaxf(x, y); };
     uint32_t kc = 0;
-    // The four warps meet at named barriers, which have no limit: a warp whose wait ran
-    // out goes on (its results are void) to the next vote, where all four leave.
+    // The warps meet at named barriers, which have no limit: a warp whose wait ran out
+    // goes on (its results are void) to the next vote, where all leave.
     bool bad = false, dead = false;
     auto wait = [&](int bar, uint32_t parity, int code) { bad |= !mbar_wait_warp(&bars[bar], parity, wc, code); };
     for (uint32_t uc = 0; !dead; ++uc) {
@@ -655,69 +692,73 @@ __global__ void __launch_bounds__(THREADS, 1)
       if constexpr (!LISTS) {
         const KvReq r{u.a, u.nq, u.L, u.off, 0};
         int lo;
-        if (tid < NR) kv_row_keys(r, (u.row0 + imin(tid, u.live - 1)) / p.G, p.causal, 0, &lo, &sh.hi[tid]);
         kv_row_keys(r, u.row0 / p.G, p.causal, 0, &lo, &hi_all);
-        softmax_sync();
+        if (tid < NR) kv_row_keys(r, (u.row0 + imin(tid, u.live - 1)) / p.G, p.causal, 0, &lo, &sh.hi[tid]);
       }
-      float ref[16], l[16];
+      if (tid < NR) {
+        sh.ref[tid] = kNone;
+        const int row = u.row0 + imin(tid, u.live - 1);
+        sh.row[tid] = LISTS ? u.n * lp.so_b + u.a * p.so_s + row * p.so_h
+                            : static_cast<int64_t>(u.a + row / p.G) * p.so_s + (row % p.G) * p.so_h;
+      }
+      float ref[8], l[8];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) ref[c] = kNone, l[c] = 0.f;
+      for (int i = 0; i < 8; ++i) ref[i] = kNone, l[i] = 0.f;
+      uint32_t seen = 0;  // some group was loaded
+      softmax_sync();
       for (int j = u.j0; j < u.j1; ++j, ++kc) {
         const int st = kc % STAGES;
-        wait(KV_FULL0 + st, (kc / STAGES) & 1, kErrWaitKV);  // (for its bits)
+        wait(FULL0 + st * GROUPS + GROUPS - 1, (kc / STAGES) & 1, kErrWaitKV);  // (for its bits)
         const uint32_t b0 = sh.bits[st][0], b1 = sh.bits[st][1], b2 = sh.bits[st][2], b3 = sh.bits[st][3];
+        seen |= b0 | b1 | b2 | b3;
         wait(S_FULL0 + (kc & 1), (kc >> 1) & 1, kErrWaitS);
         tc_fence_after();
-        uint32_t sr[32];
-        tmem_ld_frag64(tmem + quarter + T_S + 64 * (kc & 1), sr);
+        float s[16];  // 4 j + (0, 1): key ka, rows c0 + 8 j + (0, 1); 4 j + (2, 3): key ka + 8
+        tmem_ld_frag32(tmem + quarter + T_S + 64 * (kc & 1) + 32 * half, reinterpret_cast<uint32_t*>(s));
         tmem_ld_wait();
-        float* const s = reinterpret_cast<float*>(sr);
         if ((b0 & b1 & b2 & b3) != 0xffffu || (j + 1) * KT > hi_all) {
-          const uint32_t w = sh.bits[st][warp];
+          const uint32_t w = sh.bits[st][w4];
           const bool va = w & bit_a, vb = w & bit_b;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int h = LISTS ? 0x7fffffff : sh.hi[8 * (c >> 1) + c0 + (c & 1)];
-            float& x = s[4 * (c >> 1) + (c & 1)];
-            float& y = s[4 * (c >> 1) + 2 + (c & 1)];
+          for (int i = 0; i < 8; ++i) {
+            const int h = LISTS ? 0x7fffffff : sh.hi[c0 + 8 * (i >> 1) + (i & 1)];
+            float& x = s[4 * (i >> 1) + (i & 1)];
+            float& y = s[4 * (i >> 1) + 2 + (i & 1)];
             if (!va || j * KT + ka >= h) x = -INFINITY;
             if (!vb || j * KT + ka + 8 >= h) y = -INFINITY;
           }
         }
-        float over = -INFINITY;  // log2 of my largest weight
+        float top[8], over = -INFINITY;  // over: log2 of my largest weight
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          over = fmaxf(over, fmaf(fmaxf(s[4 * (c >> 1) + (c & 1)], s[4 * (c >> 1) + 2 + (c & 1)]), p.scale_log2, -ref[c]));
+        for (int i = 0; i < 8; ++i) {
+          top[i] = fmaxf(s[4 * (i >> 1) + (i & 1)], s[4 * (i >> 1) + 2 + (i & 1)]);
+          over = fmaxf(over, fmaf(top[i], p.scale_log2, -ref[i]));
+        }
         if (softmax_any(over > kMost || bad)) {
           // ---- some row's weights outgrow the type: new references for those
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float m = fmaxf(s[4 * (c >> 1) + (c & 1)], s[4 * (c >> 1) + 2 + (c & 1)]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane < 4) sh.mx[warp][8 * (c >> 1) + c0 + (c & 1)] = m;
-          }
+          sh.mx[w4][cm] = reduce8(top, lane, larger);
           if ((dead = softmax_any(bad))) break;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int row = 8 * (c >> 1) + c0 + (c & 1);
-            const float m = fmaxf(fmaxf(sh.mx[0][row], sh.mx[1][row]), fmaxf(sh.mx[2][row], sh.mx[3][row])) * p.scale_log2;
-            float f = 1.f;
-            if (m - ref[c] > kMost) {
-              f = ref[c] == kNone ? 0.f : ex2(ref[c] - (m - kTop));
-              ref[c] = m - kTop;
-            }
-            l[c] *= f;
-            if (warp == 0 && lane < 4) sh.f[row] = f;
+          if (tid < NR) {
+            const float m = fmaxf(fmaxf(sh.mx[0][tid], sh.mx[1][tid]), fmaxf(sh.mx[2][tid], sh.mx[3][tid])) * p.scale_log2;
+            const float old = sh.ref[tid];
+            const bool grown = m - old > kMost;
+            sh.f[tid] = grown ? (old == kNone ? 0.f : ex2(old - (m - kTop))) : 1.f;
+            if (grown) sh.ref[tid] = m - kTop;
           }
           softmax_sync();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = c0 + 8 * (i >> 1) + (i & 1);
+            ref[i] = sh.ref[row];
+            l[i] *= sh.f[row];
+          }
           if (j > u.j0) {
             // O^T of the tiles so far, once their products have completed
-            wait(O_DONE, (kc - 1) & 1, kErrWaitDQFull);
+            wait(O_DONE0 + ((kc - 1) & 1), ((kc - 1) >> 1) & 1, kErrWaitDQFull);
             tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < 8; ++h) {
-              const uint32_t at = tmem + quarter + T_O + 32 * h;
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t at = tmem + quarter + T_O + 128 * half + 32 * h;
               const float* const f = sh.f + 32 * (h & 1);
               uint32_t r[32];
               tmem_ld32(at, r);
@@ -733,100 +774,81 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!LISTS && (u.L & 15) && j == (u.L - 1) / KT) {
           // rows behind the last key of its group: the scores have been made, the O products follow
           const int r0 = u.L & (KT - 1), n = (16 - (u.L & 15)) * 64;
-          for (int i = tid; i < n; i += 128)
+          for (int i = tid; i < n; i += SOFT)
             *reinterpret_cast<uint4*>(sm + OFF_K + st * TILE + (i & 7) * SLAB + (r0 + (i >> 6)) * 128 + (i >> 3 & 7) * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
         }
-        uint32_t pa[8], pb[8];
+        uint8_t* const pt = sm + p_at(st);  // (in place of the key part, which the scores have used)
 #pragma unroll
-        for (int c = 0; c < 16; c += 2) {
-          const float x0 = ex2(fmaf(s[2 * c], p.scale_log2, -ref[c])), x1 = ex2(fmaf(s[2 * c + 1], p.scale_log2, -ref[c + 1]));
-          const float y0 = ex2(fmaf(s[2 * c + 2], p.scale_log2, -ref[c])), y1 = ex2(fmaf(s[2 * c + 3], p.scale_log2, -ref[c + 1]));
-          l[c] += x0 + y0, l[c + 1] += x1 + y1;
-          pa[c / 2] = pack2<BF16>(x0, x1), pb[c / 2] = pack2<BF16>(y0, y1);
-        }
-        // the previous tile's O products have read P
-        if (kc >= 1) wait(O_DONE, (kc - 1) & 1, kErrWaitDSFree);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          *reinterpret_cast<uint32_t*>(sm + OFF_P + sw128_offset(ka, c) + 2 * c0) = pa[c];
-          *reinterpret_cast<uint32_t*>(sm + OFF_P + sw128_offset(ka + 8, c) + 2 * c0) = pb[c];
+        for (int i = 0; i < 8; i += 2) {
+          const float x0 = ex2(fmaf(s[2 * i], p.scale_log2, -ref[i])), x1 = ex2(fmaf(s[2 * i + 1], p.scale_log2, -ref[i + 1]));
+          const float y0 = ex2(fmaf(s[2 * i + 2], p.scale_log2, -ref[i])), y1 = ex2(fmaf(s[2 * i + 3], p.scale_log2, -ref[i + 1]));
+          l[i] += x0 + y0, l[i + 1] += x1 + y1;
+          const uint32_t at = 4 * half + i / 2;  // 16-byte piece of a key's 64 weights
+          *reinterpret_cast<uint32_t*>(pt + sw128_offset(ka, at) + 4 * (lane & 3)) = pack2<BF16>(x0, x1);
+          *reinterpret_cast<uint32_t*>(pt + sw128_offset(ka + 8, at) + 4 * (lane & 3)) = pack2<BF16>(y0, y1);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[P_READY]);
+        if (lane == 0) mbar_arrive(&bars[P_READY0 + (kc & 1)]);
       }
       if (dead) break;
       // ---- the rows' sums, then O
       const bool had = u.j1 > u.j0;
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
-        if (lane < 4) {
-          const int row = 8 * (c >> 1) + c0 + (c & 1);
-          sh.mx[warp][row] = l[c];
-          if (warp == 0) sh.ref[row] = ref[c];
-        }
-      }
+      sh.mx[w4][cm] = reduce8(l, lane, [](float x, float y) { return x + y; });
       softmax_sync();
-      // a row's place in o (lists: heads of a token; else query and head of the request)
-      auto o_at = [&](int r) -> int64_t {
-        if constexpr (LISTS) return u.n * lp.so_b + u.a * p.so_s + (u.row0 + r) * p.so_h;
-        const int row = u.row0 + r;
-        return static_cast<int64_t>(u.a + row / p.G) * p.so_s + (row % p.G) * p.so_h;
-      };
       if (tid < NR) {
         const float sum = (sh.mx[0][tid] + sh.mx[1][tid]) + (sh.mx[2][tid] + sh.mx[3][tid]);
+        const float m = sh.ref[tid];
         sh.f[tid] = sum == 0.f ? 0.f : 1.f / sum;
         if (tid < u.live) {
           if (u.slot < 0) {
-            const float lse = sum == 0.f ? -INFINITY : (sh.ref[tid] + log2f(sum)) * 0.69314718055994531f;
-            if constexpr (LISTS) {
-              p.lse[u.n * lp.sl_b + (u.row0 + tid) * p.sl_h + u.a * p.sl_s] = lse;
-            } else {
-              const int row = u.row0 + tid;
-              p.lse[(row % p.G) * p.sl_h + static_cast<int64_t>(u.a + row / p.G) * p.sl_s] = lse;
-            }
+            const int row = u.row0 + tid;
+            float* const lse = LISTS ? p.lse + (u.n * lp.sl_b + row * p.sl_h + u.a * p.sl_s)
+                                     : p.lse + ((row % p.G) * p.sl_h + static_cast<int64_t>(u.a + row / p.G) * p.sl_s);
+            *lse = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
           } else {
-            p.part_ml[static_cast<int64_t>(u.slot) * NR + tid] = make_float2(sh.ref[tid], sum);
+            p.part_ml[static_cast<int64_t>(u.slot) * NR + tid] = make_float2(m, sum);
           }
         }
       }
       softmax_sync();
       if (had) {
-        wait(O_DONE, (kc - 1) & 1, kErrWaitDQFull);
+        wait(O_DONE0 + ((kc - 1) & 1), ((kc - 1) >> 1) & 1, kErrWaitDQFull);
         tc_fence_after();
       }
+      // My 32 latent columns of two M-tiles, 32 rows at once.  (O of a unit none of whose
+      // groups was loaded holds anything.)
 #pragma unroll 1
-      for (int h = 0; h < 8; ++h) {
-        const int d = 128 * (h >> 1) + tid, r0 = 32 * (h & 1);  // my latent column, first row
+      for (int h = 0; h < 4; ++h) {
+        const int d = 256 * half + 128 * (h >> 1) + 32 * w4 + lane, r0 = 32 * (h & 1);
         if (r0 >= u.live) continue;
         uint32_t r[32];
-        if (had) {
-          tmem_ld32(tmem + quarter + T_O + 32 * h, r);
+        if (had && seen) {
+          tmem_ld32(tmem + quarter + T_O + 128 * half + 32 * h, r);
           tmem_ld_wait();
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;
         }
+        const int n = imin(32, u.live - r0);
         if (u.slot >= 0) {
           float* const out = p.part_o + (static_cast<int64_t>(u.slot) * NR + r0) * kLatDim + d;
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (r0 + e < u.live) out[e * kLatDim] = __uint_as_float(r[e]);
+            if (e < n) out[e * kLatDim] = __uint_as_float(r[e]);
         } else {
           // neighbouring lanes swap, so that each stores two columns of one row of a pair
+          uint8_t* const out = p.o + 2 * (d & ~1);
+          const int64_t* const at = sh.row + r0 + (lane & 1);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            // (a row that has seen no key may find anything in O)
-            const float f0 = sh.f[r0 + e], f1 = sh.f[r0 + e + 1];
-            const float x = f0 == 0.f ? 0.f : __uint_as_float(r[e]) * f0, y = f1 == 0.f ? 0.f : __uint_as_float(r[e + 1]) * f1;
-            const float z = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
-            const uint32_t w = lane & 1 ? pack2<BF16>(z, y) : pack2<BF16>(x, z);
-            const int row = r0 + e + (lane & 1);
-            if (row < u.live) *reinterpret_cast<uint32_t*>(p.o + 2 * (o_at(row) + (d & ~1))) = w;
+            const float2 f = *reinterpret_cast<const float2*>(sh.f + r0 + e);
+            const uint32_t w = pack2<BF16>(__uint_as_float(r[e]) * f.x, __uint_as_float(r[e + 1]) * f.y);  // rows e, e + 1
+            const uint32_t z = __shfl_xor_sync(0xffffffffu, w, 1);
+            const uint32_t y = lane & 1 ? __byte_perm(z, w, 0x7632) : __byte_perm(w, z, 0x5410);
+            if (e + (lane & 1) < n) *reinterpret_cast<uint32_t*>(out + 2 * at[e]) = y;
           }
         }
       }
@@ -842,7 +864,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 13) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
