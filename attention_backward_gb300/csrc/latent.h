@@ -36,9 +36,9 @@ cudaError_t launch_latent_write(const LatWriteParams& p, bool bf16, cudaStream_t
 // word, with batch strides and lists here.
 struct LatParams {
   KvAttnParams a;
+  const uint8_t* rows;  // of the cache, or kv
+  int64_t row_stride;   // elements
   // lists
-  const uint8_t* rows;
-  int64_t row_stride;  // elements
   const int* idx;
   int64_t si_b, si_s, si_h;
   int64_t so_b, sl_b;
@@ -54,10 +54,7 @@ constexpr int kLatMinWork = 4;
 constexpr int kLatMaxCtas = 160;
 
 // ``group``: CTAs (1 or 2) that share a part of the line, 64 rows each of its units.
-// ``pages``: the cache's rows, dims (576, page_size, num_blocks, 1), box 64 columns x the
-// tokens of a page, at most kLatKeys.
-cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& pages, bool bf16, int group, int sms,
-                                cudaStream_t st);
+cudaError_t launch_latent_cache(const LatParams& p, bool bf16, int group, int sms, cudaStream_t st);
 // ``q``: dims (576, H, S, B), box 64 columns x 64 heads of a token.
 cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st);
 // Joins rows that were split over CTAs and writes the call's error word.

@@ -177,18 +177,13 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   if (slse.s < 1 || slse.h < 1) return ATTN_ERR_INVALID_ARG;
   const LatWs w = lat_ws();
   if (workspace_bytes < static_cast<size_t>(w.total)) return ATTN_ERR_WORKSPACE;
-  CUtensorMap pages;
-  const int64_t page_stride = cache->page_size * cache->row_stride;
-  if (page_stride >= (int64_t(1) << 39)) return ATTN_ERR_UNSUPPORTED;
-  if (!make_map(&pages, cache->rows, dtype, kLatRow, {cache->page_size, cache->num_blocks, 1},
-                {cache->row_stride, page_stride, page_stride}, {imin(static_cast<int>(cache->page_size), kLatKeys), 1, 1}))
-    return ATTN_ERR_INVALID_ARG;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   LatParams lp{};
   KvAttnParams& p = lp.a;
   p.q = static_cast<const uint8_t*>(q), p.sq_s = sq.s, p.sq_h = sq.h;
   p.o = static_cast<uint8_t*>(o), p.so_s = so.s, p.so_h = so.h;
   p.lse = lse, p.sl_s = slse.s, p.sl_h = slse.h;
+  lp.rows = static_cast<const uint8_t*>(cache->rows), lp.row_stride = cache->row_stride;
   p.table = block_table, p.table_stride = table_stride, p.max_blocks = static_cast<int>(max_blocks);
   p.num_blocks = static_cast<int>(cache->num_blocks), p.page_log2 = page_log2(cache->page_size);
   p.cu = cu_seqlens, p.kv_lens = kv_lens, p.N = static_cast<int>(num_seqs), p.T = static_cast<int>(T);
@@ -208,7 +203,7 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   // more) does not fit one.
   const int group = T * H > num_seqs * kLatRows ? 2 : 1;
   const int ctas = imin(sms, kLatMaxCtas) / group * group;
-  if (const cudaError_t e = launch_latent_cache(lp, pages, bf16, group, sms, st); e != cudaSuccess) return launch_status(e);
+  if (const cudaError_t e = launch_latent_cache(lp, bf16, group, sms, st); e != cudaSuccess) return launch_status(e);
   return launch_status(launch_latent_join(lp, bf16, group, ctas, sms, st));
 }
 

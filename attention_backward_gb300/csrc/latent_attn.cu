@@ -28,18 +28,14 @@
 // than 64 rows two CTAs share a part, 64 rows each of units of 128, so that the second
 // reads its keys from L2.  Lists: a unit a token and KV group, longest lists first.
 //
-// Rows of a page come as TMA boxes; listed rows by 16-byte asynchronous copies of four
-// warps, a slab's swizzle written by address.  (TMA gathers of four rows took 37 ns each,
-// 5.4 us a tile, four times what the products and the softmax of one take.)
+// Rows are loaded by 16-byte asynchronous copies of four warps, a slab's swizzle written
+// by address; rows that are not visible are filled with zeros.  (TMA gathers of four rows
+// took 37 ns each, 5.4 us a tile; boxes of 64 rows are as fast as the copies, but
+// take 32 ns each whatever their size, and pages of 16 need 36 a tile.)
 //
-// Keys that nobody sees: scores of rows that were not loaded are masked; their 16-key
-// groups are left out of the O products, and rows behind the last key inside a group are
-// zeroed by the softmax warps (0 * NaN is NaN).  Listed rows that are not visible are
-// filled with zeros.
-//
-// Warp roles (16 warps): 0-7 softmax and output, 8-11 loads of Q (lists: of listed
-// rows), 12 pages (lists: Q), 13 issue of the scores, 14 the walk, a unit ahead of the
-// others, 15 issue of O.  Every wait is bounded.
+// Warp roles (16 warps): 0-7 softmax and output, 8-11 loads of rows, 12 of Q, 13 issue
+// of the scores, 14 the walk, a unit ahead of the others, 15 issue of O.  Every wait is
+// bounded.
 #include <cmath>
 #include <type_traits>
 
@@ -61,14 +57,13 @@ constexpr int STAGES = 2;
 // A stage is loaded and freed in five groups: the two slabs of each M-tile of O, and the
 // key part, whose slab takes P once the scores are made.
 constexpr int GROUPS = 5;
-__device__ __forceinline__ int group_slabs(int g) { return g < 4 ? 2 : 1; }
 constexpr int kWarps = 16, THREADS = kWarps * 32;
 constexpr int SOFT = 256;  // threads of the softmax warps
 constexpr float kTop = 7.f, kMost = 15.f;  // log2 of a row's largest weight when its max is taken, and of the most it may grow to
 constexpr float kNone = -1e30f;            // reference of a row that has seen no key
 
 enum LatBar : int {
-  Q_FULL = 0,                // 4 loading warps (lists: a copy)
+  Q_FULL = 0,                // the loading warp (lists: a copy)
   Q_EMPTY,                   // every S of the unit has completed
   FULL0,                     // per stage and group of slabs
   EMPTY0 = FULL0 + STAGES * GROUPS,  // the same: its last products have completed
@@ -99,7 +94,7 @@ struct LatShared {
   float ref[NR];
   int hi[NR];         // keys that a row sees
   LatUnit units[2];
-  uint32_t bits[STAGES][4];  // of a stage's tile and 16-key group: its keys that are loaded and visible, if its mask leaves them
+  uint32_t bits[STAGES][4];  // of a stage's tile and 16-key group: its keys that are held, and visible if the mask leaves them
   uint64_t bars[NUM_BARS];
   int64_t work[kWarps];
   uint32_t tmem;
@@ -272,7 +267,7 @@ __device__ __forceinline__ LatCursor walk_to(const KvAttnParams& p, int n0, int6
 // GROUP: CTAs that share a part of the line; 0: index lists.
 template <int GROUP, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ LatParams lp) {
+    latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ LatParams lp) {  // map: of Q, for lists
   constexpr bool LISTS = GROUP == 0;
   constexpr int RT = NR * (LISTS ? 1 : GROUP);
   const KvAttnParams& p = lp.a;
@@ -329,11 +324,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
-    mbar_init(&bars[Q_FULL], LISTS ? 1 : 4);
+    mbar_init(&bars[Q_FULL], 1);
     mbar_init(&bars[Q_EMPTY], 1);
     for (int i = 0; i < STAGES * GROUPS; ++i) {
-      // (lists: every copying thread; of the last group also a lane a warp, for the bits)
-      mbar_init(&bars[FULL0 + i], LISTS ? (i % GROUPS == GROUPS - 1 ? 132 : 128) : 1);
+      // every copying thread; of the last group also a lane a warp, for the bits
+      mbar_init(&bars[FULL0 + i], i % GROUPS == GROUPS - 1 ? 132 : 128);
       mbar_init(&bars[EMPTY0 + i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -438,68 +433,39 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else if (warp == 12) {
-    uint32_t kc = 0, qc = 0;
+    // ============================================================ Q
+    uint32_t qc = 0;
     bool ok = true;
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
       if (u.valid == 2 || u.j1 <= u.j0) continue;
+      if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
+      ++qc;
       if constexpr (LISTS) {
-        // ========================================================== Q: 64 heads of the token (those past its group are not used)
-        if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
+        // 64 heads of the token (those past its group are not used)
         if (lane == 0) mbar_arrive_expect_tx(&bars[Q_FULL], TILE);
         __syncwarp();
-        if (lane < NSLAB)
-          tma_load_4d(sm + OFF_Q + lane * SLAB, &map, &bars[Q_FULL], lane * 64, u.row0, u.a, u.n);
-        ++qc;
+        if (lane < NSLAB) tma_load_4d(sm + OFF_Q + lane * SLAB, &map, &bars[Q_FULL], lane * 64, u.row0, u.a, u.n);
       } else {
-        // ========================================================== pages
-        // Lanes 0-3 look up the pages of a tile's 16-key groups, a tile ahead; a copy
-        // takes 64 columns of a page's tokens in the tile.
-        const int* const table = p.table + static_cast<int64_t>(u.n) * p.table_stride;
-        const int span = p.page_log2 >= 6 ? 4 : 1 << (p.page_log2 - 4);  // groups a copy
-        auto look_up = [&](int j) {
-          const int k = j * KT + 16 * lane;
-          const int page = lane < 4 && j < u.j1 && k < u.L ? table[k >> p.page_log2] : -1;
-          return page < p.num_blocks ? page : -1;
-        };
-        int next = look_up(u.j0);
-        for (int j = u.j0; j < u.j1; ++j, ++kc) {
-          const int st = kc % STAGES;
-          const uint32_t n = kc / STAGES;
-          const int page = next;
-          const uint32_t held = __ballot_sync(0xffffffffu, page >= 0);
-          int copies = 0;  // of a slab
-          for (int g = 0; g < 4; g += span) copies += held >> g & 1;
-          // lane i copies the i / 2-th piece of a group's first or second slab
-          const int piece = (lane >> 1) * span, pg = __shfl_sync(0xffffffffu, page, piece & 3);
-          const bool mine = piece < 4 && pg >= 0;
-          const int token = (j * KT + 16 * piece) & ((1 << p.page_log2) - 1);
-          uint8_t* const dst = sm + OFF_K + st * TILE + piece * 2048;
-          for (int g = 0; g < GROUPS; ++g) {
-            uint64_t* const full = &bars[FULL0 + st * GROUPS + g];
-            if (n >= 1 && !(ok = mbar_wait_warp(&bars[EMPTY0 + st * GROUPS + g], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
-            if (g == GROUPS - 1 && lane < 4) sh.bits[st][lane] = page >= 0 ? 0xffffu : 0u;
-            __syncwarp();
-            if (lane == 0) {
-              if (copies) mbar_arrive_expect_tx(full, copies * span * 16 * 128 * group_slabs(g));
-              else mbar_arrive(full);
-            }
-            __syncwarp();
-            const int slab = 2 * g + (lane & 1);
-            if (mine && slab < NSLAB) tma_load_4d(dst + slab * SLAB, &map, full, slab * 64, token, pg, 0);
-          }
-          if (!ok) break;
-          next = look_up(j + 1);
+        const int r = lane >> 3, c = lane & 7;  // four rows at once, 128 bytes each
+#pragma unroll 2
+        for (int at = r; at < NR; at += 4) {
+          const int row = u.row0 + at;
+          const bool on = at < u.live;
+          const uint8_t* src = p.q;
+          if (on) src += 2 * (static_cast<int64_t>(u.a + row / p.G) * p.sq_s + (row % p.G) * p.sq_h + 8 * c);
+          const uint32_t dst = smem_u32(sm + OFF_Q) + sw128_offset(at, c);
+#pragma unroll
+          for (int s = 0; s < NSLAB; ++s) copy16_async(dst + s * SLAB, on ? src + s * 128 : src, on ? 16 : 0);
         }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Q_FULL]);
       }
     }
-    // copies in flight land before the CTA exits
-    if (lane == 0) {
-      if (qc >= 1) mbar_drain(&bars[Q_FULL], (qc - 1) & 1);
-      for (uint32_t i = kc > static_cast<uint32_t>(STAGES) ? kc - STAGES : 0u; i < kc; ++i)
-        for (int g = 0; g < GROUPS; ++g) mbar_drain(&bars[FULL0 + i % STAGES * GROUPS + g], (i / STAGES) & 1);
-    }
+    if (LISTS && lane == 0 && qc >= 1) mbar_drain(&bars[Q_FULL], (qc - 1) & 1);  // a copy in flight lands before the CTA exits
     __syncwarp();
   } else if (warp == 13) {
     // ============================================================ scores
@@ -525,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
           if (!(ok = mbar_wait_warp(&bars[FULL0 + st * GROUPS + g], phase, wc, kErrWaitKV))) break;
-          if constexpr (LISTS) fence_proxy_async_smem();  // (the copies are the generic proxy's)
+          fence_proxy_async_smem();  // (the copies are the generic proxy's)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < (g < 4 ? 8 : 4); ++kk) {
@@ -557,38 +523,20 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the softmax warps have read the O of the unit before
       if (oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
       ++oc;
-      uint32_t begun = 0;  // O holds something of this unit
+      const uint32_t first = kc;
       for (const uint32_t end = kc + uniform(u.j1 - u.j0); kc < end; ++kc) {
         const uint32_t st = kc % STAGES;
         if (!(ok = mbar_wait_warp(&bars[P_READY0 + (kc & 1)], (kc >> 1) & 1, wu, kErrWaitP))) break;
         tc_fence_after();
         const uint64_t c = c_mn + sdesc_step(st * TILE), pp = p_mn + sdesc_step(st * TILE);
-        uint32_t mask = 15;  // 16-key groups that are loaded
-        if constexpr (!LISTS) mask = __ballot_sync(0xffffffffu, lane < 4 && sh.bits[st][lane & 3] != 0u);
-        if (mask == 15) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < 4; ++m) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss_e(tmem + T_O + 64 * m, c + sdesc_step(2 * m * SLAB + kk * 2048), pp + sdesc_step(kk * 2048), IDESC,
-                       kk > 0 ? 1u : begun, one);
-            mma_commit_w(&bars[EMPTY0 + st * GROUPS + m]);
-          }
-        } else {
-#pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            uint32_t some = begun;
-#pragma unroll 1
-            for (int kk = 0; kk < 4; ++kk)
-              if (mask >> kk & 1) {
-                mma_ss_e(tmem + T_O + 64 * m, c + sdesc_step(2 * m * SLAB + kk * 2048), pp + sdesc_step(kk * 2048), IDESC,
-                         some, one);
-                some = 1;
-              }
-            mma_commit_w(&bars[EMPTY0 + st * GROUPS + m]);
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss_e(tmem + T_O + 64 * m, c + sdesc_step(2 * m * SLAB + kk * 2048), pp + sdesc_step(kk * 2048), IDESC,
+                     kc != first || kk > 0, one);
+          mma_commit_w(&bars[EMPTY0 + st * GROUPS + m]);
         }
-        begun |= mask;
         mma_commit_w(&bars[EMPTY0 + st * GROUPS + GROUPS - 1]);
         mma_commit_w(&bars[O_DONE0 + (kc & 1)]);
       }
@@ -597,74 +545,61 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) mbar_drain(&bars[DRAIN0 + 1], 0);
     __syncwarp();
   } else if (warp >= 8 && warp < 12) {
-    const int w = warp - 8, r = lane >> 3, c = lane & 7;  // 16 rows a warp, 4 at once, 128 bytes each
-    uint32_t qc = 0, kc = 0;
+    // ============================================================ rows: 16 of a tile a warp
+    // Eight lanes copy 128 bytes of a row, a warp four rows of a slab at once; a barrier
+    // counts the copies' completion itself.  Lanes look up rows a tile ahead.
+    const int w = warp - 8, r = lane >> 3, c = lane & 7;
+    uint32_t kc = 0;
     bool ok = true;
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
-      if (u.valid == 2 || u.j1 <= u.j0) continue;
-      if constexpr (LISTS) {
-        // ========================================================== listed rows: 16 of a tile a warp
-        // (a barrier counts the copies' completion itself)
-        const int g = u.row0 / lp.gh;
-        const int* const list = lp.idx + u.n * lp.si_b + static_cast<int64_t>(u.a) * lp.si_s + g * lp.si_h;
-        const int64_t base = static_cast<int64_t>(u.n) * lp.SKV;
-        auto look_up = [&](int j) {
-          const int k = j * KT + 16 * w + (lane & 15);
+      if (u.valid == 2) continue;
+      const int g = LISTS ? u.row0 / lp.gh : 0;
+      const int* const list = LISTS ? lp.idx + u.n * lp.si_b + static_cast<int64_t>(u.a) * lp.si_s + g * lp.si_h
+                                    : p.table + static_cast<int64_t>(u.n) * p.table_stride;
+      auto look_up = [&](int j) {  // a row of the cache, or of the batch row's; -1: none
+        const int k = j * KT + 16 * w + (lane & 15);
+        if constexpr (LISTS) {
           const int i = j < u.j1 && k < lp.topk ? list[k] : -1;
           return i >= 0 && i < lp.SKV ? i : -1;
-        };
-        int next = look_up(u.j0);
-        for (int j = u.j0; j < u.j1; ++j, ++kc) {
-          const int st = kc % STAGES;
-          const uint32_t n = kc / STAGES;
-          const int row = next;
-          next = look_up(j + 1);
-          const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-          const uint8_t* src[4];
-          uint32_t dst[4], bytes[4];
+        } else {
+          const int page = j < u.j1 && k < u.L ? list[k >> p.page_log2] : -1;
+          return page >= 0 && page < p.num_blocks ? (page << p.page_log2) + (k & ((1 << p.page_log2) - 1)) : -1;
+        }
+      };
+      int next = look_up(u.j0);
+      for (int j = u.j0; j < u.j1; ++j, ++kc) {
+        const int st = kc % STAGES;
+        const uint32_t n = kc / STAGES;
+        const int row = next;
+        next = look_up(j + 1);
+        const uint32_t held = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+        const uint8_t* src[4];
+        uint32_t dst[4], bytes[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // my rows 4 i + r
-            const int at = __shfl_sync(0xffffffffu, row, 4 * i + r);
-            src[i] = lp.rows + (at < 0 ? 0 : 2 * (((base + at) * lp.HKV + g) * lp.row_stride + 8 * c));
-            dst[i] = smem_u32(sm + OFF_K + st * TILE) + sw128_offset(16 * w + 4 * i + r, c);
-            bytes[i] = at < 0 ? 0u : 16u;
+        for (int i = 0; i < 4; ++i) {  // my rows 4 i + r
+          const int at = __shfl_sync(0xffffffffu, row, 4 * i + r);
+          const int64_t line = LISTS ? (static_cast<int64_t>(u.n) * lp.SKV + at) * lp.HKV + g : at;
+          src[i] = lp.rows + (at < 0 ? 0 : 2 * (line * lp.row_stride + 8 * c));
+          dst[i] = smem_u32(sm + OFF_K + st * TILE) + sw128_offset(16 * w + 4 * i + r, c);
+          bytes[i] = at < 0 ? 0u : 16u;
+        }
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+          uint64_t* const full = &bars[FULL0 + st * GROUPS + k];
+          if (n >= 1 && !(ok = mbar_wait_warp(&bars[EMPTY0 + st * GROUPS + k], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
+          if (k == GROUPS - 1 && lane == 0) {
+            sh.bits[st][w] = held;
+            mbar_arrive(full);
           }
 #pragma unroll
-          for (int k = 0; k < GROUPS; ++k) {
-            uint64_t* const full = &bars[FULL0 + st * GROUPS + k];
-            if (n >= 1 && !(ok = mbar_wait_warp(&bars[EMPTY0 + st * GROUPS + k], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
-            if (k == GROUPS - 1 && lane == 0) {
-              sh.bits[st][w] = seen;
-              mbar_arrive(full);
-            }
+          for (int s = 2 * k; s < (k < 4 ? 2 * k + 2 : NSLAB); ++s)
 #pragma unroll
-            for (int s = 2 * k; s < (k < 4 ? 2 * k + 2 : NSLAB); ++s)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) copy16_async(dst[i] + s * SLAB, bytes[i] ? src[i] + s * 128 : lp.rows, bytes[i]);
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
-          }
-          if (!ok) break;
+            for (int i = 0; i < 4; ++i) copy16_async(dst[i] + s * SLAB, bytes[i] ? src[i] + s * 128 : lp.rows, bytes[i]);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
         }
-      } else {
-        // ========================================================== Q
-        if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
-        ++qc;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = 16 * w + 4 * i + r, row = u.row0 + at;
-          const bool on = at < u.live;
-          const uint8_t* src = p.q;
-          if (on) src += 2 * (static_cast<int64_t>(u.a + row / p.G) * p.sq_s + (row % p.G) * p.sq_h + 8 * c);
-          const uint32_t dst = smem_u32(sm + OFF_Q) + sw128_offset(at, c);
-#pragma unroll
-          for (int s = 0; s < NSLAB; ++s) copy16_async(dst + s * SLAB, on ? src + s * 128 : src, on ? 16 : 0);
-        }
-        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[Q_FULL]);
+        if (!ok) break;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // copies in flight land before the CTA exits
@@ -704,13 +639,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       float ref[8], l[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) ref[i] = kNone, l[i] = 0.f;
-      uint32_t seen = 0;  // some group was loaded
       softmax_sync();
       for (int j = u.j0; j < u.j1; ++j, ++kc) {
         const int st = kc % STAGES;
         wait(FULL0 + st * GROUPS + GROUPS - 1, (kc / STAGES) & 1, kErrWaitKV);  // (for its bits)
         const uint32_t b0 = sh.bits[st][0], b1 = sh.bits[st][1], b2 = sh.bits[st][2], b3 = sh.bits[st][3];
-        seen |= b0 | b1 | b2 | b3;
         wait(S_FULL0 + (kc & 1), (kc >> 1) & 1, kErrWaitS);
         tc_fence_after();
         float s[16];  // 4 j + (0, 1): key ka, rows c0 + 8 j + (0, 1); 4 j + (2, 3): key ka + 8
@@ -771,13 +704,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_st_wait();
           }
         }
-        if (!LISTS && (u.L & 15) && j == (u.L - 1) / KT) {
-          // rows behind the last key of its group: the scores have been made, the O products follow
-          const int r0 = u.L & (KT - 1), n = (16 - (u.L & 15)) * 64;
-          for (int i = tid; i < n; i += SOFT)
-            *reinterpret_cast<uint4*>(sm + OFF_K + st * TILE + (i & 7) * SLAB + (r0 + (i >> 6)) * 128 + (i >> 3 & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
         uint8_t* const pt = sm + p_at(st);  // (in place of the key part, which the scores have used)
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -818,14 +744,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         wait(O_DONE0 + ((kc - 1) & 1), ((kc - 1) >> 1) & 1, kErrWaitDQFull);
         tc_fence_after();
       }
-      // My 32 latent columns of two M-tiles, 32 rows at once.  (O of a unit none of whose
-      // groups was loaded holds anything.)
+      // my 32 latent columns of two M-tiles, 32 rows at once
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         const int d = 256 * half + 128 * (h >> 1) + 32 * w4 + lane, r0 = 32 * (h & 1);
         if (r0 >= u.live) continue;
         uint32_t r[32];
-        if (had && seen) {
+        if (had) {
           tmem_ld32(tmem + quarter + T_O + 128 * half + 32 * h, r);
           tmem_ld_wait();
         } else {
@@ -881,11 +806,11 @@ cudaError_t launch_t(const LatParams& p, const CUtensorMap& map, int grid, cudaS
 
 }  // namespace
 
-cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& pages, bool bf16, int group, int sms,
-                                cudaStream_t st) {
+cudaError_t launch_latent_cache(const LatParams& p, bool bf16, int group, int sms, cudaStream_t st) {
+  const CUtensorMap none{};
   const int grid = imin(sms, kLatMaxCtas) / group * group;
-  if (group == 1) return bf16 ? launch_t<1, true>(p, pages, grid, st) : launch_t<1, false>(p, pages, grid, st);
-  return bf16 ? launch_t<2, true>(p, pages, grid, st) : launch_t<2, false>(p, pages, grid, st);
+  if (group == 1) return bf16 ? launch_t<1, true>(p, none, grid, st) : launch_t<1, false>(p, none, grid, st);
+  return bf16 ? launch_t<2, true>(p, none, grid, st) : launch_t<2, false>(p, none, grid, st);
 }
 
 cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st) {
