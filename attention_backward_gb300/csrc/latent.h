@@ -50,11 +50,13 @@ struct LatParams {
 constexpr int kLatRows = 64;
 constexpr int kLatKeys = 64;
 constexpr int kLatCost = 2;
-constexpr int kLatMinWork = 4;
+constexpr int kLatMinWork = 2;
 constexpr int kLatMaxCtas = 160;
 
 // ``group``: CTAs (1 or 2) that share a part of the line, 64 rows each of its units.
-cudaError_t launch_latent_cache(const LatParams& p, bool bf16, int group, int sms, cudaStream_t st);
+// ``q``: where a.q is null, rows of q as dims (576, T * H, 1, 1), box 64 columns x 64 rows.
+cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& q, bool bf16, int group, int sms,
+                                cudaStream_t st);
 // ``q``: dims (576, H, S, B), box 64 columns x 64 heads of a token.
 cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st);
 // Joins rows that were split over CTAs and writes the call's error word.

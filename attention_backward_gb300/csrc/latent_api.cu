@@ -180,7 +180,15 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   LatParams lp{};
   KvAttnParams& p = lp.a;
-  p.q = static_cast<const uint8_t*>(q), p.sq_s = sq.s, p.sq_h = sq.h;
+  // Rows of q that are evenly spaced come as boxes of 64, others (heads of a wider tensor) by
+  // copies of one warp: 1.0 and 6 us a unit of 64 rows.
+  CUtensorMap rows{};
+  if (H == 1 || T == 1 || sq.s == H * sq.h) {
+    const int64_t step = H == 1 ? sq.s : sq.h;
+    if (!make_map(&rows, q, dtype, kLatRow, {T * H, 1, 1}, {step, step, step}, {kLatRows, 1, 1})) return ATTN_ERR_INVALID_ARG;
+  } else {
+    p.q = static_cast<const uint8_t*>(q), p.sq_s = sq.s, p.sq_h = sq.h;
+  }
   p.o = static_cast<uint8_t*>(o), p.so_s = so.s, p.so_h = so.h;
   p.lse = lse, p.sl_s = slse.s, p.sl_h = slse.h;
   lp.rows = static_cast<const uint8_t*>(cache->rows), lp.row_stride = cache->row_stride;
@@ -203,7 +211,7 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   // more) does not fit one.
   const int group = T * H > num_seqs * kLatRows ? 2 : 1;
   const int ctas = imin(sms, kLatMaxCtas) / group * group;
-  if (const cudaError_t e = launch_latent_cache(lp, bf16, group, sms, st); e != cudaSuccess) return launch_status(e);
+  if (const cudaError_t e = launch_latent_cache(lp, rows, bf16, group, sms, st); e != cudaSuccess) return launch_status(e);
   return launch_status(launch_latent_join(lp, bf16, group, ctas, sms, st));
 }
 

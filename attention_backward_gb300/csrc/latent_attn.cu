@@ -87,6 +87,12 @@ struct LatUnit {
   int slot;  // -1: the whole unit, else the slot of its partial rows
 };
 
+// A place on the line: request, row tile, position in it.
+struct LatCursor {
+  int n, rt, pos;
+  KvReq r;
+};
+
 struct LatShared {
   int64_t row[NR];    // a row's place in o
   float mx[4][NR];    // per quarter of the keys and row: a max, or a sum
@@ -96,7 +102,8 @@ struct LatShared {
   LatUnit units[2];
   uint32_t bits[STAGES][4];  // of a stage's tile and 16-key group: its keys that are held, and visible if the mask leaves them
   uint64_t bars[NUM_BARS];
-  int64_t work[kWarps];
+  int64_t work[kWarps];  // line positions of each warp's requests
+  LatCursor cursor;
   uint32_t tmem;
   int abort;
 };
@@ -172,85 +179,79 @@ __device__ __forceinline__ float reduce8(float (&v)[8], int lane, F f) {
   return v[0];
 }
 
-// ---------------------------------------------------------------- the walk along the line (one warp)
+// ---------------------------------------------------------------- the line
 
+template <int RT>
+__device__ __forceinline__ int tile_work(const KvReq& r, int rt, const KvAttnParams& p) {
+  return kv_row_tile<RT, KT>(r, rt, p).n + kLatCost;
+}
+
+// Positions of a request, all lanes together.
 template <int RT>
 __device__ __forceinline__ int64_t lanes_work(const KvAttnParams& p, const KvReq& r) {
   int64_t w = 0;
   const int nt = kv_row_tiles<RT>(r);
-  for (int rt = threadIdx.x & 31; rt < nt; rt += 32) w += kv_row_tile<RT, KT>(r, rt, p).n + kLatCost;
+  for (int rt = threadIdx.x & 31; rt < nt; rt += 32) w += tile_work<RT>(r, rt, p);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
   return w;
 }
 
-// Work of the requests [n0, n1), all lanes together.  A lane takes a request whose
-// rows are one tile; the others are taken by all lanes.
+__device__ __forceinline__ int64_t lanes_scan(int64_t w) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += v;
+  }
+  return w;
+}
+
+__device__ __forceinline__ KvReq from_lane(const KvReq& r, int src) {
+  return {__shfl_sync(0xffffffffu, r.a, src), __shfl_sync(0xffffffffu, r.nq, src), __shfl_sync(0xffffffffu, r.L, src),
+          __shfl_sync(0xffffffffu, r.off, src), __shfl_sync(0xffffffffu, r.R, src)};
+}
+
+// Each thread has ``per`` requests in a row: their positions, and the last of them.
 template <int RT>
-__device__ __forceinline__ int64_t requests_work(const KvAttnParams& p, int n0, int n1) {
+__device__ __forceinline__ int64_t thread_work(const KvAttnParams& p, int per, KvReq* last) {
   const int lane = threadIdx.x & 31;
   int64_t w = 0;
-  for (int b = n0; b < n1; b += 32) {
-    KvReq mine{};
-    if (b + lane < n1) mine = kv_request(b + lane, p);
-    if (mine.R > 0 && mine.R <= RT) w += kv_row_tile<RT, KT>(mine, 0, p).n + kLatCost;
-    for (uint32_t m = __ballot_sync(0xffffffffu, mine.R > RT); m != 0; m &= m - 1) {
-      const KvReq r = kv_request(b + __ffs(m) - 1, p);
-      const int64_t all = lanes_work<RT>(p, r);
-      if (lane == 0) w += all;
+  for (int k = 0; k < per; ++k) {
+    const int n = threadIdx.x * per + k;
+    KvReq r{};
+    if (n < p.N) r = kv_request(n, p);
+    if (r.R > 0 && r.R <= RT) w += tile_work<RT>(r, 0, p);
+    for (uint32_t m = __ballot_sync(0xffffffffu, r.R > RT); m != 0; m &= m - 1) {  // of several row tiles
+      const int src = __ffs(m) - 1;
+      const int64_t all = lanes_work<RT>(p, from_lane(r, src));
+      if (lane == src) w += all;
     }
+    *last = r;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
   return w;
 }
 
-struct LatCursor {
-  int n, rt, pos;
-};
-
-// Cursor of position x counted from request n0 (x lies on the line).
+// The cursor of position x, which lies x positions behind the start of the requests
+// [n0, n0 + per) and within them (one warp); r: the last of them.
 template <int RT>
-__device__ __forceinline__ LatCursor walk_to(const KvAttnParams& p, int n0, int64_t x) {
+__device__ __forceinline__ LatCursor find(const KvAttnParams& p, int n0, int per, KvReq r, int64_t x) {
   const int lane = threadIdx.x & 31;
-  LatCursor c{n0, 0, 0};
-  for (int b = n0; b < p.N; b += 32) {
-    KvReq mine{};
-    if (b + lane < p.N) mine = kv_request(b + lane, p);
-    bool found = false;
-    int64_t w = mine.R > 0 && mine.R <= RT ? kv_row_tile<RT, KT>(mine, 0, p).n + kLatCost : 0;
-    for (uint32_t m = __ballot_sync(0xffffffffu, mine.R > RT); m != 0; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const int64_t all = lanes_work<RT>(p, kv_request(b + src, p));
-      if (lane == src) w = all;
+  LatCursor c{n0 + per - 1, 0, 0, {}};
+  for (int k = 0; k + 1 < per; ++k) {
+    const KvReq q = kv_request(n0 + k, p);
+    const int64_t w = lanes_work<RT>(p, q);
+    if (x < w) {
+      c.n = n0 + k, r = q;
+      break;
     }
-    int64_t inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    const uint32_t past = __ballot_sync(0xffffffffu, x < inc);
-    if (past != 0) {
-      const int src = __ffs(past) - 1;
-      x -= __shfl_sync(0xffffffffu, inc - w, src);
-      c.n = b + src;
-      found = true;
-    } else {
-      x -= __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (found) break;
+    x -= w;
   }
-  const KvReq r = kv_request(c.n, p);
+  c.r = r;
   const int nt = kv_row_tiles<RT>(r);
   for (int b = 0; b < nt; b += 32) {
-    const int64_t w = b + lane < nt ? kv_row_tile<RT, KT>(r, b + lane, p).n + kLatCost : 0;
-    int64_t inc = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
+    const int64_t w = b + lane < nt ? tile_work<RT>(r, b + lane, p) : 0;
+    const int64_t inc = lanes_scan(w);
     const uint32_t past = __ballot_sync(0xffffffffu, x < inc);
     if (past == 0) {
       x -= __shfl_sync(0xffffffffu, inc, 31);
@@ -267,7 +268,7 @@ __device__ __forceinline__ LatCursor walk_to(const KvAttnParams& p, int n0, int6
 // GROUP: CTAs that share a part of the line; 0: index lists.
 template <int GROUP, bool BF16>
 __global__ void __launch_bounds__(THREADS, 1)
-    latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ LatParams lp) {  // map: of Q, for lists
+    latent_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ LatParams lp) {  // map: of Q
   constexpr bool LISTS = GROUP == 0;
   constexpr int RT = NR * (LISTS ? 1 : GROUP);
   const KvAttnParams& p = lp.a;
@@ -296,32 +297,41 @@ __global__ void __launch_bounds__(THREADS, 1)
   // ---------------------------------------------------------------- the CTA's part of the line
   int64_t total = 0, begin = 0, end = 0;
   int parts = 1, per = 0;
+  int64_t mine = 0, upto = 0;  // positions of my requests, and up to their end
   const int part = LISTS ? 0 : blockIdx.x / imax(GROUP, 1), sub = LISTS ? 0 : blockIdx.x % imax(GROUP, 1);
+  KvReq last{};
   if constexpr (!LISTS) {
-    per = (p.N + kWarps - 1) / kWarps;
-    const int64_t w = requests_work<RT>(p, imin(p.N, warp * per), imin(p.N, (warp + 1) * per));
-    if (lane == 0) sh.work[warp] = w;
+    per = (p.N + THREADS - 1) / THREADS;
+    mine = thread_work<RT>(p, per, &last);
+    upto = lanes_scan(mine);
+    if (lane == 31) sh.work[warp] = upto;
   }
   __syncthreads();
   if (!aligned) return;
   if constexpr (!LISTS) {
+    int64_t before = 0;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) total += sh.work[i];
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t w = sh.work[i];
+      if (i < warp) before += w;
+      total += w;
+    }
     if (total == 0) return;
+    upto += before;
     const int64_t want = (total + kLatMinWork - 1) / kLatMinWork;
     const int most = gridDim.x / GROUP;
     parts = want < most ? static_cast<int>(want) : most;
     if (part >= parts) return;
     begin = kv_part_begin(total, part, parts), end = kv_part_begin(total, part + 1, parts);
+    // the warp whose requests hold the first position looks it up
+    const uint32_t here = __ballot_sync(0xffffffffu, begin >= upto - mine && begin < upto);
+    if (here != 0) {
+      const int src = __ffs(here) - 1;
+      const LatCursor c = find<RT>(p, (threadIdx.x - lane + src) * per, per, from_lane(last, src), begin - __shfl_sync(0xffffffffu, upto - mine, src));
+      if (lane == 0) sh.cursor = c;
+    }
   }
 
-  LatCursor cur{};
-  if (!LISTS && warp == 14) {  // (while the others set up)
-    int w0 = 0;
-    int64_t x = begin;
-    while (x >= sh.work[w0]) x -= sh.work[w0++];
-    cur = walk_to<RT>(p, w0 * per, x);
-  }
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
     mbar_init(&bars[Q_FULL], 1);
@@ -400,7 +410,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!publish(uc, u) || !u.valid) break;
       }
     } else {
-      KvReq rq = kv_request(cur.n, p);
+      LatCursor cur = sh.cursor;
+      KvReq rq = cur.r;
       int64_t x = begin;
       for (uint32_t uc = 0;; ++uc) {
         LatUnit u{};
@@ -435,18 +446,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 12) {
     // ============================================================ Q
     uint32_t qc = 0;
-    bool ok = true;
+    bool ok = true, copied = false;
     for (uint32_t uc = 0; ok; ++uc) {
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
       if (u.valid == 2 || u.j1 <= u.j0) continue;
       if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
       ++qc;
-      if constexpr (LISTS) {
-        // 64 heads of the token (those past its group are not used)
+      if (LISTS || p.q == nullptr) {
+        // lists: 64 heads of the token; else 64 rows of [T * H, 576].  (Those past the
+        // unit's may be anything: they are columns of the products of their own.)
         if (lane == 0) mbar_arrive_expect_tx(&bars[Q_FULL], TILE);
         __syncwarp();
-        if (lane < NSLAB) tma_load_4d(sm + OFF_Q + lane * SLAB, &map, &bars[Q_FULL], lane * 64, u.row0, u.a, u.n);
+        if (lane < NSLAB)
+          tma_load_4d(sm + OFF_Q + lane * SLAB, &map, &bars[Q_FULL], lane * 64, LISTS ? u.row0 : u.a * p.G + u.row0,
+                      LISTS ? u.a : 0, LISTS ? u.n : 0);
+        copied = true;
       } else {
         const int r = lane >> 3, c = lane & 7;  // four rows at once, 128 bytes each
 #pragma unroll 2
@@ -465,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&bars[Q_FULL]);
       }
     }
-    if (LISTS && lane == 0 && qc >= 1) mbar_drain(&bars[Q_FULL], (qc - 1) & 1);  // a copy in flight lands before the CTA exits
+    if (copied && lane == 0) mbar_drain(&bars[Q_FULL], (qc - 1) & 1);  // a copy in flight lands before the CTA exits
     __syncwarp();
   } else if (warp == 13) {
     // ============================================================ scores
@@ -806,11 +821,11 @@ cudaError_t launch_t(const LatParams& p, const CUtensorMap& map, int grid, cudaS
 
 }  // namespace
 
-cudaError_t launch_latent_cache(const LatParams& p, bool bf16, int group, int sms, cudaStream_t st) {
-  const CUtensorMap none{};
+cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& q, bool bf16, int group, int sms,
+                                cudaStream_t st) {
   const int grid = imin(sms, kLatMaxCtas) / group * group;
-  if (group == 1) return bf16 ? launch_t<1, true>(p, none, grid, st) : launch_t<1, false>(p, none, grid, st);
-  return bf16 ? launch_t<2, true>(p, none, grid, st) : launch_t<2, false>(p, none, grid, st);
+  if (group == 1) return bf16 ? launch_t<1, true>(p, q, grid, st) : launch_t<1, false>(p, q, grid, st);
+  return bf16 ? launch_t<2, true>(p, q, grid, st) : launch_t<2, false>(p, q, grid, st);
 }
 
 cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st) {

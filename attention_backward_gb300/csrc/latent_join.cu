@@ -4,10 +4,10 @@
 //
 // Entry w of ``desc`` (first token of the request, first row of the unit in the
 // request, rows, first part) names the unit that CTA w finished and did not begin; its
-// parts are d.w to w / group in order, w = -1 where there is none.  Each row of such
-// a unit is an item; a warp takes one, or, where there are warps to spare, 2 to 16 of
-// a block take fixed shares of its parts.  Latency-bound for few requests, by L2
-// for many.
+// parts are d.w to w / group in order, w = -1 where there is none.  Each half of a row
+// of such a unit is an item; a warp takes one, or, where there are warps to spare, 2 to
+// 16 of a block take fixed shares of its parts.  Latency-bound: four parts are in
+// flight, the first while the weights are made.
 #include "cvt.cuh"
 #include "kv_launch.h"
 #include "latent.h"
@@ -17,15 +17,16 @@ namespace ab {
 
 namespace {
 
-constexpr int WARPS = 16, ND = kLatDim / 32;
-static_assert(kLatMaxCtas <= WARPS * 32, "an entry a thread");
+constexpr int WARPS = 16, HALF = kLatDim / 2, ND = HALF / 32, PF = 4;  // columns of an item and of a lane, parts in flight
+constexpr int LISTERS = (kLatMaxCtas + 31) / 32;  // warps that hold entries, one a thread
+static_assert(LISTERS <= WARPS, "an entry a thread");
 
 template <bool BF16>
 __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid_constant__ LatParams lp, int group, int ctas) {
   const KvAttnParams& p = lp.a;
   __shared__ int4 list[kLatMaxCtas];
-  __shared__ int count;
-  __shared__ float s_o[WARPS][kLatDim];
+  __shared__ int counts[WARPS];
+  __shared__ float s_o[WARPS][HALF];
   __shared__ float2 s_ml[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
@@ -35,30 +36,30 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
     if (tid == 0) *p.err = kErrNone;
     if (__syncthreads_or(err != kErrNone) && err != kErrNone) *p.err = err;
   }
-  if (tid < 32) {
-    int n = 0;
-    for (int i = 0; i < ctas; i += 32) {
-      const int w = i + lane;
-      int4 d = make_int4(0, 0, 0, -1);
-      if (w < ctas) d = p.desc[w];
-      const uint32_t m = __ballot_sync(0xffffffffu, d.w >= 0);
-      // parts in the upper half of z, this CTA's place in its group in the upper half of w
-      if (d.w >= 0)
-        list[n + __popc(m & ((1u << lane) - 1u))] = make_int4(d.x, d.y, d.z | (w / group - d.w + 1) << 16, d.w | (w % group) << 16);
-      n += __popc(m);
-    }
-    if (lane == 0) count = n;
-  }
+  int4 d = make_int4(0, 0, 0, -1);
+  if (tid < ctas) d = p.desc[tid];
+  const uint32_t held = __ballot_sync(0xffffffffu, d.w >= 0);
+  if (lane == 0) counts[warp] = __popc(held);
   __syncthreads();
-  const int items = count * kLatRows;
+  int count = 0, first = 0;
+#pragma unroll
+  for (int i = 0; i < LISTERS; ++i) {
+    if (i < warp) first += counts[i];
+    count += counts[i];
+  }
+  // parts in the upper half of z, this CTA's place in its group in the upper half of w
+  if (d.w >= 0)
+    list[first + __popc(held & ((1u << lane) - 1u))] = make_int4(d.x, d.y, d.z | (tid / group - d.w + 1) << 16, d.w | (tid % group) << 16);
+  __syncthreads();
+  const int items = count * kLatRows * 2;
   int ls = 0;  // log2 of the warps an item
   while ((1 << ls) < WARPS && items << (ls + 1) <= static_cast<int>(gridDim.x) * WARPS) ++ls;
   const int shares = 1 << ls, per_block = WARPS >> ls, share = warp & (shares - 1);
   for (int t0 = blockIdx.x * per_block; t0 < items; t0 += gridDim.x * per_block) {
     const int item = t0 + (warp >> ls);
     int4 u = make_int4(0, 0, 0, 0);
-    if (item < items) u = list[item / kLatRows];
-    const int row = item % kLatRows, live = u.z & 0xffff, parts = u.z >> 16, g0 = u.w & 0xffff, sub = u.w >> 16;
+    if (item < items) u = list[item / (2 * kLatRows)];
+    const int row = item / 2 % kLatRows, half = item % 2, live = u.z & 0xffff, parts = u.z >> 16, g0 = u.w & 0xffff, sub = u.w >> 16;
     const bool on = item < items && row < live;
     auto slot_of = [&](int i) { return 2 * ((g0 + i) * group + sub) + (i == 0 ? 1 : 0); };
     float m = -INFINITY, l = 0.f, acc[ND];
@@ -70,6 +71,17 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
         const int n = imin(32, i1 - i0);
         float2 v = make_float2(0.f, 0.f);
         if (lane < n) v = p.part_ml[static_cast<int64_t>(slot_of(i0 + lane)) * kLatRows + row];
+        float4 x[PF][ND / 4];
+        auto load = [&](int i) {  // parts i .. i + PF - 1
+#pragma unroll
+          for (int k = 0; k < PF; ++k) {
+            const float4* const src = reinterpret_cast<const float4*>(
+                p.part_o + (static_cast<int64_t>(slot_of(i0 + imin(i + k, n - 1))) * kLatRows + row) * kLatDim + half * HALF);
+#pragma unroll
+            for (int e = 0; e < ND / 4; ++e) x[k][e] = src[e * 32 + lane];
+          }
+        };
+        load(0);  // (in flight while the weights are made)
         float mx = v.y == 0.f ? -INFINITY : v.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -82,17 +94,10 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
         l = l * g + sum;
 #pragma unroll
         for (int i = 0; i < ND; ++i) acc[i] *= g;
-        for (int i = 0; i < n; i += 2) {
-          float4 x[2][ND / 4];
+        for (int i = 0; i < n; i += PF) {
+          if (i > 0) load(i);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float4* const src = reinterpret_cast<const float4*>(
-                p.part_o + (static_cast<int64_t>(slot_of(i0 + imin(i + k, n - 1))) * kLatRows + row) * kLatDim);
-#pragma unroll
-            for (int e = 0; e < ND / 4; ++e) x[k][e] = src[e * 32 + lane];
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < PF; ++k) {
             const float f = __shfl_sync(0xffffffffu, w, (i + k) & 31);
             if (i + k < n && f != 0.f) {  // (a part that saw no key of the row says nothing)
 #pragma unroll
@@ -125,14 +130,14 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
       const int64_t t = static_cast<int64_t>(u.x) + at / p.G;
       const int head = at % p.G;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint8_t* const out = p.o + 2 * (t * p.so_s + head * p.so_h);
+      uint8_t* const out = p.o + 2 * (t * p.so_s + head * p.so_h + half * HALF);
 #pragma unroll
       for (int e = 0; e < ND / 4; ++e) {
         const uint2 w = make_uint2(pack2<BF16>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
                                    pack2<BF16>(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
         *reinterpret_cast<uint2*>(out + 8 * (e * 32 + lane)) = w;
       }
-      if (lane == 0)
+      if (lane == 0 && half == 0)
         p.lse[head * p.sl_h + t * p.sl_s] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
     if (shares > 1) __syncthreads();
