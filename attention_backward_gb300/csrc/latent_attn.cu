@@ -43,6 +43,7 @@
 #include "kv_launch.h"
 #include "kv_sched.cuh"
 #include "latent.h"
+#include "latent_issue.cuh"
 #include "sm103.cuh"
 
 namespace ab {
@@ -129,20 +130,6 @@ __device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t* r) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-
-// mma_ss_w with the lane elected beforehand (``elected`` not 0 in one lane).
-__device__ __forceinline__ uint32_t elect_lane() {
-  uint32_t x;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(x));
-  return x;
-}
-__device__ __forceinline__ void mma_ss_e(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate, uint32_t elected) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected));
 }
 
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, uint32_t bytes) {  // the rest reads zeros

@@ -17,8 +17,8 @@
 // to none: those rows of V are zeroed in shared memory before the slab is published
 // (a zero P times a NaN would be NaN; of K they only make scores that are masked).
 //
-// Warp roles (12 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA producer, 9
-// MMA issue, 10-11 idle.  Every wait is bounded.
+// Warp roles (12 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA producer, 9 and
+// 10 MMA issue of a tile each, 11 idle.  Every wait is bounded.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,6 +29,7 @@
 #include "cvt.cuh"
 #include "kv_launch.h"
 #include "latent.h"
+#include "latent_issue.cuh"
 #include "sm103.cuh"
 
 namespace ab {
@@ -63,18 +64,18 @@ constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + D;
 
 enum FwdBar : int {
   Q_FULL = 0,
-  Q_EMPTY,            // every S MMA of the unit has completed: the Q tiles may be reloaded
+  Q_EMPTY,            // every S MMA of both tiles of the unit has completed: the Q tiles may be reloaded
   FULL0,              // ring slabs
-  EMPTY0 = FULL0 + RING,
+  EMPTY0 = FULL0 + RING,  // both tiles' products of it have completed
   S_FULL0 = EMPTY0 + RING,    // per tile
   P_READY0 = S_FULL0 + 2,     // per tile: 4 softmax warps stored P
   O_DONE0 = P_READY0 + 2,     // per tile: the tile's P V MMAs issued so far completed
   O_FREE0 = O_DONE0 + 2,      // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,   // 2 ring slots: the producer published a unit index
-  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 ring slots: the MMA warp and the 8 softmax warps read it
+  UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 ring slots: the 2 issuing and the 8 softmax warps read it
   TAIL = UNIT_EMPTY0 + 2,
-  DRAIN,
-  NUM_FWD_BARS
+  DRAIN0,  // of the issuing warps
+  NUM_FWD_BARS = DRAIN0 + 2
 };
 static_assert(NUM_FWD_BARS <= 40, "barrier storage");
 
@@ -83,6 +84,7 @@ static_assert(NUM_FWD_BARS <= 40, "barrier storage");
 // range [lo, hi) of 128-key blocks.
 struct FwdUnit {
   int valid, b, h, seq_start, qlen, klen, off, q0;
+  int tiles;  // 2, or 1: the second is another unit's
   int lo[2], hi[2];  // lo == hi: the tile sees no key; q0 + 128 w >= qlen: the tile is absent
 };
 
@@ -101,19 +103,43 @@ __device__ __forceinline__ void key_block_range(int q0, int qlen, int klen, int 
   *hi = static_cast<int>((ke + BK - 1) / BK);
 }
 
+// Pairs of query tiles of the launch.
+__device__ __forceinline__ int count_pairs(const LatFwdParams& p) {
+  if (p.cu_seqlens == nullptr) return (p.S + 2 * BQ - 1) / (2 * BQ) * p.B * p.H;
+  int n = 0;
+  for (int i = 0; i < p.num_seqs; ++i) {
+    const int a = clamp_pos(p.cu_seqlens[i], p.S), e = clamp_pos(p.cu_seqlens[i + 1], p.S);
+    n += e > a ? (e - a + 2 * BQ - 1) / (2 * BQ) : 0;
+  }
+  return n * p.H;
+}
+
+// The first pair that is cut into units of one tile: those of a last round that leaves at
+// least half of the CTAs without a pair (a tile by itself takes about 0.65 of a pair's
+// time).  2048 queries on 8192 keys, 64 heads: 512 pairs on 152 CTAs, 516 us, SINGLES.
+__device__ __forceinline__ int first_single(const LatFwdParams& p) {
+  const int n = count_pairs(p), last = n % static_cast<int>(gridDim.x);
+  return 2 * last <= static_cast<int>(gridDim.x) ? n - last : n;
+}
+
 // Unit u of the launch, longest first under a causal mask (the last query
 // tiles of a row see the most keys): dense rows go through the tile pairs
 // from the last, each over all (batch, head) pairs; packed sequences one after
 // another, each the same way over its heads.
-__device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p) {
+__device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p, int singles) {
   FwdUnit t{};
   t.valid = 0;
   if (u < 0) return t;  // the end-of-work marker
+  int one = -1;  // the only tile of the unit
+  if (u >= singles) {
+    one = (u - singles) & 1;
+    u = singles + ((u - singles) >> 1);
+  }
   int pair = 0;
   if (p.cu_seqlens == nullptr) {
     const int np = (p.S + 2 * BQ - 1) / (2 * BQ);
     const int bh = p.B * p.H;
-    if (u < 0 || u >= np * bh) return t;
+    if (u >= np * bh) return t;
     pair = np - 1 - u / bh;
     t.b = (u % bh) / p.H;
     t.h = (u % bh) % p.H;
@@ -141,8 +167,9 @@ __device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p) {
     }
     if (!found) return t;
   }
-  t.q0 = pair * 2 * BQ;
-  for (int w = 0; w < 2; ++w)
+  t.q0 = (2 * pair + imax(one, 0)) * BQ;
+  t.tiles = one < 0 ? 2 : 1;
+  for (int w = 0; w < t.tiles; ++w)
     key_block_range(t.q0 + w * BQ, t.qlen, t.klen, t.off, p.causal, &t.lo[w], &t.hi[w]);
   t.valid = 1;
   return t;
@@ -186,6 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_MISC + 8);
   volatile int* ring = reinterpret_cast<volatile int*>(sm + OFF_MISC + 16);  // 2 unit indices
+  int* const turn_taken = reinterpret_cast<int*>(sm + OFF_MISC + 32);  // of the issuing warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if ((smem_u32(sm) & 1023u) != 0) {  // the swizzled tiles need an aligned base
@@ -196,11 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    *turn_taken = 0;
     mbar_init(&bars[Q_FULL], 1);
-    mbar_init(&bars[Q_EMPTY], 1);
+    mbar_init(&bars[Q_EMPTY], 2);
     for (int i = 0; i < RING; ++i) {
       mbar_init(&bars[FULL0 + i], 1);
-      mbar_init(&bars[EMPTY0 + i], 1);
+      mbar_init(&bars[EMPTY0 + i], 2);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars[S_FULL0 + w], 1);
@@ -210,10 +239,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[UNIT_FULL0 + i], 1);
-      mbar_init(&bars[UNIT_EMPTY0 + i], 9);
+      mbar_init(&bars[UNIT_EMPTY0 + i], 10);
+      mbar_init(&bars[DRAIN0 + i], 1);
     }
     mbar_init(&bars[TAIL], 1);
-    mbar_init(&bars[DRAIN], 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -238,6 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     }
   };
 
+  const int singles = first_single(p);
   // the uc-th unit of this CTA (consumers): waits for the producer's draw,
   // hands the slot back, decodes; invalid once the draws are exhausted
   auto next_unit = [&](uint32_t uc, bool* okp) -> FwdUnit {
@@ -248,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const int t = ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[UNIT_EMPTY0 + slot]);
-    return decode_unit(t, p);
+    return decode_unit(t, p, singles);
   };
 
   if (warp >= 8) {
@@ -265,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         int t = 0;
         if (lane == 0) t = atomicAdd(p.unit_counter, 1);
         t = __shfl_sync(0xffffffffu, t, 0);
-        const FwdUnit u = decode_unit(t, p);
+        const FwdUnit u = decode_unit(t, p, singles);
         if (lane == 0) {
           ring[slot] = u.valid ? t : -1;
           mbar_arrive(&bars[UNIT_FULL0 + slot]);
@@ -323,110 +353,128 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
           mbar_drain(&bars[FULL0 + i % RING], (i / RING) & 1);
       }
       __syncwarp();
-    } else if (warp == 9) {
-      // ============================================================ MMA issuer
+    } else if (warp < 11) {
+      // ============================================================ MMA issue of tile w
+      // A warp a tile: neither waits on the other's softmax, and the tensor core takes
+      // what is there.  (One warp for both, unrolled, spent 4700 cycles a block on issue.)
+      const int w = warp - 9;
       constexpr uint32_t IDESC_S = idesc_f16(BF16, 128, BK, false, false);
-      constexpr uint32_t IDESC_PV = idesc_f16(BF16, 128, 64, false, true), IDESC_PV2 = idesc_f16(BF16, 128, D, false, true);
-      const uint32_t sbase = smem_u32(sm);
-      const uint64_t q_kmaj = sdesc_sw128(sbase + OFF_Q, 16, 1024);
-      const uint64_t r_kmaj = sdesc_sw128(sbase + OFF_R, 16, 1024);
-      const uint64_t r_mn = sdesc_sw128(sbase + OFF_R, SLAB, 1024);
-      uint32_t qc = 0, rc = 0, npv0 = 0, npv1 = 0, oc0 = 0, oc1 = 0;
+      constexpr uint32_t IDESC_PV = idesc_f16(BF16, 128, D, false, true), IDESC_PV1 = idesc_f16(BF16, 128, 64, false, true);
+      const uint64_t q_kmaj = sdesc_sw128(smem_u32(sm) + OFF_Q, 16, 1024) + sdesc_step(QTILE) * w;
+      const uint64_t r_kmaj = sdesc_sw128(smem_u32(sm) + OFF_R, 16, 1024);
+      const uint64_t r_mn = sdesc_sw128(smem_u32(sm) + OFF_R, SLAB, 1024);
+      const uint32_t ts = tmem + T_S0 + (T_S1 - T_S0) * w, to = tmem + T_O0 + (T_O1 - T_O0) * w;
+      const uint32_t one = elect_lane();
+      uint32_t qc = 0, rc = 0, npv = 0, oc = 0;  // units, ring slabs, blocks and units of my tile so far
       bool ok = true;
+      auto wait_slab = [&](uint32_t i) { return mbar_wait_warp(&bars[FULL0 + i % RING], (i / RING) & 1, wc, kErrWaitKV); };
+      // slabs [i, i + n): waited for, and handed back without use
+      auto skip = [&](uint32_t i, int n) -> bool {
+        for (int s = 0; s < n; ++s, ++i) {
+          if (!wait_slab(i)) return false;
+          if (lane == 0) mbar_arrive(&bars[EMPTY0 + i % RING]);
+        }
+        return true;
+      };
+      auto wait_k = [&](uint32_t i) { return wait_slab(i) && wait_slab(i + 1) && wait_slab(i + 2); };
+      // S of the block whose K starts at slab i
+      auto scores = [&](uint32_t i) {
+#pragma unroll 1
+        for (int s = 0; s < KSLABS; ++s, ++i) {
+          const uint64_t q = q_kmaj + sdesc_step(SLAB) * s, k = r_kmaj + sdesc_step(SLAB) * (i % RING);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_ss_e(ts, q + sdesc_step(kk * 32), k + sdesc_step(kk * 32), IDESC_S, s + kk > 0, one);
+          mma_commit_w(&bars[EMPTY0 + i % RING]);
+        }
+        mma_commit_w(&bars[S_FULL0 + w]);
+      };
+      // The tiles take turns at S, which is issued in one go: one's softmax then runs while
+      // the other's products do.  (Side by side, both tiles' S end at the same time, and
+      // both softmaxes run with the tensor core idle.)  Bounded as mbar_wait is.
+      auto turn = [&]() -> bool {
+        bool got = false;
+        uint64_t since = 0;
+        for (uint32_t i = 1; !got; ++i) {
+          if (lane == 0) got = atomicCAS(turn_taken, 0, 1) == 0;
+          got = __any_sync(0xffffffffu, got);
+          if (!got && (i & 255) == 0) {
+            const uint64_t now = global_ns();
+            if (i == 256) since = now;
+            const bool late = now - since > wc.timeout_ns;
+            if (late) raise_error(wc, kErrWaitTile);
+            if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+          }
+        }
+        tc_fence_after();
+        return true;
+      };
+      auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) atomicExch(turn_taken, 0);
+      };
       for (uint32_t uc = 0; ok; ++uc) {
         const FwdUnit u = next_unit(uc, &ok);
         if (!ok || !u.valid) break;
         const UnitSpan sp = unit_span(u);
         if (sp.J1 <= sp.J0) continue;
-        const int J0 = sp.J0, J1 = sp.J1;
-        const uint32_t rc0 = rc;  // slab counter at the unit's first block
-        auto in = [&](int w, int j) { return sp.has[w] && u.lo[w] <= j && j < u.hi[w]; };
-        auto slab_of = [&](int j, int s) { return rc0 + (j - J0) * BSLABS + s; };
-        auto wait_slabs = [&](int j, int s0, int s1) -> bool {
-          for (int s = s0; s < s1; ++s) {
-            const uint32_t i = slab_of(j, s);
-            if (!mbar_wait_warp(&bars[FULL0 + i % RING], (i / RING) & 1, wc, kErrWaitKV)) return false;
-          }
-          tc_fence_after();
-          return true;
-        };
-        // the slabs' readers have all been issued
-        auto free_slabs = [&](int j, int s0, int s1) {
-          for (int s = s0; s < s1; ++s) mma_commit_w(&bars[EMPTY0 + slab_of(j, s) % RING]);
-        };
-        auto issue_s = [&](int w, int j) {
-          const uint64_t qo = sdesc_step(w * QTILE);
-#pragma unroll
-          for (int s = 0; s < KSLABS; ++s) {
-            const uint64_t ko = sdesc_step((slab_of(j, s) % RING) * SLAB);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss_w(tmem + (w ? T_S1 : T_S0), q_kmaj + qo + sdesc_step(s * SLAB + kk * 32),
-                       r_kmaj + ko + sdesc_step(kk * 32), IDESC_S, s > 0 || kk > 0);
-          }
-          mma_commit_w(&bars[S_FULL0 + w]);
-        };
-        auto issue_pv = [&](int w, int j) -> bool {
-          uint32_t& npv = w ? npv1 : npv0;
-          if (!mbar_wait_warp(&bars[P_READY0 + w], npv & 1, wc, kErrWaitP)) return false;
-          if (j == u.lo[w]) {
-            // the tile's O accumulator: its softmax warps have read the previous unit's O
-            const uint32_t oc = w ? oc1 : oc0;
-            if (oc >= 1 && !mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wc, kErrWaitDQEmpty)) return false;
-          }
-          tc_fence_after();
-          const uint32_t ts = tmem + (w ? T_S1 : T_S0), to = tmem + (w ? T_O1 : T_O0);
-          const uint32_t s0 = slab_of(j, KSLABS) % RING, s1 = slab_of(j, KSLABS + 1) % RING;
-          if (s1 == s0 + 1) {  // side by side: one product of 128 columns
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              mma_ts_w(to, ts + kk * 8, r_mn + sdesc_step(s0 * SLAB + kk * 2048), IDESC_PV2, j > u.lo[w] || kk > 0);
-          } else {
-#pragma unroll
-            for (int v = 0; v < VSLABS; ++v)
+        const int J0 = sp.J0, J1 = sp.J1, lo = w ? u.lo[1] : u.lo[0], hi = w ? u.hi[1] : u.hi[0];
+        auto in = [&](int j) { return lo <= j && j < hi; };
+        if (!(ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
+        ++qc;
+        // a tile's O accumulator: its softmax warps have read the previous unit's O
+        if (lo < hi && oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
+        if (in(J0)) {
+          if (!(ok = wait_k(rc) && turn())) break;
+          scores(rc);
+          done();
+        } else if (!(ok = skip(rc, KSLABS))) {
+          break;
+        }
+        for (int j = J0; j < J1; ++j, rc += BSLABS) {
+          const uint32_t v = rc + KSLABS;
+          const bool more = j + 1 < J1 && in(j + 1);
+          if (in(j)) {
+            if (!(ok = mbar_wait_warp(&bars[P_READY0 + w], npv & 1, wc, kErrWaitP) && wait_slab(v) && wait_slab(v + 1))) break;
+            ++npv;
+            tc_fence_after();
+            const uint32_t s0 = v % RING, s1 = (v + 1) % RING;
+            const uint32_t acc = j > lo;
+            if (s1 == s0 + 1) {  // side by side: products of 128 columns
+              const uint64_t b = r_mn + sdesc_step(SLAB) * s0;
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)
-                mma_ts_w(to + 64 * v, ts + kk * 8, r_mn + sdesc_step((v ? s1 : s0) * SLAB + kk * 2048), IDESC_PV,
-                         j > u.lo[w] || kk > 0);
+                mma_ts_e(to, ts + kk * 8, b + sdesc_step(kk * 2048), IDESC_PV, kk > 0 ? 1u : acc, one);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                mma_ts_e(to, ts + kk * 8, r_mn + sdesc_step(SLAB) * s0 + sdesc_step(2048) * kk, IDESC_PV1, kk > 0 ? 1u : acc, one);
+                mma_ts_e(to + 64, ts + kk * 8, r_mn + sdesc_step(SLAB) * s1 + sdesc_step(2048) * kk, IDESC_PV1, kk > 0 ? 1u : acc, one);
+              }
+            }
+            mma_commit_w(&bars[EMPTY0 + s0]);
+            mma_commit_w(&bars[EMPTY0 + s1]);
+            mma_commit_w(&bars[O_DONE0 + w]);
+          } else if (!(ok = skip(v, VSLABS))) {
+            break;
           }
-          mma_commit_w(&bars[O_DONE0 + w]);
-          ++npv;
-          return true;
-        };
-        ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull) && wait_slabs(J0, 0, KSLABS);
-        ++qc;
-        if (ok) {
-          if (in(0, J0)) issue_s(0, J0);
-          if (in(1, J0)) issue_s(1, J0);
-          free_slabs(J0, 0, KSLABS);
-        }
-        for (int j = J0; j < J1 && ok; ++j) {
-          if (!(ok = wait_slabs(j, KSLABS, BSLABS))) break;
-          if (in(0, j) && !(ok = issue_pv(0, j))) break;
-          const bool next = j + 1 < J1;
-          if (next) {
-            if (!(ok = wait_slabs(j + 1, 0, KSLABS))) break;
-            if (in(0, j + 1)) issue_s(0, j + 1);
-          }
-          if (in(1, j) && !(ok = issue_pv(1, j))) break;
-          free_slabs(j, KSLABS, BSLABS);
-          if (next) {
-            if (in(1, j + 1)) issue_s(1, j + 1);
-            free_slabs(j + 1, 0, KSLABS);
+          if (more) {
+            if (!(ok = wait_k(rc + BSLABS) && turn())) break;
+            scores(rc + BSLABS);
+            done();
+          } else if (j + 1 < J1 && !(ok = skip(rc + BSLABS, KSLABS))) {
+            break;
           }
         }
         if (!ok) break;
         mma_commit_w(&bars[Q_EMPTY]);  // every S MMA of the unit issued
-        rc += (J1 - J0) * BSLABS;
-        oc0 += sp.has[0] ? 1u : 0u;
-        oc1 += sp.has[1] ? 1u : 0u;
+        oc += lo < hi ? 1u : 0u;
       }
       // every MMA issued by this warp completes before TMEM is released
-      mma_commit_w(&bars[DRAIN]);
-      if (lane == 0) mbar_drain(&bars[DRAIN], 0);
+      mma_commit_w(&bars[DRAIN0 + w]);
+      if (lane == 0) mbar_drain(&bars[DRAIN0 + w], 0);
       __syncwarp();
     }
-    // warps 10-11: nothing to do
+    // warp 11: nothing to do
     finish();
     return;
   }
@@ -444,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const FwdUnit u = next_unit(uc, &ok);
     if (!ok || !u.valid) break;
     const int qt0 = u.q0 + w * BQ;  // first (sequence-local) query of the tile
-    if (qt0 >= u.qlen) continue;    // the tile is past the end of its sequence
+    if (w >= u.tiles || qt0 >= u.qlen) continue;  // another unit's tile, or past the end of its sequence
     const int lo_w = w ? u.lo[1] : u.lo[0], hi_w = w ? u.hi[1] : u.hi[0];
     const int q = qt0 + row;
     const uint32_t c0 = c;
