@@ -33,12 +33,12 @@ from ._kv_cache import DT, _device, _on, _run, _strides, _table, _vec
 ROW, LAT, ROT = 576, 512, 64  # a latent row, its latent vector, its rotated columns
 NOPE, DV = 128, 128           # the expanded form's own key columns and values a head
 
-_F32, _I32 = torch.float32, torch.int32
+_F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
 
 
-class _RopeTensor(ctypes.Structure):  # attn_rope_tensor_t
-    _fields_ = [("x", c_vp), ("sx", Strides), ("y", c_vp), ("sy", Strides), ("H", c_i64), ("D", c_i64),
-                ("start", c_i64)]
+class _RopeTensor(ctypes.Structure):  # attn_rope_tensor_t, its strides spelled out
+    _fields_ = [("x", c_vp), ("sx_b", c_i64), ("sx_s", c_i64), ("sx_h", c_i64), ("y", c_vp), ("sy_b", c_i64),
+                ("sy_s", c_i64), ("sy_h", c_i64), ("H", c_i64), ("D", c_i64), ("start", c_i64)]
 
 
 class _Rows(ctypes.Structure):  # attn_latent_cache_t
@@ -126,10 +126,24 @@ def _steps(table, device, R=None):
     if not isinstance(table, RopeTable):
         raise AttnBwdError("table must be a RopeTable (rope_table)")
     t = table.steps
-    _on(device, table=t)
-    if t.dtype != torch.int64 or t.dim() != 1 or not t.is_contiguous() or (R is not None and t.shape[0] != R // 2):
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        _on(device, table=t)
+    if t.dtype != _I64 or t.dim() != 1 or not t.is_contiguous() or (R is not None and t.shape[0] != R // 2):
         raise AttnBwdError("the table's steps must be a contiguous int64 vector" + ("" if R is None else f" of {R // 2}"))
     return t.data_ptr(), t.shape[0] * 2
+
+
+def _rope_tensor(name, x, first, y):
+    """The C tensor of x turned into y (None: a new one), and y."""
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _on(x.device, **{name: y})
+        if y.dtype != x.dtype:
+            raise AttnBwdError(f"{name} must have its input's dtype")
+    sx, shape = _strides(name, x), x.shape
+    sy = sx if y is x or y.stride() == x.stride() and y.shape == shape else _strides(name, y, shape)
+    return _RopeTensor(x.data_ptr(), *sx, y.data_ptr(), *sy, shape[2], shape[3], first), y
 
 
 def rope(q, positions, table: RopeTable, k=None, interleaved: bool = False, start: int = 0, k_start: int = 0,
@@ -140,41 +154,35 @@ def rope(q, positions, table: RopeTable, k=None, interleaved: bool = False, star
     call's results it returns those of its inputs.  ``out`` (q', k') writes into
     tensors of the same shapes; the inputs themselves work in place."""
     device = _device("q", q)
-    _on(device, positions=positions)
+    if not isinstance(positions, torch.Tensor) or positions.device != device:
+        _on(device, positions=positions)
     dt = _dt("q", q)
     steps, R = _steps(table, device)
-    sq = _strides("q", q)
+    if q.dim() != 4:
+        raise AttnBwdError("q must be a 4-D tensor")
     B, S = q.shape[:2]
-    sk = None
     if k is not None:
         _on(device, k=k)
-        sk = _strides("k", k)
-        if k.dtype != q.dtype or k.shape[:2] != q.shape[:2]:
+        if k.dtype != q.dtype or k.dim() != 4 or k.shape[:2] != q.shape[:2]:
             raise AttnBwdError("k must have q's dtype, batch and length")
-    if positions.dtype != _I32 or positions.shape not in ((S,), (B, S)) or (S > 1 and positions.stride(-1) != 1):
+    pos_b = 0
+    if positions.dim() == 2:
+        pos_b = positions.stride(0) if B > 1 else 0
+    if (positions.dtype != _I32 or positions.shape not in ((S,), (B, S)) or (S > 1 and positions.stride(-1) != 1) or
+            pos_b < 0):
         raise AttnBwdError(f"positions must be int32 [{S}] or [{B}, {S}] with contiguous rows")
-    pos_b = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    if pos_b < 0:
-        raise AttnBwdError("positions must have rows in ascending order")
+    if out is not None and (len(out) != 2 or out[0] is None or (k is None) != (out[1] is None)):
+        raise AttnBwdError("out must be (q, k), k None where none is given")
 
     def body(ptr):
-        def one(name, x, sx, first, y):
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=device)
-            else:
-                _on(device, **{name: y})
-                if y.dtype != x.dtype:
-                    raise AttnBwdError(f"{name} must have its input's dtype")
-            return y, _RopeTensor(x.data_ptr(), Strides(*sx), y.data_ptr(), Strides(*_strides(name, y, x.shape)),
-                                  x.shape[2], x.shape[3], first)
-
-        if out is not None and (len(out) != 2 or (out[0] is None) or (k is None) != (out[1] is None)):
-            raise AttnBwdError("out must be (q, k), k None where none is given")
-        yq, tq = one("out q", q, sq, start, None if out is None else out[0])
-        yk, tk = (None, None) if k is None else one("out k", k, sk, k_start, None if out is None else out[1])
+        tq, yq = _rope_tensor("q", q, start, None if out is None else out[0])
+        tk = yk = None
+        if k is not None:
+            tk, yk = _rope_tensor("k", k, k_start, None if out is None else out[1])
+            tk = ctypes.byref(tk)
         _binding._status(_binding.library().attn_rope(
-            ctypes.byref(tq), None if tk is None else ctypes.byref(tk), B, S, dt, positions.data_ptr(), pos_b, steps, R,
-            table.scale, 1 if interleaved else 0, 1 if inverse else 0, ptr), "attn_rope")
+            ctypes.byref(tq), tk, B, S, dt, positions.data_ptr(), pos_b, steps, R, table.scale,
+            1 if interleaved else 0, 1 if inverse else 0, ptr), "attn_rope")
         return yq, yk
 
     return _run(device, stream, body)
@@ -246,28 +254,42 @@ def latent_cache_workspace_size() -> int:
     return int(_binding.library().attn_fwd_latent_cache_workspace_size())
 
 
-def _outputs(out, o_shape, lse_shape, dtype, device):
-    """o, lse and their strides (lse: of [B, H, S])."""
+def _outputs(out, workspace, need, o_shape, dtype, device):
+    """o, lse [B, H, S], their strides, and address and bytes of the workspace.  A small
+    workspace of the call's own lies behind lse (an allocation is a microsecond or two
+    of a short call)."""
     B, S, H, D = o_shape
+    lse_shape, own = (B, H, S), workspace is None
     if out is None:
+        n = B * H * S
+        if own and need <= 4096:
+            at = -(-n // 64) * 64
+            lse = torch.empty(at + need // 4, dtype=_F32, device=device)
+            ws, nbytes = lse.data_ptr() + 4 * at, need
+            lse = lse.as_strided(lse_shape, (H * S, S, 1))
+            own = False
+        else:
+            lse = torch.empty(lse_shape, dtype=_F32, device=device)
         o = torch.empty(o_shape, dtype=dtype, device=device)
-        lse = torch.empty(lse_shape, dtype=_F32, device=device)
+        so, sl = Strides(S * H * D, H * D, D), Strides(H * S or 1, 1, S or 1)
     else:
         o, lse = out
         _on(device, o=o, lse=lse)
         if o.dtype != dtype or lse.dtype != _F32 or lse.shape != lse_shape:
             raise AttnBwdError(f"out must be o (of q's dtype, {list(o_shape)}) and lse (float32 {list(lse_shape)})")
-    lb, lh, ls = lse.stride()
-    return o, lse, Strides(*_strides("o", o, o_shape)), Strides(lb if B > 1 else 1, ls if S > 1 else 1, lh if H > 1 else 1)
-
-
-def _workspace(ws, need, device):
-    if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _on(device, workspace=ws)
-    if not ws.is_contiguous():
-        raise AttnBwdError("workspace must be contiguous")
-    return ws
+        lb, lh, ls = lse.stride()
+        so = Strides(*_strides("o", o, o_shape))
+        sl = Strides(lb if B > 1 else 1, ls if S > 1 else 1, lh if H > 1 else 1)
+    keep = None
+    if workspace is not None:
+        _on(device, workspace=workspace)
+        if not workspace.is_contiguous():
+            raise AttnBwdError("workspace must be contiguous")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif own:
+        keep = torch.empty(need, dtype=_U8, device=device)
+        ws, nbytes = keep.data_ptr(), need
+    return o, lse, so, sl, ws, nbytes, keep
 
 
 def forward_latent_cache(q, cache, block_table, cu_seqlens, kv_lens, sm_scale: float, causal: bool = True,
@@ -290,12 +312,11 @@ def forward_latent_cache(q, cache, block_table, cu_seqlens, kv_lens, sm_scale: f
     lib = _binding.library()
 
     def body(ptr):
-        o, lse, so, sl = _outputs(out, (1, T, H, LAT), (1, H, T), q.dtype, device)
-        ws = _workspace(workspace, lib.attn_fwd_latent_cache_workspace_size(), device)
+        o, lse, so, sl, ws, nbytes, keep = _outputs(out, workspace, lib.attn_fwd_latent_cache_workspace_size(),
+                                                    (1, T, H, LAT), q.dtype, device)
         _binding._status(lib.attn_fwd_latent_cache(
             q.data_ptr(), sq, T, H, dt, sm_scale, ctypes.byref(rows), table, stride, width, cu, lens, n,
-            1 if causal else 0, o.data_ptr(), so, lse.data_ptr(), sl, ws.data_ptr(), ws.numel() * ws.element_size(),
-            ptr), "attn_fwd_latent_cache")
+            1 if causal else 0, o.data_ptr(), so, lse.data_ptr(), sl, ws, nbytes, ptr), "attn_fwd_latent_cache")
         return o, lse
 
     return _run(device, stream, body)
@@ -323,12 +344,10 @@ def sparse_forward(q, kv, idx, sm_scale: Optional[float] = None, dv_dim: int = L
         sm_scale = D ** -0.5
 
     def body(ptr):
-        o, lse, so, sl = _outputs(out, (B, S, H, dv_dim), (B, H, S), q.dtype, device)
-        ws = _workspace(workspace, 256, device)
+        o, lse, so, sl, ws, nbytes, _ = _outputs(out, workspace, 256, (B, S, H, dv_dim), q.dtype, device)
         _binding._status(_binding.library().attn_fwd_sparse(
             q.data_ptr(), sq, kv.data_ptr(), skv, idx.data_ptr(), Strides(*idx.stride()[:3]), B, S, SKV, H, HKV, D,
-            dv_dim, idx.shape[3], dt, sm_scale, o.data_ptr(), so, lse.data_ptr(), sl, ws.data_ptr(),
-            ws.numel() * ws.element_size(), ptr), "attn_fwd_sparse")
+            dv_dim, idx.shape[3], dt, sm_scale, o.data_ptr(), so, lse.data_ptr(), sl, ws, nbytes, ptr), "attn_fwd_sparse")
         return o, lse
 
     return _run(device, stream, body)
@@ -361,12 +380,10 @@ def forward_latent(q, k_nope, k_rope, v, sm_scale: float, causal: bool = True, c
     mask = _binding._mask(causal, -1, cu_seqlens, S, Sk)
 
     def body(ptr):
-        o, lse, so, sl = _outputs(out, (B, S, H, DV), (B, H, S), q.dtype, device)
-        ws = _workspace(workspace, 256, device)
+        o, lse, so, sl, ws, nbytes, _ = _outputs(out, workspace, 256, (B, S, H, DV), q.dtype, device)
         _binding._status(_binding.library().attn_fwd_latent(
             q.data_ptr(), sq, k_nope.data_ptr(), sk, k_rope.data_ptr(), sr, v.data_ptr(), sv, B, S, H, dt, sm_scale,
-            ctypes.byref(mask), o.data_ptr(), so, lse.data_ptr(), sl, ws.data_ptr(), ws.numel() * ws.element_size(),
-            ptr), "attn_fwd_latent")
+            ctypes.byref(mask), o.data_ptr(), so, lse.data_ptr(), sl, ws, nbytes, ptr), "attn_fwd_latent")
         return o, lse
 
     return _run(device, stream, body)
