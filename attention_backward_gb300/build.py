@@ -1,4 +1,5 @@
-"""Builds the CUDA library ``_build/libattn_bwd.so`` for sm_103a with nvcc.
+"""Builds the CUDA library ``_build/libattn_bwd.so`` for sm_103a with nvcc, and
+``_build/libattn_torch.so``, torch operators over some of its entry points.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library with the CUDA runtime linked statically, so the library loads on a
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libattn_bwd.so")
+TORCH_LIB = os.path.join(BUILD, "libattn_torch.so")
+TORCH_SOURCE = "torch_latent.cpp"
 SOURCES = ["api.cu", "preprocess.cu", "dense_bwd.cu", "dense128_bwd.cu", "dense_fwd.cu", "sparse_bwd.cu", "noalloc.cu", "host_pipeline.cu",
            "kv_api.cu", "kv_cache.cu", "kv_decode.cu", "kv_prompt.cu", "kv_join.cu",
            "rope.cu", "latent_api.cu", "latent_write.cu", "latent_attn.cu", "latent_join.cu", "latent_fwd.cu"]
@@ -42,6 +45,18 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_flags(cc: str) -> tuple:
+    """Flags that compile and link against the torch of this interpreter."""
+    import torch
+
+    at = os.path.dirname(torch.__file__)
+    include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"), os.path.join(ROOT, "include")]
+    return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+             *(f"-I{i}" for i in include)],
+            [f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch"])
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -53,6 +68,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(obj, src):
             jobs.append([cc, *ARCH, *FLAGS, "-c", src, "-o", obj] + (["-Xptxas", "-v"] if verbose else []))
 
+    cxx = shutil.which("g++") or "g++"
+    compile_flags, link_flags = _torch_flags(cc)
+    torch_obj, torch_src = os.path.join(BUILD, "torch_latent.o"), os.path.join(CSRC, TORCH_SOURCE)
+    torch_stale = force or _stale(torch_obj, torch_src) or not os.path.exists(TORCH_LIB)
+    cuda_jobs = len(jobs)
+    if torch_stale:
+        jobs.append([cxx, *compile_flags, "-c", torch_src, "-o", torch_obj])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -62,8 +85,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
             if verbose or r.returncode:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
-    if force or jobs or not os.path.exists(LIB):
+                raise RuntimeError(f"compiler failed: {' '.join(cmd)}")
+    if force or cuda_jobs or not os.path.exists(LIB):
         tmp = LIB + ".tmp"
         cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -71,6 +94,14 @@ def build(verbose: bool = False, force: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    if torch_stale:
+        tmp = TORCH_LIB + ".tmp"
+        _, r = run([cxx, "-shared", "-o", tmp, torch_obj, f"-L{BUILD}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN",
+                    *link_flags])
+        if r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link failed")
+        os.replace(tmp, TORCH_LIB)
     return LIB
 
 

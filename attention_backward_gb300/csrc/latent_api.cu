@@ -250,8 +250,6 @@ attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, 
   p.err = &static_cast<WsHeader*>(workspace)->err;
   p.timeout_ns = kWaitTimeoutNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // the error word starts clear; the kernel records the first wait that ran out
-  if (cudaMemsetAsync(p.err, 0, sizeof(int), st) != cudaSuccess) return ATTN_ERR_LAUNCH;
   return launch_status(launch_latent_lists(lp, heads, dtype == ATTN_DT_BF16, sm_count(), st));
 }
 

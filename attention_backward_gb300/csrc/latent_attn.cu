@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const bool aligned = (smem_u32(sm) & 1023u) == 0;
   if (threadIdx.x == 0) {
     if (LISTS) {
-      if (!aligned) atomicCAS(p.err, 0, kErrAlign);
+      // (the call's error word, which a wait sets after a second at the earliest)
+      if (blockIdx.x == 0) *p.err = aligned ? kErrNone : kErrAlign;
     } else {
       *wc.err = aligned ? kErrNone : kErrAlign;
       p.desc[blockIdx.x] = make_int4(0, 0, 0, -1);

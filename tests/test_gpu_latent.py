@@ -359,3 +359,54 @@ def test_serving_step(name):
             assert np.linalg.norm(got - f64(oe)[0]) <= 4 * EPS[name] * np.linalg.norm(got)
         start += plan.counts[1:2]
         lens.copy_(plan.kv_lens)
+
+
+def test_binding_refusals():
+    """Shapes, types, devices and orders that the binding refuses before anything runs."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    h = dict(dtype=torch.float16, device="cuda")
+    table, pos = ab.rope_table(64), i32([0, 1, 2])
+    q, kv = torch.zeros(1, 3, 4, 576, **h), torch.zeros(1, 3, 576, **h)
+    cache, t, cu, lens = ab.new_latent_cache(4, 16, torch.float16), i32([[0, 1]]), i32([0, 3]), i32([20])
+    rows, idx = torch.zeros(1, 9, 1, 576, **h), i32(np.zeros((1, 3, 1, 7)))
+    qe, up, kr = torch.zeros(1, 3, 4, 192, **h), torch.zeros(1, 3, 4, 256, **h), torch.zeros(1, 3, 64, **h)
+    kn, v = up[..., :128], up[..., 128:]
+    ws = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    bad = [
+        lambda: ab.rope(q.float(), pos, table), lambda: ab.rope(q[0], pos, table), lambda: ab.rope(q, pos.long(), table),
+        lambda: ab.rope(q, pos[:2], table), lambda: ab.rope(q, pos.cpu(), table), lambda: ab.rope(q, pos, table.steps),
+        lambda: ab.rope(q, pos, table, k=q.bfloat16()), lambda: ab.rope(q, pos, table, k=q[:, :2]),
+        lambda: ab.rope(q, pos, table, start=520), lambda: ab.rope(q, pos, table, out=(q, q)), lambda: ab.rope(q, pos, table, out=(q,)),
+        lambda: ab.rope(q, pos, table, k=q, out=(q, None)), lambda: ab.rope(q, pos, table, out=(q[..., :64], None)),
+        lambda: ab.rope(q.transpose(2, 3), pos, table), lambda: ab.rope(q, pos, ab.rope_table(24)),
+        lambda: ab.rope(q, pos, ab.rope_table(64, device="cpu")), lambda: ab.rope(None, pos, table),
+        lambda: ab.latent_cache_write(kv, pos, cache.bfloat16()), lambda: ab.latent_cache_write(kv[0], pos, cache),
+        lambda: ab.latent_cache_write(kv[..., :512], pos, cache), lambda: ab.latent_cache_write(kv, pos[:2], cache),
+        lambda: ab.latent_cache_write(kv, pos, cache, norm_weight=kv[0, 0]), lambda: ab.latent_cache_write(kv, pos, cache, table=table),
+        lambda: ab.latent_cache_write(kv, pos, cache, positions=pos), lambda: ab.latent_cache_write(kv, pos, cache[..., :512]),
+        lambda: ab.latent_cache_write(kv, pos, cache, positions=pos, table=ab.rope_table(32)),
+        lambda: ab.latent_cache_write(kv, pos, cache, out=kv.bfloat16()), lambda: ab.latent_cache_write(kv, pos, cache[:, ::2]),
+        lambda: ab.latent_cache_write(kv, pos, cache[:, :8]),
+        lambda: ab.forward_latent_cache(q.bfloat16(), cache, t, cu, lens, 0.1), lambda: ab.forward_latent_cache(qe, cache, t, cu, lens, 0.1),
+        lambda: ab.forward_latent_cache(q, cache, t[0], cu, lens, 0.1), lambda: ab.forward_latent_cache(q, cache, t, cu[:1], lens, 0.1),
+        lambda: ab.forward_latent_cache(q, cache, t.long(), cu, lens, 0.1), lambda: ab.forward_latent_cache(q, cache, t, cu, lens, 0.0),
+        lambda: ab.forward_latent_cache(q, cache, t, cu, lens, 0.1, workspace=ws),
+        lambda: ab.forward_latent_cache(q, cache, t, cu, lens, 0.1, out=(q, q)),
+        lambda: ab.sparse_forward(q, rows[..., :512], idx), lambda: ab.sparse_forward(q, rows, idx.long()),
+        lambda: ab.sparse_forward(q, rows, idx[:, :2]), lambda: ab.sparse_forward(q, rows, idx, dv_dim=256),
+        lambda: ab.sparse_forward(q, rows, idx, 0.1, workspace=ws), lambda: ab.sparse_forward(q, rows, idx.transpose(1, 3)),
+        lambda: ab.forward_latent(q, kn, kr, v, 0.1), lambda: ab.forward_latent(qe, kn[:, :2], kr, v, 0.1),
+        lambda: ab.forward_latent(qe, kn, kr[..., :32], v, 0.1), lambda: ab.forward_latent(qe, kn, kr, v.bfloat16(), 0.1),
+        lambda: ab.forward_latent(qe, kn, kr, v, 0.1, cu_seqlens=cu.long()), lambda: ab.forward_latent(qe, kn, kr, v, 0.1, cu_seqlens=cu[:1]),
+        lambda: ab.forward_latent(qe, kn, kr, v, -1.0), lambda: ab.forward_latent(qe, kn, kr, v, 0.1, out=(qe, kr)),
+    ]
+    for i, f in enumerate(bad):
+        try:
+            f()
+        except ab.AttnBwdError:
+            continue
+        raise AssertionError(f"call {i} was not refused")
+    torch.cuda.synchronize()
