@@ -28,9 +28,7 @@ __global__ void __launch_bounds__(WARPS * 32) latent_write_kernel(const __grid_c
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
   if (t >= p.T) return;
-  const int slot = p.slot_map[t];
-  const bool held = slot >= 0 && slot < p.slots;
-  if (!held && p.out == nullptr) return;
+  const int slot = p.slot_map[t];  // (its row is read meanwhile, whether it is kept or not)
   const uint8_t* const src = p.kv + 2 * t * p.kv_stride;
   uint4 x[2];
 #pragma unroll
@@ -69,6 +67,7 @@ __global__ void __launch_bounds__(WARPS * 32) latent_write_kernel(const __grid_c
     }
   }
   const uint32_t kk = pack2<BF16>(k1, k2);
+  const bool held = slot >= 0 && slot < p.slots;
   auto store = [&](uint8_t* dst) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(dst + 16 * (lane + 32 * i)) = x[i];

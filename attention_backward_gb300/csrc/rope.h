@@ -30,6 +30,8 @@ struct RopeParams {
   int per_head;  // threads a head: 16 rotated columns each, then 16 copied ones
   int lanes;     // threads a token: per_head * (heads / heads a thread, rounded up)
   int stride;    // heads between the heads of a thread
+  int split;     // blocks a token
+  int share;     // split 1: tokens a block, else a token's threads a block
 };
 
 cudaError_t launch_rope(const RopeParams& p, bool bf16, int sms, cudaStream_t st);
