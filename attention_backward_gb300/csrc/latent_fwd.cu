@@ -68,8 +68,8 @@ enum FwdBar : int {
   FULL0,              // ring slabs
   EMPTY0 = FULL0 + RING,  // both tiles' products of it have completed
   S_FULL0 = EMPTY0 + RING,    // per tile
-  P_READY0 = S_FULL0 + 2,     // per tile: 4 softmax warps stored P
-  O_DONE0 = P_READY0 + 2,     // per tile: the tile's P V MMAs issued so far completed
+  P_READY0 = S_FULL0 + 2,     // per tile and half of the keys: 4 softmax warps stored P
+  O_DONE0 = P_READY0 + 4,     // per tile: the tile's P V MMAs issued so far completed
   O_FREE0 = O_DONE0 + 2,      // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,   // 2 ring slots: the producer published a unit index
   UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 ring slots: the 2 issuing and the 8 softmax warps read it
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars[S_FULL0 + w], 1);
-      mbar_init(&bars[P_READY0 + w], 4);
+      mbar_init(&bars[P_READY0 + 2 * w], 4);
+      mbar_init(&bars[P_READY0 + 2 * w + 1], 4);
       mbar_init(&bars[O_DONE0 + w], 1);
       mbar_init(&bars[O_FREE0 + w], 4);
     }
@@ -434,23 +435,30 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
           const uint32_t v = rc + KSLABS;
           const bool more = j + 1 < J1 && in(j + 1);
           if (in(j)) {
-            if (!(ok = mbar_wait_warp(&bars[P_READY0 + w], npv & 1, wc, kErrWaitP) && wait_slab(v) && wait_slab(v + 1))) break;
-            ++npv;
-            tc_fence_after();
+            if (!(ok = wait_slab(v) && wait_slab(v + 1))) break;
             const uint32_t s0 = v % RING, s1 = (v + 1) % RING;
             const uint32_t acc = j > lo;
-            if (s1 == s0 + 1) {  // side by side: products of 128 columns
-              const uint64_t b = r_mn + sdesc_step(SLAB) * s0;
-#pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk)
-                mma_ts_e(to, ts + kk * 8, b + sdesc_step(kk * 2048), IDESC_PV, kk > 0 ? 1u : acc, one);
-            } else {
 #pragma unroll 1
-              for (int kk = 0; kk < BK / 16; ++kk) {
-                mma_ts_e(to, ts + kk * 8, r_mn + sdesc_step(SLAB) * s0 + sdesc_step(2048) * kk, IDESC_PV1, kk > 0 ? 1u : acc, one);
-                mma_ts_e(to + 64, ts + kk * 8, r_mn + sdesc_step(SLAB) * s1 + sdesc_step(2048) * kk, IDESC_PV1, kk > 0 ? 1u : acc, one);
+            for (int hf = 0; hf < 2; ++hf) {
+              if (!(ok = mbar_wait_warp(&bars[P_READY0 + 2 * w + hf], npv & 1, wc, kErrWaitP))) break;
+              tc_fence_after();
+              if (s1 == s0 + 1) {  // side by side: products of 128 columns
+                const uint64_t b = r_mn + sdesc_step(SLAB) * s0 + sdesc_step(4 * 2048) * hf;
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk)
+                  mma_ts_e(to, ts + 32 * hf + kk * 8, b + sdesc_step(kk * 2048), IDESC_PV, kk > 0 ? 1u : acc | hf, one);
+              } else {
+#pragma unroll 1
+                for (int kk = 0; kk < BK / 32; ++kk) {
+                  const uint64_t at = sdesc_step(2048) * (4 * hf + kk);
+                  const uint32_t more_o = kk > 0 ? 1u : acc | hf;
+                  mma_ts_e(to, ts + 32 * hf + kk * 8, r_mn + sdesc_step(SLAB) * s0 + at, IDESC_PV1, more_o, one);
+                  mma_ts_e(to + 64, ts + 32 * hf + kk * 8, r_mn + sdesc_step(SLAB) * s1 + at, IDESC_PV1, more_o, one);
+                }
               }
             }
+            if (!ok) break;
+            ++npv;
             mma_commit_w(&bars[EMPTY0 + s0]);
             mma_commit_w(&bars[EMPTY0 + s1]);
             mma_commit_w(&bars[O_DONE0 + w]);
@@ -570,12 +578,14 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         // P pairs of keys 32ch .. 32ch + 31 into S columns 16ch .. 16ch + 15 (the
         // scores of this row were all loaded above)
         tmem_st16(tS + ch * 16, pw);
+        if (ch & 1) {  // a half of P: its products run while the other one is made
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[P_READY0 + 2 * w + (ch >> 1)]);
+        }
       }
       l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[P_READY0 + w]);
     }
     if (!ok) break;
     // ---- O = O_w / l and the natural-log LSE of the row
