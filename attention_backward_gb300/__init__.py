@@ -48,9 +48,11 @@ from ._latent import (  # noqa: F401
     forward_latent_cache,
     latent_cache_workspace_size,
     latent_cache_write,
+    latent_workspace_size,
     new_latent_cache,
     rope,
     rope_frequencies,
     rope_table,
     sparse_forward,
+    sparse_forward_workspace_size,
 )

@@ -55,8 +55,10 @@ _binding._SIGS.update({
     "attn_fwd_latent_cache": (c_i32, [c_vp, Strides, c_i64, c_i64, c_i32, c_f32, ctypes.POINTER(_Rows), c_vp, c_i64,
                                       c_i64, c_vp, c_vp, c_i64, c_i32, c_vp, Strides, c_vp, Strides, c_vp, c_sz,
                                       c_vp]),
+    "attn_fwd_sparse_workspace_size": (c_sz, [c_i64, c_i64, c_i64]),
     "attn_fwd_sparse": (c_i32, [c_vp, Strides, c_vp, Strides, c_vp, Strides, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64,
                                 c_i64, c_i64, c_i32, c_f32, c_vp, Strides, c_vp, Strides, c_vp, c_sz, c_vp]),
+    "attn_fwd_latent_workspace_size": (c_sz, [c_i64, c_i64, c_i64, c_i64]),
     "attn_fwd_latent": (c_i32, [c_vp, Strides, c_vp, Strides, c_vp, Strides, c_vp, Strides, c_i64, c_i64, c_i64, c_i32,
                                 c_f32, ctypes.POINTER(_binding.Mask), c_vp, Strides, c_vp, Strides, c_vp, c_sz, c_vp]),
 })
@@ -207,13 +209,24 @@ def forward_latent_cache(q, cache, block_table, cu_seqlens, kv_lens, sm_scale: f
                  *_pair(out))
 
 
+def sparse_forward_workspace_size(B: int, S: int, HKV: int) -> int:
+    """Workspace bytes of sparse_forward with room to split the lists of few tokens (256 always serve)."""
+    return int(_binding.library().attn_fwd_sparse_workspace_size(B, S, HKV))
+
+
 def sparse_forward(q, kv, idx, sm_scale: Optional[float] = None, dv_dim: int = LAT, workspace=None, out=None,
                    stream=None):
     """O [B,S,H,512] and the natural-log LSE [B,H,S] of top-k sparse attention
     over shared latent rows, as ``sparse_backward`` takes them (see attn_fwd_sparse):
-    q [B,S,H,576], kv [B,SKV,HKV,576], idx int32 [B,S,HKV,topk]."""
+    q [B,S,H,576], kv [B,SKV,HKV,576], idx int32 [B,S,HKV,topk].  ``out`` (o, lse) and
+    ``workspace`` (uint8, at least 256 bytes; one per stream) may be passed to reuse them."""
     return _call("sparse_forward", q, stream, kv, idx, ROW ** -0.5 if sm_scale is None else sm_scale, dv_dim, workspace,
                  *_pair(out))
+
+
+def latent_workspace_size(B: int, S: int, H: int, num_seqs: int = 0) -> int:
+    """Workspace bytes of forward_latent."""
+    return int(_binding.library().attn_fwd_latent_workspace_size(B, S, H, num_seqs))
 
 
 def forward_latent(q, k_nope, k_rope, v, sm_scale: float, causal: bool = True, cu_seqlens=None, workspace=None,
@@ -221,5 +234,7 @@ def forward_latent(q, k_nope, k_rope, v, sm_scale: float, causal: bool = True, c
     """O [B,S,H,128] and the natural-log LSE [B,H,S] of the expanded form (see
     attn_fwd_latent): q [B,S,H,192], k_nope and v [B,Sk,H,128] (views of one projection
     serve), k_rope [B,Sk,64] shared by the heads.  Where Sk differs from S, the last
-    query stands at the last key.  ``cu_seqlens`` int32 packs sequences (B = 1, Sk = S)."""
+    query stands at the last key.  ``cu_seqlens`` int32 packs sequences (B = 1, Sk = S).
+    ``out`` (o, lse) and ``workspace`` (uint8, latent_workspace_size bytes; one per stream)
+    may be passed to reuse them."""
     return _call("forward_latent", q, stream, k_nope, k_rope, v, sm_scale, causal, cu_seqlens, workspace, *_pair(out))

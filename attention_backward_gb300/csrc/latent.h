@@ -43,7 +43,17 @@ struct LatParams {
   int64_t si_b, si_s, si_h;
   int64_t so_b, sl_b;
   int B, S, SKV, HKV, gh, topk;
+  int splits;  // parts of a list's tiles, a CTA each (1: whole)
 };
+
+// Unit u of the lists' line: later tokens first, whose lists are longest as a rule.
+struct LatListUnit {
+  int b, t, g;
+};
+__host__ __device__ inline LatListUnit list_unit(int u, const LatParams& p) {
+  const int n = p.B * p.HKV, bg = u % n;
+  return {bg / p.HKV, p.S - 1 - u / n, bg % p.HKV};
+}
 
 // Rows (query, head) of a CTA, keys a tile, what starting a unit costs in tiles,
 // fewest line positions of a part, most CTAs.
@@ -59,10 +69,12 @@ cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& q, bool b
                                 cudaStream_t st);
 // ``q``: dims (576, H, S, B), box 64 columns x 64 heads of a token.
 cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st);
-// Joins rows that were split over CTAs and writes the call's error word.
+// Joins rows that were split over CTAs and, of the cache (group > 0), writes the call's error word.
 cudaError_t launch_latent_join(const LatParams& p, bool bf16, int group, int ctas, int sms, cudaStream_t st);
 
-// The expanded form.
+// The expanded form: most units of a call that splits its keys, and their rows.
+constexpr int kLatFwdMaxUnits = 160;
+constexpr int kLatFwdRows = 256;
 struct LatFwdParams {
   int B, S, Sk, H;
   int causal;
@@ -76,10 +88,14 @@ struct LatFwdParams {
   int* err;
   int* unit_counter;
   uint64_t timeout_ns;
+  int splits;       // units a pair of query tiles, of a share of its key blocks each
+  float2* part_ml;  // splits > 1: [pairs * splits][256 rows] reference (log2 units) and sum
+  float* part_o;    // [pairs * splits][256 rows][128]
 };
 struct LatFwdMaps {
   CUtensorMap q, kn, kr, v;  // box 64 columns x 128 rows of one head
 };
-cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int grid, cudaStream_t st);
+// ``pairs``: at least the pairs of query tiles of the call.
+cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int pairs, int grid, cudaStream_t st);
 
 }  // namespace ab

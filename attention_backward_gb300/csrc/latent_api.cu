@@ -3,6 +3,7 @@
 // state.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -100,6 +101,12 @@ LatWs lat_ws() {
   w.total = w.o_off + int64_t(2) * kLatMaxCtas * kLatRows * kLatDim * 4;
   return w;
 }
+
+// Pairs of 128-row query tiles of the expanded form; a packed batch may add one a sequence.
+int64_t fwd_pairs(int64_t B, int64_t S, int64_t H, int64_t num_seqs) { return ((S + 255) / 256 + num_seqs) * B * H; }
+
+// Partial rows of lists that are split, a slot a CTA.
+constexpr int64_t kListPartBytes = int64_t(kLatMaxCtas) * kLatRows * (8 + kLatDim * 4);
 
 }  // namespace
 
@@ -215,6 +222,11 @@ attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t sq, int64_t T,
   return launch_status(launch_latent_join(lp, bf16, group, ctas, sms, st));
 }
 
+size_t attn_fwd_sparse_workspace_size(int64_t B, int64_t S, int64_t HKV) {
+  if (B < 1 || S < 1 || HKV < 1 || B >= kMax32 || HKV >= kMax32 || B > kMaxCount / HKV || B * HKV > kMaxCount / S) return 0;
+  return static_cast<size_t>(kHeaderBytes + (2 * B * S * HKV <= kLatMaxCtas ? kListPartBytes : 0));
+}
+
 attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, attn_strides_t skv, const int32_t* idx,
                               attn_strides_t sidx, int64_t B, int64_t S, int64_t SKV, int64_t H, int64_t HKV,
                               int64_t DQK, int64_t DV, int64_t topk, attn_dtype_t dtype, float sm_scale, void* o,
@@ -249,8 +261,25 @@ attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, 
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.err = &static_cast<WsHeader*>(workspace)->err;
   p.timeout_ns = kWaitTimeoutNs;
+  const int sms = imin(sm_count(), kLatMaxCtas);
+  // Lists that leave CTAs idle are split over them, two tiles a part at least, where the
+  // workspace has room for the parts.  64 heads, 2048 rows a list: 51 us whole, 14 for
+  // one token in 16 parts, 25 for 32 in 4, 38 for 76 in 2.
+  lp.splits = 1;
+  if (workspace_bytes >= static_cast<size_t>(kHeaderBytes + kListPartBytes)) {
+    lp.splits = static_cast<int>(std::max<int64_t>(1, std::min(sms / (B * S * HKV), (topk + 2 * kLatKeys - 1) / (2 * kLatKeys))));
+    p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+    p.part_o = reinterpret_cast<float*>(p.part_ml + kLatMaxCtas * kLatRows);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return launch_status(launch_latent_lists(lp, heads, dtype == ATTN_DT_BF16, sm_count(), st));
+  return launch_status(launch_latent_lists(lp, heads, dtype == ATTN_DT_BF16, sms, st));
+}
+
+size_t attn_fwd_latent_workspace_size(int64_t B, int64_t S, int64_t H, int64_t num_seqs) {
+  if (B < 1 || S < 1 || H < 1 || num_seqs < 0 || num_seqs > (1 << 20) || B > 65535 || H > 65535 || S > kMaxCount / (B * H))
+    return 0;
+  const int64_t parts = 2 * fwd_pairs(B, S, H, num_seqs) <= kLatFwdMaxUnits ? kLatFwdMaxUnits * kLatFwdRows : 0;
+  return static_cast<size_t>(kHeaderBytes + parts * (8 + 128 * 4));
 }
 
 attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, attn_strides_t skn, const void* kr,
@@ -267,7 +296,6 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
     if (!stride_ok(st->b) || !stride_ok(st->s) || !stride_ok(st->h)) return ATTN_ERR_INVALID_ARG;
   if (!stride_ok(skr.b) || !stride_ok(skr.s)) return ATTN_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || slse.b < 0 || slse.s < 0 || slse.h < 0) return ATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < static_cast<size_t>(kHeaderBytes)) return ATTN_ERR_WORKSPACE;
   int64_t Sk = S;
   LatFwdParams p{};
   if (mask) {
@@ -283,9 +311,9 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
     if (mask->kv_len > 0) Sk = mask->kv_len;
   }
   if (B > 65535 || H > 65535 || S > kMaxCount / (B * H) || Sk > kMaxCount / (B * H)) return ATTN_ERR_UNSUPPORTED;
-  // units of two 128-row query tiles of a head; a packed batch may add one partial unit a sequence
-  const int64_t units = ((S + 255) / 256 + p.num_seqs) * B * H;
-  if (units > kMaxCount) return ATTN_ERR_UNSUPPORTED;
+  const int64_t pairs = fwd_pairs(B, S, H, p.num_seqs);
+  if (pairs > kMaxCount) return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < attn_fwd_latent_workspace_size(B, S, H, p.num_seqs)) return ATTN_ERR_WORKSPACE;
   LatFwdMaps m;
   if (!make_bshd_map(&m.q, q, dtype, B, S, H, 192, sq, 1, 128) ||
       !make_bshd_map(&m.kn, kn, dtype, B, Sk, H, 128, skn, 1, 128) ||
@@ -300,10 +328,20 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
   p.unit_counter = &static_cast<WsHeader*>(workspace)->tile_counter;
   p.timeout_ns = kWaitTimeoutNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int sms = sm_count();
+  const int sms = imin(sm_count(), kLatFwdMaxUnits);
+  // Pairs that leave CTAs idle are split over them, two key blocks a part at least, from 1024
+  // keys on: 8 queries on 8192 keys, one head 164 -> 25 us, 300 on 4000, 8 heads 86 -> 29,
+  // 1024 on 1024, 8 heads 27 -> 22.5; 512 on 512, 16 heads 18 -> 21.
+  p.splits = Sk < 1024 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min(sms / pairs, (Sk + 255) / 256)));
+  if (p.splits > 1) {
+    p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+    p.part_o = reinterpret_cast<float*>(p.part_ml + kLatFwdMaxUnits * kLatFwdRows);
+  }
+  const int64_t units = pairs * p.splits;
   // the error word and the unit counter start clear
   if (cudaMemsetAsync(workspace, 0, kHeaderBytes, st) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  return launch_status(launch_latent_fwd(p, m, dtype == ATTN_DT_BF16, static_cast<int>(units < sms ? units : sms), st));
+  return launch_status(launch_latent_fwd(p, m, dtype == ATTN_DT_BF16, static_cast<int>(pairs),
+                                         static_cast<int>(units < sms ? units : sms), st));
 }
 
 }  // extern "C"

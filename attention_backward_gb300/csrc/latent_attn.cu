@@ -26,7 +26,8 @@
 // Cache: the line of kv_sched.cuh, cut evenly over the CTAs; a unit split over
 // several leaves f32 partials that latent_join.cu joins.  Where requests have more
 // than 64 rows two CTAs share a part, 64 rows each of units of 128, so that the second
-// reads its keys from L2.  Lists: a unit a token and KV group, longest lists first.
+// reads its keys from L2.  Lists: a unit a token and KV group, longest lists first, or,
+// where these are few, parts of their tiles.
 //
 // Rows are loaded by 16-byte asynchronous copies of four warps, a slab's swizzle written
 // by address; rows that are not visible are filled with zeros.  (TMA gathers of four rows
@@ -372,19 +373,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       return true;
     };
     if constexpr (LISTS) {
-      const int64_t units = static_cast<int64_t>(lp.B) * lp.S * lp.HKV;
-      const int bg_n = lp.B * lp.HKV;
+      const int64_t units = static_cast<int64_t>(lp.B) * lp.S * lp.HKV * lp.splits;
       uint32_t uc = 0;
       for (int64_t i = blockIdx.x;; i += gridDim.x, ++uc) {
         LatUnit u{};
         u.valid = i < units;
         if (u.valid) {
-          // later tokens' lists are longest as a rule
-          const int bg = static_cast<int>(i % bg_n), t = lp.S - 1 - static_cast<int>(i / bg_n);
-          u.n = bg / lp.HKV, u.a = t;
-          const int g = bg % lp.HKV;
-          u.row0 = g * lp.gh, u.live = lp.gh;
-          const int* const il = lp.idx + u.n * lp.si_b + t * lp.si_s + g * lp.si_h;
+          const LatListUnit v = list_unit(static_cast<int>(i / lp.splits), lp);
+          u.n = v.b, u.a = v.t, u.row0 = v.g * lp.gh, u.live = lp.gh;
+          const int* const il = lp.idx + v.b * lp.si_b + v.t * lp.si_s + v.g * lp.si_h;
           int last = -1;
 #pragma unroll 8
           for (int s = lane; s < lp.topk; s += 32) {
@@ -392,8 +389,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (j >= 0 && j < lp.SKV) last = s;
           }
           last = __reduce_max_sync(0xffffffffu, last);
-          u.j1 = last < 0 ? 0 : last / KT + 1;
-          u.slot = -1;
+          const int n = last < 0 ? 0 : last / KT + 1, part = static_cast<int>(i % lp.splits);
+          u.j0 = static_cast<int>(static_cast<int64_t>(n) * part / lp.splits);
+          u.j1 = static_cast<int>(static_cast<int64_t>(n) * (part + 1) / lp.splits);
+          u.slot = lp.splits > 1 ? static_cast<int>(i) : -1;
         }
         if (!publish(uc, u) || !u.valid) break;
       }
@@ -817,9 +816,10 @@ cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& q, bool b
 }
 
 cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool bf16, int sms, cudaStream_t st) {
-  const int64_t units = static_cast<int64_t>(p.B) * p.S * p.HKV;
+  const int64_t units = static_cast<int64_t>(p.B) * p.S * p.HKV * p.splits;
   const int grid = static_cast<int>(units < sms ? units : sms);
-  return bf16 ? launch_t<0, true>(p, q, grid, st) : launch_t<0, false>(p, q, grid, st);
+  const cudaError_t e = bf16 ? launch_t<0, true>(p, q, grid, st) : launch_t<0, false>(p, q, grid, st);
+  return e != cudaSuccess || p.splits == 1 ? e : launch_latent_join(p, bf16, 0, 0, sms, st);
 }
 
 }  // namespace ab

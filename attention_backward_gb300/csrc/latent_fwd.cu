@@ -9,6 +9,9 @@
 // shared keys are read where they lie, as the third 64-column slab of every head's K,
 // so that no [S, H, 192] keys are ever written.
 //
+// Calls of few pairs of tiles split their key blocks over the CTAs; f32 partials go to the
+// workspace, and a second launch joins them in order.
+//
 // Two Q tiles of 192 columns leave room for 8 slabs of 128 keys x 64 columns: K
 // and V come through a ring of slabs (three of K_j, two of V_j, ...), each loaded
 // and freed by itself, so that the next K is there while V is in use.
@@ -84,7 +87,7 @@ static_assert(NUM_FWD_BARS <= 40, "barrier storage");
 // range [lo, hi) of 128-key blocks.
 struct FwdUnit {
   int valid, b, h, seq_start, qlen, klen, off, q0;
-  int tiles;  // 2, or 1: the second is another unit's
+  int index;  // in the launch's order
   int lo[2], hi[2];  // lo == hi: the tile sees no key; q0 + 128 w >= qlen: the tile is absent
 };
 
@@ -103,38 +106,18 @@ __device__ __forceinline__ void key_block_range(int q0, int qlen, int klen, int 
   *hi = static_cast<int>((ke + BK - 1) / BK);
 }
 
-// Pairs of query tiles of the launch.
-__device__ __forceinline__ int count_pairs(const LatFwdParams& p) {
-  if (p.cu_seqlens == nullptr) return (p.S + 2 * BQ - 1) / (2 * BQ) * p.B * p.H;
-  int n = 0;
-  for (int i = 0; i < p.num_seqs; ++i) {
-    const int a = clamp_pos(p.cu_seqlens[i], p.S), e = clamp_pos(p.cu_seqlens[i + 1], p.S);
-    n += e > a ? (e - a + 2 * BQ - 1) / (2 * BQ) : 0;
-  }
-  return n * p.H;
-}
-
-// The first pair that is cut into units of one tile: those of a last round that leaves at
-// least half of the CTAs without a pair (a tile by itself takes about 0.65 of a pair's
-// time).  2048 queries on 8192 keys, 64 heads: 512 pairs on 152 CTAs, 516 us, SINGLES.
-__device__ __forceinline__ int first_single(const LatFwdParams& p) {
-  const int n = count_pairs(p), last = n % static_cast<int>(gridDim.x);
-  return 2 * last <= static_cast<int>(gridDim.x) ? n - last : n;
-}
-
 // Unit u of the launch, longest first under a causal mask (the last query
 // tiles of a row see the most keys): dense rows go through the tile pairs
 // from the last, each over all (batch, head) pairs; packed sequences one after
-// another, each the same way over its heads.
-__device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p, int singles) {
+// another, each the same way over its heads.  Each pair of tiles is p.splits units in
+// a row, of an even share of its key blocks each.
+__device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p) {
   FwdUnit t{};
   t.valid = 0;
   if (u < 0) return t;  // the end-of-work marker
-  int one = -1;  // the only tile of the unit
-  if (u >= singles) {
-    one = (u - singles) & 1;
-    u = singles + ((u - singles) >> 1);
-  }
+  t.index = u;
+  const int part = u % p.splits;
+  u /= p.splits;
   int pair = 0;
   if (p.cu_seqlens == nullptr) {
     const int np = (p.S + 2 * BQ - 1) / (2 * BQ);
@@ -167,10 +150,18 @@ __device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p, int
     }
     if (!found) return t;
   }
-  t.q0 = (2 * pair + imax(one, 0)) * BQ;
-  t.tiles = one < 0 ? 2 : 1;
-  for (int w = 0; w < t.tiles; ++w)
+  t.q0 = pair * 2 * BQ;
+  for (int w = 0; w < 2; ++w)
     key_block_range(t.q0 + w * BQ, t.qlen, t.klen, t.off, p.causal, &t.lo[w], &t.hi[w]);
+  if (p.splits > 1) {
+    const int n = imax(t.hi[0], t.hi[1]);  // (no window: the blocks of both tiles begin at 0)
+    const int a = static_cast<int>(static_cast<int64_t>(n) * part / p.splits);
+    const int e = static_cast<int>(static_cast<int64_t>(n) * (part + 1) / p.splits);
+    for (int w = 0; w < 2; ++w) {
+      t.lo[w] = imax(t.lo[w], a), t.hi[w] = imin(t.hi[w], e);
+      if (t.hi[w] <= t.lo[w]) t.lo[w] = t.hi[w] = 0;
+    }
+  }
   t.valid = 1;
   return t;
 }
@@ -268,7 +259,6 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     }
   };
 
-  const int singles = first_single(p);
   // the uc-th unit of this CTA (consumers): waits for the producer's draw,
   // hands the slot back, decodes; invalid once the draws are exhausted
   auto next_unit = [&](uint32_t uc, bool* okp) -> FwdUnit {
@@ -279,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const int t = ring[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[UNIT_EMPTY0 + slot]);
-    return decode_unit(t, p, singles);
+    return decode_unit(t, p);
   };
 
   if (warp >= 8) {
@@ -296,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         int t = 0;
         if (lane == 0) t = atomicAdd(p.unit_counter, 1);
         t = __shfl_sync(0xffffffffu, t, 0);
-        const FwdUnit u = decode_unit(t, p, singles);
+        const FwdUnit u = decode_unit(t, p);
         if (lane == 0) {
           ring[slot] = u.valid ? t : -1;
           mbar_arrive(&bars[UNIT_FULL0 + slot]);
@@ -500,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const FwdUnit u = next_unit(uc, &ok);
     if (!ok || !u.valid) break;
     const int qt0 = u.q0 + w * BQ;  // first (sequence-local) query of the tile
-    if (w >= u.tiles || qt0 >= u.qlen) continue;  // another unit's tile, or past the end of its sequence
+    if (qt0 >= u.qlen) continue;    // the tile is past the end of its sequence
     const int lo_w = w ? u.lo[1] : u.lo[0], hi_w = w ? u.hi[1] : u.hi[0];
     const int q = qt0 + row;
     const uint32_t c0 = c;
@@ -596,10 +586,16 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     }
     const bool live = q < u.qlen;
     const int64_t pos = u.seq_start + q;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (live)
-      p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] =
-          l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t part_row = static_cast<int64_t>(u.index) * 2 * BQ + w * BQ + row;  // of a split unit
+    if (live) {
+      if (p.splits > 1) {
+        p.part_ml[part_row] = make_float2(m_used, l);
+      } else {
+        p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] =
+            l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+      }
+    }
     uint8_t* const out = p.o + 2 * (u.b * p.so_b + pos * p.so_s + u.h * p.so_h);
 #pragma unroll 1
     for (int ch = 0; ch < D / 32; ++ch) {
@@ -611,7 +607,15 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 32; ++e) r[e] = 0u;
       }
-      if (live) {
+      if (live && p.splits > 1) {
+        if (l != 0.f) {  // (a part that saw no key of the row says nothing)
+          float4* const dst = reinterpret_cast<float4*>(p.part_o + part_row * D + ch * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                                 __uint_as_float(r[4 * e + 3]));
+        }
+      } else if (live) {
 #pragma unroll
         for (int c8 = 0; c8 < 4; ++c8) {
           uint4 v;
@@ -633,19 +637,65 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   finish();
 }
 
+// Joins the parts of split units: a warp a row, 4 columns a lane, the parts in order.
+constexpr int JOIN_WARPS = 8;
 template <bool BF16>
-cudaError_t launch_t(const LatFwdParams& p, const LatFwdMaps& m, int grid, cudaStream_t st) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) latent_fwd_join_kernel(const LatFwdParams p, int pairs) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int lane = threadIdx.x & 31, w = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5), pair = w / (2 * BQ), row = w % (2 * BQ);
+  if (pair >= pairs) return;
+  const FwdUnit u = decode_unit(pair * p.splits, p);
+  const int q = u.q0 + row;
+  if (!u.valid || q >= u.qlen) return;
+  const int64_t first = static_cast<int64_t>(pair) * p.splits * 2 * BQ + row;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < p.splits; i0 += 32) {
+    const int n = imin(32, p.splits - i0);
+    float2 v = make_float2(0.f, 0.f);
+    if (lane < n) v = p.part_ml[first + static_cast<int64_t>(i0 + lane) * 2 * BQ];
+    float mx = v.y == 0.f ? -INFINITY : v.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = fmaxf(mx, m);
+    const float f = v.y == 0.f ? 0.f : ex2(v.x - mx), g = m == -INFINITY ? 0.f : ex2(m - mx);
+    m = mx;
+    float sum = f * v.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * g + sum;
+    acc.x *= g, acc.y *= g, acc.z *= g, acc.w *= g;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      if (fi == 0.f) continue;
+      const float4 x = reinterpret_cast<const float4*>(p.part_o + (first + static_cast<int64_t>(i0 + i) * 2 * BQ) * D)[lane];
+      acc.x += fi * x.x, acc.y += fi * x.y, acc.z += fi * x.z, acc.w += fi * x.w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t pos = u.seq_start + q;
+  *reinterpret_cast<uint2*>(p.o + 2 * (u.b * p.so_b + pos * p.so_s + u.h * p.so_h + 4 * lane)) =
+      make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+  if (lane == 0)
+    p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <bool BF16>
+cudaError_t launch_t(const LatFwdParams& p, const LatFwdMaps& m, int pairs, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = latent_fwd_kernel<BF16>;
   if (const cudaError_t e = allow_smem_once(kern, SMEM, &done); e != cudaSuccess) return e;
   kern<<<grid, THREADS, SMEM, st>>>(m, p);
-  return cudaGetLastError();
+  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess || p.splits == 1) return e;
+  return launch_chained(latent_fwd_join_kernel<BF16>, dim3(pairs * (2 * BQ / JOIN_WARPS)), JOIN_WARPS * 32, 0, st, p, pairs);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int grid, cudaStream_t st) {
-  return bf16 ? launch_t<true>(p, m, grid, st) : launch_t<false>(p, m, grid, st);
+cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int pairs, int grid, cudaStream_t st) {
+  return bf16 ? launch_t<true>(p, m, pairs, grid, st) : launch_t<false>(p, m, pairs, grid, st);
 }
 
 }  // namespace ab

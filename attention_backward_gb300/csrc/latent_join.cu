@@ -1,8 +1,8 @@
-// The second launch of attention over the latent cache: rows whose keys were
-// split over CTAs are joined from their f32 partials in the workspace, in a fixed
-// order.
+// The second launch of attention over latent rows: rows whose keys were split over
+// CTAs are joined from their f32 partials in the workspace, in a fixed order.
 //
-// Entry w of ``desc`` (first token of the request, first row of the unit in the
+// Lists: each unit is lp.splits parts in as many slots.  The cache:
+// entry w of ``desc`` (first token of the request, first row of the unit in the
 // request, rows, first part) names the unit that CTA w finished and did not begin; its
 // parts are d.w to w / group in order, w = -1 where there is none.  Each half of a row
 // of such a unit is an item; a warp takes one, or, where there are warps to spare, 2 to
@@ -21,7 +21,7 @@ constexpr int WARPS = 16, HALF = kLatDim / 2, ND = HALF / 32, PF = 4;  // column
 constexpr int LISTERS = (kLatMaxCtas + 31) / 32;  // warps that hold entries, one a thread
 static_assert(LISTERS <= WARPS, "an entry a thread");
 
-template <bool BF16>
+template <bool LISTS, bool BF16>
 __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid_constant__ LatParams lp, int group, int ctas) {
   const KvAttnParams& p = lp.a;
   __shared__ int4 list[kLatMaxCtas];
@@ -31,26 +31,31 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_dependents_launch();
-  if (blockIdx.x == 0) {  // the call's error word: some CTA's error, if there is any
-    const int err = tid < ctas ? p.cta_err[tid] : kErrNone;
-    if (tid == 0) *p.err = kErrNone;
-    if (__syncthreads_or(err != kErrNone) && err != kErrNone) *p.err = err;
-  }
-  int4 d = make_int4(0, 0, 0, -1);
-  if (tid < ctas) d = p.desc[tid];
-  const uint32_t held = __ballot_sync(0xffffffffu, d.w >= 0);
-  if (lane == 0) counts[warp] = __popc(held);
-  __syncthreads();
-  int count = 0, first = 0;
+  int count = 0;
+  if constexpr (LISTS) {
+    count = lp.B * lp.S * lp.HKV;
+  } else {
+    if (blockIdx.x == 0) {  // the call's error word: some CTA's error, if there is any
+      const int err = tid < ctas ? p.cta_err[tid] : kErrNone;
+      if (tid == 0) *p.err = kErrNone;
+      if (__syncthreads_or(err != kErrNone) && err != kErrNone) *p.err = err;
+    }
+    int4 d = make_int4(0, 0, 0, -1);
+    if (tid < ctas) d = p.desc[tid];
+    const uint32_t held = __ballot_sync(0xffffffffu, d.w >= 0);
+    if (lane == 0) counts[warp] = __popc(held);
+    __syncthreads();
+    int first = 0;
 #pragma unroll
-  for (int i = 0; i < LISTERS; ++i) {
-    if (i < warp) first += counts[i];
-    count += counts[i];
+    for (int i = 0; i < LISTERS; ++i) {
+      if (i < warp) first += counts[i];
+      count += counts[i];
+    }
+    // parts in the upper half of z, this CTA's place in its group in the upper half of w
+    if (d.w >= 0)
+      list[first + __popc(held & ((1u << lane) - 1u))] = make_int4(d.x, d.y, d.z | (tid / group - d.w + 1) << 16, d.w | (tid % group) << 16);
+    __syncthreads();
   }
-  // parts in the upper half of z, this CTA's place in its group in the upper half of w
-  if (d.w >= 0)
-    list[first + __popc(held & ((1u << lane) - 1u))] = make_int4(d.x, d.y, d.z | (tid / group - d.w + 1) << 16, d.w | (tid % group) << 16);
-  __syncthreads();
   const int items = count * kLatRows * 2;
   int ls = 0;  // log2 of the warps an item
   while ((1 << ls) < WARPS && items << (ls + 1) <= static_cast<int>(gridDim.x) * WARPS) ++ls;
@@ -58,10 +63,11 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
   for (int t0 = blockIdx.x * per_block; t0 < items; t0 += gridDim.x * per_block) {
     const int item = t0 + (warp >> ls);
     int4 u = make_int4(0, 0, 0, 0);
-    if (item < items) u = list[item / (2 * kLatRows)];
-    const int row = item / 2 % kLatRows, half = item % 2, live = u.z & 0xffff, parts = u.z >> 16, g0 = u.w & 0xffff, sub = u.w >> 16;
+    if (!LISTS && item < items) u = list[item / (2 * kLatRows)];
+    const int unit = item / (2 * kLatRows), row = item / 2 % kLatRows, half = item % 2;
+    const int live = LISTS ? lp.gh : u.z & 0xffff, parts = LISTS ? lp.splits : u.z >> 16, g0 = u.w & 0xffff, sub = u.w >> 16;
     const bool on = item < items && row < live;
-    auto slot_of = [&](int i) { return 2 * ((g0 + i) * group + sub) + (i == 0 ? 1 : 0); };
+    auto slot_of = [&](int i) { return LISTS ? unit * lp.splits + i : 2 * ((g0 + i) * group + sub) + (i == 0 ? 1 : 0); };
     float m = -INFINITY, l = 0.f, acc[ND];
 #pragma unroll
     for (int i = 0; i < ND; ++i) acc[i] = 0.f;
@@ -126,11 +132,18 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < ND; ++i) acc[i] = acc[i] * g + s_o[warp + k][i * 32 + lane] * f;
       }
-      const int at = u.y + row;  // row of the request
-      const int64_t t = static_cast<int64_t>(u.x) + at / p.G;
-      const int head = at % p.G;
+      int64_t o_at, lse_at;
+      if constexpr (LISTS) {
+        const LatListUnit v = list_unit(unit, lp);
+        const int head = v.g * lp.gh + row;
+        o_at = v.b * lp.so_b + v.t * p.so_s + head * p.so_h, lse_at = v.b * lp.sl_b + head * p.sl_h + v.t * p.sl_s;
+      } else {
+        const int at = u.y + row, head = at % p.G;  // row of the request
+        const int64_t t = static_cast<int64_t>(u.x) + at / p.G;
+        o_at = t * p.so_s + head * p.so_h, lse_at = head * p.sl_h + t * p.sl_s;
+      }
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint8_t* const out = p.o + 2 * (t * p.so_s + head * p.so_h + half * HALF);
+      uint8_t* const out = p.o + 2 * (o_at + half * HALF);
 #pragma unroll
       for (int e = 0; e < ND / 4; ++e) {
         const uint2 w = make_uint2(pack2<BF16>(acc[4 * e] * inv, acc[4 * e + 1] * inv),
@@ -138,7 +151,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
         *reinterpret_cast<uint2*>(out + 8 * (e * 32 + lane)) = w;
       }
       if (lane == 0 && half == 0)
-        p.lse[head * p.sl_h + t * p.sl_s] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        p.lse[lse_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
     if (shares > 1) __syncthreads();
   }
@@ -147,7 +160,8 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_latent_join(const LatParams& p, bool bf16, int group, int ctas, int sms, cudaStream_t st) {
-  auto kern = bf16 ? latent_join_kernel<true> : latent_join_kernel<false>;
+  auto kern = group == 0 ? (bf16 ? latent_join_kernel<true, true> : latent_join_kernel<true, false>)
+                         : (bf16 ? latent_join_kernel<false, true> : latent_join_kernel<false, false>);
   return launch_chained(kern, dim3(2 * sms), WARPS * 32, 0, st, p, group, ctas);
 }
 

@@ -277,7 +277,7 @@ std::tuple<Tensor, Tensor> sparse_forward(const Tensor& q, const Tensor& kv, con
   const attn_strides_t skv{B > 1 ? kv.stride(0) : SKV * HKV * row, SKV > 1 ? kv.stride(1) : HKV * row, row};
   TORCH_CHECK(dv_dim >= 1, "dv_dim must be positive");
   const Launch launch(q, stream);
-  const Outputs out(q, {B, S, H, dv_dim}, o, lse, workspace, 256);
+  const Outputs out(q, {B, S, H, dv_dim}, o, lse, workspace, attn_fwd_sparse_workspace_size(B, S, HKV));
   ok(attn_fwd_sparse(q.data_ptr(), sq, kv.data_ptr(), skv, idx.const_data_ptr<int32_t>(),
                      {idx.stride(0), idx.stride(1), idx.stride(2)}, B, S, SKV, H, HKV, D, dv_dim, idx.size(3), dt,
                      static_cast<float>(sm_scale), out.o.data_ptr(), out.so, out.lse.data_ptr<float>(), out.sl, out.ws,
@@ -310,7 +310,7 @@ std::tuple<Tensor, Tensor> forward_latent(const Tensor& q, const Tensor& k_nope,
     mask.num_seqs = static_cast<int32_t>(std::min<int64_t>(cu_seqlens->size(0) - 1, 0x7fffffff));
   }
   const Launch launch(q, stream);
-  const Outputs out(q, {B, S, H, kValue}, o, lse, workspace, 256);
+  const Outputs out(q, {B, S, H, kValue}, o, lse, workspace, attn_fwd_latent_workspace_size(B, S, H, mask.num_seqs));
   ok(attn_fwd_latent(q.data_ptr(), sq, k_nope.data_ptr(), sk, k_rope.data_ptr(),
                      {B > 1 ? k_rope.stride(0) : 128, Sk > 1 ? k_rope.stride(1) : 128, 128}, v.data_ptr(), sv, B, S, H, dt,
                      static_cast<float>(sm_scale), &mask, out.o.data_ptr(), out.so, out.lse.data_ptr<float>(), out.sl,

@@ -96,6 +96,10 @@ ATTN_BWD_API attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t s
                                                  attn_strides_t slse, void* workspace, size_t workspace_bytes,
                                                  void* stream);
 
+/* Bytes of workspace with which attn_fwd_sparse may split the lists of few tokens
+ * over CTAs: the 256-byte header and their f32 partials (256 where it would not). */
+ATTN_BWD_API size_t attn_fwd_sparse_workspace_size(int64_t B, int64_t S, int64_t HKV);
+
 /* The forward of attn_bwd_sparse: per query head h of KV group g = h / (H / HKV)
  * and token t, over the rows that the list idx[b, t, g, :] names,
  *   O = softmax(sm_scale q kv_row^T) kv_row[:DV] and the natural-log LSE.
@@ -106,14 +110,20 @@ ATTN_BWD_API attn_status_t attn_fwd_latent_cache(const void* q, attn_strides_t s
  *   [B,S,HKV,topk], strides sidx, unit slot stride;  lse : f32, lse[b*slse.b +
  *   h*slse.h + s*slse.s];  H / HKV at most 64;  DQK = 576, DV = 512;  sm_scale finite and
  *   > 0.
- *   workspace : at least 256 bytes, 16-byte aligned (the header of a backward
- *   workspace serves).
+ *   workspace : at least 256 bytes, 16-byte aligned (a backward workspace serves; with
+ *   attn_fwd_sparse_workspace_size bytes the lists of few tokens are split, and joined by
+ *   a second launch in a fixed order).
  * Errors as attn_bwd_sparse's. */
 ATTN_BWD_API attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, attn_strides_t skv,
                                            const int32_t* idx, attn_strides_t sidx, int64_t B, int64_t S, int64_t SKV,
                                            int64_t H, int64_t HKV, int64_t DQK, int64_t DV, int64_t topk,
                                            attn_dtype_t dtype, float sm_scale, void* o, attn_strides_t so, float* lse,
                                            attn_strides_t slse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attn_fwd_latent needs for S queries a batch row (num_seqs: packed
+ * sequences, 0 for dense rows): the 256-byte header, and, where the queries are few,
+ * the f32 partials of rows whose keys are split over CTAs.  0 for sizes that it refuses. */
+ATTN_BWD_API size_t attn_fwd_latent_workspace_size(int64_t B, int64_t S, int64_t H, int64_t num_seqs);
 
 /* The expanded form: head h has keys (kn_h | kr), 128 columns of its own and 64
  * that all heads share, and values v_h of 128:
@@ -125,7 +135,8 @@ ATTN_BWD_API attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, con
  *   [B,S,H,128] 16-bit;  lse : f32, lse[b*slse.b + h*slse.h + s*slse.s]
  * A query that sees no key gets O = 0 and LSE = -inf.  Rows past
  * cu_seqlens[num_seqs] are not written and may hold anything.
- *   workspace : at least 256 bytes, 16-byte aligned.
+ *   workspace : attn_fwd_latent_workspace_size(B, S, H, num_seqs) bytes, 16-byte
+ *   aligned.  Rows whose keys were split are joined by a second launch in a fixed order.
  * Errors as attn_fwd_gqa's. */
 ATTN_BWD_API attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, attn_strides_t skn,
                                            const void* kr, attn_strides_t skr, const void* v, attn_strides_t sv,

@@ -198,8 +198,10 @@ def test_cache_graphs_and_streams():
 
 @pytest.mark.parametrize("B,S,SKV,H,HKV,topk,name", [
     (1, 1, 1, 1, 1, 1, "bf16"), (1, 40, 300, 64, 1, 130, "bf16"), (2, 21, 90, 96, 3, 64, "f16"), (1, 9, 70, 48, 2, 65, "f16"),
-    (1, 170, 170, 16, 1, 7, "bf16"), (1, 5, 2000, 64, 1, 1111, "f16")])
-def test_lists(B, S, SKV, H, HKV, topk, name):
+    (1, 170, 170, 16, 1, 7, "bf16"), (1, 5, 2000, 64, 1, 1111, "f16"), (1, 1, 5000, 40, 1, 4097, "bf16"),
+    (3, 13, 400, 128, 2, 260, "f16"), (1, 76, 300, 20, 1, 140, "bf16")])
+@pytest.mark.parametrize("room", [True, False])
+def test_lists(B, S, SKV, H, HKV, topk, name, room):
     import torch
 
     import attention_backward_gb300 as ab
@@ -214,7 +216,7 @@ def test_lists(B, S, SKV, H, HKV, topk, name):
         idx[:, 2] = -1
         idx[:, 3, :, 1:] = -1
         idx[:, 4, :, : topk - 1] = -1
-    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((ab.sparse_forward_workspace_size(B, S, HKV) if room else 256,), 255, dtype=torch.uint8, device="cuda")
     out = (torch.full((B, S, H, 512), float("nan"), dtype=q.dtype, device="cuda"), torch.full((B, H, S), float("nan"), device="cuda"))
     o, lse = ab.sparse_forward(q, kv, i32(idx), workspace=ws, out=out)
     ab.check_error(ws)
@@ -271,7 +273,9 @@ def test_sparse_training_step():
     (1, 1, 1, 1, True, None, "bf16"), (1, 128, 128, 2, True, None, "f16"), (2, 300, 300, 3, True, None, "bf16"),
     (1, 257, 700, 2, True, None, "f16"), (1, 400, 130, 2, True, None, "bf16"), (2, 200, 450, 2, False, None, "f16"),
     (1, 1, 900, 4, True, None, "bf16"), (1, 700, 700, 2, True, (0, 1, 1, 130, 390, 640), "bf16"),
-    (1, 520, 520, 2, False, (0, 257, 513), "f16"), (3, 1000, 1000, 1, True, None, "f16")])
+    (1, 520, 520, 2, False, (0, 257, 513), "f16"), (3, 1000, 1000, 1, True, None, "f16"),
+    (1, 5, 20000, 1, True, None, "bf16"), (1, 900, 3500, 1, True, None, "f16"), (2, 40, 1100, 3, False, None, "bf16"),
+    (1, 2100, 2100, 1, True, (0, 3, 1800, 1801, 2099), "f16"), (1, 129, 129, 40, True, None, "bf16")])
 def test_expanded(B, S, Sk, H, causal, cu, name):
     import torch
 
@@ -284,7 +288,7 @@ def test_expanded(B, S, Sk, H, causal, cu, name):
     if cu is not None:  # rows of no sequence may hold anything
         for x in (q, up, kr):
             x[:, cu[-1]:] = float("nan")
-    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((ab.latent_workspace_size(B, S, H, 0 if cu is None else len(cu) - 1),), 255, dtype=torch.uint8, device="cuda")
     out = (torch.full((B, S, H, 128), float("nan"), dtype=q.dtype, device="cuda"), torch.full((B, H, S), float("nan"), device="cuda"))
     o, lse = ab.forward_latent(q, kn, kr, v, 192 ** -0.5, causal=causal, cu_seqlens=None if cu is None else i32(cu),
                                workspace=ws, out=out)

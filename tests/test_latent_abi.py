@@ -30,7 +30,8 @@ def ab():
 @pytest.mark.parametrize("header,names", [
     ("attn_rope.h", {"attn_rope"}),
     ("attn_latent.h", {"attn_latent_cache_write", "attn_fwd_latent_cache_workspace_size", "attn_fwd_latent_cache",
-                       "attn_fwd_sparse", "attn_fwd_latent"})])
+                       "attn_fwd_sparse", "attn_fwd_sparse_workspace_size", "attn_fwd_latent",
+                       "attn_fwd_latent_workspace_size"})])
 def test_declared_symbols_are_exported(ab, header, names):
     src = open(os.path.join(ROOT, "include", header)).read()
     assert set(re.findall(r"ATTN_BWD_API\s+[\w\s\*]+?\b(attn_\w+)\s*\(", src)) == names
@@ -206,12 +207,19 @@ def test_sparse_refusals(ab, kw, want):
     assert call(ab, "attn_fwd_sparse", sparse_args(ab), **kw) == want
 
 
+def test_sparse_workspace(ab):
+    assert ab.sparse_forward_workspace_size(1, 80, 1) == ab.sparse_forward_workspace_size(2, 3, 4) > 256
+    assert ab.sparse_forward_workspace_size(1, 81, 1) == ab.sparse_forward_workspace_size(2, 4096, 1) == 256
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1 << 31, 1, 1), (1, 1 << 31, 1)):
+        assert ab.sparse_forward_workspace_size(*bad) == 0
+
+
 def expanded_args(ab, **mask):
     S = ab._binding.Strides
     m = ab._binding.Mask(*{**dict(causal=1, window=-1, cu=None, n=0, kv_len=0), **mask}.values())
     return dict(q=A, sq=S(6144, 768, 192), kn=A, skn=S(8192, 1024, 256), kr=A, skr=S(512, 64, 64), v=A,
                 sv=S(8192, 1024, 256), B=1, S=8, H=4, dtype=0, scale=0.1, mask=ctypes.byref(m), o=A,
-                so=S(4096, 512, 128), lse=A, sl=S(32, 1, 8), ws=A, ws_bytes=256, stream=None)
+                so=S(4096, 512, 128), lse=A, sl=S(32, 1, 8), ws=A, ws_bytes=ab.latent_workspace_size(1, 8, 4), stream=None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -225,6 +233,15 @@ def expanded_args(ab, **mask):
     (dict(B=65536), UNSUPPORTED), (dict(ws_bytes=255), WORKSPACE)])
 def test_expanded_refusals(ab, kw, want):
     assert call(ab, "attn_fwd_latent", expanded_args(ab), **kw) == want
+
+
+def test_expanded_workspace(ab):
+    n = ab.latent_workspace_size(1, 8, 4)
+    assert n > 256 and call(ab, "attn_fwd_latent", expanded_args(ab), ws_bytes=n - 1) == WORKSPACE
+    assert ab.latent_workspace_size(1, 8192, 64) == 256 and ab.latent_workspace_size(1, 256, 1, 300) == 256
+    assert ab.latent_workspace_size(1, 256, 1, 3) == n
+    for bad in ((0, 8, 4, 0), (1, 0, 4, 0), (1, 8, 0, 0), (1, 8, 4, -1), (1, 8, 4, (1 << 20) + 1), (1, 1 << 31, 1, 0)):
+        assert ab.latent_workspace_size(*bad) == 0
 
 
 @pytest.mark.parametrize("mask,kw,want", [
