@@ -115,6 +115,8 @@ __device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p) {
   FwdUnit t{};
   t.valid = 0;
   if (u < 0) return t;  // the end-of-work marker
+  // (offsets that do not ascend may name more pairs than partial rows have room for)
+  if (p.splits > 1 && u >= kLatFwdMaxUnits) return t;
   t.index = u;
   const int part = u % p.splits;
   u /= p.splits;
