@@ -19,6 +19,7 @@ namespace {
 using namespace ab;
 
 constexpr int64_t kMax32 = int64_t(1) << 31;
+constexpr int64_t kRopeMaxHeads = 1 << 20;
 constexpr int64_t kMaxCount = kMax32 - 4096;  // rows and tokens are counted in 32 bits, up to a few tiles past the last
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -121,8 +122,10 @@ attn_status_t attn_rope(const attn_rope_tensor_t* q, const attn_rope_tensor_t* k
   if (const attn_status_t st = check_rope(q, rotary_dim); st != ATTN_OK) return st;
   if (k)
     if (const attn_status_t st = check_rope(k, rotary_dim); st != ATTN_OK) return st;
+  // (threads of a token are counted in 32 bits too)
+  if (q->H > kRopeMaxHeads || (k && k->H > kRopeMaxHeads) || B > kMaxCount) return ATTN_ERR_UNSUPPORTED;
   const int64_t heads = q->H + (k ? k->H : 0);
-  if (q->H >= kMax32 || heads >= kMax32 || B > kMaxCount || S > kMaxCount / B || heads > kMaxCount / (B * S))
+  if (heads > kRopeMaxHeads || S > kMaxCount / B || heads > kMaxCount / (B * S))
     return ATTN_ERR_UNSUPPORTED;
   if (!positions || !steps || !aligned(positions, 4) || !aligned(steps, 8)) return ATTN_ERR_INVALID_ARG;
   RopeParams p{};

@@ -42,7 +42,7 @@ typedef struct {
  *   steps : uint64 [rotary_dim / 2], device memory;  scale finite
  *   rotary_dim : a multiple of 16, at most 1024
  * S = 0 queues nothing.  Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED
- * (dtype, rotary_dim, D above 1024, B * S or B * S * H past 2^31), ATTN_ERR_LAUNCH. */
+ * (dtype, rotary_dim, D above 1024, B * S or B * S * H past 2^31, more than 2^20 heads), ATTN_ERR_LAUNCH. */
 ATTN_BWD_API attn_status_t attn_rope(const attn_rope_tensor_t* q, const attn_rope_tensor_t* k, int64_t B, int64_t S,
                                      attn_dtype_t dtype, const int32_t* positions, int64_t positions_b,
                                      const uint64_t* steps, int64_t rotary_dim, float scale, int32_t interleaved,

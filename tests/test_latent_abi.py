@@ -66,7 +66,8 @@ def rope_args(ab):
     (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(H=0), INVALID), (dict(D=0), INVALID), (dict(D=100), INVALID),
     (dict(start=-8), INVALID), (dict(start=4), INVALID), (dict(start=72), INVALID), (dict(D=56), INVALID),
     (dict(x=A + 8), INVALID), (dict(y=A + 2), INVALID), (dict(sx=(4096, 1024, 4)), INVALID),
-    (dict(sy=(4096, 0, 128)), INVALID), (dict(sy=(-8, 1024, 128)), INVALID), (dict(D=1032), UNSUPPORTED)])
+    (dict(sy=(4096, 0, 128)), INVALID), (dict(sy=(-8, 1024, 128)), INVALID), (dict(D=1032), UNSUPPORTED),
+    (dict(H=(1 << 20) + 1), UNSUPPORTED), (dict(H=2 ** 63 - 1), UNSUPPORTED)])
 def test_rope_bad_tensors(ab, kw, want):
     assert call(ab, "attn_rope", rope_args(ab), q=tensor(ab, **kw)) == want
     assert call(ab, "attn_rope", rope_args(ab), k=tensor(ab, **kw)) == want
