@@ -14,7 +14,7 @@
 //
 // so that a tile is read once from memory, serves as K (K-major) and as C^T
 // (M-major), and 512 columns of O fit tensor memory beside the scores: rows as M
-// would need all of it.  Few rows cost no more products than 64.
+// would need all of it.  (Fewer rows take the products of 64.)
 //
 // Softmax: eight warps, a quarter of the keys and half of the rows each; the scores
 // arrive as fragments (a thread: 2 keys, 8 rows).  A row's reference m is kept until a
@@ -38,7 +38,6 @@
 // of the scores, 14 the walk, a unit ahead of the others, 15 issue of O.  Every wait is
 // bounded.
 #include <cmath>
-#include <type_traits>
 
 #include "cvt.cuh"
 #include "kv_launch.h"

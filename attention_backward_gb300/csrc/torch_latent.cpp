@@ -302,7 +302,8 @@ std::tuple<Tensor, Tensor> forward_latent(const Tensor& q, const Tensor& k_nope,
   shaped("k_nope", k_nope, {B, Sk, H, kNope}), shaped("v", v, {B, Sk, H, kValue});
   shaped("k_rope", k_rope, {B, Sk, kRot});
   TORCH_CHECK(k_rope.stride(2) == 1, "k_rope must have contiguous rows");
-  TORCH_CHECK(Sk <= 0x7fffffff, "too many keys");
+  // (a key length of 0 would stand for S)
+  TORCH_CHECK(Sk >= 1 && Sk <= 0x7fffffff, "k_nope must hold between 1 and 2^31 - 1 keys");
   attn_mask_t mask{causal, -1, nullptr, 0, Sk != S ? static_cast<int32_t>(Sk) : 0};
   if (cu_seqlens.has_value()) {
     on(q, "cu_seqlens", *cu_seqlens);

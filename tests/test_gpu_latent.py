@@ -298,6 +298,25 @@ def test_expanded(B, S, Sk, H, causal, cu, name):
         assert o[:, cu[-1]:].isnan().all() and lse[:, :, cu[-1]:].isnan().all()
 
 
+def test_expanded_offsets_that_do_not_ascend():
+    """A sequence named twice has more pairs of query tiles than the call's rows: with
+    keys in parts, no partial row is written past the workspace, and rows that were
+    computed hold what the sequence alone gives."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(22)
+    q, kn, kr, v = (rounded(rng, s, "bf16") for s in ((1, 8192, 1, 192), (1, 8192, 1, 128), (1, 8192, 64), (1, 8192, 1, 128)))
+    want = ab.forward_latent(q, kn, kr, v, 0.1, cu_seqlens=i32([0, 8192, 8192, 8192]))
+    need = ab.latent_workspace_size(1, 8192, 1, 3)
+    ws = torch.full((need + (1 << 26),), 255, dtype=torch.uint8, device="cuda")
+    got = ab.forward_latent(q, kn, kr, v, 0.1, cu_seqlens=i32([0, 8192, 0, 8192]), workspace=ws)
+    ab.check_error(ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (ws[need:] == 255).all()
+
+
 def test_expanded_sequences_do_not_touch_each_other():
     import torch
 
@@ -405,6 +424,8 @@ def test_binding_refusals():
         lambda: ab.forward_latent(q, kn, kr, v, 0.1), lambda: ab.forward_latent(qe, kn[:, :2], kr, v, 0.1),
         lambda: ab.forward_latent(qe, kn, kr[..., :32], v, 0.1), lambda: ab.forward_latent(qe, kn, kr, v.bfloat16(), 0.1),
         lambda: ab.forward_latent(qe, kn, kr, v, 0.1, cu_seqlens=cu.long()), lambda: ab.forward_latent(qe, kn, kr, v, 0.1, cu_seqlens=cu[:1]),
+        lambda: ab.forward_latent(qe, kn[:, :0], kr[:, :0], v[:, :0], 0.1), lambda: ab.sparse_forward(q, rows[:, :0], idx),
+        lambda: ab.sparse_forward(q, rows, idx[..., :0]), lambda: ab.forward_latent(qe[:, :0], kn, kr, v, 0.1),
         lambda: ab.forward_latent(qe, kn, kr, v, -1.0), lambda: ab.forward_latent(qe, kn, kr, v, 0.1, out=(qe, kr)),
     ]
     for i, f in enumerate(bad):
@@ -414,3 +435,100 @@ def test_binding_refusals():
             continue
         raise AssertionError(f"call {i} was not refused")
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("form", ["whole lists", "lists in parts", "expanded", "expanded in parts"])
+def test_prompt_graphs_streams_and_bits(form):
+    """A captured call replays on other inputs; calls on two streams with workspaces of
+    their own, and repeated ones, give the same bits."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(41)
+    if "lists" in form:
+        S = 3 if "parts" in form else 90
+        x = [rounded(rng, (1, S, 64, 576), "bf16"), rounded(rng, (1, 900, 1, 576), "bf16")]
+        idx = rng.integers(-1, 900, (1, S, 1, 700))
+        call = lambda **k: ab.sparse_forward(*x, i, 0.05, **k)  # noqa: E731
+        ref = lambda: oracle.list_forward(f64(x[0]), f64(x[1]), idx, 0.05)  # noqa: E731
+        need, i = ab.sparse_forward_workspace_size(1, S, 1), i32(idx)
+        assert (need > 256) == ("parts" in form)
+    else:
+        S = 300 if "parts" in form else 700
+        Sk = 2000 if "parts" in form else 700
+        x = [rounded(rng, s, "bf16") for s in ((1, S, 2, 192), (1, Sk, 2, 128), (1, Sk, 64), (1, Sk, 2, 128))]
+        call = lambda **k: ab.forward_latent(*x, 0.07, **k)  # noqa: E731
+        ref = lambda: oracle.expanded_forward(*(f64(t) for t in x), 0.07)  # noqa: E731
+        need = ab.latent_workspace_size(1, S, 2)
+    ws = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = [tuple(torch.empty_like(t) for t in call()) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(workspace=ws[0], out=out[0])
+    for t in x:
+        t.copy_(t.flip(1).clone() * 0.75)
+    for _ in range(3):
+        graph.replay()
+    ab.check_error(ws[0])
+    near(out[0][0], out[0][1].transpose(1, 2), ref(), "bf16")
+    want = [t.clone() for t in out[0]]
+    torch.cuda.synchronize()
+    st = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(8):
+        for k in range(2):
+            call(workspace=ws[k], out=out[k], stream=st[k])
+            with torch.cuda.stream(st[k]):
+                assert all(t.shape == w.shape for t, w in zip(call(), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in out for a, b in zip(o, want))
+
+
+def test_rows_past_32_bits():
+    """Cached rows, lists, queries and results whose elements lie past 2^31 and 2^32."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(43)
+    nb, page, name = 60000, 128, "bf16"  # 4.4e9 elements
+    cache = torch.empty(nb, page, 576, dtype=torch.bfloat16, device="cuda")
+    table = np.array([[nb - 1, 0, 58254, 30000, 29999]])  # (58254 holds element 2^32)
+    kv, new, H = 600, 5, 16
+    cache[torch.from_numpy(table[0]).cuda()] = rounded(rng, (5, page, 576), name)
+    written = rounded(rng, (1, 2, 576), name)
+    slots = [(nb - 1) * page + 7, 58254 * page + 30]
+    ab.latent_cache_write(written, i32(slots), cache)
+    assert torch.equal(cache.view(-1, 576)[torch.tensor(slots).cuda()], written[0])
+    q = rounded(rng, (1, new, H, 576), name)
+    r = oracle.cache_forward(f64(q)[0], f64(cache[torch.from_numpy(table[0]).cuda()]), np.arange(5)[None], [0, new], [kv], 0.1)
+    # queries and results far apart: tokens 2^30 + 8 elements from one another
+    far = (1 << 30) + 8
+    wide = torch.empty(4 * far + H * 576, dtype=torch.bfloat16, device="cuda")
+    qf, of = wide.as_strided((1, new, H, 576), (8, far, 576, 1)), torch.empty_like(wide).as_strided((1, new, H, 512), (8, far, 512, 1))
+    qf.copy_(q)
+    lse = torch.empty(1, H, new, device="cuda")
+    ab.forward_latent_cache(qf, cache, i32(table), i32([0, new]), i32([kv]), 0.1, out=(of, lse))
+    near(of[0], lse[0].t(), r, name)
+    rows = cache.view(1, nb * page, 1, 576)
+    pick = table[0][rng.integers(0, 5, (new, 200))] * page + rng.integers(0, page, (new, 200))
+    ab.sparse_forward(qf, rows, i32(pick[None, :, None]), 0.1, out=(of, lse))
+    used, where = np.unique(pick, return_inverse=True)
+    r = oracle.list_forward(f64(q), f64(rows[:, torch.from_numpy(used).cuda()]), where.reshape(1, new, 1, 200), 0.1)
+    near(of, lse.transpose(1, 2), r, name)
+    del cache, rows
+    x, pos, t64 = qf[..., :192], i32(np.arange(new) * 1000), ab.rope_table(64)
+    want, _ = ab.rope(q[..., :192].contiguous(), pos, t64, start=128)
+    ab.rope(x, pos, t64, start=128, out=(x, None))
+    assert torch.equal(x.contiguous(), want)
+    up = wide.as_strided((1, new, H, 256), (8, far, 256, 1))
+    up[..., 192:] = 1.0
+    qe, kr = rounded(rng, (1, new, H, 192), name), rounded(rng, (1, new, 64), name)
+    got = ab.forward_latent(qe, up[..., :128], kr, up[..., 128:], 0.1, out=(of[..., :128], lse))
+    alone = ab.forward_latent(qe, up[..., :128].contiguous(), kr, up[..., 128:].contiguous(), 0.1)
+    assert torch.equal(got[0].contiguous(), alone[0]) and torch.equal(got[1], alone[1])
+
+
+def test_cache_long_prompt():
+    """Many 64-row tiles of one request, two CTAs on the same keys, beside one of few rows."""
+    check_cache(cache_problem([2100, 900], [1500, 1], 12, 128, "f16", 17), "f16")
