@@ -54,7 +54,7 @@ def _torch_flags(cc: str) -> tuple:
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"), os.path.join(ROOT, "include")]
     return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
              *(f"-I{i}" for i in include)],
-            [f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch"])
+            [f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch"])
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
