@@ -72,7 +72,7 @@ cudaError_t launch_latent_lists(const LatParams& p, const CUtensorMap& q, bool b
 // Joins rows that were split over CTAs and, of the cache (group > 0), writes the call's error word.
 cudaError_t launch_latent_join(const LatParams& p, bool bf16, int group, int ctas, int sms, cudaStream_t st);
 
-// The expanded form: most units of a call that splits its keys, and their rows.
+// The expanded form: most parts of pairs of query tiles, and their rows.
 constexpr int kLatFwdMaxUnits = 160;
 constexpr int kLatFwdRows = 256;
 struct LatFwdParams {
@@ -88,14 +88,15 @@ struct LatFwdParams {
   int* err;
   int* unit_counter;
   uint64_t timeout_ns;
-  int splits;       // units a pair of query tiles, of a share of its key blocks each
-  float2* part_ml;  // splits > 1: [pairs * splits][256 rows] reference (log2 units) and sum
-  float* part_o;    // [pairs * splits][256 rows][128]
+  int whole;        // pairs of query tiles that are a unit each (2^31 - 1: all)
+  int splits;       // units of each further pair, of a share of its key blocks each
+  float2* part_ml;  // [parts][256 rows] reference (log2 units) and sum
+  float* part_o;    // [parts][256 rows][128]
 };
 struct LatFwdMaps {
   CUtensorMap q, kn, kr, v;  // box 64 columns x 128 rows of one head
 };
-// ``pairs``: at least the pairs of query tiles of the call.
-cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int pairs, int grid, cudaStream_t st);
+// ``split_pairs``: at least the pairs of query tiles from p.whole on, 0 where none is split.
+cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int split_pairs, int grid, cudaStream_t st);
 
 }  // namespace ab

@@ -281,7 +281,7 @@ attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, 
 size_t attn_fwd_latent_workspace_size(int64_t B, int64_t S, int64_t H, int64_t num_seqs) {
   if (B < 1 || S < 1 || H < 1 || num_seqs < 0 || num_seqs > (1 << 20) || B > 65535 || H > 65535 || S > kMaxCount / (B * H))
     return 0;
-  const int64_t parts = 2 * fwd_pairs(B, S, H, num_seqs) <= kLatFwdMaxUnits ? kLatFwdMaxUnits * kLatFwdRows : 0;
+  const int64_t parts = num_seqs == 0 || 2 * fwd_pairs(B, S, H, num_seqs) <= kLatFwdMaxUnits ? kLatFwdMaxUnits * kLatFwdRows : 0;
   return static_cast<size_t>(kHeaderBytes + parts * (8 + 128 * 4));
 }
 
@@ -332,18 +332,28 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
   p.timeout_ns = kWaitTimeoutNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int sms = imin(sm_count(), kLatFwdMaxUnits);
-  // Pairs that leave CTAs idle are split over them, two key blocks a part at least, from 1024
-  // keys on: 8 queries on 8192 keys, one head 164 -> 25 us, 300 on 4000, 8 heads 86 -> 29,
-  // 1024 on 1024, 8 heads 27 -> 22.5; 512 on 512, 16 heads 18 -> 21.
-  p.splits = Sk < 1024 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min(sms / pairs, (Sk + 255) / 256)));
-  if (p.splits > 1) {
+  // Pairs that leave CTAs idle, those of the last round over the CTAs, are split over them,
+  // two key blocks a part at least, where one sees 1024 keys (2048 behind whole rounds): 8
+  // queries on 8192 keys, one head 164 -> 25 us, 300 on 4000, 8 heads 86 -> 29, 1024 on
+  // 1024, 8 heads 27 -> 22.5, 2048 on 8192, 64 heads 478 -> 442; 512 on 512, 16 heads 18 ->
+  // 21, 8192 on 8192, 16 heads, whose last pairs see 1024, 255 -> 270.  (Of a packed batch
+  // the host has only a bound of the pairs.)
+  p.splits = 1, p.whole = 0x7fffffff;
+  const int64_t last = p.cu_seqlens ? (pairs < sms ? pairs : 0) : pairs % sms;
+  if (last > 0) {
+    const int64_t rows = (last + B * H - 1) / (B * H) * kLatFwdRows;
+    const int64_t keys = p.causal && !p.cu_seqlens ? std::min(Sk, std::max<int64_t>(0, Sk - S + rows)) : Sk;
+    p.splits = keys < (pairs < sms ? 1024 : 2048) ? 1 : static_cast<int>(std::min(sms / last, (keys + 255) / 256));
+  }
+  const int64_t split = p.splits > 1 ? last : 0, units = pairs - split + split * p.splits;
+  if (split > 0) {
+    p.whole = static_cast<int>(pairs - split);
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
     p.part_o = reinterpret_cast<float*>(p.part_ml + kLatFwdMaxUnits * kLatFwdRows);
   }
-  const int64_t units = pairs * p.splits;
   // the error word and the unit counter start clear
   if (cudaMemsetAsync(workspace, 0, kHeaderBytes, st) != cudaSuccess) return ATTN_ERR_LAUNCH;
-  return launch_status(launch_latent_fwd(p, m, dtype == ATTN_DT_BF16, static_cast<int>(pairs),
+  return launch_status(launch_latent_fwd(p, m, dtype == ATTN_DT_BF16, static_cast<int>(split),
                                          static_cast<int>(units < sms ? units : sms), st));
 }
 

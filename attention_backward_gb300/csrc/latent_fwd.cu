@@ -9,8 +9,9 @@
 // shared keys are read where they lie, as the third 64-column slab of every head's K,
 // so that no [S, H, 192] keys are ever written.
 //
-// Calls of few pairs of tiles split their key blocks over the CTAs; f32 partials go to the
-// workspace, and a second launch joins them in order.
+// The pairs of tiles of the last, unfinished round of CTAs (all, where they are few) split
+// their key blocks over the CTAs; f32 partials go to the workspace, and a second launch
+// joins them in order.
 //
 // Two Q tiles of 192 columns leave room for 8 slabs of 128 keys x 64 columns: K
 // and V come through a ring of slabs (three of K_j, two of V_j, ...), each loaded
@@ -109,17 +110,18 @@ __device__ __forceinline__ void key_block_range(int q0, int qlen, int klen, int 
 // Unit u of the launch, longest first under a causal mask (the last query
 // tiles of a row see the most keys): dense rows go through the tile pairs
 // from the last, each over all (batch, head) pairs; packed sequences one after
-// another, each the same way over its heads.  Each pair of tiles is p.splits units in
-// a row, of an even share of its key blocks each.
+// another, each the same way over its heads.  The pairs from p.whole on are p.splits
+// units each, of an even share of their key blocks.
 __device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p) {
   FwdUnit t{};
   t.valid = 0;
   if (u < 0) return t;  // the end-of-work marker
-  // (offsets that do not ascend may name more pairs than partial rows have room for)
-  if (p.splits > 1 && u >= kLatFwdMaxUnits) return t;
   t.index = u;
-  const int part = u % p.splits;
-  u /= p.splits;
+  // my slot of partial rows; offsets that do not ascend may name more pairs than there are
+  const int slot = u - p.whole;
+  if (slot >= kLatFwdMaxUnits) return t;
+  const int parts = slot >= 0 ? p.splits : 1, part = slot >= 0 ? slot % p.splits : 0;
+  u = slot >= 0 ? p.whole + slot / p.splits : u;
   int pair = 0;
   if (p.cu_seqlens == nullptr) {
     const int np = (p.S + 2 * BQ - 1) / (2 * BQ);
@@ -157,8 +159,8 @@ __device__ __forceinline__ FwdUnit decode_unit(int u, const LatFwdParams& p) {
     key_block_range(t.q0 + w * BQ, t.qlen, t.klen, t.off, p.causal, &t.lo[w], &t.hi[w]);
   if (p.splits > 1) {
     const int n = imax(t.hi[0], t.hi[1]);  // (no window: the blocks of both tiles begin at 0)
-    const int a = static_cast<int>(static_cast<int64_t>(n) * part / p.splits);
-    const int e = static_cast<int>(static_cast<int64_t>(n) * (part + 1) / p.splits);
+    const int a = static_cast<int>(static_cast<int64_t>(n) * part / parts);
+    const int e = static_cast<int>(static_cast<int64_t>(n) * (part + 1) / parts);
     for (int w = 0; w < 2; ++w) {
       t.lo[w] = imax(t.lo[w], a), t.hi[w] = imin(t.hi[w], e);
       if (t.hi[w] <= t.lo[w]) t.lo[w] = t.hi[w] = 0;
@@ -589,9 +591,9 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const bool live = q < u.qlen;
     const int64_t pos = u.seq_start + q;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t part_row = static_cast<int64_t>(u.index) * 2 * BQ + w * BQ + row;  // of a split unit
+    const int64_t part_row = static_cast<int64_t>(u.index - p.whole) * 2 * BQ + w * BQ + row;  // of a part
     if (live) {
-      if (p.splits > 1) {
+      if (u.index >= p.whole) {
         p.part_ml[part_row] = make_float2(m_used, l);
       } else {
         p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] =
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 32; ++e) r[e] = 0u;
       }
-      if (live && p.splits > 1) {
+      if (live && u.index >= p.whole) {
         if (l != 0.f) {  // (a part that saw no key of the row says nothing)
           float4* const dst = reinterpret_cast<float4*>(p.part_o + part_row * D + ch * 32);
 #pragma unroll
@@ -642,12 +644,12 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
 // Joins the parts of split units: a warp a row, 4 columns a lane, the parts in order.
 constexpr int JOIN_WARPS = 8;
 template <bool BF16>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) latent_fwd_join_kernel(const LatFwdParams p, int pairs) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) latent_fwd_join_kernel(const LatFwdParams p, int pairs) {  // of the split pairs
   grid_dependency_wait();
   grid_dependents_launch();
   const int lane = threadIdx.x & 31, w = blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5), pair = w / (2 * BQ), row = w % (2 * BQ);
   if (pair >= pairs) return;
-  const FwdUnit u = decode_unit(pair * p.splits, p);
+  const FwdUnit u = decode_unit(p.whole + pair * p.splits, p);
   const int q = u.q0 + row;
   if (!u.valid || q >= u.qlen) return;
   const int64_t first = static_cast<int64_t>(pair) * p.splits * 2 * BQ + row;
@@ -685,19 +687,21 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) latent_fwd_join_kernel(const 
 }
 
 template <bool BF16>
-cudaError_t launch_t(const LatFwdParams& p, const LatFwdMaps& m, int pairs, int grid, cudaStream_t st) {
+cudaError_t launch_t(const LatFwdParams& p, const LatFwdMaps& m, int split_pairs, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = latent_fwd_kernel<BF16>;
   if (const cudaError_t e = allow_smem_once(kern, SMEM, &done); e != cudaSuccess) return e;
   kern<<<grid, THREADS, SMEM, st>>>(m, p);
-  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess || p.splits == 1) return e;
-  return launch_chained(latent_fwd_join_kernel<BF16>, dim3(pairs * (2 * BQ / JOIN_WARPS)), JOIN_WARPS * 32, 0, st, p, pairs);
+  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess || split_pairs == 0) return e;
+  return launch_chained(latent_fwd_join_kernel<BF16>, dim3(split_pairs * (2 * BQ / JOIN_WARPS)), JOIN_WARPS * 32, 0,
+                        st, p, split_pairs);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int pairs, int grid, cudaStream_t st) {
-  return bf16 ? launch_t<true>(p, m, pairs, grid, st) : launch_t<false>(p, m, pairs, grid, st);
+cudaError_t launch_latent_fwd(const LatFwdParams& p, const LatFwdMaps& m, bool bf16, int split_pairs, int grid,
+                              cudaStream_t st) {
+  return bf16 ? launch_t<true>(p, m, split_pairs, grid, st) : launch_t<false>(p, m, split_pairs, grid, st);
 }
 
 }  // namespace ab

@@ -275,7 +275,8 @@ def test_sparse_training_step():
     (1, 1, 900, 4, True, None, "bf16"), (1, 700, 700, 2, True, (0, 1, 1, 130, 390, 640), "bf16"),
     (1, 520, 520, 2, False, (0, 257, 513), "f16"), (3, 1000, 1000, 1, True, None, "f16"),
     (1, 5, 20000, 1, True, None, "bf16"), (1, 900, 3500, 1, True, None, "f16"), (2, 40, 1100, 3, False, None, "bf16"),
-    (1, 2100, 2100, 1, True, (0, 3, 1800, 1801, 2099), "f16"), (1, 129, 129, 40, True, None, "bf16")])
+    (1, 2100, 2100, 1, True, (0, 3, 1800, 1801, 2099), "f16"), (1, 129, 129, 40, True, None, "bf16"),
+    (1, 300, 1500, 80, True, None, "f16"), (2, 260, 1100, 40, False, None, "bf16")])
 def test_expanded(B, S, Sk, H, causal, cu, name):
     import torch
 

@@ -239,7 +239,7 @@ def test_expanded_refusals(ab, kw, want):
 def test_expanded_workspace(ab):
     n = ab.latent_workspace_size(1, 8, 4)
     assert n > 256 and call(ab, "attn_fwd_latent", expanded_args(ab), ws_bytes=n - 1) == WORKSPACE
-    assert ab.latent_workspace_size(1, 8192, 64) == 256 and ab.latent_workspace_size(1, 256, 1, 300) == 256
+    assert ab.latent_workspace_size(1, 8192, 64) == n and ab.latent_workspace_size(1, 256, 1, 300) == 256
     assert ab.latent_workspace_size(1, 256, 1, 3) == n
     for bad in ((0, 8, 4, 0), (1, 0, 4, 0), (1, 8, 0, 0), (1, 8, 4, -1), (1, 8, 4, (1 << 20) + 1), (1, 1 << 31, 1, 0)):
         assert ab.latent_workspace_size(*bad) == 0
