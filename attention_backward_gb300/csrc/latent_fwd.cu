@@ -66,18 +66,24 @@ constexpr int SMEM = OFF_MISC + 64;
 static_assert(SMEM <= 227 * 1024, "shared memory budget");
 constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + D;
 
+// Where slab i of the ring lies.
+__device__ __forceinline__ uint32_t slab_at(uint32_t i) { return OFF_R + i % RING * SLAB; }
+
 enum FwdBar : int {
   Q_FULL = 0,
   Q_EMPTY,            // every S MMA of both tiles of the unit has completed: the Q tiles may be reloaded
-  FULL0,              // ring slabs
-  EMPTY0 = FULL0 + RING,  // both tiles' products of it have completed
-  S_FULL0 = EMPTY0 + RING,    // per tile
+  K_FULL0,                    // K of every other block
+  V_FULL0 = K_FULL0 + 2,      // and V
+  K_EMPTY0 = V_FULL0 + 2,     // both tiles' products of it have completed
+  V_EMPTY0 = K_EMPTY0 + 2,
+  S_FULL0 = V_EMPTY0 + 2,     // per tile
   P_READY0 = S_FULL0 + 2,     // per tile and half of the keys: 4 softmax warps stored P
   O_DONE0 = P_READY0 + 4,     // per tile: the tile's P V MMAs issued so far completed
   O_FREE0 = O_DONE0 + 2,      // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,   // 2 ring slots: the producer published a unit index
   UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 ring slots: the 2 issuing and the 8 softmax warps read it
-  TAIL = UNIT_EMPTY0 + 2,
+  TURN0 = UNIT_EMPTY0 + 2,  // per tile: the other one has issued its scores
+  TAIL = TURN0 + 2,
   DRAIN0,  // of the issuing warps
   NUM_FWD_BARS = DRAIN0 + 2
 };
@@ -208,7 +214,6 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + OFF_MISC + 8);
   volatile int* ring = reinterpret_cast<volatile int*>(sm + OFF_MISC + 16);  // 2 unit indices
-  int* const turn_taken = reinterpret_cast<int*>(sm + OFF_MISC + 32);  // of the issuing warps
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if ((smem_u32(sm) & 1023u) != 0) {  // the swizzled tiles need an aligned base
@@ -219,14 +224,14 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    *turn_taken = 0;
     mbar_init(&bars[Q_FULL], 1);
     mbar_init(&bars[Q_EMPTY], 2);
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(&bars[FULL0 + i], 1);
-      mbar_init(&bars[EMPTY0 + i], 2);
-    }
     for (int w = 0; w < 2; ++w) {
+      mbar_init(&bars[K_FULL0 + w], 1);
+      mbar_init(&bars[V_FULL0 + w], 1);
+      mbar_init(&bars[K_EMPTY0 + w], 2);
+      mbar_init(&bars[V_EMPTY0 + w], 2);
+      mbar_init(&bars[TURN0 + w], 1);
       mbar_init(&bars[S_FULL0 + w], 1);
       mbar_init(&bars[P_READY0 + 2 * w], 4);
       mbar_init(&bars[P_READY0 + 2 * w + 1], 4);
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     if (warp == 8) {
       // ============================================================ producer
       int q_pend = -1, tail_pend = -1;
-      uint32_t qc = 0, rc = 0, tail_ph = 0;  // rc: ring slabs so far
+      uint32_t qc = 0, kc = 0, vc = 0, tail_ph = 0;  // blocks so far
       bool ok = true;
       for (uint32_t uc = 0; ok; ++uc) {
         const uint32_t slot = uc & 1;
@@ -314,38 +319,47 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         ++qc;
         for (int j = sp.J0; j < sp.J1 && ok; ++j) {
           const int pos = u.seq_start + j * BK;
+          // slabs 5 kc to 5 kc + 2, behind a slab of K and both of V of two blocks ago
+          if (kc >= 2 && !(ok = mbar_wait_warp(&bars[V_EMPTY0 + (kc & 1)], ((kc >> 1) - 1) & 1, wc, kErrWaitStageEmpty))) break;
+          if (lane == 0) {
+            uint64_t* const bar = &bars[K_FULL0 + (kc & 1)];
+            mbar_arrive_expect_tx(bar, KSLABS * SLAB);
+#pragma unroll
+            for (int s = 0; s < KSLABS; ++s)
+              tma_load_4d(sm + slab_at(BSLABS * kc + s), s < KSLABS - 1 ? &maps.kn : &maps.kr, bar,
+                          s < KSLABS - 1 ? s * 64 : 0, s < KSLABS - 1 ? u.h : 0, pos, u.b);
+          }
+          ++kc;
+          // the two behind them, where two slabs of the last K were
+          if (vc >= 1 && !(ok = mbar_wait_warp(&bars[K_EMPTY0 + ((vc - 1) & 1)], ((vc - 1) >> 1) & 1, wc, kErrWaitStageEmpty))) break;
           // rows of the block behind the sequence's end (a dense row's read zeros)
           const int r0 = imin(u.klen - j * BK, BK), r1 = p.cu_seqlens ? imin(p.S - pos, BK) : 0;
-          for (int s = 0; s < BSLABS; ++s, ++rc) {
-            const uint32_t slab = rc % RING, n = rc / RING;
-            if (n >= 1 && !(ok = mbar_wait_warp(&bars[EMPTY0 + slab], (n - 1) & 1, wc, kErrWaitStageEmpty))) break;
-            uint8_t* const dst = sm + OFF_R + slab * SLAB;
-            const bool tail = s >= KSLABS && r0 < r1;
-            uint64_t* const bar = &bars[tail ? static_cast<uint32_t>(TAIL) : FULL0 + slab];
-            if (lane == 0) {
-              mbar_arrive_expect_tx(bar, SLAB);
-              if (s < KSLABS - 1) tma_load_4d(dst, &maps.kn, bar, s * 64, u.h, pos, u.b);
-              else if (s < KSLABS) tma_load_4d(dst, &maps.kr, bar, 0, 0, pos, u.b);
-              else tma_load_4d(dst, &maps.v, bar, (s - KSLABS) * 64, u.h, pos, u.b);
-            }
-            if (tail) {
-              // loaded onto the producer's own barrier, the rows zeroed, then published
-              tail_pend = tail_ph & 1;
-              if (!(ok = mbar_wait_warp(&bars[TAIL], tail_ph & 1, wc, kErrWaitTail))) break;
-              tail_pend = -1;
-              ++tail_ph;
-              zero_tile_rows(dst, 1, SLAB, r0, r1, lane);
-              if (lane == 0) mbar_arrive(&bars[FULL0 + slab]);
-            }
+          const bool tail = r0 < r1;
+          const uint32_t s0 = BSLABS * vc + KSLABS;
+          if (lane == 0) {
+            uint64_t* const bar = &bars[tail ? static_cast<uint32_t>(TAIL) : V_FULL0 + (vc & 1)];
+            mbar_arrive_expect_tx(bar, VSLABS * SLAB);
+#pragma unroll
+            for (int s = 0; s < VSLABS; ++s) tma_load_4d(sm + slab_at(s0 + s), &maps.v, bar, s * 64, u.h, pos, u.b);
           }
+          if (tail) {
+            // loaded onto the producer's own barrier, the rows zeroed, then published
+            tail_pend = tail_ph & 1;
+            if (!(ok = mbar_wait_warp(&bars[TAIL], tail_ph & 1, wc, kErrWaitTail))) break;
+            tail_pend = -1;
+            ++tail_ph;
+            for (int s = 0; s < VSLABS; ++s) zero_tile_rows(sm + slab_at(s0 + s), 1, SLAB, r0, r1, lane);
+            if (lane == 0) mbar_arrive(&bars[V_FULL0 + (vc & 1)]);
+          }
+          ++vc;
         }
       }
-      // loads still in flight land before the CTA exits: the last Q and the last slabs'
+      // loads still in flight land before the CTA exits: the last Q and the last blocks'
       if (lane == 0) {
         if (q_pend >= 0) mbar_drain(&bars[Q_FULL], q_pend);
         if (tail_pend >= 0) mbar_drain(&bars[TAIL], tail_pend);
-        for (uint32_t i = rc > static_cast<uint32_t>(RING) ? rc - RING : 0u; i < rc; ++i)
-          mbar_drain(&bars[FULL0 + i % RING], (i / RING) & 1);
+        for (uint32_t i = kc > 2u ? kc - 2 : 0u; i < kc; ++i) mbar_drain(&bars[K_FULL0 + (i & 1)], (i >> 1) & 1);
+        for (uint32_t i = vc > 2u ? vc - 2 : 0u; i < vc; ++i) mbar_drain(&bars[V_FULL0 + (i & 1)], (i >> 1) & 1);
       }
       __syncwarp();
     } else if (warp < 11) {
@@ -360,52 +374,40 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
       const uint64_t r_mn = sdesc_sw128(smem_u32(sm) + OFF_R, SLAB, 1024);
       const uint32_t ts = tmem + T_S0 + (T_S1 - T_S0) * w, to = tmem + T_O0 + (T_O1 - T_O0) * w;
       const uint32_t one = elect_lane();
-      uint32_t qc = 0, rc = 0, npv = 0, oc = 0;  // units, ring slabs, blocks and units of my tile so far
+      uint32_t qc = 0, bc = 0, npv = 0, oc = 0;  // units, blocks, blocks and units of my tile so far
       bool ok = true;
-      auto wait_slab = [&](uint32_t i) { return mbar_wait_warp(&bars[FULL0 + i % RING], (i / RING) & 1, wc, kErrWaitKV); };
-      // slabs [i, i + n): waited for, and handed back without use
-      auto skip = [&](uint32_t i, int n) -> bool {
-        for (int s = 0; s < n; ++s, ++i) {
-          if (!wait_slab(i)) return false;
-          if (lane == 0) mbar_arrive(&bars[EMPTY0 + i % RING]);
-        }
-        return true;
+      auto wait_k = [&](uint32_t b) { return mbar_wait_warp(&bars[K_FULL0 + (b & 1)], (b >> 1) & 1, wc, kErrWaitKV); };
+      // Block b's turn of my tile at the scores: tile 0's, then tile 1's, each issued in one
+      // go: one's softmax then runs while the other's products do.  (Side by side, both
+      // tiles' S end at the same time, and both softmaxes run with the tensor core idle.)
+      auto turn = [&](uint32_t b) {
+        if (w == 0 && b == 0) return true;
+        const uint32_t n = w ? b : b - 1;
+        return mbar_wait_warp(&bars[TURN0 + w], n & 1, wc, kErrWaitTile);
       };
-      auto wait_k = [&](uint32_t i) { return wait_slab(i) && wait_slab(i + 1) && wait_slab(i + 2); };
-      // S of the block whose K starts at slab i
-      auto scores = [&](uint32_t i) {
+      auto pass = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[TURN0 + 1 - w]);
+      };
+      // S of block b, whose K is there
+      auto scores = [&](uint32_t b) {
+        tc_fence_after();
 #pragma unroll 1
-        for (int s = 0; s < KSLABS; ++s, ++i) {
-          const uint64_t q = q_kmaj + sdesc_step(SLAB) * s, k = r_kmaj + sdesc_step(SLAB) * (i % RING);
+        for (int s = 0; s < KSLABS; ++s) {
+          const uint64_t q = q_kmaj + sdesc_step(SLAB) * s, k = r_kmaj + sdesc_step(SLAB) * ((BSLABS * b + s) % RING);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_ss_e(ts, q + sdesc_step(kk * 32), k + sdesc_step(kk * 32), IDESC_S, s + kk > 0, one);
-          mma_commit_w(&bars[EMPTY0 + i % RING]);
         }
         mma_commit_w(&bars[S_FULL0 + w]);
+        pass();
+        mma_commit_w(&bars[K_EMPTY0 + (b & 1)]);
       };
-      // The tiles take turns at S, which is issued in one go: one's softmax then runs while
-      // the other's products do.  (Side by side, both tiles' S end at the same time, and
-      // both softmaxes run with the tensor core idle.)  Bounded as mbar_wait is.
-      auto turn = [&]() -> bool {
-        bool got = false;
-        uint64_t since = 0;
-        for (uint32_t i = 1; !got; ++i) {
-          if (lane == 0) got = atomicCAS(turn_taken, 0, 1) == 0;
-          got = __any_sync(0xffffffffu, got);
-          if (!got && (i & 255) == 0) {
-            const uint64_t now = global_ns();
-            if (i == 256) since = now;
-            const bool late = now - since > wc.timeout_ns;
-            if (late) raise_error(wc, kErrWaitTile);
-            if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
-          }
-        }
-        tc_fence_after();
+      // block b goes without my tile
+      auto skip_k = [&](uint32_t b) -> bool {
+        if (!wait_k(b) || !turn(b)) return false;
+        pass();
+        if (lane == 0) mbar_arrive(&bars[K_EMPTY0 + (b & 1)]);
         return true;
-      };
-      auto done = [&]() {
-        __syncwarp();
-        if (lane == 0) atomicExch(turn_taken, 0);
       };
       for (uint32_t uc = 0; ok; ++uc) {
         const FwdUnit u = next_unit(uc, &ok);
@@ -416,21 +418,22 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         auto in = [&](int j) { return lo <= j && j < hi; };
         if (!(ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
         ++qc;
-        // a tile's O accumulator: its softmax warps have read the previous unit's O
-        if (lo < hi && oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
         if (in(J0)) {
-          if (!(ok = wait_k(rc) && turn())) break;
-          scores(rc);
-          done();
-        } else if (!(ok = skip(rc, KSLABS))) {
+          if (!(ok = wait_k(bc) && turn(bc))) break;
+          scores(bc);
+        } else if (!(ok = skip_k(bc))) {
           break;
         }
-        for (int j = J0; j < J1; ++j, rc += BSLABS) {
-          const uint32_t v = rc + KSLABS;
+        // (every S MMA of the unit issued: Q may be loaded anew)
+        if (J0 + 1 >= hi) mma_commit_w(&bars[Q_EMPTY]);
+        for (int j = J0; j < J1; ++j, ++bc) {
           const bool more = j + 1 < J1 && in(j + 1);
+          if (!(ok = mbar_wait_warp(&bars[V_FULL0 + (bc & 1)], (bc >> 1) & 1, wc, kErrWaitKV))) break;
           if (in(j)) {
-            if (!(ok = wait_slab(v) && wait_slab(v + 1))) break;
-            const uint32_t s0 = v % RING, s1 = (v + 1) % RING;
+            if (more && !(ok = wait_k(bc + 1))) break;
+            // my O accumulator: the softmax warps have read the previous unit's O
+            if (j == lo && oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
+            const uint32_t s0 = (BSLABS * bc + KSLABS) % RING, s1 = (BSLABS * bc + KSLABS + 1) % RING;
             const uint32_t acc = j > lo;
 #pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {
@@ -453,22 +456,21 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
             }
             if (!ok) break;
             ++npv;
-            mma_commit_w(&bars[EMPTY0 + s0]);
-            mma_commit_w(&bars[EMPTY0 + s1]);
             mma_commit_w(&bars[O_DONE0 + w]);
-          } else if (!(ok = skip(v, VSLABS))) {
-            break;
+            mma_commit_w(&bars[V_EMPTY0 + (bc & 1)]);
+          } else if (lane == 0) {
+            mbar_arrive(&bars[V_EMPTY0 + (bc & 1)]);
           }
           if (more) {
-            if (!(ok = wait_k(rc + BSLABS) && turn())) break;
-            scores(rc + BSLABS);
-            done();
-          } else if (j + 1 < J1 && !(ok = skip(rc + BSLABS, KSLABS))) {
+            if (!in(j) && !(ok = wait_k(bc + 1))) break;
+            if (!(ok = turn(bc + 1))) break;
+            scores(bc + 1);
+            if (j + 2 >= hi) mma_commit_w(&bars[Q_EMPTY]);
+          } else if (j + 1 < J1 && !(ok = skip_k(bc + 1))) {
             break;
           }
         }
         if (!ok) break;
-        mma_commit_w(&bars[Q_EMPTY]);  // every S MMA of the unit issued
         oc += lo < hi ? 1u : 0u;
       }
       // every MMA issued by this warp completes before TMEM is released
