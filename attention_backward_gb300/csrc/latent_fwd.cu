@@ -78,7 +78,7 @@ enum FwdBar : int {
   V_EMPTY0 = K_EMPTY0 + 2,
   S_FULL0 = V_EMPTY0 + 2,     // per tile
   P_READY0 = S_FULL0 + 2,     // per tile and half of the keys: 4 softmax warps stored P
-  O_DONE0 = P_READY0 + 4,     // per tile: the tile's P V MMAs issued so far completed
+  O_DONE0 = P_READY0 + 4,     // per tile: the unit's P V MMAs completed
   O_FREE0 = O_DONE0 + 2,      // per tile: 4 softmax warps read the unit's O rows
   UNIT_FULL0 = O_FREE0 + 2,   // 2 ring slots: the producer published a unit index
   UNIT_EMPTY0 = UNIT_FULL0 + 2,  // 2 ring slots: the 2 issuing and the 8 softmax warps read it
@@ -373,109 +373,113 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
       const uint64_t r_kmaj = sdesc_sw128(smem_u32(sm) + OFF_R, 16, 1024);
       const uint64_t r_mn = sdesc_sw128(smem_u32(sm) + OFF_R, SLAB, 1024);
       const uint32_t ts = tmem + T_S0 + (T_S1 - T_S0) * w, to = tmem + T_O0 + (T_O1 - T_O0) * w;
-      const uint32_t one = elect_lane();
-      uint32_t qc = 0, bc = 0, npv = 0, oc = 0;  // units, blocks, blocks and units of my tile so far
-      bool ok = true;
-      auto wait_k = [&](uint32_t b) { return mbar_wait_warp(&bars[K_FULL0 + (b & 1)], (b >> 1) & 1, wc, kErrWaitKV); };
-      // Block b's turn of my tile at the scores: tile 0's, then tile 1's, each issued in one
-      // go: one's softmax then runs while the other's products do.  (Side by side, both
-      // tiles' S end at the same time, and both softmaxes run with the tensor core idle.)
-      auto turn = [&](uint32_t b) {
-        if (w == 0 && b == 0) return true;
-        const uint32_t n = w ? b : b - 1;
-        return mbar_wait_warp(&bars[TURN0 + w], n & 1, wc, kErrWaitTile);
-      };
-      auto pass = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[TURN0 + 1 - w]);
-      };
-      // S of block b, whose K is there
-      auto scores = [&](uint32_t b) {
-        tc_fence_after();
+      // One lane does all of it: a wait or a commit of the whole warp takes 70 to 140 cycles.
+      if (elect_lane()) {
+        uint32_t qc = 0, bc = 0, npv = 0, oc = 0;  // units, blocks, blocks and units of my tile so far
+        bool ok = true;
+        auto wait_k = [&](uint32_t b) { return mbar_wait(&bars[K_FULL0 + (b & 1)], (b >> 1) & 1, wc, kErrWaitKV); };
+        // Block b's turn of my tile at the scores: tile 0's, then tile 1's, each issued in one
+        // go: one's softmax then runs while the other's products do.  (Side by side, both
+        // tiles' S end at the same time, and both softmaxes run with the tensor core idle.)
+        auto turn = [&](uint32_t b) {
+          if (w == 0 && b == 0) return true;
+          const uint32_t n = w ? b : b - 1;
+          return mbar_wait(&bars[TURN0 + w], n & 1, wc, kErrWaitTile);
+        };
+        auto pass = [&]() {
+          mbar_arrive(&bars[TURN0 + 1 - w]);
+        };
+        // S of block b, whose K is there
+        auto scores = [&](uint32_t b) {
+          tc_fence_after();
 #pragma unroll 1
-        for (int s = 0; s < KSLABS; ++s) {
-          const uint64_t q = q_kmaj + sdesc_step(SLAB) * s, k = r_kmaj + sdesc_step(SLAB) * ((BSLABS * b + s) % RING);
+          for (int s = 0; s < KSLABS; ++s) {
+            const uint64_t q = q_kmaj + sdesc_step(SLAB) * s, k = r_kmaj + sdesc_step(SLAB) * ((BSLABS * b + s) % RING);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ss_e(ts, q + sdesc_step(kk * 32), k + sdesc_step(kk * 32), IDESC_S, s + kk > 0, one);
-        }
-        mma_commit_w(&bars[S_FULL0 + w]);
-        pass();
-        mma_commit_w(&bars[K_EMPTY0 + (b & 1)]);
-      };
-      // block b goes without my tile
-      auto skip_k = [&](uint32_t b) -> bool {
-        if (!wait_k(b) || !turn(b)) return false;
-        pass();
-        if (lane == 0) mbar_arrive(&bars[K_EMPTY0 + (b & 1)]);
-        return true;
-      };
-      for (uint32_t uc = 0; ok; ++uc) {
-        const FwdUnit u = next_unit(uc, &ok);
-        if (!ok || !u.valid) break;
-        const UnitSpan sp = unit_span(u);
-        if (sp.J1 <= sp.J0) continue;
-        const int J0 = sp.J0, J1 = sp.J1, lo = w ? u.lo[1] : u.lo[0], hi = w ? u.hi[1] : u.hi[0];
-        auto in = [&](int j) { return lo <= j && j < hi; };
-        if (!(ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
-        ++qc;
-        if (in(J0)) {
-          if (!(ok = wait_k(bc) && turn(bc))) break;
-          scores(bc);
-        } else if (!(ok = skip_k(bc))) {
-          break;
-        }
-        // (every S MMA of the unit issued: Q may be loaded anew)
-        if (J0 + 1 >= hi) mma_commit_w(&bars[Q_EMPTY]);
-        for (int j = J0; j < J1; ++j, ++bc) {
-          const bool more = j + 1 < J1 && in(j + 1);
-          if (!(ok = mbar_wait_warp(&bars[V_FULL0 + (bc & 1)], (bc >> 1) & 1, wc, kErrWaitKV))) break;
-          if (in(j)) {
-            if (more && !(ok = wait_k(bc + 1))) break;
-            // my O accumulator: the softmax warps have read the previous unit's O
-            if (j == lo && oc >= 1 && !(ok = mbar_wait_warp(&bars[O_FREE0 + w], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
-            const uint32_t s0 = (BSLABS * bc + KSLABS) % RING, s1 = (BSLABS * bc + KSLABS + 1) % RING;
-            const uint32_t acc = j > lo;
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-              if (!(ok = mbar_wait_warp(&bars[P_READY0 + 2 * w + hf], npv & 1, wc, kErrWaitP))) break;
-              tc_fence_after();
-              if (s1 == s0 + 1) {  // side by side: products of 128 columns
-                const uint64_t b = r_mn + sdesc_step(SLAB) * s0 + sdesc_step(4 * 2048) * hf;
-#pragma unroll
-                for (int kk = 0; kk < BK / 32; ++kk)
-                  mma_ts_e(to, ts + 32 * hf + kk * 8, b + sdesc_step(kk * 2048), IDESC_PV, kk > 0 ? 1u : acc | hf, one);
-              } else {
-#pragma unroll 1
-                for (int kk = 0; kk < BK / 32; ++kk) {
-                  const uint64_t at = sdesc_step(2048) * (4 * hf + kk);
-                  const uint32_t more_o = kk > 0 ? 1u : acc | hf;
-                  mma_ts_e(to, ts + 32 * hf + kk * 8, r_mn + sdesc_step(SLAB) * s0 + at, IDESC_PV1, more_o, one);
-                  mma_ts_e(to + 64, ts + 32 * hf + kk * 8, r_mn + sdesc_step(SLAB) * s1 + at, IDESC_PV1, more_o, one);
-                }
-              }
-            }
-            if (!ok) break;
-            ++npv;
-            mma_commit_w(&bars[O_DONE0 + w]);
-            mma_commit_w(&bars[V_EMPTY0 + (bc & 1)]);
-          } else if (lane == 0) {
-            mbar_arrive(&bars[V_EMPTY0 + (bc & 1)]);
+            for (int kk = 0; kk < 4; ++kk) mma_ss_e(ts, q + sdesc_step(kk * 32), k + sdesc_step(kk * 32), IDESC_S, s + kk > 0, 1u);
           }
-          if (more) {
-            if (!in(j) && !(ok = wait_k(bc + 1))) break;
-            if (!(ok = turn(bc + 1))) break;
-            scores(bc + 1);
-            if (j + 2 >= hi) mma_commit_w(&bars[Q_EMPTY]);
-          } else if (j + 1 < J1 && !(ok = skip_k(bc + 1))) {
+          mma_commit_1(&bars[S_FULL0 + w]);
+          pass();
+          mma_commit_1(&bars[K_EMPTY0 + (b & 1)]);
+        };
+        // block b goes without my tile
+        auto skip_k = [&](uint32_t b) -> bool {
+          if (!wait_k(b) || !turn(b)) return false;
+          pass();
+          mbar_arrive(&bars[K_EMPTY0 + (b & 1)]);
+          return true;
+        };
+        for (uint32_t uc = 0; ok; ++uc) {
+          if (!(ok = mbar_wait(&bars[UNIT_FULL0 + (uc & 1)], (uc >> 1) & 1, wu, kErrWaitTile))) break;
+          const int t = ring[uc & 1];
+          mbar_arrive(&bars[UNIT_EMPTY0 + (uc & 1)]);
+          const FwdUnit u = decode_unit(t, p);
+          if (!u.valid) break;
+          const UnitSpan sp = unit_span(u);
+          if (sp.J1 <= sp.J0) continue;
+          const int J0 = sp.J0, J1 = sp.J1, lo = w ? u.lo[1] : u.lo[0], hi = w ? u.hi[1] : u.hi[0];
+          auto in = [&](int j) { return lo <= j && j < hi; };
+          if (!(ok = mbar_wait(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
+          ++qc;
+          if (in(J0)) {
+            if (!(ok = wait_k(bc) && turn(bc))) break;
+            scores(bc);
+          } else if (!(ok = skip_k(bc))) {
             break;
           }
+          // (every S MMA of the unit issued: Q may be loaded anew)
+          if (J0 + 1 >= hi) mma_commit_1(&bars[Q_EMPTY]);
+          for (int j = J0; j < J1; ++j, ++bc) {
+            const bool more = j + 1 < J1 && in(j + 1);
+            if (!(ok = mbar_wait(&bars[V_FULL0 + (bc & 1)], (bc >> 1) & 1, wc, kErrWaitKV))) break;
+            if (in(j)) {
+              if (more && !(ok = wait_k(bc + 1))) break;
+              // my O accumulator: the softmax warps have read the previous unit's O
+              if (j == lo && oc >= 1 && !(ok = mbar_wait(&bars[O_FREE0 + w], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
+              const uint32_t s0 = (BSLABS * bc + KSLABS) % RING, s1 = (BSLABS * bc + KSLABS + 1) % RING;
+              const uint32_t acc = j > lo;
+#pragma unroll 1
+              for (int hf = 0; hf < 2; ++hf) {
+                if (!(ok = mbar_wait(&bars[P_READY0 + 2 * w + hf], npv & 1, wc, kErrWaitP))) break;
+                tc_fence_after();
+                if (s1 == s0 + 1) {  // side by side: products of 128 columns
+                  const uint64_t b = r_mn + sdesc_step(SLAB) * s0 + sdesc_step(4 * 2048) * hf;
+#pragma unroll
+                  for (int kk = 0; kk < BK / 32; ++kk)
+                    mma_ts_e(to, ts + 32 * hf + kk * 8, b + sdesc_step(kk * 2048), IDESC_PV, kk > 0 ? 1u : acc | hf, 1u);
+                } else {
+#pragma unroll 1
+                  for (int kk = 0; kk < BK / 32; ++kk) {
+                    const uint64_t at = sdesc_step(2048) * (4 * hf + kk);
+                    const uint32_t more_o = kk > 0 ? 1u : acc | hf;
+                    mma_ts_e(to, ts + 32 * hf + kk * 8, r_mn + sdesc_step(SLAB) * s0 + at, IDESC_PV1, more_o, 1u);
+                    mma_ts_e(to + 64, ts + 32 * hf + kk * 8, r_mn + sdesc_step(SLAB) * s1 + at, IDESC_PV1, more_o, 1u);
+                  }
+                }
+              }
+              if (!ok) break;
+              ++npv;
+              mma_commit_1(&bars[V_EMPTY0 + (bc & 1)]);
+              if (j + 1 >= hi) mma_commit_1(&bars[O_DONE0 + w]);
+            } else {
+              mbar_arrive(&bars[V_EMPTY0 + (bc & 1)]);
+            }
+            if (more) {
+              if (!in(j) && !(ok = wait_k(bc + 1))) break;
+              if (!(ok = turn(bc + 1))) break;
+              scores(bc + 1);
+              if (j + 2 >= hi) mma_commit_1(&bars[Q_EMPTY]);
+            } else if (j + 1 < J1 && !(ok = skip_k(bc + 1))) {
+              break;
+            }
+          }
+          if (!ok) break;
+          oc += lo < hi ? 1u : 0u;
         }
-        if (!ok) break;
-        oc += lo < hi ? 1u : 0u;
+        // every MMA issued by this warp completes before TMEM is released
+        mma_commit_1(&bars[DRAIN0 + w]);
+        mbar_drain(&bars[DRAIN0 + w], 0);
       }
-      // every MMA issued by this warp completes before TMEM is released
-      mma_commit_w(&bars[DRAIN0 + w]);
-      if (lane == 0) mbar_drain(&bars[DRAIN0 + w], 0);
       __syncwarp();
     }
     // warp 11: nothing to do
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t tS = tmem + lane_off + (w ? T_S1 : T_S0);
   const uint32_t tO = tmem + lane_off + (w ? T_O1 : T_O0);
-  uint32_t c = 0;  // blocks of this tile over all units so far
+  uint32_t c = 0, oc = 0;  // blocks of this tile over all units so far, and units with any
   bool ok = true;
   for (uint32_t uc = 0; ok; ++uc) {
     const FwdUnit u = next_unit(uc, &ok);
@@ -538,10 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
       const bool resc = m_used != -INFINITY && m_new > m_used + kRescaleLog2;
       const float f = resc ? ex2(m_used - m_new) : 1.f;
       if (__any_sync(0xffffffffu, resc)) {
-        // the tile's previous P V (of this unit: m_used is finite) has completed
-        // before its O rows are scaled
-        if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
-        tc_fence_after();
+        // (the tile's previous P V, issued before these scores, has completed as they have)
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t r[32];
@@ -587,7 +588,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     // ---- O = O_w / l and the natural-log LSE of the row
     const bool had = c > c0;  // the tile saw a key block in this unit
     if (had) {
-      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], (c - 1) & 1, wc, kErrWaitDQFull))) break;
+      if (!(ok = mbar_wait_warp(&bars[O_DONE0 + w], oc & 1, wc, kErrWaitDQFull))) break;
+      ++oc;
       tc_fence_after();
     }
     const bool live = q < u.qlen;

@@ -26,4 +26,9 @@ __device__ __forceinline__ void mma_ts_e(uint32_t d_tmem, uint32_t a_tmem, uint6
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected));
 }
 
+// Of one lane: the barrier takes an arrival when its products so far are complete.
+__device__ __forceinline__ void mma_commit_1(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 }  // namespace ab
