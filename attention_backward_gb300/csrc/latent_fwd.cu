@@ -433,7 +433,6 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
             const bool more = j + 1 < J1 && in(j + 1);
             if (!(ok = mbar_wait(&bars[V_FULL0 + (bc & 1)], (bc >> 1) & 1, wc, kErrWaitKV))) break;
             if (in(j)) {
-              if (more && !(ok = wait_k(bc + 1))) break;
               // my O accumulator: the softmax warps have read the previous unit's O
               if (j == lo && oc >= 1 && !(ok = mbar_wait(&bars[O_FREE0 + w], (oc - 1) & 1, wu, kErrWaitDQEmpty))) break;
               const uint32_t s0 = (BSLABS * bc + KSLABS) % RING, s1 = (BSLABS * bc + KSLABS + 1) % RING;
@@ -465,8 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
               mbar_arrive(&bars[V_EMPTY0 + (bc & 1)]);
             }
             if (more) {
-              if (!in(j) && !(ok = wait_k(bc + 1))) break;
-              if (!(ok = turn(bc + 1))) break;
+              if (!(ok = wait_k(bc + 1) && turn(bc + 1))) break;
               scores(bc + 1);
               if (j + 2 >= hi) mma_commit_1(&bars[Q_EMPTY]);
             } else if (j + 1 < J1 && !(ok = skip_k(bc + 1))) {
