@@ -360,6 +360,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     return u;
   };
 
+  // the same of a lane alone: its units with tiles
+  auto next_tiles = [&](uint32_t* uc, int* tiles) -> bool {
+    for (;; ++*uc) {
+      const uint32_t slot = *uc & 1;
+      if (!mbar_wait(&bars[UNIT_FULL0 + slot], (*uc >> 1) & 1, wu, kErrWaitTile)) return false;
+      const int valid = sh.units[slot].valid;
+      *tiles = sh.units[slot].j1 - sh.units[slot].j0;
+      mbar_arrive(&bars[UNIT_EMPTY0 + slot]);
+      if (!valid) return false;
+      if (valid != 2 && *tiles > 0) return ++*uc, true;
+    }
+  };
+
   if (warp == 14) {
     // ============================================================ the walk
     auto publish = [&](uint32_t uc, const LatUnit& u) -> bool {
@@ -471,43 +484,44 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 13) {
     // ============================================================ scores
     // (O has a warp of its own: the products are so short that their issue counts, and
-    // neither warp waits on what the other is waiting for)
-    constexpr uint32_t IDESC = idesc_f16(BF16, KT, NR, false, false);
-    const uint64_t k_kmaj = sdesc_sw128(smem_u32(sm) + OFF_K, 16, 1024);
-    const uint64_t q_kmaj = sdesc_sw128(smem_u32(sm) + OFF_Q, 16, 1024);
-    const uint32_t one = elect_lane();
-    uint32_t kc = 0, qc = 0;
-    bool ok = true;
-    for (uint32_t uc = 0; ok; ++uc) {
-      const LatUnit u = next_unit(uc, &ok);
-      if (!ok || !u.valid) break;
-      if (u.valid == 2 || u.j1 <= u.j0) continue;
-      if (!(ok = mbar_wait_warp(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
-      ++qc;
-      for (const uint32_t end = kc + uniform(u.j1 - u.j0); kc < end; ++kc) {
-        const uint32_t st = kc % STAGES, phase = (kc / STAGES) & 1, d = tmem + T_S + 64 * (kc & 1);
-        // the softmax has read the scores of two tiles ago
-        if (kc >= 2 && !(ok = mbar_wait_warp(&bars[P_READY0 + (kc & 1)], ((kc >> 1) - 1) & 1, wc, kErrWaitSFree))) break;
-        const uint64_t a = k_kmaj + sdesc_step(st * TILE);
+    // neither warp waits on what the other is waiting for.  One lane does all of it, as a wait
+    // of the whole warp takes 70 to 140 cycles: 2048 lists of 1024 rows, 64 heads 356 -> 338 us.
+    // O's by one lane, whose waits are few, make that 351.)
+    if (elect_lane()) {
+      constexpr uint32_t IDESC = idesc_f16(BF16, KT, NR, false, false);
+      const uint64_t k_kmaj = sdesc_sw128(smem_u32(sm) + OFF_K, 16, 1024);
+      const uint64_t q_kmaj = sdesc_sw128(smem_u32(sm) + OFF_Q, 16, 1024);
+      uint32_t kc = 0, qc = 0, uc = 0;
+      int tiles;
+      bool ok = true;
+      while (ok && next_tiles(&uc, &tiles)) {
+        if (!(ok = mbar_wait(&bars[Q_FULL], qc & 1, wc, kErrWaitStageFull))) break;
+        ++qc;
+        for (const uint32_t end = kc + tiles; kc < end; ++kc) {
+          const uint32_t st = kc % STAGES, phase = (kc / STAGES) & 1, d = tmem + T_S + 64 * (kc & 1);
+          // the softmax has read the scores of two tiles ago
+          if (kc >= 2 && !(ok = mbar_wait(&bars[P_READY0 + (kc & 1)], ((kc >> 1) - 1) & 1, wc, kErrWaitSFree))) break;
+          const uint64_t a = k_kmaj + sdesc_step(st * TILE);
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          if (!(ok = mbar_wait_warp(&bars[FULL0 + st * GROUPS + g], phase, wc, kErrWaitKV))) break;
-          fence_proxy_async_smem();  // (the copies are the generic proxy's)
-          tc_fence_after();
+          for (int g = 0; g < GROUPS; ++g) {
+            if (!(ok = mbar_wait(&bars[FULL0 + st * GROUPS + g], phase, wc, kErrWaitKV))) break;
+            fence_proxy_async_smem();  // (the copies are the generic proxy's)
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < (g < 4 ? 8 : 4); ++kk) {
-            const uint64_t o = sdesc_step((2 * g + kk / 4) * SLAB + kk % 4 * 32);
-            mma_ss_e(d, a + o, q_kmaj + o, IDESC, g + kk > 0, one);
+            for (int kk = 0; kk < (g < 4 ? 8 : 4); ++kk) {
+              const uint64_t o = sdesc_step((2 * g + kk / 4) * SLAB + kk % 4 * 32);
+              mma_ss_e(d, a + o, q_kmaj + o, IDESC, g + kk > 0, 1u);
+            }
           }
+          if (!ok) break;
+          mma_commit_1(&bars[S_FULL0 + (kc & 1)]);
         }
-        if (!ok) break;
-        mma_commit_w(&bars[S_FULL0 + (kc & 1)]);
+        mma_commit_1(&bars[Q_EMPTY]);
       }
-      mma_commit_w(&bars[Q_EMPTY]);
+      // every product issued here completes before tensor memory is released
+      mma_commit_1(&bars[DRAIN0]);
+      mbar_drain(&bars[DRAIN0], 0);
     }
-    // every product issued by this warp completes before tensor memory is released
-    mma_commit_w(&bars[DRAIN0]);
-    if (lane == 0) mbar_drain(&bars[DRAIN0], 0);
     __syncwarp();
   } else if (warp == 15) {
     // ============================================================ O
