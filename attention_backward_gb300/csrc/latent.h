@@ -87,6 +87,7 @@ struct LatFwdParams {
   int64_t sl_b, sl_s, sl_h;
   int* err;
   int* unit_counter;
+  int units;
   uint64_t timeout_ns;
   int whole;        // pairs of query tiles that are a unit each (2^31 - 1: all)
   int splits;       // units of each further pair, of a share of its key blocks each

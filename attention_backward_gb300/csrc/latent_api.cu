@@ -351,8 +351,10 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
     p.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
     p.part_o = reinterpret_cast<float*>(p.part_ml + kLatFwdMaxUnits * kLatFwdRows);
   }
-  // the error word and the unit counter start clear
-  if (cudaMemsetAsync(workspace, 0, kHeaderBytes, st) != cudaSuccess) return ATTN_ERR_LAUNCH;
+  p.units = static_cast<int>(units);
+  // the counter of units starts clear where some are drawn (without, 128 on 128, 4 heads 10.3
+  // -> 7.0 us)
+  if (units > sms && cudaMemsetAsync(workspace, 0, kHeaderBytes, st) != cudaSuccess) return ATTN_ERR_LAUNCH;
   return launch_status(launch_latent_fwd(p, m, dtype == ATTN_DT_BF16, static_cast<int>(split),
                                          static_cast<int>(units < sms ? units : sms), st));
 }

@@ -198,14 +198,14 @@ __device__ __forceinline__ UnitSpan unit_span(const FwdUnit& u) {
   return s;
 }
 
-// Persistent: each CTA's producer draws units, longest first, from a counter
-// in the workspace header (cleared by the host before the launch) and
-// publishes each draw to the other roles through a two-slot ring in shared
-// memory; a draw past the last unit ends every role.  Barrier phases run on
-// across units (K/V stages by a block counter, the S / P / O barriers of a
-// tile by that tile's block counter), and two barriers hand the shared Q tiles
-// (Q_EMPTY: every S MMA of the unit has completed) and a tile's O accumulator
-// (O_FREE: its softmax warps have read O) to the next unit.
+// Persistent: each CTA's producer takes the unit of its number, then draws units, longest
+// first, from a counter in the workspace header (cleared by the host before the launch,
+// where there are more units than CTAs), and publishes each to the other roles through a
+// two-slot ring in shared memory; a draw past the last unit ends every role.  Barrier phases
+// run on across units (K and V by a block counter, the S and P barriers of a tile by that
+// tile's block counter), and two barriers hand the shared Q tiles (Q_EMPTY: every S MMA of
+// the unit has completed) and a tile's O accumulator (O_FREE: its softmax warps have read O)
+// to the next unit.
 template <bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_constant__ LatFwdMaps maps,
                                                                const LatFwdParams p) {
@@ -216,10 +216,13 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   volatile int* ring = reinterpret_cast<volatile int*>(sm + OFF_MISC + 16);  // 2 unit indices
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if ((smem_u32(sm) & 1023u) != 0) {  // the swizzled tiles need an aligned base
-    if (threadIdx.x == 0) atomicCAS(p.err, 0, kErrAlign);
-    return;
-  }
+  // (the join's blocks, let in at once, wait beside the last parts and slow them: 256 queries
+  // on 3000 keys, 160 heads 77 -> 80 us)
+  grid_dependency_wait();
+  const bool aligned = (smem_u32(sm) & 1023u) == 0;  // the swizzled tiles need an aligned base
+  // (the call's error word, which a wait sets after a second at the earliest)
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = aligned ? kErrNone : kErrAlign;
+  if (!aligned) return;
 
   // ---------------------------------------------------------------- set-up
   if (threadIdx.x == 0) {
@@ -293,8 +296,12 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         if (uc >= 2 && !(ok = mbar_wait_warp(&bars[UNIT_EMPTY0 + slot], ((uc >> 1) - 1) & 1, wu, kErrWaitTile)))
           break;
         int t = 0;
-        if (lane == 0) t = atomicAdd(p.unit_counter, 1);
-        t = __shfl_sync(0xffffffffu, t, 0);
+        if (uc == 0) {
+          t = blockIdx.x;
+        } else {
+          if (lane == 0) t = p.units > static_cast<int>(gridDim.x) ? gridDim.x + atomicAdd(p.unit_counter, 1) : -1;
+          t = __shfl_sync(0xffffffffu, t, 0);
+        }
         const FwdUnit u = decode_unit(t, p);
         if (lane == 0) {
           ring[slot] = u.valid ? t : -1;
@@ -693,8 +700,7 @@ cudaError_t launch_t(const LatFwdParams& p, const LatFwdMaps& m, int split_pairs
   static std::atomic<uint64_t> done{0};
   auto kern = latent_fwd_kernel<BF16>;
   if (const cudaError_t e = allow_smem_once(kern, SMEM, &done); e != cudaSuccess) return e;
-  kern<<<grid, THREADS, SMEM, st>>>(m, p);
-  if (const cudaError_t e = cudaGetLastError(); e != cudaSuccess || split_pairs == 0) return e;
+  if (const cudaError_t e = launch_chained(kern, dim3(grid), THREADS, SMEM, st, m, p); e != cudaSuccess || split_pairs == 0) return e;
   return launch_chained(latent_fwd_join_kernel<BF16>, dim3(split_pairs * (2 * BQ / JOIN_WARPS)), JOIN_WARPS * 32, 0,
                         st, p, split_pairs);
 }

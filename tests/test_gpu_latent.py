@@ -438,7 +438,7 @@ def test_binding_refusals():
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("form", ["whole lists", "lists in parts", "expanded", "expanded in parts"])
+@pytest.mark.parametrize("form", ["whole lists", "lists in parts", "expanded", "expanded in parts", "expanded in rounds"])
 def test_prompt_graphs_streams_and_bits(form):
     """A captured call replays on other inputs; calls on two streams with workspaces of
     their own, and repeated ones, give the same bits."""
@@ -458,10 +458,11 @@ def test_prompt_graphs_streams_and_bits(form):
     else:
         S = 300 if "parts" in form else 700
         Sk = 2000 if "parts" in form else 700
-        x = [rounded(rng, s, "bf16") for s in ((1, S, 2, 192), (1, Sk, 2, 128), (1, Sk, 64), (1, Sk, 2, 128))]
+        H = 64 if "rounds" in form else 2  # (more pairs of query tiles than CTAs)
+        x = [rounded(rng, s, "bf16") for s in ((1, S, H, 192), (1, Sk, H, 128), (1, Sk, 64), (1, Sk, H, 128))]
         call = lambda **k: ab.forward_latent(*x, 0.07, **k)  # noqa: E731
         ref = lambda: oracle.expanded_forward(*(f64(t) for t in x), 0.07)  # noqa: E731
-        need = ab.latent_workspace_size(1, S, 2)
+        need = ab.latent_workspace_size(1, S, H)
     ws = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
     out = [tuple(torch.empty_like(t) for t in call()) for _ in range(2)]
     graph = torch.cuda.CUDAGraph()
