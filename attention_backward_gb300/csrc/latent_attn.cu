@@ -264,8 +264,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* const bars = sh.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // (the join's blocks, let in at once, wait beside the last parts and slow them: 300 requests of
+  // 300 rows 40 -> 43 us, 64 of 4000 67 -> 68.5)
   grid_dependency_wait();
-  grid_dependents_launch();
   volatile int* const abort_flag = &sh.abort;
   const WaitCtx wc{abort_flag, LISTS ? p.err : p.cta_err + blockIdx.x, p.timeout_ns};
   // a unit lasts as long as its keys do: waits for one to begin or to be taken
