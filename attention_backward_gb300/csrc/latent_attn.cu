@@ -77,6 +77,13 @@ enum LatBar : int {
   DRAIN0 = UNIT_EMPTY0 + 2,  // of the issuing warps
   NUM_BARS = DRAIN0 + 2
 };
+// Arrivals that complete barrier i.
+__device__ __forceinline__ int arrivals(int i) {
+  // every copying thread; of the last group also a lane a warp, for the bits
+  if (i >= FULL0 && i < EMPTY0) return (i - FULL0) % GROUPS == GROUPS - 1 ? 132 : 128;
+  if (i == O_FREE || (i >= P_READY0 && i < O_DONE0)) return SOFT / 32;
+  return i >= UNIT_EMPTY0 && i < DRAIN0 ? 15 : 1;
+}
 
 // A unit, or the CTA's part of one: key tiles [j0, j1).
 struct LatUnit {
@@ -264,6 +271,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* const bars = sh.bars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // ---------------------------------------------------------------- set-up, beside the end of the launch before
+  if (warp == 12) {
+    for (int i = lane; i < NUM_BARS; i += 32) mbar_init(&bars[i], arrivals(i));
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
   // (the join's blocks, let in at once, wait beside the last parts and slow them: 300 requests of
   // 300 rows 40 -> 43 us, 64 of 4000 67 -> 68.5)
   grid_dependency_wait();
@@ -295,8 +311,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     upto = lanes_scan(mine);
     if (lane == 31) sh.work[warp] = upto;
   }
+  tc_fence_before();
   __syncthreads();
-  if (!aligned) return;
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  auto leave = [&]() {  // (all threads do)
+    if (warp == 13) tmem_dealloc(tmem, 512);
+  };
+  if (!aligned) return leave();
   if constexpr (!LISTS) {
     int64_t before = 0;
 #pragma unroll
@@ -305,12 +327,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (i < warp) before += w;
       total += w;
     }
-    if (total == 0) return;
+    if (total == 0) return leave();
     upto += before;
     const int64_t want = (total + kLatMinWork - 1) / kLatMinWork;
     const int most = gridDim.x / GROUP;
     parts = want < most ? static_cast<int>(want) : most;
-    if (part >= parts) return;
+    if (part >= parts) return leave();
     begin = kv_part_begin(total, part, parts), end = kv_part_begin(total, part + 1, parts);
     // the warp whose requests hold the first position looks it up
     const uint32_t here = __ballot_sync(0xffffffffu, begin >= upto - mine && begin < upto);
@@ -321,34 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
 
-  // ---------------------------------------------------------------- set-up
-  if (threadIdx.x == 0) {
-    mbar_init(&bars[Q_FULL], 1);
-    mbar_init(&bars[Q_EMPTY], 1);
-    for (int i = 0; i < STAGES * GROUPS; ++i) {
-      // every copying thread; of the last group also a lane a warp, for the bits
-      mbar_init(&bars[FULL0 + i], i % GROUPS == GROUPS - 1 ? 132 : 128);
-      mbar_init(&bars[EMPTY0 + i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[S_FULL0 + i], 1);
-      mbar_init(&bars[P_READY0 + i], SOFT / 32);
-      mbar_init(&bars[O_DONE0 + i], 1);
-      mbar_init(&bars[UNIT_FULL0 + i], 1);
-      mbar_init(&bars[UNIT_EMPTY0 + i], 15);
-      mbar_init(&bars[DRAIN0 + i], 1);
-    }
-    mbar_init(&bars[O_FREE], SOFT / 32);
-    fence_mbar_init();
-  }
-  if (warp == 13) {
-    tmem_alloc(&sh.tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
 
   // the uc-th unit of this CTA
   auto next_unit = [&](uint32_t uc, bool* okp) -> LatUnit {

@@ -216,15 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
   volatile int* ring = reinterpret_cast<volatile int*>(sm + OFF_MISC + 16);  // 2 unit indices
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // (the join's blocks, let in at once, wait beside the last parts and slow them: 256 queries
-  // on 3000 keys, 160 heads 77 -> 80 us)
-  grid_dependency_wait();
-  const bool aligned = (smem_u32(sm) & 1023u) == 0;  // the swizzled tiles need an aligned base
-  // (the call's error word, which a wait sets after a second at the earliest)
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = aligned ? kErrNone : kErrAlign;
-  if (!aligned) return;
-
-  // ---------------------------------------------------------------- set-up
+  // ---------------------------------------------------------------- set-up, beside the end of the launch before
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     mbar_init(&bars[Q_FULL], 1);
@@ -253,10 +245,20 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  // (the join's blocks, let in at once, wait beside the last parts and slow them: 256 queries
+  // on 3000 keys, 160 heads 77 -> 80 us)
+  grid_dependency_wait();
+  const bool aligned = (smem_u32(sm) & 1023u) == 0;  // the swizzled tiles need an aligned base
+  // (the call's error word, which a wait sets after a second at the earliest)
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = aligned ? kErrNone : kErrAlign;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!aligned) {
+    if (warp == 9) tmem_dealloc(tmem, 512);
+    return;
+  }
   const WaitCtx wc{abort_flag, p.err, p.timeout_ns};
   // a unit lasts as long as its keys do: waits for one to begin or to be taken have
   // a limit of their own (any wait that runs out ends the others too)
