@@ -3,7 +3,8 @@
 //
 // Bound by HBM (1152 bytes in and out a token), by latency for few tokens.  A warp
 // takes a token: two 16-byte pieces of c a lane, whose squares are summed across the
-// warp, and one of the 32 pairs of k a lane.
+// warp, and one of the 32 pairs of k a lane.  26859 tokens, normalised and turned: 10.9 us,
+// 5.7 TB/s, 84 % of the copy rate.
 #include "cvt.cuh"
 #include "kv_launch.h"
 #include "latent.h"

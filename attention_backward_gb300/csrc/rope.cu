@@ -7,7 +7,7 @@
 // shared memory, one or two a thread, while the first heads are on their way (eight a
 // thread, and 96 registers: 14.4 us instead of 6.9 for 2048 tokens of 20 heads of 192,
 // 64 of them turned).  32 and 4 heads of 128, 16384 tokens: 51 us, 5.9 TB/s, 87 % of the
-// copy rate.  64 columns of 65 heads of 576, 4096 tokens: 15.7 us, 4.3 TB/s, in pieces of
+// copy rate.  64 columns of 65 heads of 576, 4096 tokens: 14.8 us, 4.6 TB/s, in pieces of
 // 128 bytes.
 #include "cvt.cuh"
 #include "kv_launch.h"

@@ -1,7 +1,7 @@
 // Torch operators over include/attn_rope.h and include/attn_latent.h: argument
 // marshalling only (the checks that need a tensor, outputs, the stream), as the
 // ctypes binding does it for the other entry points.  It is C++ because the short
-// calls are bound by the host: one request of 385 cached rows takes 14 us on the GPU,
+// calls are bound by the host: one request of 385 cached rows takes 13 us on the GPU,
 // and a call took the host 31 us with its marshalling in Python, 17 with this (of
 // which 6 are the launches).
 #include <ATen/ATen.h>
