@@ -27,8 +27,9 @@
 // products wait for is the softmax of the other tile, 1400 cycles a block beside 1280 of
 // products.  (One lane issues, and waits on as few barriers as there are: with waits and
 // commits of the whole warp between P's products and the next scores the first of these took
-// 490 us.)  Three quarters of the softmax are the 128 powers; without a max, which the
-// weights' sum can stand for, the compiler has too few registers to overlap them (439 us).
+// 490 us.)  Half of the softmax are the 128 powers, 600 cycles; without a max, which the
+// weights' sum can stand for, the compiler has too few registers to overlap them (439 us), and
+// twice the warps with half a row each share the powers' unit (463).
 //
 // Warp roles (12 warps): 0-3 softmax of tile 0, 4-7 of tile 1, 8 TMA producer, 9 and
 // 10 MMA issue of a tile each, 11 idle.  Every wait is bounded.
@@ -310,7 +311,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         if (uc == 0) {
           t = blockIdx.x;
         } else {
-          if (lane == 0) t = p.units > static_cast<int>(gridDim.x) ? gridDim.x + atomicAdd(p.unit_counter, 1) : -1;
+          const int ctas = gridDim.x;
+          if (lane == 0) t = p.units > ctas ? ctas + atomicAdd(p.unit_counter, 1) : -1;
           t = __shfl_sync(0xffffffffu, t, 0);
         }
         const FwdUnit u = decode_unit(t, p);
