@@ -299,6 +299,33 @@ def test_expanded(B, S, Sk, H, causal, cu, name):
         assert o[:, cu[-1]:].isnan().all() and lse[:, :, cu[-1]:].isnan().all()
 
 
+@pytest.mark.parametrize("name,S,Sk,H", [("f16", 300, 1500, 2), ("bf16", 700, 700, 2), ("f16", 260, 900, 90)])
+def test_expanded_scores_of_any_size(name, S, Sk, H):
+    """Large scores, rising along the keys (a new reference again and again, in some
+    rows of a tile only), a sink far above many small weights, and all scores far below zero."""
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(Sk)
+    q, up, kr = rounded(rng, (1, S, H, 192), name), rounded(rng, (1, Sk, H, 256), name), rounded(rng, (1, Sk, 64), name)
+
+    def check(scale):
+        kn, v = up[..., :128], up[..., 128:]
+        o, lse = ab.forward_latent(q, kn, kr, v, scale)
+        near(o, lse.transpose(1, 2), oracle.expanded_forward(f64(q), f64(kn), f64(kr), f64(v), scale), name)
+        for _ in range(5):
+            assert all(torch.equal(x, y) for x, y in zip(ab.forward_latent(q, kn, kr, v, scale), (o, lse)))
+
+    kr.copy_(torch.linspace(-3, 3, Sk, device="cuda").view(1, Sk, 1).expand_as(kr))
+    q[:, ::3, :, 128:] = 1.5
+    check(0.25)
+    kr[:, 1] = 6.0  # the sink
+    check(0.04)
+    q[..., 128:], kr[:] = -20.0, 10.0
+    check(0.3)
+
+
 def test_expanded_offsets_that_do_not_ascend():
     """A sequence named twice has more pairs of query tiles than the call's rows: with
     keys in parts, no partial row is written past the workspace, and rows that were
