@@ -1,6 +1,6 @@
 """Binding of ``include/attn_rope.h`` and ``include/attn_latent.h``: rotary
 positions and latent attention.  Argument marshalling only, as in ``_binding``, by the
-torch operators of ``csrc/torch_latent.cpp``.
+functions of ``csrc/torch_latent.cpp``.
 
 One step of a server of latent attention (``new_lens`` new tokens a request; ``kv``
 [1, T, 576] their latent rows, ``q`` [1, T, H, 576] absorbed queries)::
@@ -22,6 +22,8 @@ stream.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 from typing import NamedTuple, Optional
@@ -122,20 +124,21 @@ _ops = None
 
 
 def _operators():
-    """The torch operators (raises if they have not been built)."""
+    """The functions of csrc/torch_latent.cpp (raises if they have not been built)."""
     global _ops
     if _ops is None:
         if not os.path.exists(TORCH_LIB_PATH):
             raise AttnBwdError(f"library missing at {TORCH_LIB_PATH}: build it with attention_backward_gb300.build")
-        torch.ops.load_library(TORCH_LIB_PATH)
-        ops = torch.ops.attention_backward_gb300
-        _ops = {n: getattr(ops, n).default for n in ("rope", "latent_cache_write", "forward_latent_cache",
-                                                     "sparse_forward", "forward_latent")}
+        loader = importlib.machinery.ExtensionFileLoader("libattn_torch", TORCH_LIB_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("libattn_torch", loader))
+        loader.exec_module(module)
+        _ops = {n: getattr(module, n) for n in ("rope", "latent_cache_write", "forward_latent_cache", "sparse_forward",
+                                                "forward_latent")}
     return _ops
 
 
 def _call(name, first, stream, *args):
-    """Operator ``name`` on ``stream`` (None: the current one of first's device)."""
+    """Function ``name`` on ``stream`` (None: the current one of first's device)."""
     if stream is not None:
         if isinstance(stream, torch.cuda.Stream) and isinstance(first, torch.Tensor) and stream.device != first.device:
             raise AttnBwdError("stream belongs to another device than the tensors")
@@ -170,8 +173,7 @@ def rope(q, positions, table: RopeTable, k=None, interleaved: bool = False, star
     call's results it returns those of its inputs.  ``out`` (q', k') writes into
     tensors of the same shapes; the inputs themselves work in place."""
     steps, scale = _table(table)
-    y = _call("rope", q, stream, positions, steps, scale, k, interleaved, start, k_start, inverse, *_pair(out))
-    return (y[0], None) if k is None else (y[0], y[1])
+    return _call("rope", q, stream, positions, steps, scale, k, interleaved, start, k_start, inverse, *_pair(out))
 
 
 def new_latent_cache(num_blocks: int, page_size: int, dtype, device=None):

@@ -1,5 +1,5 @@
 """Builds the CUDA library ``_build/libattn_bwd.so`` for sm_103a with nvcc, and
-``_build/libattn_torch.so``, torch operators over some of its entry points.
+``_build/libattn_torch.so``, Python functions on torch tensors over some of its entry points.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library with the CUDA runtime linked statically, so the library loads on a
@@ -47,14 +47,17 @@ def _stale(obj: str, src: str) -> bool:
 
 def _torch_flags(cc: str) -> tuple:
     """Flags that compile and link against the torch of this interpreter."""
+    import sysconfig
+
     import torch
 
     at = os.path.dirname(torch.__file__)
     include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
-               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"), os.path.join(ROOT, "include")]
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include"), os.path.join(ROOT, "include"),
+               sysconfig.get_paths()["include"]]
     return (["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
              *(f"-I{i}" for i in include)],
-            [f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch"])
+            [f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"])
 
 
 def build(verbose: bool = False, force: bool = False) -> str:

@@ -1,14 +1,17 @@
-// Torch operators over include/attn_rope.h and include/attn_latent.h: argument
-// marshalling only (the checks that need a tensor, outputs, the stream), as the
+// Python functions on torch tensors over include/attn_rope.h and include/attn_latent.h:
+// argument marshalling only (the checks that need a tensor, outputs, the stream), as the
 // ctypes binding does it for the other entry points.  It is C++ because the short
 // calls are bound by the host: one request of 385 cached rows takes 13 us on the GPU,
-// and a call took the host 31 us with its marshalling in Python, 17 with this (of
-// which 6 are the launches).
+// and a call took the host 31 us with its marshalling in Python, 17 as an operator of
+// torch's dispatcher and 10 with this.
+#include <Python.h>
+
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
-#include <torch/library.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <optional>
@@ -43,8 +46,8 @@ attn_dtype_t dtype_of(const char* name, const Tensor& t) {
   return ATTN_DT_BF16;
 }
 
-// A new contiguous tensor on q's device, straight from the allocator (through the
-// dispatcher a call that makes two takes 1.3 us more).
+// A new contiguous tensor on q's device, straight from the allocator (through
+// torch's dispatcher a call that makes two takes 1.3 us more).
 Tensor fresh(const Tensor& q, at::IntArrayRef shape, at::ScalarType type) {
   return at::detail::empty_cuda(shape, type, q.device(), std::nullopt);
 }
@@ -328,15 +331,180 @@ std::tuple<Tensor, Tensor> forward_latent(const Tensor& q, const Tensor& k_nope,
 
 }  // namespace
 
-TORCH_LIBRARY(attention_backward_gb300, m) {
-  m.def("rope(Tensor q, Tensor positions, Tensor steps, float scale, Tensor? k, bool interleaved, int start, int k_start, "
-        "bool inverse, Tensor? out_q, Tensor? out_k, int? stream) -> Tensor[]", rope);
-  m.def("latent_cache_write(Tensor kv, Tensor slot_map, Tensor cache, Tensor? norm_weight, float norm_eps, Tensor? positions, "
-        "Tensor? steps, float scale, bool interleaved, Tensor? out, int? stream) -> ()", latent_cache_write);
-  m.def("forward_latent_cache(Tensor q, Tensor cache, Tensor block_table, Tensor cu_seqlens, Tensor kv_lens, float sm_scale, "
-        "bool causal, Tensor? workspace, Tensor? o, Tensor? lse, int? stream) -> (Tensor, Tensor)", forward_latent_cache);
-  m.def("sparse_forward(Tensor q, Tensor kv, Tensor idx, float sm_scale, int dv_dim, Tensor? workspace, Tensor? o, "
-        "Tensor? lse, int? stream) -> (Tensor, Tensor)", sparse_forward);
-  m.def("forward_latent(Tensor q, Tensor k_nope, Tensor k_rope, Tensor v, float sm_scale, bool causal, Tensor? cu_seqlens, "
-        "Tensor? workspace, Tensor? o, Tensor? lse, int? stream) -> (Tensor, Tensor)", forward_latent);
+// ---------------------------------------------------------------- Python functions
+
+namespace {
+
+// Positional arguments, taken in order.
+class Args {
+ public:
+  Args(PyObject* const* args, Py_ssize_t n, Py_ssize_t want) : next_(args) {
+    TORCH_CHECK(n == want, "expected ", want, " arguments, got ", n);
+  }
+  const Tensor& tensor(const char* name) {
+    PyObject* const x = *next_++;
+    TORCH_CHECK(THPVariable_Check(x), name, " must be a tensor");
+    return THPVariable_Unpack(x);
+  }
+  MaybeTensor maybe(const char* name) {
+    if (*next_ == Py_None) return ++next_, std::nullopt;
+    return tensor(name);
+  }
+  double number(const char* name) {
+    const double x = PyFloat_AsDouble(*next_++);
+    no_error(name, "a number");
+    return x;
+  }
+  int64_t integer(const char* name) {
+    const int64_t x = PyLong_AsLongLong(*next_++);
+    no_error(name, "an integer");
+    return x;
+  }
+  bool flag(const char* name) {
+    const int x = PyObject_IsTrue(*next_++);
+    no_error(name, "true or false");
+    return x != 0;
+  }
+  std::optional<int64_t> stream() {
+    if (*next_ == Py_None) return ++next_, std::nullopt;
+    return integer("stream");
+  }
+
+ private:
+  static void no_error(const char* name, const char* what) {
+    if (PyErr_Occurred() == nullptr) return;
+    PyErr_Clear();
+    TORCH_CHECK(false, name, " must be ", what);
+  }
+  PyObject* const* next_;
+};
+
+// Other threads may run Python meanwhile (a launch waits where the queue is full).
+class Released {
+ public:
+  Released() : state_(PyEval_SaveThread()) {}
+  ~Released() { PyEval_RestoreThread(state_); }
+
+ private:
+  PyThreadState* state_;
+};
+
+PyObject* pair(PyObject* x, PyObject* y) {
+  PyObject* const t = x && y ? PyTuple_New(2) : nullptr;
+  if (t == nullptr) {
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(t, 0, x);
+  PyTuple_SET_ITEM(t, 1, y);
+  return t;
+}
+PyObject* pair(const std::tuple<Tensor, Tensor>& y) { return pair(THPVariable_Wrap(std::get<0>(y)), THPVariable_Wrap(std::get<1>(y))); }
+
+PyObject* py_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 12);
+  const Tensor &q = a.tensor("q"), &positions = a.tensor("positions"), &steps = a.tensor("the table's steps");
+  const double scale = a.number("the table's scale");
+  const MaybeTensor k = a.maybe("k");
+  const bool interleaved = a.flag("interleaved");
+  const int64_t start = a.integer("start"), k_start = a.integer("k_start");
+  const bool inverse = a.flag("inverse");
+  const MaybeTensor out_q = a.maybe("out"), out_k = a.maybe("out");
+  const std::optional<int64_t> stream = a.stream();
+  std::vector<Tensor> y;
+  {
+    const Released released;
+    y = rope(q, positions, steps, scale, k, interleaved, start, k_start, inverse, out_q, out_k, stream);
+  }
+  return pair(THPVariable_Wrap(y[0]), y.size() > 1 ? THPVariable_Wrap(y[1]) : Py_NewRef(Py_None));
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_latent_cache_write(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 11);
+  const Tensor &kv = a.tensor("kv"), &slot_map = a.tensor("slot_map"), &cache = a.tensor("cache");
+  const MaybeTensor weight = a.maybe("norm_weight");
+  const double eps = a.number("norm_eps");
+  const MaybeTensor positions = a.maybe("positions"), steps = a.maybe("the table's steps");
+  const double scale = a.number("the table's scale");
+  const bool interleaved = a.flag("interleaved");
+  const MaybeTensor out = a.maybe("out");
+  const std::optional<int64_t> stream = a.stream();
+  {
+    const Released released;
+    latent_cache_write(kv, slot_map, cache, weight, eps, positions, steps, scale, interleaved, out, stream);
+  }
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_forward_latent_cache(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 11);
+  const Tensor &q = a.tensor("q"), &cache = a.tensor("cache"), &table = a.tensor("block_table"), &cu = a.tensor("cu_seqlens"),
+               &lens = a.tensor("kv_lens");
+  const double scale = a.number("sm_scale");
+  const bool causal = a.flag("causal");
+  const MaybeTensor workspace = a.maybe("workspace"), o = a.maybe("out"), lse = a.maybe("out");
+  const std::optional<int64_t> stream = a.stream();
+  std::tuple<Tensor, Tensor> y;
+  {
+    const Released released;
+    y = forward_latent_cache(q, cache, table, cu, lens, scale, causal, workspace, o, lse, stream);
+  }
+  return pair(y);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_sparse_forward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 9);
+  const Tensor &q = a.tensor("q"), &kv = a.tensor("kv"), &idx = a.tensor("idx");
+  const double scale = a.number("sm_scale");
+  const int64_t dv = a.integer("dv_dim");
+  const MaybeTensor workspace = a.maybe("workspace"), o = a.maybe("out"), lse = a.maybe("out");
+  const std::optional<int64_t> stream = a.stream();
+  std::tuple<Tensor, Tensor> y;
+  {
+    const Released released;
+    y = sparse_forward(q, kv, idx, scale, dv, workspace, o, lse, stream);
+  }
+  return pair(y);
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_forward_latent(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 11);
+  const Tensor &q = a.tensor("q"), &k_nope = a.tensor("k_nope"), &k_rope = a.tensor("k_rope"), &v = a.tensor("v");
+  const double scale = a.number("sm_scale");
+  const bool causal = a.flag("causal");
+  const MaybeTensor cu = a.maybe("cu_seqlens"), workspace = a.maybe("workspace"), o = a.maybe("out"), lse = a.maybe("out");
+  const std::optional<int64_t> stream = a.stream();
+  std::tuple<Tensor, Tensor> y;
+  {
+    const Released released;
+    y = forward_latent(q, k_nope, k_rope, v, scale, causal, cu, workspace, o, lse, stream);
+  }
+  return pair(y);
+  END_HANDLE_TH_ERRORS
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
+}
+
+}  // namespace
+
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit_libattn_torch() {
+  static PyMethodDef methods[] = {method<py_rope>("rope"), method<py_latent_cache_write>("latent_cache_write"),
+                                  method<py_forward_latent_cache>("forward_latent_cache"),
+                                  method<py_sparse_forward>("sparse_forward"), method<py_forward_latent>("forward_latent"),
+                                  {nullptr, nullptr, 0, nullptr}};
+  static PyModuleDef module = {PyModuleDef_HEAD_INIT, "libattn_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+  return PyModule_Create(&module);
 }
