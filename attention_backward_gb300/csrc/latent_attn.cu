@@ -389,26 +389,28 @@ __global__ void __launch_bounds__(THREADS, 1)
       return true;
     };
     if constexpr (LISTS) {
-      const int64_t units = static_cast<int64_t>(lp.B) * lp.S * lp.HKV * lp.splits;
+      const int units = lp.B * lp.S * lp.HKV * lp.splits;
       uint32_t uc = 0;
-      for (int64_t i = blockIdx.x;; i += gridDim.x, ++uc) {
+      for (int i = blockIdx.x;; i += gridDim.x, ++uc) {
         LatUnit u{};
         u.valid = i < units;
         if (u.valid) {
-          const LatListUnit v = list_unit(static_cast<int>(i / lp.splits), lp);
+          const LatListUnit v = list_unit(i / lp.splits, lp);
           u.n = v.b, u.a = v.t, u.row0 = v.g * lp.gh, u.live = lp.gh;
           const int* const il = lp.idx + v.b * lp.si_b + v.t * lp.si_s + v.g * lp.si_h;
-          int last = -1;
-#pragma unroll 8
-          for (int s = lane; s < lp.topk; s += 32) {
-            const int j = il[s];
-            if (j >= 0 && j < lp.SKV) last = s;
+          int last = -1;  // the last entry that lists a row: from the end, 256 at a time
+          for (int s0 = (lp.topk - 1) & ~255; s0 >= 0 && last < 0; s0 -= 256) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int s = s0 + 32 * k + lane, j = s < lp.topk ? il[s] : -1;
+              if (j >= 0 && j < lp.SKV) last = s;
+            }
+            last = __reduce_max_sync(0xffffffffu, last);
           }
-          last = __reduce_max_sync(0xffffffffu, last);
-          const int n = last < 0 ? 0 : last / KT + 1, part = static_cast<int>(i % lp.splits);
+          const int n = last < 0 ? 0 : last / KT + 1, part = i % lp.splits;
           u.j0 = static_cast<int>(static_cast<int64_t>(n) * part / lp.splits);
           u.j1 = static_cast<int>(static_cast<int64_t>(n) * (part + 1) / lp.splits);
-          u.slot = lp.splits > 1 ? static_cast<int>(i) : -1;
+          u.slot = lp.splits > 1 ? i : -1;
         }
         if (!publish(uc, u) || !u.valid) break;
       }
