@@ -266,8 +266,8 @@ attn_status_t attn_fwd_sparse(const void* q, attn_strides_t sq, const void* kv, 
   p.timeout_ns = kWaitTimeoutNs;
   const int sms = imin(sm_count(), kLatMaxCtas);
   // Lists that leave CTAs idle are split over them, two tiles a part at least, where the
-  // workspace has room for the parts.  64 heads, 2048 rows a list: 51 us whole, 14 for
-  // one token in 16 parts, 25 for 32 in 4, 38 for 76 in 2.
+  // workspace has room for the parts.  64 heads, 2048 rows a list: 48 us whole, 13.3 for
+  // one token in 16 parts, 22.5 for 32 in 4, 35 for 76 in 2.
   lp.splits = 1;
   if (workspace_bytes >= static_cast<size_t>(kHeaderBytes + kListPartBytes)) {
     lp.splits = static_cast<int>(std::max<int64_t>(1, std::min(sms / (B * S * HKV), (topk + 2 * kLatKeys - 1) / (2 * kLatKeys))));
@@ -334,10 +334,10 @@ attn_status_t attn_fwd_latent(const void* q, attn_strides_t sq, const void* kn, 
   const int sms = imin(sm_count(), kLatFwdMaxUnits);
   // Pairs that leave CTAs idle, those of the last round over the CTAs, are split over them,
   // two key blocks a part at least, where one sees 1024 keys (2048 behind whole rounds): 8
-  // queries on 8192 keys, one head 164 -> 25 us, 300 on 4000, 8 heads 86 -> 29, 1024 on
-  // 1024, 8 heads 27 -> 22.5, 2048 on 8192, 64 heads 478 -> 442; 512 on 512, 16 heads 18 ->
-  // 21, 8192 on 8192, 16 heads, whose last pairs see 1024, 255 -> 270.  (Of a packed batch
-  // the host has only a bound of the pairs.)
+  // queries on 8192 keys, one head 128 -> 19 us, 300 on 4000, 8 heads 66 -> 23, 1024 on 1024,
+  // 8 heads 20.3 -> 18.7, 2048 on 8192, 64 heads 431 -> 405; 512 on 512, 16 heads would take
+  // 17.8 instead of 13.5, 8192 on 8192, 16 heads, whose last pairs see 1024, 239 instead of 231.
+  // (Of a packed batch the host has only a bound of the pairs.)
   p.splits = 1, p.whole = 0x7fffffff;
   const int64_t last = p.cu_seqlens ? (pairs < sms ? pairs : 0) : pairs % sms;
   if (last > 0) {
