@@ -561,3 +561,39 @@ def test_rows_past_32_bits():
 def test_cache_long_prompt():
     """Many 64-row tiles of one request, two CTAs on the same keys, beside one of few rows."""
     check_cache(cache_problem([2100, 900], [1500, 1], 12, 128, "f16", 17), "f16")
+
+
+def test_calls_of_several_threads():
+    """Python threads, a stream each, call at once; each gets what it gets alone."""
+    import threading
+
+    import torch
+
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(47)
+    q, cache, table, cu, kv = cache_problem([700, 90, 300], [1, 2, 1], 24, 32, "bf16", 48)
+    t, c, n = i32(table), i32(cu), i32(kv)
+    qe, up, kr = rounded(rng, (1, 260, 3, 192), "bf16"), rounded(rng, (1, 400, 3, 256), "bf16"), rounded(rng, (1, 400, 64), "bf16")
+    pos, steps = i32(np.arange(4)), ab.rope_table(64)
+    work = [lambda: (*ab.forward_latent_cache(q, cache, t, c, n, 0.1), ab.rope(q, pos, steps, start=512)[0]),
+            lambda: ab.forward_latent(qe, up[..., :128], kr, up[..., 128:], 0.1)]
+    want = [f() for f in work]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(60):
+                    if not all(torch.equal(a, b) for a, b in zip(work[i](), want[i])):
+                        bad.append(i)
+        except Exception as e:  # (of a thread: told below)
+            bad.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in (0, 1, 0)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert bad == []

@@ -277,6 +277,20 @@ def test_binding_refuses_host_tensors(ab):
 # ------------------------------------------------------------------ the oracle
 
 
+def test_binding_refuses_other_types(ab):
+    import torch
+
+    x, table = torch.zeros(1, 2, 3, 576), ab.rope_table(64, device="cpu")
+    for f in (lambda: ab.rope(x, None, table), lambda: ab.rope(x, [0, 1], table), lambda: ab.rope(x, x, table, start="0"),
+              lambda: ab.rope(x, x, table, start=1.5), lambda: ab.rope(x, x, table, k=3), lambda: ab.rope(x, x, table, start=2 ** 70),
+              lambda: ab.latent_cache_write(x, x, None), lambda: ab.latent_cache_write(x, x, x, norm_eps="small"),
+              lambda: ab.forward_latent_cache(x, x, x, x, x, None), lambda: ab.forward_latent_cache(x, x, x, x, x, 0.1, workspace=7),
+              lambda: ab.sparse_forward(x, x, x, dv_dim=None), lambda: ab.forward_latent(x, x, x, x, "0.1"),
+              lambda: ab.forward_latent(x, x, x, x, 0.1, stream="0")):
+        with pytest.raises((ab.AttnBwdError, TypeError, AttributeError)):
+            f()
+
+
 def test_oracle_turn_is_a_rotation_and_its_transpose():
     rng = np.random.default_rng(0)
     f = [1.0, 0.3, 0.01, 1e-4]
