@@ -80,7 +80,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     ``"linear"`` divides every frequency by it; ``"base"`` raises the base to
     base * factor^(R/(R-2)); ``"parts"`` divides those of pairs that turn fewer than
     ``beta_slow`` times in ``original_length`` positions, leaves those of pairs that turn
-    more than ``beta_fast`` times, goes from one to the other by a ramp over i, and
+    more than ``beta_fast`` times, goes from one to the other by a ramp over i (from the
+    first pair on at the earliest, past the last one where that turns often enough), and
     scales the result by 1 + ln(factor) / 10."""
     R = rotary_dim
     if R < 2 or R % 2:
@@ -104,8 +105,9 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     def pair_of(turns):  # the i whose pair turns so often in original_length positions
         return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
 
-    lo, hi = max(0, math.floor(pair_of(beta_fast))), min(R // 2 - 1, math.ceil(pair_of(beta_slow)))
-    ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(R // 2)]
+    # (the ramp may end past the last pair, which then keeps a share of its frequency)
+    lo, hi = max(0, math.floor(pair_of(beta_fast))), min(R - 1, math.ceil(pair_of(beta_slow)))
+    ramp = [1.0 if i >= hi else max(0.0, (i - lo) / max(hi - lo, 1)) for i in range(R // 2)]
     return [x * (1 - r) + x / factor * r for x, r in zip(w, ramp)], 1 + math.log(factor) / 10
 
 
