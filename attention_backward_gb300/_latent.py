@@ -82,7 +82,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     ``beta_slow`` times in ``original_length`` positions, leaves those of pairs that turn
     more than ``beta_fast`` times, goes from one to the other by a ramp over i (from the
     first pair on at the earliest, past the last one where that turns often enough), and
-    scales the result by 1 + ln(factor) / 10."""
+    scales the result by 1 + ln(factor) / 10 (by 1 where the factor is below 1)."""
     R = rotary_dim
     if R < 2 or R % 2:
         raise AttnBwdError("rotary_dim must be positive and even")
@@ -108,7 +108,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "non
     # (the ramp may end past the last pair, which then keeps a share of its frequency)
     lo, hi = max(0, math.floor(pair_of(beta_fast))), min(R - 1, math.ceil(pair_of(beta_slow)))
     ramp = [1.0 if i >= hi else max(0.0, (i - lo) / max(hi - lo, 1)) for i in range(R // 2)]
-    return [x * (1 - r) + x / factor * r for x, r in zip(w, ramp)], 1 + math.log(factor) / 10
+    return [x * (1 - r) + x / factor * r for x, r in zip(w, ramp)], 1 + max(0.0, math.log(factor)) / 10
 
 
 def rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,

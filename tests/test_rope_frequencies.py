@@ -41,3 +41,8 @@ def test_parts_whose_slowest_pair_turns():
     a, e = 22, 35  # floor and ceiling of the pairs that turn 32 times and once
     part = (31 - a) / (e - a)
     assert abs(p[-1] / f[-1] - (1 - part + part / 4)) < 1e-13
+
+
+@pytest.mark.parametrize("factor,scale", [(0.5, 1.0), (1.0, 1.0), (1e-3, 1.0), (math.e, 1.1), (40.0, 1 + math.log(40.0) / 10)])
+def test_parts_never_scale_the_result_down(factor, scale):
+    assert abs(ab.rope_frequencies(64, scaling="parts", factor=factor, original_length=4096)[1] - scale) < 1e-15
