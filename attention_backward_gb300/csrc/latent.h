@@ -63,6 +63,10 @@ constexpr int kLatCost = 2;
 constexpr int kLatMinWork = 2;
 constexpr int kLatMaxCtas = 160;
 
+// A weight is 2^((score - reference) scale_log2 + kLatTop); partial rows hold the reference and
+// the weights' sum.
+constexpr float kLatTop = 7.f;
+
 // ``group``: CTAs (1 or 2) that share a part of the line, 64 rows each of its units.
 // ``q``: where a.q is null, rows of q as dims (576, T * H, 1, 1), box 64 columns x 64 rows.
 cudaError_t launch_latent_cache(const LatParams& p, const CUtensorMap& q, bool bf16, int group, int sms,

@@ -9,7 +9,7 @@
 //
 //   load    64 latent rows into nine 128-byte-swizzled slabs of 64 columns
 //   S^T  = K Q^T          M = 64 keys, N = 64 rows, K = 576
-//   P^T  = 2^(S^T scale log2 e - m)     16 bits, in shared memory
+//   P^T  = 2^((S^T - m) scale log2 e + 7)  16 bits, in shared memory
 //   O^T += C^T P^T        four M-tiles of 128 latent columns, N = 64, K = 64 keys
 //
 // so that a tile is read once from memory, serves as K (K-major) and as C^T
@@ -17,11 +17,13 @@
 // would need all of it.  (Fewer rows take the products of 64.)
 //
 // Softmax: eight warps, a quarter of the keys and half of the rows each; the scores
-// arrive as fragments (a thread: 2 keys, 8 rows).  A row's reference m is kept until a
-// weight would pass 2^15: one vote of the warps a tile, and only then is the max taken,
-// l scaled and O^T scaled in tensor memory.  m is set so that the largest weight is 2^7: fp16
-// weights keep their normal range down to 2^-21 of it and steps of 2^-31.  l is summed from
-// the f32 weights, a thread's share of the keys in registers until the unit ends.
+// arrive as fragments (a thread: 2 keys, 8 rows).  A row's reference m, one of its scores, is
+// kept until a weight would pass 2^15: one vote of the warps a tile, and only then is the max
+// taken, l scaled and O^T scaled in tensor memory.  The largest weight is then 2^7: fp16
+// weights keep their normal range down to 2^-21 of it and steps of 2^-31.  (m is taken off
+// before the scaling: of scores from 2^27 on, a scaled m would be rounded by more than fp16's
+// room above 2^7.)  l is summed from the f32 weights, a thread's share of the keys in
+// registers until the unit ends.
 //
 // Cache: the line of kv_sched.cuh, cut evenly over the CTAs; a unit split over
 // several leaves f32 partials that latent_join.cu joins.  Where requests have more
@@ -68,8 +70,8 @@ constexpr int STAGES = 2;
 constexpr int GROUPS = 5;
 constexpr int kWarps = 16, THREADS = kWarps * 32;
 constexpr int SOFT = 256;  // threads of the softmax warps
-constexpr float kTop = 7.f, kMost = 15.f;  // log2 of a row's largest weight when its max is taken, and of the most it may grow to
-constexpr float kNone = -1e30f;            // reference of a row that has seen no key
+constexpr float kTop = kLatTop, kMost = 15.f;  // log2 of a row's largest weight when its max is taken, and of the most it may grow to
+constexpr float kNone = -3.402823466e38f;  // reference of a row that has seen no key, the least that one may have
 
 enum LatBar : int {
   Q_FULL = 0,                // the loading warp (lists: a copy)
@@ -657,9 +659,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         sh.row[tid] = LISTS ? u.n * lp.so_b + u.a * p.so_s + row * p.so_h
                             : static_cast<int64_t>(u.a + row / p.G) * p.so_s + (row % p.G) * p.so_h;
       }
-      float ref[8], l[8];
+      float neg[8], l[8];  // minus the references
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ref[i] = kNone, l[i] = 0.f;
+      for (int i = 0; i < 8; ++i) neg[i] = -kNone, l[i] = 0.f;
       softmax_sync();
       for (int j = u.j0; j < u.j1; ++j, ++kc) {
         const int st = kc % STAGES;
@@ -682,28 +684,28 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!vb || j * KT + ka + 8 >= h) y = -INFINITY;
           }
         }
-        float top[8], over = -INFINITY;  // over: log2 of my largest weight
+        float top[8], over = -INFINITY;  // over: my largest score, above its row's reference
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           top[i] = fmaxf(s[4 * (i >> 1) + (i & 1)], s[4 * (i >> 1) + 2 + (i & 1)]);
-          over = fmaxf(over, fmaf(top[i], p.scale_log2, -ref[i]));
+          over = fmaxf(over, top[i] + neg[i]);
         }
-        if (softmax_any(over > kMost || bad)) {
+        if (softmax_any(fmaf(over, p.scale_log2, kTop) > kMost || bad)) {
           // ---- some row's weights outgrow the type: new references for those
           sh.mx[w4][cm] = reduce8(top, lane, larger);
           if ((dead = softmax_any(bad))) break;
           if (tid < NR) {
-            const float m = fmaxf(fmaxf(sh.mx[0][tid], sh.mx[1][tid]), fmaxf(sh.mx[2][tid], sh.mx[3][tid])) * p.scale_log2;
+            const float m = fmaxf(fmaxf(sh.mx[0][tid], sh.mx[1][tid]), fmaxf(sh.mx[2][tid], sh.mx[3][tid]));
             const float old = sh.ref[tid];
-            const bool grown = m - old > kMost;
-            sh.f[tid] = grown ? (old == kNone ? 0.f : ex2(old - (m - kTop))) : 1.f;
-            if (grown) sh.ref[tid] = m - kTop;
+            const bool grown = fmaf(m - old, p.scale_log2, kTop) > kMost;
+            sh.f[tid] = grown ? ex2((old - m) * p.scale_log2) : 1.f;
+            if (grown) sh.ref[tid] = m;
           }
           softmax_sync();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int row = c0 + 8 * (i >> 1) + (i & 1);
-            ref[i] = sh.ref[row];
+            neg[i] = -sh.ref[row];
             l[i] *= sh.f[row];
           }
           if (j > u.j0) {
@@ -726,10 +728,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         uint8_t* const pt = sm + p_at(st);  // (in place of the key part, which the scores have used)
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), top2 = make_float2(kTop, kTop);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const float x0 = ex2(fmaf(s[2 * i], p.scale_log2, -ref[i])), x1 = ex2(fmaf(s[2 * i + 1], p.scale_log2, -ref[i + 1]));
-          const float y0 = ex2(fmaf(s[2 * i + 2], p.scale_log2, -ref[i])), y1 = ex2(fmaf(s[2 * i + 3], p.scale_log2, -ref[i + 1]));
+          const float2 neg2 = make_float2(neg[i], neg[i + 1]);
+          const float2 x = __ffma2_rn(__fadd2_rn(make_float2(s[2 * i], s[2 * i + 1]), neg2), scale2, top2);
+          const float2 y = __ffma2_rn(__fadd2_rn(make_float2(s[2 * i + 2], s[2 * i + 3]), neg2), scale2, top2);
+          const float x0 = ex2(x.x), x1 = ex2(x.y), y0 = ex2(y.x), y1 = ex2(y.y);
           l[i] += x0 + y0, l[i + 1] += x1 + y1;
           const uint32_t at = 4 * half + i / 2;  // 16-byte piece of a key's 64 weights
           *reinterpret_cast<uint32_t*>(pt + sw128_offset(ka, at) + 4 * (lane & 3)) = pack2<BF16>(x0, x1);
@@ -754,7 +759,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int row = u.row0 + tid;
             float* const lse = LISTS ? p.lse + (u.n * lp.sl_b + row * p.sl_h + u.a * p.sl_s)
                                      : p.lse + ((row % p.G) * p.sl_h + static_cast<int64_t>(u.a + row / p.G) * p.sl_s);
-            *lse = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+            *lse = sum == 0.f ? -INFINITY : (fmaf(m, p.scale_log2, -kTop) + log2f(sum)) * 0.69314718055994531f;
           } else {
             p.part_ml[static_cast<int64_t>(u.slot) * NR + tid] = make_float2(m, sum);
           }

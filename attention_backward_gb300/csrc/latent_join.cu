@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         mx = fmaxf(mx, m);
-        const float w = v.y == 0.f ? 0.f : ex2(v.x - mx), g = m == -INFINITY ? 0.f : ex2(m - mx);
+        const float w = v.y == 0.f ? 0.f : ex2((v.x - mx) * p.scale_log2), g = m == -INFINITY ? 0.f : ex2((m - mx) * p.scale_log2);
         m = mx;
         float sum = w * v.y;
 #pragma unroll
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
       for (int k = 1; k < shares; ++k) {
         const float2 v = s_ml[warp + k];
         if (v.y == 0.f) continue;
-        const float mx = fmaxf(m, v.x), g = l == 0.f ? 0.f : ex2(m - mx), f = ex2(v.x - mx);
+        const float mx = fmaxf(m, v.x), g = l == 0.f ? 0.f : ex2((m - mx) * p.scale_log2), f = ex2((v.x - mx) * p.scale_log2);
         l = l * g + v.y * f;
         m = mx;
 #pragma unroll
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) latent_join_kernel(const __grid
         *reinterpret_cast<uint2*>(out + 8 * (e * 32 + lane)) = w;
       }
       if (lane == 0 && half == 0)
-        p.lse[lse_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        p.lse[lse_at] = l == 0.f ? -INFINITY : (fmaf(m, p.scale_log2, -kLatTop) + log2f(l)) * 0.69314718055994531f;
     }
     if (shares > 1) __syncthreads();
   }
