@@ -95,7 +95,7 @@ struct LatFwdParams {
   uint64_t timeout_ns;
   int whole;        // pairs of query tiles that are a unit each (2^31 - 1: all)
   int splits;       // units of each further pair, of a share of its key blocks each
-  float2* part_ml;  // [parts][256 rows] reference (log2 units) and sum
+  float2* part_ml;  // [parts][256 rows] reference (a score) and sum
   float* part_o;    // [parts][256 rows][128]
 };
 struct LatFwdMaps {

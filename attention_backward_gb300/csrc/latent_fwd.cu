@@ -58,9 +58,12 @@ constexpr int THREADS = 12 * 32;
 // keeps the unit walk and the barrier phases of the persistent loop
 constexpr uint32_t REG_SOFT = 208, REG_CTL = 88;
 static_assert(2 * REG_SOFT + REG_CTL == 3 * 168, "register split must equal the launch's registers");
-// A row's reference m is set so that its largest weight is 2^7, and kept until one would
+// A row's reference is set so that its largest weight is 2^7, and kept until one would
 // pass 2^15: fp16 weights keep their normal range down to 2^-21 of the largest.
 constexpr float kTop = 7.f, kRescaleLog2 = 8.f;
+// From here on, where its steps are 1/2 and more, a reference is not taken off the scaled
+// scores but off the scores themselves.  (From 2^27 on its rounding would pass the room that fp16 leaves.)
+constexpr float kFar = 0x1p22f;
 
 constexpr int D = 128;                 // value columns
 constexpr int KSLABS = 3, VSLABS = 2;  // 64-column slabs of a row of Q or K, and of V
@@ -78,6 +81,14 @@ constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + D;
 
 // Where slab i of the ring lies.
 __device__ __forceinline__ uint32_t slab_at(uint32_t i) { return OFF_R + i % RING * SLAB; }
+
+// Score ``top`` as a reference in log2 units, and log2 of the factor that takes weights from
+// reference ``x`` to ``top``.
+__device__ __forceinline__ float scaled(float top, float scale) { return fmaf(top, scale, -kTop); }
+__device__ __forceinline__ float below(float x, float top, float scale) {
+  const float m = scaled(top, scale);
+  return fabsf(m) >= kFar ? (x - top) * scale : scaled(x, scale) - m;
+}
 
 enum FwdBar : int {
   Q_FULL = 0,
@@ -522,7 +533,8 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const int lo_w = w ? u.lo[1] : u.lo[0], hi_w = w ? u.hi[1] : u.hi[0];
     const int q = qt0 + row;
     const uint32_t c0 = c;
-    float m_used = -INFINITY, l = 0.f;
+    float top = -INFINITY, l = 0.f;  // top: the score that is the row's reference
+    bool far = false;
     for (int j = lo_w; j < hi_w; ++j, ++c) {
       if (!(ok = mbar_wait_warp(&bars[S_FULL0 + w], c & 1, wc, kErrWaitS))) break;
       tc_fence_after();
@@ -553,31 +565,39 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
         }
       }
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      // the row's reference in log2 units (scale_log2 > 0 keeps the order of the raw scores)
-      const float m_new = fmaxf(m_used, mx * p.scale_log2 - kTop);
       // a row whose max grew past the threshold is rescaled; a row that had no
-      // visible key so far adopts the new max (its O row and l are zero)
-      const bool resc = m_used != -INFINITY && m_new > m_used + kRescaleLog2;
-      const float f = resc ? ex2(m_used - m_new) : 1.f;
-      if (__any_sync(0xffffffffu, resc)) {
-        // (the tile's previous P V, issued before these scores, has completed as they have)
+      // visible key so far adopts the max (its O row and l are zero)
+      const float was = top;
+      const bool grown = (mx - top) * p.scale_log2 > kRescaleLog2;
+      if (grown) top = mx;
+      const float m = top == -INFINITY ? 0.f : scaled(top, p.scale_log2);
+      if (__any_sync(0xffffffffu, grown || far)) {
+        far = fabsf(m) >= kFar;
+        const bool resc = grown && was != -INFINITY;
+        if (__any_sync(0xffffffffu, resc)) {
+          // (the tile's previous P V, issued before these scores, has completed as they have)
+          const float f = resc ? ex2(below(was, top, p.scale_log2)) : 1.f;
+          l *= f;
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t r[32];
-          tmem_ld32(tO + ch * 32, r);
-          tmem_ld_wait();
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t r[32];
+            tmem_ld32(tO + ch * 32, r);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-          tmem_st16(tO + ch * 32, r);
-          tmem_st16(tO + ch * 32 + 16, r + 16);
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+            tmem_st16(tO + ch * 32, r);
+            tmem_st16(tO + ch * 32 + 16, r + 16);
+          }
+        }
+        if (__any_sync(0xffffffffu, far)) {
+          const float off = far ? top : 0.f;
+#pragma unroll
+          for (int k = 0; k < BK; ++k) sr[k] = __float_as_uint(__uint_as_float(sr[k]) - off);
         }
       }
-      l *= f;
-      if (resc || m_used == -INFINITY) m_used = m_new;
-      const float msub = m_used == -INFINITY ? 0.f : m_used;
       // S * scale - m two keys per instruction (f32x2 FMA), the row sum in two
       // f32x2 accumulators
-      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-msub, -msub);
+      const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = far ? make_float2(kTop, kTop) : make_float2(-m, -m);
       float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int ch = 0; ch < BK / 32; ++ch) {
@@ -616,10 +636,10 @@ __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_con
     const int64_t part_row = static_cast<int64_t>(u.index - p.whole) * 2 * BQ + w * BQ + row;  // of a part
     if (live) {
       if (u.index >= p.whole) {
-        p.part_ml[part_row] = make_float2(m_used, l);
+        p.part_ml[part_row] = make_float2(top, l);
       } else {
         p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] =
-            l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+            l == 0.f ? -INFINITY : (scaled(top, p.scale_log2) + log2f(l)) * 0.69314718055994531f;
       }
     }
     uint8_t* const out = p.o + 2 * (u.b * p.so_b + pos * p.so_s + u.h * p.so_h);
@@ -685,7 +705,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) latent_fwd_join_kernel(const 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mx = fmaxf(mx, m);
-    const float f = v.y == 0.f ? 0.f : ex2(v.x - mx), g = m == -INFINITY ? 0.f : ex2(m - mx);
+    const float f = v.y == 0.f ? 0.f : ex2(below(v.x, mx, p.scale_log2));
+    const float g = m == -INFINITY ? 0.f : ex2(below(m, mx, p.scale_log2));
     m = mx;
     float sum = f * v.y;
 #pragma unroll
@@ -705,7 +726,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) latent_fwd_join_kernel(const 
   *reinterpret_cast<uint2*>(p.o + 2 * (u.b * p.so_b + pos * p.so_s + u.h * p.so_h + 4 * lane)) =
       make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
   if (lane == 0)
-    p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    p.lse[u.b * p.sl_b + u.h * p.sl_h + pos * p.sl_s] = l == 0.f ? -INFINITY : (scaled(m, p.scale_log2) + log2f(l)) * 0.69314718055994531f;
 }
 
 template <bool BF16>

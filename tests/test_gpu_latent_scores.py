@@ -2,8 +2,7 @@
 
 One column carries the scores: powers of two of either sign in q, distinct integers of
 at most 8 bits times a power of two in the keys.  The scores are then exact in f32 and so
-far apart that a row's softmax is 1 at its largest score (several times, where a list names
-that row more than once) and 0 elsewhere: O is a row of the values as it is, and the LSE the
+far apart that a row's softmax is shared by the keys of its largest score: O is their mean, and the LSE the
 scaled score within the roundings of its scale, products and sum, 4 of them (2^-22 of it).
 Every fourth head has ordinary scores, in whose bound the others have no part."""
 import numpy as np
@@ -11,7 +10,7 @@ import pytest
 
 from oracle import latent as oracle
 from test_gpu_latent import near
-from test_gpu_rope import f64, i32, rounded
+from test_gpu_rope import EPS, STEP, f64, i32, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -40,8 +39,11 @@ def check(o, lse, r, name):
     """o [.., heads, dv], lse [.., heads] against r."""
     heads = np.arange(lse.shape[-1])
     plain, far = heads % 4 == 0, heads % 4 != 0
-    # (the definition's own f64 sum of n equal shares is off by n 2^-53 at most)
-    assert (np.abs(f64(o)[..., far, :] - r.o[..., far, :]) <= 2.0 ** -40 * np.abs(r.o[..., far, :])).all()
+    # the mean of the t <= 20 rows that share the largest score (weights of 2^7 each, without
+    # rounding): the output's rounding, and f32 sums, (t + 3) 2^-24 of the sum of |v| at most
+    want = r.o[..., far, :]
+    tol = EPS[name] * np.abs(want) + 2.0 ** -19 * r.mag[..., far, :] + STEP[name]
+    assert (np.abs(f64(o)[..., far, :] - want) <= tol).all()
     assert np.abs(r.lse[..., far]).min() > 1e7 and np.abs(r.lse).max() > 1e9
     assert (np.abs(f64(lse)[..., far] / r.lse[..., far] - 1) <= 2.0 ** -22).all()
     part = oracle.Result((0,), r.o.shape[-1])
@@ -90,3 +92,20 @@ def test_cache_of_far_scores(name, powers, power, scale, order):
     r = oracle.cache_forward(f64(q)[0], f64(cache), table[None], [0, 3], [KEYS], scale)
     o, lse = ab.forward_latent_cache(q, cache, i32(table[None]), i32([0, 3]), i32([KEYS]), scale)
     check(o[0], lse[0].t(), r, name)
+
+
+@pytest.mark.parametrize("name,powers,power,scale", SIZES)
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("S,Sk", [(3, KEYS), (2, 2000)])  # whole, and keys in parts
+def test_expanded_of_far_scores(name, powers, power, scale, order, S, Sk):
+    import attention_backward_gb300 as ab
+
+    rng = np.random.default_rng(power + 2)
+    q, last = problem(rng, name, powers, power, 12, 192, order)
+    q = q[:, :S].contiguous()
+    up, kr = rounded(rng, (1, Sk, 12, 256), name, 0.125), rounded(rng, (1, Sk, 64), name, 0.125)
+    kr[0, :, -1] = last[np.sort(rng.integers(0, KEYS, Sk)) if Sk > KEYS else np.arange(Sk)]
+    for causal in (True, False):
+        r = oracle.expanded_forward(f64(q), f64(up[..., :128]), f64(kr), f64(up[..., 128:]), scale, causal)
+        o, lse = ab.forward_latent(q, up[..., :128], kr, up[..., 128:], scale, causal=causal)
+        check(o, lse.transpose(1, 2), r, name)
