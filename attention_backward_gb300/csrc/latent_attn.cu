@@ -458,7 +458,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const LatUnit u = next_unit(uc, &ok);
       if (!ok || !u.valid) break;
       if (u.valid == 2 || u.j1 <= u.j0) continue;
-      if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wc, kErrWaitStageEmpty))) break;
+      // every S of the unit before, which lasts as long as that unit
+      if (qc >= 1 && !(ok = mbar_wait_warp(&bars[Q_EMPTY], (qc - 1) & 1, wu, kErrWaitStageEmpty))) break;
       ++qc;
       if (LISTS || p.q == nullptr) {
         // lists: 64 heads of the token; else 64 rows of [T * H, 576].  (Those past the
