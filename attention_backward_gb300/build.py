@@ -60,6 +60,12 @@ def _torch_flags(cc: str) -> tuple:
             [f"-L{os.path.join(at, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"])
 
 
+def _newer(lib: str, objs) -> bool:
+    """Whether ``lib`` has to be linked again.  By the files' times and not by what this run
+    compiled, so that a build that failed half way is taken up by the next one."""
+    return not os.path.exists(lib) or any(os.path.getmtime(o) > os.path.getmtime(lib) for o in objs)
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -69,42 +75,36 @@ def build(verbose: bool = False, force: bool = False) -> str:
         obj = os.path.join(BUILD, s.replace(".cu", ".o"))
         objs.append(obj)
         if force or _stale(obj, src):
-            jobs.append([cc, *ARCH, *FLAGS, "-c", src, "-o", obj] + (["-Xptxas", "-v"] if verbose else []))
+            jobs.append((obj, [cc, *ARCH, *FLAGS, "-c", src] + (["-Xptxas", "-v"] if verbose else [])))
 
     cxx = shutil.which("g++") or "g++"
     compile_flags, link_flags = _torch_flags(cc)
     torch_obj, torch_src = os.path.join(BUILD, "torch_latent.o"), os.path.join(CSRC, TORCH_SOURCE)
-    torch_stale = force or _stale(torch_obj, torch_src) or not os.path.exists(TORCH_LIB)
-    cuda_jobs = len(jobs)
-    if torch_stale:
-        jobs.append([cxx, *compile_flags, "-c", torch_src, "-o", torch_obj])
+    if force or _stale(torch_obj, torch_src):
+        jobs.append((torch_obj, [cxx, *compile_flags, "-c", torch_src]))
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
+    def run(job):  # a file takes its name when it is whole
+        to, cmd = job
+        tmp = to + ".tmp"
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, to)
         return cmd, r
+
+    def check(cmd, r, what):
+        if verbose or r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode:
+            raise RuntimeError(f"{what} failed: {' '.join(cmd)}")
 
     with ThreadPoolExecutor(max(1, len(jobs))) as ex:
         for cmd, r in ex.map(run, jobs):
-            if verbose or r.returncode:
-                sys.stderr.write(r.stdout + r.stderr)
-            if r.returncode:
-                raise RuntimeError(f"compiler failed: {' '.join(cmd)}")
-    if force or cuda_jobs or not os.path.exists(LIB):
-        tmp = LIB + ".tmp"
-        cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link failed")
-        os.replace(tmp, LIB)
-    if torch_stale:
-        tmp = TORCH_LIB + ".tmp"
-        _, r = run([cxx, "-shared", "-o", tmp, torch_obj, f"-L{BUILD}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN",
-                    *link_flags])
-        if r.returncode:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link failed")
-        os.replace(tmp, TORCH_LIB)
+            check(cmd, r, "compiler")
+    if force or _newer(LIB, objs):
+        check(*run((LIB, [cc, *ARCH, "-shared", *objs, "-cudart", "static"])), "link")
+    if force or _newer(TORCH_LIB, [torch_obj]):
+        check(*run((TORCH_LIB, [cxx, "-shared", torch_obj, f"-L{BUILD}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN",
+                                *link_flags])), "link")
     return LIB
 
 
