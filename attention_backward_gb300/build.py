@@ -77,12 +77,6 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(obj, src):
             jobs.append((obj, [cc, *ARCH, *FLAGS, "-c", src] + (["-Xptxas", "-v"] if verbose else [])))
 
-    cxx = shutil.which("g++") or "g++"
-    compile_flags, link_flags = _torch_flags(cc)
-    torch_obj, torch_src = os.path.join(BUILD, "torch_latent.o"), os.path.join(CSRC, TORCH_SOURCE)
-    if force or _stale(torch_obj, torch_src):
-        jobs.append((torch_obj, [cxx, *compile_flags, "-c", torch_src]))
-
     def run(job):  # a file takes its name when it is whole
         to, cmd = job
         tmp = to + ".tmp"
@@ -97,15 +91,27 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode:
             raise RuntimeError(f"{what} failed: {' '.join(cmd)}")
 
-    with ThreadPoolExecutor(max(1, len(jobs))) as ex:
+    with ThreadPoolExecutor(len(jobs) + 1) as ex:
+        extension = ex.submit(_compile_extension, cc, force, run, check)
         for cmd, r in ex.map(run, jobs):
             check(cmd, r, "compiler")
     if force or _newer(LIB, objs):
         check(*run((LIB, [cc, *ARCH, "-shared", *objs, "-cudart", "static"])), "link")
-    if force or _newer(TORCH_LIB, [torch_obj]):
-        check(*run((TORCH_LIB, [cxx, "-shared", torch_obj, f"-L{BUILD}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN",
-                                *link_flags])), "link")
+    # (the library needs neither torch nor Python's headers and is there whatever the extension lacks)
+    obj, link = extension.result()
+    if force or _newer(TORCH_LIB, [obj]):
+        check(*run((TORCH_LIB, link)), "link")
     return LIB
+
+
+def _compile_extension(cc: str, force: bool, run, check) -> tuple:
+    """Its object, and the command that links it."""
+    cxx = shutil.which("g++") or "g++"
+    compile_flags, link_flags = _torch_flags(cc)
+    obj, src = os.path.join(BUILD, "torch_latent.o"), os.path.join(CSRC, TORCH_SOURCE)
+    if force or _stale(obj, src):
+        check(*run((obj, [cxx, *compile_flags, "-c", src])), "compiler")
+    return obj, [cxx, "-shared", obj, f"-L{BUILD}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN", *link_flags]
 
 
 if __name__ == "__main__":

@@ -125,3 +125,18 @@ def test_a_build_that_was_cut_off_is_taken_up(tree, monkeypatch):
     tree.set("3")  # (no source has changed)
     tree.run()
     assert tree.libraries() == whole("2") and tree.log() == ["one.o two.o", "torch_latent.o"]
+
+
+@pytest.mark.parametrize("failing", ["torch_latent.cpp", "extension_link", "flags"])
+def test_the_library_does_not_wait_for_the_extension(tree, monkeypatch, failing):
+    """Without Python's headers, or without torch, the library is built all the same; the
+    build says what failed."""
+    tree.set("1", failing)
+    if failing == "flags":
+        def none(cc):
+            raise ImportError("No module named 'torch'")
+
+        monkeypatch.setattr(tree.build, "_torch_flags", none)
+    with pytest.raises((RuntimeError, ImportError)):
+        tree.run()
+    assert tree.libraries() == [whole("1")[0], None]
