@@ -109,8 +109,16 @@ def _compile_extension(cc: str, force: bool, run, check) -> tuple:
     cxx = shutil.which("g++") or "g++"
     compile_flags, link_flags = _torch_flags(cc)
     obj, src = os.path.join(BUILD, "torch_latent.o"), os.path.join(CSRC, TORCH_SOURCE)
-    if force or _stale(obj, src):
+    # its ABI is this interpreter's and this torch's: what an object was made for stands beside it
+    import torch
+
+    stamp, made_for = obj + ".for", "\n".join([torch.__version__, sys.version, *compile_flags, *link_flags])
+    if force or _stale(obj, src) or not os.path.exists(stamp) or open(stamp).read() != made_for:
+        if os.path.exists(stamp):
+            os.remove(stamp)
         check(*run((obj, [cxx, *compile_flags, "-c", src])), "compiler")
+        with open(stamp, "w") as f:
+            f.write(made_for)
     return obj, [cxx, "-shared", obj, f"-L{BUILD}", f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN", *link_flags]
 
 

@@ -140,3 +140,30 @@ def test_the_library_does_not_wait_for_the_extension(tree, monkeypatch, failing)
     with pytest.raises((RuntimeError, ImportError)):
         tree.run()
     assert tree.libraries() == [whole("1")[0], None]
+
+
+def test_the_extension_belongs_to_one_interpreter_and_torch(tree, monkeypatch):
+    """Another torch, interpreter or set of flags compiles and links it anew; the library
+    stays."""
+    import torch
+
+    tree.run()
+    plain = tree.build._torch_flags
+    for i, (where, name, value) in enumerate([(torch, "__version__", "9.9"), (sys, "version", "4.0 (other)"),
+                                              (tree.build, "_torch_flags", lambda cc: (plain(cc)[0] + ["-DX"], plain(cc)[1])),
+                                              (tree.build, "_torch_flags", lambda cc: (plain(cc)[0], plain(cc)[1] + ["-lx"]))]):
+        with monkeypatch.context() as m:
+            m.setattr(where, name, value)
+            tree.set(f"{i + 2}")
+            tree.run()
+            assert tree.libraries() == [whole("1")[0], whole(f"{i + 2}")[1]]
+            assert tree.log() == ["torch_latent.cpp", "torch_latent.o"]
+            tree.set("x")
+            tree.run()
+            assert tree.log() == []
+    tree.set("7", "torch_latent.cpp")  # back again, and the compiler fails: the old one is not kept for good
+    with pytest.raises(RuntimeError):
+        tree.run()
+    tree.set("8")
+    tree.run()
+    assert tree.libraries()[1] == whole("8")[1]
