@@ -17,7 +17,8 @@ One step of a server of latent attention (``new_lens`` new tokens a request; ``k
 
 Launches go to ``stream``, by default the current stream of the tensors' device,
 whichever device is current; outputs and workspaces made here belong to that
-stream.
+stream.  Autograd does not see these calls: gradients are ``rope`` with ``inverse`` and
+``sparse_backward``.
 """
 from __future__ import annotations
 
@@ -67,7 +68,9 @@ _binding._SIGS.update({
 
 
 class RopeTable(NamedTuple):
-    """Frequencies of rotary positions, as ``rope_table`` makes them."""
+    """Frequencies of rotary positions, as ``rope_table`` makes them.  Frequencies f_i of
+    another scaling, in radians a position, go in as steps[i] = round(f_i / (2 pi) * 2^64)
+    modulo 2^64, less 2^64 from 2^63 on."""
     steps: torch.Tensor  # int64 [R / 2] on the device: turns a position * 2^64 (as uint64)
     scale: float         # factor of the result
 
@@ -222,7 +225,8 @@ def sparse_forward(q, kv, idx, sm_scale: Optional[float] = None, dv_dim: int = L
                    stream=None):
     """O [B,S,H,512] and the natural-log LSE [B,H,S] of top-k sparse attention
     over shared latent rows, as ``sparse_backward`` takes them (see attn_fwd_sparse):
-    q [B,S,H,576], kv [B,SKV,HKV,576], idx int32 [B,S,HKV,topk].  ``out`` (o, lse) and
+    q [B,S,H,576], kv [B,SKV,HKV,576], idx int32 [B,S,HKV,topk], at most 64 heads a
+    group (more: a call for 64 heads each, on views of q, o and lse).  ``out`` (o, lse) and
     ``workspace`` (uint8, at least 256 bytes; one per stream) may be passed to reuse them."""
     return _call("sparse_forward", q, stream, kv, idx, ROW ** -0.5 if sm_scale is None else sm_scale, dv_dim, workspace,
                  *_pair(out))

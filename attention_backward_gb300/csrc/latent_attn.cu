@@ -37,10 +37,12 @@
 // take 32 ns each whatever their size, and pages of 16 need 36 a tile.)
 //
 // Bound by DRAM where the rows of a request fit one tile of 64: 64 single tokens of 64 heads
-// on 8192 rows 118 us with the join, 5.1 TB/s, 75 % of the copy rate (the stream itself runs
-// at 5.9).  Bound by the products' reads of shared memory (147 KB for S, 96 for O a tile) and
-// the chain from S over the softmax to O where rows come from L2: 4096 lists of 2048 rows, 64
-// heads 0.94 ms, 930 TFLOP/s, 49 % of the bf16 peak, the tensor pipe active for 60 % of it.
+// on 8192 rows 119 us with the join, 5.1 TB/s, 75 % of the copy rate (the stream itself runs
+// at 5.9).  Where rows come from L2, the products' reads of shared memory (147 KB for S, 96 for
+// O a tile) account for two thirds of a tile's time, at 128 bytes a cycle; the rest is the chain
+// from the loads over S and the softmax to O, and S's M of 64, half of the tensor core's rows:
+// 4096 lists of up to 2048 rows (1536 on average), 64 heads 0.95 ms, 920 TFLOP/s, 48 % of the
+// bf16 peak, the tensor pipe active for 60 % of it.
 // One request of 385 rows, 16 heads: 12.7 us with the join, of which 7 start and end the
 // kernels.
 //

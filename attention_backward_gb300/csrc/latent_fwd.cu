@@ -21,9 +21,11 @@
 // to none: those rows of V are zeroed in shared memory before the slab is published
 // (a zero P times a NaN would be NaN; of K they only make scores that are masked).
 //
-// Bound by the tensor core: 4096 queries on 4096 keys, 64 heads, no mask 432 us, 1590 TFLOP/s,
-// 84 % of the bf16 peak; 2048 on 8192, causal 393 us, 1520; four packed sequences of 16384
-// together, 16 heads 301 us, 1420 (units of few key blocks begin and end often).  What the
+// Bound by the tensor core.  Whole calls with the join, back to back: 4096 queries on 4096
+// keys, 64 heads, no mask 434 us, 1580 TFLOP/s, 83 % of the bf16 peak (up to 478 where the
+// power cap holds the clock down); 2048 on 8192, causal 432 us, 1390, of which the join 10;
+// four packed sequences of 16384 together, 16 heads 325 us, 1310 (units of few key blocks begin
+// and end often); 1024 packed sequences of 16, 4 heads 130 us.  What the
 // products wait for is the softmax of the other tile, 1400 cycles a block beside 1280 of
 // products.  (One lane issues, and waits on as few barriers as there are: with waits and
 // commits of the whole warp between P's products and the next scores the first of these took

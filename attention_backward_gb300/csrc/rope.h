@@ -37,8 +37,8 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams& p, bool bf16, int sms, cudaStream_t st);
 
 // cos and sin of p turns of step / 2^64.  The 64-bit product keeps the fraction of a
-// turn exactly (whole turns overflow); its upper half, as a signed multiple of
-// 2^-31 half turns, is within 2^-32 turns = 1.5e-9 radians of it.
+// turn exactly (whole turns overflow).  Its upper half is taken as a signed number of half
+// turns in f32, whose 24 bits put the angle within 2^-26 turns = 9.4e-8 radians.
 __device__ __forceinline__ void turn(int p, uint64_t step, float* c, float* s) {
   const uint64_t t = static_cast<uint64_t>(static_cast<int64_t>(p)) * step;
   sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, s, c);

@@ -105,6 +105,8 @@ ATTN_BWD_API size_t attn_fwd_sparse_workspace_size(int64_t B, int64_t S, int64_t
  *   O = softmax(sm_scale q kv_row^T) kv_row[:DV] and the natural-log LSE.
  * Entries outside [0, SKV) are not visible and never dereferenced, repeated ones
  * count once a slot; a list without a visible entry gives O = 0 and LSE = -inf.
+ * Scores and sums are f32; a weight is rounded to the 16-bit type once, and l sums the
+ * f32 weights.
  *   q : [B,S,H,576], kv : [B,SKV,HKV,576], o : [B,S,H,512] 16-bit;  the rows of kv are
  *   evenly spaced (skv.s = HKV skv.h, skv.b = SKV skv.s);  idx : int32
  *   [B,S,HKV,topk], strides sidx, unit slot stride;  lse : f32, lse[b*slse.b +
@@ -133,8 +135,10 @@ ATTN_BWD_API size_t attn_fwd_latent_workspace_size(int64_t B, int64_t S, int64_t
  *   q : [B,S,H,192] (qn | qr), kn, v : [B,Sk,H,128] (columns of one projection: any
  *   strides of 16-byte multiples), kr : [B,Sk,64] (strides skr.b, skr.s), o :
  *   [B,S,H,128] 16-bit;  lse : f32, lse[b*slse.b + h*slse.h + s*slse.s]
- * A query that sees no key gets O = 0 and LSE = -inf.  Rows past
- * cu_seqlens[num_seqs] are not written and may hold anything.
+ * Scores and sums are f32; a weight is rounded to the 16-bit type once, and l sums the
+ * f32 weights.  A query that sees no key gets O = 0 and LSE = -inf.  Rows past
+ * cu_seqlens[num_seqs] are not written and may hold anything.  (A NaN in a row of v that
+ * some query of a sequence sees may make others of it NaN, as 0 * NaN does.)
  *   workspace : attn_fwd_latent_workspace_size(B, S, H, num_seqs) bytes, 16-byte
  *   aligned.  Rows whose keys were split are joined by a second launch in a fixed order.
  * Errors as attn_fwd_gqa's. */

@@ -34,7 +34,8 @@ typedef struct {
  * the gradient of x given that of y.  The frequencies are fractions of a turn a
  * position as 64-bit fixed point: p * steps[i] keeps its fraction of a turn
  * exactly, so that far positions lose nothing (an f32 angle at 10^6 is off by
- * 2^-5 radians).  The products and sums are f32, rounded once.
+ * 2^-5 radians); the angle itself is f32, within 2^-26 turns.  The products and sums are
+ * f32, rounded once.
  *   q : a tensor;  k : another one with heads and columns of its own, or NULL (both
  *   take one launch)
  *   positions : int32, of row b at positions + b * positions_b (0: all rows
