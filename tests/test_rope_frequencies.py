@@ -4,8 +4,7 @@ import math
 import numpy as np
 import pytest
 
-__import__("__graft_entry__").build()
-import attention_backward_gb300 as ab  # noqa: E402
+import attention_backward_gb300 as ab
 
 
 @pytest.mark.parametrize("R,length,base,slow,fast", [
