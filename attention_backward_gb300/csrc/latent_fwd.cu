@@ -247,12 +247,12 @@ __device__ __forceinline__ UnitSpan unit_span(const FwdUnit& u) {
 
 // Persistent: each CTA's producer takes the unit of its number, then draws units, longest
 // first, from a counter in the workspace header (cleared by the host before the launch,
-// where there are more units than CTAs), decodes each from the place of the one before and
-// publishes it to the other roles through a two-slot ring in shared memory; a draw past the last unit ends every role.  Barrier phases
-// run on across units (K and V by a block counter, the S and P barriers of a tile by that
-// tile's block counter), and two barriers hand the shared Q tiles (Q_EMPTY: every S MMA of
-// the unit has completed) and a tile's O accumulator (O_FREE: its softmax warps have read O)
-// to the next unit.
+// where there are more units than CTAs), decodes each from the place of the one before
+// and publishes it to the other roles through a two-slot ring in shared memory; a draw
+// past the last unit ends every role.  Barrier phases run on across units (K and V by a
+// block counter, the S and P barriers of a tile by that tile's block counter), and two
+// barriers hand the shared Q tiles (Q_EMPTY: every S MMA of the unit has completed) and a
+// tile's O accumulator (O_FREE: its softmax warps have read O) to the next unit.
 template <bool BF16>
 __global__ void __launch_bounds__(THREADS, 1) latent_fwd_kernel(const __grid_constant__ LatFwdMaps maps,
                                                                const LatFwdParams p) {
